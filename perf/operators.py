@@ -245,8 +245,9 @@ def _handle(s, fmt, num_pages, hkv, d):
     cache = kvq.PagedCache(d, hkv, num_pages, fmt[0], fmt[1], fmt[2], fmt[3], s["ks"], s["vs"], PAGE)
     for name in ("k_rows", "v_rows", "k_aux", "v_aux"):
         if s[name] is not None:
-            getattr(cache, name).copy_(s[name])
-            s[name] = getattr(cache, name)
+            own_buffer = getattr(cache, name)
+            own_buffer.copy_(s[name].view(own_buffer.shape))
+            s[name] = own_buffer.view(s[name].shape)
     return cache
 
 
