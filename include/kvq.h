@@ -252,6 +252,110 @@ KVQ_API kvq_status kvq_requantize(const kvq_cache* src, const int32_t* src_slots
 KVQ_API kvq_status kvq_outlier_calibrate(const uint16_t* k, int32_t num_tokens, int32_t num_kv_heads,
                                          int32_t head_dim, int32_t* out_idx, void* stream);
 
+/* ---- rotary positions -------------------------------------------------------------
+ * What turns queries and keys by their positions before the cache sees them.  Pair j
+ * (j < rot_dim / 2) of a head at position p is turned by theta = p * w_j with
+ * w_j = base^(-2 j / rot_dim), scaled for contexts longer than the model was trained on:
+ *   (a, b) -> scale * (a cos theta - b sin theta, b cos theta + a sin theta)
+ * and the elements from rot_dim on are copied. */
+typedef enum kvq_rope_layout {
+  KVQ_ROPE_HALF = 0,        /* pair j is elements (j, j + rot_dim / 2) */
+  KVQ_ROPE_INTERLEAVED = 1  /* pair j is elements (2 j, 2 j + 1)       */
+} kvq_rope_layout;
+
+/* How the frequencies are scaled by `factor` (the ratio of the longer context):
+ *   NONE     w_j
+ *   LINEAR   w_j / factor (positions interpolated)
+ *   BASE     base replaced by base * factor^(r / (r - 2)), r = rot_dim: the slowest pair is
+ *            slowed by factor, the fastest kept (rot_dim 2 has only the fastest)
+ *   BY_PARTS pairs that make many turns over the original context are kept, those that make
+ *            few are interpolated: w_j * (g + (1 - g) / factor) with
+ *            g = clamp((original_context * w_j / 2 pi - low_turns) /
+ *                      (high_turns - low_turns), 0, 1) */
+typedef enum kvq_rope_scale_kind {
+  KVQ_ROPE_SCALE_NONE = 0,
+  KVQ_ROPE_SCALE_LINEAR = 1,
+  KVQ_ROPE_SCALE_BASE = 2,
+  KVQ_ROPE_SCALE_BY_PARTS = 3
+} kvq_rope_scale_kind;
+
+typedef struct kvq_rope_scaling {
+  int32_t kind;            /* kvq_rope_scale_kind */
+  double factor;           /* > 0; unused by NONE */
+  double original_context; /* BY_PARTS: tokens, > 0 */
+  double low_turns;        /* BY_PARTS: 0 <= low_turns < high_turns */
+  double high_turns;
+} kvq_rope_scaling;
+
+/* Frequencies for kvq_rope.turns, computed on the host in double precision: turns[j] is the
+ * fraction of a full turn per token, w_j / 2 pi modulo 1, in 64-bit fixed point (2^64 = one
+ * turn), so that a kernel reduces position * w_j exactly whatever the position.  Host output
+ * turns [rot_dim / 2], to be uploaded; scaling NULL is NONE.  rot_dim even, 2..256; base and
+ * the scaling's numbers finite and in the ranges above, else KVQ_ERR_INVALID_ARGUMENT. */
+KVQ_API kvq_status kvq_rope_table(double base, int32_t rot_dim, const kvq_rope_scaling* scaling, uint64_t* turns);
+
+typedef struct kvq_rope {
+  int32_t rot_dim; /* elements of a head that turn: even, 2..head_dim */
+  int32_t layout;  /* kvq_rope_layout */
+  const uint64_t* turns; /* device [rot_dim / 2], 8-byte aligned (kvq_rope_table) */
+  float scale;     /* factor of cos and sin (1, or a long-context attention factor) */
+} kvq_rope;
+
+/* Heads of a layer, [num_tokens][num_heads][head_dim] fp16 with strides in elements (>= 0,
+ * neighbouring elements of a head adjacent), so that q, k and v may be views of one
+ * projection's output.  `out` is separate or `x` itself with the same strides (in place);
+ * its rows may not overlap one another.  2-byte alignment is enough; addresses and strides
+ * that are multiples of 16 bytes, with rot_dim a multiple of 16, run on wide accesses. */
+typedef struct kvq_heads {
+  const uint16_t* x;
+  uint16_t* out; /* unused (may be NULL) where a call only reads */
+  int32_t num_heads;
+  int64_t x_token_stride, x_head_stride;
+  int64_t out_token_stride, out_head_stride;
+} kvq_heads;
+
+/* Turn the heads of `a` (queries, say) and `b` (keys; may be NULL) by their tokens'
+ * positions, in one launch.
+ *   positions : int32 [num_tokens], any value (negative ones turn backwards)
+ *   transpose : 0, or 1 for the transposed map, scale * R(-theta): the gradient with respect
+ *               to x of a call with transpose 0, given the gradient of out (with scale 1 also
+ *               the inverse)
+ * head_dim 64, 128 or 256 (else KVQ_ERR_UNSUPPORTED).  Angles are exact modulo a turn, cos
+ * and sin float32, the products float32 rounded once to fp16. */
+KVQ_API kvq_status kvq_rope_apply(const kvq_rope* rope, const int32_t* positions, const kvq_heads* a,
+                                  const kvq_heads* b, int32_t num_tokens, int32_t head_dim, int32_t transpose,
+                                  void* stream);
+
+/* A decode step's (or a prompt chunk's) new tokens in one call: keys are turned by their
+ * positions and appended as kvq_quantize_append appends them (the turned key goes on in
+ * float32, with no rounding to fp16 in between, and is never written back), values are
+ * appended, and queries, where given, are turned as kvq_rope_apply turns them.
+ *   k, v : heads of the new tokens, num_heads = the cache's; `out` unused.  Either may be
+ *          NULL (not both, unless num_tokens is 0).  Addresses 16-byte aligned, strides
+ *          multiples of 8 elements (else KVQ_ERR_INVALID_ARGUMENT)
+ *   q    : heads to turn, or NULL (every token's, whatever its slot)
+ *   positions, slot_mapping : int32 [num_tokens]; slots as in kvq_quantize_append
+ * The cache's sign vectors must be 16-byte aligned (else KVQ_ERR_INVALID_ARGUMENT), and
+ * num_tokens x num_kv_heads at most 2^28.  Up to 16384 vectors per side take one launch
+ * (queries whose rows are not of 16-byte units one more); larger appends one launch for the
+ * queries and one per side. */
+KVQ_API kvq_status kvq_rope_append(const kvq_cache* cache, const kvq_rope* rope, const int32_t* positions,
+                                   const kvq_heads* k, const kvq_heads* v, const kvq_heads* q, int32_t num_tokens,
+                                   const int32_t* slot_mapping, void* stream);
+
+/* Read cached tokens back: the vectors that attention sees, with the rotation undone.
+ *   slots        : int32 [num_tokens] pool slots; a negative or out-of-range slot leaves its
+ *                  rows of the outputs as they were; a slot may appear more than once
+ *   k_out, v_out : fp16 [num_tokens][num_kv_heads][head_dim], 16-byte aligned; either may be
+ *                  NULL (not both, unless num_tokens is 0)
+ * Keys with a residual sketch come back as code part plus the sketch's estimate of the
+ * residual, ||r~|| sqrt(pi/2) / KVQ_QJL_DIM * sum_j z_j S_j, whose inner product with a query
+ * is what decode adds; keys with an outlier stream with q_j s added at their channels.
+ * The cache's sign vectors must be 16-byte aligned (else KVQ_ERR_INVALID_ARGUMENT).
+ * Arithmetic in float32, rounded once to fp16.  One launch. */
+KVQ_API kvq_status kvq_dequantize(const kvq_cache* cache, const int32_t* slots, int32_t num_tokens, uint16_t* k_out,
+                                  uint16_t* v_out, void* stream);
+
 /* Workspace bytes kvq_decode_attention needs for these tiers and shapes (host output).
  * split_tokens: tokens per split-K chunk (a multiple of page_size), or 0 to let the
  * library choose; pass the same value to kvq_decode_attention.  The chunks of the longest

@@ -68,6 +68,31 @@ class KvqDecodeOptions(ctypes.Structure):
     _fields_ = [("score_gate", ctypes.c_int32), ("spike_flags", ctypes.c_void_p), ("status", ctypes.c_void_p)]
 
 
+class KvqRopeScaling(ctypes.Structure):
+    """Mirror of ``struct kvq_rope_scaling``."""
+
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("original_context", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double)]
+
+
+class KvqRope(ctypes.Structure):
+    """Mirror of ``struct kvq_rope``."""
+
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("turns", ctypes.c_void_p),
+                ("scale", ctypes.c_float)]
+
+
+class KvqHeads(ctypes.Structure):
+    """Mirror of ``struct kvq_heads``."""
+
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("num_heads", ctypes.c_int32),
+                ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
+
 SCORE_GATE_NATS = 16.0
 # device-side error bits of a decode call (kvq_decode_options.status)
 DEVERR_COPY_TIMEOUT, DEVERR_PAGE_INDEX, DEVERR_SEQ_LEN = 1, 2, 4
@@ -103,6 +128,12 @@ def lib() -> ctypes.CDLL:
             "kvq_decode_attention": [ctypes.POINTER(KvqTierView), i32, vp, i32, i32, i32, vp, vp, sz, vp],
             "kvq_decode_attention_ex": [ctypes.POINTER(KvqTierView), i32, vp, i32, i32, i32, vp, vp, sz,
                                         ctypes.POINTER(KvqDecodeOptions), vp],
+            "kvq_rope_table": [ctypes.c_double, i32, ctypes.POINTER(KvqRopeScaling), vp],
+            "kvq_rope_apply": [ctypes.POINTER(KvqRope), vp, ctypes.POINTER(KvqHeads), ctypes.POINTER(KvqHeads), i32,
+                               i32, i32, vp],
+            "kvq_rope_append": [ctypes.POINTER(KvqCache), ctypes.POINTER(KvqRope), vp, ctypes.POINTER(KvqHeads),
+                                ctypes.POINTER(KvqHeads), ctypes.POINTER(KvqHeads), i32, vp, vp],
+            "kvq_dequantize": [ctypes.POINTER(KvqCache), vp, i32, vp, vp, vp],
             "kvq_decode_attention_noalloc": [ctypes.POINTER(KvqTierView), i32, vp, i32, i32, i32, vp, vp],
         }
         for name, args in sigs.items():
@@ -211,6 +242,17 @@ def kvq_make_signs(seed: int, layer: int, num_kv_heads: int, head_dim: int):
     return k, v
 
 
+def kvq_rope_table(base: float, rot_dim: int, scaling="none", factor: float = 1.0, original_context: float = 0.0,
+                   low_turns: float = 0.0, high_turns: float = 0.0) -> np.ndarray:
+    """uint64 [rot_dim / 2]: the fraction of a turn per token of every pair (host, by the
+    library).  scaling: "none" | "linear" | "base" | "by_parts"."""
+    turns = np.zeros(max(0, rot_dim // 2), dtype=np.uint64)
+    s = KvqRopeScaling(ROPE_SCALINGS.get(scaling, scaling), factor, original_context, low_turns, high_turns)
+    _check(lib().kvq_rope_table(base, rot_dim, ctypes.byref(s), turns.ctypes.data if turns.size else None),
+           "kvq_rope_table")
+    return turns
+
+
 # ----------------------------------------------------------------------------- GPU entry points
 
 
@@ -245,6 +287,100 @@ def kvq_requantize(src: KvqCache, src_slots, dst: KvqCache, dst_slots, stream=No
     _arg(dst_slots, "dst_slots", "int32", (None,), min_numel=int(src_slots.shape[0]))
     _check(lib().kvq_requantize(ctypes.byref(src), _ptr(src_slots), ctypes.byref(dst), _ptr(dst_slots),
                                 int(src_slots.shape[0]), _stream(stream)), "kvq_requantize")
+
+
+def _on_device(stream, *tensors) -> None:
+    """The tensors of one call lie on one device, which is the current one unless the caller
+    names a stream (of that device)."""
+    devices = {t.device for t in tensors if t is not None and hasattr(t, "device")}
+    if len(devices) > 1:
+        raise ValueError(f"tensors of one call on different devices: {sorted(map(str, devices))}")
+    if devices and stream is None:
+        import torch
+        d = devices.pop()
+        if d.index is not None and d.index != torch.cuda.current_device():
+            raise ValueError(f"tensors on {d}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _check_heads(x, name: str, tokens: int, head_dim: int, num_heads=None, out=None) -> None:
+    """x (and out, where given, of its shape): fp16 [tokens, heads, head_dim], the elements of a
+    head adjacent, token and head strides free."""
+    for t, what in ((x, name), (out, name + "_out")):
+        if t is None:
+            continue
+        _arg(t, what, "float16", (tokens, num_heads, head_dim) if t is x else tuple(x.shape))
+        if t.stride(2) != 1:
+            raise ValueError(f"the elements of a head of {what} must be adjacent")
+    if x is not None and x.shape[1] == 0:
+        raise ValueError(f"{name} needs at least one head")
+
+
+def _heads(x, out=None, write: bool = False) -> Optional[KvqHeads]:
+    """Checked heads as the C ABI's struct; write: the call writes `out`, or x itself where it
+    is None."""
+    if x is None:
+        return None
+    h = KvqHeads()
+    h.num_heads = x.shape[1]
+    h.x, h.x_token_stride, h.x_head_stride = x.data_ptr(), x.stride(0), x.stride(1)
+    if write:
+        dst = x if out is None else out
+        h.out, h.out_token_stride, h.out_head_stride = dst.data_ptr(), dst.stride(0), dst.stride(1)
+    return h
+
+
+def kvq_rope_apply(rope: "Rope", positions, q, k=None, q_out=None, k_out=None, transpose: bool = False,
+                   stream=None) -> None:
+    """q [T, Hq, D], k [T, Hkv, D] (or None): fp16 CUDA tensors or strided views; positions:
+    int32 [T].  Writes q_out / k_out (any strides), or q / k themselves where they are None.
+    transpose: the transposed map (the gradient with respect to q and k)."""
+    _arg(q, "q", "float16", (None, None, None))
+    t, d = int(q.shape[0]), int(q.shape[2])
+    _dense(positions)
+    _arg(positions, "positions", "int32", (None,), min_numel=t)
+    _check_heads(q, "q", t, d, out=q_out)
+    _check_heads(k, "k", t, d, out=k_out)
+    _on_device(stream, q, k, q_out, k_out, positions)
+    a, b = _heads(q, q_out, True), _heads(k, k_out, True)
+    _check(lib().kvq_rope_apply(ctypes.byref(rope.struct), _ptr(positions), ctypes.byref(a), ctypes.byref(b) if b else None, t, d,
+                                1 if transpose else 0, _stream(stream)), "kvq_rope_apply")
+
+
+def kvq_rope_append(cache: KvqCache, rope: "Rope", positions, k, v, slot_mapping, q=None, q_out=None,
+                    stream=None) -> None:
+    """Keys turned by their positions and appended, values appended, queries (if given) turned
+    into q_out (or in place).  k, v: fp16 [T, Hkv, D] CUDA tensors or strided views (either may
+    be None); q: fp16 [T, Hq, D]; positions, slot_mapping: int32 [T]."""
+    if k is None and v is None:
+        raise ValueError("kvq_rope_append needs k or v")
+    x = k if k is not None else v
+    _arg(x, "k" if k is not None else "v", "float16", (None, cache.num_kv_heads, cache.head_dim))
+    t, d = int(x.shape[0]), cache.head_dim
+    _dense(positions, slot_mapping)
+    _arg(positions, "positions", "int32", (None,), min_numel=t)
+    _arg(slot_mapping, "slot_mapping", "int32", (None,), min_numel=t)
+    _check_heads(k, "k", t, d, cache.num_kv_heads)
+    _check_heads(v, "v", t, d, cache.num_kv_heads)
+    _check_heads(q, "q", t, d, out=q_out)
+    _on_device(stream, k, v, q, q_out, positions, slot_mapping)
+    kh, vh, qh = (ctypes.byref(h) if h else None for h in (_heads(k), _heads(v), _heads(q, q_out, True)))
+    _check(lib().kvq_rope_append(ctypes.byref(cache), ctypes.byref(rope.struct), _ptr(positions), kh, vh, qh, t,
+                                 _ptr(slot_mapping), _stream(stream)), "kvq_rope_append")
+
+
+def kvq_dequantize(cache: KvqCache, slots, k_out=None, v_out=None, stream=None) -> None:
+    """Cached tokens back as fp16 vectors: slots int32 [T]; k_out, v_out fp16 [T, Hkv, D]
+    (either may be None), written where the slot is in range."""
+    _dense(slots, k_out, v_out)
+    if k_out is None and v_out is None:
+        raise ValueError("kvq_dequantize needs k_out or v_out")
+    _arg(slots, "slots", "int32", (None,))
+    t = int(slots.shape[0])
+    for x, name in ((k_out, "k_out"), (v_out, "v_out")):
+        _arg(x, name, "float16", (t, cache.num_kv_heads, cache.head_dim))
+    _on_device(stream, slots, k_out, v_out)
+    _check(lib().kvq_dequantize(ctypes.byref(cache), _ptr(slots), t, _ptr(k_out), _ptr(v_out), _stream(stream)),
+           "kvq_dequantize")
 
 
 def _views(tiers: Sequence["TierView"], batch: int = 0):
@@ -387,6 +523,24 @@ class PagedCache:
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.k_rows, self.v_rows, self.k_aux, self.v_aux)
                    if t is not None)
+
+
+class Rope:
+    """Owns the device table of a layer's rotary frequencies and its ``KvqRope`` struct.
+
+    rot_dim: elements of a head that turn; layout: "half" | "interleaved"; scaling: "none" |
+    "linear" | "base" | "by_parts" with its factor (and original_context, low_turns,
+    high_turns for "by_parts"); scale: factor of cos and sin."""
+
+    def __init__(self, rot_dim, layout="half", base=10000.0, scaling="none", factor=1.0, original_context=0.0,
+                 low_turns=0.0, high_turns=0.0, scale=1.0, device="cuda"):
+        import torch
+        table = kvq_rope_table(base, rot_dim, scaling, factor, original_context, low_turns, high_turns)
+        self.turns = torch.from_numpy(table.view(np.int64)).to(torch.device(device))  # the bits, as they are
+        s = KvqRope()
+        s.rot_dim, s.layout, s.scale = rot_dim, ROPE_LAYOUTS.get(layout, layout), scale
+        s.turns = _ptr(self.turns)
+        self.struct = s
 
 
 class TierView:

@@ -282,14 +282,10 @@ __device__ __forceinline__ void load_signs(const int8_t* signs_h, int sub, uint3
   }
 }
 
-// y = H (s * x) (unnormalised) of one vector: thread `sub` ends with coordinates
-// [32 sub, 32 sub + 32) in y.  xv: the vector's fp16 coordinates; area: the vector's shared
-// transpose area; vw: the vector's position in its warp.
+// The thread's 32 fp16 coordinates of a vector, as 16 words in run order.
 template <int TPV>
-__device__ __forceinline__ void load_rotate(const uint16_t* xv, const uint32_t (&sw)[8], uint32_t area, int sub,
-                                            int vw, unsigned gmask, float (&y)[32]) {
+__device__ __forceinline__ void load_runs(const uint16_t* xv, int sub, uint32_t (&xw)[16]) {
   constexpr int R = 32 / TPV;
-  uint32_t xw[16];
 #pragma unroll
   for (int k = 0; k < TPV; ++k) {
     const uint16_t* src = xv + 32 * k + R * sub;
@@ -308,17 +304,14 @@ __device__ __forceinline__ void load_rotate(const uint16_t* xv, const uint32_t (
       }
     }
   }
-  // signs: bytes 2j, 2j+1 (int8 +-1, bit 7 set for -1) -> fp16 sign bits 15, 31 of pair j;
-  // the first stage (index bit 0, a pair's two halves) in scalar
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint32_t m = __byte_perm(sw[j >> 1], 0, (j & 1) ? 0x3424 : 0x1404) & 0x80008000u;
-    const uint32_t xs = xw[j] ^ m;
-    const __half2 h2 = *reinterpret_cast<const __half2*>(&xs);
-    const float a = __low2float(h2), c = __high2float(h2);
-    y[2 * j] = a + c;
-    y[2 * j + 1] = a - c;
-  }
+}
+
+// The rotation after its first stage: thread `sub` passes its runs (stage 0 done) and ends
+// with coordinates [32 sub, 32 sub + 32).  area: the vector's shared transpose area; vw: the
+// vector's position in its warp.
+template <int TPV>
+__device__ __forceinline__ void rotate_runs(uint32_t area, int sub, int vw, unsigned gmask, float (&y)[32]) {
+  constexpr int R = 32 / TPV;
   // the other four register stages on f32x2 pairs
 #pragma unroll
   for (int hs = 2; hs < 32; hs <<= 1) {
@@ -366,6 +359,28 @@ __device__ __forceinline__ void load_rotate(const uint16_t* xv, const uint32_t (
       }
     }
   }
+}
+
+// y = H (s * x) (unnormalised) of one vector: thread `sub` ends with coordinates
+// [32 sub, 32 sub + 32) in y.  xv: the vector's fp16 coordinates; area: the vector's shared
+// transpose area; vw: the vector's position in its warp.
+template <int TPV>
+__device__ __forceinline__ void load_rotate(const uint16_t* xv, const uint32_t (&sw)[8], uint32_t area, int sub,
+                                            int vw, unsigned gmask, float (&y)[32]) {
+  uint32_t xw[16];
+  load_runs<TPV>(xv, sub, xw);
+  // signs: bytes 2j, 2j+1 (int8 +-1, bit 7 set for -1) -> fp16 sign bits 15, 31 of pair j;
+  // the first stage (index bit 0, a pair's two halves) in scalar
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t m = __byte_perm(sw[j >> 1], 0, (j & 1) ? 0x3424 : 0x1404) & 0x80008000u;
+    const uint32_t xs = xw[j] ^ m;
+    const __half2 h2 = *reinterpret_cast<const __half2*>(&xs);
+    const float a = __low2float(h2), c = __high2float(h2);
+    y[2 * j] = a + c;
+    y[2 * j + 1] = a - c;
+  }
+  rotate_runs<TPV>(area, sub, vw, gmask, y);
 }
 
 // One vector's TPV lanes: y holds coordinates [sub * kE, (sub + 1) * kE) of the rotated

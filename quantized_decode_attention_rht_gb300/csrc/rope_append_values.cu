@@ -1,0 +1,8 @@
+// Large appends of strided values: the value side's instances (rope_append_large.cuh).
+#include "rope_append_large.cuh"
+
+namespace kvq {
+cudaError_t launch_append_values(const LargeParams& p, int head_dim, int sms, cudaStream_t stream) {
+  return launch_large_dim<false>(p, head_dim, sms, stream);
+}
+}  // namespace kvq

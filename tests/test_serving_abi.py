@@ -1,0 +1,212 @@
+"""The serving entry points without a GPU: the rotary table against the oracle, and argument
+checks that fail before anything is launched."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import rope as orope
+from tests.test_binding_checks import Dev
+
+KINDS = [("none", 1.0, 0.0, 0.0, 0.0), ("linear", 4.0, 0.0, 0.0, 0.0), ("base", 8.0, 0.0, 0.0, 0.0),
+         ("by_parts", 8.0, 8192.0, 1.0, 32.0)]
+INVALID, UNSUPPORTED = 1, 2
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    from quantized_decode_attention_rht_gb300 import build
+    build.build()
+    import quantized_decode_attention_rht_gb300 as m
+    m.lib()
+    return m
+
+
+class Heads(Dev):
+    """A strided stand-in of heads."""
+
+    def stride(self, i=None):
+        return self.t.stride() if i is None else self.t.stride(i)
+
+
+def dev(shape, dtype):
+    return Dev(torch.zeros(shape, dtype=dtype))
+
+
+def heads(*shape, dtype=torch.float16):
+    return Heads(torch.zeros(shape, dtype=dtype))
+
+
+@pytest.mark.parametrize("rot", [2, 6, 64, 128, 256])
+@pytest.mark.parametrize("kind,factor,context,low,high", KINDS)
+def test_table_matches_oracle(kvq, rot, kind, factor, context, low, high):
+    t = kvq.kvq_rope_table(10000.0, rot, kind, factor, context, low, high)
+    w = orope.frequencies(10000.0, rot, kind, factor, context, low, high)
+    want = np.array([int(math.fmod(x / (2 * math.pi), 1.0) * 2.0 ** 64) for x in w], dtype=object)
+    # pow and the scaling's few operations: a few units in the last of 53 bits
+    for got, x in zip(t.tolist(), want):
+        assert abs(int(got) - x) <= 16 * 2.0 ** -53 * x + 1
+
+
+def test_table_wraps_whole_turns(kvq):
+    # base below 1 gives pairs that turn more than once per token; whole turns do not matter
+    t = kvq.kvq_rope_table(0.001, 4)
+    w = orope.frequencies(0.001, 4)
+    assert w[1] > 2 * math.pi
+    assert abs(int(t[1]) / 2.0 ** 64 - math.fmod(w[1] / (2 * math.pi), 1.0)) < 1e-14
+
+
+def test_table_refusals(kvq):
+    for args in [(0.0, 64), (-1.0, 64), (math.inf, 64), (math.nan, 64), (1e4, 0), (1e4, 3), (1e4, 258), (1e4, -2),
+                 (1e4, 64, 4), (1e4, 64, -1), (1e4, 64, "linear", 0.0), (1e4, 64, "linear", math.nan),
+                 (1e4, 64, "base", math.inf), (1e4, 64, "by_parts", 8.0, 0.0, 1.0, 2.0),
+                 (1e4, 64, "by_parts", 8.0, 1e4, 2.0, 2.0), (1e4, 64, "by_parts", 8.0, 1e4, -1.0, 2.0),
+                 (1e4, 64, "by_parts", 8.0, 1e4, 1.0, math.inf), (1e4, 64, "by_parts", 8.0, 1e4, math.nan, 2.0)]:
+        with pytest.raises(kvq.KvqError) as e:
+            kvq.kvq_rope_table(*args)
+        assert e.value.status == INVALID, args
+    assert kvq.lib().kvq_rope_table(1e4, 64, None, None) == INVALID
+
+
+def rope_struct(kvq, rot=128, layout=0, turns=64):
+    s = kvq.KvqRope()
+    s.rot_dim, s.layout, s.turns, s.scale = rot, layout, turns, 1.0
+    return s
+
+
+def heads_struct(kvq, x=256, out=4096, n=2, xt=256, xh=128, ot=256, oh=128):
+    h = kvq.KvqHeads()
+    h.x, h.out, h.num_heads = x, out, n
+    h.x_token_stride, h.x_head_stride, h.out_token_stride, h.out_head_stride = xt, xh, ot, oh
+    return h
+
+
+def test_rope_apply_refusals(kvq):
+    """Every refusal is taken on the host; the addresses are never read."""
+    f = kvq.lib().kvq_rope_apply
+    ref = ctypes.byref
+
+    def call(rope=None, pos=64, a=None, b=None, t=3, d=128, tr=0):
+        rope = rope if rope is not None else rope_struct(kvq)
+        a = a if a is not None else heads_struct(kvq)
+        return f(ref(rope), pos, ref(a), ref(b) if b is not None else None, t, d, tr, None)
+
+    n = kvq.kvq_kernel_launches()
+    assert call(t=0) == 0  # nothing to do
+    assert f(None, 64, ref(heads_struct(kvq)), None, 3, 128, 0, None) == INVALID
+    assert f(ref(rope_struct(kvq)), 64, None, None, 3, 128, 0, None) == INVALID
+    for d in (0, 32, 96, 512):
+        assert call(d=d) == UNSUPPORTED
+    for bad in (dict(rot=0), dict(rot=3), dict(rot=130), dict(rot=-2), dict(layout=2), dict(layout=-1),
+                dict(turns=0), dict(turns=68)):
+        assert call(rope=rope_struct(kvq, **bad)) == INVALID, bad
+    assert call(t=-1) == INVALID and call(pos=None) == INVALID and call(pos=66) == INVALID and call(tr=2) == INVALID
+    for bad in (dict(x=0), dict(out=0), dict(x=257), dict(out=4097), dict(n=0), dict(xt=-1), dict(xh=-8), dict(ot=-1),
+                dict(ot=200), dict(oh=64), dict(ot=0), dict(xt=1 << 40),
+                dict(out=256, ot=512)):  # in place with other strides
+        assert call(a=heads_struct(kvq, **bad)) == INVALID, bad
+        assert call(b=heads_struct(kvq, **bad)) == INVALID, bad
+    assert kvq.kvq_kernel_launches() == n
+
+
+def test_rope_append_and_dequantize_refusals(kvq):
+    ref = ctypes.byref
+    d, hkv = 128, 2
+    signs = np.ones((hkv, d), dtype=np.int8)
+    cache = kvq.PagedCache(d, hkv, 4, "codebook", "int4_g32", 4, 0, signs, signs, device="cpu")
+
+    def struct(**kw):
+        s = kvq.KvqCache()
+        ctypes.memmove(ref(s), ref(cache.struct), ctypes.sizeof(s))
+        # addresses that are never read
+        s.k_rows, s.v_rows, s.k_aux, s.v_aux, s.k_signs, s.v_signs = (1 << 12,) * 6
+        for name, v in kw.items():
+            setattr(s, name, v)
+        return s
+
+    def append(c=None, rope=None, pos=64, k=0, v=0, q=None, t=3, slots=64):
+        k = heads_struct(kvq, out=None) if k == 0 else k
+        v = heads_struct(kvq, out=None) if v == 0 else v
+        return kvq.lib().kvq_rope_append(ref(c or struct()), ref(rope or rope_struct(kvq)), pos,
+                                         ref(k) if k else None, ref(v) if v else None, ref(q) if q else None, t,
+                                         slots, None)
+
+    n = kvq.kvq_kernel_launches()
+    assert append(t=0) == 0
+    assert append(k=None, v=None) == INVALID
+    assert append(pos=None) == INVALID and append(slots=None) == INVALID and append(slots=66) == INVALID
+    assert append(t=-1) == INVALID
+    assert append(rope=rope_struct(kvq, rot=256)) == INVALID
+    for bad in (dict(x=264), dict(xt=260), dict(xh=132), dict(n=3), dict(x=0), dict(xt=-256)):
+        assert append(k=heads_struct(kvq, **bad)) == INVALID, bad
+        assert append(v=heads_struct(kvq, **bad)) == INVALID, bad
+    assert append(q=heads_struct(kvq, out=0)) == INVALID
+    assert append(c=struct(k_bounds=None)) == INVALID
+    assert append(c=struct(k_signs=(1 << 12) + 8)) == INVALID
+    assert append(c=struct(k_rows=None)) == INVALID
+    assert append(c=struct(head_dim=96)) == UNSUPPORTED
+    assert append(c=struct(v_format=4)) in (INVALID, UNSUPPORTED)  # a sketch on values
+    assert append(t=(1 << 28) // hkv + 1) == INVALID
+
+    def read(c=None, slots=64, t=3, k=256, v=256):
+        return kvq.lib().kvq_dequantize(ref(c or struct()), slots, t, k, v, None)
+
+    assert read(t=0) == 0
+    assert read(k=None, v=None) == INVALID and read(slots=None) == INVALID and read(slots=65) == INVALID
+    assert read(t=-1) == INVALID and read(k=264) == INVALID and read(v=258) == INVALID
+    assert read(c=struct(v_signs=(1 << 12) + 4)) == INVALID
+    assert read(c=struct(k_rows=8)) == INVALID
+    assert read(c=struct(k_centroids=None)) == INVALID
+    assert read(c=struct(num_pages=0)) == 0  # a pool without pages holds no slot
+    assert kvq.lib().kvq_dequantize(None, 64, 3, 256, 256, None) == INVALID
+    assert kvq.kvq_kernel_launches() == n
+
+
+def test_binding_checks(kvq):
+    d, hkv, hq, t = 128, 2, 4, 5
+    signs = np.ones((hkv, d), dtype=np.int8)
+    cache = kvq.PagedCache(d, hkv, 4, "codebook", "codebook", 4, 4, signs, signs, device="cpu").struct
+    rope = kvq.Rope(128, "half", device="cpu")
+    pos, slots = dev((t,), torch.int32), dev((t,), torch.int32)
+    q, k = heads(t, hq, d), heads(t, hkv, d)
+    with pytest.raises(AssertionError):  # valid: the call goes as far as the pointers
+        kvq.kvq_rope_apply(rope, pos, q, k)
+    with pytest.raises(ValueError, match="CUDA"):
+        kvq.kvq_rope_apply(rope, pos, torch.zeros((t, hq, d), dtype=torch.float16))
+    with pytest.raises(TypeError):
+        kvq.kvq_rope_apply(rope, pos, heads(t, hq, d, dtype=torch.float32))
+    with pytest.raises(TypeError):
+        kvq.kvq_rope_apply(rope, dev((t,), torch.int64), q)
+    with pytest.raises(ValueError, match="elements"):
+        kvq.kvq_rope_apply(rope, dev((t - 1,), torch.int32), q)
+    with pytest.raises(ValueError, match="adjacent"):
+        kvq.kvq_rope_apply(rope, pos, Heads(torch.zeros((t, d, hq), dtype=torch.float16).transpose(1, 2)))
+    with pytest.raises(ValueError, match="shape"):
+        kvq.kvq_rope_apply(rope, pos, q, heads(t + 1, hkv, d))
+    with pytest.raises((ValueError, AssertionError)):
+        kvq.kvq_rope_apply(rope, pos, q, q_out=heads(t, hq + 1, d))
+    with pytest.raises(ValueError, match="head"):
+        kvq.kvq_rope_apply(rope, pos, heads(t, 0, d))
+
+    with pytest.raises(AssertionError):
+        kvq.kvq_rope_append(cache, rope, pos, k, k, slots, q)
+    with pytest.raises(ValueError):
+        kvq.kvq_rope_append(cache, rope, pos, None, None, slots, q)
+    with pytest.raises(ValueError, match="shape"):
+        kvq.kvq_rope_append(cache, rope, pos, heads(t, hkv + 1, d), None, slots)
+    with pytest.raises(ValueError, match="shape"):
+        kvq.kvq_rope_append(cache, rope, pos, k, heads(t - 1, hkv, d), slots)
+    with pytest.raises(ValueError, match="elements"):
+        kvq.kvq_rope_append(cache, rope, pos, k, k, dev((t - 1,), torch.int32))
+
+    out = dev((t, hkv, d), torch.float16)
+    with pytest.raises(AssertionError):
+        kvq.kvq_dequantize(cache, slots, out, None)
+    with pytest.raises(ValueError):
+        kvq.kvq_dequantize(cache, slots)
+    with pytest.raises(ValueError, match="shape"):
+        kvq.kvq_dequantize(cache, slots, dev((t - 1, hkv, d), torch.float16))
+    with pytest.raises(TypeError):
+        kvq.kvq_dequantize(cache, slots, out, dev((t, hkv, d), torch.float32))
