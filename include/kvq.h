@@ -48,6 +48,7 @@ extern "C" {
 
 #define KVQ_MAX_TIERS 4  /* decode attends over at most this many tiers at once */
 #define KVQ_MAX_SPLITS 1024  /* split-K chunks per sequence, summed over the tiers */
+#define KVQ_MAX_PREFIX_GROUPS 256 /* groups of sequences sharing a prefix in one call */
 #define KVQ_INT4_GROUP 32 /* coordinates sharing one fp16 scale in KVQ_FMT_INT4_G32 */
 #define KVQ_QJL_DIM 128   /* rows m of the residual sketch's projection (KVQ_FMT_CODEBOOK_QJL) */
 #define KVQ_OUTLIER_CHANNELS 8  /* outlier channels per kv head (KVQ_FMT_CODEBOOK_OUTLIER) */
@@ -447,6 +448,48 @@ KVQ_API kvq_status kvq_decode_attention_ex(const kvq_tier_view* tiers, int32_t n
                                            int32_t num_q_heads, int32_t split_tokens,
                                            float* out, void* workspace, size_t workspace_bytes,
                                            const kvq_decode_options* options, void* stream);
+
+/* Decode attention for groups of sequences that share a cached prefix (a system prompt, the
+ * samples of one prompt).  The prefix's pages are read and decoded once for all query heads of a
+ * group, on the tensor cores, instead of once per sequence:
+ *   out[b][h] = softmax_t( q[b][h] . K[t] / sqrt(D) ) V[t]
+ * over every token of the prefix of b's group and every token of b's own tiers.
+ *   prefix_tiers  : host array [num_prefix_tiers], 1 or more; block_table int32
+ *                   [num_groups][max_pages] and seq_lens int32 [num_groups] hold one row per
+ *                   GROUP (a length of 0 is allowed).  The prefix may lie in the same cache as
+ *                   the sequences' tiers
+ *   group_offsets : HOST int32 [num_groups + 1], not decreasing, in [0, batch]: group i is the
+ *                   sequences group_offsets[i] .. group_offsets[i + 1] - 1 (none where the two
+ *                   are equal); sequences before the first or from the last on have no prefix.
+ *                   1 <= num_groups <= KVQ_MAX_PREFIX_GROUPS
+ *   tiers         : host array [num_tiers] as in kvq_decode_attention (the tokens that each
+ *                   sequence has of its own); num_tiers 0 where there are none
+ *   q             : fp16 [batch][num_q_heads][head_dim], 16-byte aligned
+ *   out           : fp16 [batch][num_q_heads][head_dim], 16-byte aligned
+ *   workspace     : >= kvq_decode_shared_workspace_size() bytes for the same offsets and shapes,
+ *                   256-byte aligned, scratch only.  Calls that may overlap on the GPU (two
+ *                   streams, two captured graphs) need one each
+ *   status        : optional device int32: the call's KVQ_DEVERR_* bits (as in
+ *                   kvq_decode_options; not written by a call with batch 0)
+ * All tiers agree in head_dim, num_kv_heads, page_size and signs, and num_prefix_tiers +
+ * num_tiers <= KVQ_MAX_TIERS.  A call captured into a graph keeps its group offsets; lengths and
+ * block tables are read when it runs.
+ * The output is fp16, and so is what the tensor cores multiply (rotated queries, decoded rows
+ * that are not fp16 values already, softmax weights), with float32 scores, sums and
+ * accumulators: within about 2^-10 of the attention-weighted mean of |V|, where
+ * kvq_decode_attention gives float32.  Prefix tiers run so for head_dim 128, any page size, and
+ * format pairs fp16/fp16, fp8/INT4, fp8/fp16 and codebook/codebook; otherwise (head_dim 64 and
+ * 256, keys with a sketch or an outlier stream) the prefix is attended as a tier of every
+ * sequence by kvq_decode_attention's kernels, with its limits and results. */
+KVQ_API kvq_status kvq_decode_shared_workspace_size(const kvq_tier_view* prefix_tiers, int32_t num_prefix_tiers,
+                                                    const int32_t* group_offsets, int32_t num_groups,
+                                                    const kvq_tier_view* tiers, int32_t num_tiers, int32_t batch,
+                                                    int32_t num_q_heads, size_t* bytes);
+KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers, int32_t num_prefix_tiers,
+                                               const int32_t* group_offsets, int32_t num_groups,
+                                               const kvq_tier_view* tiers, int32_t num_tiers, const uint16_t* q,
+                                               int32_t batch, int32_t num_q_heads, uint16_t* out, void* workspace,
+                                               size_t workspace_bytes, int32_t* status, void* stream);
 
 /* Decode attention for callers that cannot allocate device memory.
  *

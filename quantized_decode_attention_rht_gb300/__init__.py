@@ -134,6 +134,10 @@ def lib() -> ctypes.CDLL:
             "kvq_rope_append": [ctypes.POINTER(KvqCache), ctypes.POINTER(KvqRope), vp, ctypes.POINTER(KvqHeads),
                                 ctypes.POINTER(KvqHeads), ctypes.POINTER(KvqHeads), i32, vp, vp],
             "kvq_dequantize": [ctypes.POINTER(KvqCache), vp, i32, vp, vp, vp],
+            "kvq_decode_shared_workspace_size": [ctypes.POINTER(KvqTierView), i32, vp, i32, ctypes.POINTER(KvqTierView),
+                                                 i32, i32, i32, szp],
+            "kvq_decode_attention_shared": [ctypes.POINTER(KvqTierView), i32, vp, i32, ctypes.POINTER(KvqTierView),
+                                            i32, vp, i32, i32, vp, vp, sz, vp, vp],
             "kvq_decode_attention_noalloc": [ctypes.POINTER(KvqTierView), i32, vp, i32, i32, i32, vp, vp],
         }
         for name, args in sigs.items():
@@ -438,6 +442,47 @@ def kvq_decode_attention(tiers, q, out, workspace, split_tokens: int = 0, stream
     opts = KvqDecodeOptions(1 if score_gate else 0, _ptr(spike_flags), _ptr(status))
     _check(lib().kvq_decode_attention_ex(arr, len(tiers), _ptr(q), b, hq, split_tokens, _ptr(out), _ptr(workspace),
                                          ws_bytes, ctypes.byref(opts), _stream(stream)), "kvq_decode_attention_ex")
+
+
+def _offsets(group_offsets) -> np.ndarray:
+    off = np.ascontiguousarray(group_offsets, dtype=np.int32)
+    if off.ndim != 1 or off.size < 2:
+        raise ValueError("group_offsets holds num_groups + 1 sequence numbers")
+    return off
+
+
+def kvq_decode_shared_workspace_size(prefix_tiers, group_offsets, tiers, batch: int, num_q_heads: int) -> int:
+    off, n = _offsets(group_offsets), ctypes.c_size_t()
+    pre, own = _views(prefix_tiers), _views(tiers) if tiers else None
+    _check(lib().kvq_decode_shared_workspace_size(pre, len(prefix_tiers), off.ctypes.data, off.size - 1, own,
+                                                  len(tiers or ()), batch, num_q_heads, ctypes.byref(n)),
+           "kvq_decode_shared_workspace_size")
+    return n.value
+
+
+def kvq_decode_attention_shared(prefix_tiers, group_offsets, tiers, q, out, workspace, status=None,
+                                stream=None) -> None:
+    """Decode for groups of sequences that share a cached prefix.  prefix_tiers: TierViews whose
+    block_table [groups, max_pages] and seq_lens [groups] hold one row per group; group_offsets:
+    host sequence of groups + 1 sequence numbers (group i is sequences offsets[i] ..
+    offsets[i + 1] - 1); tiers: the sequences' own TierViews (empty or None: none); q, out: fp16
+    [B, Hq, D]; workspace: uint8 CUDA tensor; status: int32 CUDA tensor of one element."""
+    off = _offsets(group_offsets)
+    _dense(q, out, workspace, status)
+    if not prefix_tiers:
+        raise ValueError("a shared decode needs at least one prefix tier")
+    _arg(q, "q", "float16", (None, None, prefix_tiers[0].cache.struct.head_dim))
+    _arg(out, "out", "float16", tuple(q.shape))
+    _arg(status, "status", "int32", None, min_numel=1)
+    if workspace is None or not getattr(workspace, "is_cuda", False):
+        raise ValueError("workspace must be a CUDA tensor")
+    _on_device(stream, q, out, workspace, status)
+    b, hq = int(q.shape[0]), int(q.shape[1])
+    pre, own = _views(prefix_tiers, off.size - 1), _views(tiers, b) if tiers else None
+    _check(lib().kvq_decode_attention_shared(pre, len(prefix_tiers), off.ctypes.data, off.size - 1, own,
+                                             len(tiers or ()), _ptr(q), b, hq, _ptr(out), _ptr(workspace),
+                                             workspace.numel() * workspace.element_size(), _ptr(status),
+                                             _stream(stream)), "kvq_decode_attention_shared")
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20

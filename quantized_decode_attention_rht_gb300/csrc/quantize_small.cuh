@@ -244,11 +244,9 @@ __device__ __forceinline__ void split_outliers(const int32_t* outl, int lane, fl
   }
 }
 
-// y <- H (s * y) (unnormalised), as load_rotate does it.
+// y <- H y (unnormalised), as load_rotate does it.
 template <int E>
-__device__ __forceinline__ void sign_rotate(const int8_t* sg, int lane, float (&y)[E]) {
-#pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = __ldg(sg + lane * E + e) < 0 ? -y[e] : y[e];
+__device__ __forceinline__ void sign_free_rotate(int lane, float (&y)[E]) {
 #pragma unroll
   for (int hs = 1; hs < E; hs <<= 1) {
 #pragma unroll
@@ -266,6 +264,14 @@ __device__ __forceinline__ void sign_rotate(const int8_t* sg, int lane, float (&
 #pragma unroll
     for (int e = 0; e < E; ++e) y[e] = fmaf(sgn, y[e], __shfl_xor_sync(0xFFFFFFFFu, y[e], m));
   }
+}
+
+// y <- H (s * y).
+template <int E>
+__device__ __forceinline__ void sign_rotate(const int8_t* sg, int lane, float (&y)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] = __ldg(sg + lane * E + e) < 0 ? -y[e] : y[e];
+  sign_free_rotate<E>(lane, y);
 }
 
 // y = x~ for the lane's coordinates, from a stored fp16 row of the rotated vector.

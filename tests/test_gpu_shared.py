@@ -1,0 +1,291 @@
+"""GPU parity of kvq_decode_attention_shared against the float64 oracle, on bytes that the
+oracle wrote.
+
+Tolerance, derived before the first run, u = 2^-11 (half an ulp of fp16, relative).
+A score: the rotated queries are rounded once and the decoded keys at most twice (table entry,
+product with the norm), so with S_t = sum_i |q~_i| |k~_ti| / sqrt(D) a score is off by at most
+3 u S_t (1 + 2^-9) and float32 accumulation (2^-15 S_t covers 128 additions); a weight by the
+factor e^d, d = max_t of that, twice (numerator and denominator).  The weights themselves are
+rounded to fp16 in the numerator (u, or 2^-25 absolute where they fall below 2^-14 of the running
+maximum, which itself is within 2^8 of the row's: 2^-17 of the largest weight at most, summed
+over L tokens L 2^-17 ... taken exactly as 2^-25 L max|V| / sum of weights >= 1), the decoded
+values at most twice (2 u of |v~|, spread by the inverse rotation: |v~|'s 2-norm is |v|'s, and a
+coordinate of the result sees at most the 2-norm of the rounding errors, 2 u |v|_2), and the
+output once.  The bound is worst-case; independent roundings add in squares, so the 2-norm
+over all outputs is held to 2^-9 of the outputs' besides: scores off by about u sqrt(3) (unit
+variance), weights u, values u sqrt(2), output u: in squares under 3 u, and 4 u allowed."""
+import math
+
+import numpy as np
+import pytest
+
+import workloads as W
+from oracle import attention as oatt
+from oracle import rotation as orot
+from oracle import shared as oshared
+from tests import gpu_util as gu
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -11
+
+SPECS = {
+    "fp16": W.Tier("fp16", "fp16"),
+    "fp8_int4": W.Tier("fp8_e4m3", "int4_g32"),
+    "fp8_fp16": W.Tier("fp8_e4m3", "fp16"),
+    "cb4": W.Tier("codebook", "codebook", 4, 4),
+    "cb32": W.Tier("codebook", "codebook", 3, 2),
+    "cb23": W.Tier("codebook", "codebook", 2, 3, codebook="uniform"),
+    "qjl": W.Tier("codebook_qjl", "codebook", 3, 4),
+    "outlier": W.Tier("codebook_outlier", "codebook", 4, 4),
+}
+
+
+class Case:
+    def __init__(self, kvq, torch, specs, prefix_lens, offsets, own_specs, own_lens, hq, hkv, d=128, ps=16, seed=0,
+                 spread=1.0):
+        """specs / own_specs: tier names; prefix_lens: per tier, a length per group; own_lens: per
+        tier, a length per sequence."""
+        rng = np.random.default_rng([seed, hq, hkv, d, ps])
+        self.batch = len(own_lens[0]) if own_specs else offsets[-1]
+        n = max(self.batch, len(offsets) - 1, 1)
+        kv = []
+        for lens in list(prefix_lens) + list(own_lens):
+            lens = list(lens) + [0] * (n - len(lens))
+            kv.append([tuple((rng.standard_normal((L, hkv, d)) * s).astype(np.float16) for s in (spread, 1.0)) for L in lens])
+        ks, vs = (np.where(rng.integers(0, 2, (hkv, d)) == 0, 1, -1).astype(np.int8) for _ in range(2))
+        tiers = [SPECS[s] for s in list(specs) + list(own_specs)]
+        proj = rng.standard_normal((128, d)).astype(np.float32)
+        outl = np.stack([rng.choice(d, 8, replace=False) for _ in range(hkv)]).astype(np.int32)
+        self.built = gu.build_exact(kvq, torch, tiers, kv, ks, vs, ps, shuffle_seed=seed + 1, k_qjl=proj, k_outl=outl)
+        first = self.built.gpu[0].struct
+        for c in self.built.gpu[1:]:  # one projection, as the calls want it
+            c.struct.k_signs, c.struct.v_signs = first.k_signs, first.v_signs
+            if c.struct.k_qjl and first.k_qjl:
+                c.struct.k_qjl = first.k_qjl
+        m = len(specs)
+        self.prefix, self.own = self.built.views[:m], self.built.views[m:]
+        self.offsets = list(offsets)
+        ora = self.built.ora
+        for t in ora[m:]:
+            t.block_table, t.lens = t.block_table[:self.batch], t.lens[:self.batch]
+        self.tiers = oshared.as_tiers(ora[:m], self.offsets, ora[m:], self.batch)
+        self.q = rng.standard_normal((self.batch, hq, d)).astype(np.float16)
+        self.hq, self.hkv, self.d = hq, hkv, d
+
+    def run(self, kvq, torch, q=None, out=None, ws=None):
+        q = torch.from_numpy(self.q).cuda() if q is None else q
+        need = kvq.kvq_decode_shared_workspace_size(self.prefix, self.offsets, self.own, self.batch, self.hq)
+        out_buf, out = gu.guarded_empty(torch, tuple(q.shape), torch.float16)
+        ws_buf, ws = gu.guarded_empty(torch, (need,), torch.uint8)
+        ws.fill_(0xFF)  # what a workspace holds does not matter
+        status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+        kvq.kvq_decode_attention_shared(self.prefix, self.offsets, self.own, q, out, ws, status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0, f"device error bits {int(status.item())}"
+        gu.assert_guards(out_buf, out)
+        gu.assert_guards(ws_buf, ws)
+        return out.cpu().numpy()
+
+    def check(self, got, heads=None):
+        grp = self.hq // self.hkv
+        sum_off = sum_size = 0.0
+        for b in range(self.batch):
+            for h in range(self.hq):
+                if heads is not None and (b, h) not in heads:
+                    continue
+                keys, values = oatt.dequantised_kv(self.tiers, b, h // grp)
+                g = got[b, h].astype(np.float64)
+                if keys is None:
+                    assert not g.any()
+                    continue
+                q = self.q[b, h].astype(np.float64)
+                extra = oatt.sketch_terms(self.tiers, b, h // grp, q)
+                s = (keys @ q + extra) / math.sqrt(self.d)
+                w = np.exp(s - s.max())
+                w /= w.sum()
+                want = w @ values
+                signs = self.built.k_signs[h // grp]
+                qr, kr = np.abs(orot.rotate(q, signs)), np.abs(orot.rotate(keys, signs))
+                off = float(np.max((3 * U * (1 + 2.0 ** -9) + 2.0 ** -15) * (kr @ qr) / math.sqrt(self.d)))
+                size = np.linalg.norm(values, axis=-1)
+                tol = (2 * math.expm1(off) + U) * (w @ np.abs(values)) + 2 * U * (w @ size)
+                tol = (tol + 2.0 ** -25 * len(w) * np.max(np.abs(values))) * (1 + 2.0 ** -9) + U * np.abs(want) + 2.0 ** -25
+                bad = np.abs(g - want) > tol
+                assert not bad.any(), f"({b}, {h}): {int(bad.sum())} off, worst {np.max(np.abs(g - want) / tol)}"
+                sum_off += float(np.sum((g - want) ** 2))
+                sum_size += float(np.sum(want ** 2))
+        rel = math.sqrt(sum_off / max(sum_size, 1e-300))
+        assert sum_size == 0 or rel <= 2.0 ** -9, f"relative error {rel}"
+
+
+def modules():
+    return gu.torch_cuda(), gu.kvq_module()
+
+
+@pytest.mark.parametrize("length", [1, 2, 15, 16, 17, 127, 128, 129, 255, 257, 1000])
+def test_lengths(length):
+    """One prefix of every awkward length, a few sequences of one token each."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["fp16"], [[length]], [0, 3], ["fp16"], [[1, 1, 1]], hq=4, hkv=2, seed=length)
+    c.check(c.run(kvq, torch))
+
+
+@pytest.mark.parametrize("name", ["fp16", "fp8_int4", "fp8_fp16", "cb4", "cb32", "cb23"])
+@pytest.mark.parametrize("group", [1, 2, 4, 8])
+def test_formats_and_groups(name, group):
+    torch, kvq = modules()
+    own = [[0, 5, 33, 16, 1]]
+    c = Case(kvq, torch, [name], [[700]], [0, 5], [name], own, hq=2 * group, hkv=2, seed=group)
+    c.check(c.run(kvq, torch))
+
+
+@pytest.mark.parametrize("batch,group", [(16, 8), (17, 8), (31, 8), (32, 8), (33, 8), (70, 4), (130, 1), (300, 1)])
+def test_row_blocks(batch, group):
+    """Rows around the sizes of an accumulator (128) and of an item (256), more than one item."""
+    torch, kvq = modules()
+    rng = np.random.default_rng(batch)
+    c = Case(kvq, torch, ["fp8_int4"], [[391]], [0, batch], ["fp8_int4"], [rng.integers(0, 9, batch)], hq=group, hkv=1,
+             seed=batch)
+    heads = {(b, h) for b in list(range(0, batch, 7)) + [batch - 1, batch - 2] for h in range(group)}
+    c.check(c.run(kvq, torch), heads)
+
+
+@pytest.mark.parametrize("ps", [1, 5, 12, 16, 24, 64])
+def test_page_sizes(ps):
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["cb4"], [[333]], [0, 4], ["cb4"], [[3, 0, 40, 7]], hq=4, hkv=2, ps=ps, seed=ps)
+    c.check(c.run(kvq, torch))
+
+
+def test_ragged_groups():
+    """Groups of different sizes and lengths, one empty, one of length 0, sequences before the
+    first group and behind the last, a sequence without a token."""
+    torch, kvq = modules()
+    offsets = [2, 5, 5, 40, 41, 43]
+    own = np.random.default_rng(3).integers(0, 50, 45)
+    own[0], own[41], own[44] = 0, 0, 0  # 0: no group and nothing of its own
+    c = Case(kvq, torch, ["cb4"], [[300, 77, 1500, 0, 129]], offsets, ["cb4"], [own], hq=8, hkv=2, seed=5)
+    got = c.run(kvq, torch)
+    assert not got[0].any() and not got[44].any()
+    c.check(got, {(b, h) for b in (0, 1, 2, 4, 5, 20, 39, 40, 41, 42, 43, 44) for h in range(8)})
+
+
+def test_tiers_of_the_prefix_and_of_the_sequences():
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["fp16", "fp8_int4"], [[100, 0], [900, 260]], [0, 4, 7], ["fp8_int4", "fp16"],
+             [[20, 0, 3, 200, 1, 7, 0], [0, 16, 16, 16, 2, 0, 0]], hq=8, hkv=2, seed=8)
+    c.check(c.run(kvq, torch))
+
+
+def test_no_tokens_of_their_own():
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["cb32"], [[450]], [0, 6], [], [], hq=4, hkv=2, seed=9)
+    c.check(c.run(kvq, torch))
+
+
+@pytest.mark.parametrize("spread", [8.0, 40.0])
+def test_large_scores(spread):
+    """Keys large enough that running maxima move by far more than the rescaling threshold."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["fp16"], [[1200]], [0, 20], ["fp16"], [[4] * 20], hq=8, hkv=1, seed=10, spread=spread)
+    got = c.run(kvq, torch)
+    grp = c.hq // c.hkv
+    # scores of this size leave no worst-case bound to speak of; a score's float32 and fp16
+    # roundings, independent, give it 2 u sqrt(sum (q~ k~)^2 / D) of noise (three sigma), and the
+    # weights that factor: compared where the softmax is not decided by less than that
+    for b in range(0, c.batch, 5):
+        for h in range(c.hq):
+            keys, values = oatt.dequantised_kv(c.tiers, b, h // grp)
+            q = c.q[b, h].astype(np.float64)
+            s = keys @ q / math.sqrt(c.d)
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            signs = c.built.k_signs[0]
+            noise = 2 * U * np.sqrt((orot.rotate(keys, signs) ** 2) @ (orot.rotate(q, signs) ** 2)) / math.sqrt(c.d)
+            d = 3 * float(np.max(noise))
+            tol = 2 * math.expm1(d) * (w @ np.abs(values - w @ values)) + 8 * U * (w @ np.linalg.norm(values, axis=-1))
+            assert np.all(np.abs(got[b, h] - w @ values) <= tol + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("name,d", [("qjl", 128), ("outlier", 128), ("outlier", 256), ("cb4", 64), ("fp8_int4", 64),
+                                    ("cb4", 256), ("fp16", 256)])
+def test_prefix_as_a_tier_of_every_sequence(name, d):
+    """Formats and sizes the prefix kernel is not built for."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, [name], [[200, 37]], [1, 3, 5], [name], [[5, 0, 20, 1, 0, 3]], hq=4, hkv=2, d=d, seed=d)
+    c.check(c.run(kvq, torch))
+
+
+def test_same_result_as_plain_decode():
+    """The prefix as an ordinary tier of every sequence, by kvq_decode_attention: the same
+    function, within the bounds of both (its own is far smaller)."""
+    torch, kvq = modules()
+    batch = 24
+    c = Case(kvq, torch, ["fp8_int4"], [[2000]], [0, batch], ["fp16"], [[10] * batch], hq=32, hkv=8, seed=12)
+    got = c.run(kvq, torch).astype(np.float64)
+    pre = c.prefix[0]
+    views = [kvq.TierView(pre.cache, pre.block_table[:1].expand(batch, -1).contiguous(),
+                          pre.seq_lens[:1].expand(batch).contiguous()), c.own[0]]
+    want = gu.gpu_decode(kvq, torch, views, c.q).astype(np.float64)
+    assert np.linalg.norm(got - want) <= 2.0 ** -9 * np.linalg.norm(want)
+
+
+def test_deterministic_replays_and_two_graphs():
+    """Two captured graphs with a workspace each, an eager call on another stream; lengths that
+    grow between replays are read when the graph runs."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["cb4"], [[640]], [0, 9], ["cb4"], [[30] * 9], hq=8, hkv=2, seed=13)
+    q = torch.from_numpy(c.q).cuda()
+    need = kvq.kvq_decode_shared_workspace_size(c.prefix, c.offsets, c.own, 9, 8)
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    outs = [torch.zeros_like(q) for _ in range(3)]
+    call = lambda i: kvq.kvq_decode_attention_shared(c.prefix, c.offsets, c.own, q, outs[i], ws[i])  # noqa: E731
+    call(0)
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(i)
+        graphs.append(g)
+    for lens in ([30] * 9, list(range(20, 29))):
+        c.own[0].seq_lens[:9].copy_(torch.tensor(lens, dtype=torch.int32))
+        c.tiers[-1].lens[:] = lens
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        for g in graphs:
+            g.replay()
+        with torch.cuda.stream(side):
+            call(2)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+        c.check(outs[0].cpu().numpy())
+
+
+def test_bad_lengths_and_pages_are_reported():
+    """What only the device can see: a length beyond the table, a page outside the pool.  Checked on
+    the CPU first (tests/test_index_checks.py): no read is made through either."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["cb4"], [[300]], [0, 3], ["cb4"], [[4, 4, 4]], hq=2, hkv=2, seed=14)
+    q, out = torch.from_numpy(c.q).cuda(), torch.empty(c.q.shape, dtype=torch.float16, device="cuda")
+    ws = torch.empty(kvq.kvq_decode_shared_workspace_size(c.prefix, c.offsets, c.own, 3, 2), dtype=torch.uint8,
+                     device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def bits():
+        kvq.kvq_decode_attention_shared(c.prefix, c.offsets, c.own, q, out, ws, status)
+        return int(status.item())
+
+    assert bits() == 0
+    table, lens = c.prefix[0].block_table, c.prefix[0].seq_lens
+    keep = table.clone()
+    for bad in (-1, c.built.gpu[0].num_pages, 2 ** 31 - 1):
+        table[0, 3] = bad
+        assert bits() == kvq.DEVERR_PAGE_INDEX
+        table.copy_(keep)
+    for bad in (-5, table.shape[1] * 16 + 1, 2 ** 31 - 1):
+        lens[0] = bad
+        assert bits() & kvq.DEVERR_SEQ_LEN
+    lens[0] = 300
+    assert bits() == 0
+    c.check(out.cpu().numpy())
