@@ -662,6 +662,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_gqa_kernel(const __grid
     }
     item = __shfl_sync(kFull, next, 0);
   }
+  // Launched as a programmatic dependent, this grid ran alongside the one before it, whose
+  // partials it does not read; it completes only after that one has.  Without the attribute
+  // there is nothing to wait for.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace
@@ -673,7 +677,7 @@ bool gqa_fast_supported(int head_dim, int group, int k_fmt, int v_fmt) {
 
 int gqa_max_chunk_tokens() { return kMaxPagesPerItem * PS; }
 
-cudaError_t launch_decode_gqa(const DecParams& dp, int* counter, cudaStream_t stream, bool trigger) {
+cudaError_t launch_decode_gqa(const DecParams& dp, int* counter, cudaStream_t stream, bool trigger, bool after) {
   constexpr int smem = kWarps * kWarpSmem;
   static std::atomic<bool> configured[64];  // shared-memory limit raised on this device (threads may race: a
                                            // second raise is harmless)
@@ -731,8 +735,18 @@ cudaError_t launch_decode_gqa(const DecParams& dp, int* counter, cudaStream_t st
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int ctas = std::max(1, std::min(sms, (items + kWarps - 1) / kWarps));
-  decode_gqa_kernel<<<ctas, kWarps * 32, smem, stream>>>(p);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, decode_gqa_kernel, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess) note_launch();
   return e;
 }

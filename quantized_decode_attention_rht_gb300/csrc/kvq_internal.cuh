@@ -143,7 +143,9 @@ cudaError_t launch_decode(const DecParams& p, int head_dim, int group, cudaStrea
 bool gqa_fast_supported(int head_dim, int group, int k_fmt, int v_fmt);
 int gqa_max_chunk_tokens();
 // trigger: a codebook split-K launch follows and may start on SMs this grid leaves idle.
-cudaError_t launch_decode_gqa(const DecParams& p, int* counter, cudaStream_t stream, bool trigger);
+// after: a pass whose results this one does not read precedes (and lets dependents start); the
+// grid runs alongside it, as its programmatic dependent, and completes only after it.
+cudaError_t launch_decode_gqa(const DecParams& p, int* counter, cudaStream_t stream, bool trigger, bool after = false);
 // Fused tensor-core decode over codebook tiers (codebook K and V), head_dim 128 or 256,
 // 1, 2 or 4 query heads per kv head; one launch per tier (after one projection launch when
 // a tier's keys carry a sketch).  `counters`: the 256-byte counter block, zero at launch

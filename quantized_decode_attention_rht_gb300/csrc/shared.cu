@@ -124,12 +124,24 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
   if (row >= (long long)p.pre.batch * p.pre.hq) return;  // whole warps; with eight warps a row, whole blocks
   const int b = (int)(row / p.pre.hq), h = (int)(row - (long long)b * p.pre.hq);
   const Parts n = find_parts(p, b, h);
-  const float2* ml;
-  const float* acc;
-  float mx = -INFINITY;
-  for (int j = part * 32 + lane; j < n.total; j += 32 * kRowWarps) {
-    locate(p, n, row, j, ml, acc);
-    mx = fmaxf(mx, ml->x);
+  // a lane looks after one partial at a time: its (max, sum) and where its accumulator lies
+  auto look = [&](int j, float2& x) -> const float* {
+    const float2* ml;
+    const float* acc = nullptr;
+    x = make_float2(-INFINITY, 0.f);
+    if (j < n.total) {
+      locate(p, n, row, j, ml, acc);
+      x = *ml;
+    }
+    return acc;
+  };
+  const int j0 = lane * kRowWarps + part;
+  float2 x0, x;
+  const float* acc0 = look(j0, x0);
+  float mx = x0.x;
+  for (int j = j0 + 32 * kRowWarps; j < n.total; j += 32 * kRowWarps) {
+    look(j, x);
+    mx = fmaxf(mx, x.x);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
@@ -140,20 +152,28 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
     for (int i = 0; i < kRowWarps; ++i) mx = fmaxf(mx, s_m[i]);
   }
   float y[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-#pragma unroll 4
-  for (int j = part; j < n.total; j += kRowWarps) {
-    locate(p, n, row, j, ml, acc);
-    const float2 x = *ml;
-    if (x.x == -INFINITY) continue;  // a part without tokens leaves its accumulator unwritten
-    float f;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(x.x - mx));
-    const float4 a = reinterpret_cast<const float4*>(acc)[lane];
+  for (int first = 0; first < n.total; first += 32 * kRowWarps) {  // once, but for very many partials
+    const float* acc = acc0;
+    x = x0;
+    if (first) acc = look(first + j0, x);
+    float f = 0.f;  // a part without tokens leaves its accumulator unwritten: weight 0, not read
+    if (x.x != -INFINITY) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(x.x - mx));
     l = fmaf(x.y, f, l);
-    y[0] = fmaf(a.x, f, y[0]);
-    y[1] = fmaf(a.y, f, y[1]);
-    y[2] = fmaf(a.z, f, y[2]);
-    y[3] = fmaf(a.w, f, y[3]);
+    const int live = min(32, (n.total - first - part + kRowWarps - 1) / kRowWarps);
+#pragma unroll 8
+    for (int i = 0; i < live; ++i) {
+      const float fi = __shfl_sync(0xFFFFFFFFu, f, i);
+      const float* ai = reinterpret_cast<const float*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(acc), i));
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (fi != 0.f) a = reinterpret_cast<const float4*>(ai)[lane];
+      y[0] = fmaf(a.x, fi, y[0]);
+      y[1] = fmaf(a.y, fi, y[1]);
+      y[2] = fmaf(a.z, fi, y[2]);
+      y[3] = fmaf(a.w, fi, y[3]);
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
   if constexpr (kRowWarps > 1) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) s_acc[part][4 * lane + k] = y[k];
@@ -346,13 +366,14 @@ cudaError_t launched() {
   return e;
 }
 
-// The split-K passes over the sequences' own tiers.
-cudaError_t launch_own(const DecParams& p, const Plan& plan, int d, int group, int* counters, cudaStream_t s) {
+// The split-K passes over the sequences' own tiers.  after: the prefix pass precedes; the
+// fused kernels then start on SMs it leaves idle and complete only after it.
+cudaError_t launch_own(const DecParams& p, const Plan& plan, int d, int group, int* counters, bool after, cudaStream_t s) {
   bool fam[3] = {false, false, false};
   for (int i = 0; i < p.num_tiers; ++i) fam[plan.kind[i]] = true;
   cudaError_t e = cudaSuccess;
-  if (fam[TIER_GQA]) e = launch_decode_gqa(p, counters + kGqaCounter, s, fam[TIER_CB]);
-  if (e == cudaSuccess && fam[TIER_CB]) e = launch_decode_cb(p, d, counters, s, fam[TIER_GQA]);
+  if (fam[TIER_GQA]) e = launch_decode_gqa(p, counters + kGqaCounter, s, fam[TIER_CB], after);
+  if (e == cudaSuccess && fam[TIER_CB]) e = launch_decode_cb(p, d, counters, s, fam[TIER_GQA] || after);
   if (e == cudaSuccess && fam[TIER_GENERIC]) e = launch_decode(p, d, group, s);
   return e;
 }
@@ -502,7 +523,7 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
     e = launched();
     if (e == cudaSuccess) e = launch_shared_prefix(p, s);
   }
-  if (e == cudaSuccess && num_tiers > 0) e = launch_own(j.dec, plan.dec, d, group, counters, s);
+  if (e == cudaSuccess && num_tiers > 0) e = launch_own(j.dec, plan.dec, d, group, counters, p.num_items > 0, s);
   if (e == cudaSuccess) {
     if (2 * plan.total_splits + plan.dec.total > 24)
       join_kernel<8><<<(unsigned)rows, 256, 0, s>>>(j);

@@ -39,7 +39,9 @@ namespace kvq {
 namespace {
 
 constexpr int kDim = 128;
-constexpr int kThreads = 544;
+constexpr int kThreads = 640;
+// registers per thread after the split: launched with 96 x 640 = 61440 = 256 x 136 + 256 x 88 + 128 x 32
+constexpr int kSoftmaxRegs = 136, kDecodeRegs = 88, kIssueRegs = 32;
 constexpr int kTileBytes = kTileTokens * kDim * 2;  // 32 KB: two halves of 128 rows x 128 bytes
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kStages = 2;
@@ -77,7 +79,7 @@ struct Ctl {
 static_assert(sizeof(Ctl) <= 256, "control block");
 
 // Waits for a phase; false once the block has given up (two seconds for any one wait).
-__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
   unsigned long long t0, t;
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
   for (;;) {
@@ -104,7 +106,21 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// (the loaded registers pass through, so that nothing reads them before the wait)
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                 "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])::"memory");
+}
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                 "+r"(v[15])::"memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 columns of the warp's 32 lanes.
@@ -119,16 +135,13 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&v)[32]) {
         "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr));
 }
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&v)[16]) {
   asm volatile(
@@ -200,150 +213,148 @@ struct Source {
   uint32_t lut;          // shared address of the pair table (codebooks)
 };
 
-// Row of token t in the pool, or -1 (past the end, or a page outside the pool).
-__device__ __forceinline__ long long row_of(const Source& s, int t, int* bits) {
-  if (t >= s.end) return -1;
-  const int lp = s.page_shift >= 0 ? t >> s.page_shift : t / s.page_size;
-  const int phys = __ldg(s.table + lp);
-  if (!page_in_pool(phys, s.num_pages, bits)) return -1;
-  return ((long long)phys * s.hkv + s.hk) * s.page_size + (t - lp * s.page_size);
-}
-
 // Formats as the decoding warps see them.
 enum { D_F16, D_F8, D_I4, D_CB4, D_CB3, D_CB2 };
 __host__ __device__ constexpr int lanes_per_row(int f) { return f == D_F16 ? 16 : (f == D_F8 ? 8 : 4); }
 __host__ __device__ constexpr int unit_words(int f) { return f == D_CB3 ? 3 : (f == D_CB2 ? 2 : 4); }
 
-// One tile's data in a thread's registers: a unit per pass.
+// A unit of one pass in a thread's registers, with its norm or group scale in both halves.
 template <int F>
-struct Regs {
-  static constexpr int kPasses = lanes_per_row(F);  // 128 threads, 128 rows
-  uint32_t w[kPasses][unit_words(F)];
-  uint32_t scale[F == D_F16 || F == D_F8 ? 1 : kPasses];  // norm or group scale, both halves
+struct Unit {
+  uint32_t w[unit_words(F)], scale;
 };
 
+// Page of the token that the thread reads in pass P of the tile at t0 (-1 past the end).
 template <int F>
-__device__ __forceinline__ void fetch(const Source& s, int t0, int tid, Regs<F>& r, int* bits) {
-  constexpr int L = lanes_per_row(F), W = unit_words(F);
-  const int u = tid % L;
-#pragma unroll
-  for (int p = 0; p < Regs<F>::kPasses; ++p) {
-    const long long row = row_of(s, t0 + p * (128 / L) + tid / L, bits);
-    if (row >= 0) {
-      const uint8_t* src = s.rows + row * s.row_bytes + u * (4 * W);
-      if constexpr (W == 4) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
-        r.w[p][0] = x.x;
-        r.w[p][1] = x.y;
-        r.w[p][2] = x.z;
-        r.w[p][3] = x.w;
-      } else if constexpr (W == 2) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-        r.w[p][0] = x.x;
-        r.w[p][1] = x.y;
-      } else {
-#pragma unroll
-        for (int k = 0; k < 3; ++k) r.w[p][k] = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
-      }
-      if constexpr (F == D_I4) r.scale[p] = __half_as_ushort(__ldg(s.aux + row * 4 + u)) * 0x10001u;
-      else if constexpr (F >= D_CB4) r.scale[p] = __half_as_ushort(__ldg(s.aux + row)) * 0x10001u;
-    } else {  // a token that is not there reads as zero (level 8 of INT4)
-#pragma unroll
-      for (int k = 0; k < W; ++k) r.w[p][k] = 0u;
-      if constexpr (F != D_F16 && F != D_F8) r.scale[p] = 0u;
-    }
-  }
+__device__ __forceinline__ int page_of(const Source& s, int t0, int pass, int tid) {
+  const int t = t0 + pass * (128 / lanes_per_row(F)) + tid / lanes_per_row(F);
+  if (t >= s.end) return -1;
+  return __ldg(s.table + (s.page_shift >= 0 ? t >> s.page_shift : t / s.page_size));
+}
+
+// Where that token's unit lies, if it is there: false past the end and for a page outside the
+// pool (reported in bits).
+template <int F>
+__device__ __forceinline__ bool find_unit(const Source& s, int t0, int pass, int tid, int page, int* bits, size_t* row) {
+  const int t = t0 + pass * (128 / lanes_per_row(F)) + tid / lanes_per_row(F);
+  if (t >= s.end || !page_in_pool(page, s.num_pages, bits)) return false;
+  const int off = s.page_shift >= 0 ? t & (s.page_size - 1) : t % s.page_size;
+  *row = ((size_t)page * s.hkv + s.hk) * s.page_size + off;
+  return true;
 }
 
 template <int F>
-__device__ __forceinline__ void store_tile(const Source& s, uint32_t tile, int tid, const Regs<F>& r) {
-  constexpr int L = lanes_per_row(F);
+__device__ __forceinline__ void load_unit(const Source& s, int t0, int pass, int tid, int page, Unit<F>& x, int* bits) {
+  constexpr int L = lanes_per_row(F), W = unit_words(F);
   const int u = tid % L;
+  size_t row;
 #pragma unroll
-  for (int p = 0; p < Regs<F>::kPasses; ++p) {
-    const int t = p * (128 / L) + tid / L;  // row of the tile
-    const uint32_t row = tile + t * 128;
-    const int x = t & 7;
-    if constexpr (F == D_F16) {
-      sts16(row + (u >> 3) * kHalfBytes + (((u & 7) ^ x) << 4), r.w[p][0], r.w[p][1], r.w[p][2], r.w[p][3]);
-    } else if constexpr (F == D_F8) {
-      // 16 values, two chunks; the upper half's lanes store theirs in the other order, so that
-      // the eight lanes of a row meet eight different 16-byte banks
-      uint32_t h[8];
+  for (int k = 0; k < W; ++k) x.w[k] = 0u;  // a token that is not there reads as zero
+  x.scale = 0u;
+  if (!find_unit<F>(s, t0, pass, tid, page, bits, &row)) return;
+  const uint8_t* src = s.rows + row * s.row_bytes + u * (4 * W);
+  if constexpr (W == 4) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+    x.w[0] = v.x;
+    x.w[1] = v.y;
+    x.w[2] = v.z;
+    x.w[3] = v.w;
+  } else if constexpr (W == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+    x.w[0] = v.x;
+    x.w[1] = v.y;
+  } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[k]) : "h"((uint16_t)(r.w[p][k / 2] >> (16 * (k & 1)))));
-      const uint32_t at = row + (u >> 2) * kHalfBytes;
-      const int c = (2 * u) & 7, odd = u >> 2;
+    for (int k = 0; k < 3; ++k) x.w[k] = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
+  }
+  if constexpr (F == D_I4) x.scale = __half_as_ushort(__ldg(s.aux + row * 4 + u));
+  else if constexpr (F >= D_CB4) x.scale = __half_as_ushort(__ldg(s.aux + row));
+}
+
+// The unit decoded to fp16, into its row of the tile.
+template <int F>
+__device__ __forceinline__ void store_unit(const Source& s, uint32_t tile, int pass, int tid, const Unit<F>& z) {
+  constexpr int L = lanes_per_row(F);
+  const int u = tid % L, t = pass * (128 / L) + tid / L;  // t: row of the tile
+  const uint32_t row = tile + t * 128;
+  const int x = t & 7;
+  if constexpr (F == D_F8) {
+    // 16 values, two chunks; the upper half's lanes store theirs in the other order, so that
+    // the eight lanes of a row meet eight different 16-byte banks
+    uint32_t h[8];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bool second = (i ^ odd) != 0;
-        sts16(at + (((c + second) ^ x) << 4), second ? h[4] : h[0], second ? h[5] : h[1], second ? h[6] : h[2],
-              second ? h[7] : h[3]);
-      }
+    for (int k = 0; k < 8; ++k)
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[k]) : "h"((uint16_t)(z.w[k / 2] >> (16 * (k & 1)))));
+    const uint32_t at = row + (u >> 2) * kHalfBytes;
+    const int c = (2 * u) & 7, odd = u >> 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool second = (i ^ odd) != 0;
+      sts16(at + (((c + second) ^ x) << 4), second ? h[4] : h[0], second ? h[5] : h[1], second ? h[6] : h[2],
+            second ? h[7] : h[3]);
+    }
+  } else {
+    // 32 values, four chunks of 8 (b bytes each); lanes of a row pair store them in four
+    // different orders, so that eight lanes meet eight different 16-byte banks
+    constexpr int B = F == D_I4 || F == D_CB4 ? 4 : (F == D_CB3 ? 3 : 2);
+    const uint32_t scale = z.scale * 0x10001u;
+    uint32_t c[4];
+    if constexpr (B == 4) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[k] = z.w[k];
+    } else if constexpr (B == 3) {
+      c[0] = z.w[0];
+      c[1] = __funnelshift_r(z.w[0], z.w[1], 24);
+      c[2] = __funnelshift_r(z.w[1], z.w[2], 16);
+      c[3] = z.w[2] >> 8;
     } else {
-      // 32 values, four chunks of 8 (b bytes each); lanes of a row pair store them in four
-      // different orders, so that eight lanes meet eight different 16-byte banks
-      constexpr int B = F == D_I4 || F == D_CB4 ? 4 : (F == D_CB3 ? 3 : 2);
-      uint32_t c[4];
-      if constexpr (B == 4) {
+      c[0] = z.w[0];
+      c[1] = z.w[0] >> 16;
+      c[2] = z.w[1];
+      c[3] = z.w[1] >> 16;
+    }
+    const int flip = (u >> 1) ^ ((t & 1) << 1);
+    if (flip & 1) {
+      uint32_t y = c[0];
+      c[0] = c[1];
+      c[1] = y;
+      y = c[2];
+      c[2] = c[3];
+      c[3] = y;
+    }
+    if (flip & 2) {
+      uint32_t y = c[0];
+      c[0] = c[2];
+      c[2] = y;
+      y = c[1];
+      c[1] = c[3];
+      c[3] = y;
+    }
+    const uint32_t at = row + (u >> 1) * kHalfBytes;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = r.w[p][k];
-      } else if constexpr (B == 3) {
-        c[0] = r.w[p][0];
-        c[1] = __funnelshift_r(r.w[p][0], r.w[p][1], 24);
-        c[2] = __funnelshift_r(r.w[p][1], r.w[p][2], 16);
-        c[3] = r.w[p][2] >> 8;
-      } else {
-        c[0] = r.w[p][0];
-        c[1] = r.w[p][0] >> 16;
-        c[2] = r.w[p][1];
-        c[3] = r.w[p][1] >> 16;
-      }
-      const int flip = (u >> 1) ^ ((t & 1) << 1);
-      if (flip & 1) {
-        uint32_t y = c[0];
-        c[0] = c[1];
-        c[1] = y;
-        y = c[2];
-        c[2] = c[3];
-        c[3] = y;
-      }
-      if (flip & 2) {
-        uint32_t y = c[0];
-        c[0] = c[2];
-        c[2] = y;
-        y = c[1];
-        c[1] = c[3];
-        c[3] = y;
-      }
-      const uint32_t at = row + (u >> 1) * kHalfBytes;
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[4];
+      if constexpr (F == D_I4) {
+        // nibbles as 1024 + n in fp16, minus 1032: exact; times the scale, rounded once
+        const uint32_t even = c[i] & 0x0F0F0F0Fu, odd = (c[i] >> 4) & 0x0F0F0F0Fu;
+        const __half2 off = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t h[4];
-        if constexpr (F == D_I4) {
-          // nibbles as 1024 + n in fp16, minus 1032: exact; times the scale, rounded once
-          const uint32_t even = c[i] & 0x0F0F0F0Fu, odd = (c[i] >> 4) & 0x0F0F0F0Fu;
-          const __half2 off = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t v = (__byte_perm(even, odd, k | ((4 + k) << 8)) & 0xFFu) |
-                               ((__byte_perm(even, odd, (4 + k)) & 0xFFu) << 16) | 0x64006400u;
-            const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&v), off);
-            h[k] = hmul2(*reinterpret_cast<const uint32_t*>(&n), r.scale[p]);
-          }
-        } else {
-          // pairs of codes through the block's table of centroid pairs / sqrt(D)
-          constexpr int C = F == D_CB4 ? 16 : 32;  // copies: one per lane (4 bits: per half-warp lane)
-          const uint32_t base = s.lut + 4u * (tid & (C - 1));
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t e = (c[i] >> (2 * B * k)) & ((1u << (2 * B)) - 1u);
-            h[k] = hmul2(lds32(base + e * (4u * C)), r.scale[p]);
-          }
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t v = (__byte_perm(even, odd, k | (k << 4) | ((4 + k) << 8) | (k << 12)) & 0x00FF00FFu) | 0x64006400u;
+          const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&v), off);
+          h[k] = hmul2(*reinterpret_cast<const uint32_t*>(&n), scale);
         }
-        sts16(at + (((4 * (u & 1) + (i ^ flip)) ^ x) << 4), h[0], h[1], h[2], h[3]);
+      } else {
+        // pairs of codes through the block's table of centroid pairs / sqrt(D)
+        constexpr int C = F == D_CB4 ? 16 : 32;  // copies: one per lane (4 bits: per half-warp lane)
+        const uint32_t base = s.lut + 4u * (tid & (C - 1));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t e = (c[i] >> (2 * B * k)) & ((1u << (2 * B)) - 1u);
+          h[k] = hmul2(lds32(base + e * (4u * C)), scale);
+        }
       }
+      sts16(at + (((4 * (u & 1) + (i ^ flip)) ^ x) << 4), h[0], h[1], h[2], h[3]);
     }
   }
 }
@@ -353,19 +364,77 @@ struct Ring {
   uint32_t tiles, full, empty;  // shared addresses
 };
 
+// A pass's registers are loaded with the next tile's unit as soon as its unit of this tile is
+// decoded, and its page number a tile before that: every load has a tile's time to arrive.
 template <int F>
 __device__ __forceinline__ void produce(const Source& s, const Ring& ring, int tile0, int tile1, int tid,
                                         volatile int* abort, int* err) {
+  constexpr int kPasses = lanes_per_row(F);  // 128 threads, 128 rows
   int bits = 0;
-  Regs<F> r;
-  fetch<F>(s, tile0 * kTileTokens, tid, r, &bits);
+  Unit<F> x[kPasses];
+  int page[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) page[p] = page_of<F>(s, tile0 * kTileTokens, p, tid);
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) load_unit<F>(s, tile0 * kTileTokens, p, tid, page[p], x[p], &bits);
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) page[p] = page_of<F>(s, (tile0 + 1) * kTileTokens, p, tid);
   for (int t = tile0, i = 0; t < tile1; ++t, ++i) {
     const int st = i & 1;
     if (i >= kStages && !bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err)) break;
-    store_tile<F>(s, ring.tiles + st * kTileBytes, tid, r);
-    if (t + 1 < tile1) fetch<F>(s, (t + 1) * kTileTokens, tid, r, &bits);
+    const bool more = t + 1 < tile1;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      store_unit<F>(s, ring.tiles + st * kTileBytes, p, tid, x[p]);
+      if (more) {
+        load_unit<F>(s, (t + 1) * kTileTokens, p, tid, page[p], x[p], &bits);
+        page[p] = page_of<F>(s, (t + 2) * kTileTokens, p, tid);
+      }
+    }
     fence_async_smem();
     bar_arrive(ring.full + 8 * st);
+  }
+  if (bits) atomicOr(err, bits);
+}
+
+// fp16 rows need no decoding: asynchronous copies, a tile signalled once the next one's copies
+// are under way.
+template <>
+__device__ __forceinline__ void produce<D_F16>(const Source& s, const Ring& ring, int tile0, int tile1, int tid,
+                                               volatile int* abort, int* err) {
+  constexpr int kPasses = lanes_per_row(D_F16);
+  int bits = 0;
+  int page[kPasses];
+  const int u = tid % 16;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) page[p] = page_of<D_F16>(s, tile0 * kTileTokens, p, tid);
+  bool ok = true;
+  for (int t = tile0, i = 0; t < tile1; ++t, ++i) {
+    const int st = i & 1;
+    if (i >= kStages && !(ok = bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err))) break;
+    const uint32_t tile = ring.tiles + st * kTileBytes + (u >> 3) * kHalfBytes;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      size_t row = 0;
+      const bool there = find_unit<D_F16>(s, t * kTileTokens, p, tid, page[p], &bits, &row);
+      const int r = p * 8 + tid / 16;
+      // (a row that is not there: no bytes read, 16 zeros written)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + r * 128 + (((u & 7) ^ (r & 7)) << 4)),
+                   "l"(s.rows + row * s.row_bytes + u * 16), "r"(there ? 16 : 0)
+                   : "memory");
+      page[p] = page_of<D_F16>(s, (t + 1) * kTileTokens, p, tid);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (i > 0) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      fence_async_smem();
+      bar_arrive(ring.full + 8 * (st ^ 1));
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (ok) {
+    fence_async_smem();
+    bar_arrive(ring.full + 8 * ((tile1 - tile0 - 1) & 1));
   }
   if (bits) atomicOr(err, bits);
 }
@@ -392,15 +461,57 @@ __device__ __forceinline__ int decode_kind(int fmt, int bits) {
 }
 
 // Pairs of centroids / sqrt(D) in fp16: entry e = codes (e mod 2^b, e / 2^b), a copy per lane of
-// a warp (16 copies of 4-bit pairs).
-__device__ __forceinline__ void build_lut(uint32_t lut, const float* cent, int bits) {
-  const int copies = bits == 4 ? 16 : 32, n = 1 << (2 * bits), mask = (1 << bits) - 1;
+// a warp (16 copies of 4-bit pairs).  tid: 256 threads.
+__device__ __forceinline__ void build_lut(uint32_t lut, const float* cent, int bits, int tid) {
+  const int copies = bits == 4 ? 16 : 32;
+  if (tid >= (1 << (2 * bits))) return;
   const float inv = inv_sqrt_dim(kDim);
-  for (int i = threadIdx.x; i < n * copies; i += kThreads) {
-    const int e = i / copies;
-    const uint32_t v = half2_bits(__ldg(cent + (e & mask)) * inv, __ldg(cent + (e >> bits)) * inv);
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(lut + 4u * i), "r"(v) : "memory");
+  const uint32_t v = half2_bits(__ldg(cent + (tid & ((1 << bits) - 1))) * inv, __ldg(cent + (tid >> bits)) * inv);
+  for (int i = 0; i < copies; i += 4) sts16(lut + 4u * (tid * copies + i), v, v, v, v);
+}
+
+// ------------------------------------------------------------------------ softmax
+// A row's maximum has grown: from f on (2^(old - new)), scale what the old one is in: the
+// accumulator (if any product has gone into it) and the tile's first `done` weight columns.
+__device__ __forceinline__ void rescale(uint32_t o_at, bool acc, uint32_t p_at, int done, float f) {
+  uint32_t v[16];
+  if (acc) {
+#pragma unroll 1
+    for (int c = 0; c < kDim; c += 16) {
+      tc_ld16(o_at + c, v);
+      tc_wait_ld(v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+      tc_st16(o_at + c, v);
+    }
   }
+  for (int c = 0; c < done; c += 16) {
+    tc_ld16(p_at + c, v);
+    tc_wait_ld(v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
+      v[e] = half2_bits(x.x * f, x.y * f);
+    }
+    tc_st16(p_at + c, v);
+  }
+  tc_wait_st();
+}
+
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long r) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
+  return f;
 }
 
 // ------------------------------------------------------------------------ the kernel
@@ -477,15 +588,20 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (T.k_fmt == KVQ_FMT_CODEBOOK) build_lut(smem + kOffLut, T.k_cent, T.k_bits);
-  if (T.v_fmt == KVQ_FMT_CODEBOOK) build_lut(smem + kOffLut + kLutBytes, T.v_cent, T.v_bits);
+  if (T.k_fmt == KVQ_FMT_CODEBOOK && warp < 8) build_lut(smem + kOffLut, T.k_cent, T.k_bits, threadIdx.x);
+  if (T.v_fmt == KVQ_FMT_CODEBOOK && warp >= 8 && warp < 16)
+    build_lut(smem + kOffLut + kLutBytes, T.v_cent, T.v_bits, threadIdx.x - 256);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
 
+  // chunks of the sequences' own tiers may start on SMs that this grid leaves idle
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   if (warp < 8) {
     // ---- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const uint32_t q_tile = smem + kOffQ + w * kTileBytes;
     {
       // the group's queries into shared memory, 16 lanes a row
@@ -509,66 +625,61 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     if (live && my_jobs > 0) {
       const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_at = lane_base + w * 128, o_at = lane_base + 256 + w * 128;
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY;
+      unsigned long long l2 = 0;  // the row's sum, even and odd columns
       bool ok = true;
       for (int k = 0; k < my_jobs; ++k) {
         const int i = 2 * k + w, tile = tile0 + (both ? i : i >> 1);
         const int valid = min(kTileTokens, len - tile * kTileTokens);
         if (!(ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * (B_SFULL + w), k & 1, abort, p.err)))) break;
         tc_fence_after();
-        uint32_t v[32];
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tc_ld32(s_at + 32 * c, v);
-          tc_wait_ld();
-          if (valid >= kTileTokens) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e < valid) mx = fmaxf(mx, __uint_as_float(v[e]));
-          }
-        }
-        if (k == 0) {
-          m = mx;
-        } else if (__any_sync(0xFFFFFFFFu, mx > m + 8.0f)) {
-          const float mn = fmaxf(m, mx), f = ex2(m - mn);
-          m = mn;
-          l *= f;
-          if (!(ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * (B_OFULL + w), (k - 1) & 1, abort, p.err)))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tc_ld32(o_at + 32 * c, v);
-            tc_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-            tc_st32(o_at + 32 * c, v);
-          }
-        }
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tc_ld32(s_at + 32 * c, v);
-          tc_wait_ld();
-          uint32_t h[16];
+        uint32_t va[32], vb[32];
+        tc_ld32(s_at, va);
+        // 32 scores: the row's maximum (a rise of more than 2^8 rescales), weights, their sum
+        auto weigh = [&](int c, uint32_t (&v)[32], uint32_t (&next)[32]) {
           if (valid < kTileTokens) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (32 * c + e >= valid) v[e] = 0xFF800000u;  // -inf: weight 0
           }
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            m0 = fmaxf(fmaxf(m0, __uint_as_float(v[e])), __uint_as_float(v[e + 1]));
+            m1 = fmaxf(fmaxf(m1, __uint_as_float(v[e + 2])), __uint_as_float(v[e + 3]));
+          }
+          const float mx = fmaxf(m0, m1);
+          if (__any_sync(0xFFFFFFFFu, mx > m + 8.0f)) {
+            const float mn = fmaxf(m, mx), f = ex2(m - mn);
+            m = mn;
+            const float2 ll = unpack2(l2);
+            l2 = pack2(ll.x * f, ll.y * f);
+            // (the products of earlier tiles are complete: they precede these scores)
+            tc_wait_ld(next);  // nothing in flight across the call
+            if (k > 0 || c > 0) rescale(o_at, k > 0, s_at, 16 * c, f);
+          }
+          const unsigned long long neg = pack2(-m, -m);
+          uint32_t h[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float a = ex2(__uint_as_float(v[2 * e]) - m), b = ex2(__uint_as_float(v[2 * e + 1]) - m);
-            l0 += a;
-            l1 += b;
+            const float2 x = unpack2(add2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), neg));
+            const float a = ex2(x.x), b = ex2(x.y);
+            l2 = add2(l2, pack2(a, b));
             h[e] = half2_bits(a, b);
           }
           tc_st16(s_at + 16 * c, h);  // over scores that this warp has read
-        }
-        l += l0 + l1;
+        };
+        tc_wait_ld(va);
+        tc_ld32(s_at + 32, vb);
+        weigh(0, va, vb);
+        tc_wait_ld(vb);
+        tc_ld32(s_at + 64, va);
+        weigh(1, vb, va);
+        tc_wait_ld(va);
+        tc_ld32(s_at + 96, vb);
+        weigh(2, va, vb);
+        tc_wait_ld(vb);
+        weigh(3, vb, va);
         tc_wait_st();
         tc_fence_before();
         bar_arrive(bars + 8 * (B_PREADY + w));
@@ -580,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tc_ld32(o_at + 32 * c, v);
-          tc_wait_ld();
+          tc_wait_ld(v);
           if (out_row >= 0) {
             float* dst = p.acc + (part + out_row) * kDim + 32 * c;
 #pragma unroll
@@ -592,12 +703,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
           }
         }
       }
-      if (out_row >= 0) *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) = ok ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+      if (out_row >= 0) *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) =
+            ok ? make_float2(m, unpack2(l2).x + unpack2(l2).y) : make_float2(-INFINITY, 0.f);
     } else if (out_row >= 0) {  // a second group without a tile of its own
       *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) = make_float2(-INFINITY, 0.f);
     }
   } else if (warp < 16) {
     // ---- decoding
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDecodeRegs));
     const bool keys = warp < 12;
     Source s;
     s.rows = keys ? T.k_rows : T.v_rows;
@@ -617,8 +730,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     ring.empty = bars + 8 * (keys ? B_KEMPTY : B_VEMPTY);
     produce_any(keys ? decode_kind(T.k_fmt, T.k_bits) : decode_kind(T.v_fmt, T.v_bits), s, ring, tile0, tile1,
                 threadIdx.x & 127, abort, p.err);
-  } else if (lane == 0) {
+  } else {
     // ---- products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 16 && lane == 0) {
     const uint64_t kmajor = desc_base(16, 1024), mnmajor = desc_base(kHalfBytes, 1024);
     auto scores = [&](int i) -> bool {  // S of job i
       const int tile = both ? i : i >> 1, st = tile & 1, ws = i & 1;
@@ -651,6 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       tc_commit(bars + 8 * (B_OFULL + ws));
       if (both || ws) tc_commit(bars + 8 * (B_VEMPTY + st));
       if (i + 2 < jobs) ok = scores(i + 2);
+    }
     }
   }
   __syncwarp();
