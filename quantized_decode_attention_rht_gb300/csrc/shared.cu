@@ -304,6 +304,12 @@ kvq_status make_shared_plan(const Call& c, const kvq_tier_view* all, bool q16, S
   for (int i = 0; i < c.num_prefix; ++i)
     plan->fast = plan->fast && shared_tier_supported(d, all[i].cache->k_format, all[i].cache->v_format);
   plan->fast = plan->fast && aligned(c0->k_signs, 16) && aligned(c0->v_signs, 16);
+  for (int i = 0; i < c.num_prefix; ++i) {
+    // the prefix kernel reads INT4 scales four at a time and counts rows in 32 bits
+    const kvq_cache* k = all[i].cache;
+    plan->fast = plan->fast && (k->v_format != KVQ_FMT_INT4_G32 || aligned(k->v_aux, 8)) &&
+                 (long long)k->num_pages * k->page_size * k->num_kv_heads < 0xFFFFFFFFLL;
+  }
   kvq_status st;
   size_t at = 0;
   const size_t rows = (size_t)c.batch * c.hq;

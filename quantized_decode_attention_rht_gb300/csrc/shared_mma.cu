@@ -45,9 +45,13 @@ constexpr int kSoftmaxRegs = 136, kDecodeRegs = 88, kIssueRegs = 32;
 constexpr int kTileBytes = kTileTokens * kDim * 2;  // 32 KB: two halves of 128 rows x 128 bytes
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kStages = 2;
-constexpr int kLutBytes = 16 << 10;  // per side
+// Beside the operand tiles, per side: rows on their way (and a codebook's table), then the
+// row numbers of three tiles and the norms or scales of two.
 constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kStages * kTileBytes;
-constexpr int kOffLut = kOffV + kStages * kTileBytes, kOffCtl = kOffLut + 2 * kLutBytes;
+constexpr int kOffRaw = kOffV + kStages * kTileBytes, kRawBytes = 24 << 10;
+constexpr int kOffRow = kOffRaw + kRawBytes, kRowBytes = 3 * kTileTokens * 4;   // per side
+constexpr int kOffAux = kOffRow + 2 * kRowBytes, kAuxBytes = 2 * kTileTokens * 8;  // per side
+constexpr int kOffCtl = kOffAux + 2 * kAuxBytes;
 constexpr int kSmem = kOffCtl + 256 + 1024;  // 1024: the base is aligned by hand
 
 // barriers, in units of 8 bytes from kOffCtl
@@ -203,238 +207,282 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 }
 
 // ------------------------------------------------------------------------ decoding a tile
-// What one side (K or V) of an item reads.
+// Formats as the decoding warps see them.
+enum { D_F16, D_F8, D_I4, D_CB4, D_CB3, D_CB2 };
+
+// A thread's piece of a row ("unit"), the passes of 128 threads that cover a tile, and how many
+// passes' units are on their way at a time.
+__host__ __device__ constexpr int unit_bytes(int f) { return f == D_CB3 ? 12 : (f == D_CB2 ? 8 : 16); }
+__host__ __device__ constexpr int unit_passes(int f) { return f == D_F16 ? 16 : (f == D_F8 ? 8 : 4); }
+__host__ __device__ constexpr int unit_slots(int f) { return f == D_F8 ? 8 : (f == D_I4 ? 4 : 2); }
+// Copies of a codebook's pair table, one per lane (eight of the 1 KB of 4-bit pairs).
+__host__ __device__ constexpr int lut_copies(int f) { return f == D_CB4 ? 8 : 32; }
+constexpr int kLutBytes = 8 << 10;
+
+// What one side (K or V) of an item reads, and where its pieces of shared memory lie.
 struct Source {
   const uint8_t* rows;
   const __half* aux;
   const int32_t* table;  // the group's block-table row
   int row_bytes, num_pages, page_size, page_shift, hkv, hk;
   int end;               // tokens of the prefix
-  uint32_t lut;          // shared address of the pair table (codebooks)
+  uint32_t lut, raw, rowbuf, auxbuf;  // shared addresses
+  int side;              // 0 keys, 1 values (named barrier 1 + side)
 };
-
-// Formats as the decoding warps see them.
-enum { D_F16, D_F8, D_I4, D_CB4, D_CB3, D_CB2 };
-__host__ __device__ constexpr int lanes_per_row(int f) { return f == D_F16 ? 16 : (f == D_F8 ? 8 : 4); }
-__host__ __device__ constexpr int unit_words(int f) { return f == D_CB3 ? 3 : (f == D_CB2 ? 2 : 4); }
-
-// A unit of one pass in a thread's registers, with its norm or group scale in both halves.
-template <int F>
-struct Unit {
-  uint32_t w[unit_words(F)], scale;
-};
-
-// Page of the token that the thread reads in pass P of the tile at t0 (-1 past the end).
-template <int F>
-__device__ __forceinline__ int page_of(const Source& s, int t0, int pass, int tid) {
-  const int t = t0 + pass * (128 / lanes_per_row(F)) + tid / lanes_per_row(F);
-  if (t >= s.end) return -1;
-  return __ldg(s.table + (s.page_shift >= 0 ? t >> s.page_shift : t / s.page_size));
-}
-
-// Where that token's unit lies, if it is there: false past the end and for a page outside the
-// pool (reported in bits).
-template <int F>
-__device__ __forceinline__ bool find_unit(const Source& s, int t0, int pass, int tid, int page, int* bits, size_t* row) {
-  const int t = t0 + pass * (128 / lanes_per_row(F)) + tid / lanes_per_row(F);
-  if (t >= s.end || !page_in_pool(page, s.num_pages, bits)) return false;
-  const int off = s.page_shift >= 0 ? t & (s.page_size - 1) : t % s.page_size;
-  *row = ((size_t)page * s.hkv + s.hk) * s.page_size + off;
-  return true;
-}
-
-template <int F>
-__device__ __forceinline__ void load_unit(const Source& s, int t0, int pass, int tid, int page, Unit<F>& x, int* bits) {
-  constexpr int L = lanes_per_row(F), W = unit_words(F);
-  const int u = tid % L;
-  size_t row;
-#pragma unroll
-  for (int k = 0; k < W; ++k) x.w[k] = 0u;  // a token that is not there reads as zero
-  x.scale = 0u;
-  if (!find_unit<F>(s, t0, pass, tid, page, bits, &row)) return;
-  const uint8_t* src = s.rows + row * s.row_bytes + u * (4 * W);
-  if constexpr (W == 4) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-    x.w[0] = v.x;
-    x.w[1] = v.y;
-    x.w[2] = v.z;
-    x.w[3] = v.w;
-  } else if constexpr (W == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-    x.w[0] = v.x;
-    x.w[1] = v.y;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 3; ++k) x.w[k] = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
-  }
-  if constexpr (F == D_I4) x.scale = __half_as_ushort(__ldg(s.aux + row * 4 + u));
-  else if constexpr (F >= D_CB4) x.scale = __half_as_ushort(__ldg(s.aux + row));
-}
-
-// The unit decoded to fp16, into its row of the tile.
-template <int F>
-__device__ __forceinline__ void store_unit(const Source& s, uint32_t tile, int pass, int tid, const Unit<F>& z) {
-  constexpr int L = lanes_per_row(F);
-  const int u = tid % L, t = pass * (128 / L) + tid / L;  // t: row of the tile
-  const uint32_t row = tile + t * 128;
-  const int x = t & 7;
-  if constexpr (F == D_F8) {
-    // 16 values, two chunks; the upper half's lanes store theirs in the other order, so that
-    // the eight lanes of a row meet eight different 16-byte banks
-    uint32_t h[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[k]) : "h"((uint16_t)(z.w[k / 2] >> (16 * (k & 1)))));
-    const uint32_t at = row + (u >> 2) * kHalfBytes;
-    const int c = (2 * u) & 7, odd = u >> 2;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool second = (i ^ odd) != 0;
-      sts16(at + (((c + second) ^ x) << 4), second ? h[4] : h[0], second ? h[5] : h[1], second ? h[6] : h[2],
-            second ? h[7] : h[3]);
-    }
-  } else {
-    // 32 values, four chunks of 8 (b bytes each); lanes of a row pair store them in four
-    // different orders, so that eight lanes meet eight different 16-byte banks
-    constexpr int B = F == D_I4 || F == D_CB4 ? 4 : (F == D_CB3 ? 3 : 2);
-    const uint32_t scale = z.scale * 0x10001u;
-    uint32_t c[4];
-    if constexpr (B == 4) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) c[k] = z.w[k];
-    } else if constexpr (B == 3) {
-      c[0] = z.w[0];
-      c[1] = __funnelshift_r(z.w[0], z.w[1], 24);
-      c[2] = __funnelshift_r(z.w[1], z.w[2], 16);
-      c[3] = z.w[2] >> 8;
-    } else {
-      c[0] = z.w[0];
-      c[1] = z.w[0] >> 16;
-      c[2] = z.w[1];
-      c[3] = z.w[1] >> 16;
-    }
-    const int flip = (u >> 1) ^ ((t & 1) << 1);
-    if (flip & 1) {
-      uint32_t y = c[0];
-      c[0] = c[1];
-      c[1] = y;
-      y = c[2];
-      c[2] = c[3];
-      c[3] = y;
-    }
-    if (flip & 2) {
-      uint32_t y = c[0];
-      c[0] = c[2];
-      c[2] = y;
-      y = c[1];
-      c[1] = c[3];
-      c[3] = y;
-    }
-    const uint32_t at = row + (u >> 1) * kHalfBytes;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t h[4];
-      if constexpr (F == D_I4) {
-        // nibbles as 1024 + n in fp16, minus 1032: exact; times the scale, rounded once
-        const uint32_t even = c[i] & 0x0F0F0F0Fu, odd = (c[i] >> 4) & 0x0F0F0F0Fu;
-        const __half2 off = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t v = (__byte_perm(even, odd, k | (k << 4) | ((4 + k) << 8) | (k << 12)) & 0x00FF00FFu) | 0x64006400u;
-          const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&v), off);
-          h[k] = hmul2(*reinterpret_cast<const uint32_t*>(&n), scale);
-        }
-      } else {
-        // pairs of codes through the block's table of centroid pairs / sqrt(D)
-        constexpr int C = F == D_CB4 ? 16 : 32;  // copies: one per lane (4 bits: per half-warp lane)
-        const uint32_t base = s.lut + 4u * (tid & (C - 1));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t e = (c[i] >> (2 * B * k)) & ((1u << (2 * B)) - 1u);
-          h[k] = hmul2(lds32(base + e * (4u * C)), scale);
-        }
-      }
-      sts16(at + (((4 * (u & 1) + (i ^ flip)) ^ x) << 4), h[0], h[1], h[2], h[3]);
-    }
-  }
-}
-
-// Tiles [tile0, tile1) of one side, into the ring.
 struct Ring {
   uint32_t tiles, full, empty;  // shared addresses
 };
 
-// A pass's registers are loaded with the next tile's unit as soon as its unit of this tile is
-// decoded, and its page number a tile before that: every load has a tile's time to arrive.
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;  // a token that is not there: reads as zero
+
+// Page of token t (-1 past the end).
+__device__ __forceinline__ int page_of(const Source& s, int t) {
+  if (t >= s.end) return -1;
+  return __ldg(s.table + (s.page_shift >= 0 ? t >> s.page_shift : t / s.page_size));
+}
+// Its row in the pool: kNoRow past the end, and for a page outside the pool (reported in bits).
+__device__ __forceinline__ uint32_t row_of(const Source& s, int t, int page, int* bits) {
+  if (t >= s.end || !page_in_pool(page, s.num_pages, bits)) return kNoRow;
+  const uint32_t off = s.page_shift >= 0 ? t & (s.page_size - 1) : t % s.page_size;
+  return ((uint32_t)page * s.hkv + s.hk) * s.page_size + off;  // below 2^32: the plan checks
+}
+// Its norm, or its four group scales.
+template <int F>
+__device__ __forceinline__ uint2 aux_of(const Source& s, uint32_t row) {
+  if (row == kNoRow) return make_uint2(0u, 0u);
+  if constexpr (F == D_I4) return __ldg(reinterpret_cast<const uint2*>(s.aux) + row);
+  else if constexpr (F >= D_CB4) return make_uint2(__half_as_ushort(__ldg(s.aux + row)), 0u);
+  else return make_uint2(0u, 0u);
+}
+
+// Token (row of the tile) and unit of a thread in pass p.  A quarter-warp holds eight tokens
+// and one unit, so that its 16-byte stores meet eight different banks of the swizzled tile; a
+// warp reads 64 neighbouring bytes of each row.
+template <int F>
+__device__ __forceinline__ void place(int p, int tid, int& t, int& u) {
+  if constexpr (F == D_F16) {
+    t = p * 8 + (tid >> 4);
+    u = tid & 15;
+  } else if constexpr (F == D_F8) {
+    t = (p >> 1) * 32 + (tid >> 5) * 8 + (tid & 7);
+    u = (p & 1) * 4 + ((tid >> 3) & 3);
+  } else {
+    t = p * 32 + (tid >> 5) * 8 + (tid & 7);
+    u = (tid >> 3) & 3;
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src, bool there) {
+  const int n = there ? N : 0;  // no bytes read, N zeros written
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// The side's 128 threads meet; true if all of them are well (so that they leave together).
+__device__ __forceinline__ bool side_sync(const Source& s, bool well) {
+  uint32_t all;
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.and.pred q, %2, 128, p;\nselp.u32 %0, 1, 0, q;\n}"
+               : "=r"(all)
+               : "r"((uint32_t)well), "r"(1 + s.side)
+               : "memory");
+  return all != 0;
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// The thread's unit of pass p towards its slot.
+template <int F>
+__device__ __forceinline__ void request(const Source& s, uint32_t rowbuf, int p, int tid) {
+  int t, u;
+  place<F>(p, tid, t, u);
+  const uint32_t row = lds32(rowbuf + 4u * t);
+  const bool there = row != kNoRow;
+  const uint8_t* src = s.rows + (size_t)(there ? row : 0) * s.row_bytes + u * unit_bytes(F);
+  const uint32_t dst = s.raw + ((p % unit_slots(F)) * 128 + tid) * unit_bytes(F);
+  if constexpr (unit_bytes(F) == 12) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) copy_async<4>(dst + 4 * k, src + 4 * k, there);
+  } else {
+    copy_async<unit_bytes(F)>(dst, src, there);
+  }
+}
+
+// The unit in its slot, decoded to fp16, into its row of the tile.
+template <int F>
+__device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, uint32_t auxbuf, int p, int tid) {
+  int t, u;
+  place<F>(p, tid, t, u);
+  const uint32_t slot = s.raw + ((p % unit_slots(F)) * 128 + tid) * unit_bytes(F);
+  const uint32_t row = tile + t * 128;
+  const int x = t & 7;
+  if constexpr (F == D_F8) {  // 16 values: two chunks
+    uint32_t w[4], h[8];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(slot));
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[k]) : "h"((uint16_t)(w[k / 2] >> (16 * (k & 1)))));
+    const uint32_t at = row + (u >> 2) * kHalfBytes;
+    const int c = (2 * u) & 7;
+    sts16(at + ((c ^ x) << 4), h[0], h[1], h[2], h[3]);
+    sts16(at + (((c + 1) ^ x) << 4), h[4], h[5], h[6], h[7]);
+  } else {  // 32 values: four chunks of 8
+    constexpr int B = F == D_I4 || F == D_CB4 ? 4 : (F == D_CB3 ? 3 : 2);
+    uint32_t c[4];
+    if constexpr (B == 4) {
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(slot));
+    } else if constexpr (B == 3) {
+      const uint32_t w0 = lds32(slot), w1 = lds32(slot + 4), w2 = lds32(slot + 8);
+      c[0] = w0;
+      c[1] = __funnelshift_r(w0, w1, 24);
+      c[2] = __funnelshift_r(w1, w2, 16);
+      c[3] = w2 >> 8;
+    } else {
+      const uint32_t w0 = lds32(slot), w1 = lds32(slot + 4);
+      c[0] = w0;
+      c[1] = w0 >> 16;
+      c[2] = w1;
+      c[3] = w1 >> 16;
+    }
+    uint16_t half_scale;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(half_scale) : "r"(auxbuf + 8u * t + (F == D_I4 ? 2u * u : 0u)));
+    const uint32_t scale = half_scale * 0x10001u;
+    const uint32_t at = row + (u >> 1) * kHalfBytes;
+    const uint32_t base = s.lut + 4u * (tid & (lut_copies(F) - 1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[4];
+      if constexpr (F == D_I4) {
+        // Levels n - 8 of nibbles (k, k + 4), exact in fp16: 1024 + n less 1032, or (from the
+        // upper nibble of a byte) (1024 + 16 n) / 16 less 72; times the scale, rounded once.  The
+        // pairs leave a chunk's coordinates in the order 0 4 1 5 2 6 3 7, and so the accumulator's
+        // columns (undone where it is stored).
+        const __half2 a = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));  // 1032
+        const __half2 b = __halves2half2(__ushort_as_half(0x2C00), __ushort_as_half(0x2C00));  // 1 / 16
+        const __half2 d = __halves2half2(__ushort_as_half(0xD480), __ushort_as_half(0xD480));  // -72
+        const uint32_t w = c[i], w8 = c[i] >> 8;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t lo = ((k ? w8 : w) & 0x000F000Fu) | 0x64006400u, hi = ((k ? w8 : w) & 0x00F000F0u) | 0x64006400u;
+          const __half2 nl = __hsub2(*reinterpret_cast<const __half2*>(&lo), a);
+          const __half2 nh = __hfma2(*reinterpret_cast<const __half2*>(&hi), b, d);
+          h[2 * k] = hmul2(*reinterpret_cast<const uint32_t*>(&nl), scale);
+          h[2 * k + 1] = hmul2(*reinterpret_cast<const uint32_t*>(&nh), scale);
+        }
+      } else {
+        // pairs of codes through the block's table of centroid pairs / sqrt(D)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t e = (c[i] >> (2 * B * k)) & ((1u << (2 * B)) - 1u);
+          h[k] = hmul2(lds32(base + e * (4u * lut_copies(F))), scale);
+        }
+      }
+      sts16(at + (((4 * (u & 1) + i) ^ x) << 4), h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+
+// Tiles [tile0, tile1) of one side, into the ring.  Rows travel by asynchronous copies into
+// slots that belong to the thread that decodes them (nobody else waits for them), a slot being
+// requested anew as soon as it is decoded.  Page numbers, rows, norms and scales are looked up
+// by one thread a token, a tile ahead.  The loops stay rolled: eight warps of four kinds share
+// the instruction caches of a scheduler, and unrolled passes spent more time fetching
+// instructions than running them.
 template <int F>
 __device__ __forceinline__ void produce(const Source& s, const Ring& ring, int tile0, int tile1, int tid,
                                         volatile int* abort, int* err) {
-  constexpr int kPasses = lanes_per_row(F);  // 128 threads, 128 rows
+  constexpr int kPasses = unit_passes(F), kSlots = unit_slots(F);
   int bits = 0;
-  Unit<F> x[kPasses];
-  int page[kPasses];
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) page[p] = page_of<F>(s, tile0 * kTileTokens, p, tid);
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) load_unit<F>(s, tile0 * kTileTokens, p, tid, page[p], x[p], &bits);
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) page[p] = page_of<F>(s, (tile0 + 1) * kTileTokens, p, tid);
-  for (int t = tile0, i = 0; t < tile1; ++t, ++i) {
+  int t = tile0 * kTileTokens + tid;  // the token this thread looks up
+  uint32_t row = row_of(s, t, page_of(s, t), &bits);
+  sts32(s.rowbuf + 4u * tid, row);
+  uint2 aux = aux_of<F>(s, row);
+  t += kTileTokens;
+  int page = page_of(s, t);
+  bool ok = side_sync(s, true);
+#pragma unroll 1
+  for (int p = 0; p < kSlots; ++p) {
+    request<F>(s, s.rowbuf, p, tid);
+    copy_commit();
+  }
+  uint32_t now = s.rowbuf, next = s.rowbuf + 4u * kTileTokens;
+  const int n = tile1 - tile0;
+  for (int i = 0; i < n; ++i) {
     const int st = i & 1;
-    if (i >= kStages && !bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err)) break;
-    const bool more = t + 1 < tile1;
-#pragma unroll
+    const uint32_t auxbuf = s.auxbuf + st * (8u * kTileTokens);
+    if constexpr (F >= D_I4)
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(auxbuf + 8u * tid), "r"(aux.x), "r"(aux.y) : "memory");
+    row = row_of(s, t, page, &bits);
+    sts32(next + 4u * tid, row);
+    aux = aux_of<F>(s, row);
+    t += kTileTokens;
+    page = page_of(s, t);
+    if (!side_sync(s, ok)) break;
+    if (i >= kStages && !(ok = bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err))) continue;
+#pragma unroll 1
     for (int p = 0; p < kPasses; ++p) {
-      store_unit<F>(s, ring.tiles + st * kTileBytes, p, tid, x[p]);
-      if (more) {
-        load_unit<F>(s, (t + 1) * kTileTokens, p, tid, page[p], x[p], &bits);
-        page[p] = page_of<F>(s, (t + 2) * kTileTokens, p, tid);
-      }
+      copy_wait<kSlots - 1>();
+      decode_unit<F>(s, ring.tiles + st * kTileBytes, auxbuf, p, tid);
+      const int q = p + kSlots;
+      if (q < kPasses) request<F>(s, now, q, tid);
+      else if (i + 1 < n) request<F>(s, next, q - kPasses, tid);
+      copy_commit();
     }
+    now = next;
+    next = next == s.rowbuf + 8u * kTileTokens ? s.rowbuf : next + 4u * kTileTokens;
     fence_async_smem();
     bar_arrive(ring.full + 8 * st);
   }
+  copy_wait<0>();
   if (bits) atomicOr(err, bits);
 }
 
-// fp16 rows need no decoding: asynchronous copies, a tile signalled once the next one's copies
-// are under way.
+// fp16 rows need no decoding: copies straight into the tile, a tile signalled once the next
+// one's copies are under way.
 template <>
 __device__ __forceinline__ void produce<D_F16>(const Source& s, const Ring& ring, int tile0, int tile1, int tid,
                                                volatile int* abort, int* err) {
-  constexpr int kPasses = lanes_per_row(D_F16);
   int bits = 0;
-  int page[kPasses];
-  const int u = tid % 16;
-#pragma unroll
-  for (int p = 0; p < kPasses; ++p) page[p] = page_of<D_F16>(s, tile0 * kTileTokens, p, tid);
+  int t = tile0 * kTileTokens + tid;
+  int page = page_of(s, t);
   bool ok = true;
-  for (int t = tile0, i = 0; t < tile1; ++t, ++i) {
+  const int n = tile1 - tile0;
+  uint32_t now = s.rowbuf;
+  for (int i = 0; i < n; ++i) {
     const int st = i & 1;
-    if (i >= kStages && !(ok = bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err))) break;
-    const uint32_t tile = ring.tiles + st * kTileBytes + (u >> 3) * kHalfBytes;
-#pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      size_t row = 0;
-      const bool there = find_unit<D_F16>(s, t * kTileTokens, p, tid, page[p], &bits, &row);
-      const int r = p * 8 + tid / 16;
-      // (a row that is not there: no bytes read, 16 zeros written)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tile + r * 128 + (((u & 7) ^ (r & 7)) << 4)),
-                   "l"(s.rows + row * s.row_bytes + u * 16), "r"(there ? 16 : 0)
-                   : "memory");
-      page[p] = page_of<D_F16>(s, (t + 1) * kTileTokens, p, tid);
+    sts32(now + 4u * tid, row_of(s, t, page, &bits));
+    t += kTileTokens;
+    page = page_of(s, t);
+    if (!side_sync(s, ok)) break;
+    if (i >= kStages && !(ok = bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err))) continue;
+#pragma unroll 2
+    for (int p = 0; p < unit_passes(D_F16); ++p) {
+      int r, u;
+      place<D_F16>(p, tid, r, u);
+      const uint32_t row = lds32(now + 4u * r);
+      const bool there = row != kNoRow;
+      copy_async<16>(ring.tiles + st * kTileBytes + (u >> 3) * kHalfBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4),
+                     s.rows + (size_t)(there ? row : 0) * s.row_bytes + u * 16, there);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    copy_commit();
+    now = now == s.rowbuf + 8u * kTileTokens ? s.rowbuf : now + 4u * kTileTokens;
     if (i > 0) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      copy_wait<1>();
       fence_async_smem();
       bar_arrive(ring.full + 8 * (st ^ 1));
     }
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  copy_wait<0>();
   if (ok) {
     fence_async_smem();
-    bar_arrive(ring.full + 8 * ((tile1 - tile0 - 1) & 1));
+    bar_arrive(ring.full + 8 * ((n - 1) & 1));
   }
   if (bits) atomicOr(err, bits);
 }
@@ -460,10 +508,9 @@ __device__ __forceinline__ int decode_kind(int fmt, int bits) {
   }
 }
 
-// Pairs of centroids / sqrt(D) in fp16: entry e = codes (e mod 2^b, e / 2^b), a copy per lane of
-// a warp (16 copies of 4-bit pairs).  tid: 256 threads.
+// Pairs of centroids / sqrt(D) in fp16: entry e = codes (e mod 2^b, e / 2^b).  tid: 256 threads.
 __device__ __forceinline__ void build_lut(uint32_t lut, const float* cent, int bits, int tid) {
-  const int copies = bits == 4 ? 16 : 32;
+  const int copies = lut_copies(bits == 4 ? D_CB4 : D_CB3);
   if (tid >= (1 << (2 * bits))) return;
   const float inv = inv_sqrt_dim(kDim);
   const uint32_t v = half2_bits(__ldg(cent + (tid & ((1 << bits) - 1))) * inv, __ldg(cent + (tid >> bits)) * inv);
@@ -588,9 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (T.k_fmt == KVQ_FMT_CODEBOOK && warp < 8) build_lut(smem + kOffLut, T.k_cent, T.k_bits, threadIdx.x);
+  if (T.k_fmt == KVQ_FMT_CODEBOOK && warp < 8) build_lut(smem + kOffRaw, T.k_cent, T.k_bits, threadIdx.x);
   if (T.v_fmt == KVQ_FMT_CODEBOOK && warp >= 8 && warp < 16)
-    build_lut(smem + kOffLut + kLutBytes, T.v_cent, T.v_bits, threadIdx.x - 256);
+    build_lut(smem + kOffRaw + kRawBytes / 2, T.v_cent, T.v_bits, threadIdx.x - 256);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -633,14 +680,17 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         const int valid = min(kTileTokens, len - tile * kTileTokens);
         if (!(ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * (B_SFULL + w), k & 1, abort, p.err)))) break;
         tc_fence_after();
-        uint32_t va[32], vb[32];
-        tc_ld32(s_at, va);
-        // 32 scores: the row's maximum (a rise of more than 2^8 rescales), weights, their sum
-        auto weigh = [&](int c, uint32_t (&v)[32], uint32_t (&next)[32]) {
+        // 32 scores at a time: the row's maximum (a rise of more than 2^8 rescales), weights, their
+        // sum.  (Rolled, as the decoding loops are.)
+#pragma unroll 1
+        for (int c = 0; c < kTileTokens; c += 32) {
+          uint32_t v[32];
+          tc_ld32(s_at + c, v);
+          tc_wait_ld(v);
           if (valid < kTileTokens) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= valid) v[e] = 0xFF800000u;  // -inf: weight 0
+              if (c + e >= valid) v[e] = 0xFF800000u;  // -inf: weight 0
           }
           float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
@@ -655,8 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
             const float2 ll = unpack2(l2);
             l2 = pack2(ll.x * f, ll.y * f);
             // (the products of earlier tiles are complete: they precede these scores)
-            tc_wait_ld(next);  // nothing in flight across the call
-            if (k > 0 || c > 0) rescale(o_at, k > 0, s_at, 16 * c, f);
+            if (k > 0 || c > 0) rescale(o_at, k > 0, s_at, c / 2, f);
           }
           const unsigned long long neg = pack2(-m, -m);
           uint32_t h[16];
@@ -667,19 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
             l2 = add2(l2, pack2(a, b));
             h[e] = half2_bits(a, b);
           }
-          tc_st16(s_at + 16 * c, h);  // over scores that this warp has read
-        };
-        tc_wait_ld(va);
-        tc_ld32(s_at + 32, vb);
-        weigh(0, va, vb);
-        tc_wait_ld(vb);
-        tc_ld32(s_at + 64, va);
-        weigh(1, vb, va);
-        tc_wait_ld(va);
-        tc_ld32(s_at + 96, vb);
-        weigh(2, va, vb);
-        tc_wait_ld(vb);
-        weigh(3, vb, va);
+          tc_st16(s_at + c / 2, h);  // over scores that this warp has read
+        }
         tc_wait_st();
         tc_fence_before();
         bar_arrive(bars + 8 * (B_PREADY + w));
@@ -694,12 +732,16 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
           tc_wait_ld(v);
           if (out_row >= 0) {
             float* dst = p.acc + (part + out_row) * kDim + 32 * c;
+            const bool int4 = T.v_fmt == KVQ_FMT_INT4_G32;  // columns 0 4 1 5 2 6 3 7 of every eight
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + e), "r"(v[e]),
-                           "r"(v[e + 1]), "r"(v[e + 2]), "r"(v[e + 3]), "r"(v[e + 4]), "r"(v[e + 5]), "r"(v[e + 6]),
-                           "r"(v[e + 7])
+            for (int e = 0; e < 32; e += 8) {
+              const uint32_t o1 = int4 ? v[e + 2] : v[e + 1], o2 = int4 ? v[e + 4] : v[e + 2];
+              const uint32_t o3 = int4 ? v[e + 6] : v[e + 3], o4 = int4 ? v[e + 1] : v[e + 4];
+              const uint32_t o5 = int4 ? v[e + 3] : v[e + 5], o6 = int4 ? v[e + 5] : v[e + 6];
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + e), "r"(v[e]), "r"(o1),
+                           "r"(o2), "r"(o3), "r"(o4), "r"(o5), "r"(o6), "r"(v[e + 7])
                            : "memory");
+            }
           }
         }
       }
@@ -723,7 +765,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     s.hkv = p.hkv;
     s.hk = hk;
     s.end = len;
-    s.lut = smem + kOffLut + (keys ? 0 : kLutBytes);
+    // codebooks: half of the area a side, the table first; otherwise 16 KB of keys, 8 of values
+    const bool codes = T.k_fmt == KVQ_FMT_CODEBOOK;
+    s.lut = smem + kOffRaw + (keys ? 0 : kRawBytes / 2);
+    s.raw = codes ? s.lut + kLutBytes : smem + kOffRaw + (keys ? 0 : 16 << 10);
+    s.rowbuf = smem + kOffRow + (keys ? 0 : kRowBytes);
+    s.auxbuf = smem + kOffAux + (keys ? 0 : kAuxBytes);
+    s.side = keys ? 0 : 1;
     Ring ring;
     ring.tiles = smem + (keys ? kOffK : kOffV);
     ring.full = bars + 8 * (keys ? B_KFULL : B_VFULL);
