@@ -165,6 +165,13 @@ __device__ __forceinline__ uint64_t desc_base(uint32_t leading, uint32_t stride)
 }
 __device__ __forceinline__ uint64_t desc_at(uint64_t base, uint32_t addr) { return base | ((addr >> 4) & 0x3FFFu); }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
+}
+
 // f16 inputs, f32 accumulator, 128 x 128; bit 16: B is MN-major
 constexpr uint32_t kIdescQK = (1u << 4) | ((kTileTokens >> 3) << 17) | ((kTileRows >> 4) << 24);
 constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((kDim >> 3) << 17) | ((kTileRows >> 4) << 24);
@@ -568,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (smem - smem_u32(smem_raw)) + kOffCtl);
   volatile int* abort = &ctl->abort;
   const uint32_t bars = smem + kOffCtl;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
 
   // ---- the item: split, kv head, row block (blocks of one split and head side by side, so
   // that they meet the same cache bytes in L2)
@@ -781,40 +788,51 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   } else {
     // ---- products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-    if (warp == 16 && lane == 0) {
-    const uint64_t kmajor = desc_base(16, 1024), mnmajor = desc_base(kHalfBytes, 1024);
-    auto scores = [&](int i) -> bool {  // S of job i
-      const int tile = both ? i : i >> 1, st = tile & 1, ws = i & 1;
-      if (!bar_wait(bars + 8 * (B_KFULL + st), (tile >> 1) & 1, abort, p.err)) return false;
-      tc_fence_after();
-      const uint32_t a = smem + kOffQ + ws * kTileBytes, b = smem + kOffK + st * kTileBytes;
+    // The whole warp walks the jobs and one lane issues: with all of it uniform, descriptors are
+    // formed in uniform registers (issued from one lane's branch, each product cost about 110
+    // cycles of register moves, twice what it takes to run).
+    if (warp == 16) {
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const uint64_t qd = desc_at(desc_base(16, 1024), smem + kOffQ), kd = desc_at(desc_base(16, 1024), smem + kOffK);
+      const uint64_t vd = desc_at(desc_base(kHalfBytes, 1024), smem + kOffV);
+      auto well = [&](uint32_t bar, uint32_t parity) -> bool {
+        return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, abort, p.err));
+      };
+      auto scores = [&](int i) -> bool {  // S of job i
+        const int tile = both ? i : i >> 1, st = tile & 1, ws = i & 1;
+        if (!well(bars + 8 * (B_KFULL + st), (tile >> 1) & 1)) return false;
+        tc_fence_after();
+        const uint64_t a = qd + ws * (kTileBytes >> 4), b = kd + st * (kTileBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < kDim / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * kHalfBytes + (kk & 3) * 32;
-        mma_ss(tmem + ws * 128, desc_at(kmajor, a + off), desc_at(kmajor, b + off), kIdescQK, kk > 0);
+          for (int kk = 0; kk < kDim / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+            mma_ss(tm + ws * 128, a + off, b + off, kIdescQK, kk > 0);
+          }
+          tc_commit(bars + 8 * (B_SFULL + ws));
+          if (both || ws) tc_commit(bars + 8 * (B_KEMPTY + st));
+        }
+        __syncwarp();
+        return true;
+      };
+      bool ok = true;
+      for (int i = 0; i < 2 && i < jobs && ok; ++i) ok = well(bars + 8 * (B_QFULL + i), 0) && scores(i);
+      for (int i = 0; i < jobs && ok; ++i) {
+        const int tile = both ? i : i >> 1, st = tile & 1, ws = i & 1;
+        ok = well(bars + 8 * (B_VFULL + st), (tile >> 1) & 1) && well(bars + 8 * (B_PREADY + ws), (i >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t b = vd + st * (kTileBytes >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kTileTokens / 16; ++kk)
+            mma_ts(tm + 256 + ws * 128, tm + ws * 128 + kk * 8, b + ((kk * 2048) >> 4), kIdescPV, i > 1 || kk > 0);
+          tc_commit(bars + 8 * (B_OFULL + ws));
+          if (both || ws) tc_commit(bars + 8 * (B_VEMPTY + st));
+        }
+        __syncwarp();
+        if (i + 2 < jobs) ok = scores(i + 2);
       }
-      tc_commit(bars + 8 * (B_SFULL + ws));
-      if (both || ws) tc_commit(bars + 8 * (B_KEMPTY + st));
-      return true;
-    };
-    bool ok = true;
-    for (int i = 0; i < 2 && i < jobs && ok; ++i)
-      ok = bar_wait(bars + 8 * (B_QFULL + i), 0, abort, p.err) && scores(i);
-    for (int i = 0; i < jobs && ok; ++i) {
-      const int tile = both ? i : i >> 1, st = tile & 1, ws = i & 1;
-      ok = bar_wait(bars + 8 * (B_VFULL + st), (tile >> 1) & 1, abort, p.err) &&
-           bar_wait(bars + 8 * (B_PREADY + ws), (i >> 1) & 1, abort, p.err);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t b = smem + kOffV + st * kTileBytes;
-#pragma unroll
-      for (int kk = 0; kk < kTileTokens / 16; ++kk)
-        mma_ts(tmem + 256 + ws * 128, tmem + ws * 128 + kk * 8, desc_at(mnmajor, b + kk * 2048), kIdescPV,
-               i > 1 || kk > 0);
-      tc_commit(bars + 8 * (B_OFULL + ws));
-      if (both || ws) tc_commit(bars + 8 * (B_VEMPTY + st));
-      if (i + 2 < jobs) ok = scores(i + 2);
-    }
     }
   }
   __syncwarp();
