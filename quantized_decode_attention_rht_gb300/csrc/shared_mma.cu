@@ -20,9 +20,9 @@
 // tile; with up to 128 rows both have the same rows and take alternate tiles, which leaves two
 // partial results.  TMEM: two S and two O of 128 columns, all 512.
 //
-// An accumulator is rescaled only when its row's maximum grows by more than 2^8 (weights
-// then stay below 256, far inside fp16, and the sums are float32), which after the first tiles
-// is rare.
+// An accumulator is rescaled only when a tile's weights against the running maximum sum to
+// more than 2^14 in some row of a warp, which after the first tile is rare: until then
+// weights stay inside fp16 and the sums, in float32, inside their range.
 //
 // Rounded to fp16 on the way, each a half-ulp of 2^-11: the rotated queries, the decoded keys
 // and values where their format is not exact in fp16 (fp16 and fp8 are; INT4 levels times
@@ -40,8 +40,8 @@ namespace {
 
 constexpr int kDim = 128;
 constexpr int kThreads = 640;
-// registers per thread after the split: launched with 96 x 640 = 61440 = 256 x 136 + 256 x 88 + 128 x 32
-constexpr int kSoftmaxRegs = 136, kDecodeRegs = 88, kIssueRegs = 32;
+// registers per thread after the split: launched with 96 x 640 = 61440 = 256 x 152 + 256 x 72 + 128 x 32
+constexpr int kSoftmaxRegs = 152, kDecodeRegs = 72, kIssueRegs = 32;
 constexpr int kTileBytes = kTileTokens * kDim * 2;  // 32 KB: two halves of 128 rows x 128 bytes
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kStages = 2;
@@ -525,31 +525,21 @@ __device__ __forceinline__ void build_lut(uint32_t lut, const float* cent, int b
 }
 
 // ------------------------------------------------------------------------ softmax
-// A row's maximum has grown: from f on (2^(old - new)), scale what the old one is in: the
-// accumulator (if any product has gone into it) and the tile's first `done` weight columns.
-__device__ __forceinline__ void rescale(uint32_t o_at, bool acc, uint32_t p_at, int done, float f) {
+// A tile's weights against the running maximum may sum to this before it is raised (the largest
+// fp16 is 2^16).
+constexpr float kMostWeight = 16384.0f;
+
+// A row's maximum has grown: the accumulator is scaled by f = 2^(old - new).
+__device__ __forceinline__ void rescale(uint32_t o_at, float f) {
   uint32_t v[16];
-  if (acc) {
 #pragma unroll 1
-    for (int c = 0; c < kDim; c += 16) {
-      tc_ld16(o_at + c, v);
-      tc_wait_ld(v);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-      tc_st16(o_at + c, v);
-    }
-  }
-  for (int c = 0; c < done; c += 16) {
-    tc_ld16(p_at + c, v);
+  for (int c = 0; c < kDim; c += 16) {
+    tc_ld16(o_at + c, v);
     tc_wait_ld(v);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
-      v[e] = half2_bits(x.x * f, x.y * f);
-    }
-    tc_st16(p_at + c, v);
+    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+    tc_st16(o_at + c, v);
   }
-  tc_wait_st();
 }
 
 __device__ __forceinline__ unsigned long long pack2(float a, float b) {
@@ -687,43 +677,70 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         const int valid = min(kTileTokens, len - tile * kTileTokens);
         if (!(ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * (B_SFULL + w), k & 1, abort, p.err)))) break;
         tc_fence_after();
-        // 32 scores at a time: the row's maximum (a rise of more than 2^8 rescales), weights, their
-        // sum.  (Rolled, as the decoding loops are.)
+        // Weights of the whole tile against the running maximum as it is, kept in registers: no
+        // maximum is taken.  All weights are positive, so a sum of at most kMostWeight says that
+        // none is too large for fp16 either; only where it is exceeded (always in the first tile,
+        // where the maximum is -inf) the maximum is raised and the tile, still in TMEM, weighed
+        // again.
+        uint32_t h[64];
+        unsigned long long sum;
 #pragma unroll 1
-        for (int c = 0; c < kTileTokens; c += 32) {
-          uint32_t v[32];
-          tc_ld32(s_at + c, v);
-          tc_wait_ld(v);
-          if (valid < kTileTokens) {
+        for (int again = 0;; ++again) {
+          const unsigned long long neg = pack2(-m, -m);
+          unsigned long long s0 = 0, s1 = 0;
+          auto weigh = [&](int c, uint32_t (&v)[32]) {
+            if (valid < kTileTokens) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c + e >= valid) v[e] = 0xFF800000u;  // -inf: weight 0
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 x = unpack2(add2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), neg));
+              const float a = ex2(x.x), b = ex2(x.y);
+              if (e & 1) s1 = add2(s1, pack2(a, b));
+              else s0 = add2(s0, pack2(a, b));
+              h[c / 2 + e] = half2_bits(a, b);
+            }
+          };
+          uint32_t va[32], vb[32];
+          tc_ld32(s_at, va);
+          tc_wait_ld(va);
+          tc_ld32(s_at + 32, vb);
+          weigh(0, va);
+          tc_wait_ld(vb);
+          tc_ld32(s_at + 64, va);
+          weigh(32, vb);
+          tc_wait_ld(va);
+          tc_ld32(s_at + 96, vb);
+          weigh(64, va);
+          tc_wait_ld(vb);
+          weigh(96, vb);
+          sum = add2(s0, s1);
+          const float2 t = unpack2(sum);
+          if (again || __all_sync(0xFFFFFFFFu, t.x + t.y <= kMostWeight)) break;
+          float mx = m;
+#pragma unroll 1
+          for (int c = 0; c < kTileTokens; c += 32) {
+            tc_ld32(s_at + c, va);
+            tc_wait_ld(va);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (c + e >= valid) v[e] = 0xFF800000u;  // -inf: weight 0
+              if (c + e < valid) mx = fmaxf(mx, __uint_as_float(va[e]));
           }
-          float m0 = -INFINITY, m1 = -INFINITY;
+          const float f = ex2(m - mx);
+          m = mx;
+          const float2 ll = unpack2(l2);
+          l2 = pack2(ll.x * f, ll.y * f);
+          if (k > 0) rescale(o_at, f);  // the products of earlier tiles are complete: they precede these scores
+        }
+        l2 = add2(l2, sum);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            m0 = fmaxf(fmaxf(m0, __uint_as_float(v[e])), __uint_as_float(v[e + 1]));
-            m1 = fmaxf(fmaxf(m1, __uint_as_float(v[e + 2])), __uint_as_float(v[e + 3]));
-          }
-          const float mx = fmaxf(m0, m1);
-          if (__any_sync(0xFFFFFFFFu, mx > m + 8.0f)) {
-            const float mn = fmaxf(m, mx), f = ex2(m - mn);
-            m = mn;
-            const float2 ll = unpack2(l2);
-            l2 = pack2(ll.x * f, ll.y * f);
-            // (the products of earlier tiles are complete: they precede these scores)
-            if (k > 0 || c > 0) rescale(o_at, k > 0, s_at, c / 2, f);
-          }
-          const unsigned long long neg = pack2(-m, -m);
-          uint32_t h[16];
+        for (int c = 0; c < 64; c += 16) {  // over the scores
+          uint32_t part[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 x = unpack2(add2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), neg));
-            const float a = ex2(x.x), b = ex2(x.y);
-            l2 = add2(l2, pack2(a, b));
-            h[e] = half2_bits(a, b);
-          }
-          tc_st16(s_at + c / 2, h);  // over scores that this warp has read
+          for (int e = 0; e < 16; ++e) part[e] = h[c + e];
+          tc_st16(s_at + c, part);
         }
         tc_wait_st();
         tc_fence_before();
