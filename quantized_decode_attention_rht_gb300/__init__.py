@@ -165,28 +165,72 @@ def _dense(*tensors) -> None:
             raise ValueError("tensors passed to libkvq must be contiguous")
 
 
+_torch = None
+_DTYPES = {}
+
+
+def _load_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+        for name in ("float16", "float32", "int32", "int64", "uint8"):
+            _DTYPES[name] = getattr(torch, name)
+    return _torch
+
+
 def _arg(t, name: str, dtype: str, shape=None, min_numel: int = 0) -> None:
     """The C ABI takes device pointers of fixed element types: refuse a host tensor, another
     dtype, a shape that disagrees with the call (None entries in `shape` are free) or fewer
     elements than the call reads, before the library is called."""
     if t is None:
         return
-    import torch
+    if _torch is None:
+        _load_torch()
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != getattr(torch, dtype):
+    if t.dtype is not _DTYPES[dtype]:
         raise TypeError(f"{name} must be torch.{dtype}, got {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape))):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)} (None: any)")
-    if t.numel() < min_numel:
+    if shape is not None:
+        have = t.shape
+        if len(have) != len(shape):
+            raise ValueError(f"{name} has shape {tuple(have)}, expected {tuple(shape)} (None: any)")
+        for w, n in zip(shape, have):
+            if w is not None and w != n:
+                raise ValueError(f"{name} has shape {tuple(have)}, expected {tuple(shape)} (None: any)")
+    if min_numel and t.numel() < min_numel:
         raise ValueError(f"{name} holds {t.numel()} elements, the call reads {min_numel}")
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
+        torch = _load_torch()
         return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _call_stream(stream, *tensors) -> Optional[int]:
+    """The stream of a call, whose tensors lie on one device: the current one, unless the caller
+    names a stream (of that device)."""
+    torch = _load_torch()
+    index = None
+    for t in tensors:
+        if t is None or not hasattr(t, "get_device"):
+            continue
+        d = t.get_device()
+        if index is None:
+            index = d
+        elif d != index:
+            raise ValueError(f"tensors of one call on different devices: cuda:{index} and cuda:{d}")
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    if index is None:
+        return _stream(None)
+    current = torch.cuda.current_device()
+    if index != current:
+        raise ValueError(f"tensors on cuda:{index}, but the current device is cuda:{current}")
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same stream, without an object around it
+    return raw(index) if raw is not None else torch.cuda.current_stream().cuda_stream
 
 
 # ----------------------------------------------------------------------------- host-side entry points
@@ -293,44 +337,34 @@ def kvq_requantize(src: KvqCache, src_slots, dst: KvqCache, dst_slots, stream=No
                                 int(src_slots.shape[0]), _stream(stream)), "kvq_requantize")
 
 
-def _on_device(stream, *tensors) -> None:
-    """The tensors of one call lie on one device, which is the current one unless the caller
-    names a stream (of that device)."""
-    devices = {t.device for t in tensors if t is not None and hasattr(t, "device")}
-    if len(devices) > 1:
-        raise ValueError(f"tensors of one call on different devices: {sorted(map(str, devices))}")
-    if devices and stream is None:
-        import torch
-        d = devices.pop()
-        if d.index is not None and d.index != torch.cuda.current_device():
-            raise ValueError(f"tensors on {d}, but the current device is cuda:{torch.cuda.current_device()}")
-
-
 def _check_heads(x, name: str, tokens: int, head_dim: int, num_heads=None, out=None) -> None:
     """x (and out, where given, of its shape): fp16 [tokens, heads, head_dim], the elements of a
     head adjacent, token and head strides free."""
-    for t, what in ((x, name), (out, name + "_out")):
-        if t is None:
-            continue
-        _arg(t, what, "float16", (tokens, num_heads, head_dim) if t is x else tuple(x.shape))
-        if t.stride(2) != 1:
-            raise ValueError(f"the elements of a head of {what} must be adjacent")
-    if x is not None and x.shape[1] == 0:
+    if x is None:
+        return
+    _arg(x, name, "float16", (tokens, num_heads, head_dim))
+    if x.stride(2) != 1:
+        raise ValueError(f"the elements of a head of {name} must be adjacent")
+    if x.shape[1] == 0:
         raise ValueError(f"{name} needs at least one head")
+    if out is not None:
+        _arg(out, name + "_out", "float16", x.shape)
+        if out.stride(2) != 1:
+            raise ValueError(f"the elements of a head of {name}_out must be adjacent")
 
 
-def _heads(x, out=None, write: bool = False) -> Optional[KvqHeads]:
-    """Checked heads as the C ABI's struct; write: the call writes `out`, or x itself where it
-    is None."""
+def _heads(x, out=None, write: bool = False):
+    """Checked heads by reference to the C ABI's struct (None for no heads); write: the call
+    writes `out`, or x itself where it is None."""
     if x is None:
         return None
-    h = KvqHeads()
-    h.num_heads = x.shape[1]
-    h.x, h.x_token_stride, h.x_head_stride = x.data_ptr(), x.stride(0), x.stride(1)
-    if write:
-        dst = x if out is None else out
-        h.out, h.out_token_stride, h.out_head_stride = dst.data_ptr(), dst.stride(0), dst.stride(1)
-    return h
+    st, sh, _ = x.stride()
+    if not write:
+        return ctypes.byref(KvqHeads(x.data_ptr(), None, x.shape[1], st, sh, 0, 0))
+    if out is None:
+        return ctypes.byref(KvqHeads(x.data_ptr(), x.data_ptr(), x.shape[1], st, sh, st, sh))
+    ot, oh, _ = out.stride()
+    return ctypes.byref(KvqHeads(x.data_ptr(), out.data_ptr(), x.shape[1], st, sh, ot, oh))
 
 
 def kvq_rope_apply(rope: "Rope", positions, q, k=None, q_out=None, k_out=None, transpose: bool = False,
@@ -344,10 +378,12 @@ def kvq_rope_apply(rope: "Rope", positions, q, k=None, q_out=None, k_out=None, t
     _arg(positions, "positions", "int32", (None,), min_numel=t)
     _check_heads(q, "q", t, d, out=q_out)
     _check_heads(k, "k", t, d, out=k_out)
-    _on_device(stream, q, k, q_out, k_out, positions)
-    a, b = _heads(q, q_out, True), _heads(k, k_out, True)
-    _check(lib().kvq_rope_apply(ctypes.byref(rope.struct), _ptr(positions), ctypes.byref(a), ctypes.byref(b) if b else None, t, d,
-                                1 if transpose else 0, _stream(stream)), "kvq_rope_apply")
+    status = (_lib_handle or lib()).kvq_rope_apply(ctypes.byref(rope.struct), positions.data_ptr(),
+                                                   _heads(q, q_out, True), _heads(k, k_out, True), t, d,
+                                                   1 if transpose else 0,
+                                                   _call_stream(stream, q, k, q_out, k_out, positions))
+    if status:
+        raise KvqError(status, "kvq_rope_apply")
 
 
 def kvq_rope_append(cache: KvqCache, rope: "Rope", positions, k, v, slot_mapping, q=None, q_out=None,
@@ -366,10 +402,12 @@ def kvq_rope_append(cache: KvqCache, rope: "Rope", positions, k, v, slot_mapping
     _check_heads(k, "k", t, d, cache.num_kv_heads)
     _check_heads(v, "v", t, d, cache.num_kv_heads)
     _check_heads(q, "q", t, d, out=q_out)
-    _on_device(stream, k, v, q, q_out, positions, slot_mapping)
-    kh, vh, qh = (ctypes.byref(h) if h else None for h in (_heads(k), _heads(v), _heads(q, q_out, True)))
-    _check(lib().kvq_rope_append(ctypes.byref(cache), ctypes.byref(rope.struct), _ptr(positions), kh, vh, qh, t,
-                                 _ptr(slot_mapping), _stream(stream)), "kvq_rope_append")
+    status = (_lib_handle or lib()).kvq_rope_append(ctypes.byref(cache), ctypes.byref(rope.struct),
+                                                    positions.data_ptr(), _heads(k), _heads(v),
+                                                    _heads(q, q_out, True), t, slot_mapping.data_ptr(),
+                                                    _call_stream(stream, k, v, q, q_out, positions, slot_mapping))
+    if status:
+        raise KvqError(status, "kvq_rope_append")
 
 
 def kvq_dequantize(cache: KvqCache, slots, k_out=None, v_out=None, stream=None) -> None:
@@ -382,25 +420,27 @@ def kvq_dequantize(cache: KvqCache, slots, k_out=None, v_out=None, stream=None) 
     t = int(slots.shape[0])
     for x, name in ((k_out, "k_out"), (v_out, "v_out")):
         _arg(x, name, "float16", (t, cache.num_kv_heads, cache.head_dim))
-    _on_device(stream, slots, k_out, v_out)
-    _check(lib().kvq_dequantize(ctypes.byref(cache), _ptr(slots), t, _ptr(k_out), _ptr(v_out), _stream(stream)),
-           "kvq_dequantize")
+    status = (_lib_handle or lib()).kvq_dequantize(ctypes.byref(cache), slots.data_ptr(), t, _ptr(k_out),
+                                                   _ptr(v_out), _call_stream(stream, slots, k_out, v_out))
+    if status:
+        raise KvqError(status, "kvq_dequantize")
 
 
 def _views(tiers: Sequence["TierView"], batch: int = 0):
     """The tiers as the C ABI's array; `batch` > 0: the call reads that many rows of every
     block table and entries of every length array."""
     arr = (KvqTierView * len(tiers))()
-    for i, t in enumerate(tiers):
-        _dense(t.block_table, t.seq_lens)
-        _arg(t.block_table, "block_table", "int32", (None, None))
-        _arg(t.seq_lens, "seq_lens", "int32", (None,), min_numel=batch)
-        if batch and t.block_table is not None and t.block_table.shape[0] < batch:
-            raise ValueError(f"block_table has {t.block_table.shape[0]} rows for {batch} sequences")
-        arr[i].cache = ctypes.pointer(t.cache.struct)
-        arr[i].block_table = _ptr(t.block_table)
-        arr[i].seq_lens = _ptr(t.seq_lens)
-        arr[i].max_pages = int(t.block_table.shape[1]) if t.block_table is not None else 0
+    for v, t in zip(arr, tiers):
+        table, lens = t.block_table, t.seq_lens
+        _dense(table, lens)
+        _arg(table, "block_table", "int32", (None, None))
+        _arg(lens, "seq_lens", "int32", (None,), min_numel=batch)
+        if batch and table is not None and table.shape[0] < batch:
+            raise ValueError(f"block_table has {table.shape[0]} rows for {batch} sequences")
+        v.cache = ctypes.pointer(t.cache.struct)
+        v.block_table = _ptr(table)
+        v.seq_lens = _ptr(lens)
+        v.max_pages = int(table.shape[1]) if table is not None else 0
     return arr
 
 
@@ -444,17 +484,20 @@ def kvq_decode_attention(tiers, q, out, workspace, split_tokens: int = 0, stream
                                          ws_bytes, ctypes.byref(opts), _stream(stream)), "kvq_decode_attention_ex")
 
 
-def _offsets(group_offsets) -> np.ndarray:
-    off = np.ascontiguousarray(group_offsets, dtype=np.int32)
-    if off.ndim != 1 or off.size < 2:
+def _offsets(group_offsets):
+    """groups + 1 sequence numbers as a C array of int32."""
+    off = [int(x) for x in group_offsets]
+    if len(off) < 2:
         raise ValueError("group_offsets holds num_groups + 1 sequence numbers")
-    return off
+    if min(off) < -(2 ** 31) or max(off) >= 2 ** 31:
+        raise ValueError("group_offsets holds numbers beyond int32")
+    return (ctypes.c_int32 * len(off))(*off)
 
 
 def kvq_decode_shared_workspace_size(prefix_tiers, group_offsets, tiers, batch: int, num_q_heads: int) -> int:
     off, n = _offsets(group_offsets), ctypes.c_size_t()
     pre, own = _views(prefix_tiers), _views(tiers) if tiers else None
-    _check(lib().kvq_decode_shared_workspace_size(pre, len(prefix_tiers), off.ctypes.data, off.size - 1, own,
+    _check(lib().kvq_decode_shared_workspace_size(pre, len(prefix_tiers), off, len(off) - 1, own,
                                                   len(tiers or ()), batch, num_q_heads, ctypes.byref(n)),
            "kvq_decode_shared_workspace_size")
     return n.value
@@ -476,13 +519,15 @@ def kvq_decode_attention_shared(prefix_tiers, group_offsets, tiers, q, out, work
     _arg(status, "status", "int32", None, min_numel=1)
     if workspace is None or not getattr(workspace, "is_cuda", False):
         raise ValueError("workspace must be a CUDA tensor")
-    _on_device(stream, q, out, workspace, status)
     b, hq = int(q.shape[0]), int(q.shape[1])
-    pre, own = _views(prefix_tiers, off.size - 1), _views(tiers, b) if tiers else None
-    _check(lib().kvq_decode_attention_shared(pre, len(prefix_tiers), off.ctypes.data, off.size - 1, own,
-                                             len(tiers or ()), _ptr(q), b, hq, _ptr(out), _ptr(workspace),
-                                             workspace.numel() * workspace.element_size(), _ptr(status),
-                                             _stream(stream)), "kvq_decode_attention_shared")
+    pre, own = _views(prefix_tiers, len(off) - 1), _views(tiers, b) if tiers else None
+    result = (_lib_handle or lib()).kvq_decode_attention_shared(
+        pre, len(prefix_tiers), off, len(off) - 1, own, len(tiers or ()), q.data_ptr(), b, hq, out.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status),
+        _call_stream(stream, q, out, workspace, status, *(x for t in (*prefix_tiers, *(tiers or ()))
+                                                          for x in (t.block_table, t.seq_lens))))
+    if result:
+        raise KvqError(result, "kvq_decode_attention_shared")
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20

@@ -1,6 +1,6 @@
 // Decode attention for groups of sequences that share a cached prefix
-// (kvq_decode_attention_shared): host side, the query rotation before the prefix pass and the
-// pass that joins the partial results.
+// (kvq_decode_attention_shared): host side and the pass that
+// joins the partial results.
 //
 // With O_i = sum_t 2^(s_t - m_i) V_t, l_i = sum_t 2^(s_t - m_i) over the tokens of part i of a
 // row's context and m_i the part's largest score, the row's output is
@@ -17,23 +17,6 @@
 
 namespace kvq {
 namespace {
-
-// ------------------------------------------------------------------------ queries
-// One warp per query head: H s q / sqrt(D), times log2(e) / sqrt(D) so that scores are in
-// base-2 units, rounded to fp16.
-__global__ void __launch_bounds__(kWarps * 32) rotate_queries_kernel(const uint16_t* q, const int8_t* signs, __half* out,
-                                                                     long long rows, int hq, int group) {
-  constexpr int D = 128, E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long v = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (v >= rows) return;
-  float y[E];
-  load_rotate<E>(q + v * D, signs + (size_t)((int)(v % hq) / group) * D, lane, y);
-  constexpr float c = 1.4426950408889634f / D;  // log2(e), 1 / sqrt(D) of the rotation and of the scores
-  const __half2 a = __floats2half2_rn(y[0] * c, y[1] * c), b = __floats2half2_rn(y[2] * c, y[3] * c);
-  reinterpret_cast<uint2*>(out + v * D)[lane] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-}
 
 // ------------------------------------------------------------------------ joining
 struct JoinParams {
@@ -110,6 +93,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
   __shared__ float s_acc[kRowWarps > 1 ? kRowWarps : 1][128];
   __shared__ float s_l[kRowWarps], s_m[kRowWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // every partial is complete
   const long long row = (long long)blockIdx.x * kRows + warp / kRowWarps;
   const int part = warp % kRowWarps;
   if (p.status && blockIdx.x == 0 && warp == 0) {
@@ -246,7 +230,7 @@ struct SharedPlan {
   Plan dec;
   bool sketch;
   // workspace: byte offsets
-  size_t dec_bytes, q, acc, ml, tables, lens, out32, total;
+  size_t dec_bytes, acc, ml, tables, lens, out32, total;
 };
 
 struct Call {
@@ -356,8 +340,6 @@ kvq_status make_shared_plan(const Call& c, const kvq_tier_view* all, bool q16, S
   }
   if (plan->num_blocks == 0) plan->total_splits = 0;
   if ((long long)plan->num_blocks * c0->num_kv_heads * plan->total_splits > 0x7FFFFFFFLL) return KVQ_ERR_UNSUPPORTED;
-  plan->q = at;
-  at += align_up(rows * d * 2, 256);
   plan->ml = at;
   at += align_up(2 * (size_t)plan->total_splits * rows * 8, 256);
   plan->acc = at;
@@ -501,8 +483,8 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
     t.num_splits = plan.splits[i];
     at += plan.splits[i];
   }
-  __half* qr = reinterpret_cast<__half*>(ws + plan.q);
-  p.q = qr;
+  p.q = reinterpret_cast<const __half*>(q);
+  p.k_signs = c0->k_signs;
   p.acc = reinterpret_cast<float*>(ws + plan.acc);
   p.ml = reinterpret_cast<float*>(ws + plan.ml);
   p.err = j.dec.err;
@@ -523,19 +505,22 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
   j.out = reinterpret_cast<__half*>(out);
   j.status = status;
   e = cudaMemsetAsync(counters, 0, 256, s);  // work counters and the error word
-  if (e == cudaSuccess && p.num_items > 0) {
-    rotate_queries_kernel<<<(unsigned)((rows + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(q, c0->k_signs, qr, rows,
-                                                                                          num_q_heads, group);
-    e = launched();
-    if (e == cudaSuccess) e = launch_shared_prefix(p, s);
-  }
+  if (e == cudaSuccess && p.num_items > 0) e = launch_shared_prefix(p, s);
   if (e == cudaSuccess && num_tiers > 0) e = launch_own(j.dec, plan.dec, d, group, counters, p.num_items > 0, s);
   if (e == cudaSuccess) {
-    if (2 * plan.total_splits + plan.dec.total > 24)
-      join_kernel<8><<<(unsigned)rows, 256, 0, s>>>(j);
-    else
-      join_kernel<1><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(j);
-    e = launched();
+    // eight warps a row where a row has many partials (one warp would wait for them in turn)
+    const bool many = 2 * plan.total_splits + plan.dec.total > 24;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(many ? rows : (rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = many ? cudaLaunchKernelEx(&cfg, join_kernel<8>, j) : cudaLaunchKernelEx(&cfg, join_kernel<1>, j);
+    if (e == cudaSuccess) e = launched();
   }
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }

@@ -24,7 +24,8 @@ struct SharedTier {
 struct SharedParams {
   SharedTier tier[KVQ_MAX_TIERS];
   int num_tiers, num_groups;
-  const __half* q;   // rotated queries [batch * hq][128], scaled to base-2 scores
+  const __half* q;        // queries [batch * hq][128]
+  const int8_t* k_signs;  // [hkv][128]
   float* acc;        // partials [2 * splits][batch * hq][128]
   float* ml;         // (max, sum) [2 * splits][batch * hq][2]
   int* err;

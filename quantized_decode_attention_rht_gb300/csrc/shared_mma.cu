@@ -12,7 +12,8 @@
 //   8 softmax warps (two groups of 128 threads, a thread per row): S from TMEM, P back to TMEM
 //   4 + 4 decoding warps: K and V tiles of 128 tokens, read from the packed cache into
 //     registers two tiles ahead, decoded to fp16 into shared memory (128-byte swizzle)
-//   1 warp: issues the products and allocates TMEM.
+//   1 warp: issues the products and allocates TMEM
+//   1 warp: looks up page numbers, rows, norms and scales, up to three tiles ahead.
 // Both products are tcgen05.mma of 128 x 128 x 16 steps: S = q~ K^T from shared memory, O += P V
 // with P read from TMEM (it overwrites S) and V as it lies (tokens x coordinates, the
 // MN-major form).  The two softmax groups alternate, so that one's products run while the
@@ -40,22 +41,25 @@ namespace {
 
 constexpr int kDim = 128;
 constexpr int kThreads = 640;
-// registers per thread after the split: launched with 96 x 640 = 61440 = 256 x 152 + 256 x 72 + 128 x 32
-constexpr int kSoftmaxRegs = 152, kDecodeRegs = 72, kIssueRegs = 32;
+// registers per thread after the split: launched with 96 x 640 = 61440 = 256 x 144 + 256 x 72 + 128 x 48
+constexpr int kSoftmaxRegs = 144, kDecodeRegs = 72, kIssueRegs = 48;
 constexpr int kTileBytes = kTileTokens * kDim * 2;  // 32 KB: two halves of 128 rows x 128 bytes
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kStages = 2;
-// Beside the operand tiles, per side: rows on their way (and a codebook's table), then the
-// row numbers of three tiles and the norms or scales of two.
+// Beside the operand tiles: codebook tables, then of kAhead tiles the rows and per side the
+// norms or scales.
 constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kStages * kTileBytes;
-constexpr int kOffRaw = kOffV + kStages * kTileBytes, kRawBytes = 24 << 10;
-constexpr int kOffRow = kOffRaw + kRawBytes, kRowBytes = 3 * kTileTokens * 4;   // per side
-constexpr int kOffAux = kOffRow + 2 * kRowBytes, kAuxBytes = 2 * kTileTokens * 8;  // per side
-constexpr int kOffCtl = kOffAux + 2 * kAuxBytes;
+constexpr int kOffLut = kOffV + kStages * kTileBytes, kLutBytes = 24 << 10;
+constexpr int kAhead = 4;
+constexpr int kOffRow = kOffLut + kLutBytes, kRowBytes = kTileTokens * 4;                       // a tile
+// (keys: a 4-byte norm a token; values: a norm, or four scales in 8 bytes)
+constexpr int kOffKAux = kOffRow + kAhead * kRowBytes, kOffVAux = kOffKAux + kAhead * kTileTokens * 4;
+constexpr int kOffCtl = kOffVAux + kAhead * kTileTokens * 8;
 constexpr int kSmem = kOffCtl + 256 + 1024;  // 1024: the base is aligned by hand
+static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 
 // barriers, in units of 8 bytes from kOffCtl
-enum { B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_QFULL = 8, B_SFULL = 10, B_PREADY = 12, B_OFULL = 14, B_COUNT = 16 };
+enum { B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_QFULL = 8, B_SFULL = 10, B_PREADY = 12, B_OFULL = 14, B_QRAW = 16, B_QROT = 17, B_ROWS = 18, B_ROWS_READ = 22, B_AUX = 26, B_COUNT = 30 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -221,47 +225,40 @@ enum { D_F16, D_F8, D_I4, D_CB4, D_CB3, D_CB2 };
 // passes' units are on their way at a time.
 __host__ __device__ constexpr int unit_bytes(int f) { return f == D_CB3 ? 12 : (f == D_CB2 ? 8 : 16); }
 __host__ __device__ constexpr int unit_passes(int f) { return f == D_F16 ? 16 : (f == D_F8 ? 8 : 4); }
-__host__ __device__ constexpr int unit_slots(int f) { return f == D_F8 ? 8 : (f == D_I4 ? 4 : 2); }
-// Copies of a codebook's pair table, one per lane (eight of the 1 KB of 4-bit pairs).
-__host__ __device__ constexpr int lut_copies(int f) { return f == D_CB4 ? 8 : 32; }
-constexpr int kLutBytes = 8 << 10;
 
 // What one side (K or V) of an item reads, and where its pieces of shared memory lie.
 struct Source {
   const uint8_t* rows;
-  const __half* aux;
+  int row_bytes;
+  uint32_t rowbuf, auxbuf;    // shared addresses: kAhead tiles of rows; of this side's norms or scales
+  uint32_t aux_shift;         // log2 of the latter's bytes a token
+  uint32_t lut, lut_stride;   // the lane's copy of entry 0, bytes between entries (codebooks)
+};
+// What the look-ups read.
+struct Pages {
   const int32_t* table;  // the group's block-table row
-  int row_bytes, num_pages, page_size, page_shift, hkv, hk;
+  int num_pages, page_size, page_shift, hkv, hk;
   int end;               // tokens of the prefix
-  uint32_t lut, raw, rowbuf, auxbuf;  // shared addresses
-  int side;              // 0 keys, 1 values (named barrier 1 + side)
 };
 struct Ring {
   uint32_t tiles, full, empty;  // shared addresses
+  uint32_t rows, aux, rows_read;  // the look-ups' barriers
+  uint32_t first_use;             // what the second stage waits for before its first tile, or 0
 };
 
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;  // a token that is not there: reads as zero
 
 // Page of token t (-1 past the end).
-__device__ __forceinline__ int page_of(const Source& s, int t) {
+__device__ __forceinline__ int page_of(const Pages& s, int t) {
   if (t >= s.end) return -1;
   return __ldg(s.table + (s.page_shift >= 0 ? t >> s.page_shift : t / s.page_size));
 }
 // Its row in the pool: kNoRow past the end, and for a page outside the pool (reported in bits).
-__device__ __forceinline__ uint32_t row_of(const Source& s, int t, int page, int* bits) {
+__device__ __forceinline__ uint32_t row_of(const Pages& s, int t, int page, int* bits) {
   if (t >= s.end || !page_in_pool(page, s.num_pages, bits)) return kNoRow;
   const uint32_t off = s.page_shift >= 0 ? t & (s.page_size - 1) : t % s.page_size;
   return ((uint32_t)page * s.hkv + s.hk) * s.page_size + off;  // below 2^32: the plan checks
 }
-// Its norm, or its four group scales.
-template <int F>
-__device__ __forceinline__ uint2 aux_of(const Source& s, uint32_t row) {
-  if (row == kNoRow) return make_uint2(0u, 0u);
-  if constexpr (F == D_I4) return __ldg(reinterpret_cast<const uint2*>(s.aux) + row);
-  else if constexpr (F >= D_CB4) return make_uint2(__half_as_ushort(__ldg(s.aux + row)), 0u);
-  else return make_uint2(0u, 0u);
-}
-
 // Token (row of the tile) and unit of a thread in pass p.  A quarter-warp holds eight tokens
 // and one unit, so that its 16-byte stores meet eight different banks of the swizzled tile; a
 // warp reads 64 neighbouring bytes of each row.
@@ -292,47 +289,108 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// The side's 128 threads meet; true if all of them are well (so that they leave together).
-__device__ __forceinline__ bool side_sync(const Source& s, bool well) {
-  uint32_t all;
-  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbarrier.cta.red.and.pred q, %2, 128, p;\nselp.u32 %0, 1, 0, q;\n}"
-               : "=r"(all)
-               : "r"((uint32_t)well), "r"(1 + s.side)
-               : "memory");
-  return all != 0;
-}
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// The thread's unit of pass p towards its slot.
-template <int F>
-__device__ __forceinline__ void request(const Source& s, uint32_t rowbuf, int p, int tid) {
-  int t, u;
-  place<F>(p, tid, t, u);
-  const uint32_t row = lds32(rowbuf + 4u * t);
-  const bool there = row != kNoRow;
-  const uint8_t* src = s.rows + (size_t)(there ? row : 0) * s.row_bytes + u * unit_bytes(F);
-  const uint32_t dst = s.raw + ((p % unit_slots(F)) * 128 + tid) * unit_bytes(F);
-  if constexpr (unit_bytes(F) == 12) {
+// The look-up warp: rows of every tile's tokens, then (a tile later, when their loads have
+// arrived) their norms (codebooks) or group scales (INT4 values); page numbers are read a tile
+// before their rows are formed.
+__device__ __forceinline__ void look_up(const Pages& s, const __half* k_norm, const __half* v_norm,
+                                        const __half* v_scale, uint32_t smem, uint32_t bars, int tile0, int n,
+                                        volatile int* abort, int* err) {
+  const int lane = threadIdx.x & 31;
+  int bits = 0;
+  int page[4];
+  uint2 aux[4];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) copy_async<4>(dst + 4 * k, src + 4 * k, there);
+  for (int j = 0; j < 4; ++j) page[j] = page_of(s, tile0 * kTileTokens + lane + 32 * j);
+  for (int i = 0; i <= n; ++i) {
+    const int at = i % kAhead;
+    uint32_t row[4];
+    if (i < n) {
+      if (i >= kAhead && !bar_wait(bars + 8 * (B_ROWS_READ + at), ((i / kAhead) & 1) ^ 1, abort, err)) break;
+      const int t0 = (tile0 + i) * kTileTokens + lane;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        row[j] = row_of(s, t0 + 32 * j, page[j], &bits);
+        sts32(smem + kOffRow + at * kRowBytes + 4 * (lane + 32 * j), row[j]);
+      }
+      bar_arrive(bars + 8 * (B_ROWS + at));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) page[j] = page_of(s, t0 + kTileTokens + 32 * j);
+    }
+    if (!k_norm && !v_scale) continue;
+    if (i > 0) {
+      const int before = (i - 1) % kAhead;
+      const uint32_t ka = smem + kOffKAux + before * kTileTokens * 4 + 4 * lane;
+      const uint32_t va = smem + kOffVAux + before * kTileTokens * 8 + 8 * lane;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (k_norm) {
+          sts32(ka + 128 * j, aux[j].x);
+          sts32(va + 256 * j, aux[j].y);
+        } else {
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(va + 256 * j), "r"(aux[j].x), "r"(aux[j].y) : "memory");
+        }
+      }
+      bar_arrive(bars + 8 * (B_AUX + before));
+    }
+    if (i < n) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        aux[j] = make_uint2(0u, 0u);
+        if (row[j] == kNoRow) continue;
+        if (k_norm) {
+          aux[j].x = __half_as_ushort(__ldg(k_norm + row[j]));
+          aux[j].y = __half_as_ushort(__ldg(v_norm + row[j]));
+        } else {
+          aux[j] = __ldg(reinterpret_cast<const uint2*>(v_scale) + row[j]);
+        }
+      }
+    }
+  }
+  if (bits) atomicOr(err, bits);
+}
+
+// A unit of the row, into registers.
+template <int F>
+__device__ __forceinline__ void request(const Source& s, uint32_t row, int u, uint32_t (&w)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = 0u;
+  if (row == kNoRow) return;
+  const uint8_t* src = s.rows + (size_t)row * s.row_bytes + u * unit_bytes(F);
+  if constexpr (unit_bytes(F) == 16) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+    w[0] = x.x;
+    w[1] = x.y;
+    w[2] = x.z;
+    w[3] = x.w;
+  } else if constexpr (unit_bytes(F) == 8) {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+    w[0] = x.x;
+    w[1] = x.y;
   } else {
-    copy_async<unit_bytes(F)>(dst, src, there);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) w[k] = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
   }
 }
 
-// The unit in its slot, decoded to fp16, into its row of the tile.
+// A table entry (not volatile: the table does not change, so look-ups may move).
+__device__ __forceinline__ uint32_t look_pair(uint32_t addr) {
+  uint32_t v;
+  asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+// A unit decoded to fp16, into row t of the tile.
 template <int F>
-__device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, uint32_t auxbuf, int p, int tid) {
-  int t, u;
-  place<F>(p, tid, t, u);
-  const uint32_t slot = s.raw + ((p % unit_slots(F)) * 128 + tid) * unit_bytes(F);
+__device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, int t, int u, uint32_t half_scale,
+                                            const uint32_t (&w)[4]) {
   const uint32_t row = tile + t * 128;
   const int x = t & 7;
   if constexpr (F == D_F8) {  // 16 values: two chunks
-    uint32_t w[4], h[8];
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(slot));
+    uint32_t h[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[k]) : "h"((uint16_t)(w[k / 2] >> (16 * (k & 1)))));
@@ -342,144 +400,129 @@ __device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, uint
     sts16(at + (((c + 1) ^ x) << 4), h[4], h[5], h[6], h[7]);
   } else {  // 32 values: four chunks of 8
     constexpr int B = F == D_I4 || F == D_CB4 ? 4 : (F == D_CB3 ? 3 : 2);
-    uint32_t c[4];
+    uint32_t c[4], h[16];
     if constexpr (B == 4) {
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3]) : "r"(slot));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[k] = w[k];
     } else if constexpr (B == 3) {
-      const uint32_t w0 = lds32(slot), w1 = lds32(slot + 4), w2 = lds32(slot + 8);
-      c[0] = w0;
-      c[1] = __funnelshift_r(w0, w1, 24);
-      c[2] = __funnelshift_r(w1, w2, 16);
-      c[3] = w2 >> 8;
+      c[0] = w[0];
+      c[1] = __funnelshift_r(w[0], w[1], 24);
+      c[2] = __funnelshift_r(w[1], w[2], 16);
+      c[3] = w[2] >> 8;
     } else {
-      const uint32_t w0 = lds32(slot), w1 = lds32(slot + 4);
-      c[0] = w0;
-      c[1] = w0 >> 16;
-      c[2] = w1;
-      c[3] = w1 >> 16;
+      c[0] = w[0];
+      c[1] = w[0] >> 16;
+      c[2] = w[1];
+      c[3] = w[1] >> 16;
     }
-    uint16_t half_scale;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(half_scale) : "r"(auxbuf + 8u * t + (F == D_I4 ? 2u * u : 0u)));
     const uint32_t scale = half_scale * 0x10001u;
-    const uint32_t at = row + (u >> 1) * kHalfBytes;
-    const uint32_t base = s.lut + 4u * (tid & (lut_copies(F) - 1));
+    if constexpr (F == D_I4) {
+      // Levels n - 8 of nibbles (k, k + 4), exact in fp16: 1024 + n less 1032, or (from the
+      // upper nibble of a byte) (1024 + 16 n) / 16 less 72; times the scale, rounded once.  The
+      // pairs leave a chunk's coordinates in the order 0 4 1 5 2 6 3 7, and so the accumulator's
+      // columns (undone where it is stored).
+      const __half2 a = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));  // 1032
+      const __half2 b = __halves2half2(__ushort_as_half(0x2C00), __ushort_as_half(0x2C00));  // 1 / 16
+      const __half2 d = __halves2half2(__ushort_as_half(0xD480), __ushort_as_half(0xD480));  // -72
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t h[4];
-      if constexpr (F == D_I4) {
-        // Levels n - 8 of nibbles (k, k + 4), exact in fp16: 1024 + n less 1032, or (from the
-        // upper nibble of a byte) (1024 + 16 n) / 16 less 72; times the scale, rounded once.  The
-        // pairs leave a chunk's coordinates in the order 0 4 1 5 2 6 3 7, and so the accumulator's
-        // columns (undone where it is stored).
-        const __half2 a = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));  // 1032
-        const __half2 b = __halves2half2(__ushort_as_half(0x2C00), __ushort_as_half(0x2C00));  // 1 / 16
-        const __half2 d = __halves2half2(__ushort_as_half(0xD480), __ushort_as_half(0xD480));  // -72
-        const uint32_t w = c[i], w8 = c[i] >> 8;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t lo = ((k ? w8 : w) & 0x000F000Fu) | 0x64006400u, hi = ((k ? w8 : w) & 0x00F000F0u) | 0x64006400u;
-          const __half2 nl = __hsub2(*reinterpret_cast<const __half2*>(&lo), a);
-          const __half2 nh = __hfma2(*reinterpret_cast<const __half2*>(&hi), b, d);
-          h[2 * k] = hmul2(*reinterpret_cast<const uint32_t*>(&nl), scale);
-          h[2 * k + 1] = hmul2(*reinterpret_cast<const uint32_t*>(&nh), scale);
-        }
-      } else {
-        // pairs of codes through the block's table of centroid pairs / sqrt(D)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t e = (c[i] >> (2 * B * k)) & ((1u << (2 * B)) - 1u);
-          h[k] = hmul2(lds32(base + e * (4u * lut_copies(F))), scale);
-        }
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t v = i & 1 ? c[i / 2] >> 8 : c[i / 2];
+        const uint32_t lo = (v & 0x000F000Fu) | 0x64006400u, hi = (v & 0x00F000F0u) | 0x64006400u;
+        const __half2 nl = __hsub2(*reinterpret_cast<const __half2*>(&lo), a);
+        const __half2 nh = __hfma2(*reinterpret_cast<const __half2*>(&hi), b, d);
+        h[2 * i] = *reinterpret_cast<const uint32_t*>(&nl);
+        h[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&nh);
       }
-      sts16(at + (((4 * (u & 1) + i) ^ x) << 4), h[0], h[1], h[2], h[3]);
+    } else {
+      // pairs of codes through the block's table of centroid pairs / sqrt(D)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t e = (c[i / 4] >> (2 * B * (i % 4))) & ((1u << (2 * B)) - 1u);
+        h[i] = look_pair(s.lut + e * s.lut_stride);
+      }
     }
+    const uint32_t at = row + (u >> 1) * kHalfBytes;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sts16(at + (((4 * (u & 1) + i) ^ x) << 4), hmul2(h[4 * i], scale), hmul2(h[4 * i + 1], scale),
+            hmul2(h[4 * i + 2], scale), hmul2(h[4 * i + 3], scale));
   }
 }
 
-// Tiles [tile0, tile1) of one side, into the ring.  Rows travel by asynchronous copies into
-// slots that belong to the thread that decodes them (nobody else waits for them), a slot being
-// requested anew as soon as it is decoded.  Page numbers, rows, norms and scales are looked up
-// by one thread a token, a tile ahead.  The loops stay rolled: eight warps of four kinds share
-// the instruction caches of a scheduler, and unrolled passes spent more time fetching
-// instructions than running them.
+// The side's n tiles, into the ring.  A thread's units of a tile travel in registers, each slot
+// requested anew as soon as it is decoded, so that a load has a tile's time to arrive.  What a
+// pass needs from shared memory (rows, scales) is read for all of them first: a warp has its
+// scheduler's slots to itself only now and then, and a chain of look-ups in every pass took
+// five times as long as the instructions.
 template <int F>
-__device__ __forceinline__ void produce(const Source& s, const Ring& ring, int tile0, int tile1, int tid,
-                                        volatile int* abort, int* err) {
-  constexpr int kPasses = unit_passes(F), kSlots = unit_slots(F);
-  int bits = 0;
-  int t = tile0 * kTileTokens + tid;  // the token this thread looks up
-  uint32_t row = row_of(s, t, page_of(s, t), &bits);
-  sts32(s.rowbuf + 4u * tid, row);
-  uint2 aux = aux_of<F>(s, row);
-  t += kTileTokens;
-  int page = page_of(s, t);
-  bool ok = side_sync(s, true);
-#pragma unroll 1
-  for (int p = 0; p < kSlots; ++p) {
-    request<F>(s, s.rowbuf, p, tid);
-    copy_commit();
+__device__ __forceinline__ void produce(const Source& s, const Ring& ring, int n, int tid, volatile int* abort,
+                                        int* err) {
+  constexpr int kPasses = unit_passes(F);
+  uint32_t x[kPasses][4];
+  if (!bar_wait(ring.rows, 0, abort, err)) return;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    int t, u;
+    place<F>(p, tid, t, u);
+    request<F>(s, lds32(s.rowbuf + 4u * t), u, x[p]);
   }
-  uint32_t now = s.rowbuf, next = s.rowbuf + 4u * kTileTokens;
-  const int n = tile1 - tile0;
   for (int i = 0; i < n; ++i) {
-    const int st = i & 1;
-    const uint32_t auxbuf = s.auxbuf + st * (8u * kTileTokens);
-    if constexpr (F >= D_I4)
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(auxbuf + 8u * tid), "r"(aux.x), "r"(aux.y) : "memory");
-    row = row_of(s, t, page, &bits);
-    sts32(next + 4u * tid, row);
-    aux = aux_of<F>(s, row);
-    t += kTileTokens;
-    page = page_of(s, t);
-    if (!side_sync(s, ok)) break;
-    if (i >= kStages && !(ok = bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err))) continue;
-#pragma unroll 1
+    const int st = i & 1, at = i % kAhead, after = (i + 1) % kAhead;
+    const bool more = i + 1 < n;
+    uint32_t row[kPasses], scale[kPasses];
+    if (more && !bar_wait(ring.rows + 8 * after, ((i + 1) / kAhead) & 1, abort, err)) return;
+    if (F >= D_I4 && !bar_wait(ring.aux + 8 * at, (i / kAhead) & 1, abort, err)) return;
+#pragma unroll
     for (int p = 0; p < kPasses; ++p) {
-      copy_wait<kSlots - 1>();
-      decode_unit<F>(s, ring.tiles + st * kTileBytes, auxbuf, p, tid);
-      const int q = p + kSlots;
-      if (q < kPasses) request<F>(s, now, q, tid);
-      else if (i + 1 < n) request<F>(s, next, q - kPasses, tid);
-      copy_commit();
+      int t, u;
+      place<F>(p, tid, t, u);
+      row[p] = more ? lds32(s.rowbuf + after * kRowBytes + 4u * t) : kNoRow;
+      scale[p] = 0;
+      if constexpr (F >= D_I4) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=h"(v)
+                     : "r"(s.auxbuf + (((uint32_t)(at * kTileTokens + t)) << s.aux_shift) + (F == D_I4 ? 2u * u : 0u)));
+        scale[p] = v;
+      }
     }
-    now = next;
-    next = next == s.rowbuf + 8u * kTileTokens ? s.rowbuf : next + 4u * kTileTokens;
+    if (i >= kStages && !bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err)) return;
+    if (i == 1 && ring.first_use && !bar_wait(ring.first_use, 0, abort, err)) return;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      int t, u;
+      place<F>(p, tid, t, u);
+      decode_unit<F>(s, ring.tiles + st * kTileBytes, t, u, scale[p], x[p]);
+      request<F>(s, row[p], u, x[p]);
+    }
     fence_async_smem();
     bar_arrive(ring.full + 8 * st);
+    bar_arrive(ring.rows_read + 8 * at);
   }
-  copy_wait<0>();
-  if (bits) atomicOr(err, bits);
 }
 
 // fp16 rows need no decoding: copies straight into the tile, a tile signalled once the next
 // one's copies are under way.
 template <>
-__device__ __forceinline__ void produce<D_F16>(const Source& s, const Ring& ring, int tile0, int tile1, int tid,
-                                               volatile int* abort, int* err) {
-  int bits = 0;
-  int t = tile0 * kTileTokens + tid;
-  int page = page_of(s, t);
+__device__ __forceinline__ void produce<D_F16>(const Source& s, const Ring& ring, int n, int tid, volatile int* abort,
+                                               int* err) {
   bool ok = true;
-  const int n = tile1 - tile0;
-  uint32_t now = s.rowbuf;
   for (int i = 0; i < n; ++i) {
-    const int st = i & 1;
-    sts32(now + 4u * tid, row_of(s, t, page, &bits));
-    t += kTileTokens;
-    page = page_of(s, t);
-    if (!side_sync(s, ok)) break;
-    if (i >= kStages && !(ok = bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err))) continue;
+    const int st = i & 1, at = i % kAhead;
+    if (!(ok = bar_wait(ring.rows + 8 * at, (i / kAhead) & 1, abort, err))) break;
+    if (i >= kStages && !(ok = bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err))) break;
+    if (i == 1 && ring.first_use && !(ok = bar_wait(ring.first_use, 0, abort, err))) break;
 #pragma unroll 2
     for (int p = 0; p < unit_passes(D_F16); ++p) {
       int r, u;
       place<D_F16>(p, tid, r, u);
-      const uint32_t row = lds32(now + 4u * r);
+      const uint32_t row = lds32(s.rowbuf + at * kRowBytes + 4u * r);
       const bool there = row != kNoRow;
       copy_async<16>(ring.tiles + st * kTileBytes + (u >> 3) * kHalfBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4),
                      s.rows + (size_t)(there ? row : 0) * s.row_bytes + u * 16, there);
     }
     copy_commit();
-    now = now == s.rowbuf + 8u * kTileTokens ? s.rowbuf : now + 4u * kTileTokens;
+    bar_arrive(ring.rows_read + 8 * at);
     if (i > 0) {
       copy_wait<1>();
       fence_async_smem();
@@ -491,18 +534,17 @@ __device__ __forceinline__ void produce<D_F16>(const Source& s, const Ring& ring
     fence_async_smem();
     bar_arrive(ring.full + 8 * ((n - 1) & 1));
   }
-  if (bits) atomicOr(err, bits);
 }
 
-__device__ __forceinline__ void produce_any(int f, const Source& s, const Ring& ring, int tile0, int tile1, int tid,
-                                            volatile int* abort, int* err) {
+__device__ __forceinline__ void produce_any(int f, const Source& s, const Ring& ring, int n, int tid, volatile int* abort,
+                                            int* err) {
   switch (f) {
-    case D_F16: produce<D_F16>(s, ring, tile0, tile1, tid, abort, err); break;
-    case D_F8: produce<D_F8>(s, ring, tile0, tile1, tid, abort, err); break;
-    case D_I4: produce<D_I4>(s, ring, tile0, tile1, tid, abort, err); break;
-    case D_CB4: produce<D_CB4>(s, ring, tile0, tile1, tid, abort, err); break;
-    case D_CB3: produce<D_CB3>(s, ring, tile0, tile1, tid, abort, err); break;
-    default: produce<D_CB2>(s, ring, tile0, tile1, tid, abort, err); break;
+    case D_F16: produce<D_F16>(s, ring, n, tid, abort, err); break;
+    case D_F8: produce<D_F8>(s, ring, n, tid, abort, err); break;
+    case D_I4: produce<D_I4>(s, ring, n, tid, abort, err); break;
+    case D_CB4: produce<D_CB4>(s, ring, n, tid, abort, err); break;
+    case D_CB3: produce<D_CB3>(s, ring, n, tid, abort, err); break;
+    default: produce<D_CB2>(s, ring, n, tid, abort, err); break;
   }
 }
 
@@ -515,13 +557,45 @@ __device__ __forceinline__ int decode_kind(int fmt, int bits) {
   }
 }
 
-// Pairs of centroids / sqrt(D) in fp16: entry e = codes (e mod 2^b, e / 2^b).  tid: 256 threads.
-__device__ __forceinline__ void build_lut(uint32_t lut, const float* cent, int bits, int tid) {
-  const int copies = lut_copies(bits == 4 ? D_CB4 : D_CB3);
+// Pairs of centroids / sqrt(D) in fp16: entry e = codes (e mod 2^b, e / 2^b), one copy per lane
+// where there is room (a warp's look-ups then never meet in a bank), else 16 or 8 of them (two
+// or three bank rounds a look-up).  tid: 256 threads.
+__device__ __forceinline__ void build_lut(uint32_t lut, int copies, const float* cent, int bits, int tid) {
   if (tid >= (1 << (2 * bits))) return;
   const float inv = inv_sqrt_dim(kDim);
   const uint32_t v = half2_bits(__ldg(cent + (tid & ((1 << bits) - 1))) * inv, __ldg(cent + (tid >> bits)) * inv);
   for (int i = 0; i < copies; i += 4) sts16(lut + 4u * (tid * copies + i), v, v, v, v);
+}
+
+// Where the two tables lie.  With up to 128 rows the second query tile is free: 32 KB more.
+struct Tables {
+  uint32_t at[2];
+  int copies[2];
+};
+__device__ __forceinline__ Tables place_tables(uint32_t smem, int k_bits, int v_bits, bool same, bool both) {
+  const uint32_t lut = smem + kOffLut, spare = smem + kOffQ + kTileBytes;
+  Tables t;
+  t.at[0] = lut;
+  t.at[1] = lut + kLutBytes / 2;
+  t.copies[0] = k_bits == 4 ? 8 : 32;  // 2^(2 bits) entries: 8 KB
+  t.copies[1] = v_bits == 4 ? 8 : 32;
+  if (k_bits == 4 && v_bits == 4 && same) {
+    t.at[0] = t.at[1] = both ? spare : lut;
+    t.copies[0] = t.copies[1] = both ? 32 : 16;
+  } else if (both) {
+    if (k_bits == 4) {
+      t.at[0] = spare;
+      t.copies[0] = 32;
+      if (v_bits == 4) {
+        t.at[1] = lut;
+        t.copies[1] = 16;
+      }
+    } else if (v_bits == 4) {
+      t.at[1] = spare;
+      t.copies[1] = 32;
+    }
+  }
+  return t;
 }
 
 // ------------------------------------------------------------------------ softmax
@@ -625,6 +699,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       bar_init(bars + 8 * (B_PREADY + i), max(1, (live + 31) / 32 * 32));  // the warps that hold rows
       bar_init(bars + 8 * (B_OFULL + i), 1);
     }
+    bar_init(bars + 8 * B_QRAW, 256);
+    bar_init(bars + 8 * B_QROT, 1);
+    for (int i = 0; i < kAhead; ++i) {
+      bar_init(bars + 8 * (B_ROWS + i), 32);
+      bar_init(bars + 8 * (B_AUX + i), 32);
+      bar_init(bars + 8 * (B_ROWS_READ + i), 256);
+    }
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -632,9 +713,16 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (T.k_fmt == KVQ_FMT_CODEBOOK && warp < 8) build_lut(smem + kOffRaw, T.k_cent, T.k_bits, threadIdx.x);
-  if (T.v_fmt == KVQ_FMT_CODEBOOK && warp >= 8 && warp < 16)
-    build_lut(smem + kOffRaw + kRawBytes / 2, T.v_cent, T.v_bits, threadIdx.x - 256);
+  Tables tables;
+  if (T.k_fmt == KVQ_FMT_CODEBOOK && warp < 16) {
+    const int lane = threadIdx.x & 31;
+    bool same = T.k_bits == T.v_bits;  // the same table for keys and values (often so)
+    if (same) same = lane >= (1 << T.k_bits) || __ldg(T.k_cent + lane) == __ldg(T.v_cent + lane);
+    same = __all_sync(0xFFFFFFFFu, same);
+    tables = place_tables(smem, T.k_bits, T.v_bits, same, both);
+    if (warp < 8) build_lut(tables.at[0], tables.copies[0], T.k_cent, T.k_bits, threadIdx.x);
+    else if (tables.at[1] != tables.at[0]) build_lut(tables.at[1], tables.copies[1], T.v_cent, T.v_bits, threadIdx.x - 256);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -646,23 +734,79 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   if (warp < 8) {
     // ---- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const uint32_t q_tile = smem + kOffQ + w * kTileBytes;
+    // The block's queries: H s q as one more product, of the queries as they come (fp16, exact)
+    // and the matrix of elements s_k (-1)^popc(n & k) (exact too), in float32; then, from TMEM,
+    // times log2(e) / D (1 / sqrt(D) of the rotation and of the scores, which are then in base-2
+    // units), rounded to fp16 into the query tiles.  (Butterflies by shuffles took 15 us for
+    // 256 rows.)
+    bool ok = true;
     {
-      // the group's queries into shared memory, 16 lanes a row
-      const int tid = threadIdx.x & 127;
-      for (int i = tid; i < kTileRows * 16; i += 128) {
-        const int row = i >> 4, c = i & 15;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        const int rr = (both ? 0 : w * kTileRows) + row;
-        if (rr < rows) {
-          const int gr = lb * kItemRows + rr, sq = gr / p.group;
-          const size_t orow = (size_t)(p.offset[g] + sq) * p.hq + hk * p.group + (gr - sq * p.group);
-          x = __ldg(reinterpret_cast<const uint4*>(p.q + orow * kDim) + c);
+      const int tid = threadIdx.x & 255;
+      const int shift = __ffs(p.group) - 1;
+      for (int first = 0; first < (both ? kTileRows : kItemRows); first += 128) {
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = first + i * 16 + (tid >> 4);
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (row < rows) {
+            const int gr = lb * kItemRows + row, sq = gr >> shift;
+            const size_t orow = (size_t)(p.offset[g] + sq) * p.hq + hk * p.group + (gr - (sq << shift));
+            v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + orow * kDim) + (tid & 15));
+          }
         }
-        sts16(q_tile + (c >> 3) * kHalfBytes + row * 128 + (((c & 7) ^ (row & 7)) << 4), x.x, x.y, x.z, x.w);
+        const uint32_t to = smem + kOffQ + (first >> 7) * kTileBytes + ((tid & 15) >> 3) * kHalfBytes;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 16 + (tid >> 4);
+          sts16(to + r * 128 + (((tid & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+        }
+      }
+      const int c = tid & 15;  // elements 8c .. 8c + 7 of rows n
+      const uint2 sg = __ldg(reinterpret_cast<const uint2*>(p.k_signs + (size_t)hk * kDim) + c);
+      const uint32_t to = smem + kOffV + kTileBytes + (c >> 3) * kHalfBytes;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int n7 = (tid >> 4) & 7, nr = i * 16 + (tid >> 4);
+        const bool flip = __popc((nr >> 3) & c) & 1;  // the chunk's part of the parity
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t s0 = (k < 2 ? sg.x >> (16 * k) : sg.y >> (16 * (k - 2)));  // sign bytes 2k, 2k + 1
+          const uint32_t lo = ((s0 >> 7) ^ __popc(n7 & (2 * k)) ^ (uint32_t)flip) & 1u;
+          const uint32_t hi = ((s0 >> 15) ^ __popc(n7 & (2 * k + 1)) ^ (uint32_t)flip) & 1u;
+          h[k] = 0x3C003C00u | (lo << 15) | (hi << 31);
+        }
+        sts16(to + nr * 128 + (((c & 7) ^ (nr & 7)) << 4), h[0], h[1], h[2], h[3]);
       }
       fence_async_smem();
-      bar_arrive(bars + 8 * (B_QFULL + w));
+      bar_arrive(bars + 8 * B_QRAW);
+      if (!(both && w)) {
+        ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * B_QROT, 0, abort, p.err));
+        tc_fence_after();
+        const int r = threadIdx.x & 127;
+        const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + w * 128;
+        const uint32_t to = smem + kOffQ + w * kTileBytes + r * 128;
+        constexpr float scale = 1.4426950408889634f / kDim;
+#pragma unroll
+        for (int part = 0; part < 4; ++part) {
+          uint32_t v[32];
+          tc_ld32(from + 32 * part, v);
+          tc_wait_ld(v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              h[k] = half2_bits(__uint_as_float(v[8 * i + 2 * k]) * scale, __uint_as_float(v[8 * i + 2 * k + 1]) * scale);
+            const int at = 4 * part + i;
+            sts16(to + (at >> 3) * kHalfBytes + (((at & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+          }
+        }
+        tc_fence_before();
+        fence_async_smem();
+        bar_arrive(bars + 8 * (B_QFULL + w));
+      }
     }
     const int my_jobs = jobs > w ? (jobs - w + 1) / 2 : 0;
     const bool live = (warp & 3) * 32 < rows_of_group;  // the warp holds rows
@@ -671,8 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       const uint32_t s_at = lane_base + w * 128, o_at = lane_base + 256 + w * 128;
       float m = -INFINITY;
       unsigned long long l2 = 0;  // the row's sum, even and odd columns
-      bool ok = true;
-      for (int k = 0; k < my_jobs; ++k) {
+      for (int k = 0; k < my_jobs && ok; ++k) {
         const int i = 2 * k + w, tile = tile0 + (both ? i : i >> 1);
         const int valid = min(kTileTokens, len - tile * kTileTokens);
         if (!(ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * (B_SFULL + w), k & 1, abort, p.err)))) break;
@@ -748,28 +891,43 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       }
       if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * (B_OFULL + w), (my_jobs - 1) & 1, abort, p.err));
       tc_fence_after();
+      // The accumulator leaves through shared memory, 16 KB a warp, so that rows are written
+      // whole: the tiles are free (the group that ends first has the key stages, whose products
+      // precede its last one, the other the value stages).
       if (ok) {
+        const bool last = ((jobs - 1) & 1) == w;
+        const int lane = threadIdx.x & 31;
+        const uint32_t stage = smem + (last ? kOffV : kOffK) + (warp & 3) * (32 * kDim * 4);
+        const bool int4 = T.v_fmt == KVQ_FMT_INT4_G32;  // columns 0 4 1 5 2 6 3 7 of every eight
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tc_ld32(o_at + 32 * c, v);
           tc_wait_ld(v);
-          if (out_row >= 0) {
-            float* dst = p.acc + (part + out_row) * kDim + 32 * c;
-            const bool int4 = T.v_fmt == KVQ_FMT_INT4_G32;  // columns 0 4 1 5 2 6 3 7 of every eight
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              const uint32_t o1 = int4 ? v[e + 2] : v[e + 1], o2 = int4 ? v[e + 4] : v[e + 2];
-              const uint32_t o3 = int4 ? v[e + 6] : v[e + 3], o4 = int4 ? v[e + 1] : v[e + 4];
-              const uint32_t o5 = int4 ? v[e + 3] : v[e + 5], o6 = int4 ? v[e + 5] : v[e + 6];
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + e), "r"(v[e]), "r"(o1),
-                           "r"(o2), "r"(o3), "r"(o4), "r"(o5), "r"(o6), "r"(v[e + 7])
-                           : "memory");
-            }
+          for (int e = 0; e < 32; e += 8) {
+            const uint32_t o1 = int4 ? v[e + 2] : v[e + 1], o2 = int4 ? v[e + 4] : v[e + 2];
+            const uint32_t o3 = int4 ? v[e + 6] : v[e + 3], o4 = int4 ? v[e + 1] : v[e + 4];
+            const uint32_t o5 = int4 ? v[e + 3] : v[e + 5], o6 = int4 ? v[e + 5] : v[e + 6];
+            const int at = 8 * c + e / 4;  // 16-byte chunk of the lane's row
+            sts16(stage + lane * (kDim * 4) + ((at ^ (lane & 7)) << 4), v[e], o1, o2, o3);
+            sts16(stage + lane * (kDim * 4) + (((at + 1) ^ (lane & 7)) << 4), o4, o5, o6, v[e + 7]);
           }
         }
+        __syncwarp();
+        float* base = p.acc + part * kDim;
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+          const long long to = __shfl_sync(0xFFFFFFFFu, out_row, i);
+          float4 x;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                       : "r"(stage + i * (kDim * 4) + ((lane ^ (i & 7)) << 4)));
+          if (to >= 0) reinterpret_cast<float4*>(base + to * kDim)[lane] = x;
+        }
       }
-      if (out_row >= 0) *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) =
+      if (out_row >= 0)
+        *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) =
             ok ? make_float2(m, unpack2(l2).x + unpack2(l2).y) : make_float2(-INFINITY, 0.f);
     } else if (out_row >= 0) {  // a second group without a tile of its own
       *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) = make_float2(-INFINITY, 0.f);
@@ -780,27 +938,24 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     const bool keys = warp < 12;
     Source s;
     s.rows = keys ? T.k_rows : T.v_rows;
-    s.aux = keys ? T.k_aux : T.v_aux;
-    s.table = T.block_table + (size_t)g * T.max_pages;
     s.row_bytes = keys ? T.k_row_bytes : T.v_row_bytes;
-    s.num_pages = T.num_pages;
-    s.page_size = p.page_size;
-    s.page_shift = p.page_shift;
-    s.hkv = p.hkv;
-    s.hk = hk;
-    s.end = len;
-    // codebooks: half of the area a side, the table first; otherwise 16 KB of keys, 8 of values
-    const bool codes = T.k_fmt == KVQ_FMT_CODEBOOK;
-    s.lut = smem + kOffRaw + (keys ? 0 : kRawBytes / 2);
-    s.raw = codes ? s.lut + kLutBytes : smem + kOffRaw + (keys ? 0 : 16 << 10);
-    s.rowbuf = smem + kOffRow + (keys ? 0 : kRowBytes);
-    s.auxbuf = smem + kOffAux + (keys ? 0 : kAuxBytes);
-    s.side = keys ? 0 : 1;
+    if (T.k_fmt == KVQ_FMT_CODEBOOK) {
+      const int side = keys ? 0 : 1;
+      s.lut = tables.at[side] + 4u * (threadIdx.x & (tables.copies[side] - 1));
+      s.lut_stride = 4u * tables.copies[side];
+    }
+    s.rowbuf = smem + kOffRow;
+    s.auxbuf = smem + (keys ? kOffKAux : kOffVAux);
+    s.aux_shift = keys ? 2 : 3;
     Ring ring;
     ring.tiles = smem + (keys ? kOffK : kOffV);
     ring.full = bars + 8 * (keys ? B_KFULL : B_VFULL);
     ring.empty = bars + 8 * (keys ? B_KEMPTY : B_VEMPTY);
-    produce_any(keys ? decode_kind(T.k_fmt, T.k_bits) : decode_kind(T.v_fmt, T.v_bits), s, ring, tile0, tile1,
+    ring.rows = bars + 8 * B_ROWS;
+    ring.aux = bars + 8 * B_AUX;
+    ring.rows_read = bars + 8 * B_ROWS_READ;
+    ring.first_use = keys ? 0 : bars + 8 * B_QROT;  // the second value stage first holds the rotation
+    produce_any(keys ? decode_kind(T.k_fmt, T.k_bits) : decode_kind(T.v_fmt, T.v_bits), s, ring, n,
                 threadIdx.x & 127, abort, p.err);
   } else {
     // ---- products
@@ -819,7 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         const int tile = both ? i : i >> 1, st = tile & 1, ws = i & 1;
         if (!well(bars + 8 * (B_KFULL + st), (tile >> 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t a = qd + ws * (kTileBytes >> 4), b = kd + st * (kTileBytes >> 4);
+        const uint64_t a = qd + (both ? 0 : ws) * (kTileBytes >> 4), b = kd + st * (kTileBytes >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kDim / 16; ++kk) {
@@ -832,8 +987,23 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         __syncwarp();
         return true;
       };
-      bool ok = true;
-      for (int i = 0; i < 2 && i < jobs && ok; ++i) ok = well(bars + 8 * (B_QFULL + i), 0) && scores(i);
+      bool ok = well(bars + 8 * B_QRAW, 0);
+      if (ok) {  // the rotated queries, into the score columns
+        tc_fence_after();
+        const uint64_t rd = desc_at(desc_base(16, 1024), smem + kOffV + kTileBytes);
+        if (elect_one()) {
+          for (int ws = 0; ws < (both ? 1 : 2); ++ws) {
+#pragma unroll
+            for (int kk = 0; kk < kDim / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+              mma_ss(tm + ws * 128, qd + ws * (kTileBytes >> 4) + off, rd + off, kIdescQK, kk > 0);
+            }
+          }
+          tc_commit(bars + 8 * B_QROT);
+        }
+        __syncwarp();
+      }
+      for (int i = 0; i < 2 && i < jobs && ok; ++i) ok = well(bars + 8 * (B_QFULL + (both ? 0 : i)), 0) && scores(i);
       for (int i = 0; i < jobs && ok; ++i) {
         const int tile = both ? i : i >> 1, st = tile & 1, ws = i & 1;
         ok = well(bars + 8 * (B_VFULL + st), (tile >> 1) & 1) && well(bars + 8 * (B_PREADY + ws), (i >> 1) & 1);
@@ -850,6 +1020,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         __syncwarp();
         if (i + 2 < jobs) ok = scores(i + 2);
       }
+    } else if (warp == 17) {
+      // ---- look-ups
+      Pages s;
+      s.table = T.block_table + (size_t)g * T.max_pages;
+      s.num_pages = T.num_pages;
+      s.page_size = p.page_size;
+      s.page_shift = p.page_shift;
+      s.hkv = p.hkv;
+      s.hk = hk;
+      s.end = len;
+      const bool codes = T.k_fmt == KVQ_FMT_CODEBOOK;
+      look_up(s, codes ? T.k_aux : nullptr, codes ? T.v_aux : nullptr, T.v_fmt == KVQ_FMT_INT4_G32 ? T.v_aux : nullptr,
+              smem, bars, tile0, n, abort, p.err);
     }
   }
   __syncwarp();
