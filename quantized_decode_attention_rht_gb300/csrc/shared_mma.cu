@@ -21,7 +21,7 @@
 // tile; with up to 128 rows both have the same rows and take alternate tiles, which leaves two
 // partial results.  TMEM: two S and two O of 128 columns, all 512.
 //
-// An accumulator is rescaled only when a tile's weights against the running maximum sum to
+// An accumulator is rescaled only when half a tile's weights against the running maximum sum to
 // more than 2^14 in some row of a warp, which after the first tile is rare: until then
 // weights stay inside fp16 and the sums, in float32, inside their range.
 //
@@ -41,8 +41,8 @@ namespace {
 
 constexpr int kDim = 128;
 constexpr int kThreads = 640;
-// registers per thread after the split: launched with 96 x 640 = 61440 = 256 x 144 + 256 x 72 + 128 x 48
-constexpr int kSoftmaxRegs = 144, kDecodeRegs = 72, kIssueRegs = 48;
+// registers per thread after the split: launched with 96 x 640 = 61440 = 256 x 136 + 256 x 80 + 128 x 48
+constexpr int kSoftmaxRegs = 136, kDecodeRegs = 80, kIssueRegs = 48;
 constexpr int kTileBytes = kTileTokens * kDim * 2;  // 32 KB: two halves of 128 rows x 128 bytes
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kStages = 2;
@@ -230,7 +230,8 @@ __host__ __device__ constexpr int unit_passes(int f) { return f == D_F16 ? 16 : 
 struct Source {
   const uint8_t* rows;
   int row_bytes;
-  uint32_t rowbuf, auxbuf;    // shared addresses: kAhead tiles of rows; of this side's norms or scales
+  uint32_t raw;               // shared addresses: the threads' slots;
+  uint32_t rowbuf, auxbuf;    // kAhead tiles of rows; of this side's norms or scales
   uint32_t aux_shift;         // log2 of the latter's bytes a token
   uint32_t lut, lut_stride;   // the lane's copy of entry 0, bytes between entries (codebooks)
 };
@@ -353,26 +354,25 @@ __device__ __forceinline__ void look_up(const Pages& s, const __half* k_norm, co
   if (bits) atomicOr(err, bits);
 }
 
-// A unit of the row, into registers.
+// A unit of the row, on its way to the thread's slot.
 template <int F>
-__device__ __forceinline__ void request(const Source& s, uint32_t row, int u, uint32_t (&w)[4]) {
+__device__ __forceinline__ void request(const Source& s, uint32_t row, int u, uint32_t slot) {
+  const bool there = row != kNoRow;
+  const uint8_t* src = s.rows + (size_t)(there ? row : 0) * s.row_bytes + u * unit_bytes(F);
+  if constexpr (unit_bytes(F) == 12) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] = 0u;
-  if (row == kNoRow) return;
-  const uint8_t* src = s.rows + (size_t)row * s.row_bytes + u * unit_bytes(F);
+    for (int k = 0; k < 3; ++k) copy_async<4>(slot + 4 * k, src + 4 * k, there);
+  } else {
+    copy_async<unit_bytes(F)>(slot, src, there);
+  }
+}
+template <int F>
+__device__ __forceinline__ void take(uint32_t slot, uint32_t (&w)[4]) {
   if constexpr (unit_bytes(F) == 16) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
-    w[0] = x.x;
-    w[1] = x.y;
-    w[2] = x.z;
-    w[3] = x.w;
-  } else if constexpr (unit_bytes(F) == 8) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-    w[0] = x.x;
-    w[1] = x.y;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(slot) : "memory");
   } else {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) w[k] = __ldg(reinterpret_cast<const uint32_t*>(src) + k);
+    for (int k = 0; k < unit_bytes(F) / 4; ++k) w[k] = lds32(slot + 4 * k);
   }
 }
 
@@ -449,62 +449,81 @@ __device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, int 
   }
 }
 
-// The side's n tiles, into the ring.  A thread's units of a tile travel in registers, each slot
-// requested anew as soon as it is decoded, so that a load has a tile's time to arrive.  What a
-// pass needs from shared memory (rows, scales) is read for all of them first: a warp has its
-// scheduler's slots to itself only now and then, and a chain of look-ups in every pass took
-// five times as long as the instructions.
-template <int F>
+// The side's n tiles, into the ring.  A thread's units travel by asynchronous copies into slots
+// of its own (nobody else waits for them), `slots` passes ahead, a slot being requested anew as
+// soon as it is taken.  The loop stays rolled, a pass of 32 values or two of 16 a turn: warps of
+// several kinds share a scheduler's instruction cache, and with all passes unrolled (217 KB of
+// text) they spent more time fetching instructions than running them.
+template <int F, int SLOTS>
 __device__ __forceinline__ void produce(const Source& s, const Ring& ring, int n, int tid, volatile int* abort,
                                         int* err) {
-  constexpr int kPasses = unit_passes(F);
-  uint32_t x[kPasses][4];
+  constexpr int kPasses = unit_passes(F), kTurn = F == D_F8 ? 2 : 1;  // passes a turn
+  constexpr uint32_t kSlotStep = 128 * unit_bytes(F);
+  static_assert(SLOTS % kTurn == 0 && SLOTS <= kPasses && kPasses % SLOTS == 0, "slots");
+  const uint32_t slot0 = s.raw + tid * unit_bytes(F);
   if (!bar_wait(ring.rows, 0, abort, err)) return;
+#pragma unroll 1
+  for (int p = 0; p < SLOTS; p += kTurn) {
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {
-    int t, u;
-    place<F>(p, tid, t, u);
-    request<F>(s, lds32(s.rowbuf + 4u * t), u, x[p]);
+    for (int j = 0; j < kTurn; ++j) {
+      int t, u;
+      place<F>(p + j, tid, t, u);
+      request<F>(s, lds32(s.rowbuf + 4u * t), u, slot0 + (p + j) * kSlotStep);
+    }
+    copy_commit();
   }
   for (int i = 0; i < n; ++i) {
     const int st = i & 1, at = i % kAhead, after = (i + 1) % kAhead;
     const bool more = i + 1 < n;
-    uint32_t row[kPasses], scale[kPasses];
-    if (more && !bar_wait(ring.rows + 8 * after, ((i + 1) / kAhead) & 1, abort, err)) return;
-    if (F >= D_I4 && !bar_wait(ring.aux + 8 * at, (i / kAhead) & 1, abort, err)) return;
+    if (more && !bar_wait(ring.rows + 8 * after, ((i + 1) / kAhead) & 1, abort, err)) break;
+    if (F >= D_I4 && !bar_wait(ring.aux + 8 * at, (i / kAhead) & 1, abort, err)) break;
+    if (i >= kStages && !bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err)) break;
+    if (i == 1 && ring.first_use && !bar_wait(ring.first_use, 0, abort, err)) break;
+    const uint32_t tile = ring.tiles + st * kTileBytes, aux = s.auxbuf + ((uint32_t)(at * kTileTokens) << s.aux_shift);
+    uint32_t slot = slot0;
+#pragma unroll 1
+    for (int p = 0; p < kPasses; p += kTurn) {
+      const bool here = p + SLOTS < kPasses;  // the slots' next units are of this tile
+      const int q = here ? p + SLOTS : p + SLOTS - kPasses;
+      const uint32_t rows = s.rowbuf + (here ? at : after) * kRowBytes;
+      copy_wait<SLOTS / kTurn - 1>();
+      uint32_t w[kTurn][4], row[kTurn];
+      uint32_t scale = 0;
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      int t, u;
-      place<F>(p, tid, t, u);
-      row[p] = more ? lds32(s.rowbuf + after * kRowBytes + 4u * t) : kNoRow;
-      scale[p] = 0;
-      if constexpr (F >= D_I4) {
-        uint16_t v;
-        asm volatile("ld.shared.u16 %0, [%1];"
-                     : "=h"(v)
-                     : "r"(s.auxbuf + (((uint32_t)(at * kTileTokens + t)) << s.aux_shift) + (F == D_I4 ? 2u * u : 0u)));
-        scale[p] = v;
+      for (int j = 0; j < kTurn; ++j) {
+        int t, u;
+        take<F>(slot + j * kSlotStep, w[j]);
+        place<F>(q + j, tid, t, u);
+        row[j] = lds32(rows + 4u * t);
+        if constexpr (F >= D_I4) {
+          uint16_t v;
+          place<F>(p, tid, t, u);
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(aux + ((uint32_t)t << s.aux_shift) + (F == D_I4 ? 2u * u : 0u)));
+          scale = v;
+        }
       }
-    }
-    if (i >= kStages && !bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err)) return;
-    if (i == 1 && ring.first_use && !bar_wait(ring.first_use, 0, abort, err)) return;
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      int t, u;
-      place<F>(p, tid, t, u);
-      decode_unit<F>(s, ring.tiles + st * kTileBytes, t, u, scale[p], x[p]);
-      request<F>(s, row[p], u, x[p]);
+      for (int j = 0; j < kTurn; ++j) {
+        int t, u;
+        place<F>(p + j, tid, t, u);
+        decode_unit<F>(s, tile, t, u, scale, w[j]);
+        place<F>(q + j, tid, t, u);
+        if (here || more) request<F>(s, row[j], u, slot + j * kSlotStep);
+      }
+      copy_commit();
+      slot = p + kTurn == SLOTS || p + kTurn == 2 * SLOTS ? slot0 : slot + kTurn * kSlotStep;
     }
     fence_async_smem();
     bar_arrive(ring.full + 8 * st);
     bar_arrive(ring.rows_read + 8 * at);
   }
+  copy_wait<0>();
 }
 
 // fp16 rows need no decoding: copies straight into the tile, a tile signalled once the next
 // one's copies are under way.
 template <>
-__device__ __forceinline__ void produce<D_F16>(const Source& s, const Ring& ring, int n, int tid, volatile int* abort,
+__device__ __forceinline__ void produce<D_F16, 1>(const Source& s, const Ring& ring, int n, int tid, volatile int* abort,
                                                int* err) {
   bool ok = true;
   for (int i = 0; i < n; ++i) {
@@ -536,15 +555,25 @@ __device__ __forceinline__ void produce<D_F16>(const Source& s, const Ring& ring
   }
 }
 
-__device__ __forceinline__ void produce_any(int f, const Source& s, const Ring& ring, int n, int tid, volatile int* abort,
-                                            int* err) {
+// deep: there is room for a whole tile's units of a codebook side
+__device__ __forceinline__ void produce_any(int f, bool deep, const Source& s, const Ring& ring, int n, int tid,
+                                            volatile int* abort, int* err) {
   switch (f) {
-    case D_F16: produce<D_F16>(s, ring, n, tid, abort, err); break;
-    case D_F8: produce<D_F8>(s, ring, n, tid, abort, err); break;
-    case D_I4: produce<D_I4>(s, ring, n, tid, abort, err); break;
-    case D_CB4: produce<D_CB4>(s, ring, n, tid, abort, err); break;
-    case D_CB3: produce<D_CB3>(s, ring, n, tid, abort, err); break;
-    default: produce<D_CB2>(s, ring, n, tid, abort, err); break;
+    case D_F16: produce<D_F16, 1>(s, ring, n, tid, abort, err); break;
+    case D_F8: produce<D_F8, 8>(s, ring, n, tid, abort, err); break;
+    case D_I4: produce<D_I4, 4>(s, ring, n, tid, abort, err); break;
+    case D_CB4:
+      if (deep) produce<D_CB4, 4>(s, ring, n, tid, abort, err);
+      else produce<D_CB4, 2>(s, ring, n, tid, abort, err);
+      break;
+    case D_CB3:
+      if (deep) produce<D_CB3, 4>(s, ring, n, tid, abort, err);
+      else produce<D_CB3, 2>(s, ring, n, tid, abort, err);
+      break;
+    default:
+      if (deep) produce<D_CB2, 4>(s, ring, n, tid, abort, err);
+      else produce<D_CB2, 2>(s, ring, n, tid, abort, err);
+      break;
   }
 }
 
@@ -557,9 +586,9 @@ __device__ __forceinline__ int decode_kind(int fmt, int bits) {
   }
 }
 
-// Pairs of centroids / sqrt(D) in fp16: entry e = codes (e mod 2^b, e / 2^b), one copy per lane
-// where there is room (a warp's look-ups then never meet in a bank), else 16 or 8 of them (two
-// or three bank rounds a look-up).  tid: 256 threads.
+// Pairs of centroids / sqrt(D) in fp16: entry e = codes (e mod 2^b, e / 2^b), in copies, one per
+// lane where there is room (a warp's look-ups then never meet in a bank), else 16 or 8 of them
+// (two or three bank rounds a look-up).  tid: 256 threads.
 __device__ __forceinline__ void build_lut(uint32_t lut, int copies, const float* cent, int bits, int tid) {
   if (tid >= (1 << (2 * bits))) return;
   const float inv = inv_sqrt_dim(kDim);
@@ -567,52 +596,55 @@ __device__ __forceinline__ void build_lut(uint32_t lut, int copies, const float*
   for (int i = 0; i < copies; i += 4) sts16(lut + 4u * (tid * copies + i), v, v, v, v);
 }
 
-// Where the two tables lie.  With up to 128 rows the second query tile is free: 32 KB more.
+// Where the two tables lie, and the slots.  24 KB are set aside: fp8 keys and INT4 values use
+// them for slots alone (16 and 8 KB).  With up to 128 rows the second query tile is free as
+// well: the tables go there (one of 32 copies where keys and values have the same, else 16
+// copies each), and the slots, four passes a side, have the 24 KB.  With more rows both share
+// them: 16 KB of tables (16 copies of one, or 8 of each), 4 KB of slots a side.
 struct Tables {
-  uint32_t at[2];
+  uint32_t at[2], raw[2];
   int copies[2];
 };
 __device__ __forceinline__ Tables place_tables(uint32_t smem, int k_bits, int v_bits, bool same, bool both) {
   const uint32_t lut = smem + kOffLut, spare = smem + kOffQ + kTileBytes;
   Tables t;
-  t.at[0] = lut;
-  t.at[1] = lut + kLutBytes / 2;
-  t.copies[0] = k_bits == 4 ? 8 : 32;  // 2^(2 bits) entries: 8 KB
-  t.copies[1] = v_bits == 4 ? 8 : 32;
-  if (k_bits == 4 && v_bits == 4 && same) {
-    t.at[0] = t.at[1] = both ? spare : lut;
-    t.copies[0] = t.copies[1] = both ? 32 : 16;
-  } else if (both) {
-    if (k_bits == 4) {
-      t.at[0] = spare;
-      t.copies[0] = 32;
-      if (v_bits == 4) {
-        t.at[1] = lut;
-        t.copies[1] = 16;
-      }
-    } else if (v_bits == 4) {
-      t.at[1] = spare;
-      t.copies[1] = 32;
-    }
-  }
+  const int of_1kb = (both ? 16 : 8) << (same ? 1 : 0);
+  t.copies[0] = k_bits == 4 ? of_1kb : 32;  // (smaller tables: 8 KB at most)
+  t.copies[1] = v_bits == 4 ? of_1kb : 32;
+  t.at[0] = both ? spare : lut;
+  t.at[1] = t.at[0] + (same ? 0 : (both ? 16 << 10 : 8 << 10));
+  t.raw[0] = both ? lut : lut + (16 << 10);
+  t.raw[1] = t.raw[0] + (both ? 8 << 10 : 4 << 10);
   return t;
 }
 
 // ------------------------------------------------------------------------ softmax
-// A tile's weights against the running maximum may sum to this before it is raised (the largest
+// Half a tile's weights against the running maximum may sum to this before it is raised (the largest
 // fp16 is 2^16).
 constexpr float kMostWeight = 16384.0f;
 
-// A row's maximum has grown: the accumulator is scaled by f = 2^(old - new).
-__device__ __forceinline__ void rescale(uint32_t o_at, float f) {
+// A row's maximum has grown, f = 2^(old - new): the accumulator (if any product has gone into it)
+// and the tile's first `done` weight columns are scaled.
+__device__ __forceinline__ void rescale(uint32_t o_at, bool acc, uint32_t p_at, int done, float f) {
   uint32_t v[16];
 #pragma unroll 1
-  for (int c = 0; c < kDim; c += 16) {
+  for (int c = 0; acc && c < kDim; c += 16) {
     tc_ld16(o_at + c, v);
     tc_wait_ld(v);
 #pragma unroll
     for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
     tc_st16(o_at + c, v);
+  }
+#pragma unroll 1
+  for (int c = 0; c < done; c += 16) {
+    tc_ld16(p_at + c, v);
+    tc_wait_ld(v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
+      v[e] = half2_bits(x.x * f, x.y * f);
+    }
+    tc_st16(p_at + c, v);
   }
 }
 
@@ -820,70 +852,68 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         const int valid = min(kTileTokens, len - tile * kTileTokens);
         if (!(ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * (B_SFULL + w), k & 1, abort, p.err)))) break;
         tc_fence_after();
-        // Weights of the whole tile against the running maximum as it is, kept in registers: no
+        // Half a tile's weights at a time, against the running maximum as it is, in registers: no
         // maximum is taken.  All weights are positive, so a sum of at most kMostWeight says that
-        // none is too large for fp16 either; only where it is exceeded (always in the first tile,
-        // where the maximum is -inf) the maximum is raised and the tile, still in TMEM, weighed
-        // again.
-        uint32_t h[64];
-        unsigned long long sum;
+        // none is too large for fp16 either; only where it is exceeded (always at first, where the
+        // maximum is -inf) the maximum is raised and the half, still in TMEM, weighed again.
 #pragma unroll 1
-        for (int again = 0;; ++again) {
-          const unsigned long long neg = pack2(-m, -m);
-          unsigned long long s0 = 0, s1 = 0;
-          auto weigh = [&](int c, uint32_t (&v)[32]) {
-            if (valid < kTileTokens) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c + e >= valid) v[e] = 0xFF800000u;  // -inf: weight 0
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 x = unpack2(add2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), neg));
-              const float a = ex2(x.x), b = ex2(x.y);
-              if (e & 1) s1 = add2(s1, pack2(a, b));
-              else s0 = add2(s0, pack2(a, b));
-              h[c / 2 + e] = half2_bits(a, b);
-            }
-          };
-          uint32_t va[32], vb[32];
-          tc_ld32(s_at, va);
-          tc_wait_ld(va);
-          tc_ld32(s_at + 32, vb);
-          weigh(0, va);
-          tc_wait_ld(vb);
-          tc_ld32(s_at + 64, va);
-          weigh(32, vb);
-          tc_wait_ld(va);
-          tc_ld32(s_at + 96, vb);
-          weigh(64, va);
-          tc_wait_ld(vb);
-          weigh(96, vb);
-          sum = add2(s0, s1);
-          const float2 t = unpack2(sum);
-          if (again || __all_sync(0xFFFFFFFFu, t.x + t.y <= kMostWeight)) break;
-          float mx = m;
+        for (int c0 = 0; c0 < kTileTokens; c0 += 64) {
+          uint32_t h[32];
+          unsigned long long sum;
 #pragma unroll 1
-          for (int c = 0; c < kTileTokens; c += 32) {
-            tc_ld32(s_at + c, va);
+          for (int again = 0;; ++again) {
+            const unsigned long long neg = pack2(-m, -m);
+            unsigned long long s0 = 0, s1 = 0;
+            auto weigh = [&](int c, uint32_t (&v)[32]) {
+              if (valid < kTileTokens) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (c0 + c + e >= valid) v[e] = 0xFF800000u;  // -inf: weight 0
+              }
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float2 x = unpack2(add2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), neg));
+                const float a = ex2(x.x), b = ex2(x.y);
+                if (e & 1) s1 = add2(s1, pack2(a, b));
+                else s0 = add2(s0, pack2(a, b));
+                h[c / 2 + e] = half2_bits(a, b);
+              }
+            };
+            uint32_t va[32], vb[32];
+            tc_ld32(s_at + c0, va);
             tc_wait_ld(va);
+            tc_ld32(s_at + c0 + 32, vb);
+            weigh(0, va);
+            tc_wait_ld(vb);
+            weigh(32, vb);
+            sum = add2(s0, s1);
+            const float2 t = unpack2(sum);
+            if (again || __all_sync(0xFFFFFFFFu, t.x + t.y <= kMostWeight)) break;
+            float mx = m;
+#pragma unroll 1
+            for (int c = c0; c < c0 + 64; c += 16) {
+              uint32_t x[16];
+              tc_ld16(s_at + c, x);
+              tc_wait_ld(x);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c + e < valid) mx = fmaxf(mx, __uint_as_float(va[e]));
+              for (int e = 0; e < 16; ++e)
+                if (c + e < valid) mx = fmaxf(mx, __uint_as_float(x[e]));
+            }
+            const float f = ex2(m - mx);
+            m = mx;
+            const float2 ll = unpack2(l2);
+            l2 = pack2(ll.x * f, ll.y * f);
+            // (the products of earlier tiles are complete: they precede these scores)
+            rescale(o_at, k > 0, s_at, c0 / 2, f);
           }
-          const float f = ex2(m - mx);
-          m = mx;
-          const float2 ll = unpack2(l2);
-          l2 = pack2(ll.x * f, ll.y * f);
-          if (k > 0) rescale(o_at, f);  // the products of earlier tiles are complete: they precede these scores
-        }
-        l2 = add2(l2, sum);
+          l2 = add2(l2, sum);
 #pragma unroll
-        for (int c = 0; c < 64; c += 16) {  // over the scores
-          uint32_t part[16];
+          for (int c = 0; c < 32; c += 16) {  // over the scores
+            uint32_t part[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) part[e] = h[c + e];
-          tc_st16(s_at + c, part);
+            for (int e = 0; e < 16; ++e) part[e] = h[c + e];
+            tc_st16(s_at + c0 / 2 + c, part);
+          }
         }
         tc_wait_st();
         tc_fence_before();
@@ -943,6 +973,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       const int side = keys ? 0 : 1;
       s.lut = tables.at[side] + 4u * (threadIdx.x & (tables.copies[side] - 1));
       s.lut_stride = 4u * tables.copies[side];
+      s.raw = tables.raw[side];
+    } else {
+      s.raw = smem + kOffLut + (keys ? 0 : 16 << 10);
     }
     s.rowbuf = smem + kOffRow;
     s.auxbuf = smem + (keys ? kOffKAux : kOffVAux);
@@ -955,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     ring.aux = bars + 8 * B_AUX;
     ring.rows_read = bars + 8 * B_ROWS_READ;
     ring.first_use = keys ? 0 : bars + 8 * B_QROT;  // the second value stage first holds the rotation
-    produce_any(keys ? decode_kind(T.k_fmt, T.k_bits) : decode_kind(T.v_fmt, T.v_bits), s, ring, n,
+    produce_any(keys ? decode_kind(T.k_fmt, T.k_bits) : decode_kind(T.v_fmt, T.v_bits), both, s, ring, n,
                 threadIdx.x & 127, abort, p.err);
   } else {
     // ---- products
