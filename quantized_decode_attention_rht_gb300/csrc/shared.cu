@@ -19,11 +19,23 @@ namespace kvq {
 namespace {
 
 // ------------------------------------------------------------------------ joining
-struct JoinParams {
-  SharedParams pre;
-  DecParams dec;  // the sequences' own tiers (num_tiers may be 0)
+struct JoinTier {  // of the sequences' own
+  const int32_t* seq_lens;
+  int max_pages, chunk, num_splits, split_begin;
+};
+struct JoinParams {  // small: a launch's parameters are read through a cold cache
+  const float* acc;  // the prefix's partials [2 * splits][rows][128], (max, sum) beside them
+  const float2* ml;
+  const float* own_acc;  // [rows][own splits][128]
+  const float2* own_ml;
+  const int8_t* v_signs;
   __half* out;
   int* status;
+  const int* err;
+  int batch, hq, group_shift, page_size;
+  int splits, own_splits, num_tiers, num_groups;
+  JoinTier tier[KVQ_MAX_TIERS];
+  int offset[KVQ_MAX_PREFIX_GROUPS + 1];
 };
 
 // Where row (b, h)'s partials lie: the prefix's first, then those of the sequence's tiers.
@@ -33,57 +45,49 @@ struct Parts {
   int total;
 };
 
-__device__ __forceinline__ Parts find_parts(const JoinParams& p, int b, int h) {
-  Parts n;
-  n.pre = 0;
-  n.per_split = 1;
-  const SharedParams& s = p.pre;
-  int lo = 0, hi = s.num_groups;
+__device__ __forceinline__ void find_prefix_parts(const JoinParams& p, int b, int h, Parts& n) {
+  int lo = 0, hi = p.num_groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (s.offset[mid] <= b) lo = mid;
+    if (p.offset[mid] <= b) lo = mid;
     else hi = mid;
   }
-  if (b >= s.offset[lo] && b < s.offset[lo + 1]) {
-    const int row = (b - s.offset[lo]) * s.group + h % s.group;
-    n.per_split = block_partials((s.offset[lo + 1] - s.offset[lo]) * s.group, row / kItemRows);
-    n.pre = s.total_splits * n.per_split;
+  const int first = p.offset[lo], end = p.offset[lo + 1];
+  n.pre = 0;
+  n.per_split = 1;
+  if (b >= first && b < end) {
+    const int row = ((b - first) << p.group_shift) + (h & ((1 << p.group_shift) - 1));
+    n.per_split = block_partials((end - first) << p.group_shift, row / kItemRows);
+    n.pre = p.splits * n.per_split;
   }
+}
+__device__ __forceinline__ void find_own_parts(const JoinParams& p, const int (&lens)[KVQ_MAX_TIERS], Parts& n) {
   n.total = n.pre;
 #pragma unroll
   for (int i = 0; i < KVQ_MAX_TIERS; ++i) {
     n.own[i] = 0;
-    if (i < p.dec.num_tiers) {
-      const DecTier& T = p.dec.tier[i];
+    if (i < p.num_tiers) {
       int bits = 0;
-      n.own[i] = splits_holding_tokens(checked_len(T.seq_lens[b], T.max_pages, p.dec.page_size, &bits), T.chunk,
-                                       T.num_splits);
+      n.own[i] = splits_holding_tokens(checked_len(lens[i], p.tier[i].max_pages, p.page_size, &bits), p.tier[i].chunk,
+                                       p.tier[i].num_splits);
       n.total += n.own[i];
     }
   }
-  return n;
 }
 
 // Partial j of the row: its (max, sum) and accumulator.
-__device__ __forceinline__ void locate(const JoinParams& p, const Parts& n, size_t row, int j, const float2*& ml,
-                                       const float*& acc) {
-  if (j < n.pre) {
-    const int part = n.per_split == 2 ? j : 2 * j;
-    const size_t at = (size_t)part * p.pre.batch * p.pre.hq + row;
-    ml = reinterpret_cast<const float2*>(p.pre.ml) + at;
-    acc = p.pre.acc + at * 128;
-    return;
-  }
-  j -= n.pre;
+__device__ __forceinline__ size_t prefix_part(const JoinParams& p, const Parts& n, size_t row, int j) {
+  return (size_t)(n.per_split == 2 ? j : 2 * j) * p.batch * p.hq + row;
+}
+__device__ __forceinline__ size_t own_part(const JoinParams& p, const Parts& n, size_t row, int j) {
   int split = 0;
+  j -= n.pre;
 #pragma unroll
   for (int i = 0; i < KVQ_MAX_TIERS; ++i) {
-    if (j >= 0 && j < n.own[i]) split = p.dec.tier[i].split_begin + j;
+    if (j >= 0 && j < n.own[i]) split = p.tier[i].split_begin + j;
     j -= n.own[i];
   }
-  const size_t at = row * p.dec.total_splits + split;
-  ml = reinterpret_cast<const float2*>(p.dec.ws_ml) + at;
-  acc = p.dec.ws_acc + at * 128;
+  return row * p.own_splits + split;
 }
 
 // kRowWarps warps per row: one where rows have few partials, eight where they have many.
@@ -93,35 +97,49 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
   __shared__ float s_acc[kRowWarps > 1 ? kRowWarps : 1][128];
   __shared__ float s_l[kRowWarps], s_m[kRowWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // every partial is complete
   const long long row = (long long)blockIdx.x * kRows + warp / kRowWarps;
-  const int part = warp % kRowWarps;
+  const int part = warp % kRowWarps, j0 = lane * kRowWarps + part;
+  const bool there = row < (long long)p.batch * p.hq;  // whole warps; with eight warps a row, whole blocks
+  const int b = there ? (int)(row / p.hq) : 0, h = there ? (int)(row - (long long)b * p.hq) : 0;
+  Parts n;
+  find_prefix_parts(p, b, h, n);
+  const uint32_t sg =
+      __ldg(reinterpret_cast<const uint32_t*>(p.v_signs + (size_t)(h >> p.group_shift) * 128) + lane);
+  int lens[KVQ_MAX_TIERS];
+#pragma unroll
+  for (int i = 0; i < KVQ_MAX_TIERS; ++i) lens[i] = i < p.num_tiers ? __ldg(p.tier[i].seq_lens + b) : 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // every partial is complete
   if (p.status && blockIdx.x == 0 && warp == 0) {
     int bits = 0;  // lengths out of range, of sequences; the prefix pass reports its own
-    for (int i = lane; i < p.dec.batch * p.dec.num_tiers; i += 32) {
-      const DecTier& T = p.dec.tier[i % p.dec.num_tiers];
-      checked_len(T.seq_lens[i / p.dec.num_tiers], T.max_pages, p.dec.page_size, &bits);
+    for (int i = lane; i < p.batch * p.num_tiers; i += 32) {
+      const JoinTier& T = p.tier[i % p.num_tiers];
+      checked_len(T.seq_lens[i / p.num_tiers], T.max_pages, p.page_size, &bits);
     }
     bits = __reduce_or_sync(0xFFFFFFFFu, bits);
-    if (lane == 0) *p.status = bits | *reinterpret_cast<volatile int*>(p.pre.err);
+    if (lane == 0) *p.status = bits | *reinterpret_cast<const volatile int*>(p.err);
   }
-  if (row >= (long long)p.pre.batch * p.pre.hq) return;  // whole warps; with eight warps a row, whole blocks
-  const int b = (int)(row / p.pre.hq), h = (int)(row - (long long)b * p.pre.hq);
-  const Parts n = find_parts(p, b, h);
+  if (!there) return;
   // a lane looks after one partial at a time: its (max, sum) and where its accumulator lies
-  auto look = [&](int j, float2& x) -> const float* {
-    const float2* ml;
-    const float* acc = nullptr;
-    x = make_float2(-INFINITY, 0.f);
-    if (j < n.total) {
-      locate(p, n, row, j, ml, acc);
-      x = *ml;
-    }
-    return acc;
+  float2 x0 = make_float2(-INFINITY, 0.f), x;
+  const float* acc0 = nullptr;
+  if (j0 < n.pre) {
+    const size_t at = prefix_part(p, n, row, j0);
+    x0 = p.ml[at];
+    acc0 = p.acc + at * 128;
+  }
+  find_own_parts(p, lens, n);
+  if (j0 >= n.pre && j0 < n.total) {
+    const size_t at = own_part(p, n, row, j0);
+    x0 = p.own_ml[at];
+    acc0 = p.own_acc + at * 128;
+  }
+  auto look = [&](int j, float2& y) -> const float* {
+    y = make_float2(-INFINITY, 0.f);
+    if (j >= n.total) return nullptr;
+    const size_t at = j < n.pre ? prefix_part(p, n, row, j) : own_part(p, n, row, j);
+    y = j < n.pre ? p.ml[at] : p.own_ml[at];
+    return (j < n.pre ? p.acc : p.own_acc) + at * 128;
   };
-  const int j0 = lane * kRowWarps + part;
-  float2 x0, x;
-  const float* acc0 = look(j0, x0);
   float mx = x0.x;
   for (int j = j0 + 32 * kRowWarps; j < n.total; j += 32 * kRowWarps) {
     look(j, x);
@@ -178,7 +196,6 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
 #pragma unroll
   for (int k = 0; k < 4; ++k) y[k] *= inv;
   sign_free_rotate<4>(lane, y);
-  const uint32_t sg = __ldg(reinterpret_cast<const uint32_t*>(p.dec.v_signs + (size_t)(h / p.pre.group) * 128) + lane);
 #pragma unroll
   for (int k = 0; k < 4; ++k) y[k] = (sg >> (8 * k)) & 0x80u ? -y[k] : y[k];
   const __half2 a = __floats2half2_rn(y[0], y[1]), c = __floats2half2_rn(y[2], y[3]);
@@ -262,15 +279,18 @@ kvq_status check_call(const Call& c, kvq_tier_view* all) {
 // and joining partial results does not cost more than the idle SMs would.  In units of one
 // tile's time (both accumulators): an item is its tiles plus a fixed start and end, a split's
 // partials are a pass over them at memory speed.
-int choose_splits(long long row_blocks, long long rows, int max_tiles, int sms) {
-  const double start = 4.0;                                   // tiles' worth of set-up, fill and drain
-  const double partial = (double)rows * 1040.0 / 3.5e12 / 1.1e-6;  // write + read of one split's partials
+int choose_splits(long long row_blocks, long long rows, int max_tiles, int sms, int own_blocks) {
+  const double start = 5.0;                                   // tiles' worth of set-up, fill and drain
+  const double partial = (double)rows * 1040.0 / 3.5e12 / 1.5e-6;  // write + read of one split's partials
   int best = 1;
   double least = 1e300;
   for (int s = 1; s <= std::min(max_tiles, 256); ++s) {
     const int per = (max_tiles + s - 1) / s;
     if ((max_tiles + per - 1) / per != s) continue;  // the same chunks with fewer splits
-    const double waves = (double)((row_blocks * s + sms - 1) / sms);
+    // one wave leaves the sequences' own pass SMs to run on beside it; more make room as they end
+    const long long items = row_blocks * s;
+    const int room = items <= sms ? std::max(1, sms - own_blocks) : sms;
+    const double waves = (double)((items + room - 1) / room);
     const double t = waves * (per + start) + s * partial;
     if (t < least) {
       least = t;
@@ -331,7 +351,8 @@ kvq_status make_shared_plan(const Call& c, const kvq_tier_view* all, bool q16, S
   }
   const long long prefix_rows = (long long)(c.offsets[c.num_groups] - c.offsets[0]) * c.hq;
   const int want = sum ? choose_splits((long long)plan->num_blocks * c0->num_kv_heads, prefix_rows,
-                                       (int)std::min<long long>(sum, 1 << 30), device_sms())
+                                       (int)std::min<long long>(sum, 1 << 30), device_sms(),
+                                       c.num_tiers > 0 ? device_sms() / 7 : 0)
                        : 0;
   const long long per = want ? (sum + want - 1) / want : 1;
   for (int i = 0; i < c.num_prefix; ++i) {
@@ -443,21 +464,14 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
     return launched() == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
   }
 
-  JoinParams j;
-  memset(static_cast<void*>(&j), 0, sizeof(j));
-  if (num_tiers > 0) {
-    fill_decode(all + num_prefix_tiers, num_tiers, plan.dec, q, batch, num_q_heads, ws, plan.sketch, &j.dec);
-  } else {
-    j.dec.batch = batch;
-    j.dec.hq = num_q_heads;
-    j.dec.hkv = hkv;
-    j.dec.page_size = c0->page_size;
-    j.dec.k_signs = c0->k_signs;
-    j.dec.v_signs = c0->v_signs;
-  }
+  DecParams own;
+  memset(&own, 0, sizeof(own));
+  if (num_tiers > 0)
+    fill_decode(all + num_prefix_tiers, num_tiers, plan.dec, q, batch, num_q_heads, ws, plan.sketch, &own);
   int* counters = reinterpret_cast<int*>(ws + plan.dec_bytes - 256);
-  j.dec.err = counters + kErrorWord;
-  SharedParams& p = j.pre;
+  own.err = counters + kErrorWord;
+  SharedParams p;
+  memset(&p, 0, sizeof(p));
   int at = 0;
   for (int i = 0; i < num_prefix_tiers; ++i) {
     const kvq_cache* k = all[i].cache;
@@ -487,7 +501,7 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
   p.k_signs = c0->k_signs;
   p.acc = reinterpret_cast<float*>(ws + plan.acc);
   p.ml = reinterpret_cast<float*>(ws + plan.ml);
-  p.err = j.dec.err;
+  p.err = own.err;
   p.batch = batch;
   p.hq = num_q_heads;
   p.hkv = hkv;
@@ -502,11 +516,31 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
     p.offset[g] = group_offsets[g];
     p.block[g] = plan.block[g];
   }
+  JoinParams j;
+  memset(&j, 0, sizeof(j));
+  j.acc = p.acc;
+  j.ml = reinterpret_cast<const float2*>(p.ml);
+  j.own_acc = own.ws_acc;
+  j.own_ml = reinterpret_cast<const float2*>(own.ws_ml);
+  j.v_signs = c0->v_signs;
   j.out = reinterpret_cast<__half*>(out);
   j.status = status;
+  j.err = p.err;
+  j.batch = batch;
+  j.hq = num_q_heads;
+  while ((1 << j.group_shift) < group) ++j.group_shift;
+  j.page_size = c0->page_size;
+  j.splits = p.total_splits;
+  j.own_splits = plan.dec.total;
+  j.num_tiers = num_tiers;
+  j.num_groups = num_groups;
+  for (int i = 0; i < num_tiers; ++i)
+    j.tier[i] = {own.tier[i].seq_lens, own.tier[i].max_pages, own.tier[i].chunk, own.tier[i].num_splits,
+                 own.tier[i].split_begin};
+  for (int g = 0; g <= num_groups; ++g) j.offset[g] = group_offsets[g];
   e = cudaMemsetAsync(counters, 0, 256, s);  // work counters and the error word
   if (e == cudaSuccess && p.num_items > 0) e = launch_shared_prefix(p, s);
-  if (e == cudaSuccess && num_tiers > 0) e = launch_own(j.dec, plan.dec, d, group, counters, p.num_items > 0, s);
+  if (e == cudaSuccess && num_tiers > 0) e = launch_own(own, plan.dec, d, group, counters, p.num_items > 0, s);
   if (e == cudaSuccess) {
     // eight warps a row where a row has many partials (one warp would wait for them in turn)
     const bool many = 2 * plan.total_splits + plan.dec.total > 24;

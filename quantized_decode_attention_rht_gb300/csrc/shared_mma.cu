@@ -13,7 +13,7 @@
 //   4 + 4 decoding warps: K and V tiles of 128 tokens, read from the packed cache into
 //     registers two tiles ahead, decoded to fp16 into shared memory (128-byte swizzle)
 //   1 warp: issues the products and allocates TMEM
-//   1 warp: looks up page numbers, rows, norms and scales, up to three tiles ahead.
+//   3 warps: look up page numbers, rows, norms and scales, up to four tiles ahead.
 // Both products are tcgen05.mma of 128 x 128 x 16 steps: S = q~ K^T from shared memory, O += P V
 // with P read from TMEM (it overwrites S) and V as it lies (tokens x coordinates, the
 // MN-major form).  The two softmax groups alternate, so that one's products run while the
@@ -294,62 +294,57 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// The look-up warp: rows of every tile's tokens, then (a tile later, when their loads have
-// arrived) their norms (codebooks) or group scales (INT4 values); page numbers are read a tile
-// before their rows are formed.
+// Look-up warp `first` of kLookUps, which take tiles in turn (a look-up is a chain of three
+// loads, longer than a tile's products): rows of a tile's tokens, then their norms (codebooks) or
+// group scales (INT4 values).  Page numbers are read a turn ahead.
+constexpr int kLookUps = 3;
 __device__ __forceinline__ void look_up(const Pages& s, const __half* k_norm, const __half* v_norm,
-                                        const __half* v_scale, uint32_t smem, uint32_t bars, int tile0, int n,
+                                        const __half* v_scale, uint32_t smem, uint32_t bars, int tile0, int n, int first,
                                         volatile int* abort, int* err) {
   const int lane = threadIdx.x & 31;
   int bits = 0;
   int page[4];
-  uint2 aux[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) page[j] = page_of(s, tile0 * kTileTokens + lane + 32 * j);
-  for (int i = 0; i <= n; ++i) {
+  for (int j = 0; j < 4; ++j) page[j] = first < n ? page_of(s, (tile0 + first) * kTileTokens + lane + 32 * j) : -1;
+#pragma unroll 1
+  for (int i = first; i < n; i += kLookUps) {
     const int at = i % kAhead;
+    if (i >= kAhead && !bar_wait(bars + 8 * (B_ROWS_READ + at), ((i / kAhead) & 1) ^ 1, abort, err)) break;
+    const int t0 = (tile0 + i) * kTileTokens + lane;
     uint32_t row[4];
-    if (i < n) {
-      if (i >= kAhead && !bar_wait(bars + 8 * (B_ROWS_READ + at), ((i / kAhead) & 1) ^ 1, abort, err)) break;
-      const int t0 = (tile0 + i) * kTileTokens + lane;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        row[j] = row_of(s, t0 + 32 * j, page[j], &bits);
-        sts32(smem + kOffRow + at * kRowBytes + 4 * (lane + 32 * j), row[j]);
-      }
-      bar_arrive(bars + 8 * (B_ROWS + at));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) page[j] = page_of(s, t0 + kTileTokens + 32 * j);
+    for (int j = 0; j < 4; ++j) {
+      row[j] = row_of(s, t0 + 32 * j, page[j], &bits);
+      sts32(smem + kOffRow + at * kRowBytes + 4 * (lane + 32 * j), row[j]);
     }
-    if (!k_norm && !v_scale) continue;
-    if (i > 0) {
-      const int before = (i - 1) % kAhead;
-      const uint32_t ka = smem + kOffKAux + before * kTileTokens * 4 + 4 * lane;
-      const uint32_t va = smem + kOffVAux + before * kTileTokens * 8 + 8 * lane;
+    bar_arrive(bars + 8 * (B_ROWS + at));
+    uint2 aux[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (k_norm) {
-          sts32(ka + 128 * j, aux[j].x);
-          sts32(va + 256 * j, aux[j].y);
-        } else {
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(va + 256 * j), "r"(aux[j].x), "r"(aux[j].y) : "memory");
-        }
-      }
-      bar_arrive(bars + 8 * (B_AUX + before));
-    }
-    if (i < n) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        aux[j] = make_uint2(0u, 0u);
-        if (row[j] == kNoRow) continue;
-        if (k_norm) {
-          aux[j].x = __half_as_ushort(__ldg(k_norm + row[j]));
-          aux[j].y = __half_as_ushort(__ldg(v_norm + row[j]));
-        } else {
-          aux[j] = __ldg(reinterpret_cast<const uint2*>(v_scale) + row[j]);
-        }
+    for (int j = 0; j < 4; ++j) {
+      aux[j] = make_uint2(0u, 0u);
+      if (row[j] != kNoRow && k_norm) {
+        aux[j].x = __half_as_ushort(__ldg(k_norm + row[j]));
+        aux[j].y = __half_as_ushort(__ldg(v_norm + row[j]));
+      } else if (row[j] != kNoRow && v_scale) {
+        aux[j] = __ldg(reinterpret_cast<const uint2*>(v_scale) + row[j]);
       }
     }
+    if (i + kLookUps < n) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) page[j] = page_of(s, t0 + kLookUps * kTileTokens + 32 * j);
+    }
+    const uint32_t ka = smem + kOffKAux + at * kTileTokens * 4 + 4 * lane;
+    const uint32_t va = smem + kOffVAux + at * kTileTokens * 8 + 8 * lane;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (k_norm) {
+        sts32(ka + 128 * j, aux[j].x);
+        sts32(va + 256 * j, aux[j].y);
+      } else if (v_scale) {
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(va + 256 * j), "r"(aux[j].x), "r"(aux[j].y) : "memory");
+      }
+    }
+    bar_arrive(bars + 8 * (B_AUX + at));
   }
   if (bits) atomicOr(err, bits);
 }
@@ -589,11 +584,14 @@ __device__ __forceinline__ int decode_kind(int fmt, int bits) {
 // Pairs of centroids / sqrt(D) in fp16: entry e = codes (e mod 2^b, e / 2^b), in copies, one per
 // lane where there is room (a warp's look-ups then never meet in a bank), else 16 or 8 of them
 // (two or three bank rounds a look-up).  tid: 256 threads.
-__device__ __forceinline__ void build_lut(uint32_t lut, int copies, const float* cent, int bits, int tid) {
-  if (tid >= (1 << (2 * bits))) return;
+// c: centroid `lane` in every lane of the warp.
+__device__ __forceinline__ void build_lut(uint32_t lut, int copies, float c, int bits, int tid) {
   const float inv = inv_sqrt_dim(kDim);
-  const uint32_t v = half2_bits(__ldg(cent + (tid & ((1 << bits) - 1))) * inv, __ldg(cent + (tid >> bits)) * inv);
-  for (int i = 0; i < copies; i += 4) sts16(lut + 4u * (tid * copies + i), v, v, v, v);
+  const float lo = __shfl_sync(0xFFFFFFFFu, c, tid & ((1 << bits) - 1)), hi = __shfl_sync(0xFFFFFFFFu, c, (tid >> bits) & 31);
+  if (tid >= (1 << (2 * bits))) return;
+  const uint32_t v = half2_bits(lo * inv, hi * inv);
+  // (each lane begins at another copy: side by side they would meet in one bank)
+  for (int i = 0; i < copies; i += 4) sts16(lut + 4u * (tid * copies + ((i + 4 * tid) & (copies - 1))), v, v, v, v);
 }
 
 // Where the two tables lie, and the slots.  24 KB are set aside: fp8 keys and INT4 values use
@@ -748,12 +746,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   Tables tables;
   if (T.k_fmt == KVQ_FMT_CODEBOOK && warp < 16) {
     const int lane = threadIdx.x & 31;
-    bool same = T.k_bits == T.v_bits;  // the same table for keys and values (often so)
-    if (same) same = lane >= (1 << T.k_bits) || __ldg(T.k_cent + lane) == __ldg(T.v_cent + lane);
-    same = __all_sync(0xFFFFFFFFu, same);
+    const float kc = lane < (1 << T.k_bits) ? __ldg(T.k_cent + lane) : 0.f;
+    const float vc = lane < (1 << T.v_bits) ? __ldg(T.v_cent + lane) : 0.f;
+    // the same table for keys and values (often so)
+    const bool same = T.k_bits == T.v_bits && __all_sync(0xFFFFFFFFu, kc == vc);
     tables = place_tables(smem, T.k_bits, T.v_bits, same, both);
-    if (warp < 8) build_lut(tables.at[0], tables.copies[0], T.k_cent, T.k_bits, threadIdx.x);
-    else if (tables.at[1] != tables.at[0]) build_lut(tables.at[1], tables.copies[1], T.v_cent, T.v_bits, threadIdx.x - 256);
+    if (warp < 8) build_lut(tables.at[0], tables.copies[0], kc, T.k_bits, threadIdx.x);
+    else if (!same) build_lut(tables.at[1], tables.copies[1], vc, T.v_bits, threadIdx.x - 256);
   }
   tc_fence_before();
   __syncthreads();
@@ -1053,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         __syncwarp();
         if (i + 2 < jobs) ok = scores(i + 2);
       }
-    } else if (warp == 17) {
+    } else {
       // ---- look-ups
       Pages s;
       s.table = T.block_table + (size_t)g * T.max_pages;
@@ -1065,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       s.end = len;
       const bool codes = T.k_fmt == KVQ_FMT_CODEBOOK;
       look_up(s, codes ? T.k_aux : nullptr, codes ? T.v_aux : nullptr, T.v_fmt == KVQ_FMT_INT4_G32 ? T.v_aux : nullptr,
-              smem, bars, tile0, n, abort, p.err);
+              smem, bars, tile0, n, warp - 17, abort, p.err);
     }
   }
   __syncwarp();
