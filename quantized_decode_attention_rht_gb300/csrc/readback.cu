@@ -7,7 +7,12 @@
 // on those, and each run is stored with the signs and 1 / sqrt(D) applied.  Stage order does
 // not matter (the stages commute), so no exchange between lanes is needed beyond the one
 // transpose.  Codebook centroids come from a 16-entry shared table: 16 words in 16 banks, so
-// a warp's lookups never conflict whatever the codes.
+// a warp's lookups never conflict whatever the codes.  Four blocks of 256 threads an SM (64
+// registers; three, at 80, took 98.7 us instead of 93.9 for 65536 tokens x 8 heads of fp8 keys and
+// INT4 values, 59% of the measured copy rate).  What bounds it is the shared-memory pipe: per
+// vector of 128 coordinates, 8 wavefronts of transpose, 4 of table look-ups and 2 to 3 of rows
+// in and out, against 14 cycles of an SM's share of the memory rate.  (Prefetching the next
+// vector's row into L2 cost more than it hid: 102 us.)
 #include <algorithm>
 
 #include "api_checks.cuh"
@@ -139,7 +144,7 @@ __device__ __forceinline__ void decode_row(const ReadSide& s, size_t prow, int s
 }
 
 template <int TPV, bool EXTRA>
-__global__ void __launch_bounds__(kThreads, EXTRA ? 2 : 3) read_kernel(const ReadParams p) {
+__global__ void __launch_bounds__(kThreads, EXTRA ? 2 : 4) read_kernel(const ReadParams p) {
   constexpr int D = 32 * TPV, R = 32 / TPV, VPB = kThreads / TPV;
   extern __shared__ __align__(16) float area_all[];  // D floats per vector of the block
   __shared__ float cent[16];
@@ -254,7 +259,7 @@ template <int TPV>
 cudaError_t launch_read(const ReadParams& p, int sides, int sms, cudaStream_t stream) {
   constexpr int VPB = kThreads / TPV;
   const long long nvec = (long long)p.num_tokens * p.hkv;
-  const long long blocks = std::max<long long>(1, std::min<long long>((nvec + VPB - 1) / VPB, sms * 3LL / sides));
+  const long long blocks = std::max<long long>(1, std::min<long long>((nvec + VPB - 1) / VPB, sms * 4LL / sides));
   const dim3 grid((unsigned)blocks, sides);
   const int kf = p.kind_first == 0 ? p.side[0].fmt : KVQ_FMT_CODEBOOK;
   if (kf == KVQ_FMT_CODEBOOK_QJL || kf == KVQ_FMT_CODEBOOK_OUTLIER)

@@ -86,14 +86,20 @@ __global__ void __launch_bounds__(512) rope_kernel(const RopeApply p) {
     }
   }
   for (int i = threadIdx.x; i < nt * pairs; i += blockDim.x) {
-    const int t = i / pairs;
-    cs[i] = rope_cos_sin(p.rope, i - t * pairs, __ldg(p.rope.positions + t0 + t));
+    const int t = i / pairs, j = i - t * pairs;
+    cs[t * pairs + (j % V) * p.rot_units + j / V] = rope_cos_sin(p.rope, j, __ldg(p.rope.positions + t0 + t));
   }
   __syncthreads();
+  float2 k[V];
+  int held = -1;  // the unit (of which token) whose coefficients k holds
   for (int i = threadIdx.x; i < total;) {
     if (live) {
       if (c < p.rot_units) {
-        const float2* k = cs + tl * pairs + c * V;
+        if (const int unit = tl * pairs + c; unit != held) {
+          held = unit;
+#pragma unroll
+          for (int e = 0; e < V; ++e) k[e] = cs[tl * pairs + e * p.rot_units + c];
+        }
         if constexpr (HALF) {
 #pragma unroll
           for (int e = 0; e < V; ++e) {
@@ -179,11 +185,14 @@ cudaError_t launch_rope(const RopeParams& rope, const kvq_heads* a, const kvq_he
   p.share = (int)((units + parts - 1) / parts);
   parts = (units + p.share - 1) / p.share;
   const long long work = (long long)p.per_block * p.share;
-  const long long passes = (work + 511) / 512;
-  const int threads = (int)std::min<long long>(512, ((work + passes - 1) / passes + 31) / 32 * 32);
+  // about four units a thread where there is work for all SMs, else one
+  const long long each = blocks * parts >= 4LL * sms ? 4 : 1;
+  long long threads = std::min<long long>(512, std::max<long long>(64, (work + each - 1) / each));
+  threads = (threads + 31) / 32 * 32;
+  while (threads + 32 <= 512 && threads % p.head_units != 0 && p.head_units <= 64) threads += 32;
   const size_t smem = (size_t)p.per_block * (rope.rot / 2) * sizeof(float2);
   const dim3 grid((unsigned)blocks, (unsigned)parts);
-  return wide ? launch_rope_v<8>(p, grid, threads, smem, stream) : launch_rope_v<1>(p, grid, threads, smem, stream);
+  return wide ? launch_rope_v<8>(p, grid, (int)threads, smem, stream) : launch_rope_v<1>(p, grid, (int)threads, smem, stream);
 }
 
 kvq_status check_rope(const kvq_rope* rope, int head_dim) {
