@@ -511,7 +511,6 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
   p.num_groups = num_groups;
   p.num_blocks = plan.num_blocks;
   p.total_splits = plan.total_splits;
-  p.num_items = plan.num_blocks * hkv * plan.total_splits;
   for (int g = 0; g <= num_groups; ++g) {
     p.offset[g] = group_offsets[g];
     p.block[g] = plan.block[g];
@@ -539,8 +538,9 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
                  own.tier[i].split_begin};
   for (int g = 0; g <= num_groups; ++g) j.offset[g] = group_offsets[g];
   e = cudaMemsetAsync(counters, 0, 256, s);  // work counters and the error word
-  if (e == cudaSuccess && p.num_items > 0) e = launch_shared_prefix(p, s);
-  if (e == cudaSuccess && num_tiers > 0) e = launch_own(own, plan.dec, d, group, counters, p.num_items > 0, s);
+  const bool prefix = plan.num_blocks > 0 && plan.total_splits > 0;
+  if (e == cudaSuccess && prefix) e = launch_shared_prefix(p, s);
+  if (e == cudaSuccess && num_tiers > 0) e = launch_own(own, plan.dec, d, group, counters, prefix, s);
   if (e == cudaSuccess) {
     // eight warps a row where a row has many partials (one warp would wait for them in turn)
     const bool many = 2 * plan.total_splits + plan.dec.total > 24;

@@ -19,6 +19,7 @@ struct SharedTier {
   int k_fmt, v_fmt, k_bits, v_bits, k_row_bytes, v_row_bytes;
   int num_pages, max_pages;
   int split_begin, num_splits;
+  int first;  // first split of the tier in its launch
 };
 
 struct SharedParams {
@@ -30,7 +31,7 @@ struct SharedParams {
   float* ml;         // (max, sum) [2 * splits][batch * hq][2]
   int* err;
   int batch, hq, hkv, group, page_size, page_shift;
-  int total_splits, num_items, num_blocks;  // num_blocks: row blocks of all groups
+  int total_splits, num_blocks;           // num_blocks: row blocks of all groups
   int offset[KVQ_MAX_PREFIX_GROUPS + 1];    // first sequence of each group
   int block[KVQ_MAX_PREFIX_GROUPS + 1];     // first row block of each group
 };

@@ -13,7 +13,7 @@
 //   4 + 4 decoding warps: K and V tiles of 128 tokens, read from the packed cache into
 //     registers two tiles ahead, decoded to fp16 into shared memory (128-byte swizzle)
 //   1 warp: issues the products and allocates TMEM
-//   3 warps: look up page numbers, rows, norms and scales, up to four tiles ahead.
+//   2 warps: look up page numbers, rows, norms and scales, up to four tiles ahead.
 // Both products are tcgen05.mma of 128 x 128 x 16 steps: S = q~ K^T from shared memory, O += P V
 // with P read from TMEM (it overwrites S) and V as it lies (tokens x coordinates, the
 // MN-major form).  The two softmax groups alternate, so that one's products run while the
@@ -25,11 +25,16 @@
 // more than 2^14 in some row of a warp, which after the first tile is rare: until then
 // weights stay inside fp16 and the sums, in float32, inside their range.
 //
-// Rounded to fp16 on the way, each a half-ulp of 2^-11: the rotated queries, the decoded keys
-// and values where their format is not exact in fp16 (fp16 and fp8 are; INT4 levels times
-// their scale and centroids times their norm are not), the weights.  fp16 is what the tensor
-// cores multiply at full rate; the output is fp16, and none of these errors is larger than
-// its own rounding.  Scores, maxima, sums and accumulators are float32.
+// Rounded to fp16 on the way, each by at most 2^-11 of itself: the rotated queries, the weights,
+// INT4 levels times their scale, value centroids times their norm, and the centroids
+// themselves.  fp16 is what the tensor cores multiply at full rate.  Scores, maxima, sums and
+// accumulators are float32.  Two things keep the codebook formats as exact as the others, whose
+// keys are fp16 values already: a centroid's rounding is the same in every coordinate that has
+// its code, which with an outlier channel is nearly all of them, so the table is scaled by the
+// factor out of 256 whose roundings are smallest (undone in float32); and a key's norm
+// multiplies its scores, in float32, in place of its coordinates.  (On caches with x30 outlier
+// channels the 2-norm of the output's error falls from 2.3e-3 to 7e-4 of the output's; fp8
+// keys: 6e-4.)
 //
 // Every wait has a limit: a block whose wait runs out sets KVQ_DEVERR_COPY_TIMEOUT and ends.
 #include <atomic>
@@ -52,10 +57,10 @@ constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kStages * kTile
 constexpr int kOffLut = kOffV + kStages * kTileBytes, kLutBytes = 24 << 10;
 constexpr int kAhead = 4;
 constexpr int kOffRow = kOffLut + kLutBytes, kRowBytes = kTileTokens * 4;                       // a tile
-// (keys: a 4-byte norm a token; values: a norm, or four scales in 8 bytes)
+// (keys: a float32 norm a token; values: a norm, or four scales, in 8 bytes)
 constexpr int kOffKAux = kOffRow + kAhead * kRowBytes, kOffVAux = kOffKAux + kAhead * kTileTokens * 4;
 constexpr int kOffCtl = kOffVAux + kAhead * kTileTokens * 8;
-constexpr int kSmem = kOffCtl + 256 + 1024;  // 1024: the base is aligned by hand
+constexpr int kSmem = kOffCtl + 512 + 1024;  // 1024: the base is aligned by hand
 static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 
 // barriers, in units of 8 bytes from kOffCtl
@@ -83,8 +88,11 @@ struct Ctl {
   unsigned long long bars[B_COUNT];
   uint32_t tmem;
   int abort;
+  float best[2][4];    // per side and warp: a table scale's error, and
+  int best_at[2][4];   // which it is
+  float unscale[2];    // what a side's table values are to be multiplied by
 };
-static_assert(sizeof(Ctl) <= 256, "control block");
+static_assert(sizeof(Ctl) <= 512, "control block");
 
 // Waits for a phase; false once the block has given up (two seconds for any one wait).
 __device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* err) {
@@ -231,8 +239,8 @@ struct Source {
   const uint8_t* rows;
   int row_bytes;
   uint32_t raw;               // shared addresses: the threads' slots;
-  uint32_t rowbuf, auxbuf;    // kAhead tiles of rows; of this side's norms or scales
-  uint32_t aux_shift;         // log2 of the latter's bytes a token
+  uint32_t rowbuf, auxbuf;    // kAhead tiles of rows; of the values' norms or scales
+  bool keys;
   uint32_t lut, lut_stride;   // the lane's copy of entry 0, bytes between entries (codebooks)
 };
 // What the look-ups read.
@@ -294,15 +302,24 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// The codebooks' tables are made: the eight decoding warps and the look-up warps meet once
+// (320 = 256 + 32 kLookUps threads).
+__device__ __forceinline__ void tables_made() { asm volatile("bar.sync 3, 320;" ::: "memory"); }
+
 // Look-up warp `first` of kLookUps, which take tiles in turn (a look-up is a chain of three
 // loads, longer than a tile's products): rows of a tile's tokens, then their norms (codebooks) or
-// group scales (INT4 values).  Page numbers are read a turn ahead.
-constexpr int kLookUps = 3;
+// group scales (INT4 values).  Page numbers are read a turn ahead.  kLookUps divides kAhead, so
+// that a stage belongs to one warp, which waits for every one of its releases: the softmax groups
+// release stages out of order, and a warp that waited only for some of them could take one
+// phase of the barrier for the one before the last.
+constexpr int kLookUps = 2;
+static_assert(kAhead % kLookUps == 0, "a stage's releases are waited for by one warp");
 __device__ __forceinline__ void look_up(const Pages& s, const __half* k_norm, const __half* v_norm,
-                                        const __half* v_scale, uint32_t smem, uint32_t bars, int tile0, int n, int first,
+                                        const __half* v_scale, volatile float* unscale, uint32_t smem, uint32_t bars, int tile0, int n, int first,
                                         volatile int* abort, int* err) {
   const int lane = threadIdx.x & 31;
   int bits = 0;
+  float key_unit = 0.f;  // of the keys' table (known once the tables are made)
   int page[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) page[j] = first < n ? page_of(s, (tile0 + first) * kTileTokens + lane + 32 * j) : -1;
@@ -333,12 +350,18 @@ __device__ __forceinline__ void look_up(const Pages& s, const __half* k_norm, co
 #pragma unroll
       for (int j = 0; j < 4; ++j) page[j] = page_of(s, t0 + kLookUps * kTileTokens + 32 * j);
     }
+    if (k_norm && i == first) {
+      tables_made();
+      key_unit = unscale[0];
+    }
     const uint32_t ka = smem + kOffKAux + at * kTileTokens * 4 + 4 * lane;
     const uint32_t va = smem + kOffVAux + at * kTileTokens * 8 + 8 * lane;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (k_norm) {
-        sts32(ka + 128 * j, aux[j].x);
+        // (1 for a token that is not there: its score, -inf, stays that)
+        const float norm = __half2float(__ushort_as_half((uint16_t)aux[j].x)) * key_unit;
+        sts32(ka + 128 * j, __float_as_uint(row[j] != kNoRow ? norm : 1.0f));
         sts32(va + 256 * j, aux[j].y);
       } else if (v_scale) {
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(va + 256 * j), "r"(aux[j].x), "r"(aux[j].y) : "memory");
@@ -346,6 +369,7 @@ __device__ __forceinline__ void look_up(const Pages& s, const __half* k_norm, co
     }
     bar_arrive(bars + 8 * (B_AUX + at));
   }
+  if (k_norm && key_unit == 0.f) tables_made();  // (no tile, or none that got so far)
   if (bits) atomicOr(err, bits);
 }
 
@@ -444,6 +468,92 @@ __device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, int 
   }
 }
 
+// The scale of a codebook's table, out of 2^(k / 256) / 16, k < 256: the one whose fp16 roundings
+// are smallest, by the sum of squares of their relative errors.  c: centroid `lane` in every
+// lane (0 beyond the codebook); the side's four warps, which share the candidates.
+__device__ __forceinline__ float scale_table(Ctl* ctl, float c, int bits, int side, int tid) {
+  const int lane = tid & 31, warp = tid >> 5;
+  float least = INFINITY;
+  int at = 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int k = 2 * tid + j;
+    const float beta = exp2f((float)k * (1.0f / 256.0f)) * 0.0625f;
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < (1 << bits); ++i) {
+      const float x = __shfl_sync(0xFFFFFFFFu, c, i) * beta;
+      const float off = x != 0.f ? __fdividef(__half2float(__float2half_rn(x)) - x, x) : 0.f;
+      sum = fmaf(off, off, sum);
+    }
+    if (sum < least) {
+      least = sum;
+      at = k;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, least, o);
+    const int k = __shfl_xor_sync(0xFFFFFFFFu, at, o);
+    if (other < least || (other == least && k < at)) {
+      least = other;
+      at = k;
+    }
+  }
+  if (lane == 0) {
+    ctl->best[side][warp] = least;
+    ctl->best_at[side][warp] = at;
+  }
+  if (side == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
+  else asm volatile("bar.sync 2, 128;" ::: "memory");
+  for (int i = 0; i < 4; ++i) {
+    const float other = ctl->best[side][i];
+    const int k = ctl->best_at[side][i];
+    if (other < least || (other == least && k < at)) {
+      least = other;
+      at = k;
+    }
+  }
+  const float beta = exp2f((float)at * (1.0f / 256.0f)) * 0.0625f;
+  if (tid == 0) ctl->unscale[side] = inv_sqrt_dim(kDim) / beta;
+  return beta;
+}
+
+// Pairs of scaled centroids in fp16: entry e = codes (e mod 2^b, e / 2^b), in copies, one per
+// lane where there is room (a warp's look-ups then never meet in a bank), else 16 or 8 of them
+// (two or three bank rounds a look-up).  tid: 128 threads; c as above, times the scale.
+__device__ __forceinline__ void build_lut(uint32_t lut, int copies, float c, int bits, int tid) {
+  for (int e = tid; e < max(128, 1 << (2 * bits)); e += 128) {  // (whole warps: the shuffles need them)
+    const float lo = __shfl_sync(0xFFFFFFFFu, c, e & ((1 << bits) - 1)), hi = __shfl_sync(0xFFFFFFFFu, c, (e >> bits) & 31);
+    if (e >= (1 << (2 * bits))) break;
+    const uint32_t v = half2_bits(lo, hi);
+    // (each lane begins at another copy: side by side they would meet in one bank)
+    for (int i = 0; i < copies; i += 4) sts16(lut + 4u * (e * copies + ((i + 4 * e) & (copies - 1))), v, v, v, v);
+  }
+}
+
+// Where the two tables lie, and the slots.  24 KB are set aside: fp8 keys and INT4 values use
+// them for slots alone (16 and 8 KB).  With up to 128 rows the second query tile is free as
+// well: the tables go there (one of 32 copies where keys and values have the same, else 16
+// copies each), and the slots, four passes a side, have the 24 KB.  With more rows both share
+// them: 16 KB of tables (16 copies of one, or 8 of each), 4 KB of slots a side.
+struct Tables {
+  uint32_t at[2], raw[2];
+  int copies[2];
+};
+__device__ __forceinline__ Tables place_tables(uint32_t smem, int k_bits, int v_bits, bool same, bool both) {
+  const uint32_t lut = smem + kOffLut, spare = smem + kOffQ + kTileBytes;
+  Tables t;
+  const int of_1kb = (both ? 16 : 8) << (same ? 1 : 0);
+  t.copies[0] = k_bits == 4 ? of_1kb : 32;  // (smaller tables: 8 KB at most)
+  t.copies[1] = v_bits == 4 ? of_1kb : 32;
+  t.at[0] = both ? spare : lut;
+  t.at[1] = t.at[0] + (same ? 0 : (both ? 16 << 10 : 8 << 10));
+  t.raw[0] = both ? lut : lut + (16 << 10);
+  t.raw[1] = t.raw[0] + (both ? 8 << 10 : 4 << 10);
+  return t;
+}
+
 // The side's n tiles, into the ring.  A thread's units travel by asynchronous copies into slots
 // of its own (nobody else waits for them), `slots` passes ahead, a slot being requested anew as
 // soon as it is taken.  The loop stays rolled, a pass of 32 values or two of 16 a turn: warps of
@@ -471,10 +581,10 @@ __device__ __forceinline__ void produce(const Source& s, const Ring& ring, int n
     const int st = i & 1, at = i % kAhead, after = (i + 1) % kAhead;
     const bool more = i + 1 < n;
     if (more && !bar_wait(ring.rows + 8 * after, ((i + 1) / kAhead) & 1, abort, err)) break;
-    if (F >= D_I4 && !bar_wait(ring.aux + 8 * at, (i / kAhead) & 1, abort, err)) break;
+    if (F >= D_I4 && !s.keys && !bar_wait(ring.aux + 8 * at, (i / kAhead) & 1, abort, err)) break;
     if (i >= kStages && !bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err)) break;
     if (i == 1 && ring.first_use && !bar_wait(ring.first_use, 0, abort, err)) break;
-    const uint32_t tile = ring.tiles + st * kTileBytes, aux = s.auxbuf + ((uint32_t)(at * kTileTokens) << s.aux_shift);
+    const uint32_t tile = ring.tiles + st * kTileBytes, aux = s.auxbuf + (uint32_t)(at * kTileTokens * 8);
     uint32_t slot = slot0;
 #pragma unroll 1
     for (int p = 0; p < kPasses; p += kTurn) {
@@ -493,8 +603,8 @@ __device__ __forceinline__ void produce(const Source& s, const Ring& ring, int n
         if constexpr (F >= D_I4) {
           uint16_t v;
           place<F>(p, tid, t, u);
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(aux + ((uint32_t)t << s.aux_shift) + (F == D_I4 ? 2u * u : 0u)));
-          scale = v;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(aux + 8u * t + (F == D_I4 ? 2u * u : 0u)));
+          scale = s.keys ? 0x3C00u : v;  // (a key's norm multiplies its scores: here 1)
         }
       }
 #pragma unroll
@@ -551,24 +661,21 @@ __device__ __forceinline__ void produce<D_F16, 1>(const Source& s, const Ring& r
 }
 
 // deep: there is room for a whole tile's units of a codebook side
+template <bool CODES>
 __device__ __forceinline__ void produce_any(int f, bool deep, const Source& s, const Ring& ring, int n, int tid,
                                             volatile int* abort, int* err) {
-  switch (f) {
-    case D_F16: produce<D_F16, 1>(s, ring, n, tid, abort, err); break;
-    case D_F8: produce<D_F8, 8>(s, ring, n, tid, abort, err); break;
-    case D_I4: produce<D_I4, 4>(s, ring, n, tid, abort, err); break;
-    case D_CB4:
-      if (deep) produce<D_CB4, 4>(s, ring, n, tid, abort, err);
-      else produce<D_CB4, 2>(s, ring, n, tid, abort, err);
-      break;
-    case D_CB3:
-      if (deep) produce<D_CB3, 4>(s, ring, n, tid, abort, err);
-      else produce<D_CB3, 2>(s, ring, n, tid, abort, err);
-      break;
-    default:
-      if (deep) produce<D_CB2, 4>(s, ring, n, tid, abort, err);
-      else produce<D_CB2, 2>(s, ring, n, tid, abort, err);
-      break;
+  if constexpr (!CODES) {
+    if (f == D_F16) produce<D_F16, 1>(s, ring, n, tid, abort, err);
+    else if (f == D_F8) produce<D_F8, 8>(s, ring, n, tid, abort, err);
+    else produce<D_I4, 4>(s, ring, n, tid, abort, err);
+  } else if (deep) {
+    if (f == D_CB4) produce<D_CB4, 4>(s, ring, n, tid, abort, err);
+    else if (f == D_CB3) produce<D_CB3, 4>(s, ring, n, tid, abort, err);
+    else produce<D_CB2, 4>(s, ring, n, tid, abort, err);
+  } else {
+    if (f == D_CB4) produce<D_CB4, 2>(s, ring, n, tid, abort, err);
+    else if (f == D_CB3) produce<D_CB3, 2>(s, ring, n, tid, abort, err);
+    else produce<D_CB2, 2>(s, ring, n, tid, abort, err);
   }
 }
 
@@ -579,41 +686,6 @@ __device__ __forceinline__ int decode_kind(int fmt, int bits) {
     case KVQ_FMT_INT4_G32: return D_I4;
     default: return bits == 4 ? D_CB4 : (bits == 3 ? D_CB3 : D_CB2);
   }
-}
-
-// Pairs of centroids / sqrt(D) in fp16: entry e = codes (e mod 2^b, e / 2^b), in copies, one per
-// lane where there is room (a warp's look-ups then never meet in a bank), else 16 or 8 of them
-// (two or three bank rounds a look-up).  tid: 256 threads.
-// c: centroid `lane` in every lane of the warp.
-__device__ __forceinline__ void build_lut(uint32_t lut, int copies, float c, int bits, int tid) {
-  const float inv = inv_sqrt_dim(kDim);
-  const float lo = __shfl_sync(0xFFFFFFFFu, c, tid & ((1 << bits) - 1)), hi = __shfl_sync(0xFFFFFFFFu, c, (tid >> bits) & 31);
-  if (tid >= (1 << (2 * bits))) return;
-  const uint32_t v = half2_bits(lo * inv, hi * inv);
-  // (each lane begins at another copy: side by side they would meet in one bank)
-  for (int i = 0; i < copies; i += 4) sts16(lut + 4u * (tid * copies + ((i + 4 * tid) & (copies - 1))), v, v, v, v);
-}
-
-// Where the two tables lie, and the slots.  24 KB are set aside: fp8 keys and INT4 values use
-// them for slots alone (16 and 8 KB).  With up to 128 rows the second query tile is free as
-// well: the tables go there (one of 32 copies where keys and values have the same, else 16
-// copies each), and the slots, four passes a side, have the 24 KB.  With more rows both share
-// them: 16 KB of tables (16 copies of one, or 8 of each), 4 KB of slots a side.
-struct Tables {
-  uint32_t at[2], raw[2];
-  int copies[2];
-};
-__device__ __forceinline__ Tables place_tables(uint32_t smem, int k_bits, int v_bits, bool same, bool both) {
-  const uint32_t lut = smem + kOffLut, spare = smem + kOffQ + kTileBytes;
-  Tables t;
-  const int of_1kb = (both ? 16 : 8) << (same ? 1 : 0);
-  t.copies[0] = k_bits == 4 ? of_1kb : 32;  // (smaller tables: 8 KB at most)
-  t.copies[1] = v_bits == 4 ? of_1kb : 32;
-  t.at[0] = both ? spare : lut;
-  t.at[1] = t.at[0] + (same ? 0 : (both ? 16 << 10 : 8 << 10));
-  t.raw[0] = both ? lut : lut + (16 << 10);
-  t.raw[1] = t.raw[0] + (both ? 8 << 10 : 4 << 10);
-  return t;
 }
 
 // ------------------------------------------------------------------------ softmax
@@ -656,6 +728,11 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 __device__ __forceinline__ float2 unpack2(unsigned long long r) {
   float2 f;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
@@ -663,6 +740,9 @@ __device__ __forceinline__ float2 unpack2(unsigned long long r) {
 }
 
 // ------------------------------------------------------------------------ the kernel
+// CODES: tiers of codebook formats, else of the others (a branch on the format in the softmax loop
+// made it a third slower for both).
+template <bool CODES>
 __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid_constant__ SharedParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -676,7 +756,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   int item = blockIdx.x;
   const int blk = item % p.num_blocks;
   item /= p.num_blocks;
-  const int hk = item % p.hkv, split = item / p.hkv;
+  const int hk = item % p.hkv;
+  int split = item / p.hkv;
   int lo = 0, hi = p.num_groups;  // the group whose row blocks hold blk
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -687,14 +768,15 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   const int rows = (p.offset[g + 1] - p.offset[g]) * p.group - lb * kItemRows;  // > 0
   const bool both = rows <= kTileRows;  // both softmax groups on the same rows
   int ti = 0;
-  while (ti + 1 < p.num_tiers && split >= p.tier[ti + 1].split_begin) ++ti;
+  while (ti + 1 < p.num_tiers && split >= p.tier[ti + 1].first) ++ti;
   const SharedTier& T = p.tier[ti];
+  split -= T.first;  // of the tier's
   int bits = 0;
   const int len = checked_len(__ldg(T.lens + g), T.max_pages, p.page_size, &bits);
   if (bits && threadIdx.x == 0) atomicOr(p.err, bits);
   const int all = (len + kTileTokens - 1) / kTileTokens;
   const int per = (all + T.num_splits - 1) / T.num_splits;
-  const int tile0 = min((split - T.split_begin) * per, all), tile1 = min(tile0 + per, all);
+  const int tile0 = min(split * per, all), tile1 = min(tile0 + per, all);
   const int n = tile1 - tile0;
   const int jobs = both ? n : 2 * n;  // job i: softmax group i & 1, tile both ? i : i / 2
 
@@ -707,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     out_row = (long long)(p.offset[g] + i) * p.hq + hk * p.group + (gr - i * p.group);
   }
   const size_t out_rows = (size_t)p.batch * p.hq;
-  const size_t part = (2 * (size_t)split + (both ? w : 0)) * out_rows;
+  const size_t part = (2 * (size_t)(T.split_begin + split) + (both ? w : 0)) * out_rows;
 
   if (n == 0) {  // no tokens: partials of weight zero
     if (out_row >= 0) *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) = make_float2(-INFINITY, 0.f);
@@ -734,7 +816,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     for (int i = 0; i < kAhead; ++i) {
       bar_init(bars + 8 * (B_ROWS + i), 32);
       bar_init(bars + 8 * (B_AUX + i), 32);
-      bar_init(bars + 8 * (B_ROWS_READ + i), 256);
+      // the decoding threads, and (norms of keys) the softmax warps that read the tile's scores
+      bar_init(bars + 8 * (B_ROWS_READ + i), 256 + (CODES ? (min(rows, kItemRows) + 31) / 32 : 0));
     }
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -742,17 +825,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  Tables tables;
-  if (T.k_fmt == KVQ_FMT_CODEBOOK && warp < 16) {
-    const int lane = threadIdx.x & 31;
-    const float kc = lane < (1 << T.k_bits) ? __ldg(T.k_cent + lane) : 0.f;
-    const float vc = lane < (1 << T.v_bits) ? __ldg(T.v_cent + lane) : 0.f;
-    // the same table for keys and values (often so)
-    const bool same = T.k_bits == T.v_bits && __all_sync(0xFFFFFFFFu, kc == vc);
-    tables = place_tables(smem, T.k_bits, T.v_bits, same, both);
-    if (warp < 8) build_lut(tables.at[0], tables.copies[0], kc, T.k_bits, threadIdx.x);
-    else if (!same) build_lut(tables.at[1], tables.copies[1], vc, T.v_bits, threadIdx.x - 256);
   }
   tc_fence_before();
   __syncthreads();
@@ -849,7 +921,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       for (int k = 0; k < my_jobs && ok; ++k) {
         const int i = 2 * k + w, tile = tile0 + (both ? i : i >> 1);
         const int valid = min(kTileTokens, len - tile * kTileTokens);
-        if (!(ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * (B_SFULL + w), k & 1, abort, p.err)))) break;
+        const int local = both ? i : i >> 1, at = local % kAhead;
+        const float* norm = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(ctl) - kOffCtl + kOffKAux) + at * kTileTokens;
+        ok = bar_wait(bars + 8 * (B_SFULL + w), k & 1, abort, p.err);
+        if (CODES) ok = ok && bar_wait(bars + 8 * (B_AUX + at), (local / kAhead) & 1, abort, p.err);
+        if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
         tc_fence_after();
         // Half a tile's weights at a time, against the running maximum as it is, in registers: no
         // maximum is taken.  All weights are positive, so a sum of at most kMostWeight says that
@@ -870,12 +946,23 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
                   if (c0 + c + e >= valid) v[e] = 0xFF800000u;  // -inf: weight 0
               }
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float2 x = unpack2(add2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), neg));
-                const float a = ex2(x.x), b = ex2(x.y);
-                if (e & 1) s1 = add2(s1, pack2(a, b));
-                else s0 = add2(s0, pack2(a, b));
-                h[c / 2 + e] = half2_bits(a, b);
+              for (int e = 0; e < 32; e += 4) {
+                unsigned long long t0 = pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                unsigned long long t1 = pack2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+                if constexpr (CODES) {  // scores are multiplied by the keys' norms
+                  const float4 n = *reinterpret_cast<const float4*>(norm + c0 + c + e);
+                  t0 = fma2(t0, pack2(n.x, n.y), neg);
+                  t1 = fma2(t1, pack2(n.z, n.w), neg);
+                } else {
+                  t0 = add2(t0, neg);
+                  t1 = add2(t1, neg);
+                }
+                const float2 x = unpack2(t0), y = unpack2(t1);
+                const float a = ex2(x.x), b = ex2(x.y), d = ex2(y.x), f = ex2(y.y);
+                s0 = add2(s0, pack2(a, b));
+                s1 = add2(s1, pack2(d, f));
+                h[(c + e) / 2] = half2_bits(a, b);
+                h[(c + e) / 2 + 1] = half2_bits(d, f);
               }
             };
             uint32_t va[32], vb[32];
@@ -896,7 +983,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
               tc_wait_ld(x);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (c + e < valid) mx = fmaxf(mx, __uint_as_float(x[e]));
+                if (c + e < valid)
+                  mx = fmaxf(mx, __uint_as_float(x[e]) * (CODES ? norm[c + e] : 1.f));
             }
             const float f = ex2(m - mx);
             m = mx;
@@ -914,6 +1002,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
             tc_st16(s_at + c0 / 2 + c, part);
           }
         }
+        if constexpr (CODES) {
+          __syncwarp();
+          if ((threadIdx.x & 31) == 0) bar_arrive(bars + 8 * (B_ROWS_READ + at));
+        }
         tc_wait_st();
         tc_fence_before();
         bar_arrive(bars + 8 * (B_PREADY + w));
@@ -927,12 +1019,17 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         const bool last = ((jobs - 1) & 1) == w;
         const int lane = threadIdx.x & 31;
         const uint32_t stage = smem + (last ? kOffV : kOffK) + (warp & 3) * (32 * kDim * 4);
+        const float value_unit = CODES ? *reinterpret_cast<volatile float*>(&ctl->unscale[1]) : 1.f;
         const bool int4 = T.v_fmt == KVQ_FMT_INT4_G32;  // columns 0 4 1 5 2 6 3 7 of every eight
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t v[32];
           tc_ld32(o_at + 32 * c, v);
           tc_wait_ld(v);
+          if constexpr (CODES) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * value_unit);
+          }
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             const uint32_t o1 = int4 ? v[e + 2] : v[e + 1], o2 = int4 ? v[e + 4] : v[e + 2];
@@ -968,17 +1065,25 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     Source s;
     s.rows = keys ? T.k_rows : T.v_rows;
     s.row_bytes = keys ? T.k_row_bytes : T.v_row_bytes;
-    if (T.k_fmt == KVQ_FMT_CODEBOOK) {
-      const int side = keys ? 0 : 1;
-      s.lut = tables.at[side] + 4u * (threadIdx.x & (tables.copies[side] - 1));
+    if constexpr (CODES) {  // (while the look-up warps find the first rows)
+      const int side = keys ? 0 : 1, tid = threadIdx.x & 127, lane = threadIdx.x & 31;
+      const float kc = lane < (1 << T.k_bits) ? __ldg(T.k_cent + lane) : 0.f;
+      const float vc = lane < (1 << T.v_bits) ? __ldg(T.v_cent + lane) : 0.f;
+      const bool same = T.k_bits == T.v_bits && __all_sync(0xFFFFFFFFu, kc == vc);  // one table (often so)
+      const Tables tables = place_tables(smem, T.k_bits, T.v_bits, same, both);
+      const int bits = keys ? T.k_bits : T.v_bits;
+      const float beta = scale_table(ctl, keys ? kc : vc, bits, side, tid);
+      if (keys || !same) build_lut(tables.at[side], tables.copies[side], (keys ? kc : vc) * beta, bits, tid);
+      tables_made();
+      s.lut = tables.at[side] + 4u * (tid & (tables.copies[side] - 1));
       s.lut_stride = 4u * tables.copies[side];
       s.raw = tables.raw[side];
     } else {
       s.raw = smem + kOffLut + (keys ? 0 : 16 << 10);
     }
     s.rowbuf = smem + kOffRow;
-    s.auxbuf = smem + (keys ? kOffKAux : kOffVAux);
-    s.aux_shift = keys ? 2 : 3;
+    s.auxbuf = smem + kOffVAux;
+    s.keys = keys;
     Ring ring;
     ring.tiles = smem + (keys ? kOffK : kOffV);
     ring.full = bars + 8 * (keys ? B_KFULL : B_VFULL);
@@ -987,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     ring.aux = bars + 8 * B_AUX;
     ring.rows_read = bars + 8 * B_ROWS_READ;
     ring.first_use = keys ? 0 : bars + 8 * B_QROT;  // the second value stage first holds the rotation
-    produce_any(keys ? decode_kind(T.k_fmt, T.k_bits) : decode_kind(T.v_fmt, T.v_bits), both, s, ring, n,
+    produce_any<CODES>(keys ? decode_kind(T.k_fmt, T.k_bits) : decode_kind(T.v_fmt, T.v_bits), both, s, ring, n,
                 threadIdx.x & 127, abort, p.err);
   } else {
     // ---- products
@@ -1052,7 +1157,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         __syncwarp();
         if (i + 2 < jobs) ok = scores(i + 2);
       }
-    } else {
+    } else if (warp < 17 + kLookUps) {
       // ---- look-ups
       Pages s;
       s.table = T.block_table + (size_t)g * T.max_pages;
@@ -1062,9 +1167,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       s.hkv = p.hkv;
       s.hk = hk;
       s.end = len;
-      const bool codes = T.k_fmt == KVQ_FMT_CODEBOOK;
-      look_up(s, codes ? T.k_aux : nullptr, codes ? T.v_aux : nullptr, T.v_fmt == KVQ_FMT_INT4_G32 ? T.v_aux : nullptr,
-              smem, bars, tile0, n, warp - 17, abort, p.err);
+      look_up(s, CODES ? T.k_aux : nullptr, CODES ? T.v_aux : nullptr, T.v_fmt == KVQ_FMT_INT4_G32 ? T.v_aux : nullptr,
+              ctl->unscale, smem, bars, tile0, n, warp - 17, abort, p.err);
     }
   }
   __syncwarp();
@@ -1082,22 +1186,46 @@ bool shared_tier_supported(int head_dim, int k_fmt, int v_fmt) {
   return k_fmt == KVQ_FMT_CODEBOOK && v_fmt == KVQ_FMT_CODEBOOK;
 }
 
-cudaError_t launch_shared_prefix(const SharedParams& p, cudaStream_t stream) {
-  if (p.num_items == 0) return cudaSuccess;
-  static std::atomic<bool> configured[64];  // shared-memory limit raised on this device
+namespace {
+
+template <bool CODES>
+cudaError_t launch_kind(const SharedParams& all, cudaStream_t stream) {
+  SharedParams p = all;
+  p.num_tiers = 0;
+  int splits = 0;
+  for (int i = 0; i < all.num_tiers; ++i) {
+    if ((all.tier[i].k_fmt == KVQ_FMT_CODEBOOK) != CODES) continue;
+    SharedTier& t = p.tier[p.num_tiers++];
+    t = all.tier[i];
+    t.first = splits;
+    splits += t.num_splits;
+  }
+  const long long items = (long long)p.num_blocks * p.hkv * splits;
+  if (items == 0) return cudaSuccess;
+  auto kern = shared_prefix_kernel<CODES>;
+  static std::atomic<bool> configured[64];  // shared-memory limit raised on this device (a racing second
+                                           // raise is harmless)
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     configured[dev].store(true, std::memory_order_relaxed);
   }
-  shared_prefix_kernel<<<p.num_items, kThreads, kSmem, stream>>>(p);
+  kern<<<(unsigned)items, kThreads, kSmem, stream>>>(p);
   e = cudaGetLastError();
   if (e == cudaSuccess) note_launch();
   return e;
+}
+
+}  // namespace
+
+// One launch per kind of tier.
+cudaError_t launch_shared_prefix(const SharedParams& p, cudaStream_t stream) {
+  const cudaError_t e = launch_kind<false>(p, stream);
+  return e == cudaSuccess ? launch_kind<true>(p, stream) : e;
 }
 
 }  // namespace kvq

@@ -157,6 +157,17 @@ def test_page_sizes(ps):
     c.check(c.run(kvq, torch))
 
 
+@pytest.mark.parametrize("name", ["cb4", "cb32", "fp8_int4", "fp16"])
+@pytest.mark.parametrize("batch,group", [(5, 1), (40, 4)])
+def test_long_chunks(name, batch, group):
+    """Work items of ten tiles and more, both ways of sharing them between the softmax groups: the
+    rings of tiles, rows and norms go round several times."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, [name], [[20000]], [0, batch], [name], [[3] * batch], hq=8 * group, hkv=8, seed=batch)
+    heads = {(b, h) for b, h in ((0, 0), (1, group), (batch - 1, 8 * group - 1), (batch // 2, 5 * group))}
+    c.check(c.run(kvq, torch), heads)
+
+
 def test_ragged_groups():
     """Groups of different sizes and lengths, one empty, one of length 0, sequences before the
     first group and behind the last, a sequence without a token."""
@@ -174,6 +185,14 @@ def test_tiers_of_the_prefix_and_of_the_sequences():
     torch, kvq = modules()
     c = Case(kvq, torch, ["fp16", "fp8_int4"], [[100, 0], [900, 260]], [0, 4, 7], ["fp8_int4", "fp16"],
              [[20, 0, 3, 200, 1, 7, 0], [0, 16, 16, 16, 2, 0, 0]], hq=8, hkv=2, seed=8)
+    c.check(c.run(kvq, torch))
+
+
+def test_codebook_and_other_tiers_of_one_prefix():
+    """Two kinds of prefix tier: a launch each."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["cb32", "fp16"], [[700, 90], [64, 16]], [0, 4, 7], ["cb4"], [[20, 0, 3, 200, 1, 7, 0]], hq=8,
+             hkv=2, seed=15)
     c.check(c.run(kvq, torch))
 
 
