@@ -26,6 +26,7 @@ FORMATS = {"codebook": FMT_CODEBOOK, "fp16": FMT_FP16, "fp8_e4m3": FMT_FP8_E4M3,
 QJL_DIM = 128
 OUTLIER_CHANNELS = 8
 MAX_TIERS = 4
+MAX_PREFIX_GROUPS = 256
 INT4_GROUP = 32
 
 STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_INVALID_ARGUMENT", 2: "KVQ_ERR_UNSUPPORTED",
@@ -426,20 +427,28 @@ def kvq_dequantize(cache: KvqCache, slots, k_out=None, v_out=None, stream=None) 
         raise KvqError(status, "kvq_dequantize")
 
 
-def _views(tiers: Sequence["TierView"], batch: int = 0):
-    """The tiers as the C ABI's array; `batch` > 0: the call reads that many rows of every
-    block table and entries of every length array."""
-    arr = (KvqTierView * len(tiers))()
-    for v, t in zip(arr, tiers):
+def _check_views(tiers: Sequence["TierView"], batch: int = 0) -> None:
+    """`batch` > 0: the call reads that many rows of every block table and entries of every
+    length array."""
+    for t in tiers:
         table, lens = t.block_table, t.seq_lens
         _dense(table, lens)
         _arg(table, "block_table", "int32", (None, None))
         _arg(lens, "seq_lens", "int32", (None,), min_numel=batch)
         if batch and table is not None and table.shape[0] < batch:
             raise ValueError(f"block_table has {table.shape[0]} rows for {batch} sequences")
+
+
+def _views(tiers: Sequence["TierView"], batch: int = 0, checked: bool = False):
+    """The tiers as the C ABI's array, checked first (see _check_views)."""
+    if not checked:
+        _check_views(tiers, batch)
+    arr = (KvqTierView * len(tiers))()
+    for v, t in zip(arr, tiers):
+        table = t.block_table
         v.cache = ctypes.pointer(t.cache.struct)
         v.block_table = _ptr(table)
-        v.seq_lens = _ptr(lens)
+        v.seq_lens = _ptr(t.seq_lens)
         v.max_pages = int(table.shape[1]) if table is not None else 0
     return arr
 
@@ -520,7 +529,9 @@ def kvq_decode_attention_shared(prefix_tiers, group_offsets, tiers, q, out, work
     if workspace is None or not getattr(workspace, "is_cuda", False):
         raise ValueError("workspace must be a CUDA tensor")
     b, hq = int(q.shape[0]), int(q.shape[1])
-    pre, own = _views(prefix_tiers, len(off) - 1), _views(tiers, b) if tiers else None
+    _check_views(prefix_tiers, len(off) - 1)
+    _check_views(tiers or (), b)
+    pre, own = _views(prefix_tiers, checked=True), _views(tiers, checked=True) if tiers else None
     result = (_lib_handle or lib()).kvq_decode_attention_shared(
         pre, len(prefix_tiers), off, len(off) - 1, own, len(tiers or ()), q.data_ptr(), b, hq, out.data_ptr(),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status),

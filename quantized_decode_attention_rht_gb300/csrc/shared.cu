@@ -284,7 +284,9 @@ int choose_splits(long long row_blocks, long long rows, int max_tiles, int sms, 
   const double partial = (double)rows * 1040.0 / 3.5e12 / 1.5e-6;  // write + read of one split's partials
   int best = 1;
   double least = 1e300;
-  for (int s = 1; s <= std::min(max_tiles, 256); ++s) {
+  // (beyond two waves more splits only add partials)
+  const int most = (int)std::min<long long>(std::min(max_tiles, 256), 2LL * sms / std::max<long long>(1, row_blocks) + 1);
+  for (int s = 1; s <= most; ++s) {
     const int per = (max_tiles + s - 1) / s;
     if ((max_tiles + per - 1) / per != s) continue;  // the same chunks with fewer splits
     // one wave leaves the sequences' own pass SMs to run on beside it; more make room as they end

@@ -181,6 +181,19 @@ def test_ragged_groups():
     c.check(got, {(b, h) for b in (0, 1, 2, 4, 5, 20, 39, 40, 41, 42, 43, 44) for h in range(8)})
 
 
+def test_most_groups():
+    """As many groups as a call takes, most of one sequence or none."""
+    torch, kvq = modules()
+    n = kvq.MAX_PREFIX_GROUPS
+    rng = np.random.default_rng(17)
+    offsets = [0] + np.cumsum(rng.integers(0, 3, n)).tolist()
+    lens = rng.integers(0, 200, n)
+    c = Case(kvq, torch, ["fp8_int4"], [lens], offsets, ["fp8_int4"], [rng.integers(0, 5, offsets[-1] + 2)], hq=2, hkv=1,
+             seed=17)
+    heads = {(b, h) for b in list(range(0, c.batch, 11)) + [offsets[-1] - 1, c.batch - 1] for h in range(2)}
+    c.check(c.run(kvq, torch), heads)
+
+
 def test_tiers_of_the_prefix_and_of_the_sequences():
     torch, kvq = modules()
     c = Case(kvq, torch, ["fp16", "fp8_int4"], [[100, 0], [900, 260]], [0, 4, 7], ["fp8_int4", "fp16"],

@@ -210,3 +210,93 @@ def test_binding_checks(kvq):
         kvq.kvq_dequantize(cache, slots, dev((t - 1, hkv, d), torch.float16))
     with pytest.raises(TypeError):
         kvq.kvq_dequantize(cache, slots, out, dev((t, hkv, d), torch.float32))
+
+
+def shared_call(kvq, tiers, prefix, offsets, own, batch=4, hq=4, q=1 << 12, out=1 << 12, ws=1 << 12, ws_bytes=1 << 40,
+                status=None, size=False):
+    """kvq_decode_attention_shared (or its size function) on addresses that are never read."""
+    def views(which):
+        arr = (kvq.KvqTierView * max(1, len(which)))()
+        for v, (c, table, lens, pages) in zip(arr, which):
+            v.cache, v.block_table, v.seq_lens, v.max_pages = ctypes.pointer(c), table, lens, pages
+        return arr
+    off = (ctypes.c_int32 * len(offsets))(*offsets) if offsets is not None else None
+    groups = len(offsets) - 1 if offsets is not None else 1
+    if size:
+        n = ctypes.c_size_t()
+        st = kvq.lib().kvq_decode_shared_workspace_size(views(prefix), len(prefix), off, groups, views(own), len(own),
+                                                        batch, hq, ctypes.byref(n))
+        return st, n.value
+    return kvq.lib().kvq_decode_attention_shared(views(prefix), len(prefix), off, groups, views(own), len(own), q,
+                                                 batch, hq, out, ws, ws_bytes, status, None)
+
+
+def test_shared_refusals(kvq):
+    d, hkv = 128, 2
+    signs = np.ones((hkv, d), dtype=np.int8)
+    cache = kvq.PagedCache(d, hkv, 64, "codebook", "codebook", 4, 4, signs, signs, device="cpu")
+
+    def struct(**kw):
+        s = kvq.KvqCache()
+        ctypes.memmove(ctypes.byref(s), ctypes.byref(cache.struct), ctypes.sizeof(s))
+        s.k_rows, s.v_rows, s.k_aux, s.v_aux, s.k_signs, s.v_signs = (1 << 12,) * 6
+        for name, v in kw.items():
+            setattr(s, name, v)
+        return s
+
+    c = struct()
+    view = (c, 64, 64, 8)
+    ok = dict(tiers=None, prefix=[view], offsets=[0, 4], own=[view])
+    st, need = shared_call(kvq, **ok, size=True)
+    assert st == 0 and need > 0
+    n = kvq.kvq_kernel_launches()
+    assert shared_call(kvq, **ok, batch=0) == INVALID  # offsets beyond the batch
+    assert shared_call(kvq, None, [view], [0, 0], [view], batch=0) == 0  # nothing to do
+    for offsets in ([1, 0], [-1, 4], [0, 5], [0, 3, 2, 4], None, [0] * (kvq.MAX_PREFIX_GROUPS + 2)):
+        assert shared_call(kvq, None, [view], offsets, [view]) == INVALID, offsets
+        assert shared_call(kvq, None, [view], offsets, [view], size=True)[0] == INVALID, offsets
+    assert shared_call(kvq, None, [], [0, 4], [view]) == INVALID  # no prefix tier
+    assert shared_call(kvq, None, [view] * 3, [0, 4], [view] * 2) == INVALID  # five tiers
+    for bad in ((c, 0, 64, 8), (c, 64, 0, 8), (c, 66, 64, 8), (c, 64, 65, 8), (c, 64, 64, -1)):
+        assert shared_call(kvq, None, [bad], [0, 4], [view]) == INVALID, bad[1:]
+        assert shared_call(kvq, None, [view], [0, 4], [bad]) == INVALID, bad[1:]
+    for other in (struct(page_size=32), struct(num_kv_heads=4), struct(k_signs=1 << 13), struct(k_rows=0)):
+        assert shared_call(kvq, None, [view], [0, 4], [(other, 64, 64, 8)]) == INVALID
+    assert shared_call(kvq, **ok, hq=3) == INVALID and shared_call(kvq, **ok, hq=6) == UNSUPPORTED
+    assert shared_call(kvq, **ok, hq=32) == UNSUPPORTED  # sixteen query heads per kv head
+    for bad in (dict(q=0), dict(q=(1 << 12) + 8), dict(out=0), dict(out=(1 << 12) + 2), dict(ws=0),
+                dict(ws=(1 << 12) + 128), dict(status=66)):
+        assert shared_call(kvq, **ok, **bad) == INVALID, bad
+    assert shared_call(kvq, **ok, ws_bytes=need - 1) == 3  # KVQ_ERR_WORKSPACE_TOO_SMALL
+    assert shared_call(kvq, None, [view], [0, 4], [view], batch=(1 << 22) + 1) == UNSUPPORTED
+    assert kvq.lib().kvq_decode_shared_workspace_size(None, 1, None, 1, None, 0, 4, 4, None) == INVALID
+    assert kvq.kvq_kernel_launches() == n
+
+
+def test_shared_binding_checks(kvq):
+    d, hkv, hq, b = 128, 2, 4, 3
+    signs = np.ones((hkv, d), dtype=np.int8)
+    cache = kvq.PagedCache(d, hkv, 4, "codebook", "codebook", 4, 4, signs, signs, device="cpu")
+    view = lambda rows, lens=None: kvq.TierView(cache, dev((rows, 4), torch.int32), dev((lens or rows,), torch.int32))  # noqa: E731
+    q, out, ws = dev((b, hq, d), torch.float16), dev((b, hq, d), torch.float16), dev((64,), torch.uint8)
+    call = kvq.kvq_decode_attention_shared
+    with pytest.raises(AssertionError):  # valid: as far as the pointers
+        call([view(1)], [0, 3], [view(b)], q, out, ws)
+    with pytest.raises(AssertionError):
+        call([view(2)], [0, 1, 3], None, q, out, ws)
+    with pytest.raises(TypeError):
+        call([view(1)], [0, 3], [view(b)], q, dev((b, hq, d), torch.float32), ws)
+    with pytest.raises(ValueError, match="shape"):
+        call([view(1)], [0, 3], [view(b)], dev((b, hq, 64), torch.float16), out, ws)
+    with pytest.raises(ValueError, match="tier"):
+        call([], [0, 3], [view(b)], q, out, ws)
+    with pytest.raises(ValueError, match="group_offsets"):
+        call([view(1)], [0], [view(b)], q, out, ws)
+    with pytest.raises(ValueError, match="rows"):
+        call([view(1, 2)], [0, 1, 3], [view(b)], q, out, ws)
+    with pytest.raises(ValueError, match="elements"):
+        call([view(1)], [0, 3], [view(b, b - 1)], q, out, ws)
+    with pytest.raises(ValueError, match="workspace"):
+        call([view(1)], [0, 3], [view(b)], q, out, None)
+    with pytest.raises(TypeError):
+        call([view(1)], [0, 3], [view(b)], q, out, ws, status=dev((1,), torch.int64))
