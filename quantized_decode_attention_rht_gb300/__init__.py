@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -130,10 +131,9 @@ def lib() -> ctypes.CDLL:
             "kvq_decode_attention_ex": [ctypes.POINTER(KvqTierView), i32, vp, i32, i32, i32, vp, vp, sz,
                                         ctypes.POINTER(KvqDecodeOptions), vp],
             "kvq_rope_table": [ctypes.c_double, i32, ctypes.POINTER(KvqRopeScaling), vp],
-            "kvq_rope_apply": [ctypes.POINTER(KvqRope), vp, ctypes.POINTER(KvqHeads), ctypes.POINTER(KvqHeads), i32,
-                               i32, i32, vp],
-            "kvq_rope_append": [ctypes.POINTER(KvqCache), ctypes.POINTER(KvqRope), vp, ctypes.POINTER(KvqHeads),
-                                ctypes.POINTER(KvqHeads), ctypes.POINTER(KvqHeads), i32, vp, vp],
+            # (kvq_heads structs go as their bytes: see _heads)
+            "kvq_rope_apply": [ctypes.POINTER(KvqRope), vp, vp, vp, i32, i32, i32, vp],
+            "kvq_rope_append": [ctypes.POINTER(KvqCache), ctypes.POINTER(KvqRope), vp, vp, vp, vp, i32, vp, vp],
             "kvq_dequantize": [ctypes.POINTER(KvqCache), vp, i32, vp, vp, vp],
             "kvq_decode_shared_workspace_size": [ctypes.POINTER(KvqTierView), i32, vp, i32, ctypes.POINTER(KvqTierView),
                                                  i32, i32, i32, szp],
@@ -210,28 +210,27 @@ def _stream(stream) -> Optional[int]:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _call_stream(stream, *tensors) -> Optional[int]:
+_current_device = _raw_stream = None  # torch's look-ups without an object around the stream
+
+
+def _call_stream(stream, first, *others) -> Optional[int]:
     """The stream of a call, whose tensors lie on one device: the current one, unless the caller
     names a stream (of that device)."""
-    torch = _load_torch()
-    index = None
-    for t in tensors:
-        if t is None or not hasattr(t, "get_device"):
-            continue
-        d = t.get_device()
-        if index is None:
-            index = d
-        elif d != index:
-            raise ValueError(f"tensors of one call on different devices: cuda:{index} and cuda:{d}")
+    global _current_device, _raw_stream
+    index = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors of one call on different devices: cuda:{index} and cuda:{t.get_device()}")
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    if index is None:
-        return _stream(None)
-    current = torch.cuda.current_device()
-    if index != current:
-        raise ValueError(f"tensors on cuda:{index}, but the current device is cuda:{current}")
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same stream, without an object around it
-    return raw(index) if raw is not None else torch.cuda.current_stream().cuda_stream
+    if _current_device is None:
+        torch = _load_torch()
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda _: torch.cuda.current_stream().cuda_stream)
+    if index != _current_device():
+        raise ValueError(f"tensors on cuda:{index}, but the current device is cuda:{_current_device()}")
+    return _raw_stream(index)
 
 
 # ----------------------------------------------------------------------------- host-side entry points
@@ -338,34 +337,43 @@ def kvq_requantize(src: KvqCache, src_slots, dst: KvqCache, dst_slots, stream=No
                                 int(src_slots.shape[0]), _stream(stream)), "kvq_requantize")
 
 
-def _check_heads(x, name: str, tokens: int, head_dim: int, num_heads=None, out=None) -> None:
-    """x (and out, where given, of its shape): fp16 [tokens, heads, head_dim], the elements of a
-    head adjacent, token and head strides free."""
-    if x is None:
-        return
-    _arg(x, name, "float16", (tokens, num_heads, head_dim))
-    if x.stride(2) != 1:
+def _check_heads(x, name: str, tokens, heads, head_dim):
+    """x: fp16 [tokens, heads, head_dim] (None: free), the elements of a head adjacent, token and
+    head strides free.  Returns its strides."""
+    if _torch is None:
+        _load_torch()
+    shape, strides = x.shape, x.stride()
+    if (not getattr(x, "is_cuda", False) or x.dtype is not _DTYPES["float16"] or len(shape) != 3
+            or (tokens is not None and shape[0] != tokens) or (heads is not None and shape[1] != heads)
+            or shape[2] != head_dim):
+        _arg(x, name, "float16", (tokens, heads, head_dim))
+    if strides[2] != 1:
         raise ValueError(f"the elements of a head of {name} must be adjacent")
-    if x.shape[1] == 0:
+    if shape[1] == 0:
         raise ValueError(f"{name} needs at least one head")
-    if out is not None:
-        _arg(out, name + "_out", "float16", x.shape)
-        if out.stride(2) != 1:
-            raise ValueError(f"the elements of a head of {name}_out must be adjacent")
+    return strides
 
 
-def _heads(x, out=None, write: bool = False):
-    """Checked heads by reference to the C ABI's struct (None for no heads); write: the call
-    writes `out`, or x itself where it is None."""
-    if x is None:
-        return None
-    st, sh, _ = x.stride()
-    if not write:
-        return ctypes.byref(KvqHeads(x.data_ptr(), None, x.shape[1], st, sh, 0, 0))
+_HEADS = struct.Struct("@PPi4xqqqq")  # kvq_heads: x, out, num_heads, token and head strides of x and of out
+assert _HEADS.size == ctypes.sizeof(KvqHeads)
+
+
+def _heads(x, strides, out, out_strides) -> bytes:
+    """Checked heads as the bytes of the C ABI's struct (a quarter of what filling one by ctypes
+    takes); out None: the call only reads."""
     if out is None:
-        return ctypes.byref(KvqHeads(x.data_ptr(), x.data_ptr(), x.shape[1], st, sh, st, sh))
-    ot, oh, _ = out.stride()
-    return ctypes.byref(KvqHeads(x.data_ptr(), out.data_ptr(), x.shape[1], st, sh, ot, oh))
+        return _HEADS.pack(x.data_ptr(), 0, x.shape[1], strides[0], strides[1], 0, 0)
+    return _HEADS.pack(x.data_ptr(), out.data_ptr(), x.shape[1], strides[0], strides[1], out_strides[0], out_strides[1])
+
+
+def _int_vector(x, name: str, n: int) -> None:
+    """x: dense int32 [>= n]."""
+    if _torch is None:
+        _load_torch()
+    if (not getattr(x, "is_cuda", False) or x.dtype is not _DTYPES["int32"] or x.dim() != 1 or x.numel() < n
+            or not x.is_contiguous()):
+        _dense(x)
+        _arg(x, name, "int32", (None,), min_numel=n)
 
 
 def kvq_rope_apply(rope: "Rope", positions, q, k=None, q_out=None, k_out=None, transpose: bool = False,
@@ -373,16 +381,18 @@ def kvq_rope_apply(rope: "Rope", positions, q, k=None, q_out=None, k_out=None, t
     """q [T, Hq, D], k [T, Hkv, D] (or None): fp16 CUDA tensors or strided views; positions:
     int32 [T].  Writes q_out / k_out (any strides), or q / k themselves where they are None.
     transpose: the transposed map (the gradient with respect to q and k)."""
-    _arg(q, "q", "float16", (None, None, None))
-    t, d = int(q.shape[0]), int(q.shape[2])
-    _dense(positions)
-    _arg(positions, "positions", "int32", (None,), min_numel=t)
-    _check_heads(q, "q", t, d, out=q_out)
-    _check_heads(k, "k", t, d, out=k_out)
-    status = (_lib_handle or lib()).kvq_rope_apply(ctypes.byref(rope.struct), positions.data_ptr(),
-                                                   _heads(q, q_out, True), _heads(k, k_out, True), t, d,
-                                                   1 if transpose else 0,
-                                                   _call_stream(stream, q, k, q_out, k_out, positions))
+    if len(q.shape) != 3:
+        _arg(q, "q", "float16", (None, None, None))
+    t, n, d = q.shape
+    qs = _check_heads(q, "q", t, None, d)
+    qo, qos = (q, qs) if q_out is None else (q_out, _check_heads(q_out, "q_out", t, n, d))
+    if k is not None:
+        ks = _check_heads(k, "k", t, None, d)
+        ko, kos = (k, ks) if k_out is None else (k_out, _check_heads(k_out, "k_out", t, k.shape[1], d))
+    _int_vector(positions, "positions", t)
+    status = (_lib_handle or lib()).kvq_rope_apply(
+        rope.reference, positions.data_ptr(), _heads(q, qs, qo, qos), None if k is None else _heads(k, ks, ko, kos), t, d,
+        1 if transpose else 0, _call_stream(stream, q, k, q_out, k_out, positions))
     if status:
         raise KvqError(status, "kvq_rope_apply")
 
@@ -394,19 +404,19 @@ def kvq_rope_append(cache: KvqCache, rope: "Rope", positions, k, v, slot_mapping
     be None); q: fp16 [T, Hq, D]; positions, slot_mapping: int32 [T]."""
     if k is None and v is None:
         raise ValueError("kvq_rope_append needs k or v")
-    x = k if k is not None else v
-    _arg(x, "k" if k is not None else "v", "float16", (None, cache.num_kv_heads, cache.head_dim))
-    t, d = int(x.shape[0]), cache.head_dim
-    _dense(positions, slot_mapping)
-    _arg(positions, "positions", "int32", (None,), min_numel=t)
-    _arg(slot_mapping, "slot_mapping", "int32", (None,), min_numel=t)
-    _check_heads(k, "k", t, d, cache.num_kv_heads)
-    _check_heads(v, "v", t, d, cache.num_kv_heads)
-    _check_heads(q, "q", t, d, out=q_out)
-    status = (_lib_handle or lib()).kvq_rope_append(ctypes.byref(cache), ctypes.byref(rope.struct),
-                                                    positions.data_ptr(), _heads(k), _heads(v),
-                                                    _heads(q, q_out, True), t, slot_mapping.data_ptr(),
-                                                    _call_stream(stream, k, v, q, q_out, positions, slot_mapping))
+    hkv, d = cache.num_kv_heads, cache.head_dim
+    t = (k if k is not None else v).shape[0]
+    ks = None if k is None else _check_heads(k, "k", t, hkv, d)
+    vs = None if v is None else _check_heads(v, "v", t, hkv, d)
+    if q is not None:
+        qs = _check_heads(q, "q", t, None, d)
+        qo, qos = (q, qs) if q_out is None else (q_out, _check_heads(q_out, "q_out", t, q.shape[1], d))
+    _int_vector(positions, "positions", t)
+    _int_vector(slot_mapping, "slot_mapping", t)
+    status = (_lib_handle or lib()).kvq_rope_append(
+        ctypes.byref(cache), rope.reference, positions.data_ptr(), None if k is None else _heads(k, ks, None, None),
+        None if v is None else _heads(v, vs, None, None), None if q is None else _heads(q, qs, qo, qos), t,
+        slot_mapping.data_ptr(), _call_stream(stream, positions, k, v, q, q_out, slot_mapping))
     if status:
         raise KvqError(status, "kvq_rope_append")
 
@@ -414,15 +424,16 @@ def kvq_rope_append(cache: KvqCache, rope: "Rope", positions, k, v, slot_mapping
 def kvq_dequantize(cache: KvqCache, slots, k_out=None, v_out=None, stream=None) -> None:
     """Cached tokens back as fp16 vectors: slots int32 [T]; k_out, v_out fp16 [T, Hkv, D]
     (either may be None), written where the slot is in range."""
-    _dense(slots, k_out, v_out)
     if k_out is None and v_out is None:
         raise ValueError("kvq_dequantize needs k_out or v_out")
-    _arg(slots, "slots", "int32", (None,))
-    t = int(slots.shape[0])
+    _dense(k_out, v_out)
+    _int_vector(slots, "slots", 0)
+    t = slots.shape[0]
     for x, name in ((k_out, "k_out"), (v_out, "v_out")):
-        _arg(x, name, "float16", (t, cache.num_kv_heads, cache.head_dim))
-    status = (_lib_handle or lib()).kvq_dequantize(ctypes.byref(cache), slots.data_ptr(), t, _ptr(k_out),
-                                                   _ptr(v_out), _call_stream(stream, slots, k_out, v_out))
+        if x is not None:
+            _check_heads(x, name, t, cache.num_kv_heads, cache.head_dim)
+    status = (_lib_handle or lib()).kvq_dequantize(ctypes.byref(cache), slots.data_ptr(), t, _ptr(k_out), _ptr(v_out),
+                                                   _call_stream(stream, slots, k_out, v_out))
     if status:
         raise KvqError(status, "kvq_dequantize")
 
@@ -535,8 +546,8 @@ def kvq_decode_attention_shared(prefix_tiers, group_offsets, tiers, q, out, work
     result = (_lib_handle or lib()).kvq_decode_attention_shared(
         pre, len(prefix_tiers), off, len(off) - 1, own, len(tiers or ()), q.data_ptr(), b, hq, out.data_ptr(),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status),
-        _call_stream(stream, q, out, workspace, status, *(x for t in (*prefix_tiers, *(tiers or ()))
-                                                          for x in (t.block_table, t.seq_lens))))
+        _call_stream(stream, q, out, workspace, status, *[x for t in (*prefix_tiers, *(tiers or ()))
+                                                          for x in (t.block_table, t.seq_lens)]))
     if result:
         raise KvqError(result, "kvq_decode_attention_shared")
 
@@ -641,7 +652,7 @@ class Rope:
         s = KvqRope()
         s.rot_dim, s.layout, s.scale = rot_dim, ROPE_LAYOUTS.get(layout, layout), scale
         s.turns = _ptr(self.turns)
-        self.struct = s
+        self.struct, self.reference = s, ctypes.byref(s)
 
 
 class TierView:

@@ -175,6 +175,8 @@ def test_binding_checks(kvq):
         kvq.kvq_rope_apply(rope, pos, q, k)
     with pytest.raises(ValueError, match="CUDA"):
         kvq.kvq_rope_apply(rope, pos, torch.zeros((t, hq, d), dtype=torch.float16))
+    with pytest.raises(ValueError, match="shape"):
+        kvq.kvq_rope_apply(rope, pos, heads(t, hq * d))
     with pytest.raises(TypeError):
         kvq.kvq_rope_apply(rope, pos, heads(t, hq, d, dtype=torch.float32))
     with pytest.raises(TypeError):
@@ -201,15 +203,15 @@ def test_binding_checks(kvq):
     with pytest.raises(ValueError, match="elements"):
         kvq.kvq_rope_append(cache, rope, pos, k, k, dev((t - 1,), torch.int32))
 
-    out = dev((t, hkv, d), torch.float16)
+    out = heads(t, hkv, d)
     with pytest.raises(AssertionError):
         kvq.kvq_dequantize(cache, slots, out, None)
     with pytest.raises(ValueError):
         kvq.kvq_dequantize(cache, slots)
     with pytest.raises(ValueError, match="shape"):
-        kvq.kvq_dequantize(cache, slots, dev((t - 1, hkv, d), torch.float16))
+        kvq.kvq_dequantize(cache, slots, heads(t - 1, hkv, d))
     with pytest.raises(TypeError):
-        kvq.kvq_dequantize(cache, slots, out, dev((t, hkv, d), torch.float32))
+        kvq.kvq_dequantize(cache, slots, out, heads(t, hkv, d, dtype=torch.float32))
 
 
 def shared_call(kvq, tiers, prefix, offsets, own, batch=4, hq=4, q=1 << 12, out=1 << 12, ws=1 << 12, ws_bytes=1 << 40,
