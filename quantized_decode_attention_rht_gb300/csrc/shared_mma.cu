@@ -31,7 +31,7 @@
 // accumulators are float32.  Two things keep the codebook formats as exact as the others, whose
 // keys are fp16 values already: a centroid's rounding is the same in every coordinate that has
 // its code, which with an outlier channel is nearly all of them, so the table is scaled by the
-// factor out of 256 whose roundings are smallest (undone in float32); and a key's norm
+// factor out of 128 whose roundings are smallest (undone in float32); and a key's norm
 // multiplies its scores, in float32, in place of its coordinates.  (On caches with x30 outlier
 // channels the 2-norm of the output's error falls from 2.3e-3 to 7e-4 of the output's; fp8
 // keys: 6e-4.)
@@ -64,7 +64,7 @@ constexpr int kSmem = kOffCtl + 512 + 1024;  // 1024: the base is aligned by han
 static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 
 // barriers, in units of 8 bytes from kOffCtl
-enum { B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_QFULL = 8, B_SFULL = 10, B_PREADY = 12, B_OFULL = 14, B_QRAW = 16, B_QROT = 17, B_ROWS = 18, B_ROWS_READ = 22, B_AUX = 26, B_COUNT = 30 };
+enum { B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_QFULL = 8, B_SFULL = 10, B_PREADY = 12, B_OFULL = 14, B_QROT = 16, B_ROWS = 18, B_ROWS_READ = 22, B_AUX = 26, B_COUNT = 30 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
@@ -302,10 +302,6 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// The codebooks' tables are made: the eight decoding warps and the look-up warps meet once
-// (320 = 256 + 32 kLookUps threads).
-__device__ __forceinline__ void tables_made() { asm volatile("bar.sync 3, 320;" ::: "memory"); }
-
 // Look-up warp `first` of kLookUps, which take tiles in turn (a look-up is a chain of three
 // loads, longer than a tile's products): rows of a tile's tokens, then their norms (codebooks) or
 // group scales (INT4 values).  Page numbers are read a turn ahead.  kLookUps divides kAhead, so
@@ -314,15 +310,17 @@ __device__ __forceinline__ void tables_made() { asm volatile("bar.sync 3, 320;" 
 // phase of the barrier for the one before the last.
 constexpr int kLookUps = 2;
 static_assert(kAhead % kLookUps == 0, "a stage's releases are waited for by one warp");
-__device__ __forceinline__ void look_up(const Pages& s, const __half* k_norm, const __half* v_norm,
+__device__ __forceinline__ void first_pages(const Pages& s, int tile0, int n, int first, int (&page)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    page[j] = first < n ? page_of(s, (tile0 + first) * kTileTokens + (threadIdx.x & 31) + 32 * j) : -1;
+}
+__device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __half* k_norm, const __half* v_norm,
                                         const __half* v_scale, volatile float* unscale, uint32_t smem, uint32_t bars, int tile0, int n, int first,
                                         volatile int* abort, int* err) {
   const int lane = threadIdx.x & 31;
   int bits = 0;
-  float key_unit = 0.f;  // of the keys' table (known once the tables are made)
-  int page[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) page[j] = first < n ? page_of(s, (tile0 + first) * kTileTokens + lane + 32 * j) : -1;
+  const float key_unit = k_norm ? unscale[0] : 0.f;  // of the keys' table
 #pragma unroll 1
   for (int i = first; i < n; i += kLookUps) {
     const int at = i % kAhead;
@@ -350,10 +348,6 @@ __device__ __forceinline__ void look_up(const Pages& s, const __half* k_norm, co
 #pragma unroll
       for (int j = 0; j < 4; ++j) page[j] = page_of(s, t0 + kLookUps * kTileTokens + 32 * j);
     }
-    if (k_norm && i == first) {
-      tables_made();
-      key_unit = unscale[0];
-    }
     const uint32_t ka = smem + kOffKAux + at * kTileTokens * 4 + 4 * lane;
     const uint32_t va = smem + kOffVAux + at * kTileTokens * 8 + 8 * lane;
 #pragma unroll
@@ -369,7 +363,6 @@ __device__ __forceinline__ void look_up(const Pages& s, const __half* k_norm, co
     }
     bar_arrive(bars + 8 * (B_AUX + at));
   }
-  if (k_norm && key_unit == 0.f) tables_made();  // (no tile, or none that got so far)
   if (bits) atomicOr(err, bits);
 }
 
@@ -468,29 +461,22 @@ __device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, int 
   }
 }
 
-// The scale of a codebook's table, out of 2^(k / 256) / 16, k < 256: the one whose fp16 roundings
+// The scale of a codebook's table, out of 2^(k / 128) / 16, k < 128: the one whose fp16 roundings
 // are smallest, by the sum of squares of their relative errors.  c: centroid `lane` in every
-// lane (0 beyond the codebook); the side's four warps, which share the candidates.
+// lane (0 beyond the codebook); the side's four warps, a candidate a thread.
 __device__ __forceinline__ float scale_table(Ctl* ctl, float c, int bits, int side, int tid) {
   const int lane = tid & 31, warp = tid >> 5;
-  float least = INFINITY;
-  int at = 0;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int k = 2 * tid + j;
-    const float beta = exp2f((float)k * (1.0f / 256.0f)) * 0.0625f;
-    float sum = 0.f;
+  const float over = c != 0.f ? __fdividef(1.0f, c) : 0.f;
+  const float mine = exp2f((float)tid * (1.0f / 128.0f)) * 0.0625f;
+  float least = 0.f;
+  int at = tid;
 #pragma unroll 4
-    for (int i = 0; i < (1 << bits); ++i) {
-      const float x = __shfl_sync(0xFFFFFFFFu, c, i) * beta;
-      const float off = x != 0.f ? __fdividef(__half2float(__float2half_rn(x)) - x, x) : 0.f;
-      sum = fmaf(off, off, sum);
-    }
-    if (sum < least) {
-      least = sum;
-      at = k;
-    }
+  for (int i = 0; i < (1 << bits); ++i) {
+    const float x = __shfl_sync(0xFFFFFFFFu, c, i) * mine;
+    const float off = (__half2float(__float2half_rn(x)) - x) * __shfl_sync(0xFFFFFFFFu, over, i);
+    least = fmaf(off, off, least);
   }
+  least = __fdividef(least, mine * mine);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float other = __shfl_xor_sync(0xFFFFFFFFu, least, o);
@@ -514,7 +500,7 @@ __device__ __forceinline__ float scale_table(Ctl* ctl, float c, int bits, int si
       at = k;
     }
   }
-  const float beta = exp2f((float)at * (1.0f / 256.0f)) * 0.0625f;
+  const float beta = exp2f((float)at * (1.0f / 128.0f)) * 0.0625f;
   if (tid == 0) ctl->unscale[side] = inv_sqrt_dim(kDim) / beta;
   return beta;
 }
@@ -744,6 +730,8 @@ __device__ __forceinline__ float2 unpack2(unsigned long long r) {
 // made it a third slower for both).
 template <bool CODES>
 __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid_constant__ SharedParams p) {
+  // the pass over the sequences' own tiers may start on SMs that this grid leaves idle
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (smem - smem_u32(smem_raw)) + kOffCtl);
@@ -811,7 +799,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       bar_init(bars + 8 * (B_PREADY + i), max(1, (live + 31) / 32 * 32));  // the warps that hold rows
       bar_init(bars + 8 * (B_OFULL + i), 1);
     }
-    bar_init(bars + 8 * B_QRAW, 256);
     bar_init(bars + 8 * B_QROT, 1);
     for (int i = 0; i < kAhead; ++i) {
       bar_init(bars + 8 * (B_ROWS + i), 32);
@@ -822,95 +809,115 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     ctl->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 16) {
+  Tables tables;
+  int page[4];
+  Pages pages;
+  pages.table = T.block_table + (size_t)g * T.max_pages;
+  pages.num_pages = T.num_pages;
+  pages.page_size = p.page_size;
+  pages.page_shift = p.page_shift;
+  pages.hkv = p.hkv;
+  pages.hk = hk;
+  pages.end = len;
+  // ---- before the block meets: everything that needs no barrier
+  if (warp < 8) {
+    // The block's queries are rotated as one more product, of the queries as they come (fp16,
+    // exact) and the matrix of elements s_k (-1)^popc(n & k) (exact too), in float32: here both
+    // are laid out.  (Butterflies by shuffles took 15 us for 256 rows.)
+    const int tid = threadIdx.x & 255;
+    const int shift = __ffs(p.group) - 1;
+    for (int first = 0; first < (both ? kTileRows : kItemRows); first += 128) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = first + i * 16 + (tid >> 4);
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (row < rows) {
+          const int gr = lb * kItemRows + row, sq = gr >> shift;
+          const size_t orow = (size_t)(p.offset[g] + sq) * p.hq + hk * p.group + (gr - (sq << shift));
+          v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + orow * kDim) + (tid & 15));
+        }
+      }
+      const uint32_t to = smem + kOffQ + (first >> 7) * kTileBytes + ((tid & 15) >> 3) * kHalfBytes;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 16 + (tid >> 4);
+        sts16(to + r * 128 + (((tid & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+      }
+    }
+    const int c = tid & 15;  // elements 8c .. 8c + 7 of rows n
+    const uint2 sg = __ldg(reinterpret_cast<const uint2*>(p.k_signs + (size_t)hk * kDim) + c);
+    const uint32_t to = smem + kOffV + kTileBytes + (c >> 3) * kHalfBytes;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int n7 = (tid >> 4) & 7, nr = i * 16 + (tid >> 4);
+      const bool flip = __popc((nr >> 3) & c) & 1;  // the chunk's part of the parity
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t s0 = (k < 2 ? sg.x >> (16 * k) : sg.y >> (16 * (k - 2)));  // sign bytes 2k, 2k + 1
+        const uint32_t lo = ((s0 >> 7) ^ __popc(n7 & (2 * k)) ^ (uint32_t)flip) & 1u;
+        const uint32_t hi = ((s0 >> 15) ^ __popc(n7 & (2 * k + 1)) ^ (uint32_t)flip) & 1u;
+        h[k] = 0x3C003C00u | (lo << 15) | (hi << 31);
+      }
+      sts16(to + nr * 128 + (((c & 7) ^ (nr & 7)) << 4), h[0], h[1], h[2], h[3]);
+    }
+    fence_async_smem();
+  } else if (warp < 16) {
+    if constexpr (CODES) {
+      const bool keys = warp < 12;
+      const int side = keys ? 0 : 1, tid = threadIdx.x & 127, lane = threadIdx.x & 31;
+      const float kc = lane < (1 << T.k_bits) ? __ldg(T.k_cent + lane) : 0.f;
+      const float vc = lane < (1 << T.v_bits) ? __ldg(T.v_cent + lane) : 0.f;
+      const bool same = T.k_bits == T.v_bits && __all_sync(0xFFFFFFFFu, kc == vc);  // one table (often so)
+      tables = place_tables(smem, T.k_bits, T.v_bits, same, both);
+      const int bits = keys ? T.k_bits : T.v_bits;
+      const float beta = scale_table(ctl, keys ? kc : vc, bits, side, tid);
+      if (keys || !same) build_lut(tables.at[side], tables.copies[side], (keys ? kc : vc) * beta, bits, tid);
+    }
+  } else if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (warp < 17 + kLookUps) {
+    first_pages(pages, tile0, n, warp - 17, page);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
 
-  // chunks of the sequences' own tiers may start on SMs that this grid leaves idle
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
   if (warp < 8) {
     // ---- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    // The block's queries: H s q as one more product, of the queries as they come (fp16, exact)
-    // and the matrix of elements s_k (-1)^popc(n & k) (exact too), in float32; then, from TMEM,
-    // times log2(e) / D (1 / sqrt(D) of the rotation and of the scores, which are then in base-2
-    // units), rounded to fp16 into the query tiles.  (Butterflies by shuffles took 15 us for
-    // 256 rows.)
+    // The rotated queries, from TMEM: times log2(e) / D (1 / sqrt(D) of the rotation and of the
+    // scores, which are then in base-2 units), rounded to fp16 into the query tiles.
     bool ok = true;
-    {
-      const int tid = threadIdx.x & 255;
-      const int shift = __ffs(p.group) - 1;
-      for (int first = 0; first < (both ? kTileRows : kItemRows); first += 128) {
-        uint4 v[8];
+    if (!(both && w)) {
+      ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * B_QROT, 0, abort, p.err));
+      tc_fence_after();
+      const int r = threadIdx.x & 127;
+      const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + w * 128;
+      const uint32_t to = smem + kOffQ + w * kTileBytes + r * 128;
+      constexpr float scale = 1.4426950408889634f / kDim;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = first + i * 16 + (tid >> 4);
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (row < rows) {
-            const int gr = lb * kItemRows + row, sq = gr >> shift;
-            const size_t orow = (size_t)(p.offset[g] + sq) * p.hq + hk * p.group + (gr - (sq << shift));
-            v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + orow * kDim) + (tid & 15));
-          }
-        }
-        const uint32_t to = smem + kOffQ + (first >> 7) * kTileBytes + ((tid & 15) >> 3) * kHalfBytes;
+      for (int part = 0; part < 4; ++part) {
+        uint32_t v[32];
+        tc_ld32(from + 32 * part, v);
+        tc_wait_ld(v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 16 + (tid >> 4);
-          sts16(to + r * 128 + (((tid & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            h[k] = half2_bits(__uint_as_float(v[8 * i + 2 * k]) * scale, __uint_as_float(v[8 * i + 2 * k + 1]) * scale);
+          const int at = 4 * part + i;
+          sts16(to + (at >> 3) * kHalfBytes + (((at & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
         }
       }
-      const int c = tid & 15;  // elements 8c .. 8c + 7 of rows n
-      const uint2 sg = __ldg(reinterpret_cast<const uint2*>(p.k_signs + (size_t)hk * kDim) + c);
-      const uint32_t to = smem + kOffV + kTileBytes + (c >> 3) * kHalfBytes;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int n7 = (tid >> 4) & 7, nr = i * 16 + (tid >> 4);
-        const bool flip = __popc((nr >> 3) & c) & 1;  // the chunk's part of the parity
-        uint32_t h[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t s0 = (k < 2 ? sg.x >> (16 * k) : sg.y >> (16 * (k - 2)));  // sign bytes 2k, 2k + 1
-          const uint32_t lo = ((s0 >> 7) ^ __popc(n7 & (2 * k)) ^ (uint32_t)flip) & 1u;
-          const uint32_t hi = ((s0 >> 15) ^ __popc(n7 & (2 * k + 1)) ^ (uint32_t)flip) & 1u;
-          h[k] = 0x3C003C00u | (lo << 15) | (hi << 31);
-        }
-        sts16(to + nr * 128 + (((c & 7) ^ (nr & 7)) << 4), h[0], h[1], h[2], h[3]);
-      }
+      tc_fence_before();
       fence_async_smem();
-      bar_arrive(bars + 8 * B_QRAW);
-      if (!(both && w)) {
-        ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * B_QROT, 0, abort, p.err));
-        tc_fence_after();
-        const int r = threadIdx.x & 127;
-        const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + w * 128;
-        const uint32_t to = smem + kOffQ + w * kTileBytes + r * 128;
-        constexpr float scale = 1.4426950408889634f / kDim;
-#pragma unroll
-        for (int part = 0; part < 4; ++part) {
-          uint32_t v[32];
-          tc_ld32(from + 32 * part, v);
-          tc_wait_ld(v);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t h[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              h[k] = half2_bits(__uint_as_float(v[8 * i + 2 * k]) * scale, __uint_as_float(v[8 * i + 2 * k + 1]) * scale);
-            const int at = 4 * part + i;
-            sts16(to + (at >> 3) * kHalfBytes + (((at & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-          }
-        }
-        tc_fence_before();
-        fence_async_smem();
-        bar_arrive(bars + 8 * (B_QFULL + w));
+      bar_arrive(bars + 8 * (B_QFULL + w));
       }
-    }
     const int my_jobs = jobs > w ? (jobs - w + 1) / 2 : 0;
     const bool live = (warp & 3) * 32 < rows_of_group;  // the warp holds rows
     if (live && my_jobs > 0) {
@@ -1065,17 +1072,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     Source s;
     s.rows = keys ? T.k_rows : T.v_rows;
     s.row_bytes = keys ? T.k_row_bytes : T.v_row_bytes;
-    if constexpr (CODES) {  // (while the look-up warps find the first rows)
-      const int side = keys ? 0 : 1, tid = threadIdx.x & 127, lane = threadIdx.x & 31;
-      const float kc = lane < (1 << T.k_bits) ? __ldg(T.k_cent + lane) : 0.f;
-      const float vc = lane < (1 << T.v_bits) ? __ldg(T.v_cent + lane) : 0.f;
-      const bool same = T.k_bits == T.v_bits && __all_sync(0xFFFFFFFFu, kc == vc);  // one table (often so)
-      const Tables tables = place_tables(smem, T.k_bits, T.v_bits, same, both);
-      const int bits = keys ? T.k_bits : T.v_bits;
-      const float beta = scale_table(ctl, keys ? kc : vc, bits, side, tid);
-      if (keys || !same) build_lut(tables.at[side], tables.copies[side], (keys ? kc : vc) * beta, bits, tid);
-      tables_made();
-      s.lut = tables.at[side] + 4u * (tid & (tables.copies[side] - 1));
+    if constexpr (CODES) {
+      const int side = keys ? 0 : 1;
+      s.lut = tables.at[side] + 4u * (threadIdx.x & (tables.copies[side] - 1));
       s.lut_stride = 4u * tables.copies[side];
       s.raw = tables.raw[side];
     } else {
@@ -1124,9 +1123,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         __syncwarp();
         return true;
       };
-      bool ok = well(bars + 8 * B_QRAW, 0);
-      if (ok) {  // the rotated queries, into the score columns
-        tc_fence_after();
+      bool ok = true;
+      {  // the rotated queries, into the score columns
         const uint64_t rd = desc_at(desc_base(16, 1024), smem + kOffV + kTileBytes);
         if (elect_one()) {
           for (int ws = 0; ws < (both ? 1 : 2); ++ws) {
@@ -1159,15 +1157,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       }
     } else if (warp < 17 + kLookUps) {
       // ---- look-ups
-      Pages s;
-      s.table = T.block_table + (size_t)g * T.max_pages;
-      s.num_pages = T.num_pages;
-      s.page_size = p.page_size;
-      s.page_shift = p.page_shift;
-      s.hkv = p.hkv;
-      s.hk = hk;
-      s.end = len;
-      look_up(s, CODES ? T.k_aux : nullptr, CODES ? T.v_aux : nullptr, T.v_fmt == KVQ_FMT_INT4_G32 ? T.v_aux : nullptr,
+      look_up(pages, page, CODES ? T.k_aux : nullptr, CODES ? T.v_aux : nullptr, T.v_fmt == KVQ_FMT_INT4_G32 ? T.v_aux : nullptr,
               ctl->unscale, smem, bars, tile0, n, warp - 17, abort, p.err);
     }
   }
