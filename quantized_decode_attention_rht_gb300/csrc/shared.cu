@@ -31,10 +31,12 @@ struct JoinParams {  // small: a launch's parameters are read through a cold cac
   const int8_t* v_signs;
   __half* out;
   int* status;
-  const int* err;
+  int* err;
   int batch, hq, group_shift, page_size;
   int splits, own_splits, num_tiers, num_groups;
   JoinTier tier[KVQ_MAX_TIERS];
+  const int32_t* idle_lens[KVQ_MAX_TIERS];  // per group, of prefix tiers without pages: 0, or out of range
+  int num_idle;
   int offset[KVQ_MAX_PREFIX_GROUPS + 1];
 };
 
@@ -109,14 +111,19 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
 #pragma unroll
   for (int i = 0; i < KVQ_MAX_TIERS; ++i) lens[i] = i < p.num_tiers ? __ldg(p.tier[i].seq_lens + b) : 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // every partial is complete
-  if (p.status && blockIdx.x == 0 && warp == 0) {
+  if (p.status && blockIdx.x == gridDim.x - 1) {  // a block of its own
     int bits = 0;  // lengths out of range, of sequences; the prefix pass reports its own
-    for (int i = lane; i < p.batch * p.num_tiers; i += 32) {
+    for (int i = threadIdx.x; i < p.batch * p.num_tiers; i += 256) {
       const JoinTier& T = p.tier[i % p.num_tiers];
       checked_len(T.seq_lens[i / p.num_tiers], T.max_pages, p.page_size, &bits);
     }
-    bits = __reduce_or_sync(0xFFFFFFFFu, bits);
-    if (lane == 0) *p.status = bits | *reinterpret_cast<const volatile int*>(p.err);
+    for (int i = threadIdx.x; i < p.num_groups * p.num_idle; i += 256)
+      if (p.offset[i / p.num_idle] < p.offset[i / p.num_idle + 1])
+        checked_len(p.idle_lens[i % p.num_idle][i / p.num_idle], 0, p.page_size, &bits);
+    if (bits) atomicOr(p.err, bits);
+    __syncthreads();
+    if (threadIdx.x == 0) *p.status = *reinterpret_cast<volatile int*>(p.err);
+    return;
   }
   if (!there) return;
   // a lane looks after one partial at a time: its (max, sum) and where its accumulator lies
@@ -477,7 +484,7 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
   int at = 0;
   for (int i = 0; i < num_prefix_tiers; ++i) {
     const kvq_cache* k = all[i].cache;
-    if (plan.splits[i] == 0) continue;  // a tier without a table
+    if (plan.splits[i] == 0) continue;  // a tier without pages
     SharedTier& t = p.tier[p.num_tiers++];
     t.k_rows = static_cast<const uint8_t*>(k->k_rows);
     t.v_rows = static_cast<const uint8_t*>(k->v_rows);
@@ -538,6 +545,8 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
   for (int i = 0; i < num_tiers; ++i)
     j.tier[i] = {own.tier[i].seq_lens, own.tier[i].max_pages, own.tier[i].chunk, own.tier[i].num_splits,
                  own.tier[i].split_begin};
+  for (int i = 0; i < num_prefix_tiers; ++i)
+    if (plan.splits[i] == 0) j.idle_lens[j.num_idle++] = all[i].seq_lens;
   for (int g = 0; g <= num_groups; ++g) j.offset[g] = group_offsets[g];
   e = cudaMemsetAsync(counters, 0, 256, s);  // work counters and the error word
   const bool prefix = plan.num_blocks > 0 && plan.total_splits > 0;
@@ -547,7 +556,7 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
     // eight warps a row where a row has many partials (one warp would wait for them in turn)
     const bool many = 2 * plan.total_splits + plan.dec.total > 24;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(many ? rows : (rows + 7) / 8));
+    cfg.gridDim = dim3((unsigned)((many ? rows : (rows + 7) / 8) + (status ? 1 : 0)));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -321,3 +321,90 @@ def test_bad_lengths_and_pages_are_reported():
     lens[0] = 300
     assert bits() == 0
     c.check(out.cpu().numpy())
+
+
+def test_one_token_against_a_long_tail():
+    """A token that outweighs each of 131071 others 2^25.5 times: together they hold 0.3% of the
+    weight, and with values eight times as large 2% of the output.  Half a step of fp16 against a
+    weight of 1 would lose them all; with a largest weight of 4 each is kept to 2^-25 / 4 of it,
+    together 2^17 2^-27 8 = 2^-7 of the large token's value, beside 2^-9 (2-norm) for the other
+    roundings (losing them all would be 2.2%).  The others are one page, 8191 times in the table."""
+    torch, kvq = modules()
+    d, ps, hkv, group, batch, pages = 128, 16, 150, 8, 16, 8192
+    rng = np.random.default_rng(15)
+    ks, vs = (np.where(rng.integers(0, 2, (hkv, d)) == 0, 1, -1).astype(np.int8) for _ in range(2))
+    cache = kvq.PagedCache(d, hkv, 2, "fp16", "fp16", 0, 0, ks, vs, ps)
+    u = rng.standard_normal((hkv, d))
+    u /= np.linalg.norm(u, axis=-1, keepdims=True)
+    gap = 25.5 * math.log(2.0)  # nats, between scores of the queries below
+    length = 12.0  # of the queries
+    k = np.repeat((-0.5 * gap * math.sqrt(d) / length * u)[None], 2 * ps, 0).astype(np.float16)
+    k[5] = (0.5 * gap * math.sqrt(d) / length * u).astype(np.float16)
+    v = np.repeat(8 * rng.standard_normal((1, hkv, d)), 2 * ps, 0).astype(np.float16)
+    v[5] = rng.standard_normal((hkv, d)).astype(np.float16)
+    slots = torch.arange(2 * ps, dtype=torch.int32, device="cuda")
+    cache.append(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), slots)
+    table = torch.ones(1, pages, dtype=torch.int32, device="cuda")
+    table[0, 0] = 0
+    view = kvq.TierView(cache, table, torch.tensor([pages * ps], dtype=torch.int32, device="cuda"))
+    q = np.repeat((length * u).astype(np.float16), group, 0)[None].repeat(batch, 0)
+    qd = torch.from_numpy(np.ascontiguousarray(q)).cuda()
+    out = torch.empty_like(qd)
+    ws = torch.empty(kvq.kvq_decode_shared_workspace_size([view], [0, batch], None, batch, hkv * group),
+                     dtype=torch.uint8, device="cuda")
+    kvq.kvq_decode_attention_shared([view], [0, batch], None, qd, out, ws)
+    got = out.cpu().numpy().astype(np.float64)
+    # what the cache holds, read back (each vector rounded once more: 2^-11 of it)
+    kb, vb = (torch.empty(2 * ps, hkv, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    kvq.kvq_dequantize(cache.struct, slots, kb, vb)
+    kb, vb = kb.cpu().numpy().astype(np.float64), vb.cpu().numpy().astype(np.float64)
+    for h in range(0, hkv, 7):
+        s = kb[:, h] @ q[0, h * group].astype(np.float64) / math.sqrt(d)
+        count = np.array([1.0] * ps + [float(pages - 1)] * ps)  # page 1's tokens, 8191 times
+        p = count * np.exp(s - s.max())
+        tail = 1.0 - p[5] / p.sum()
+        assert 1e-3 < tail < 6e-3, tail
+        want = (p / p.sum()) @ vb[:, h]
+        for b in (0, batch - 1):
+            off = np.linalg.norm(got[b, h * group:(h + 1) * group] - want, axis=-1)
+            # scores near +-8.8 nats: queries and keys rounded, together 4 u of a score at most, move the
+            # tail's share by 2 * 8.9 * 4 u = 3.5% of itself, 0.1% of the output
+            limit = (2.0 ** -9 + 2.0 ** -7) * np.linalg.norm(vb[5, h]) + 0.035 * tail * np.linalg.norm(vb[0, h])
+            assert np.all(off <= limit), (off.max(), limit, tail * np.linalg.norm(vb[0, h]))
+
+
+def test_a_tier_without_pages_is_reported():
+    """A prefix tier whose table has no columns: a length above zero is out of range, and the other
+    tiers are attended as if it were not there."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["fp16", "fp16"], [[300], [0]], [0, 3], ["fp16"], [[4, 4, 4]], hq=2, hkv=2, seed=16)
+    empty = kvq.TierView(c.prefix[1].cache, torch.zeros(1, 0, dtype=torch.int32, device="cuda"),
+                         torch.zeros(1, dtype=torch.int32, device="cuda"))
+    q, out = torch.from_numpy(c.q).cuda(), torch.empty(c.q.shape, dtype=torch.float16, device="cuda")
+    pre = [c.prefix[0], empty]
+    ws = torch.empty(kvq.kvq_decode_shared_workspace_size(pre, [0, 3], c.own, 3, 2), dtype=torch.uint8, device="cuda")
+    status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    for length, bits in ((0, 0), (1, kvq.DEVERR_SEQ_LEN), (-1, kvq.DEVERR_SEQ_LEN), (0, 0)):
+        empty.seq_lens.fill_(length)
+        kvq.kvq_decode_attention_shared(pre, [0, 3], c.own, q, out, ws, status)
+        assert int(status.item()) == bits
+        c.check(out.cpu().numpy())
+
+
+def test_status_of_many_sequences():
+    """A length out of range is found wherever it stands among 2000 sequences."""
+    torch, kvq = modules()
+    batch = 2000
+    c = Case(kvq, torch, ["fp8_int4"], [[40]], [0, batch], ["fp8_int4"], [[1] * batch], hq=1, hkv=1, seed=17)
+    q, out = torch.from_numpy(c.q).cuda(), torch.empty(c.q.shape, dtype=torch.float16, device="cuda")
+    ws = torch.empty(kvq.kvq_decode_shared_workspace_size(c.prefix, c.offsets, c.own, batch, 1), dtype=torch.uint8,
+                     device="cuda")
+    status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    lens = c.own[0].seq_lens
+    for at in (None, 0, 777, batch - 1):
+        if at is not None:
+            lens[at] = -3
+        kvq.kvq_decode_attention_shared(c.prefix, c.offsets, c.own, q, out, ws, status)
+        assert int(status.item()) == (0 if at is None else kvq.DEVERR_SEQ_LEN)
+        if at is not None:
+            lens[at] = 1
