@@ -352,8 +352,10 @@ KVQ_API kvq_status kvq_rope_append(const kvq_cache* cache, const kvq_rope* rope,
  * Keys with a residual sketch come back as code part plus the sketch's estimate of the
  * residual, ||r~|| sqrt(pi/2) / KVQ_QJL_DIM * sum_j z_j S_j, whose inner product with a query
  * is what decode adds; keys with an outlier stream with q_j s added at their channels.
- * The cache's sign vectors must be 16-byte aligned (else KVQ_ERR_INVALID_ARGUMENT).
- * Arithmetic in float32, rounded once to fp16.  One launch. */
+ * The cache's sign vectors must be 16-byte aligned (else KVQ_ERR_INVALID_ARGUMENT), and
+ * num_tokens x num_kv_heads at most 2^32.  Arithmetic in float32 (on the tensor cores with
+ * stored values and centroids as sums of two fp16 numbers: 2^-22), rounded once to fp16.  One
+ * launch. */
 KVQ_API kvq_status kvq_dequantize(const kvq_cache* cache, const int32_t* slots, int32_t num_tokens, uint16_t* k_out,
                                   uint16_t* v_out, void* stream);
 

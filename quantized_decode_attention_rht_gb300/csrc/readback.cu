@@ -1,18 +1,20 @@
 // Cached tokens read back as fp16 vectors (kvq_dequantize).
 //
-// The mirror image of the append's per-thread kernel: D / 32 neighbouring lanes share a
-// vector, each decoding 32 neighbouring coordinates of the stored row; five Walsh-Hadamard
-// stages run in its registers, one transpose through shared memory hands it runs of
-// R = 32 / (lanes per vector) coordinates at every multiple of 32, the remaining stages run
-// on those, and each run is stored with the signs and 1 / sqrt(D) applied.  Stage order does
-// not matter (the stages commute), so no exchange between lanes is needed beyond the one
-// transpose.  Codebook centroids come from a 16-entry shared table: 16 words in 16 banks, so
-// a warp's lookups never conflict whatever the codes.  Four blocks of 256 threads an SM (64
-// registers; three, at 80, took 98.7 us instead of 93.9 for 65536 tokens x 8 heads of fp8 keys and
-// INT4 values, 59% of the measured copy rate).  What bounds it is the shared-memory pipe: per
-// vector of 128 coordinates, 8 wavefronts of transpose, 4 of table look-ups and 2 to 3 of rows
-// in and out, against 14 cycles of an SM's share of the memory rate.  (Prefetching the next
-// vector's row into L2 cost more than it hid: 102 us.)
+// With the stored rotated vector x~ = H s x / sqrt(D), x = s H x~ / sqrt(D).  H is a product of
+// one butterfly stage per bit of the coordinate's index, in any order: four of them (the two
+// that a lane number selects and two inside a lane) are one product with the 16 x 16 matrix
+// (-1)^popc(m & k) on the tensor cores, the others run on the product's float32 results in
+// registers.  A warp takes eight vectors (head_dim 256: four, their halves being columns of
+// their own) of one head and neighbouring tokens; the product's operand and result layouts
+// make every lane read 2 x 2T neighbouring coordinates (T = 8 result tiles; 4 for head_dim 64) of
+// one vector and end with 2T neighbouring ones of two, so nothing passes through shared memory.
+//
+// The product multiplies fp16 and adds in float32.  Nothing is lost: fp16 and fp8 rows are fp16
+// values; an INT4 level times its scale and a centroid are the sum of two fp16 numbers, the
+// first the nearest one (levels exactly, centroids to 2^-22), and go in as two products.
+// Norms and 1 / sqrt(D) are applied in float32 behind it.
+//
+// What bounds it is memory: the next vectors' rows are on their way while these are worked on.
 #include <algorithm>
 
 #include "api_checks.cuh"
@@ -61,8 +63,7 @@ __device__ __forceinline__ void decode_codes(const uint8_t* row, const float* ce
 }
 
 // The thread's coordinates [32 sub, 32 sub + 32) of the rotated vector.
-// EXTRA: keys with a residual sketch or an outlier stream, which need more registers.
-template <int TPV, bool EXTRA>
+template <int TPV>
 __device__ __forceinline__ void decode_row(const ReadSide& s, size_t prow, int sub, const float* cent,
                                            float (&y)[32]) {
   constexpr int D = 32 * TPV;
@@ -112,14 +113,14 @@ __device__ __forceinline__ void decode_row(const ReadSide& s, size_t prow, int s
   if (s.bits == 4) decode_codes<4>(row + 16 * sub, cent, y);
   else if (s.bits == 3) decode_codes<3>(row + 12 * sub, cent, y);
   else decode_codes<2>(row + 8 * sub, cent, y);
-  if (!EXTRA || s.fmt == KVQ_FMT_CODEBOOK) scale = __half2float(s.aux[prow]);
+  if (s.fmt == KVQ_FMT_CODEBOOK) scale = __half2float(s.aux[prow]);
   else if (s.fmt == KVQ_FMT_CODEBOOK_QJL) scale = __half2float(s.aux[2 * prow]);
   else scale = __half2float(*reinterpret_cast<const __half*>(reinterpret_cast<const uint8_t*>(s.aux) +
                                                              prow * (4 + KVQ_OUTLIER_CHANNELS)));
   scale *= inv_sqrt_dim(D);
 #pragma unroll
   for (int e = 0; e < 32; ++e) y[e] *= scale;
-  if (EXTRA && s.fmt == KVQ_FMT_CODEBOOK_QJL) {
+  if (s.fmt == KVQ_FMT_CODEBOOK_QJL) {
     // + ||r|| sqrt(pi / 2) / m * sum_j z_j S_j: the projection rows stay in L1 / L2
     const float c = __half2float(s.aux[2 * prow + 1]) * (1.2533141373155003f / KVQ_QJL_DIM);
     const uint32_t* z = reinterpret_cast<const uint32_t*>(row + D * s.bits / 8);
@@ -143,8 +144,12 @@ __device__ __forceinline__ void decode_row(const ReadSide& s, size_t prow, int s
   }
 }
 
-template <int TPV, bool EXTRA>
-__global__ void __launch_bounds__(kThreads, EXTRA ? 2 : 4) read_kernel(const ReadParams p) {
+// Caches whose keys carry a residual sketch or an outlier stream: D / 32 neighbouring lanes share a
+// vector, each decoding 32 neighbouring coordinates (and adding the sketch's estimate to them);
+// five stages run in its registers, one transpose through shared memory hands it the runs for the
+// others.  Bounded by the sketch's arithmetic (128 projection rows a vector).
+template <int TPV>
+__global__ void __launch_bounds__(kThreads, 2) read_extra_kernel(const ReadParams p) {
   constexpr int D = 32 * TPV, R = 32 / TPV, VPB = kThreads / TPV;
   extern __shared__ __align__(16) float area_all[];  // D floats per vector of the block
   __shared__ float cent[16];
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, EXTRA ? 2 : 4) read_kernel(const Rea
     const int page = p.page_shift >= 0 ? slot >> p.page_shift : slot / p.page_size;
     const size_t prow = ((size_t)page * p.hkv + h) * p.page_size + (slot - page * p.page_size);
     float y[32];
-    decode_row<TPV, EXTRA>(side, prow, sub, cent, y);
+    decode_row<TPV>(side, prow, sub, cent, y);
     // index bits 0 .. 4
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, EXTRA ? 2 : 4) read_kernel(const Rea
       const uint32_t neg = (sw[e / 4] << (24 - 8 * (e % 4))) & 0x80000000u;
       y[e] = __uint_as_float(__float_as_uint(y[e] * inv) ^ neg);
     }
-    if (EXTRA && side.fmt == KVQ_FMT_CODEBOOK_OUTLIER) {  // + q_j s at channel c_j
+    if (side.fmt == KVQ_FMT_CODEBOOK_OUTLIER) {  // + q_j s at channel c_j
       const uint8_t* rec = reinterpret_cast<const uint8_t*>(side.aux) + prow * (4 + KVQ_OUTLIER_CHANNELS);
       const float s = __half2float(*reinterpret_cast<const __half*>(rec + 2));
       for (int j = 0; j < KVQ_OUTLIER_CHANNELS; ++j) {
@@ -255,17 +260,317 @@ __global__ void __launch_bounds__(kThreads, EXTRA ? 2 : 4) read_kernel(const Rea
   }
 }
 
-template <int TPV>
+// ------------------------------------------------------------------------ plain formats
+enum { R_F16, R_F8, R_I4, R_C4, R_C3, R_C2 };
+constexpr int kReadThreads = 128, kReadBlocks = 6;  // blocks an SM
+
+__host__ __device__ constexpr int code_bits(int kind) { return kind == R_C4 ? 4 : (kind == R_C3 ? 3 : 2); }
+// Bytes of a lane's coordinates in a row, and the registers that hold them.
+__host__ __device__ constexpr int lane_bytes(int kind, int n) {
+  return kind == R_F16 ? 2 * n : (kind == R_F8 ? n : (kind == R_I4 || kind == R_C4 ? n / 2 : n * code_bits(kind) / 8));
+}
+__host__ __device__ constexpr int lane_words(int kind, int n) { return (lane_bytes(kind, n) + 3) / 4; }
+
+template <int BYTES>
+__device__ __forceinline__ void load_bytes(const uint8_t* src, uint32_t* w) {
+  if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+      w[4 * i] = u.x;
+      w[4 * i + 1] = u.y;
+      w[4 * i + 2] = u.z;
+      w[4 * i + 3] = u.w;
+    }
+  } else if constexpr (BYTES == 8) {
+    const uint2 u = __ldcs(reinterpret_cast<const uint2*>(src));
+    w[0] = u.x;
+    w[1] = u.y;
+  } else if constexpr (BYTES % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 4; ++i) w[i] = __ldcs(reinterpret_cast<const uint32_t*>(src) + i);
+  } else {  // 6 bytes: 3-bit codes of head_dim 64
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
+    w[0] = (uint32_t)__ldcs(h) | ((uint32_t)__ldcs(h + 1) << 16);
+    w[1] = __ldcs(h + 2);
+  }
+}
+
+__device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+
+// The operand words of coordinates (c, c + 2T) of the lane: their fp16 value, or the nearest one
+// (hi) and the rest (lo).  w: the lane's packed coordinates; scale: INT4's, twice.
+template <int KIND, int T>
+__device__ __forceinline__ void operand(const uint32_t* w, int c, __half2 scale, const uint32_t* table, uint32_t& hi,
+                                        uint32_t& lo) {
+  if constexpr (KIND == R_F16) {
+    hi = __byte_perm(w[c / 2], w[c / 2 + T], c % 2 ? 0x7632 : 0x5410);
+  } else if constexpr (KIND == R_F8) {
+    const uint32_t two = __byte_perm(w[c / 4], w[c / 4 + T / 2], (uint32_t)(c % 4) | ((uint32_t)(c % 4 + 4) << 4));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)two));
+  } else if constexpr (KIND == R_I4) {
+    constexpr int kFar = T == 8 ? 2 : 1;  // words from c's to (c + 2T)'s
+    const uint32_t both = __byte_perm(w[c / 8], w[c / 8 + kFar], c % 8 < 4 ? 0x5410 : 0x7632);
+    const __half2 level = __hsub2(half2_of(((both >> (4 * (c % 4))) & 0x000F000Fu) | 0x64006400u),
+                                  __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
+    const __half2 x = __hmul2(level, scale);
+    hi = bits_of(x);
+    lo = bits_of(__hfma2(level, scale, __hneg2(x)));  // exact: 15 bits of product, 11 taken
+  } else {
+    constexpr int B = code_bits(KIND);
+    uint32_t e[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = (c + 2 * T * i) * B;
+      const uint32_t f = at % 32 + B <= 32 ? w[at / 32] >> (at % 32) : __funnelshift_r(w[at / 32], w[at / 32 + 1], at % 32);
+      e[i] = table[f & ((1u << B) - 1u)];
+    }
+    hi = __byte_perm(e[0], e[1], 0x5410);
+    lo = __byte_perm(e[0], e[1], 0x7632);
+  }
+}
+
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 2 x 16 bytes, in one store where the address allows it.
+__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&w)[8], bool aligned32) {
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// Lane (g, q) = (lane / 4, lane % 4).  With k the bits of a row of the operand and m those of a
+// result row, k bit 0 (the two halves of a word) is coordinate bit log2(2T), k bits 1, 2 (q) the
+// two bits above it, k bit 3 (the two words) coordinate bit log2(T), the tile the bits below:
+// lane q reads coordinates [4T q, 4T q + 4T) of column g's vector, and result rows g and g + 8 of
+// all tiles are coordinates [2T g, 2T g + 2T) of columns 2q and 2q + 1.
+template <int D, int KIND>
+__device__ __forceinline__ void read_side(const ReadParams& p, const ReadSide& side, uint32_t* table) {
+  constexpr int T = D == 64 ? 4 : 8, kRun = 4 * T, kWords = lane_words(KIND, kRun);
+  constexpr int kHalves = D == 256 ? 2 : 1, kTokens = 8 / kHalves;  // columns a token takes, tokens of a warp
+  constexpr bool kCodes = KIND >= R_C4;
+  constexpr float inv = inv_sqrt_dim(D);
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  float unit = inv;
+  if constexpr (kCodes) {
+    // centroids times a power of two that takes the largest to [2^9, 2^10): neither part leaves
+    // fp16's normal range, unless it is below 2^-10 of the largest centroid's rounding
+    constexpr int n = 1 << code_bits(KIND);
+    float most = 0.f;
+    for (int i = 0; i < n; ++i) most = fmaxf(most, fabsf(__ldg(side.cent + i)));
+    int e = 0;
+    if (most > 0.f && most < INFINITY) frexpf(most, &e);
+    const int up = max(-100, min(100, 10 - e));
+    if (threadIdx.x < n) {
+      const float c = ldexpf(__ldg(side.cent + threadIdx.x), up);
+      const __half hi = __float2half_rn(c);
+      table[threadIdx.x] = bits_of(__halves2half2(hi, __float2half_rn(c - __half2float(hi))));
+    }
+    unit = inv * inv * ldexpf(1.0f, -up);
+    __syncthreads();
+  }
+  // rows g and g + 8, columns (2q, 2q + 1) and those + 8 of (-1)^popc(m & k)
+  uint32_t a[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = g + (i & 1) * 8, k = 2 * q + (i >> 1) * 8;
+    a[i] = 0x3C003C00u | ((uint32_t)(__popc(m & k) & 1) << 15) | ((uint32_t)(__popc(m & (k + 1)) & 1) << 31);
+  }
+  const int my_token = g / kHalves, my_half = kHalves == 2 ? g & 1 : 0;
+  const bool wide = (reinterpret_cast<uintptr_t>(side.out) & 31) == 0;
+  // Items: kTokens tokens of a head; neighbouring warps take neighbouring heads of the same tokens.
+  // (below 2^32, as the host checks; the step in tokens and heads is divided out once)
+  const uint32_t hkv = p.hkv, stride = gridDim.x * (kReadThreads / 32);
+  const uint32_t step_tokens = stride / hkv * kTokens, step_heads = stride % hkv;
+  struct At {
+    long long token;  // the first
+    uint32_t head;
+  };
+  auto advance = [&](At& at) {
+    at.token += step_tokens;
+    if ((at.head += step_heads) >= hkv) {
+      at.head -= hkv;
+      at.token += kTokens;
+    }
+  };
+  auto slot_of = [&](const At& at) -> int {
+    const long long t = at.token + my_token;
+    const int slot = t < p.num_tokens ? __ldg(p.slots + t) : -1;
+    return slot < p.num_slots ? slot : -1;
+  };
+  struct Fetched {
+    uint32_t w[kWords + (KIND == R_C3 ? 1 : 0)];
+    __half aux;
+  };
+  auto fetch = [&](const At& at, int slot, Fetched& f) {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(f.w) / 4); ++i) f.w[i] = 0u;
+    f.aux = __ushort_as_half(0);
+    if (slot < 0) return;
+    const int page = p.page_shift >= 0 ? slot >> p.page_shift : slot / p.page_size;
+    const size_t prow = ((size_t)page * p.hkv + at.head) * p.page_size + (slot - page * p.page_size);
+    const int part = 4 * my_half + q;  // of the row, in runs
+    load_bytes<lane_bytes(KIND, kRun)>(side.rows + prow * side.row_bytes + part * lane_bytes(KIND, kRun), f.w);
+    if constexpr (KIND == R_I4) f.aux = side.aux[prow * (D / kGroup) + part * kRun / kGroup];
+    if constexpr (kCodes) f.aux = side.aux[prow];
+  };
+
+  const uint32_t first = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5);
+  At here = {(long long)(first / hkv) * kTokens, first % hkv}, then = here, later;
+  advance(then);
+  int slot = slot_of(here), next_slot = slot_of(then);
+  Fetched cur, next;
+  fetch(here, slot, cur);
+  while (here.token < p.num_tokens) {
+    fetch(then, next_slot, next);
+    later = then;
+    advance(later);
+    const int after = slot_of(later);
+    const uint32_t there = __ballot_sync(0xFFFFFFFFu, slot >= 0);
+    __half2 scale = __half2half2(cur.aux);
+    uint32_t big = 0;  // lanes of vectors with a scale whose products could leave fp16: an eighth of it
+    if constexpr (KIND == R_I4) {
+      big = __ballot_sync(0xFFFFFFFFu, __half2float(cur.aux) > 8000.0f);
+      constexpr uint32_t kOwn = kHalves == 2 ? 0xFFu : 0xFu;
+      if (big & (kOwn << (4 * (g / kHalves * kHalves)))) scale = __hmul2(scale, __float2half2_rn(0.125f));
+    }
+    float c[T][4];
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      uint32_t h0, h1, l0, l1;
+      operand<KIND, T>(cur.w, t, scale, table, h0, l0);
+      operand<KIND, T>(cur.w, t + T, scale, table, h1, l1);
+      c[t][0] = c[t][1] = c[t][2] = c[t][3] = 0.f;
+      mma16(c[t], a, h0, h1);
+      if constexpr (KIND >= R_I4) mma16(c[t], a, l0, l1);
+    }
+    u64 y[2][T];  // result rows g, g + 8: columns (2q, 2q + 1)
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      y[0][t] = pk(c[t][0], c[t][1]);
+      y[1][t] = pk(c[t][2], c[t][3]);
+    }
+#pragma unroll
+    for (int hs = 1; hs < T; hs <<= 1) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          if ((t & hs) == 0) {
+            const u64 u = y[i][t], v = y[i][t + hs];
+            y[i][t] = add2(u, v);
+            y[i][t + hs] = sub2(u, v);
+          }
+        }
+      }
+    }
+    // what the columns are multiplied by
+    float s0 = unit, s1 = unit;
+    if constexpr (kCodes) {
+      s0 *= __shfl_sync(0xFFFFFFFFu, __half2float(cur.aux), 8 * q);
+      s1 *= __shfl_sync(0xFFFFFFFFu, __half2float(cur.aux), 8 * q + 4);
+    }
+    if constexpr (KIND == R_I4) {
+      if (kHalves == 2) {
+        if (big & (0xFFu << (8 * q))) s0 = s1 = 8.0f * unit;
+      } else {
+        if (big & (0xFu << (8 * q))) s0 = 8.0f * unit;
+        if (big & (0xFu << (8 * q + 4))) s1 = 8.0f * unit;
+      }
+    }
+    const u64 s2 = pk(s0, s1);
+    const uint32_t h = here.head;
+    float z[2][2 * T];  // the columns' runs
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        float u, v;
+        upk(mul2(y[i][t], s2), u, v);
+        z[0][i * T + t] = kHalves == 2 ? u + v : u;  // the stage of coordinate bit 7
+        z[1][i * T + t] = kHalves == 2 ? u - v : v;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int token = kHalves == 2 ? q : 2 * q + k, at = (kHalves == 2 ? k * 128 : 0) + 2 * T * g;
+      uint32_t sw[T / 2];  // sign bytes of the run
+      const int8_t* signs = side.signs + (size_t)h * D + at;
+      if constexpr (T == 8) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(signs));
+        sw[0] = u.x;
+        sw[1] = u.y;
+        sw[2] = u.z;
+        sw[3] = u.w;
+      } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(signs));
+        sw[0] = u.x;
+        sw[1] = u.y;
+      }
+      uint32_t w[T];
+#pragma unroll
+      for (int j = 0; j < T; ++j) {
+        const __half2 h2 = __floats2half2_rn(z[k][2 * j], z[k][2 * j + 1]);
+        w[j] = bits_of(h2) ^ (__byte_perm(sw[j >> 1], 0, (j & 1) ? 0x3424 : 0x1404) & 0x80008000u);
+      }
+      if (!((there >> (4 * kHalves * token)) & 1u)) continue;
+      uint16_t* dst = side.out + ((size_t)(here.token + token) * hkv + h) * D + at;
+      if constexpr (T == 8) store32(dst, w, wide);
+      else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    here = then;
+    then = later;
+    cur = next;
+    slot = next_slot;
+    next_slot = after;
+  }
+}
+
+// Grid row blockIdx.y: side kind_first + y.
+template <int D>
+__global__ void __launch_bounds__(kReadThreads, kReadBlocks) read_kernel(const ReadParams p) {
+  __shared__ uint32_t table[16];
+  const ReadSide& side = p.side[p.kind_first + blockIdx.y];
+  switch (side.fmt) {
+    case KVQ_FMT_FP16: read_side<D, R_F16>(p, side, table); break;
+    case KVQ_FMT_FP8_E4M3: read_side<D, R_F8>(p, side, table); break;
+    case KVQ_FMT_INT4_G32: read_side<D, R_I4>(p, side, table); break;
+    default:
+      if (side.bits == 4) read_side<D, R_C4>(p, side, table);
+      else if (side.bits == 3) read_side<D, R_C3>(p, side, table);
+      else read_side<D, R_C2>(p, side, table);
+  }
+}
+
+template <int D>
 cudaError_t launch_read(const ReadParams& p, int sides, int sms, cudaStream_t stream) {
-  constexpr int VPB = kThreads / TPV;
-  const long long nvec = (long long)p.num_tokens * p.hkv;
-  const long long blocks = std::max<long long>(1, std::min<long long>((nvec + VPB - 1) / VPB, sms * 4LL / sides));
-  const dim3 grid((unsigned)blocks, sides);
   const int kf = p.kind_first == 0 ? p.side[0].fmt : KVQ_FMT_CODEBOOK;
-  if (kf == KVQ_FMT_CODEBOOK_QJL || kf == KVQ_FMT_CODEBOOK_OUTLIER)
-    read_kernel<TPV, true><<<grid, kThreads, kXposeBytes, stream>>>(p);
-  else
-    read_kernel<TPV, false><<<grid, kThreads, kXposeBytes, stream>>>(p);
+  if (kf == KVQ_FMT_CODEBOOK_QJL || kf == KVQ_FMT_CODEBOOK_OUTLIER) {
+    if constexpr (D != 64) {  // (such keys have head_dim 128 or 256)
+      constexpr int VPB = kThreads / (D / 32);
+      const long long nvec = (long long)p.num_tokens * p.hkv;
+      const long long blocks = std::max<long long>(1, std::min<long long>((nvec + VPB - 1) / VPB, sms * 2LL / sides));
+      read_extra_kernel<D / 32><<<dim3((unsigned)blocks, sides), kThreads, kXposeBytes, stream>>>(p);
+    }
+  } else {
+    constexpr int kTokens = D == 256 ? 4 : 8, kWarps = kReadThreads / 32;
+    const long long items = ((long long)p.num_tokens + kTokens - 1) / kTokens * p.hkv;
+    const long long blocks =
+        std::max<long long>(1, std::min<long long>((items + kWarps - 1) / kWarps, (long long)sms * kReadBlocks / sides));
+    read_kernel<D><<<dim3((unsigned)blocks, sides), kReadThreads, 0, stream>>>(p);
+  }
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) note_launch();
   return e;
@@ -314,10 +619,11 @@ extern "C" KVQ_API kvq_status kvq_dequantize(const kvq_cache* cache, const int32
   p.kind_first = k_out ? 0 : 1;
   const int sides = (k_out && v_out) ? 2 : 1, sms = device_sms();
   if (p.num_slots == 0) return KVQ_OK;
+  if ((long long)num_tokens * c->num_kv_heads > (1LL << 32)) return KVQ_ERR_INVALID_ARGUMENT;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (c->head_dim == 64) e = launch_read<2>(p, sides, sms, s);
-  else if (c->head_dim == 128) e = launch_read<4>(p, sides, sms, s);
-  else e = launch_read<8>(p, sides, sms, s);
+  if (c->head_dim == 64) e = launch_read<64>(p, sides, sms, s);
+  else if (c->head_dim == 128) e = launch_read<128>(p, sides, sms, s);
+  else e = launch_read<256>(p, sides, sms, s);
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
