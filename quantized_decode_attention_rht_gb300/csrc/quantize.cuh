@@ -131,6 +131,16 @@ __device__ void build_table(Table& t, float2* cells, const float* bounds, const 
   __syncthreads();
 }
 
+// A vector whose sum of squares is not finite has no codes (the table has no cell for a NaN, and its
+// look-up would leave shared memory): its coordinates count as zero, and the stored norm tells.
+template <int E>
+__device__ __forceinline__ void zero_unless_finite(float ss, float (&y)[E]) {
+  if (!(ss < INFINITY)) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = 0.f;
+  }
+}
+
 // 12582912 = 1.5 * 2^23: adding it rounds t (|t| < 2^22) to the integer held in the low
 // mantissa bits, 0x4B400000 + rint(t).
 constexpr float kMagic = 12582912.0f;
@@ -414,6 +424,7 @@ __device__ __forceinline__ void quantize_vector(const QuantParams& p, const Quan
     const float ny = sqrtf(ss);
     const float inv = ny > 0.0f ? sqrt_d / ny : 0.0f;  // u = sqrt(D) y / ||y||
     const __half norm16 = __float2half_rn(ny * inv_sqrt_d);
+    zero_unless_finite(ss, y);
     if constexpr (FMT == F_CB) {
       encode_codebook<BITS, kE>(table, y, inv * table.inv_w, row + sub * (kE * BITS / 8), store);
       if (store && sub == 0) side.aux[prow] = norm16;

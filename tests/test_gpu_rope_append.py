@@ -218,3 +218,45 @@ def test_capture_and_replay():
         slots += t
     torch.cuda.synchronize()
     assert torch.equal(eager.k_rows, graphed.k_rows) and torch.equal(eager.v_rows, graphed.v_rows)
+
+
+@pytest.mark.parametrize("fmt", FORMATS, ids=lambda f: f"{f[0]}{f[1] or ''}_{f[2]}{f[3] or ''}")
+@pytest.mark.parametrize("d,t,hkv", [(64, 40, 3), (64, 5601, 3), (128, 40, 3), (128, 2049, 9), (256, 2050, 9)])
+def test_values_that_are_not_finite_stay_in_their_vector(fmt, d, t, hkv):
+    """Infinities and NaN in some vectors: every other vector's row is what it is without them, in
+    both kinds of append (kvq_quantize_append too), and a codebook's norm tells which are bad."""
+    torch, kvq = gu.torch_cuda(), gu.kvq_module()
+    kf, kb, vf, vb = fmt
+    rng = np.random.default_rng(d + t)
+    x = rng.standard_normal((t, hkv, d)).astype(np.float16)
+    bad = [(0, 0), (1, hkv - 1), (t // 2, 1), (t - 1, hkv - 1)]
+    y = x.copy()
+    for (i, h), v in zip(bad, (np.nan, np.inf, -np.inf, np.nan)):
+        y[i, h, int(rng.integers(d))] = v
+    y[t // 2, 1, :2] = np.inf, -np.inf
+    pos = torch.from_numpy(rng.integers(0, 1 << 16, t).astype(np.int32)).cuda()
+    ks, vs = (np.where(rng.integers(0, 2, (hkv, d)) == 0, 1, -1).astype(np.int8) for _ in range(2))
+    pages = (t + 15) // 16
+    slots = torch.arange(t, dtype=torch.int32, device="cuda")
+    rope = make_rope(kvq, d, "half")
+    for fused in (True, False):
+        got = []
+        for z in (x, y):
+            cache = kvq.PagedCache(d, hkv, pages, kf, vf, kb, vb, ks, vs)
+            zd = torch.from_numpy(z).cuda()
+            if fused:
+                kvq.kvq_rope_append(cache.struct, rope, pos, zd, zd, slots)
+            else:
+                cache.append(zd, zd, slots)
+            torch.cuda.synchronize()
+            got.append([None if a is None else gu.pool_rows(a, np.arange(t))
+                        for a in (cache.k_rows, cache.v_rows, cache.k_aux, cache.v_aux)])
+        well = np.ones((t, hkv), bool)
+        for i, h in bad:
+            well[i, h] = False
+        for side, (a, b) in enumerate(zip(*got)):
+            if a is None:
+                continue
+            assert np.array_equal(a[well].view(np.uint8), b[well].view(np.uint8))
+            if side >= 2 and (kf, vf)[side - 2] == "codebook":
+                assert not np.isfinite(b[~well].astype(np.float32)).any()
