@@ -15,6 +15,9 @@
 // Norms and 1 / sqrt(D) are applied in float32 behind it.
 //
 // What bounds it is memory: the next vectors' rows are on their way while these are worked on.
+// 65536 tokens x 8 heads of fp8 keys and INT4 values (373 MB): 67.8 us, 81% of the measured copy rate,
+// with six blocks of 128 threads an SM (80 registers; five 71.5, eight, which spill, 91.4).  With the
+// transposes in shared memory it took 93.5.
 #include <algorithm>
 
 #include "api_checks.cuh"
