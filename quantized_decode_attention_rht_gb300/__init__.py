@@ -392,7 +392,7 @@ def kvq_rope_apply(rope: "Rope", positions, q, k=None, q_out=None, k_out=None, t
     _int_vector(positions, "positions", t)
     status = (_lib_handle or lib()).kvq_rope_apply(
         rope.reference, positions.data_ptr(), _heads(q, qs, qo, qos), None if k is None else _heads(k, ks, ko, kos), t, d,
-        1 if transpose else 0, _call_stream(stream, q, k, q_out, k_out, positions))
+        1 if transpose else 0, _call_stream(stream, q, k, q_out, k_out, positions, rope.turns))
     if status:
         raise KvqError(status, "kvq_rope_apply")
 
@@ -416,7 +416,7 @@ def kvq_rope_append(cache: KvqCache, rope: "Rope", positions, k, v, slot_mapping
     status = (_lib_handle or lib()).kvq_rope_append(
         ctypes.byref(cache), rope.reference, positions.data_ptr(), None if k is None else _heads(k, ks, None, None),
         None if v is None else _heads(v, vs, None, None), None if q is None else _heads(q, qs, qo, qos), t,
-        slot_mapping.data_ptr(), _call_stream(stream, positions, k, v, q, q_out, slot_mapping))
+        slot_mapping.data_ptr(), _call_stream(stream, positions, k, v, q, q_out, slot_mapping, rope.turns))
     if status:
         raise KvqError(status, "kvq_rope_append")
 

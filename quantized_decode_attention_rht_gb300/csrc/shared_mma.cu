@@ -464,13 +464,17 @@ __device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, int 
   }
 }
 
-// The scale of a codebook's table, out of 2^(k / 128) / 16, k < 128: the one whose fp16 roundings
-// are smallest, by the sum of squares of their relative errors.  c: centroid `lane` in every
+// The scale of a codebook's table, out of 128 steps of 2^(1 / 128) that bring its largest magnitude
+// to 2^-3 .. 2^-1: the one whose fp16 roundings are smallest, by the sum of squares of their
+// relative errors.  c: centroid `lane` in every
 // lane (0 beyond the codebook); the side's four warps, a candidate a thread.
 __device__ __forceinline__ float scale_table(Ctl* ctl, float c, int bits, int side, int tid) {
   const int lane = tid & 31, warp = tid >> 5;
   const float over = c != 0.f ? __fdividef(1.0f, c) : 0.f;
-  const float mine = exp2f((float)tid * (1.0f / 128.0f)) * 0.0625f;
+  const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(c)));
+  // 2^-3 over the largest magnitude's power of two
+  const float unit = __uint_as_float((251u - min(max(most >> 23, 2u), 249u)) << 23);
+  const float step = exp2f((float)tid * (1.0f / 128.0f)), mine = step * unit;
   float least = 0.f;
   int at = tid;
 #pragma unroll 4
@@ -479,7 +483,7 @@ __device__ __forceinline__ float scale_table(Ctl* ctl, float c, int bits, int si
     const float off = (__half2float(__float2half_rn(x)) - x) * __shfl_sync(0xFFFFFFFFu, over, i);
     least = fmaf(off, off, least);
   }
-  least = __fdividef(least, mine * mine);
+  least = __fdividef(least, step * step);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float other = __shfl_xor_sync(0xFFFFFFFFu, least, o);
@@ -503,7 +507,7 @@ __device__ __forceinline__ float scale_table(Ctl* ctl, float c, int bits, int si
       at = k;
     }
   }
-  const float beta = exp2f((float)at * (1.0f / 128.0f)) * 0.0625f;
+  const float beta = exp2f((float)at * (1.0f / 128.0f)) * unit;
   if (tid == 0) ctl->unscale[side] = inv_sqrt_dim(kDim) / beta;
   return beta;
 }

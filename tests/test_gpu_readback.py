@@ -141,3 +141,56 @@ def test_write_then_read():
         err = ((2 * math.log2(d) + 4) * 2.0 ** -24 * np.sum(np.abs(x), -1, keepdims=True)
                + np.sum(2.0 ** -11 * rot + 2.0 ** -25, -1, keepdims=True)) / math.sqrt(d)
         assert np.all(np.abs(got.cpu().numpy() - x) <= err * (1 + 2.0 ** -9) + 2.0 ** -11 * np.abs(x) * (1 + 2.0 ** -9) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_int4_scales_near_the_largest(d):
+    """Vectors along the signs put everything in one coordinate, 25000 sqrt(D): scales whose products
+    with a level pass fp16's largest number, beside small ones."""
+    torch, kvq = gu.torch_cuda(), gu.kvq_module()
+    rng = np.random.default_rng(d)
+    n, hkv, ps = 37, 3, 16
+    ks, vs = (np.where(rng.integers(0, 2, (hkv, d)) == 0, 1, -1).astype(np.int8) for _ in range(2))
+    k, v = (rng.standard_normal((n, hkv, d)).astype(np.float16) for _ in range(2))
+    for i in range(0, n, 3):
+        v[i] = (25000.0 if i % 2 else 12000.0) * vs
+    b = gu.build_exact(kvq, torch, [SPECS["fp8_int4"]], [[(k, v)]], ks, vs, ps, shuffle_seed=d)
+    tier = b.ora[0]
+    assert np.max(np.asarray(tier.v.aux).astype(np.float64)) > 8000
+    t = np.arange(n)
+    slots = (tier.block_table[0][t // ps] * ps + t % ps).astype(np.int32)
+    out = torch.empty((n, hkv, d), dtype=torch.float16, device="cuda")
+    kvq.kvq_dequantize(b.gpu[0].struct, torch.from_numpy(slots).cuda(), None, out)
+    got = out.cpu().numpy()
+    assert np.isfinite(got).all()
+    check(got, tier.v, slots, ps)
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4])
+@pytest.mark.parametrize("power", [-30, -7, 9, 30])
+def test_codebooks_of_any_size(bits, power):
+    """Centroids times a power of two, norms over it: the same vectors, to the bit."""
+    torch, kvq = gu.torch_cuda(), gu.kvq_module()
+    rng = np.random.default_rng(bits)
+    t, hkv, d = 50, 2, 128
+    signs = np.where(rng.integers(0, 2, (hkv, d)) == 0, 1, -1).astype(np.int8)
+    cache = kvq.PagedCache(d, hkv, 4, "codebook", "codebook", bits, bits, signs, signs)
+    x = torch.from_numpy(rng.standard_normal((t, hkv, d)).astype(np.float16)).cuda()
+    slots = torch.arange(t, dtype=torch.int32, device="cuda")
+    cache.append(x, x, slots)
+    want, got = torch.empty_like(x), torch.empty_like(x)
+    kvq.kvq_dequantize(cache.struct, slots, want)
+    if abs(power) < 10:  # norms are fp16: they take the factor back while they can
+        cache.k_aux.mul_(2.0 ** -power)
+        cache.k_centroids.mul_(2.0 ** power)
+        kvq.kvq_dequantize(cache.struct, slots, got)
+        assert torch.equal(got, want)
+    else:  # the vectors leave fp16's range or its normal numbers
+        cache.k_centroids.mul_(2.0 ** power)
+        kvq.kvq_dequantize(cache.struct, slots, got)
+        scaled = want.float() * 2.0 ** power
+        if power > 0:
+            big = scaled.abs() > 65520
+            assert torch.isinf(got[big]).all()
+        else:
+            assert (got.float() - scaled).abs().max() <= 2.0 ** -24

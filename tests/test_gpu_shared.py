@@ -408,3 +408,18 @@ def test_status_of_many_sequences():
         assert int(status.item()) == (0 if at is None else kvq.DEVERR_SEQ_LEN)
         if at is not None:
             lens[at] = 1
+
+
+@pytest.mark.parametrize("power", [-9, 7])
+@pytest.mark.parametrize("name", ["cb4", "cb23"])
+def test_codebooks_of_any_size(name, power):
+    """Centroids times a power of two, norms over it: the same output, to the bit."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, [name], [[500]], [0, 3], [], [], hq=8, hkv=2, seed=18)
+    want = c.run(kvq, torch)
+    c.check(want)
+    cache = c.built.gpu[0]
+    for cent, aux in ((cache.k_centroids, cache.k_aux), (cache.v_centroids, cache.v_aux)):
+        cent.mul_(2.0 ** power)
+        aux.mul_(2.0 ** -power)
+    assert np.array_equal(c.run(kvq, torch), want)
