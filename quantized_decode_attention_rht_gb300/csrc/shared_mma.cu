@@ -1071,9 +1071,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
           if (to >= 0) reinterpret_cast<float4*>(base + to * kDim)[lane] = x;
         }
       }
-      if (out_row >= 0)
+      if (out_row >= 0) {
+        // (a row of NaN has no maximum: its partial must not pass for one without tokens)
+        const float l = unpack2(l2).x + unpack2(l2).y;
         *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) =
-            ok ? make_float2(m, unpack2(l2).x + unpack2(l2).y) : make_float2(-INFINITY, 0.f);
+            ok ? make_float2(l == l ? m : l, l) : make_float2(-INFINITY, 0.f);
+      }
     } else if (out_row >= 0) {  // a second group without a tile of its own
       *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) = make_float2(-INFINITY, 0.f);
     }

@@ -423,3 +423,58 @@ def test_codebooks_of_any_size(name, power):
         cent.mul_(2.0 ** power)
         aux.mul_(2.0 ** -power)
     assert np.array_equal(c.run(kvq, torch), want)
+
+
+@pytest.mark.parametrize("name,batch,group", [("cb4", 6, 4), ("fp8_int4", 40, 8)])
+def test_a_query_that_is_not_finite_stays_in_its_row(name, batch, group):
+    """A NaN or an infinity in one query: its own output is NaN, every other row as ever."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, [name], [[900]], [0, batch], [name], [[3] * batch], hq=2 * group, hkv=2, seed=19)
+    q = c.q.copy()
+    bad = {(1, 0): np.nan, (batch - 1, 2 * group - 1): np.inf}
+    for (b, h), v in bad.items():
+        q[b, h, 5] = v
+    out = c.run(kvq, torch, torch.from_numpy(q).cuda())
+    for b, h in bad:
+        assert np.isnan(out[b, h]).all()
+    heads = {(b, h) for b in (0, 1, batch // 2, batch - 1) for h in range(2 * group)} - set(bad)
+    c.check(out, heads)
+
+
+@pytest.mark.parametrize("name", ["fp16", "cb4"])
+@pytest.mark.parametrize("length", [1, 130, 261])
+def test_what_lies_behind_the_prefix_is_not_read(name, length):
+    """NaN in every slot of the pool that holds no token of the prefix, its last page's among them."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, [name], [[length]], [0, 3], [], [], hq=8, hkv=2, seed=length)
+    want = c.run(kvq, torch)
+    c.check(want)
+    cache, table = c.built.gpu[0], c.prefix[0].block_table.cpu().numpy()[0]
+    t = np.arange(length)
+    held = table[t // 16] * 16 + t % 16
+    free = np.setdiff1d(np.arange(cache.num_pages * 16), held)
+    pages, offs = (torch.from_numpy(x).cuda() for x in (free // 16, free % 16))
+    sides = (cache.k_rows, cache.v_rows) if name == "fp16" else (cache.k_aux, cache.v_aux)
+    for a in sides:
+        if a.dtype == torch.float16:
+            a[pages, :, offs] = float("nan")
+        else:
+            a[pages, :, offs] = 0x7E  # bytes of fp16 NaN
+    assert np.array_equal(c.run(kvq, torch), want)
+
+
+def test_one_page_many_times():
+    """A block table that names one page again and again: attention over copies of its tokens."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["fp8_int4"], [[16]], [0, 5], [], [], hq=8, hkv=2, seed=20)
+    want = c.run(kvq, torch).astype(np.float64)
+    c.check(want)
+    view = c.prefix[0]
+    many = kvq.TierView(view.cache, view.block_table[:, :1].expand(-1, 300).contiguous(),
+                        torch.full_like(view.seq_lens, 4800))
+    q = torch.from_numpy(c.q).cuda()
+    out = torch.empty_like(q)
+    ws = torch.empty(kvq.kvq_decode_shared_workspace_size([many], [0, 5], None, 5, 8), dtype=torch.uint8, device="cuda")
+    kvq.kvq_decode_attention_shared([many], [0, 5], None, q, out, ws)
+    got = out.cpu().numpy().astype(np.float64)
+    assert np.linalg.norm(got - want) <= 2.0 ** -9 * np.linalg.norm(want)
