@@ -475,15 +475,15 @@ KVQ_API kvq_status kvq_decode_attention_ex(const kvq_tier_view* tiers, int32_t n
  *                   kvq_decode_options; not written by a call with batch 0)
  * All tiers agree in head_dim, num_kv_heads, page_size and signs (else
  * KVQ_ERR_INVALID_ARGUMENT), num_prefix_tiers + num_tiers <= KVQ_MAX_TIERS, and batch x
- * num_q_heads <= 2^24 (else KVQ_ERR_UNSUPPORTED).  A call captured into a graph keeps its group offsets; lengths and
- * block tables are read when it runs.
+ * num_q_heads <= 2^24 (else KVQ_ERR_UNSUPPORTED).  A call captured into a graph keeps its group
+ * offsets; lengths and block tables are read when it runs.
  * The output is fp16, and so is what the tensor cores multiply (rotated queries, decoded rows
  * that are not fp16 values already, softmax weights), with float32 scores, sums and
  * accumulators: the output's error is a few 2^-11 of its size (2-norm), where
  * kvq_decode_attention gives float32.  A rotated query has to fit fp16: the magnitudes of a
- * query's elements may sum to at most 5.8e6.  Prefix tiers run so for head_dim 128, any page size, and
- * format pairs fp16/fp16, fp8/INT4, fp8/fp16 and codebook/codebook; otherwise (head_dim 64 and
- * 256, keys with a sketch or an outlier stream) the prefix is attended as a tier of every
+ * query's elements may sum to at most 5.8e6.  Prefix tiers run so for head_dim 128, any page
+ * size, and format pairs fp16/fp16, fp8/INT4, fp8/fp16 and codebook/codebook; otherwise (head_dim
+ * 64 and 256, keys with a sketch or an outlier stream) the prefix is attended as a tier of every
  * sequence by kvq_decode_attention's kernels, with its limits and results. */
 KVQ_API kvq_status kvq_decode_shared_workspace_size(const kvq_tier_view* prefix_tiers, int32_t num_prefix_tiers,
                                                     const int32_t* group_offsets, int32_t num_groups,

@@ -466,8 +466,8 @@ __device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, int 
 
 // The scale of a codebook's table, out of 128 steps of 2^(1 / 128) that bring its largest magnitude
 // to 2^-3 .. 2^-1: the one whose fp16 roundings are smallest, by the sum of squares of their
-// relative errors.  c: centroid `lane` in every
-// lane (0 beyond the codebook); the side's four warps, a candidate a thread.
+// relative errors.  c: centroid `lane` in every lane (0 beyond the codebook); the side's four warps, a
+// candidate a thread.
 __device__ __forceinline__ float scale_table(Ctl* ctl, float c, int bits, int side, int tid) {
   const int lane = tid & 31, warp = tid >> 5;
   const float over = c != 0.f ? __fdividef(1.0f, c) : 0.f;
