@@ -687,8 +687,11 @@ __device__ __forceinline__ int decode_kind(int fmt, int bits) {
 constexpr float kMostWeight = 32768.0f, kHeadroom = 2.0f;
 
 // A row's m has grown, f = 2^(old - new): the accumulator (if any product has gone into it)
-// and the tile's first `done` weight columns are scaled.
+// and the tile's first `done` weight columns are scaled.  Both may have been stored for this
+// same tile (the weights of its first half, the accumulator by a rescaling for that half), and a load
+// is not ordered behind a store that has not been waited for.
 __device__ __forceinline__ void rescale(uint32_t o_at, bool acc, uint32_t p_at, int done, float f) {
+  tc_wait_st();
   uint32_t v[16];
 #pragma unroll 1
   for (int c = 0; acc && c < kDim; c += 16) {

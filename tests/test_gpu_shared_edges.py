@@ -1,0 +1,81 @@
+"""kvq_decode_attention_shared where the prefix pass leaves its usual course: running maxima that are
+raised again and again, pages outside the pool, values at the ends of their formats.
+
+u = 2^-11 (half a step of fp16).  Expectations are attention in float64 over what the cache holds,
+read back by kvq_dequantize (rounded once more, u of a vector) or decoded by the oracle."""
+import math
+
+import numpy as np
+import pytest
+
+from tests import gpu_util as gu
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -11
+
+
+def modules():
+    return gu.torch_cuda(), gu.kvq_module()
+
+
+def call(kvq, torch, prefix, offsets, own, q, status=0):
+    """The shared decode of q (numpy fp16 [B, Hq, D]) as float64."""
+    qd = torch.from_numpy(np.ascontiguousarray(q)).cuda()
+    out = torch.empty_like(qd)
+    need = kvq.kvq_decode_shared_workspace_size(prefix, offsets, own, q.shape[0], q.shape[1])
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    bits = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    kvq.kvq_decode_attention_shared(prefix, offsets, own, qd, out, ws, bits)
+    assert int(bits.item()) == status
+    return out.cpu().numpy().astype(np.float64)
+
+
+def read_back(kvq, torch, cache, tokens):
+    hkv, d = cache.num_kv_heads, cache.head_dim
+    k, v = (torch.empty(tokens, hkv, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    kvq.kvq_dequantize(cache.struct, torch.arange(tokens, dtype=torch.int32, device="cuda"), k, v)
+    return k.cpu().numpy().astype(np.float64), v.cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("batch", [2, 20])  # 16 rows: tiles in turn between the softmax groups; 160: every tile both
+@pytest.mark.parametrize("fmt,bits", [("fp16", 0), ("codebook", 4)])
+def test_maxima_that_rise_in_both_halves_of_a_tile(fmt, bits, batch):
+    """Four tiles of one work item (320 kv heads leave one chunk): scores level in the first two, then
+    2^9 and 2^18 times the weight in the halves of the third and of the fourth.  Whichever tiles a softmax group takes,
+    its second one raises the maximum twice: the accumulator is rescaled, and rescaled again with
+    the half's weights that were just stored.  The level tiles' values are 64 times one vector: beside
+    the mean of 128 vectors (2-norm 1) they count 256 2^-18 / 128 64 sqrt(128) = 2^-7.5, and with one
+    of the two rescalings lost 2^9 times that.
+
+    Tolerance (2-norm): a half's weights are alike and so is their rounding (u), values, output and
+    read-back are rounded (u each), together at most 4 u = 2^-9; a score (at most 12.5 nats) is off
+    by u sqrt(3) of itself at most, 0.011, which moves the shares of the lighter levels (2^-8 and 2^-7.5) by as
+    much of themselves."""
+    torch, kvq = modules()
+    d, ps, hkv, group, n = 128, 16, 320, 8, 512
+    rng = np.random.default_rng(bits + batch)
+    ks, vs = (np.where(rng.integers(0, 2, (hkv, d)) == 0, 1, -1).astype(np.int8) for _ in range(2))
+    cache = kvq.PagedCache(d, hkv, n // ps, fmt, fmt, bits, bits, ks, vs, ps)
+    level = np.zeros(n)
+    level[256:320], level[320:384], level[384:448], level[448:] = 9.0, 18.0, 9.0, 18.0
+    u = rng.standard_normal((hkv, d))
+    u /= np.linalg.norm(u, axis=-1, keepdims=True)
+    length = 12.0  # of a query; a key of length x scores length x / sqrt(d) nats
+    x = (level * math.log(2.0) + 0.5) * math.sqrt(d) / length  # (half a nat: no key is zero)
+    k = (x[:, None, None] * u).astype(np.float16)
+    v = rng.standard_normal((n, hkv, d))
+    v[:256] = 64 * v[0]
+    cache.append(torch.from_numpy(k).cuda(), torch.from_numpy(v.astype(np.float16)).cuda(),
+                 torch.arange(n, dtype=torch.int32, device="cuda"))
+    view = kvq.TierView(cache, torch.arange(n // ps, dtype=torch.int32, device="cuda")[None],
+                        torch.tensor([n], dtype=torch.int32, device="cuda"))
+    q = np.repeat((length * u).astype(np.float16), group, 0)[None].repeat(batch, 0)
+    got = call(kvq, torch, [view], [0, batch], None, q)
+    kb, vb = read_back(kvq, torch, cache, n)
+    for h in range(0, hkv, 13):
+        s = kb[:, h] @ q[0, h * group].astype(np.float64) / math.sqrt(d)
+        p = np.exp(s - s.max())
+        want = (p / p.sum()) @ vb[:, h]
+        limit = 2.0 ** -9 * np.linalg.norm(want) + 0.011 * (2.0 ** -8 + 2.0 ** -7.5)
+        for b in (0, batch - 1):
+            assert np.all(np.linalg.norm(got[b, h * group:(h + 1) * group] - want, axis=-1) <= limit)
