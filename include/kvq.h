@@ -410,7 +410,8 @@ KVQ_API kvq_status kvq_decode_attention(const kvq_tier_view* tiers, int32_t num_
 #define KVQ_DEVERR_PAGE_INDEX 2   /* a block-table entry outside [0, num_pages): no read is made
                                      through it -- the fused fp16 / fp8 kernel leaves out the
                                      split-K chunk holding it, the codebook kernel reads page 0
-                                     in its place, the generic kernel leaves out the page */
+                                     in its place, the generic kernel leaves out the page, the
+                                     shared-prefix pass leaves out its chunk of the prefix */
 #define KVQ_DEVERR_SEQ_LEN 4      /* a seq_lens entry outside [0, max_pages * page_size] (a pool
                                      with num_pages 0 has no room: any length above 0): it is
                                      cut into that range */

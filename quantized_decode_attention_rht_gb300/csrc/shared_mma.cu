@@ -91,6 +91,7 @@ struct Ctl {
   unsigned long long bars[B_COUNT];
   uint32_t tmem;
   int abort;
+  int bad_page;        // a token of the item lies in a page outside the pool
   float best[2][4];    // per side and warp: a table scale's error, and
   int best_at[2][4];   // which it is
   float unscale[2];    // what a side's table values are to be multiplied by
@@ -258,7 +259,9 @@ struct Ring {
   uint32_t first_use;             // what the second stage waits for before its first tile, or 0
 };
 
-constexpr uint32_t kNoRow = 0xFFFFFFFFu;  // a token that is not there: reads as zero
+// A token that is not there reads as zero.  Past the end of the prefix its score is -inf; in a page
+// outside the pool it has a score like any other, and the whole item is left out (Ctl::bad_page).
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
 // Page of token t (-1 past the end).
 __device__ __forceinline__ int page_of(const Pages& s, int t) {
@@ -319,7 +322,8 @@ __device__ __forceinline__ void first_pages(const Pages& s, int tile0, int n, in
     page[j] = first < n ? page_of(s, (tile0 + first) * kTileTokens + (threadIdx.x & 31) + 32 * j) : -1;
 }
 __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __half* k_norm, const __half* v_norm,
-                                        const __half* v_scale, volatile float* unscale, uint32_t smem, uint32_t bars, int tile0, int n, int first,
+                                        const __half* v_scale, volatile float* unscale, volatile int* bad_page,
+                                        uint32_t smem, uint32_t bars, int tile0, int n, int first,
                                         volatile int* abort, int* err) {
   const int lane = threadIdx.x & 31;
   int bits = 0;
@@ -335,6 +339,7 @@ __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __
       row[j] = row_of(s, t0 + 32 * j, page[j], &bits);
       sts32(smem + kOffRow + at * kRowBytes + 4 * (lane + 32 * j), row[j]);
     }
+    if (bits) *bad_page = 1;
     bar_arrive(bars + 8 * (B_ROWS + at));
     uint2 aux[4];
 #pragma unroll
@@ -356,7 +361,7 @@ __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (k_norm) {
-        // (1 for a token that is not there: its score, -inf, stays that)
+        // (1 for a token that is not there: past the end its score, -inf, stays that)
         const float norm = __half2float(__ushort_as_half((uint16_t)aux[j].x)) * key_unit;
         sts32(ka + 128 * j, __float_as_uint(row[j] != kNoRow ? norm : 1.0f));
         sts32(va + 256 * j, aux[j].y);
@@ -822,6 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       bar_init(bars + 8 * (B_ROWS_READ + i), 256 + (CODES ? (min(rows, kItemRows) + 31) / 32 : 0));
     }
     ctl->abort = 0;
+    ctl->bad_page = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   Tables tables;
@@ -1074,6 +1080,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
           if (to >= 0) reinterpret_cast<float4*>(base + to * kDim)[lane] = x;
         }
       }
+      // A page outside the pool anywhere in the item leaves it out of the result.  (The other group's
+      // last tile may be one behind: its look-ups too have to be over.)
+      if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * (B_ROWS + (n - 1) % kAhead), ((n - 1) / kAhead) & 1, abort, p.err));
+      ok = ok && !*reinterpret_cast<volatile int*>(&ctl->bad_page);
       if (out_row >= 0) {
         // (a row of NaN has no maximum: its partial must not pass for one without tokens)
         const float l = unpack2(l2).x + unpack2(l2).y;
@@ -1176,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     } else if (warp < 17 + kLookUps) {
       // ---- look-ups
       look_up(pages, page, CODES ? T.k_aux : nullptr, CODES ? T.v_aux : nullptr, T.v_fmt == KVQ_FMT_INT4_G32 ? T.v_aux : nullptr,
-              ctl->unscale, smem, bars, tile0, n, warp - 17, abort, p.err);
+              ctl->unscale, &ctl->bad_page, smem, bars, tile0, n, warp - 17, abort, p.err);
     }
   }
   __syncwarp();

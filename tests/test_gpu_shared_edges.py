@@ -8,7 +8,9 @@ import math
 import numpy as np
 import pytest
 
+from oracle import attention as oatt
 from tests import gpu_util as gu
+from tests.test_gpu_shared import Case
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -11
@@ -79,3 +81,57 @@ def test_maxima_that_rise_in_both_halves_of_a_tile(fmt, bits, batch):
         limit = 2.0 ** -9 * np.linalg.norm(want) + 0.011 * (2.0 ** -8 + 2.0 ** -7.5)
         for b in (0, batch - 1):
             assert np.all(np.linalg.norm(got[b, h * group:(h + 1) * group] - want, axis=-1) <= limit)
+
+
+@pytest.mark.parametrize("name", ["fp16", "fp8_int4", "cb4", "cb32"])
+@pytest.mark.parametrize("length", [100, 128, 900])
+@pytest.mark.parametrize("batch,group", [(3, 2), (40, 4)])
+def test_a_page_outside_the_pool_is_left_out(name, length, batch, group):
+    """The chunk of the prefix that holds the page counts for nothing: one tile is one chunk, and a
+    longer prefix loses a run of whole tiles around the page, whatever the plan made of it.  Other
+    groups keep theirs."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, [name], [[length, 70]], [0, batch, batch + 2], [name], [[5] * (batch + 2)], hq=2 * group, hkv=2,
+             seed=length + batch)
+    rows = [b for b in (0, 1, batch - 1)]
+    heads = {(b, h) for b in rows for h in (0, 2 * group - 1)}
+    other = {(b, h) for b in (batch, batch + 1) for h in (0, 2 * group - 1)}
+    tiles = -(-length // 128)
+    keep = c.prefix[0].block_table.clone()
+    for at in sorted({0, tiles // 2, tiles - 1}):  # the page's tile
+        for bad in (-1, c.built.gpu[0].num_pages):
+            c.prefix[0].block_table.copy_(keep)
+            c.prefix[0].block_table[0, min(8 * at + 2, (length - 1) // 16)] = bad
+            got = call(kvq, torch, c.prefix, c.offsets, c.own, c.q, kvq.DEVERR_PAGE_INDEX)
+            c.check(got, other)
+            want = {}
+            for per in range(1, tiles + 1):  # tiles of a chunk
+                lo = at // per * per
+                want[lo, min(lo + per, tiles)] = None
+            fits = []
+            for lo, hi in want:
+                try:
+                    check_without(c, got, heads, lo * 128, min(hi * 128, length))
+                    fits.append((lo, hi))
+                except AssertionError:
+                    pass
+            assert fits, "the output fits no chunk left out"
+            if tiles == 1:
+                assert fits == [(0, 1)]
+
+
+def check_without(c, got, heads, lo, hi):
+    """The output against attention without tokens [lo, hi) of group 0's prefix (2-norm, 2^-9 of the
+    output as in test_gpu_shared)."""
+    grp = c.hq // c.hkv
+    off = size = 0.0
+    for b, h in heads:
+        keys, values = oatt.dequantised_kv(c.tiers, b, h // grp)
+        n = int(c.tiers[0].lens[b])
+        there = np.r_[0:lo, hi:n, n:len(keys)]
+        s = keys[there] @ c.q[b, h].astype(np.float64) / math.sqrt(c.d)
+        w = np.exp(s - s.max())
+        want = (w / w.sum()) @ values[there]
+        off += float(np.sum((got[b, h] - want) ** 2))
+        size += float(np.sum(want ** 2))
+    assert math.sqrt(off / size) <= 2.0 ** -9, math.sqrt(off / size)
