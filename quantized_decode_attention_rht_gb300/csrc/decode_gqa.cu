@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "kvq_internal.cuh"
 
@@ -47,6 +48,7 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kQScale = 64.0f;   // q' is stored x 2^6 in the B fragments
 constexpr float kWScale = 256.0f;  // weights are stored x 2^8 in the B fragments
+constexpr float kMostScale = 255.0f;  // INT4 scales whose weights, at most 1 x 2^8 x scale, fit fp16
 
 // far tier stage: K fp8 16 x 128 B, V INT4 16 x 64 B, scales 16 x 4 fp16 (rows padded)
 constexpr int F_KSTR = 144, F_VSTR = 80;
@@ -336,7 +338,12 @@ struct Far {
     const uint2 sc0 = lds64(s0 + F_S + 8 * g), sc1 = lds64(s0 + F_S + 8 * (g + 8));
     const __half2* h0 = reinterpret_cast<const __half2*>(&sc0);
     const __half2* h1 = reinterpret_cast<const __half2*>(&sc1);
-    const float q0 = p0 * kWScale, q1 = p1 * kWScale;
+    // A page with a scale above kMostScale (values beyond 1785: hardly ever) takes its weights without
+    // the 2^8 and its levels with it, which fp16 holds exactly.
+    const __half2 top = __hmax2(__hmax2(h0[0], h0[1]), __hmax2(h1[0], h1[1]));
+    const bool big = __any_sync(kFull, fmaxf(__low2float(top), __high2float(top)) > kMostScale);
+    const float wscale = big ? 1.0f : kWScale;
+    const float q0 = p0 * wscale, q1 = p1 * wscale;
     float w0g[4], w1g[4];
     w0g[0] = q0 * __low2float(h0[0]);
     w0g[1] = q0 * __high2float(h0[0]);
@@ -380,28 +387,33 @@ struct Far {
     const uint32_t magic = 0x64006400u;
     const __half2 off_lo = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));  // 1032
     const __half2 off_hi = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-    auto lvl = [&](uint32_t bits, __half2 off) {
-      __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&bits), off);
-      return *reinterpret_cast<uint32_t*>(&h);
-    };
+    auto add_values = [&](auto scaled) {  // scaled: the levels carry the 2^8
+      auto lvl = [&](uint32_t bits, __half2 off) {
+        __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&bits), off);
+        if constexpr (decltype(scaled)::value) h = __hmul2(h, __float2half2_rn(kWScale));
+        return *reinterpret_cast<uint32_t*>(&h);
+      };
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const uint32_t x0s = R[a][0] >> 8, x1s = R[a][1] >> 8;
-      uint32_t am[4];
-      // m-tile (group a, m = 0): rows g -> coordinate 4g (low nibble of byte 2g),
-      // rows g+8 -> 4g+1 (high nibble)
-      am[0] = lvl((R[a][0] & 0x000F000Fu) | magic, off_lo);
-      am[1] = lvl((R[a][0] & 0x00F000F0u) | magic, off_hi);
-      am[2] = lvl((R[a][1] & 0x000F000Fu) | magic, off_lo);
-      am[3] = lvl((R[a][1] & 0x00F000F0u) | magic, off_hi);
-      mma16816(s.acc[a][0], am, bf[a][0], bf[a][1]);
-      // m = 1: coordinates 4g+2, 4g+3 (byte 2g+1)
-      am[0] = lvl((x0s & 0x000F000Fu) | magic, off_lo);
-      am[1] = lvl((x0s & 0x00F000F0u) | magic, off_hi);
-      am[2] = lvl((x1s & 0x000F000Fu) | magic, off_lo);
-      am[3] = lvl((x1s & 0x00F000F0u) | magic, off_hi);
-      mma16816(s.acc[a][1], am, bf[a][0], bf[a][1]);
-    }
+      for (int a = 0; a < 4; ++a) {
+        const uint32_t x0s = R[a][0] >> 8, x1s = R[a][1] >> 8;
+        uint32_t am[4];
+        // m-tile (group a, m = 0): rows g -> coordinate 4g (low nibble of byte 2g),
+        // rows g+8 -> 4g+1 (high nibble)
+        am[0] = lvl((R[a][0] & 0x000F000Fu) | magic, off_lo);
+        am[1] = lvl((R[a][0] & 0x00F000F0u) | magic, off_hi);
+        am[2] = lvl((R[a][1] & 0x000F000Fu) | magic, off_lo);
+        am[3] = lvl((R[a][1] & 0x00F000F0u) | magic, off_hi);
+        mma16816(s.acc[a][0], am, bf[a][0], bf[a][1]);
+        // m = 1: coordinates 4g+2, 4g+3 (byte 2g+1)
+        am[0] = lvl((x0s & 0x000F000Fu) | magic, off_lo);
+        am[1] = lvl((x0s & 0x00F000F0u) | magic, off_hi);
+        am[2] = lvl((x1s & 0x000F000Fu) | magic, off_lo);
+        am[3] = lvl((x1s & 0x00F000F0u) | magic, off_hi);
+        mma16816(s.acc[a][1], am, bf[a][0], bf[a][1]);
+      }
+    };
+    if (!big) add_values(std::false_type{});
+    else add_values(std::true_type{});
   }
 
   // Partial for head c: acc[32a + 4g + k] = sum_t p_t s_ta (u - 8), relative to the max.

@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 
 from oracle import attention as oatt
+from oracle import cache as ocache
 from tests import gpu_util as gu
 from tests.test_gpu_shared import Case
 
@@ -135,3 +136,46 @@ def check_without(c, got, heads, lo, hi):
         off += float(np.sum((got[b, h] - want) ** 2))
         size += float(np.sum(want ** 2))
     assert math.sqrt(off / size) <= 2.0 ** -9, math.sqrt(off / size)
+
+
+def check_norm(c, got, heads, limit):
+    off = size = 0.0
+    for b, h in heads:
+        keys, values = oatt.dequantised_kv(c.tiers, b, h // (c.hq // c.hkv))
+        s = keys @ c.q[b, h].astype(np.float64) / math.sqrt(c.d)
+        w = np.exp(s - s.max())
+        want = (w / w.sum()) @ values
+        off += float(np.sum((got[b, h] - want) ** 2))
+        size += float(np.sum(want ** 2))
+    assert math.sqrt(off / size) <= limit, math.sqrt(off / size)
+
+
+def put_large_values(torch, c, side, sequences, size):
+    """Every third value of a tier along the signs, so that one rotated coordinate holds it all: in the
+    oracle's pool and in the cache."""
+    tier, cache = c.built.ora[side], c.built.gpu[side]
+    ps = tier.page_size
+    for i in range(sequences):
+        t = np.arange(0, int(tier.lens[i]), 3)
+        v = (np.where((i + t) % 2, 1.0, 0.4) * size)[:, None, None] * c.built.v_signs
+        ocache.write(tier.v, tier.block_table[i][t // ps] * ps + t % ps, v.astype(np.float16), ps)
+    cache.v_rows.copy_(torch.from_numpy(tier.v.rows))
+    cache.v_aux.copy_(torch.from_numpy(tier.v.aux.reshape(cache.v_aux.shape)))
+
+
+@pytest.mark.parametrize("size", [100.0, 157.0, 160.0, 1000.0, 25000.0])
+@pytest.mark.parametrize("batch,group", [(3, 2), (4, 8)])
+def test_int4_scales_of_any_size_in_the_sequences_own_tier(size, batch, group):
+    """Scales (1.6 times the size) up to 2^8 and beyond, whose product with a weight times 2^8 passes fp16's
+    largest number: by kvq_decode_attention too, whose weights keep 22 bits (2^-16 with the
+    scores' float32 errors)."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["fp8_int4"], [[200]], [0, batch], ["fp8_int4"], [[300, 21, 16, 5][:batch]], hq=2 * group, hkv=2,
+             seed=int(size))
+    put_large_values(torch, c, 1, batch, size)
+    assert np.max(c.tiers[1].v.aux.astype(np.float64)) > 1.5 * size
+    heads = {(b, h) for b in range(batch) for h in range(2 * group)}
+    check_norm(c, call(kvq, torch, c.prefix, c.offsets, c.own, c.q), heads, 2.0 ** -9)
+    own = gu.gpu_decode(kvq, torch, c.own, c.q).astype(np.float64)
+    c.tiers = c.tiers[1:]
+    check_norm(c, own, heads, 2.0 ** -16)
