@@ -415,6 +415,9 @@ KVQ_API kvq_status kvq_decode_attention(const kvq_tier_view* tiers, int32_t num_
 #define KVQ_DEVERR_SEQ_LEN 4      /* a seq_lens entry outside [0, max_pages * page_size] (a pool
                                      with num_pages 0 has no room: any length above 0): it is
                                      cut into that range */
+#define KVQ_DEVERR_VALUE_RANGE 8  /* an INT4 scale above 9352 in a shared prefix, whose values
+                                     (rotated, beyond 65504) the fp16 of the prefix pass
+                                     cannot hold: infinities or NaN in the output of its group */
 
 /* Options of kvq_decode_attention_ex: two features of the FoveatedKV page's fused kernel
  * ("Making it fast"), and the device error report.  All zero is the plain computation of
@@ -482,7 +485,8 @@ KVQ_API kvq_status kvq_decode_attention_ex(const kvq_tier_view* tiers, int32_t n
  * that are not fp16 values already, softmax weights), with float32 scores, sums and
  * accumulators: the output's error is a few 2^-11 of its size (2-norm), where
  * kvq_decode_attention gives float32.  A rotated query has to fit fp16: the magnitudes of a
- * query's elements may sum to at most 5.8e6.  Prefix tiers run so for head_dim 128, any page
+ * query's elements may sum to at most 5.8e6.  So has a prefix's value row: INT4 scales may be up
+ * to 9352 (reported beyond: KVQ_DEVERR_VALUE_RANGE).  Prefix tiers run so for head_dim 128, any page
  * size, and format pairs fp16/fp16, fp8/INT4, fp8/fp16 and codebook/codebook; otherwise (head_dim
  * 64 and 256, keys with a sketch or an outlier stream) the prefix is attended as a tier of every
  * sequence by kvq_decode_attention's kernels, with its limits and results. */

@@ -97,7 +97,7 @@ ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
 
 SCORE_GATE_NATS = 16.0
 # device-side error bits of a decode call (kvq_decode_options.status)
-DEVERR_COPY_TIMEOUT, DEVERR_PAGE_INDEX, DEVERR_SEQ_LEN = 1, 2, 4
+DEVERR_COPY_TIMEOUT, DEVERR_PAGE_INDEX, DEVERR_SEQ_LEN, DEVERR_VALUE_RANGE = 1, 2, 4, 8
 
 _lib_handle = None
 

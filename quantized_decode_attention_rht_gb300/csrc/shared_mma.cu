@@ -339,7 +339,7 @@ __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __
       row[j] = row_of(s, t0 + 32 * j, page[j], &bits);
       sts32(smem + kOffRow + at * kRowBytes + 4 * (lane + 32 * j), row[j]);
     }
-    if (bits) *bad_page = 1;
+    if (bits & KVQ_DEVERR_PAGE_INDEX) *bad_page = 1;
     bar_arrive(bars + 8 * (B_ROWS + at));
     uint2 aux[4];
 #pragma unroll
@@ -350,6 +350,11 @@ __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __
         aux[j].y = __half_as_ushort(__ldg(v_norm + row[j]));
       } else if (row[j] != kNoRow && v_scale) {
         aux[j] = __ldg(reinterpret_cast<const uint2*>(v_scale) + row[j]);
+        // a finite scale above 9352: seven times it is no fp16 number
+        const uint32_t w[4] = {aux[j].x, aux[j].x >> 16, aux[j].y, aux[j].y >> 16};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((w[k] & 0x7FFFu) - 0x7092u < 0x7C00u - 0x7092u) bits |= KVQ_DEVERR_VALUE_RANGE;
       }
     }
     if (i + kLookUps < n) {

@@ -179,3 +179,18 @@ def test_int4_scales_of_any_size_in_the_sequences_own_tier(size, batch, group):
     own = gu.gpu_decode(kvq, torch, c.own, c.q).astype(np.float64)
     c.tiers = c.tiers[1:]
     check_norm(c, own, heads, 2.0 ** -16)
+
+
+@pytest.mark.parametrize("size", [157.0, 160.0, 5700.0, 5900.0, 25000.0])
+@pytest.mark.parametrize("batch,group", [(3, 2), (40, 4)])
+def test_int4_scales_of_a_prefix(size, batch, group):
+    """Scales whose values fit fp16 (up to 9352) are attended, larger ones are reported."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["fp8_int4"], [[400]], [0, batch], ["fp8_int4"], [[7] * batch], hq=2 * group, hkv=2,
+             seed=int(size))
+    put_large_values(torch, c, 0, 1, size)
+    most = np.max(c.tiers[0].v.aux.astype(np.float64))
+    assert (most > 9352) == (size > 5800)
+    got = call(kvq, torch, c.prefix, c.offsets, c.own, c.q, kvq.DEVERR_VALUE_RANGE if most > 9352 else 0)
+    if most <= 9352:
+        check_norm(c, got, {(b, h) for b in (0, 1, batch - 1) for h in range(2 * group)}, 2.0 ** -9)
