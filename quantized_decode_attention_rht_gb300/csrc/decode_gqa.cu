@@ -83,6 +83,9 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+__device__ __forceinline__ void sts128_zero(uint32_t a) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
+}
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
@@ -335,7 +338,10 @@ struct Far {
     // score gate: every token of the page, for every live head, far below the running max
     if (gate && __all_sync(kFull, !live || mt - s.m < -kGateLog2)) return;
     // ---- weights w = p * scale (x 2^8) per group for this lane's tokens (g, g+8), head c
-    const uint2 sc0 = lds64(s0 + F_S + 8 * g), sc1 = lds64(s0 + F_S + 8 * (g + 8));
+    // (of tokens past the end 0, whatever their slots hold: a weight of 0 times NaN would be NaN)
+    uint2 sc0 = lds64(s0 + F_S + 8 * g), sc1 = lds64(s0 + F_S + 8 * (g + 8));
+    if (!v0) sc0 = make_uint2(0u, 0u);
+    if (!v1) sc1 = make_uint2(0u, 0u);
     const __half2* h0 = reinterpret_cast<const __half2*>(&sc0);
     const __half2* h1 = reinterpret_cast<const __half2*>(&sc1);
     // A page with a scale above kMostScale (values beyond 1785: hardly ever) takes its weights without
@@ -543,6 +549,11 @@ struct Near {
     const uint32_t bh = __shfl_sync(kFull, hi, srcB), bl = __shfl_sync(kFull, lo, srcB);
     const uint32_t A = lo_part ? al : ah, B = lo_part ? bl : bh;
     const uint32_t b0 = __byte_perm(A, B, 0x5410), b1 = __byte_perm(A, B, 0x7632);
+    // rows past the end, whatever their slots hold, are zero: a weight of 0 times NaN would be NaN
+    if (nvalid < PS) {
+      for (int i = 16 * nvalid + lane; i < 16 * PS; i += 32) sts128_zero(s0 + N_V + (i >> 4) * N_VSTR + (i & 15) * 16);
+      __syncwarp();
+    }
     // ---- values: ldmatrix.trans gives V^T[16 coordinates x 16 tokens] fragments
     const uint32_t vaddr = s0 + N_V + ((mi >> 1) * 8 + t) * N_VSTR + (mi & 1) * 16;
 #pragma unroll

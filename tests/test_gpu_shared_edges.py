@@ -194,3 +194,29 @@ def test_int4_scales_of_a_prefix(size, batch, group):
     got = call(kvq, torch, c.prefix, c.offsets, c.own, c.q, kvq.DEVERR_VALUE_RANGE if most > 9352 else 0)
     if most <= 9352:
         check_norm(c, got, {(b, h) for b in (0, 1, batch - 1) for h in range(2 * group)}, 2.0 ** -9)
+
+
+@pytest.mark.parametrize("name,d,hq", [("fp16", 128, 8), ("fp8_int4", 128, 8), ("cb4", 128, 8), ("cb4", 128, 2),
+                                       ("cb32", 128, 4), ("fp8_fp16", 128, 8), ("fp16", 64, 4), ("fp8_int4", 256, 4),
+                                       ("cb4", 256, 2), ("qjl", 128, 4), ("outlier", 128, 4)])
+def test_what_lies_behind_the_sequences_is_not_attended(name, d, hq):
+    """NaN in every slot of the pool that holds no token, those behind a sequence's last token in its
+    last page among them: the outputs of the shared and of the plain decode stay the same, to the bit."""
+    torch, kvq = modules()
+    lens = [1, 15, 16, 17, 250, 0]
+    c = Case(kvq, torch, ["fp8_int4" if name in ("qjl", "outlier") else name], [[40]], [0, 6], [name], [lens], hq=hq, hkv=2,
+             d=d, seed=d + hq)
+    run = lambda: (call(kvq, torch, c.prefix, c.offsets, c.own, c.q), gu.gpu_decode(kvq, torch, c.own, c.q))  # noqa: E731
+    want = run()
+    assert all(np.isfinite(x).all() for x in want)
+    cache, table = c.built.gpu[1], c.own[0].block_table.cpu().numpy()
+    held = np.concatenate([table[i][np.arange(n) // 16] * 16 + np.arange(n) % 16 for i, n in enumerate(lens)])
+    free = np.setdiff1d(np.arange(cache.num_pages * 16), held)
+    pages, offs = (torch.from_numpy(x).cuda() for x in (free // 16, free % 16))
+    for a in (cache.k_rows, cache.v_rows, cache.k_aux, cache.v_aux):
+        if a is not None and a.dtype == torch.float16:
+            a[pages, :, offs] = float("nan")
+        elif a is not None:  # bytes of NaN in fp16 and in fp8 rows, of -1 and a NaN norm in codes and outliers
+            a[pages, :, offs] = 0x7F if a is cache.k_aux or "fp" in name else 0xFF
+    for got, x in zip(run(), want):
+        assert np.array_equal(got, x)
