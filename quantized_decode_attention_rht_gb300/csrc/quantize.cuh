@@ -68,6 +68,13 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
   return r;
 }
 
+// The larger of two; NaN if either is (fmaxf drops it: a group with a NaN would look like zeros).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 __device__ __forceinline__ void prefetch_l2(const void* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
 
 // ---------------------------------------------------------------- decision table
@@ -489,7 +496,7 @@ __device__ __forceinline__ void quantize_vector(const QuantParams& p, const Quan
     for (int g = 0; g < NG; ++g) {
       float amax = 0.0f;
 #pragma unroll
-      for (int e = 0; e < kGroup; ++e) amax = fmaxf(amax, fabsf(y[kGroup * g + e] * inv_sqrt_d));
+      for (int e = 0; e < kGroup; ++e) amax = max_nan(amax, fabsf(y[kGroup * g + e] * inv_sqrt_d));
       const __half s16 = __float2half_rn(amax / 7.0f);
       const float s = __half2float(s16);
       const float r = s > 0.0f ? 1.0f / s : 0.0f;

@@ -433,7 +433,7 @@ __device__ __forceinline__ void append_side(const P& p, const QuantSide& side, c
         // the outlier stream: int8 with a per-token scale s = fp16(max |x_cj| / 127)
         float amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < KVQ_OUTLIER_CHANNELS; ++j) amax = fmaxf(amax, fabsf(xo[j]));
+        for (int j = 0; j < KVQ_OUTLIER_CHANNELS; ++j) amax = max_nan(amax, fabsf(xo[j]));
         const __half s16 = __float2half_rn(amax / 127.0f);
         const float sc = __half2float(s16);
         uint32_t qw[2] = {0u, 0u};
@@ -492,9 +492,9 @@ __device__ __forceinline__ void append_side(const P& p, const QuantSide& side, c
       constexpr int LG = kGroup / E;
       float amax = 0.0f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(y[e] * ys));
+      for (int e = 0; e < E; ++e) amax = max_nan(amax, fabsf(y[e] * ys));
 #pragma unroll
-      for (int m = 1; m < LG; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
+      for (int m = 1; m < LG; m <<= 1) amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
       const __half s16 = __float2half_rn(amax / 7.0f);
       const float s = __half2float(s16);
       const float rcp = s > 0.0f ? 1.0f / s : 0.0f;

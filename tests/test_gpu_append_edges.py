@@ -1,0 +1,70 @@
+"""What the two appends (kvq_quantize_append, kvq_rope_append; a warp per vector, and the per-thread
+kernels above 16384 vectors) store for values at the ends of their formats."""
+import numpy as np
+import pytest
+
+from oracle import cache as ocache
+from tests import gpu_util as gu
+from tests.test_gpu_rope import make_rope
+
+pytestmark = pytest.mark.gpu
+
+SIZES = [(64, 40, 3), (64, 5601, 3), (128, 40, 3), (128, 2049, 9), (256, 40, 3), (256, 2050, 9)]
+
+
+def store(kvq, torch, x, kf, vf, kb=0, vb=0, fused=True, **kw):
+    """x [T, Hkv, D] as keys (fused: turned by small positions) and as values; their pool rows."""
+    t, hkv, d = x.shape
+    rng = np.random.default_rng(hkv)
+    ks, vs = (np.where(rng.integers(0, 2, (hkv, d)) == 0, 1, -1).astype(np.int8) for _ in range(2))
+    cache = kvq.PagedCache(d, hkv, (t + 15) // 16, kf, vf, kb, vb, ks, vs, **kw)
+    slots, xd = torch.arange(t, dtype=torch.int32, device="cuda"), torch.from_numpy(x).cuda()
+    if fused:
+        kvq.kvq_rope_append(cache.struct, make_rope(kvq, d, "half"), slots % 100, xd, xd, slots)
+    else:
+        cache.append(xd, xd, slots)
+    back = [torch.empty_like(xd) for _ in range(2)]
+    kvq.kvq_dequantize(cache.struct, slots, *back)
+    torch.cuda.synchronize()
+    rows = [None if a is None else gu.pool_rows(a, np.arange(t)) for a in (cache.k_rows, cache.v_rows, cache.k_aux, cache.v_aux)]
+    return rows, [b.cpu().numpy() for b in back]
+
+
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("d,t,hkv", SIZES)
+def test_a_nan_in_an_int4_vector_is_stored_as_nan(d, t, hkv, fused):
+    """The rotation spreads it over the vector: every group's scale is NaN and every level 0, as the
+    oracle has it, and the vector is read back as NaN.  Its neighbours are what they were."""
+    torch, kvq = gu.torch_cuda(), gu.kvq_module()
+    rng = np.random.default_rng(d + t)
+    x = rng.standard_normal((t, hkv, d)).astype(np.float16)
+    y = x.copy()
+    bad = np.zeros((t, hkv), bool)
+    for i, h in ((0, 0), (1, hkv - 1), (t // 2, 1), (t - 1, hkv - 1)):
+        y[i, h, int(rng.integers(d))], bad[i, h] = np.nan, True
+    _, oracle = ocache.encode(y[0, 0], np.ones(d), "int4_g32")
+    assert np.isnan(oracle).all()
+    want, back0 = store(kvq, torch, x, "int4_g32", "int4_g32", fused=fused)
+    got, back = store(kvq, torch, y, "int4_g32", "int4_g32", fused=fused)
+    for side in (0, 1):
+        assert np.isnan(got[2 + side][bad]).all() and (got[side][bad] == 0x88).all()
+        assert np.isnan(back[side][bad]).all()
+        assert np.array_equal(got[side][~bad], want[side][~bad]) and np.array_equal(got[2 + side][~bad], want[2 + side][~bad])
+        assert np.array_equal(back[side][~bad], back0[side][~bad])
+
+
+@pytest.mark.parametrize("fused", [True, False])
+@pytest.mark.parametrize("t", [40, 5700])
+def test_a_nan_in_an_outlier_channel_is_stored_as_nan(t, fused):
+    torch, kvq = gu.torch_cuda(), gu.kvq_module()
+    rng = np.random.default_rng(t)
+    hkv, d = 3, 128
+    outl = np.stack([rng.choice(d, 8, replace=False) for _ in range(hkv)]).astype(np.int32)
+    x = rng.standard_normal((t, hkv, d)).astype(np.float16)
+    x[t // 2, 1, outl[1, 3]] = np.nan
+    rows, back = store(kvq, torch, x, "codebook_outlier", "codebook", 4, 4, fused, k_outliers=outl)
+    _, scale, q = ocache.unpack_outlier_aux(rows[2])
+    bad = np.zeros((t, hkv), bool)
+    bad[t // 2, 1] = True
+    assert np.isnan(scale[bad]).all() and not q[bad].any() and np.isfinite(scale[~bad]).all()
+    assert np.isnan(back[0][t // 2, 1, outl[1]]).all() and np.isfinite(back[0][~bad]).all()
