@@ -138,14 +138,16 @@ __device__ void build_table(Table& t, float2* cells, const float* bounds, const 
   __syncthreads();
 }
 
-// A vector whose sum of squares is not finite has no codes (the table has no cell for a NaN, and its
-// look-up would leave shared memory): its coordinates count as zero, and the stored norm tells.
+// A vector whose sum of squares is not finite has no codes: code 0 is stored for every coordinate (both
+// appends, whatever the coordinates), and the norm tells.  The table has no cell for a NaN, and its
+// look-up would leave shared memory: the coordinates are looked up as zeros, and the mask
+// returned clears the codes.
 template <int E>
-__device__ __forceinline__ void zero_unless_finite(float ss, float (&y)[E]) {
-  if (!(ss < INFINITY)) {
+__device__ __forceinline__ uint32_t zero_unless_finite(float ss, float (&y)[E]) {
+  if (ss < INFINITY) return 0xFFFFFFFFu;
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = 0.f;
-  }
+  for (int e = 0; e < E; ++e) y[e] = 0.f;
+  return 0u;
 }
 
 // 12582912 = 1.5 * 2^23: adding it rounds t (|t| < 2^22) to the integer held in the low
@@ -154,10 +156,10 @@ constexpr float kMagic = 12582912.0f;
 constexpr uint32_t kMagicBits = 0x4B400000u;
 
 // Code indices of coordinates t = y[e] * scale (scale = sqrt(D) / ||y|| / w), packed
-// little-endian and stored (E * BITS / 8 bytes at row).
+// little-endian and stored (E * BITS / 8 bytes at row), under the mask `keep`.
 template <int BITS, int E, bool RESIDUAL = false>
 __device__ __forceinline__ void encode_codebook(const Table& tb, float (&y)[E], float scale, uint8_t* row,
-                                                bool store, float rscale = 0.f, float dscale = 0.f) {
+                                                bool store, uint32_t keep, float rscale = 0.f, float dscale = 0.f) {
   constexpr int W = E * BITS / 32;
   uint32_t w[W];
 #pragma unroll
@@ -197,6 +199,8 @@ __device__ __forceinline__ void encode_codebook(const Table& tb, float (&y)[E], 
     w[o1 / 32] += i1 * (1u << (o1 % 32));
     if ((o1 % 32) + BITS > 32) w[o1 / 32 + 1] += i1 >> (32 - (o1 % 32));
   }
+#pragma unroll
+  for (int k = 0; k < W; ++k) w[k] &= keep;
   if (store) {  // the lane's run is W words at a multiple of its own size (3 words: of 4 bytes)
     if (W % 4 == 0) {
 #pragma unroll
@@ -431,13 +435,13 @@ __device__ __forceinline__ void quantize_vector(const QuantParams& p, const Quan
     const float ny = sqrtf(ss);
     const float inv = ny > 0.0f ? sqrt_d / ny : 0.0f;  // u = sqrt(D) y / ||y||
     const __half norm16 = __float2half_rn(ny * inv_sqrt_d);
-    zero_unless_finite(ss, y);
+    const uint32_t keep = zero_unless_finite(ss, y);
     if constexpr (FMT == F_CB) {
-      encode_codebook<BITS, kE>(table, y, inv * table.inv_w, row + sub * (kE * BITS / 8), store);
+      encode_codebook<BITS, kE>(table, y, inv * table.inv_w, row + sub * (kE * BITS / 8), store, keep);
       if (store && sub == 0) side.aux[prow] = norm16;
     } else {
       // codes, and y <- the residual against the decoded vector (stored fp16 norm)
-      encode_codebook<BITS, kE, true>(table, y, inv * table.inv_w, row + sub * (kE * BITS / 8), store, inv_sqrt_d,
+      encode_codebook<BITS, kE, true>(table, y, inv * table.inv_w, row + sub * (kE * BITS / 8), store, keep, inv_sqrt_d,
                                       __half2float(norm16) * inv_sqrt_d);
       u64 racc = pk(0.f, 0.f);
 #pragma unroll

@@ -412,7 +412,8 @@ __device__ __forceinline__ void append_side(const P& p, const QuantSide& side, c
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) ss = fmaf(y[e], y[e], ss);
-      const float ny = sqrtf(warp_sum(ss));
+      ss = warp_sum(ss);
+      const float ny = sqrtf(ss);
       const float inv = ny > 0.0f ? sqrt_d / ny : 0.0f;  // u = sqrt(D) y / ||y||
       const __half norm16 = __float2half_rn(ny * ys);
       uint32_t fields = 0u;
@@ -426,6 +427,7 @@ __device__ __forceinline__ void append_side(const P& p, const QuantSide& side, c
         idx[e] = c;
         fields |= (uint32_t)c << (e * BITS);
       }
+      if (!(ss < INFINITY)) fields = 0u;  // no codes (see zero_unless_finite)
       if (part == 0) store_fields<D, E, BITS>(buf, fields, row, lane);  // warp-uniform
       if constexpr (FMT == F_CB) {
         if (lane == 0) side.aux[prow] = norm16;

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 SIZES = [(64, 40, 3), (64, 5601, 3), (128, 40, 3), (128, 2049, 9), (256, 40, 3), (256, 2050, 9)]
 
 
-def store(kvq, torch, x, kf, vf, kb=0, vb=0, fused=True, **kw):
+def store(kvq, torch, x, kf, vf, kb=0, vb=0, fused=True, scale=1.0, **kw):
     """x [T, Hkv, D] as keys (fused: turned by small positions) and as values; their pool rows."""
     t, hkv, d = x.shape
     rng = np.random.default_rng(hkv)
@@ -20,7 +20,7 @@ def store(kvq, torch, x, kf, vf, kb=0, vb=0, fused=True, **kw):
     cache = kvq.PagedCache(d, hkv, (t + 15) // 16, kf, vf, kb, vb, ks, vs, **kw)
     slots, xd = torch.arange(t, dtype=torch.int32, device="cuda"), torch.from_numpy(x).cuda()
     if fused:
-        kvq.kvq_rope_append(cache.struct, make_rope(kvq, d, "half"), slots % 100, xd, xd, slots)
+        kvq.kvq_rope_append(cache.struct, make_rope(kvq, d, "half", scale=scale), slots % 100, xd, xd, slots)
     else:
         cache.append(xd, xd, slots)
     back = [torch.empty_like(xd) for _ in range(2)]
@@ -68,3 +68,24 @@ def test_a_nan_in_an_outlier_channel_is_stored_as_nan(t, fused):
     bad[t // 2, 1] = True
     assert np.isnan(scale[bad]).all() and not q[bad].any() and np.isfinite(scale[~bad]).all()
     assert np.isnan(back[0][t // 2, 1, outl[1]]).all() and np.isfinite(back[0][~bad]).all()
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4])
+@pytest.mark.parametrize("d,hkv", [(64, 3), (128, 3), (256, 5)])
+def test_a_codebook_vector_that_is_not_finite_has_codes_of_zero(d, hkv, bits):
+    """NaN, infinities, and finite values whose sum of squares leaves float32: code 0 everywhere and a norm
+    that is not finite, from both kernels of both appends."""
+    torch, kvq = gu.torch_cuda(), gu.kvq_module()
+    rng = np.random.default_rng(bits)
+    for t in (40, 5700):
+        for fused, scale in ((True, 1.0), (False, 1.0), (True, 1e30)):
+            x = rng.standard_normal((t, hkv, d)).astype(np.float16)
+            x[3, 1, 5], x[7, 2, d - 1], x[t - 1, 0, 0] = np.nan, np.inf, -np.inf
+            x[20, 1, :2] = np.inf, -np.inf
+            x[9, 0] = 0
+            bad = ~np.isfinite(x).all(-1)
+            rows, _ = store(kvq, torch, x, "codebook", "codebook", bits, bits, fused, scale=scale)
+            for side in (0, 1):
+                gone = bad if side or scale == 1.0 else x.any(-1)  # values are not scaled
+                assert not rows[side][gone].any() and not np.isfinite(rows[2 + side][gone]).any()
+                assert np.isfinite(rows[2 + side][~gone]).all() and rows[side][~gone].any(-1).all()
