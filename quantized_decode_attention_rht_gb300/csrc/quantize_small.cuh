@@ -153,18 +153,26 @@ struct TurnParams : QuantParams {
   long long xt[2], xh[2];  // K, V: token and head strides
 };
 
+// A load of input heads: through the read-only path, but for heads that the same kernel may write in
+// place (queries).
+template <bool IN_PLACE, class T>
+__device__ __forceinline__ T load_input(const T* p) {
+  if constexpr (IN_PLACE) return *p;
+  else return __ldg(p);
+}
+
 // The lane's coordinates [lane * E, lane * E + E) of a head's fp16 vector as floats.
-template <int E>
+template <int E, bool IN_PLACE>
 __device__ __forceinline__ void load_run(const uint16_t* x, int at, float (&y)[E]) {
   uint32_t w[E / 2];
   if constexpr (E == 2) {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(x + at));
+    w[0] = load_input<IN_PLACE>(reinterpret_cast<const uint32_t*>(x + at));
   } else if constexpr (E == 4) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(x + at));
+    const uint2 u = load_input<IN_PLACE>(reinterpret_cast<const uint2*>(x + at));
     w[0] = u.x;
     w[1] = u.y;
   } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + at));
+    const uint4 u = load_input<IN_PLACE>(reinterpret_cast<const uint4*>(x + at));
     w[0] = u.x;
     w[1] = u.y;
     w[2] = u.z;
@@ -181,11 +189,11 @@ __device__ __forceinline__ void load_run(const uint16_t* x, int at, float (&y)[E
 // y = the lane's coordinates of x, turned by its token's position if TURN.  A pair of the
 // half layout may lie in two lanes: each loads the partner's run too (an L1 hit) rather than
 // exchange it, which works for every rotated size.
-template <int D, int E, bool TURN>
+template <int D, int E, bool TURN, bool IN_PLACE = false>
 __device__ __forceinline__ void load_heads(const uint16_t* x, const RopeParams& rope, int token, int lane,
                                            float (&y)[E]) {
   const int c0 = lane * E;
-  load_run<E>(x, c0, y);
+  load_run<E, IN_PLACE>(x, c0, y);
   if constexpr (TURN) {
     const int pos = __ldg(rope.positions + token), half = rope.rot / 2;
     if (c0 < rope.rot) {
@@ -202,12 +210,12 @@ __device__ __forceinline__ void load_heads(const uint16_t* x, const RopeParams& 
       } else {
         float o[E];
         if (half % E == 0) {  // the run lies in one half of the pairs, as does its partner
-          load_run<E>(x, c0 < half ? c0 + half : c0 - half, o);
+          load_run<E, IN_PLACE>(x, c0 < half ? c0 + half : c0 - half, o);
         } else {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const int c = c0 + e;
-            o[e] = c < rope.rot ? __half2float(__ushort_as_half(__ldg(x + (c < half ? c + half : c - half)))) : 0.f;
+            o[e] = c < rope.rot ? __half2float(__ushort_as_half(load_input<IN_PLACE>(x + (c < half ? c + half : c - half)))) : 0.f;
           }
         }
 #pragma unroll

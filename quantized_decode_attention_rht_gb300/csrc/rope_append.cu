@@ -29,7 +29,7 @@ __device__ __forceinline__ void turn_queries(const SmallParams& p) {
   for (long long v = blockIdx.x * kWarps + (threadIdx.x >> 5); v < n; v += (long long)gridDim.x * kWarps) {
     const int token = (int)(v / p.hq), h = (int)(v - (long long)token * p.hq);
     float y[E];
-    load_heads<D, E, true>(p.q + token * p.qt + h * p.qh, p.rope, token, lane, y);
+    load_heads<D, E, true, true>(p.q + token * p.qt + h * p.qh, p.rope, token, lane, y);
     uint32_t w[E / 2];
 #pragma unroll
     for (int k = 0; k < E / 2; ++k) {

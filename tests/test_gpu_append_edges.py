@@ -89,3 +89,26 @@ def test_a_codebook_vector_that_is_not_finite_has_codes_of_zero(d, hkv, bits):
                 gone = bad if side or scale == 1.0 else x.any(-1)  # values are not scaled
                 assert not rows[side][gone].any() and not np.isfinite(rows[2 + side][gone]).any()
                 assert np.isfinite(rows[2 + side][~gone]).all() and rows[side][~gone].any(-1).all()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d,rot", [(64, 64), (64, 36), (128, 128), (128, 50), (256, 256), (256, 100)])
+def test_queries_in_place_in_the_same_launch(d, rot, layout):
+    """Queries of a step turned in place, many heads to an SM, partners in other lanes: what they are out
+    of place, to the bit, whatever lies beside them."""
+    torch, kvq = gu.torch_cuda(), gu.kvq_module()
+    t, hq, hkv = 150, 96, 2
+    rng = np.random.default_rng(rot)
+    signs = np.ones((hkv, d), dtype=np.int8)
+    cache = kvq.PagedCache(d, hkv, 10, "fp16", "fp16", 0, 0, signs, signs)
+    x = torch.from_numpy(rng.standard_normal((t, hq + 2 * hkv, d)).astype(np.float16)).cuda()
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    rest = x[:, hq:].clone()
+    pos = torch.from_numpy(rng.integers(0, 1 << 20, t).astype(np.int32)).cuda()
+    slots = torch.arange(t, dtype=torch.int32, device="cuda")
+    rope = make_rope(kvq, rot, layout)
+    for _ in range(5):
+        want = torch.empty(t, hq, d, dtype=torch.float16, device="cuda")
+        kvq.kvq_rope_append(cache.struct, rope, pos, k, v, slots, q, want)
+        kvq.kvq_rope_append(cache.struct, rope, pos, k, v, slots, q)
+        assert torch.equal(q, want) and torch.equal(x[:, hq:], rest)
