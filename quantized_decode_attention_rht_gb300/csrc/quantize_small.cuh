@@ -215,7 +215,8 @@ __device__ __forceinline__ void load_heads(const uint16_t* x, const RopeParams& 
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const int c = c0 + e;
-            o[e] = c < rope.rot ? __half2float(__ushort_as_half(load_input<IN_PLACE>(x + (c < half ? c + half : c - half)))) : 0.f;
+            const uint16_t* partner = x + (c < half ? c + half : c - half);
+            o[e] = c < rope.rot ? __half2float(__ushort_as_half(load_input<IN_PLACE>(partner))) : 0.f;
           }
         }
 #pragma unroll

@@ -4,8 +4,10 @@ import numpy as np
 import pytest
 
 from oracle import cache as ocache
+from oracle import formats as ofmt
+from oracle import rope as orope
 from tests import gpu_util as gu
-from tests.test_gpu_rope import make_rope
+from tests.test_gpu_rope import frequencies, make_rope
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +114,68 @@ def test_queries_in_place_in_the_same_launch(d, rot, layout):
         kvq.kvq_rope_append(cache.struct, rope, pos, k, v, slots, q, want)
         kvq.kvq_rope_append(cache.struct, rope, pos, k, v, slots, q)
         assert torch.equal(q, want) and torch.equal(x[:, hq:], rest)
+
+
+@pytest.mark.parametrize("quarters", [True, False])
+@pytest.mark.parametrize("t", [1, 33, 5700])
+@pytest.mark.parametrize("fmt", ["codebook_qjl", "codebook_outlier"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_side_data_of_turned_keys(fmt, t, layout, quarters):
+    """Everything a key with a sketch or an outlier stream stores (codes, norm, sketch bits, residual norm;
+    outlier scale and levels), against the oracle's encode of the turned key.
+
+    Quarter turns: cos and sin are 0 and +-1, the turned key is an fp16 vector, and the criteria are
+    those of kvq_quantize_append.  Any angle: a turned element is within (|a| + |b|) 2^-21 of the
+    exact one.  That is far below a step of what is stored, so fp16 numbers differ by at most one
+    step and levels by at most one; codes and sketch bits may differ where they are that close to a
+    border: the error of u, about 2^-19, times the density of 7 borders and of the projections at theirs,
+    below 1e-4 of them in either, and 1e-3 allowed.  Rows whose codes differ have another residual."""
+    torch, kvq = gu.torch_cuda(), gu.kvq_module()
+    rng = np.random.default_rng(t)
+    hkv, d, ps, bits = 3, 128, 16, 3
+    k = rng.standard_normal((t, hkv, d)).astype(np.float16)
+    k[:, :, 11] *= 20
+    pos = rng.integers(0, 1 << 16, t).astype(np.int32)
+    signs = np.where(rng.integers(0, 2, (hkv, d)) == 0, 1, -1).astype(np.int8)
+    proj = rng.standard_normal((128, d)).astype(np.float32)
+    outl = np.stack([rng.choice(d, 8, replace=False) for _ in range(hkv)]).astype(np.int32)
+    pages = (t + ps - 1) // ps
+    cache = kvq.PagedCache(d, hkv, pages, fmt, "codebook", bits, 4, signs, signs, ps, k_qjl=proj, k_outliers=outl)
+    slots = rng.permutation(pages * ps)[:t].astype(np.int32)
+    rope = make_rope(kvq, d, layout)
+    if quarters:
+        rope.turns.fill_(1 << 62)
+    kd = torch.from_numpy(k).cuda()
+    kvq.kvq_rope_append(cache.struct, rope, torch.from_numpy(pos).cuda(), kd, kd, torch.from_numpy(slots).cuda())
+    torch.cuda.synchronize()
+    rows, aux = gu.pool_rows(cache.k_rows, slots), gu.pool_rows(cache.k_aux, slots)
+    if quarters:
+        a, b = orope.pair_index(d, layout)
+        turned = k.copy()
+        c, s = (np.array(x)[pos % 4][:, None, None] for x in ([1, 0, -1, 0], [0, 1, 0, -1]))
+        turned[..., a], turned[..., b] = k[..., a] * c - k[..., b] * s, k[..., b] * c + k[..., a] * s
+        for h in range(hkv):
+            if fmt == "codebook_qjl":
+                gu.check_qjl_rows(turned[:, h], signs[h], bits, proj, rows[:, h], aux[:, h])
+            else:
+                gu.check_outlier_rows(turned[:, h], signs[h], bits, outl[h], rows[:, h], aux[:, h])
+        return
+    turned = orope.apply(k, pos, frequencies(d, "none"), layout)
+    c32, b32 = gu.tables("lloyd_max", bits)
+    step = lambda x, y: np.abs(x.view(np.int16).astype(int) - y.view(np.int16).astype(int))  # noqa: E731
+    nb, off, all_bits = d * bits // 8, 0, 0
+    for h in range(hkv):
+        ro, ao = ocache.encode(turned[:, h], signs[h], fmt, bits, b32, c32, proj, outl[h])
+        got = ofmt.unpack_bits(rows[:, h, :nb], bits, d) != ofmt.unpack_bits(ro[:, :nb], bits, d)
+        assert np.mean(got) < 1e-3
+        same = ~got.any(-1)
+        if fmt == "codebook_qjl":
+            assert step(aux[:, h, 0], ao[:, 0]).max() <= 1 and np.all(step(aux[same, h, 1], ao[same, 1]) <= 1)
+            off += int(np.sum(ofmt.unpack_bits(rows[same, h, nb:], 1, 128) != ofmt.unpack_bits(ro[same, nb:], 1, 128)))
+            all_bits += 128 * int(same.sum())
+        else:
+            for x, y in zip(ocache.unpack_outlier_aux(aux[:, h])[:2], ocache.unpack_outlier_aux(ao)[:2]):
+                assert step(x, y).max() <= 1
+            q, qo = (ocache.unpack_outlier_aux(z)[2].astype(int) for z in (aux[:, h], ao))
+            assert np.abs(q - qo).max() <= 1 and np.mean(q != qo) < 0.02
+    assert off <= 1e-3 * all_bits
