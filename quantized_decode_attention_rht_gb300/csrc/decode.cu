@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_tier_kernel(const DecParam
     float a = 0.f, s = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w_m[w][g] == -INFINITY) continue;  // a warp that saw no token
+      if (w_l[w][g] == 0.f) continue;  // a warp that saw no token (scores of NaN leave a sum of NaN)
       const float f = exp2_fast(w_m[w][g] - mx);
       a += w_acc[w][g][j] * f;
       s += w_l[w][g] * f;

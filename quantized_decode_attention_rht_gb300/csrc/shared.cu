@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
       for (int k = 0; k < 4; ++k) y[k] += s_acc[i][4 * lane + k];
     }
   }
-  const float inv = l > 0.f ? inv_sqrt_dim(128) / l : 0.f;  // no token at all: zeros
+  // No token at all: zeros.  (A query that is not finite has no maximum and a sum of NaN: NaN.)
+  const float inv = l == 0.f ? 0.f : inv_sqrt_dim(128) / l;
 #pragma unroll
   for (int k = 0; k < 4; ++k) y[k] *= inv;
   sign_free_rotate<4>(lane, y);

@@ -220,3 +220,27 @@ def test_what_lies_behind_the_sequences_is_not_attended(name, d, hq):
             a[pages, :, offs] = 0x7F if a is cache.k_aux or "fp" in name else 0xFF
     for got, x in zip(run(), want):
         assert np.array_equal(got, x)
+
+
+@pytest.mark.parametrize("name,d,hq", [("fp16", 128, 8), ("fp8_int4", 128, 8), ("cb4", 128, 8), ("cb4", 128, 2),
+                                       ("cb32", 128, 4), ("fp8_fp16", 128, 8), ("fp16", 64, 4), ("fp8_int4", 256, 4),
+                                       ("cb4", 256, 2)])
+def test_a_query_that_is_not_finite_without_a_prefix(name, d, hq):
+    """Sequences outside every group, of one token and of many, and one without any: a query with a NaN
+    or an infinity gives NaN, of the shared and of the plain decode, and zeros only where no token is."""
+    torch, kvq = modules()
+    lens = [1, 40, 700, 0, 9]
+    c = Case(kvq, torch, [name], [[30]], [4, 5], [name], [lens], hq=hq, hkv=2, d=d, seed=d + hq)
+    want = call(kvq, torch, c.prefix, c.offsets, c.own, c.q), gu.gpu_decode(kvq, torch, c.own, c.q)
+    keep = c.q.copy()
+    bad = [(0, 0), (1, hq - 1), (2, 1), (3, 0), (4, hq - 1)]
+    for i, (b, h) in enumerate(bad):
+        c.q[b, h, 7] = (np.nan, np.inf, -np.inf, np.nan, np.nan)[i]
+    got = call(kvq, torch, c.prefix, c.offsets, c.own, c.q), gu.gpu_decode(kvq, torch, c.own, c.q)
+    c.q = keep
+    for x, y in zip(got, want):
+        for b, h in bad:
+            if lens[b]:
+                assert np.isnan(x[b, h]).all(), (b, h)
+            x[b, h] = y[b, h] if lens[b] else x[b, h]
+        assert np.array_equal(x, y)
