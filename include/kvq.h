@@ -479,7 +479,8 @@ KVQ_API kvq_status kvq_decode_attention_ex(const kvq_tier_view* tiers, int32_t n
  *                   kvq_decode_options; not written by a call with batch 0)
  * All tiers agree in head_dim, num_kv_heads, page_size and signs (else
  * KVQ_ERR_INVALID_ARGUMENT), num_prefix_tiers + num_tiers <= KVQ_MAX_TIERS, and batch x
- * num_q_heads <= 2^24 (else KVQ_ERR_UNSUPPORTED).  A call captured into a graph keeps its group
+ * num_q_heads <= 2^24 and a prefix table's max_pages x page_size < 2^31 - 256 (else
+ * KVQ_ERR_UNSUPPORTED).  A call captured into a graph keeps its group
  * offsets; lengths and block tables are read when it runs.
  * The output is fp16, and so is what the tensor cores multiply (rotated queries, decoded rows
  * that are not fp16 values already, softmax weights), with float32 scores, sums and

@@ -283,6 +283,9 @@ kvq_status check_call(const Call& c, kvq_tier_view* all) {
   const kvq_status st = check_tiers(all, c.num_prefix + c.num_tiers, c.batch, c.hq);
   if (st != KVQ_OK) return st;
   if ((long long)c.batch * c.hq > (1LL << 24)) return KVQ_ERR_UNSUPPORTED;
+  // the prefix pass counts the tokens of a tile, the last one's end among them, in 32 bits
+  for (int i = 0; i < c.num_prefix; ++i)
+    if ((long long)usable_pages(all[i]) * all[i].cache->page_size > 0x7FFFFFFFLL - 2 * kTileTokens) return KVQ_ERR_UNSUPPORTED;
   return KVQ_OK;
 }
 

@@ -302,3 +302,33 @@ def test_shared_binding_checks(kvq):
         call([view(1)], [0, 3], [view(b)], q, out, None)
     with pytest.raises(TypeError):
         call([view(1)], [0, 3], [view(b)], q, out, ws, status=dev((1,), torch.int64))
+
+
+def test_shared_prefix_tables_stay_inside_32_bits(kvq):
+    """A table that names pages again and again may reach 2^31 tokens from a small pool.  The prefix
+    pass counts tokens in 32 bits up to the end of the last tile: a table whose last tile may end
+    beyond is refused, whatever the kernel family, before anything is launched."""
+    d, hkv = 128, 2
+    signs = np.ones((hkv, d), dtype=np.int8)
+    n = kvq.kvq_kernel_launches()
+    for fmt, bits in (("codebook", 4), ("fp16", 0)):
+        cache = kvq.PagedCache(d, hkv, 2, fmt, fmt, bits, bits, signs, signs, page_size=16, device="cpu")
+
+        def struct(ps):
+            s = kvq.KvqCache()
+            ctypes.memmove(ctypes.byref(s), ctypes.byref(cache.struct), ctypes.sizeof(s))
+            s.k_rows, s.v_rows, s.k_signs, s.v_signs = (1 << 12,) * 4
+            s.k_aux = s.v_aux = 1 << 12
+            s.page_size = ps
+            return s
+
+        for ps, most in ((16, (1 << 27) - 17), (1 << 20, (1 << 11) - 1)):
+            c = struct(ps)
+            assert shared_call(kvq, None, [(c, 64, 64, most)], [0, 4], [], size=True)[0] == 0, ps
+            for pages in (most + 1, 1 << 30):
+                assert shared_call(kvq, None, [(c, 64, 64, pages)], [0, 4], [], size=True)[0] == UNSUPPORTED, (ps, pages)
+                assert shared_call(kvq, None, [(c, 64, 64, pages)], [0, 4], []) == UNSUPPORTED, (ps, pages)
+                if ps > 16:  # a tier behind a shorter one
+                    both = [(c, 64, 64, 1), (c, 64, 64, pages)]
+                    assert shared_call(kvq, None, both, [0, 4], []) == UNSUPPORTED
+    assert kvq.kvq_kernel_launches() == n
