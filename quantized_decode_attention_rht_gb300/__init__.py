@@ -214,15 +214,14 @@ _current_device = _raw_stream = None  # torch's look-ups without an object aroun
 
 
 def _call_stream(stream, first, *others) -> Optional[int]:
-    """The stream of a call, whose tensors lie on one device: the current one, unless the caller
-    names a stream (of that device)."""
+    """The stream of a call, whose tensors lie on the current device: its current one, unless the caller
+    names a stream of that device.  (The library launches on the current device, and a plain
+    number, 0 among them, does not tell which device's stream it is.)"""
     global _current_device, _raw_stream
     index = first.get_device()
     for t in others:
         if t is not None and t.get_device() != index:
             raise ValueError(f"tensors of one call on different devices: cuda:{index} and cuda:{t.get_device()}")
-    if stream is not None:
-        return stream if isinstance(stream, int) else stream.cuda_stream
     if _current_device is None:
         torch = _load_torch()
         _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -230,7 +229,13 @@ def _call_stream(stream, first, *others) -> Optional[int]:
                               lambda _: torch.cuda.current_stream().cuda_stream)
     if index != _current_device():
         raise ValueError(f"tensors on cuda:{index}, but the current device is cuda:{_current_device()}")
-    return _raw_stream(index)
+    if stream is None:
+        return _raw_stream(index)
+    if isinstance(stream, int):
+        return stream
+    if getattr(stream, "device_index", index) != index:
+        raise ValueError(f"tensors on cuda:{index}, but a stream of cuda:{stream.device_index}")
+    return stream.cuda_stream
 
 
 # ----------------------------------------------------------------------------- host-side entry points

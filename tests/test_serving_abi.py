@@ -332,3 +332,76 @@ def test_shared_prefix_tables_stay_inside_32_bits(kvq):
                     both = [(c, 64, 64, 1), (c, 64, 64, pages)]
                     assert shared_call(kvq, None, both, [0, 4], []) == UNSUPPORTED
     assert kvq.kvq_kernel_launches() == n
+
+
+class On(Heads):
+    """A stand-in on a device, with an address that is never read."""
+
+    def __init__(self, t, index=0):
+        super().__init__(t)
+        self.index = index
+
+    def get_device(self):
+        return self.index
+
+    def data_ptr(self):
+        return 1 << 12
+
+    def element_size(self):
+        return self.t.element_size()
+
+
+class Stream:
+    def __init__(self, device_index):
+        self.device_index, self.cuda_stream = device_index, 77
+
+
+def test_serving_calls_stay_on_the_current_device(kvq, monkeypatch):
+    """The library launches on the current device: tensors of another one, a stream of another one and
+    tensors of two are refused by the binding, whether the caller names a stream or not."""
+    seen = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: seen.append((name, args)) or 0
+
+    d, hkv, hq, t = 128, 2, 4, 3
+    signs = np.ones((hkv, d), dtype=np.int8)
+    cache = kvq.PagedCache(d, hkv, 4, "codebook", "codebook", 4, 4, signs, signs, device="cpu")
+    rope = kvq.Rope(128, "half", device="cpu")
+    monkeypatch.setattr(kvq, "_lib_handle", Library())
+    monkeypatch.setattr(kvq, "_current_device", lambda: 0)
+    monkeypatch.setattr(kvq, "_raw_stream", lambda index: 1000 + index)
+    on = lambda shape, dtype=torch.float16, index=0: On(torch.zeros(shape, dtype=dtype), index)  # noqa: E731
+    i32 = torch.int32
+
+    def calls(index, stream, odd=None):
+        """The four calls with tensors on `index`, one of them (odd) on the other device."""
+        at = lambda name: 1 - index if name == odd else index  # noqa: E731
+        rope.turns = On(torch.zeros(64, dtype=torch.int64), at("turns"))
+        pos, slots = on((t,), i32, at("ints")), on((t,), i32, index)
+        q, k = on((t, hq, d), index=index), on((t, hkv, d), index=at("heads"))
+        view = lambda n: kvq.TierView(cache, on((n, 4), i32, at("table")), on((n,), i32, index))  # noqa: E731
+        yield "turns ints heads", lambda: kvq.kvq_rope_apply(rope, pos, q, k, stream=stream)
+        yield "turns ints heads", lambda: kvq.kvq_rope_append(cache.struct, rope, pos, k, k, slots, q, stream=stream)
+        yield "ints heads", lambda: kvq.kvq_dequantize(cache.struct, pos, k, on((t, hkv, d), index=index), stream=stream)
+        yield "table", lambda: kvq.kvq_decode_attention_shared([view(1)], [0, t], [view(t)], q, on((t, hq, d), index=index),
+                                                               on((64,), torch.uint8, index), stream=stream)
+
+    for stream, handle in ((None, 1000), (0, 0), (5, 5), (Stream(0), 77)):
+        for _, call in calls(0, stream):
+            call()
+            assert seen.pop()[1][-1] == handle and not seen  # the stream is every call's last argument
+    for stream in (None, 0, 5, Stream(0), Stream(1)):
+        for _, call in calls(1, stream):
+            with pytest.raises(ValueError, match="device"):
+                call()
+        for odd in ("turns", "ints", "heads", "table"):
+            for parts, call in calls(0, stream, odd):
+                if odd in parts:
+                    with pytest.raises(ValueError, match="device"):
+                        call()
+    for _, call in calls(0, Stream(1)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+    assert not seen
