@@ -3,11 +3,12 @@
 // Pair j of a head at position p is turned by theta = p w_j.  What the turn needs is theta
 // modulo a full turn, and in float32 the product p w_j has lost it long before today's
 // context lengths (half an ulp of 2^20 radians is 0.06).  So a pair's frequency is stored as
-// the fraction of a turn per token in 64-bit fixed point, t_j = round(2^64 w_j / 2 pi) mod
+// the fraction of a turn per token in 64-bit fixed point, t_j = floor(2^64 w_j / 2 pi) mod
 // 2^64, and the position multiplies it modulo 2^64: the reduction is exact, for negative
-// positions too, and only the stored frequency's own rounding (2^-53 relative: it comes from
-// a double) grows with p.  The top 32 bits, as a signed number, are the angle in
-// [-1/2, 1/2) turns.
+// positions too, and only the stored frequency's own rounding (2^-53 relative, it comes from
+// a double, and 2^-64 of a turn) grows with p.  The 64 bits, as a signed number, are the angle in
+// [-1/2, 1/2) turns.  (The top 32 alone would do for the cosine, but a slow pair's angle at a
+// small position, 2^-22 turns, would keep ten bits of its sine.)
 #pragma once
 #include "kvq_internal.cuh"
 
@@ -23,7 +24,7 @@ struct RopeParams {
 // Angle in half turns, in [-1, 1), of a pair at a position: rounded once, to 2^-24 of itself.
 __device__ __forceinline__ float rope_half_turns(unsigned long long turns, int position) {
   const unsigned long long phase = turns * (unsigned long long)(long long)position;
-  return (float)(int32_t)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31
+  return (float)(long long)phase * 1.0842021724855044e-19f;  // 2^-63
 }
 
 // (cos, sin) times the scale.  sincospif: within 1 ulp, so the float32 coefficients carry
