@@ -120,7 +120,8 @@ struct Plan {
   const bool ps16 = c->page_size == 16;
   if (ps16 && q16 && split_tokens <= gqa_max_chunk_tokens() &&
       gqa_fast_supported(c->head_dim, group, c->k_format, c->v_format) && aligned(c->k_signs, 16) &&
-      aligned(c->v_signs, 16))
+      aligned(c->v_signs, 16) &&
+      (c->v_format != KVQ_FMT_INT4_G32 || aligned(c->v_aux, 16)))  // scales are copied 16 bytes at a time
     return TIER_GQA;
   if (ps16 && cb_fast_supported(c->head_dim, group, c->k_format, c->v_format) && aligned(c->k_aux, 16) &&
       aligned(c->v_aux, 16))  // bulk copies of the norm runs need 16-byte aligned sources

@@ -244,3 +244,20 @@ def test_a_query_that_is_not_finite_without_a_prefix(name, d, hq):
                 assert np.isnan(x[b, h]).all(), (b, h)
             x[b, h] = y[b, h] if lens[b] else x[b, h]
         assert np.array_equal(x, y)
+
+
+@pytest.mark.parametrize("shift", [1, 4])  # fp16 numbers: 2 bytes, and the 8 that the prefix pass takes
+def test_int4_scales_at_other_addresses(shift):
+    """Scales that are not 16-byte aligned, of the prefix and of the sequences' own tier."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["fp8_int4"], [[300]], [0, 3], ["fp8_int4"], [[20, 0, 133]], hq=8, hkv=2, seed=shift)
+    want = call(kvq, torch, c.prefix, c.offsets, c.own, c.q), gu.gpu_decode(kvq, torch, c.own, c.q)
+    for cache in c.built.gpu:
+        flat = torch.empty(cache.v_aux.numel() + 8, dtype=torch.float16, device="cuda")
+        moved = flat[shift:shift + cache.v_aux.numel()].view(cache.v_aux.shape)
+        moved.copy_(cache.v_aux)
+        assert moved.data_ptr() % 16 == 2 * shift
+        cache.v_aux, cache.struct.v_aux = moved, moved.data_ptr()
+    c.check(call(kvq, torch, c.prefix, c.offsets, c.own, c.q))
+    got = gu.gpu_decode(kvq, torch, c.own, c.q)
+    assert np.linalg.norm(got - want[1]) <= 2.0 ** -16 * np.linalg.norm(want[1])

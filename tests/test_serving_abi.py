@@ -405,3 +405,43 @@ def test_serving_calls_stay_on_the_current_device(kvq, monkeypatch):
         with pytest.raises(ValueError, match="stream"):
             call()
     assert not seen
+
+
+def test_misaligned_int4_scales_leave_the_fused_kernel(kvq):
+    """The fused fp16 / fp8 kernel copies INT4 scales 16 bytes at a time: scales at other addresses make
+    the plan of the generic kernel (as another alignment of the signs does), in the plain and in the
+    shared decode."""
+    d, hkv, hq, b = 128, 2, 8, 4
+    signs = np.ones((hkv, d), dtype=np.int8)
+    cache = kvq.PagedCache(d, hkv, 64, "fp8_e4m3", "int4_g32", 0, 0, signs, signs, device="cpu")
+
+    def struct(**kw):
+        s = kvq.KvqCache()
+        ctypes.memmove(ctypes.byref(s), ctypes.byref(cache.struct), ctypes.sizeof(s))
+        s.k_rows, s.v_rows, s.k_aux, s.v_aux, s.k_signs, s.v_signs = (1 << 12,) * 6
+        for name, v in kw.items():
+            setattr(s, name, v)
+        return s
+
+    def plain(c):
+        arr = (kvq.KvqTierView * 1)()
+        arr[0].cache, arr[0].block_table, arr[0].seq_lens, arr[0].max_pages = ctypes.pointer(c), 64, 64, 512
+        n = ctypes.c_size_t()
+        assert kvq.lib().kvq_decode_workspace_size(arr, 1, b, hq, 0, ctypes.byref(n)) == 0
+        return n.value
+
+    def shared(c):
+        view = (c, 64, 64, 512)
+        st, n = shared_call(kvq, None, [view], [0, b], [view], batch=b, hq=hq, size=True)
+        assert st == 0
+        return n
+
+    generic = struct(k_signs=(1 << 12) + 4, v_signs=(1 << 12) + 4)
+    for off in (2, 4, 8, 14):
+        bad = struct(v_aux=(1 << 12) + off)
+        # (the size covers queries at any address, the generic kernel's plan too: never the smaller one)
+        assert plain(bad) == plain(generic)
+        if off % 8:
+            assert shared(bad) == shared(generic)
+    assert shared(struct(v_aux=(1 << 12) + 8)) != shared(struct())  # own tiers: another kernel's chunks
+    assert plain(struct()) >= plain(generic)
