@@ -212,6 +212,8 @@ KVQ_API kvq_status kvq_codebook_tables(int32_t bits, const double* centroids,
  * an empty append returns KVQ_OK whatever the pointers).  slot_mapping: int32
  * [num_tokens]; a negative slot skips the token; slots >= num_pages * page_size are
  * skipped too.  Two tokens of one call must not share a slot.  k, v: 16-byte aligned.
+ * Sign vectors aligned to head_dim / 32 bytes (else KVQ_ERR_INVALID_ARGUMENT); to 16 for the
+ * kernel of large appends.
  * Up to 16384 vectors per side (a decode step) take one launch for both sides; larger
  * appends one launch per side (keys with an outlier stream: one launch). */
 KVQ_API kvq_status kvq_quantize_append(const kvq_cache* cache, const uint16_t* k,

@@ -95,6 +95,9 @@ KVQ_API kvq_status kvq_quantize_append(const kvq_cache* cache, const uint16_t* k
   if (v && (st = check_side(c, c->v_format, c->v_bits, c->v_rows, c->v_aux, c->v_centroids, c->v_bounds,
                             c->v_signs, true, false)) != KVQ_OK)
     return st;
+  // a lane reads the signs of its head_dim / 32 coordinates in one piece
+  const int run = c->head_dim / 32;
+  if ((k && !aligned(c->k_signs, run)) || (v && !aligned(c->v_signs, run))) return KVQ_ERR_INVALID_ARGUMENT;
   QuantParams p;
   memset(&p, 0, sizeof(p));
   p.x[0] = k;

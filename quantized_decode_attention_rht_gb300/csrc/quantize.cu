@@ -44,10 +44,14 @@ cudaError_t launch_quantize(const QuantParams& p, int head_dim, cudaStream_t str
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // small appends, and keys with an outlier stream (whose channel split the per-thread
-  // kernel does not carry), take the warp-per-vector kernel
+  // small appends, keys with an outlier stream (whose channel split the per-thread kernel does
+  // not carry) and signs that it cannot read 16 bytes at a time take the warp-per-vector kernel
   const bool outl = p.side[0].fmt == KVQ_FMT_CODEBOOK_OUTLIER && p.kind_first == 0;
-  if ((long long)p.num_tokens * p.hkv <= kSmallMaxVectors || outl) return launch_quantize_small(p, head_dim, sms, stream);
+  bool apart = false;
+  for (int i = p.kind_first; i < p.kind_first + p.num_kinds; ++i)
+    apart = apart || reinterpret_cast<uintptr_t>(p.side[i].signs) % 16 != 0;
+  if (apart && (long long)p.num_tokens * p.hkv > (1LL << 28)) return cudaErrorInvalidValue;  // its units fit an int
+  if ((long long)p.num_tokens * p.hkv <= kSmallMaxVectors || outl || apart) return launch_quantize_small(p, head_dim, sms, stream);
   // kCoords coordinates per thread: head_dim / kCoords lanes per vector
   switch (head_dim) {
     case 64: return launch_tpv<64 / kCoords>(p, sms, stream);

@@ -184,3 +184,26 @@ def test_side_data_of_turned_keys(fmt, t, layout, quarters):
             q, qo = (ocache.unpack_outlier_aux(z)[2].astype(int) for z in (aux[:, h], ao))
             assert np.abs(q - qo).max() <= 1 and np.mean(q != qo) < 0.02
     assert off <= 1e-3 * all_bits
+
+
+@pytest.mark.parametrize("fmt,bits", [("codebook", 4), ("fp16", 0), ("int4_g32", 0)])
+@pytest.mark.parametrize("d,t,hkv", SIZES)
+def test_signs_at_other_addresses(d, t, hkv, fmt, bits):
+    """Signs aligned to head_dim / 32 bytes only, whatever the size of the append: vectors within the
+    float32 rounding of another kernel (codes and levels at a border)."""
+    torch, kvq = gu.torch_cuda(), gu.kvq_module()
+    rng = np.random.default_rng(d)
+    x = torch.from_numpy(rng.standard_normal((t, hkv, d)).astype(np.float16)).cuda()
+    signs = torch.from_numpy(np.where(rng.integers(0, 2, (hkv, d)) == 0, 1, -1).astype(np.int8)).cuda()
+    flat = torch.empty(hkv * d + 32, dtype=torch.int8, device="cuda")
+    moved = flat[d // 32:d // 32 + hkv * d].view(hkv, d)
+    moved.copy_(signs)
+    slots = torch.arange(t, dtype=torch.int32, device="cuda")
+    a, b = (kvq.PagedCache(d, hkv, (t + 15) // 16, fmt, fmt, bits, bits, s, s) for s in (signs, moved))
+    for cache in (a, b):
+        cache.append(x, x, slots)
+    assert b.k_signs.data_ptr() % 16 == d // 32
+    for m, n in ((a.k_rows, b.k_rows), (a.v_rows, b.v_rows)):
+        assert (m != n).float().mean().item() < 1e-3
+        if t == 40:
+            assert torch.equal(m, n)

@@ -445,3 +445,24 @@ def test_misaligned_int4_scales_leave_the_fused_kernel(kvq):
             assert shared(bad) == shared(generic)
     assert shared(struct(v_aux=(1 << 12) + 8)) != shared(struct())  # own tiers: another kernel's chunks
     assert plain(struct()) >= plain(generic)
+
+
+def test_append_refuses_signs_it_cannot_read(kvq):
+    """A lane reads the signs of head_dim / 32 coordinates at once: other addresses are refused before
+    anything is launched, for the side that is appended."""
+    for d in (64, 128, 256):
+        signs = np.ones((2, d), dtype=np.int8)
+        cache = kvq.PagedCache(d, 2, 4, "fp16", "fp16", 0, 0, signs, signs, device="cpu")
+        s = kvq.KvqCache()
+        ctypes.memmove(ctypes.byref(s), ctypes.byref(cache.struct), ctypes.sizeof(s))
+        s.k_rows = s.v_rows = 1 << 12
+        f = kvq.lib().kvq_quantize_append
+        n = kvq.kvq_kernel_launches()
+        for off in range(1, d // 32):
+            s.k_signs, s.v_signs = (1 << 12) + off, 1 << 12
+            assert f(ctypes.byref(s), 256, 256, 3, 64, None) == INVALID
+            assert f(ctypes.byref(s), 256, None, 3, 64, None) == INVALID
+            s.k_signs, s.v_signs = 1 << 12, (1 << 12) + off
+            assert f(ctypes.byref(s), 256, 256, 3, 64, None) == INVALID
+            assert f(ctypes.byref(s), None, 256, 3, 64, None) == INVALID
+        assert kvq.kvq_kernel_launches() == n
