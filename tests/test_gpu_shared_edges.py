@@ -10,6 +10,7 @@ import pytest
 
 from oracle import attention as oatt
 from oracle import cache as ocache
+from oracle import shared as oshared
 from tests import gpu_util as gu
 from tests.test_gpu_shared import Case
 
@@ -261,3 +262,82 @@ def test_int4_scales_at_other_addresses(shift):
     c.check(call(kvq, torch, c.prefix, c.offsets, c.own, c.q))
     got = gu.gpu_decode(kvq, torch, c.own, c.q)
     assert np.linalg.norm(got - want[1]) <= 2.0 ** -16 * np.linalg.norm(want[1])
+
+
+@pytest.mark.parametrize("name", ["fp16", "fp8_int4", "cb4", "cb32"])
+def test_long_sequences_beside_a_prefix(name):
+    """Sequences of their own long enough for hundreds of partial results a row, beside one of a few
+    tokens and one of none: the joining pass goes over its partials more than once."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, [name], [[3000]], [0, 3], [name], [[60000, 0, 77]], hq=4, hkv=1, seed=40)
+    got = call(kvq, torch, c.prefix, c.offsets, c.own, c.q)
+    c.check(got)
+
+
+@pytest.mark.parametrize("name,d", [("fp16", 128), ("cb4", 128), ("fp16", 64)])
+@pytest.mark.parametrize("own", [True, False])
+@pytest.mark.parametrize("offsets", [[0, 0], [2, 2, 2], [3, 3], [0, 2]])
+def test_groups_without_sequences(offsets, own, name, d):
+    """Groups without a sequence, eager and replayed: no prefix pass runs, sequences outside have their
+    own tokens or none (zeros)."""
+    torch, kvq = modules()
+    lens = [[5, 0, 40]] if own else []
+    c = Case(kvq, torch, [name], [[50] * (len(offsets) - 1)], offsets, [name] if own else [], lens or [[0] * 3], hq=4,
+             hkv=2, d=d, seed=41)
+    c.batch = 3
+    c.q = np.random.default_rng(3).standard_normal((3, 4, d)).astype(np.float16)
+    ora = c.built.ora
+    c.tiers = oshared.as_tiers(ora[:1], offsets, ora[1:], 3)
+    q = torch.from_numpy(c.q).cuda()
+    out, again = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    ws = torch.full((kvq.kvq_decode_shared_workspace_size(c.prefix, offsets, c.own, 3, 4),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    bits = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    run = lambda to: kvq.kvq_decode_attention_shared(c.prefix, offsets, c.own, q, to, ws, bits)  # noqa: E731
+    run(out)
+    torch.cuda.synchronize()
+    c.check(out.cpu().numpy())
+    assert int(bits.item()) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(again)
+    ws.fill_(0xFF)
+    bits.fill_(-1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, again) and int(bits.item()) == 0
+
+
+@pytest.mark.parametrize("name,d", [("fp8_int4", 128), ("cb4", 128), ("cb4", 256)])
+def test_output_over_the_queries(name, d):
+    """out may be q itself: every pass has read the queries before the last one writes."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, [name], [[700]], [0, 20], [name], [[30] * 20], hq=8, hkv=2, d=d, seed=42)
+    want = call(kvq, torch, c.prefix, c.offsets, c.own, c.q)
+    q = torch.from_numpy(c.q).cuda()
+    ws = torch.empty(kvq.kvq_decode_shared_workspace_size(c.prefix, c.offsets, c.own, 20, 8), dtype=torch.uint8, device="cuda")
+    kvq.kvq_decode_attention_shared(c.prefix, c.offsets, c.own, q, q, ws)
+    assert np.array_equal(q.cpu().numpy().astype(np.float64), want)
+
+
+def test_calls_on_many_streams_at_once():
+    """Sixteen calls in flight on as many streams, of both kinds of prefix and several shapes, with a
+    workspace each: the results of the calls alone."""
+    torch, kvq = modules()
+    cases = [Case(kvq, torch, [name], [[length]], [0, batch], [name], [[9] * batch], hq=8, hkv=2, seed=43 + i)
+             for i, (name, length, batch) in enumerate([("cb4", 900, 6), ("fp8_int4", 3000, 40), ("fp16", 130, 2),
+                                                        ("cb32", 5000, 33)])]
+    q = [torch.from_numpy(c.q).cuda() for c in cases]
+    want = [call(kvq, torch, c.prefix, c.offsets, c.own, c.q) for c in cases]
+    jobs = []
+    for i in range(16):
+        c, x = cases[i % 4], q[i % 4]
+        need = kvq.kvq_decode_shared_workspace_size(c.prefix, c.offsets, c.own, c.batch, 8)
+        jobs.append((c, x, torch.empty_like(x), torch.empty(need, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, x, out, ws, stream in jobs:
+            kvq.kvq_decode_attention_shared(c.prefix, c.offsets, c.own, x, out, ws, stream=stream)
+    torch.cuda.synchronize()
+    for i, (_, _, out, _, _) in enumerate(jobs):
+        assert np.array_equal(out.cpu().numpy().astype(np.float64), want[i % 4]), i
