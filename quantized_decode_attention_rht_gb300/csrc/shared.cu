@@ -42,12 +42,12 @@ struct JoinParams {  // small: a launch's parameters are read through a cold cac
 
 // Where row (b, h)'s partials lie: the prefix's first, then those of the sequence's tiers.
 struct Parts {
-  int pre, per_split;            // prefix partials; 1 or 2 per split
+  int pre;                       // prefix partials, two a split
   int own[KVQ_MAX_TIERS];        // split-K chunks of each tier that hold tokens
   int total;
 };
 
-__device__ __forceinline__ void find_prefix_parts(const JoinParams& p, int b, int h, Parts& n) {
+__device__ __forceinline__ void find_prefix_parts(const JoinParams& p, int b, Parts& n) {
   int lo = 0, hi = p.num_groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -55,13 +55,7 @@ __device__ __forceinline__ void find_prefix_parts(const JoinParams& p, int b, in
     else hi = mid;
   }
   const int first = p.offset[lo], end = p.offset[lo + 1];
-  n.pre = 0;
-  n.per_split = 1;
-  if (b >= first && b < end) {
-    const int row = ((b - first) << p.group_shift) + (h & ((1 << p.group_shift) - 1));
-    n.per_split = block_partials((end - first) << p.group_shift, row / kItemRows);
-    n.pre = p.splits * n.per_split;
-  }
+  n.pre = b >= first && b < end ? 2 * p.splits : 0;
 }
 __device__ __forceinline__ void find_own_parts(const JoinParams& p, const int (&lens)[KVQ_MAX_TIERS], Parts& n) {
   n.total = n.pre;
@@ -78,8 +72,8 @@ __device__ __forceinline__ void find_own_parts(const JoinParams& p, const int (&
 }
 
 // Partial j of the row: its (max, sum) and accumulator.
-__device__ __forceinline__ size_t prefix_part(const JoinParams& p, const Parts& n, size_t row, int j) {
-  return (size_t)(n.per_split == 2 ? j : 2 * j) * p.batch * p.hq + row;
+__device__ __forceinline__ size_t prefix_part(const JoinParams& p, size_t row, int j) {
+  return (size_t)j * p.batch * p.hq + row;
 }
 __device__ __forceinline__ size_t own_part(const JoinParams& p, const Parts& n, size_t row, int j) {
   int split = 0;
@@ -106,7 +100,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
   const bool there = row < (long long)p.batch * p.hq;  // whole warps; with eight warps a row, whole blocks
   const int b = there ? (int)(row / p.hq) : 0, h = there ? (int)(row - (long long)b * p.hq) : 0;
   Parts n;
-  find_prefix_parts(p, b, h, n);
+  find_prefix_parts(p, b, n);
   const uint32_t sg =
       __ldg(reinterpret_cast<const uint32_t*>(p.v_signs + (size_t)(h >> p.group_shift) * 128) + lane);
   int lens[KVQ_MAX_TIERS];
@@ -132,7 +126,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
   float2 x0 = make_float2(-INFINITY, 0.f), x;
   const float* acc0 = nullptr;
   if (j0 < n.pre) {
-    const size_t at = prefix_part(p, n, row, j0);
+    const size_t at = prefix_part(p, row, j0);
     x0 = p.ml[at];
     acc0 = p.acc + at * 128;
   }
@@ -145,7 +139,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinP
   auto look = [&](int j, float2& y) -> const float* {
     y = make_float2(-INFINITY, 0.f);
     if (j >= n.total) return nullptr;
-    const size_t at = j < n.pre ? prefix_part(p, n, row, j) : own_part(p, n, row, j);
+    const size_t at = j < n.pre ? prefix_part(p, row, j) : own_part(p, n, row, j);
     y = j < n.pre ? p.ml[at] : p.own_ml[at];
     return (j < n.pre ? p.acc : p.own_acc) + at * 128;
   };
@@ -291,11 +285,11 @@ kvq_status check_call(const Call& c, kvq_tier_view* all) {
 
 // Chunks of the prefix: enough items to fill the GPU in whole waves, few enough that writing
 // and joining partial results does not cost more than the idle SMs would.  In units of one
-// tile's time (both accumulators): an item is its tiles plus a fixed start and end, a split's
+// tile's time: an item is its tiles plus a fixed start and end, a split's
 // partials are a pass over them at memory speed.
 int choose_splits(long long row_blocks, long long rows, int max_tiles, int sms, int own_blocks) {
   const double start = 5.0;                                   // tiles' worth of set-up, fill and drain
-  const double partial = (double)rows * 1040.0 / 3.5e12 / 1.5e-6;  // write + read of one split's partials
+  const double partial = (double)rows * 2080.0 / 3.5e12 / 1.5e-6;  // write + read of one split's two partials
   int best = 1;
   double least = 1e300;
   // (beyond two waves more splits only add partials)
@@ -357,7 +351,7 @@ kvq_status make_shared_plan(const Call& c, const kvq_tier_view* all, bool q16, S
   at = align_up(plan->dec_bytes, 256);
   for (int g = 0; g < c.num_groups; ++g) {
     const long long r = (long long)(c.offsets[g + 1] - c.offsets[g]) * group;
-    plan->block[g + 1] = plan->block[g] + (int)((r + kItemRows - 1) / kItemRows);
+    plan->block[g + 1] = plan->block[g] + (int)((r + kTileRows - 1) / kTileRows);
   }
   plan->num_blocks = plan->block[c.num_groups];
   long long tiles[KVQ_MAX_TIERS], sum = 0;

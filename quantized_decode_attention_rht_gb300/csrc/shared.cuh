@@ -4,8 +4,8 @@
 
 namespace kvq {
 
-// Tokens of a tile, query rows of one accumulator, rows of a work item (two accumulators).
-constexpr int kTileTokens = 128, kTileRows = 128, kItemRows = 2 * kTileRows;
+// Tokens of a tile, query rows of a work item.
+constexpr int kTileTokens = 128, kTileRows = 128;
 
 struct SharedTier {
   const uint8_t* k_rows;
@@ -27,7 +27,7 @@ struct SharedParams {
   int num_tiers, num_groups;
   const __half* q;        // queries [batch * hq][128]
   const int8_t* k_signs;  // [hkv][128]
-  float* acc;        // partials [2 * splits][batch * hq][128]
+  float* acc;        // partials [2 * splits][batch * hq][128]: of each split's even and odd tiles
   float* ml;         // (max, sum) [2 * splits][batch * hq][2]
   int* err;
   int batch, hq, hkv, group, page_size, page_shift;
@@ -35,12 +35,6 @@ struct SharedParams {
   int offset[KVQ_MAX_PREFIX_GROUPS + 1];    // first sequence of each group
   int block[KVQ_MAX_PREFIX_GROUPS + 1];     // first row block of each group
 };
-
-// Partials that a row block leaves per split: one accumulator each where the block holds
-// more than kTileRows rows, else two (alternate tiles), at 2 s and 2 s + 1.
-__host__ __device__ __forceinline__ int block_partials(int rows_in_group, int block) {
-  return rows_in_group - block * kItemRows > kTileRows ? 1 : 2;
-}
 
 bool shared_tier_supported(int head_dim, int k_fmt, int v_fmt);
 cudaError_t launch_shared_prefix(const SharedParams& p, cudaStream_t stream);

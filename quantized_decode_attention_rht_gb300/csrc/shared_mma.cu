@@ -5,39 +5,42 @@
 // rotated queries q~ (rows) and the decoded rotated keys and values K, V of a chunk of the
 // prefix,
 //   S = q~ K^T,  P = 2^(S - m),  O = P V,  l = rowsum P
-// with an m that follows the row's running maximum.  The cache is read and decoded once for up to 256 rows,
+// with an m that follows the row's running maximum.  The cache is read and decoded once for up to 128 rows,
 // instead of once for every sequence.
 //
-// A block takes one work item: (chunk of the prefix, kv head, 256 rows).  Roles:
+// A block takes one work item: (chunk of the prefix, kv head, 128 rows).  Roles:
 //   8 softmax warps (two groups of 128 threads, a thread per row): S from TMEM, P back to TMEM
-//   4 + 4 decoding warps: K and V tiles of 128 tokens, read from the packed cache into
-//     registers two tiles ahead, decoded to fp16 into shared memory (128-byte swizzle)
+//   4 + 4 decoding warps: K and V tiles of 128 tokens; rows travel by asynchronous copies into slots of
+//     the decoding thread, and are decoded to fp16 into shared memory (128-byte swizzle)
 //   1 warp: issues the products and allocates TMEM
 //   2 warps: look up page numbers, rows, norms and scales, up to four tiles ahead.
-// Both products are tcgen05.mma of 128 x 128 x 16 steps: S = q~ K^T from shared memory, O += P V
+// All products are tcgen05.mma of 128 x 128 x 16 steps: S = q~ K^T from shared memory, O += P V
 // with P read from TMEM (it overwrites S) and V as it lies (tokens x coordinates, the
-// MN-major form).  The two softmax groups alternate, so that one's products run while the
-// other works on its scores: with more than 128 rows each has its own rows and both use every
-// tile; with up to 128 rows both have the same rows and take alternate tiles, which leaves two
-// partial results.  TMEM: two S and two O of 128 columns, all 512.
+// MN-major form).  The two softmax groups hold the same rows and take alternate tiles, so that one's
+// products run while the other works on its scores; that leaves two partial results.  TMEM: two S
+// and two O of 128 columns, all 512.
 //
 // m lies 2 (a factor of 4) below the largest score of the half tile that last raised it, so that
 // fp16 rounds a weight by at most 2^-27 of the largest: a tail of 2^17 such tokens is off by
 // 2^-10 of it at most.  An accumulator is rescaled only when half a tile's weights sum to more than
 // 2^15 in some row of a warp, which after the first tile is rare: until then weights stay inside
-// fp16 and the sums, in float32, inside their range.  (A larger distance makes it less rare:
-// 256 sequences x 64 heads on 16384 tokens took 144.1 us with none, 147.5 with 2, 149.3 with 3, 153.6 with 6.)
+// fp16.
 //
-// Rounded to fp16 on the way, each by at most 2^-11 of itself: the rotated queries, the weights,
-// INT4 levels times their scale, value centroids times their norm, and the centroids
-// themselves.  fp16 is what the tensor cores multiply at full rate.  Scores, maxima, sums and
-// accumulators are float32.  Two things keep the codebook formats as exact as the others, whose
-// keys are fp16 values already: a centroid's rounding is the same in every coordinate that has
-// its code, which with an outlier channel is nearly all of them, so the table is scaled by the
-// factor out of 128 whose roundings are smallest (undone in float32); and a key's norm
-// multiplies its scores, in float32, in place of its coordinates.  (On caches with x30 outlier
-// channels the 2-norm of the output's error falls from 2.3e-3 to 7e-4 of the output's; fp8
-// keys: 6e-4.)
+// Scores, maxima, sums and accumulators are float32.  What the tensor cores multiply is fp16, and each
+// rounding to it (2^-11 of a number at most, 2e-4 in the mean) is weighed against the output's own
+// (2.1e-4 of it, 2-norm):
+//   queries   two fp16 numbers, the nearest one and the rest (2^-22): one alone would add 2.5e-4 on
+//             fp16 keys and up to 6.5e-4 on codes with x30 outlier channels
+//   weights   one fp16 number (of codebooks the weight times the value's norm), 1e-4 over a long context;
+//             where a few tokens have most of the weight the sum is taken of the rounded numbers (not of
+//             codebooks, where that costs a tenth of the time and gains nothing measurable)
+//   values    INT4 levels times their scale one number (1.9e-4); of codebooks the centroid alone (norms in
+//             the values, rounded once more, would be 2.9e-4)
+//   centroids one number, scaled so that their roundings matter least (scale_table, 1.5e-4); a key's norm
+//             multiplies its scores in float32.
+// Together 2.3e-4 to 3.3e-4 of the output on caches with outlier channels.  (With queries, and values times
+// norms, as single numbers, it was 5e-4 to 9e-4, with twice the rows in a block and 150 instead of
+// 202 us for the largest case below; the others took 0 to 10% less.)
 //
 // Every wait has a limit: a block whose wait runs out sets KVQ_DEVERR_COPY_TIMEOUT and ends.
 #include <atomic>
@@ -49,8 +52,8 @@ namespace {
 
 constexpr int kDim = 128;
 constexpr int kThreads = 640;
-// registers per thread after the split: launched with 96 x 640 = 61440 = 256 x 136 + 256 x 80 + 128 x 48
-constexpr int kSoftmaxRegs = 136, kDecodeRegs = 80, kIssueRegs = 48;
+// registers per thread after the split: launched with 96 x 640 = 61440 = 256 x 128 + 256 x 80 + 128 x 64
+constexpr int kSoftmaxRegs = 128, kDecodeRegs = 80, kIssueRegs = 64;
 constexpr int kTileBytes = kTileTokens * kDim * 2;  // 32 KB: two halves of 128 rows x 128 bytes
 constexpr int kHalfBytes = kTileBytes / 2;
 constexpr int kStages = 2;
@@ -60,7 +63,7 @@ constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kStages * kTile
 constexpr int kOffLut = kOffV + kStages * kTileBytes, kLutBytes = 24 << 10;
 constexpr int kAhead = 4;
 constexpr int kOffRow = kOffLut + kLutBytes, kRowBytes = kTileTokens * 4;                       // a tile
-// (keys: a float32 norm a token; values: a norm, or four scales, in 8 bytes)
+// (keys: a float32 norm a token; values: the same, or four fp16 scales, in 8 bytes)
 constexpr int kOffKAux = kOffRow + kAhead * kRowBytes, kOffVAux = kOffKAux + kAhead * kTileTokens * 4;
 constexpr int kOffCtl = kOffVAux + kAhead * kTileTokens * 8;
 constexpr int kSmem = kOffCtl + 512 + 1024;  // 1024: the base is aligned by hand
@@ -94,7 +97,10 @@ struct Ctl {
   int bad_page;        // a token of the item lies in a page outside the pool
   float best[2][4];    // per side and warp: a table scale's error, and
   int best_at[2][4];   // which it is
+  float best_slope[2][4];  // and the slope of its roundings
   float unscale[2];    // what a side's table values are to be multiplied by
+  float norm_unit;     // what the values' norms are divided by: a power of two
+  float norm_top[kAhead];  // of a tile, above all of its values' norms (so divided): a power of two
 };
 static_assert(sizeof(Ctl) <= 512, "control block");
 
@@ -216,6 +222,7 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ float2 unpack_half2(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -243,8 +250,7 @@ struct Source {
   const uint8_t* rows;
   int row_bytes;
   uint32_t raw;               // shared addresses: the threads' slots;
-  uint32_t rowbuf, auxbuf;    // kAhead tiles of rows; of the values' norms or scales
-  bool keys;
+  uint32_t rowbuf, auxbuf;    // kAhead tiles of rows; of the values' scales
   uint32_t lut, lut_stride;   // the lane's copy of entry 0, bytes between entries (codebooks)
 };
 // What the look-ups read.
@@ -321,13 +327,24 @@ __device__ __forceinline__ void first_pages(const Pages& s, int tile0, int n, in
   for (int j = 0; j < 4; ++j)
     page[j] = first < n ? page_of(s, (tile0 + first) * kTileTokens + (threadIdx.x & 31) + 32 * j) : -1;
 }
+// The power of two above the finite norms of a tile's values, from the largest of each lane's four as
+// fp16 bits (2^-13 where all are zero).  Norms are divided by that of the item's first tile, so that a weight
+// times a norm is an fp16 number like a weight.
+__device__ __forceinline__ float power_above(uint32_t most) {
+  return __uint_as_float(((__reduce_max_sync(0xFFFFFFFFu, max(most, 0x0400u)) >> 10) + 113u) << 23);
+}
+__device__ __forceinline__ uint32_t finite_bits(uint32_t norm) {
+  norm &= 0x7FFFu;
+  return norm < 0x7C00u ? norm : 0u;
+}
+
 __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __half* k_norm, const __half* v_norm,
-                                        const __half* v_scale, volatile float* unscale, volatile int* bad_page,
-                                        uint32_t smem, uint32_t bars, int tile0, int n, int first,
-                                        volatile int* abort, int* err) {
+                                        const __half* v_scale, Ctl* ctl, uint32_t smem, uint32_t bars, int tile0, int n,
+                                        int first, volatile int* abort, int* err) {
   const int lane = threadIdx.x & 31;
   int bits = 0;
-  const float key_unit = k_norm ? unscale[0] : 0.f;  // of the keys' table
+  const float key_unit = k_norm ? *reinterpret_cast<volatile float*>(&ctl->unscale[0]) : 0.f;  // of the keys' table
+  float value_unit = 0.f;  // 1 / the norms' power, once it is known
 #pragma unroll 1
   for (int i = first; i < n; i += kLookUps) {
     const int at = i % kAhead;
@@ -339,7 +356,7 @@ __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __
       row[j] = row_of(s, t0 + 32 * j, page[j], &bits);
       sts32(smem + kOffRow + at * kRowBytes + 4 * (lane + 32 * j), row[j]);
     }
-    if (bits & KVQ_DEVERR_PAGE_INDEX) *bad_page = 1;
+    if (bits & KVQ_DEVERR_PAGE_INDEX) *reinterpret_cast<volatile int*>(&ctl->bad_page) = 1;
     bar_arrive(bars + 8 * (B_ROWS + at));
     uint2 aux[4];
 #pragma unroll
@@ -361,17 +378,41 @@ __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __
 #pragma unroll
       for (int j = 0; j < 4; ++j) page[j] = page_of(s, t0 + kLookUps * kTileTokens + 32 * j);
     }
+    if (k_norm) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) most = max(most, finite_bits(aux[j].y));  // (0 where the token is not there)
+      const float top = power_above(most);
+      if (i == first) {
+        float power = top;  // of the item's first tile, which another warp may look after
+        if (first) {
+          most = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            int ignored = 0;
+            const int t = tile0 * kTileTokens + lane + 32 * j;
+            const uint32_t head = row_of(s, t, page_of(s, t), &ignored);
+            if (head != kNoRow) most = max(most, finite_bits(__half_as_ushort(__ldg(v_norm + head))));
+          }
+          power = power_above(most);
+        }
+        value_unit = 1.0f / power;
+        if (!first && lane == 0) *reinterpret_cast<volatile float*>(&ctl->norm_unit) = power;
+      }
+      if (lane == 0) *reinterpret_cast<volatile float*>(&ctl->norm_top[at]) = top * value_unit;
+    }
     const uint32_t ka = smem + kOffKAux + at * kTileTokens * 4 + 4 * lane;
-    const uint32_t va = smem + kOffVAux + at * kTileTokens * 8 + 8 * lane;
+    const uint32_t va = smem + kOffVAux + at * kTileTokens * 8;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (k_norm) {
-        // (1 for a token that is not there: past the end its score, -inf, stays that)
-        const float norm = __half2float(__ushort_as_half((uint16_t)aux[j].x)) * key_unit;
-        sts32(ka + 128 * j, __float_as_uint(row[j] != kNoRow ? norm : 1.0f));
-        sts32(va + 256 * j, aux[j].y);
+        // (1 for a token that is not there: past the end its score, -inf, stays that, and its weight 0)
+        const float kn = __half2float(__ushort_as_half((uint16_t)aux[j].x)) * key_unit;
+        const float vn = __half2float(__ushort_as_half((uint16_t)aux[j].y)) * value_unit;
+        sts32(ka + 128 * j, __float_as_uint(row[j] != kNoRow ? kn : 1.0f));
+        sts32(va + 4 * lane + 128 * j, __float_as_uint(row[j] != kNoRow ? vn : 1.0f));
       } else if (v_scale) {
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(va + 256 * j), "r"(aux[j].x), "r"(aux[j].y) : "memory");
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(va + 8 * lane + 256 * j), "r"(aux[j].x), "r"(aux[j].y) : "memory");
       }
     }
     bar_arrive(bars + 8 * (B_AUX + at));
@@ -440,7 +481,6 @@ __device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, int 
       c[2] = w[1];
       c[3] = w[1] >> 16;
     }
-    const uint32_t scale = half_scale * 0x10001u;
     if constexpr (F == D_I4) {
       // Levels n - 8 of nibbles (k, k + 4), exact in fp16: 1024 + n less 1032, or (from the
       // upper nibble of a byte) (1024 + 16 n) / 16 less 72; times the scale, rounded once.  The
@@ -449,17 +489,18 @@ __device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, int 
       const __half2 a = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));  // 1032
       const __half2 b = __halves2half2(__ushort_as_half(0x2C00), __ushort_as_half(0x2C00));  // 1 / 16
       const __half2 d = __halves2half2(__ushort_as_half(0xD480), __ushort_as_half(0xD480));  // -72
+      const uint32_t scale = half_scale * 0x10001u;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t v = i & 1 ? c[i / 2] >> 8 : c[i / 2];
         const uint32_t lo = (v & 0x000F000Fu) | 0x64006400u, hi = (v & 0x00F000F0u) | 0x64006400u;
         const __half2 nl = __hsub2(*reinterpret_cast<const __half2*>(&lo), a);
         const __half2 nh = __hfma2(*reinterpret_cast<const __half2*>(&hi), b, d);
-        h[2 * i] = *reinterpret_cast<const uint32_t*>(&nl);
-        h[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&nh);
+        h[2 * i] = hmul2(*reinterpret_cast<const uint32_t*>(&nl), scale);
+        h[2 * i + 1] = hmul2(*reinterpret_cast<const uint32_t*>(&nh), scale);
       }
     } else {
-      // pairs of codes through the block's table of centroid pairs / sqrt(D)
+      // pairs of codes through the block's table of scaled centroid pairs
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const uint32_t e = (c[i / 4] >> (2 * B * (i % 4))) & ((1u << (2 * B)) - 1u);
@@ -469,42 +510,70 @@ __device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, int 
     const uint32_t at = row + (u >> 1) * kHalfBytes;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      sts16(at + (((4 * (u & 1) + i) ^ x) << 4), hmul2(h[4 * i], scale), hmul2(h[4 * i + 1], scale),
-            hmul2(h[4 * i + 2], scale), hmul2(h[4 * i + 3], scale));
+      sts16(at + (((4 * (u & 1) + i) ^ x) << 4), h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
   }
 }
 
-// The scale of a codebook's table, out of 128 steps of 2^(1 / 128) that bring its largest magnitude
-// to 2^-3 .. 2^-1: the one whose fp16 roundings are smallest, by the sum of squares of their
-// relative errors.  c: centroid `lane` in every lane (0 beyond the codebook); the side's four warps, a
-// candidate a thread.
+// The scale of a codebook's table, out of 512 steps of 2^(1 / 512) that bring its largest magnitude
+// to 2^-3 .. 2^-1: the one whose fp16 roundings r of the scaled centroids x are nearest, up to a common
+// factor: least sum w (a r - x)^2 / scale^2 with a = 1 - slope, slope = sum w r (r - x) / sum w r^2.  (In those
+// terms nothing cancels: the sum is sum w (r - x)^2 - slope sum w r (r - x).)  What a rounding does to a key
+// adds up where its coordinates have one magnitude, and those of a key with an outlier channel all are
+// near their root mean square.  So the centroids there weigh most: w = exp(-3.125 (|c| / c1 - 1)^2), c1 = the
+// largest over 1.51, 2.15 or 2.73, what 2, 3 or 4 bits of N(0, 1) reach to.  (4-bit keys with x30 outlier
+// channels: 1.5e-4 of the output instead of 2.9e-4 with equal weights and 128 steps.)  c: centroid `lane` in every
+// lane (0 beyond the codebook); the side's four warps, four candidates a thread.
 __device__ __forceinline__ float scale_table(Ctl* ctl, float c, int bits, int side, int tid) {
+  constexpr int kEach = 4, kSteps = 128 * kEach;
   const int lane = tid & 31, warp = tid >> 5;
-  const float over = c != 0.f ? __fdividef(1.0f, c) : 0.f;
   const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(c)));
+  const float over = (bits == 4 ? 2.73f : (bits == 3 ? 2.15f : 1.51f)) / __uint_as_float(max(most, 0x00800000u));
+  const float away = fabsf(c) * over - 1.0f;
+  const float weight = lane < (1 << bits) ? exp2f(-4.508f * away * away) : 0.f;  // 3.125 log2 e
   // 2^-3 over the largest magnitude's power of two
   const float unit = __uint_as_float((251u - min(max(most >> 23, 2u), 249u)) << 23);
-  const float step = exp2f((float)tid * (1.0f / 128.0f)), mine = step * unit;
-  float least = 0.f;
-  int at = tid;
-#pragma unroll 4
-  for (int i = 0; i < (1 << bits); ++i) {
-    const float x = __shfl_sync(0xFFFFFFFFu, c, i) * mine;
-    const float off = (__half2float(__float2half_rn(x)) - x) * __shfl_sync(0xFFFFFFFFu, over, i);
-    least = fmaf(off, off, least);
+  float mine[kEach], dd[kEach], rd[kEach], rr[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    mine[k] = exp2f((float)(k * 128 + tid) * (1.0f / kSteps));
+    dd[k] = rd[k] = rr[k] = 0.f;
   }
-  least = __fdividef(least, step * step);
+#pragma unroll 2
+  for (int i = 0; i < (1 << bits); ++i) {
+    const float ci = __shfl_sync(0xFFFFFFFFu, c, i) * unit, w = __shfl_sync(0xFFFFFFFFu, weight, i);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const float x = ci * mine[k], r = __half2float(__float2half_rn(x)), d = r - x, wd = w * d;
+      dd[k] = fmaf(wd, d, dd[k]);
+      rd[k] = fmaf(wd, r, rd[k]);
+      rr[k] = fmaf(w * r, r, rr[k]);
+    }
+  }
+  float least = INFINITY, slope = 0.f;
+  int at = tid;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const float a = rr[k] > 0.f ? __fdividef(rd[k], rr[k]) : 0.f;
+    const float e = __fdividef(fmaf(-a, rd[k], dd[k]), mine[k] * mine[k]);
+    if (e < least) {
+      least = e;
+      slope = a;
+      at = k * 128 + tid;
+    }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const float other = __shfl_xor_sync(0xFFFFFFFFu, least, o);
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, least, o), its = __shfl_xor_sync(0xFFFFFFFFu, slope, o);
     const int k = __shfl_xor_sync(0xFFFFFFFFu, at, o);
     if (other < least || (other == least && k < at)) {
       least = other;
+      slope = its;
       at = k;
     }
   }
   if (lane == 0) {
     ctl->best[side][warp] = least;
+    ctl->best_slope[side][warp] = slope;
     ctl->best_at[side][warp] = at;
   }
   if (side == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -514,11 +583,12 @@ __device__ __forceinline__ float scale_table(Ctl* ctl, float c, int bits, int si
     const int k = ctl->best_at[side][i];
     if (other < least || (other == least && k < at)) {
       least = other;
+      slope = ctl->best_slope[side][i];
       at = k;
     }
   }
-  const float beta = exp2f((float)at * (1.0f / 128.0f)) * unit;
-  if (tid == 0) ctl->unscale[side] = inv_sqrt_dim(kDim) / beta;
+  const float beta = exp2f((float)at * (1.0f / kSteps)) * unit;
+  if (tid == 0) ctl->unscale[side] = inv_sqrt_dim(kDim) * (1.0f - slope) / beta;
   return beta;
 }
 
@@ -535,25 +605,23 @@ __device__ __forceinline__ void build_lut(uint32_t lut, int copies, float c, int
   }
 }
 
-// Where the two tables lie, and the slots.  24 KB are set aside: fp8 keys and INT4 values use
-// them for slots alone (16 and 8 KB).  With up to 128 rows the second query tile is free as
-// well: the tables go there (one of 32 copies where keys and values have the same, else 16
-// copies each), and the slots, four passes a side, have the 24 KB.  With more rows both share
-// them: 16 KB of tables (16 copies of one, or 8 of each), 4 KB of slots a side.
+// Where the two tables lie, and the slots, in 24 KB: fp8 keys and INT4 values use them for slots
+// alone (16 and 8 KB); codebooks have 16 KB of tables (16 copies of one where keys and values have
+// the same, else 8 of each) and 4 KB of slots a side.
 struct Tables {
   uint32_t at[2], raw[2];
   int copies[2];
 };
-__device__ __forceinline__ Tables place_tables(uint32_t smem, int k_bits, int v_bits, bool same, bool both) {
-  const uint32_t lut = smem + kOffLut, spare = smem + kOffQ + kTileBytes;
+__device__ __forceinline__ Tables place_tables(uint32_t smem, int k_bits, int v_bits, bool same) {
+  const uint32_t lut = smem + kOffLut;
   Tables t;
-  const int of_1kb = (both ? 16 : 8) << (same ? 1 : 0);
+  const int of_1kb = same ? 16 : 8;
   t.copies[0] = k_bits == 4 ? of_1kb : 32;  // (smaller tables: 8 KB at most)
   t.copies[1] = v_bits == 4 ? of_1kb : 32;
-  t.at[0] = both ? spare : lut;
-  t.at[1] = t.at[0] + (same ? 0 : (both ? 16 << 10 : 8 << 10));
-  t.raw[0] = both ? lut : lut + (16 << 10);
-  t.raw[1] = t.raw[0] + (both ? 8 << 10 : 4 << 10);
+  t.at[0] = lut;
+  t.at[1] = t.at[0] + (same ? 0 : 8 << 10);
+  t.raw[0] = lut + (16 << 10);
+  t.raw[1] = t.raw[0] + (4 << 10);
   return t;
 }
 
@@ -584,7 +652,7 @@ __device__ __forceinline__ void produce(const Source& s, const Ring& ring, int n
     const int st = i & 1, at = i % kAhead, after = (i + 1) % kAhead;
     const bool more = i + 1 < n;
     if (more && !bar_wait(ring.rows + 8 * after, ((i + 1) / kAhead) & 1, abort, err)) break;
-    if (F >= D_I4 && !s.keys && !bar_wait(ring.aux + 8 * at, (i / kAhead) & 1, abort, err)) break;
+    if (F == D_I4 && !bar_wait(ring.aux + 8 * at, (i / kAhead) & 1, abort, err)) break;
     if (i >= kStages && !bar_wait(ring.empty + 8 * st, ((i >> 1) & 1) ^ 1, abort, err)) break;
     if (i == 1 && ring.first_use && !bar_wait(ring.first_use, 0, abort, err)) break;
     const uint32_t tile = ring.tiles + st * kTileBytes, aux = s.auxbuf + (uint32_t)(at * kTileTokens * 8);
@@ -603,11 +671,11 @@ __device__ __forceinline__ void produce(const Source& s, const Ring& ring, int n
         take<F>(slot + j * kSlotStep, w[j]);
         place<F>(q + j, tid, t, u);
         row[j] = lds32(rows + 4u * t);
-        if constexpr (F >= D_I4) {
+        if constexpr (F == D_I4) {
           uint16_t v;
           place<F>(p, tid, t, u);
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(aux + 8u * t + (F == D_I4 ? 2u * u : 0u)));
-          scale = s.keys ? 0x3C00u : v;  // (a key's norm multiplies its scores: here 1)
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(aux + 8u * t + 2u * u));
+          scale = v;
         }
       }
 #pragma unroll
@@ -663,18 +731,13 @@ __device__ __forceinline__ void produce<D_F16, 1>(const Source& s, const Ring& r
   }
 }
 
-// deep: there is room for a whole tile's units of a codebook side
 template <bool CODES>
-__device__ __forceinline__ void produce_any(int f, bool deep, const Source& s, const Ring& ring, int n, int tid,
-                                            volatile int* abort, int* err) {
+__device__ __forceinline__ void produce_any(int f, const Source& s, const Ring& ring, int n, int tid, volatile int* abort,
+                                            int* err) {
   if constexpr (!CODES) {
     if (f == D_F16) produce<D_F16, 1>(s, ring, n, tid, abort, err);
     else if (f == D_F8) produce<D_F8, 8>(s, ring, n, tid, abort, err);
     else produce<D_I4, 4>(s, ring, n, tid, abort, err);
-  } else if (deep) {
-    if (f == D_CB4) produce<D_CB4, 4>(s, ring, n, tid, abort, err);
-    else if (f == D_CB3) produce<D_CB3, 4>(s, ring, n, tid, abort, err);
-    else produce<D_CB2, 4>(s, ring, n, tid, abort, err);
   } else {
     if (f == D_CB4) produce<D_CB4, 2>(s, ring, n, tid, abort, err);
     else if (f == D_CB3) produce<D_CB3, 2>(s, ring, n, tid, abort, err);
@@ -717,7 +780,7 @@ __device__ __forceinline__ void rescale(uint32_t o_at, bool acc, uint32_t p_at, 
     tc_wait_ld(v);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
+      const float2 x = unpack_half2(v[e]);
       v[e] = half2_bits(x.x * f, x.y * f);
     }
     tc_st16(p_at + c, v);
@@ -734,6 +797,11 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
   unsigned long long r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -748,11 +816,11 @@ __device__ __forceinline__ float2 unpack2(unsigned long long r) {
 // ------------------------------------------------------------------------ the kernel
 // CODES: tiers of codebook formats, else of the others (a branch on the format in the softmax loop
 // made it a third slower for both).
-// Measured (GB300): 256 sequences x 64 / 8 heads on 16384 tokens of fp8 keys and INT4 values, 143 us:
-// 960 TFLOP/s, half of the measured bf16 rate, 1.7 us a tile of 256 rows where the products alone
-// take 1.64 (both operands of S from shared memory), on 128 of 152 SMs.  8 sequences x 32 heads on
-// 8192 tokens of 4-bit codes, 39 us: 1.3 us a tile, of which shared memory is busy 1.1 (table look-ups,
-// tiles written and read), and about 10 us of set-up, first tile and drain.
+// Measured (GB300): 256 sequences x 64 / 8 heads on 16384 tokens of fp8 keys and INT4 values, 202 us,
+// 1.5 us a tile of 128 rows on 128 of 152 SMs: the softmax warps' arithmetic (the sum of rounded
+// weights is 12 us of it; without the queries' second part it takes the same time).  8 sequences x
+// 32 heads on 8192 tokens of 4-bit codes, 47 us: 1.4 us a tile, of which shared memory is busy most
+// (table look-ups, tiles written and read), and about 10 us of set-up, first tile and drain.
 template <bool CODES>
 __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid_constant__ SharedParams p) {
   // the pass over the sequences' own tiers may start on SMs that this grid leaves idle
@@ -778,8 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     else hi = mid;
   }
   const int g = lo, lb = blk - p.block[g];
-  const int rows = (p.offset[g + 1] - p.offset[g]) * p.group - lb * kItemRows;  // > 0
-  const bool both = rows <= kTileRows;  // both softmax groups on the same rows
+  const int rows = min((p.offset[g + 1] - p.offset[g]) * p.group - lb * kTileRows, kTileRows);  // > 0
   int ti = 0;
   while (ti + 1 < p.num_tiers && split >= p.tier[ti + 1].first) ++ti;
   const SharedTier& T = p.tier[ti];
@@ -791,25 +858,23 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   const int per = (all + T.num_splits - 1) / T.num_splits;
   const int tile0 = min(split * per, all), tile1 = min(tile0 + per, all);
   const int n = tile1 - tile0;
-  const int jobs = both ? n : 2 * n;  // job i: softmax group i & 1, tile both ? i : i / 2
-
-  // row of this softmax thread, as an output row (sequence, query head), or -1
   const int w = warp >> 2;  // softmax group of the first eight warps
-  const int r = (both ? 0 : w * kTileRows) + (threadIdx.x & 127);
-  long long out_row = -1;
-  if (warp < 8 && r < rows) {
-    const int gr = lb * kItemRows + r, i = gr / p.group;
-    out_row = (long long)(p.offset[g] + i) * p.hq + hk * p.group + (gr - i * p.group);
-  }
-  const size_t out_rows = (size_t)p.batch * p.hq;
-  const size_t part = (2 * (size_t)(T.split_begin + split) + (both ? w : 0)) * out_rows;
+  const int r = threadIdx.x & 127;
+  // Row of this softmax thread, as an output row (sequence, query head), or -1; and where the group's
+  // partials lie (tiles w, w + 2, ...).  Worked out where they are used: registers are short in between.
+  auto output_row = [&]() -> long long {
+    if (warp >= 8 || r >= rows) return -1;
+    const int gr = lb * kTileRows + r, i = gr / p.group;
+    return (long long)(p.offset[g] + i) * p.hq + hk * p.group + (gr - i * p.group);
+  };
+  auto partials = [&]() -> size_t { return (2 * (size_t)(T.split_begin + split) + w) * ((size_t)p.batch * p.hq); };
 
   if (n == 0) {  // no tokens: partials of weight zero
-    if (out_row >= 0) *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) = make_float2(-INFINITY, 0.f);
+    const long long out_row = output_row();
+    if (out_row >= 0) *reinterpret_cast<float2*>(p.ml + 2 * (partials() + out_row)) = make_float2(-INFINITY, 0.f);
     return;
   }
 
-  const int rows_of_group = both ? min(rows, kTileRows) : min(rows - w * kTileRows, kTileRows);  // w of a softmax warp
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       bar_init(bars + 8 * (B_KFULL + i), 128);
@@ -818,18 +883,17 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       bar_init(bars + 8 * (B_VEMPTY + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      const int live = both ? rows : min(max(rows - i * kTileRows, 0), kTileRows);
-      bar_init(bars + 8 * (B_QFULL + i), 128);
       bar_init(bars + 8 * (B_SFULL + i), 1);
-      bar_init(bars + 8 * (B_PREADY + i), max(1, (live + 31) / 32 * 32));  // the warps that hold rows
+      bar_init(bars + 8 * (B_PREADY + i), (rows + 31) / 32 * 32);  // the warps that hold rows
       bar_init(bars + 8 * (B_OFULL + i), 1);
     }
+    bar_init(bars + 8 * B_QFULL, 128);
     bar_init(bars + 8 * B_QROT, 1);
     for (int i = 0; i < kAhead; ++i) {
       bar_init(bars + 8 * (B_ROWS + i), 32);
       bar_init(bars + 8 * (B_AUX + i), 32);
       // the decoding threads, and (norms of keys) the softmax warps that read the tile's scores
-      bar_init(bars + 8 * (B_ROWS_READ + i), 256 + (CODES ? (min(rows, kItemRows) + 31) / 32 : 0));
+      bar_init(bars + 8 * (B_ROWS_READ + i), 256 + (CODES ? (rows + 31) / 32 : 0));
     }
     ctl->abort = 0;
     ctl->bad_page = 0;
@@ -852,19 +916,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     // are laid out.  (Butterflies by shuffles took 15 us for 256 rows.)
     const int tid = threadIdx.x & 255;
     const int shift = __ffs(p.group) - 1;
-    for (int first = 0; first < (both ? kTileRows : kItemRows); first += 128) {
+    {
       uint4 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int row = first + i * 16 + (tid >> 4);
+        const int row = i * 16 + (tid >> 4);
         v[i] = make_uint4(0, 0, 0, 0);
         if (row < rows) {
-          const int gr = lb * kItemRows + row, sq = gr >> shift;
+          const int gr = lb * kTileRows + row, sq = gr >> shift;
           const size_t orow = (size_t)(p.offset[g] + sq) * p.hq + hk * p.group + (gr - (sq << shift));
           v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + orow * kDim) + (tid & 15));
         }
       }
-      const uint32_t to = smem + kOffQ + (first >> 7) * kTileBytes + ((tid & 15) >> 3) * kHalfBytes;
+      const uint32_t to = smem + kOffQ + ((tid & 15) >> 3) * kHalfBytes;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = i * 16 + (tid >> 4);
@@ -896,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       const float kc = lane < (1 << T.k_bits) ? __ldg(T.k_cent + lane) : 0.f;
       const float vc = lane < (1 << T.v_bits) ? __ldg(T.v_cent + lane) : 0.f;
       const bool same = T.k_bits == T.v_bits && __all_sync(0xFFFFFFFFu, kc == vc);  // one table (often so)
-      tables = place_tables(smem, T.k_bits, T.v_bits, same, both);
+      tables = place_tables(smem, T.k_bits, T.v_bits, same);
       const int bits = keys ? T.k_bits : T.v_bits;
       const float beta = scale_table(ctl, keys ? kc : vc, bits, side, tid);
       if (keys || !same) build_lut(tables.at[side], tables.copies[side], (keys ? kc : vc) * beta, bits, tid);
@@ -916,14 +980,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     // ---- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // The rotated queries, from TMEM: times log2(e) / D (1 / sqrt(D) of the rotation and of the
-    // scores, which are then in base-2 units), rounded to fp16 into the query tiles.
+    // scores, which are then in base-2 units), as two fp16 numbers into the query tiles.
     bool ok = true;
-    if (!(both && w)) {
+    if (w == 0) {
       ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * B_QROT, 0, abort, p.err));
       tc_fence_after();
-      const int r = threadIdx.x & 127;
-      const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + w * 128;
-      const uint32_t to = smem + kOffQ + w * kTileBytes + r * 128;
+      const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t to = smem + kOffQ + r * 128, rest = kTileBytes;
       constexpr float scale = 1.4426950408889634f / kDim;
 #pragma unroll
       for (int part = 0; part < 4; ++part) {
@@ -932,38 +995,47 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         tc_wait_ld(v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t h[4];
+          uint32_t h[4], l[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            h[k] = half2_bits(__uint_as_float(v[8 * i + 2 * k]) * scale, __uint_as_float(v[8 * i + 2 * k + 1]) * scale);
+          for (int k = 0; k < 4; ++k) {
+            const float a = __uint_as_float(v[8 * i + 2 * k]) * scale, b = __uint_as_float(v[8 * i + 2 * k + 1]) * scale;
+            h[k] = half2_bits(a, b);
+            const float2 near = unpack_half2(h[k]);
+            l[k] = half2_bits(a - near.x, b - near.y);
+          }
           const int at = 4 * part + i;
-          sts16(to + (at >> 3) * kHalfBytes + (((at & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+          const uint32_t chunk = to + (at >> 3) * kHalfBytes + (((at & 7) ^ (r & 7)) << 4);
+          sts16(chunk, h[0], h[1], h[2], h[3]);
+          sts16(chunk + rest, l[0], l[1], l[2], l[3]);
         }
       }
       tc_fence_before();
       fence_async_smem();
-      bar_arrive(bars + 8 * (B_QFULL + w));
+      bar_arrive(bars + 8 * B_QFULL);
     }
-    const int my_jobs = jobs > w ? (jobs - w + 1) / 2 : 0;
-    const bool live = (warp & 3) * 32 < rows_of_group;  // the warp holds rows
-    if (live && my_jobs > 0) {
+    const int my_tiles = n > w ? (n - w + 1) / 2 : 0;
+    const bool live = (warp & 3) * 32 < rows;  // the warp holds rows
+    if (live && my_tiles > 0) {
       const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t s_at = lane_base + w * 128, o_at = lane_base + 256 + w * 128;
       float m = -INFINITY;
       unsigned long long l2 = 0;  // the row's sum, even and odd columns
-      for (int k = 0; k < my_jobs && ok; ++k) {
-        const int i = 2 * k + w, tile = tile0 + (both ? i : i >> 1);
-        const int valid = min(kTileTokens, len - tile * kTileTokens);
-        const int local = both ? i : i >> 1, at = local % kAhead;
-        const float* norm = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(ctl) - kOffCtl + kOffKAux) + at * kTileTokens;
+      for (int k = 0; k < my_tiles && ok; ++k) {
+        const int i = 2 * k + w, at = i % kAhead;
+        const int valid = min(kTileTokens, len - (tile0 + i) * kTileTokens);
+        const uint8_t* base = reinterpret_cast<const uint8_t*>(ctl) - kOffCtl;
+        const float* norm = reinterpret_cast<const float*>(base + kOffKAux) + at * kTileTokens;
+        const float* v_norm = reinterpret_cast<const float*>(base + kOffVAux) + at * kTileTokens * 2;
         ok = bar_wait(bars + 8 * (B_SFULL + w), k & 1, abort, p.err);
-        if (CODES) ok = ok && bar_wait(bars + 8 * (B_AUX + at), (local / kAhead) & 1, abort, p.err);
+        if (CODES) ok = ok && bar_wait(bars + 8 * (B_AUX + at), (i / kAhead) & 1, abort, p.err);
         if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
         tc_fence_after();
         // Half a tile's weights at a time, against m as it is, in registers: no maximum is taken.
         // All weights are positive, so a sum of at most kMostWeight says that none is too large for
         // fp16 either; only where it is exceeded (always at first, where m is -inf) m is raised
-        // and the half, still in TMEM, weighed again.
+        // and the half, still in TMEM, weighed again.  Of codebooks P holds weights times values'
+        // norms: both steps allow for the tile's largest.
+        const float top = CODES ? *reinterpret_cast<volatile float*>(&ctl->norm_top[at]) : 1.f;
 #pragma unroll 1
         for (int c0 = 0; c0 < kTileTokens; c0 += 64) {
           uint32_t h[32];
@@ -991,11 +1063,22 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
                   t1 = add2(t1, neg);
                 }
                 const float2 x = unpack2(t0), y = unpack2(t1);
-                const float a = ex2(x.x), b = ex2(x.y), d = ex2(y.x), f = ex2(y.y);
-                s0 = add2(s0, pack2(a, b));
-                s1 = add2(s1, pack2(d, f));
-                h[(c + e) / 2] = half2_bits(a, b);
-                h[(c + e) / 2 + 1] = half2_bits(d, f);
+                unsigned long long a = pack2(ex2(x.x), ex2(x.y)), b = pack2(ex2(y.x), ex2(y.y));
+                if constexpr (CODES) {
+                  s0 = add2(s0, a);
+                  s1 = add2(s1, b);
+                  const float4 n = *reinterpret_cast<const float4*>(v_norm + c0 + c + e);
+                  a = mul2(a, pack2(n.x, n.y));
+                  b = mul2(b, pack2(n.z, n.w));
+                }
+                const float2 u = unpack2(a), w = unpack2(b);
+                h[(c + e) / 2] = half2_bits(u.x, u.y);
+                h[(c + e) / 2 + 1] = half2_bits(w.x, w.y);
+                if constexpr (!CODES) {  // the sum of what is multiplied: a token that outweighs all others keeps its value
+                  const float2 ru = unpack_half2(h[(c + e) / 2]), rw = unpack_half2(h[(c + e) / 2 + 1]);
+                  s0 = add2(s0, pack2(ru.x, ru.y));
+                  s1 = add2(s1, pack2(rw.x, rw.y));
+                }
               }
             };
             uint32_t va[32], vb[32];
@@ -1007,7 +1090,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
             weigh(32, vb);
             sum = add2(s0, s1);
             const float2 t = unpack2(sum);
-            if (again || __all_sync(0xFFFFFFFFu, t.x + t.y <= kMostWeight)) break;
+            if (again || __all_sync(0xFFFFFFFFu, (t.x + t.y) * top <= kMostWeight)) break;
+            const float head = kHeadroom - (float)((int)(__float_as_uint(top) >> 23) - 127);
             float mx = m;
 #pragma unroll 1
             for (int c = c0; c < c0 + 64; c += 16) {
@@ -1017,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 if (c + e < valid)
-                  mx = fmaxf(mx, __uint_as_float(x[e]) * (CODES ? norm[c + e] : 1.f) - kHeadroom);
+                  mx = fmaxf(mx, __uint_as_float(x[e]) * (CODES ? norm[c + e] : 1.f) - head);
             }
             const float f = ex2(m - mx);
             m = mx;
@@ -1043,16 +1127,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         tc_fence_before();
         bar_arrive(bars + 8 * (B_PREADY + w));
       }
-      if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * (B_OFULL + w), (my_jobs - 1) & 1, abort, p.err));
+      if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * (B_OFULL + w), (my_tiles - 1) & 1, abort, p.err));
       tc_fence_after();
+      const long long out_row = output_row();
+      const size_t part = partials();
       // The accumulator leaves through shared memory, 16 KB a warp, so that rows are written
       // whole: the tiles are free (the group that ends first has the key stages, whose products
       // precede its last one, the other the value stages).
       if (ok) {
-        const bool last = ((jobs - 1) & 1) == w;
+        const bool last = ((n - 1) & 1) == w;
         const int lane = threadIdx.x & 31;
         const uint32_t stage = smem + (last ? kOffV : kOffK) + (warp & 3) * (32 * kDim * 4);
-        const float value_unit = CODES ? *reinterpret_cast<volatile float*>(&ctl->unscale[1]) : 1.f;
+        const float value_unit = CODES ? *reinterpret_cast<volatile float*>(&ctl->unscale[1]) *
+                                             *reinterpret_cast<volatile float*>(&ctl->norm_unit) : 1.f;
         const bool int4 = T.v_fmt == KVQ_FMT_INT4_G32;  // columns 0 4 1 5 2 6 3 7 of every eight
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -1095,8 +1182,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) =
             ok ? make_float2(l == l ? m : l, l) : make_float2(-INFINITY, 0.f);
       }
-    } else if (out_row >= 0) {  // a second group without a tile of its own
-      *reinterpret_cast<float2*>(p.ml + 2 * (part + out_row)) = make_float2(-INFINITY, 0.f);
+    } else if (const long long out_row = output_row(); out_row >= 0) {  // a second group without a tile of its own
+      *reinterpret_cast<float2*>(p.ml + 2 * (partials() + out_row)) = make_float2(-INFINITY, 0.f);
     }
   } else if (warp < 16) {
     // ---- decoding
@@ -1115,7 +1202,6 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     }
     s.rowbuf = smem + kOffRow;
     s.auxbuf = smem + kOffVAux;
-    s.keys = keys;
     Ring ring;
     ring.tiles = smem + (keys ? kOffK : kOffV);
     ring.full = bars + 8 * (keys ? B_KFULL : B_VFULL);
@@ -1124,7 +1210,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     ring.aux = bars + 8 * B_AUX;
     ring.rows_read = bars + 8 * B_ROWS_READ;
     ring.first_use = keys ? 0 : bars + 8 * B_QROT;  // the second value stage first holds the rotation
-    produce_any<CODES>(keys ? decode_kind(T.k_fmt, T.k_bits) : decode_kind(T.v_fmt, T.v_bits), both, s, ring, n,
+    produce_any<CODES>(keys ? decode_kind(T.k_fmt, T.k_bits) : decode_kind(T.v_fmt, T.v_bits), s, ring, n,
                 threadIdx.x & 127, abort, p.err);
   } else {
     // ---- products
@@ -1139,59 +1225,61 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
       auto well = [&](uint32_t bar, uint32_t parity) -> bool {
         return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, abort, p.err));
       };
-      auto scores = [&](int i) -> bool {  // S of job i
-        const int tile = both ? i : i >> 1, st = tile & 1, ws = i & 1;
-        if (!well(bars + 8 * (B_KFULL + st), (tile >> 1) & 1)) return false;
+      auto scores = [&](int i) -> bool {  // S of tile i, for softmax group i & 1
+        const int st = i & 1;
+        if (!well(bars + 8 * (B_KFULL + st), (i >> 1) & 1)) return false;
         tc_fence_after();
-        const uint64_t a = qd + (both ? 0 : ws) * (kTileBytes >> 4), b = kd + st * (kTileBytes >> 4);
+        const uint64_t b = kd + st * (kTileBytes >> 4);
         if (elect_one()) {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {  // the queries' first parts, then the second (unrolled, descriptors spill)
+            const uint64_t a = qd + half * (kTileBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kDim / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-            mma_ss(tm + ws * 128, a + off, b + off, kIdescQK, kk > 0);
+            for (int kk = 0; kk < kDim / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+              mma_ss(tm + st * 128, a + off, b + off, kIdescQK, half + kk > 0);
+            }
           }
-          tc_commit(bars + 8 * (B_SFULL + ws));
-          if (both || ws) tc_commit(bars + 8 * (B_KEMPTY + st));
+          tc_commit(bars + 8 * (B_SFULL + st));
+          tc_commit(bars + 8 * (B_KEMPTY + st));
         }
         __syncwarp();
         return true;
       };
-      bool ok = true;
       {  // the rotated queries, into the score columns
         const uint64_t rd = desc_at(desc_base(16, 1024), smem + kOffV + kTileBytes);
         if (elect_one()) {
-          for (int ws = 0; ws < (both ? 1 : 2); ++ws) {
 #pragma unroll
-            for (int kk = 0; kk < kDim / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-              mma_ss(tm + ws * 128, qd + ws * (kTileBytes >> 4) + off, rd + off, kIdescQK, kk > 0);
-            }
+          for (int kk = 0; kk < kDim / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+            mma_ss(tm, qd + off, rd + off, kIdescQK, kk > 0);
           }
           tc_commit(bars + 8 * B_QROT);
         }
         __syncwarp();
       }
-      for (int i = 0; i < 2 && i < jobs && ok; ++i) ok = well(bars + 8 * (B_QFULL + (both ? 0 : i)), 0) && scores(i);
-      for (int i = 0; i < jobs && ok; ++i) {
-        const int tile = both ? i : i >> 1, st = tile & 1, ws = i & 1;
-        ok = well(bars + 8 * (B_VFULL + st), (tile >> 1) & 1) && well(bars + 8 * (B_PREADY + ws), (i >> 1) & 1);
+      bool ok = well(bars + 8 * B_QFULL, 0);
+      for (int i = 0; i < 2 && i < n && ok; ++i) ok = scores(i);
+      for (int i = 0; i < n && ok; ++i) {
+        const int st = i & 1;
+        ok = well(bars + 8 * (B_VFULL + st), (i >> 1) & 1) && well(bars + 8 * (B_PREADY + st), (i >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         const uint64_t b = vd + st * (kTileBytes >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kTileTokens / 16; ++kk)
-            mma_ts(tm + 256 + ws * 128, tm + ws * 128 + kk * 8, b + ((kk * 2048) >> 4), kIdescPV, i > 1 || kk > 0);
-          tc_commit(bars + 8 * (B_OFULL + ws));
-          if (both || ws) tc_commit(bars + 8 * (B_VEMPTY + st));
+            mma_ts(tm + 256 + st * 128, tm + st * 128 + kk * 8, b + ((kk * 2048) >> 4), kIdescPV, i > 1 || kk > 0);
+          tc_commit(bars + 8 * (B_OFULL + st));
+          tc_commit(bars + 8 * (B_VEMPTY + st));
         }
         __syncwarp();
-        if (i + 2 < jobs) ok = scores(i + 2);
+        if (i + 2 < n) ok = scores(i + 2);
       }
     } else if (warp < 17 + kLookUps) {
       // ---- look-ups
       look_up(pages, page, CODES ? T.k_aux : nullptr, CODES ? T.v_aux : nullptr, T.v_fmt == KVQ_FMT_INT4_G32 ? T.v_aux : nullptr,
-              ctl->unscale, &ctl->bad_page, smem, bars, tile0, n, warp - 17, abort, p.err);
+              ctl, smem, bars, tile0, n, warp - 17, abort, p.err);
     }
   }
   __syncwarp();

@@ -12,7 +12,7 @@ from oracle import attention as oatt
 from oracle import cache as ocache
 from oracle import shared as oshared
 from tests import gpu_util as gu
-from tests.test_gpu_shared import Case
+from tests.test_gpu_shared import SPECS, Case
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -11
@@ -341,3 +341,85 @@ def test_calls_on_many_streams_at_once():
     torch.cuda.synchronize()
     for i, (_, _, out, _, _) in enumerate(jobs):
         assert np.array_equal(out.cpu().numpy().astype(np.float64), want[i % 4]), i
+
+
+@pytest.mark.parametrize("name", ["fp16", "fp8_int4", "fp8_fp16", "cb4", "cb32", "cb23"])
+@pytest.mark.parametrize("batch,group", [(2, 1), (8, 4), (33, 4)])
+def test_error_beside_the_outputs_own_rounding(name, batch, group):
+    """Keys and values with x30 outlier channels, as a model's: scores of several nats, a few tokens with
+    most of the weight.  The output is rounded to fp16: 0.42 u of it (2-norm; u times the root mean square
+    of a rounding over a binade, 1 / sqrt(3) 0.72).  Beside it stand one rounding each of the weights and of
+    INT4 values (0.42 u) and of centroids (0.35 u of a key's score, which with several nats is as much of the
+    output): 0.84 u in squares.  At most u.  A query rounded to one fp16 number alone would add
+    0.5 to 1.3 u."""
+    torch, kvq = modules()
+    hkv, d, n = 8, 128, 2500
+    rng = np.random.default_rng([batch, len(name)])
+    ks, vs = (np.where(rng.integers(0, 2, (hkv, d)) == 0, 1, -1).astype(np.int8) for _ in range(2))
+    loud = lambda: np.where(rng.random((hkv, d)) < 0.015, 30.0, 1.0)  # noqa: E731
+    draw = lambda L, f: (rng.standard_normal((L, hkv, d)) * f).astype(np.float16)  # noqa: E731
+    fk, fv = loud(), loud()
+    kv = [[(draw(n, fk), draw(n, fv))] + [(draw(0, fk), draw(0, fv))] * (batch - 1),
+          [(draw(5, fk), draw(5, fv)) for _ in range(batch)]]
+    built = gu.build_exact(kvq, torch, [SPECS[name], SPECS[name]], kv, ks, vs, 16, shuffle_seed=batch)
+    first, second = (c.struct for c in built.gpu)
+    second.k_signs, second.v_signs = first.k_signs, first.v_signs
+    q = rng.standard_normal((batch, hkv * group, d)).astype(np.float16)
+    got = call(kvq, torch, built.views[:1], [0, batch], built.views[1:], q)
+    tiers = oshared.as_tiers(built.ora[:1], [0, batch], built.ora[1:], batch)
+    off = size = 0.0
+    for b in sorted({0, 1, batch // 2, batch - 1}):
+        for h in range(hkv):
+            keys, values = oatt.dequantised_kv(tiers, b, h)
+            s = q[b, h * group:(h + 1) * group].astype(np.float64) @ keys.T / math.sqrt(d)
+            w = np.exp(s - s.max(-1, keepdims=True))
+            want = (w / w.sum(-1, keepdims=True)) @ values
+            off += float(np.sum((got[b, h * group:(h + 1) * group] - want) ** 2))
+            size += float(np.sum(want ** 2))
+    assert math.sqrt(off / size) <= U, math.sqrt(off / size) / U
+
+
+@pytest.mark.parametrize("how", ["any", "small first", "large first", "none first", "sink"])
+@pytest.mark.parametrize("name", ["cb4", "cb32"])
+@pytest.mark.parametrize("batch,group", [(2, 2), (12, 8)])
+def test_values_of_any_norm(name, how, batch, group):
+    """The prefix pass multiplies weights by the values' norms, over that of the item's first tile: norms
+    from 2^-8 to 2^12 at random; a first tile 2^-14 or 2^14 times the others; a first tile of zeros; a
+    token of value zero that outweighs all others 2^30 times (what is left of the output is tiny, and
+    fp16's smallest step, 2^-25 of a weight of 2, of every token bounds it)."""
+    torch, kvq = modules()
+    hkv, d, n = 4, 128, 1500
+    rng = np.random.default_rng([batch, len(how), len(name)])
+    ks, vs = (np.where(rng.integers(0, 2, (hkv, d)) == 0, 1, -1).astype(np.int8) for _ in range(2))
+    size = np.ones(n)
+    if how == "any":
+        size = 2.0 ** rng.uniform(-11, 9, n)
+    elif how != "sink":
+        size[:128] = {"small first": 2.0 ** -14, "large first": 2.0 ** 12, "none first": 0.0}[how]
+        size[128:] = {"small first": 1.0, "large first": 0.25, "none first": 1.0}[how]
+    k = (0.3 * rng.standard_normal((n, hkv, d))).astype(np.float16)
+    v = rng.standard_normal((n, hkv, d)) * size[:, None, None]
+    q = rng.standard_normal((batch, hkv, d)).repeat(group, 1)
+    if how == "sink":
+        q[:] = q[0]
+        u = q[0, ::group] / np.linalg.norm(q[0, ::group], axis=-1, keepdims=True)
+        k[5] = 30 * math.log(2.0) * math.sqrt(d) / np.linalg.norm(q[0, ::group], axis=-1, keepdims=True) * u
+        v[5] = 0
+    empty = np.zeros((0, hkv, d), np.float16)
+    kv = [[(k, v.astype(np.float16))] + [(empty, empty)] * (batch - 1)]
+    built = gu.build_exact(kvq, torch, [SPECS[name]], kv, ks, vs, 16, shuffle_seed=batch)
+    q = q.astype(np.float16)
+    got = call(kvq, torch, built.views, [0, batch], None, q)
+    tiers = oshared.as_tiers(built.ora, [0, batch], [], batch)
+    for b in sorted({0, batch - 1}):
+        for h in range(hkv):
+            keys, values = oatt.dequantised_kv(tiers, b, h)
+            s = q[b, h * group:(h + 1) * group].astype(np.float64) @ keys.T / math.sqrt(d)
+            w = np.exp(s - s.max(-1, keepdims=True))
+            w /= w.sum(-1, keepdims=True)
+            want = w @ values
+            off = np.linalg.norm(got[b, h * group:(h + 1) * group] - want, axis=-1)
+            floor = 2.0 ** -25 * math.sqrt(d)  # fp16 outputs below its normal numbers
+            if how == "sink":
+                floor += 2.0 ** -25 * np.linalg.norm(values, axis=-1).max() * math.sqrt(n)
+            assert np.all(off <= 2.0 ** -9 * np.linalg.norm(want, axis=-1) + floor), (off, np.linalg.norm(want, axis=-1))
