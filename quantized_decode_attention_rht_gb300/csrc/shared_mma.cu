@@ -36,7 +36,7 @@
 //             codebooks, where that costs a tenth of the time and gains nothing measurable)
 //   values    INT4 levels times their scale one number (1.9e-4); of codebooks the centroid alone (norms in
 //             the values, rounded once more, would be 2.9e-4)
-//   centroids one number, scaled so that their roundings matter least (scale_table, 1.5e-4); a key's norm
+//   centroids one number, scaled so that their roundings matter least (scale_table, 1.3e-4); a key's norm
 //             multiplies its scores in float32.
 // Together 2.3e-4 to 3.3e-4 of the output on caches with outlier channels.  (With queries, and values times
 // norms, as single numbers, it was 5e-4 to 9e-4, with twice the rows in a block and 150 instead of
@@ -521,7 +521,7 @@ __device__ __forceinline__ void decode_unit(const Source& s, uint32_t tile, int 
 // adds up where its coordinates have one magnitude, and those of a key with an outlier channel all are
 // near their root mean square.  So the centroids there weigh most: w = exp(-3.125 (|c| / c1 - 1)^2), c1 = the
 // largest over 1.51, 2.15 or 2.73, what 2, 3 or 4 bits of N(0, 1) reach to.  (4-bit keys with x30 outlier
-// channels: 1.5e-4 of the output instead of 2.9e-4 with equal weights and 128 steps.)  c: centroid `lane` in every
+// channels: 1.3e-4 of the output instead of 2.9e-4 with equal weights and 128 steps.)  c: centroid `lane` in every
 // lane (0 beyond the codebook); the side's four warps, four candidates a thread.
 __device__ __forceinline__ float scale_table(Ctl* ctl, float c, int bits, int side, int tid) {
   constexpr int kEach = 4, kSteps = 128 * kEach;
@@ -817,10 +817,11 @@ __device__ __forceinline__ float2 unpack2(unsigned long long r) {
 // CODES: tiers of codebook formats, else of the others (a branch on the format in the softmax loop
 // made it a third slower for both).
 // Measured (GB300): 256 sequences x 64 / 8 heads on 16384 tokens of fp8 keys and INT4 values, 202 us,
-// 1.5 us a tile of 128 rows on 128 of 152 SMs: the softmax warps' arithmetic (the sum of rounded
-// weights is 12 us of it; without the queries' second part it takes the same time).  8 sequences x
-// 32 heads on 8192 tokens of 4-bit codes, 47 us: 1.4 us a tile, of which shared memory is busy most
-// (table look-ups, tiles written and read), and about 10 us of set-up, first tile and drain.
+// 1.5 us a tile of 128 rows on 128 of 152 SMs: a softmax group's chain of scores, weights and products
+// (issue slots 59% busy; the sum of rounded weights is 12 us of it, and without the queries' second
+// part it takes the same time).  8 sequences x 32 heads on 8192 tokens of 4-bit codes, 47 us: 1.4 us a
+// tile whatever the rows (table look-ups, tiles written and read), and about 10 us of set-up, first
+// tile and drain.
 template <bool CODES>
 __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid_constant__ SharedParams p) {
   // the pass over the sequences' own tiers may start on SMs that this grid leaves idle
