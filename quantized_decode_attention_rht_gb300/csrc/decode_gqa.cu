@@ -48,7 +48,6 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kQScale = 64.0f;   // q' is stored x 2^6 in the B fragments
 constexpr float kWScale = 256.0f;  // weights are stored x 2^8 in the B fragments
-constexpr float kMostScale = 255.0f;  // INT4 scales whose weights, at most 1 x 2^8 x scale, fit fp16
 
 // far tier stage: K fp8 16 x 128 B, V INT4 16 x 64 B, scales 16 x 4 fp16 (rows padded)
 constexpr int F_KSTR = 144, F_VSTR = 80;
@@ -82,6 +81,9 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
+}
+__device__ __forceinline__ void sts64_zero(uint32_t a) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(a), "r"(0u) : "memory");
 }
 __device__ __forceinline__ void sts128_zero(uint32_t a) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0u) : "memory");
@@ -219,6 +221,7 @@ __device__ __forceinline__ void rotate_query(const GqaParams& p, int b, int hk, 
 // ------------------------------------------------------------ far tier (fp8 K, INT4-g32 V)
 struct Far {
   static constexpr int STAGE = F_STAGE, S = F_STAGES;
+  static constexpr bool kRetry = true;
 
   // B fragments of q' for k-step kk: lane (g, c) holds column g = (head g/2, part g%2) at the
   // coordinates 32c + 4kk + {0,1} (b0b1) and {2,3} (b2b3); the key fragments below use the
@@ -297,6 +300,23 @@ struct Far {
     }
   }
 
+  // An accumulator that is not finite under a finite sum of weights: a scale above 255 (values beyond
+  // 1785: hardly ever), whose weight x 2^8 passes fp16's largest number, or values that are not finite
+  // themselves.  (A query that is not finite has no such sum, and is no reason to repeat its neighbours.)
+  __device__ static bool overflowed(const State& s) {
+    float sum = 0.f;  // 0 x finite is 0
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum = fmaf(s.acc[a][m][k], 0.f, sum);
+    }
+    return sum != 0.f && s.l < INFINITY;
+  }
+
+  // WIDE: the weights go without the 2^8 and the levels with it, which fp16 holds exactly.
+  template <bool WIDE>
   __device__ static void page(const uint8_t* st, int nvalid, const uint32_t (&qf)[8][2], State& s, int lane,
                               bool track, bool gate, bool live) {
     const int g = lane >> 2, c = lane & 3;
@@ -338,17 +358,15 @@ struct Far {
     // score gate: every token of the page, for every live head, far below the running max
     if (gate && __all_sync(kFull, !live || mt - s.m < -kGateLog2)) return;
     // ---- weights w = p * scale (x 2^8) per group for this lane's tokens (g, g+8), head c
-    // (of tokens past the end 0, whatever their slots hold: a weight of 0 times NaN would be NaN)
-    uint2 sc0 = lds64(s0 + F_S + 8 * g), sc1 = lds64(s0 + F_S + 8 * (g + 8));
-    if (!v0) sc0 = make_uint2(0u, 0u);
-    if (!v1) sc1 = make_uint2(0u, 0u);
+    // (scales past the end, whatever their slots hold, are zero: a weight of 0 times NaN would be NaN)
+    if (nvalid < PS) {
+      if (lane >= nvalid && lane < PS) sts64_zero(s0 + F_S + 8 * lane);
+      __syncwarp();
+    }
+    const uint2 sc0 = lds64(s0 + F_S + 8 * g), sc1 = lds64(s0 + F_S + 8 * (g + 8));
     const __half2* h0 = reinterpret_cast<const __half2*>(&sc0);
     const __half2* h1 = reinterpret_cast<const __half2*>(&sc1);
-    // A page with a scale above kMostScale (values beyond 1785: hardly ever) takes its weights without
-    // the 2^8 and its levels with it, which fp16 holds exactly.
-    const __half2 top = __hmax2(__hmax2(h0[0], h0[1]), __hmax2(h1[0], h1[1]));
-    const bool big = __any_sync(kFull, fmaxf(__low2float(top), __high2float(top)) > kMostScale);
-    const float wscale = big ? 1.0f : kWScale;
+    constexpr float wscale = WIDE ? 1.0f : kWScale;
     const float q0 = p0 * wscale, q1 = p1 * wscale;
     float w0g[4], w1g[4];
     w0g[0] = q0 * __low2float(h0[0]);
@@ -393,33 +411,29 @@ struct Far {
     const uint32_t magic = 0x64006400u;
     const __half2 off_lo = __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408));  // 1032
     const __half2 off_hi = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-    auto add_values = [&](auto scaled) {  // scaled: the levels carry the 2^8
-      auto lvl = [&](uint32_t bits, __half2 off) {
-        __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&bits), off);
-        if constexpr (decltype(scaled)::value) h = __hmul2(h, __float2half2_rn(kWScale));
-        return *reinterpret_cast<uint32_t*>(&h);
-      };
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const uint32_t x0s = R[a][0] >> 8, x1s = R[a][1] >> 8;
-        uint32_t am[4];
-        // m-tile (group a, m = 0): rows g -> coordinate 4g (low nibble of byte 2g),
-        // rows g+8 -> 4g+1 (high nibble)
-        am[0] = lvl((R[a][0] & 0x000F000Fu) | magic, off_lo);
-        am[1] = lvl((R[a][0] & 0x00F000F0u) | magic, off_hi);
-        am[2] = lvl((R[a][1] & 0x000F000Fu) | magic, off_lo);
-        am[3] = lvl((R[a][1] & 0x00F000F0u) | magic, off_hi);
-        mma16816(s.acc[a][0], am, bf[a][0], bf[a][1]);
-        // m = 1: coordinates 4g+2, 4g+3 (byte 2g+1)
-        am[0] = lvl((x0s & 0x000F000Fu) | magic, off_lo);
-        am[1] = lvl((x0s & 0x00F000F0u) | magic, off_hi);
-        am[2] = lvl((x1s & 0x000F000Fu) | magic, off_lo);
-        am[3] = lvl((x1s & 0x00F000F0u) | magic, off_hi);
-        mma16816(s.acc[a][1], am, bf[a][0], bf[a][1]);
-      }
+    auto lvl = [&](uint32_t bits, __half2 off) {
+      __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&bits), off);
+      if constexpr (WIDE) h = __hmul2(h, __float2half2_rn(kWScale));
+      return *reinterpret_cast<uint32_t*>(&h);
     };
-    if (!big) add_values(std::false_type{});
-    else add_values(std::true_type{});
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const uint32_t x0s = R[a][0] >> 8, x1s = R[a][1] >> 8;
+      uint32_t am[4];
+      // m-tile (group a, m = 0): rows g -> coordinate 4g (low nibble of byte 2g),
+      // rows g+8 -> 4g+1 (high nibble)
+      am[0] = lvl((R[a][0] & 0x000F000Fu) | magic, off_lo);
+      am[1] = lvl((R[a][0] & 0x00F000F0u) | magic, off_hi);
+      am[2] = lvl((R[a][1] & 0x000F000Fu) | magic, off_lo);
+      am[3] = lvl((R[a][1] & 0x00F000F0u) | magic, off_hi);
+      mma16816(s.acc[a][0], am, bf[a][0], bf[a][1]);
+      // m = 1: coordinates 4g+2, 4g+3 (byte 2g+1)
+      am[0] = lvl((x0s & 0x000F000Fu) | magic, off_lo);
+      am[1] = lvl((x0s & 0x00F000F0u) | magic, off_hi);
+      am[2] = lvl((x1s & 0x000F000Fu) | magic, off_lo);
+      am[3] = lvl((x1s & 0x00F000F0u) | magic, off_hi);
+      mma16816(s.acc[a][1], am, bf[a][0], bf[a][1]);
+    }
   }
 
   // Partial for head c: acc[32a + 4g + k] = sum_t p_t s_ta (u - 8), relative to the max.
@@ -449,6 +463,7 @@ struct Far {
 // ------------------------------------------------------------ near tier (fp16 K, fp16 V)
 struct Near {
   static constexpr int STAGE = N_STAGE, S = N_STAGES;
+  static constexpr bool kRetry = false;  // weights are at most 2^8
 
   // B fragments in the natural coordinate order: b0b1 = 16kk + 2c, +1; b2b3 = +8, +9.
   __device__ static void qfrag(const float* qbuf, uint32_t (&qf)[8][2], int g, int c) {
@@ -499,6 +514,7 @@ struct Near {
     s.mn = INFINITY;
   }
 
+  template <bool>
   __device__ static void page(const uint8_t* st, int nvalid, const uint32_t (&qf)[8][2], State& s, int lane,
                               bool track, bool gate, bool live) {
     const int g = lane >> 2, c = lane & 3;
@@ -626,25 +642,35 @@ __device__ __forceinline__ void run_item(const GqaParams& p, const GqaTier& T, i
     return;
   }
   const uint32_t ring = smem_addr(wsm);
-#pragma unroll 1
-  for (int s = 0; s < TT::S; ++s) {
-    if (s < npg) TT::issue(T, pl, btab[s], hk, p.hkv, ring + s * TT::STAGE, lane);
-    cp_commit();
-  }
   typename TT::State st;
-  TT::init(st);
+  auto pages = [&](auto wide) {
 #pragma unroll 1
-  for (int i = 0; i < npg; ++i) {
-    cp_wait<TT::S - 1>();
-    __syncwarp();
-    const int slot = i % TT::S;
-    const int nvalid = min(PS, t1 - (pg0 + i) * PS);
-    TT::page(wsm + slot * TT::STAGE, nvalid, qf, st, lane, track, p.gate != 0, c < p.igroup);
-    __syncwarp();
-    if (i + TT::S < npg) TT::issue(T, pl, btab[i + TT::S], hk, p.hkv, ring + slot * TT::STAGE, lane);
-    cp_commit();
+    for (int s = 0; s < TT::S; ++s) {
+      if (s < npg) TT::issue(T, pl, btab[s], hk, p.hkv, ring + s * TT::STAGE, lane);
+      cp_commit();
+    }
+    TT::init(st);
+#pragma unroll 1
+    for (int i = 0; i < npg; ++i) {
+      cp_wait<TT::S - 1>();
+      __syncwarp();
+      const int slot = i % TT::S;
+      const int nvalid = min(PS, t1 - (pg0 + i) * PS);
+      TT::template page<decltype(wide)::value>(wsm + slot * TT::STAGE, nvalid, qf, st, lane, track, p.gate != 0,
+                                               c < p.igroup);
+      __syncwarp();
+      if (i + TT::S < npg) TT::issue(T, pl, btab[i + TT::S], hk, p.hkv, ring + slot * TT::STAGE, lane);
+      cp_commit();
+    }
+    cp_wait<0>();
+  };
+  pages(std::false_type{});
+  if constexpr (TT::kRetry) {  // the item once more, with room for its scales
+    if (__any_sync(kFull, TT::overflowed(st))) {
+      __syncwarp();
+      pages(std::true_type{});
+    }
   }
-  cp_wait<0>();
   const bool live = c < p.igroup;
   const size_t part = live ? ((size_t)b * p.hq + hk * p.group + h0 + c) * p.total_splits + T.split_begin + chunk : 0;
   TT::finish(st, p.ws_acc + part * D, p.ws_ml + 2 * part, track ? p.ws_min + part : nullptr, lane, live);
