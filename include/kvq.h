@@ -486,9 +486,9 @@ KVQ_API kvq_status kvq_decode_attention_ex(const kvq_tier_view* tiers, int32_t n
  * offsets; lengths and block tables are read when it runs.
  * The output is fp16, and so is what the tensor cores multiply (rotated queries as the sum of two
  * numbers, decoded rows that are not fp16 values already and softmax weights as one), with
- * float32 scores, sums and accumulators: on caches with outlier channels the output's error is
- * below 2^-11 of its size (2-norm; 0.42 2^-11 is its own rounding), where kvq_decode_attention
- * gives float32.  A rotated query has to fit fp16: the magnitudes of a
+ * float32 scores, sums and accumulators: the output's error is 2^-12 to 2^-11 of its size (2-norm
+ * over the outputs, on caches with outlier channels; 0.42 2^-11 is its own rounding), where
+ * kvq_decode_attention gives float32.  A rotated query has to fit fp16: the magnitudes of a
  * query's elements may sum to at most 5.8e6.  So has a prefix's value row: INT4 scales may be up
  * to 9352 (reported beyond: KVQ_DEVERR_VALUE_RANGE).  Prefix tiers run so for head_dim 128, any page
  * size, and format pairs fp16/fp16, fp8/INT4, fp8/fp16 and codebook/codebook; otherwise (head_dim
