@@ -420,6 +420,8 @@ KVQ_API kvq_status kvq_decode_attention(const kvq_tier_view* tiers, int32_t num_
 #define KVQ_DEVERR_VALUE_RANGE 8  /* an INT4 scale above 9352 in a shared prefix, whose values
                                      (rotated, beyond 65504) the fp16 of the prefix pass
                                      cannot hold: infinities or NaN in the output of its group */
+#define KVQ_DEVERR_OFFSETS 16     /* chunk offsets that fall or leave [0, num_tokens]: they are
+                                     raised to the largest one before them, or cut */
 
 /* Options of kvq_decode_attention_ex: two features of the FoveatedKV page's fused kernel
  * ("Making it fast"), and the device error report.  All zero is the plain computation of
@@ -503,6 +505,69 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
                                                const kvq_tier_view* tiers, int32_t num_tiers, const uint16_t* q,
                                                int32_t batch, int32_t num_q_heads, uint16_t* out, void* workspace,
                                                size_t workspace_bytes, int32_t* status, void* stream);
+
+/* ---- chunks of new tokens, and windows ----------------------------------------------------
+ * Which of a sequence's cached tokens a query sees.  The tokens of its tiles stand one after the
+ * other: token t of tier i at position t + the lengths of tiers 0 .. i - 1 (so tiers are listed
+ * oldest tokens first).  A query at position p sees position t where
+ *   t <= p  and  (window == 0  or  t > p - window  or  t < sinks):
+ * itself and what stands before it; of that, with a sliding window, the last `window` positions
+ * (its own among them) and the first `sinks`.  NULL in place of the struct: no window. */
+typedef struct kvq_visible {
+  int32_t window; /* >= 0 */
+  int32_t sinks;  /* >= 0; 0 unless window > 0 */
+} kvq_visible;
+
+/* Attention of a chunk of new tokens of every sequence (a prompt or a part of one, drafted tokens to
+ * be checked, a step's single token) over all that the sequence has cached, the chunk itself
+ * included: append it first (kvq_rope_append), then attend.
+ *   out[q_offsets[b] + i][h] = softmax_t( q[q_offsets[b] + i][h] . K[t] / sqrt(D) ) V[t]
+ * over the positions t that the query sees; it stands at p = L_b - T_b + i, with L_b the sequence's
+ * cached tokens (its tiers' lengths together) and T_b = q_offsets[b + 1] - q_offsets[b].  A query
+ * that sees nothing (of a chunk longer than its sequence, p < 0) gives zeros.  K[t], V[t] are the
+ * dequantised cache rows with the rotation undone.
+ *   tiers     : host array [num_tiers], 1..KVQ_MAX_TIERS, as in kvq_decode_attention; the same
+ *               formats and groups, any page size
+ *   q         : heads of the new tokens and, in q->out, of the outputs (fp16, separate or in place;
+ *               num_heads / num_kv_heads in {1,2,4,8}).  Addresses 16-byte aligned, strides
+ *               multiples of 8 elements (else KVQ_ERR_INVALID_ARGUMENT)
+ *   q_offsets : DEVICE int32 [batch + 1], not decreasing, in [0, num_tokens]; a sequence may have
+ *               no new token.  Output rows outside all chunks are left as they were.  NULL where
+ *               every sequence has one new token (num_tokens == batch)
+ *   workspace : >= kvq_chunk_workspace_size() bytes for the same sizes and block tables, 256-byte
+ *               aligned, scratch only.  Calls that may overlap on the GPU need one each
+ *   status    : optional device int32: the call's KVQ_DEVERR_* bits (as in kvq_decode_options; not
+ *               written by a call with batch 0 or num_tokens 0).  A token whose page lies outside
+ *               the pool reads as zeros here
+ * Offsets, lengths and block tables are read on the device when the call runs, also in a captured
+ * graph.  Sign vectors 16-byte aligned; num_tokens x num_q_heads at most 2^26, batch at most 65536,
+ * block tables of less than 2^31 - 256 tokens together and pools of less than 2^32 - 1 rows a side
+ * (else KVQ_ERR_UNSUPPORTED).
+ * The output is fp16, and so is what the tensor cores multiply (rotated queries as the sum of two
+ * numbers, decoded rows that are not fp16 values already and softmax weights as one), with float32
+ * scores, sums and accumulators.  The magnitudes of a query's elements may sum to at most 45000 x
+ * head_dim.  INT4 scales above 9352 are reported (KVQ_DEVERR_VALUE_RANGE).  A cached vector that is
+ * not finite gives NaN in the outputs of the queries that see it (its key alone may also give them no
+ * weight), and does not reach the others. */
+KVQ_API kvq_status kvq_chunk_workspace_size(const kvq_tier_view* tiers, int32_t num_tiers, int32_t batch,
+                                            int32_t num_tokens, int32_t num_q_heads, const kvq_visible* visible,
+                                            size_t* bytes);
+KVQ_API kvq_status kvq_chunk_attention(const kvq_tier_view* tiers, int32_t num_tiers, const kvq_heads* q,
+                                       const int32_t* q_offsets, int32_t batch, int32_t num_tokens,
+                                       const kvq_visible* visible, void* workspace, size_t workspace_bytes,
+                                       int32_t* status, void* stream);
+
+/* Decode attention of layers with a sliding window: one query per sequence, its newest cached token
+ * (p = L_b - 1), over the positions that it sees.  Reads the sinks' and the window's pages only.
+ *   q, out : fp16 [batch][num_q_heads][head_dim], 16-byte aligned
+ * The rest as in kvq_chunk_attention with one token a sequence; kvq_decode_window_workspace_size
+ * gives the workspace.  visible NULL or with window 0 sees everything. */
+KVQ_API kvq_status kvq_decode_window_workspace_size(const kvq_tier_view* tiers, int32_t num_tiers, int32_t batch,
+                                                    int32_t num_q_heads, const kvq_visible* visible, size_t* bytes);
+KVQ_API kvq_status kvq_decode_attention_window(const kvq_tier_view* tiers, int32_t num_tiers, const uint16_t* q,
+                                               int32_t batch, int32_t num_q_heads, const kvq_visible* visible,
+                                               uint16_t* out, void* workspace, size_t workspace_bytes,
+                                               int32_t* status, void* stream);
 
 /* Decode attention for callers that cannot allocate device memory.
  *

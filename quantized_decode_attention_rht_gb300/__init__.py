@@ -84,6 +84,12 @@ class KvqRope(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class KvqVisible(ctypes.Structure):
+    """Mirror of ``struct kvq_visible``."""
+
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+
+
 class KvqHeads(ctypes.Structure):
     """Mirror of ``struct kvq_heads``."""
 
@@ -98,6 +104,7 @@ ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
 SCORE_GATE_NATS = 16.0
 # device-side error bits of a decode call (kvq_decode_options.status)
 DEVERR_COPY_TIMEOUT, DEVERR_PAGE_INDEX, DEVERR_SEQ_LEN, DEVERR_VALUE_RANGE = 1, 2, 4, 8
+DEVERR_OFFSETS = 16
 
 _lib_handle = None
 
@@ -139,6 +146,13 @@ def lib() -> ctypes.CDLL:
                                                  i32, i32, i32, szp],
             "kvq_decode_attention_shared": [ctypes.POINTER(KvqTierView), i32, vp, i32, ctypes.POINTER(KvqTierView),
                                             i32, vp, i32, i32, vp, vp, sz, vp, vp],
+            "kvq_chunk_workspace_size": [ctypes.POINTER(KvqTierView), i32, i32, i32, i32, ctypes.POINTER(KvqVisible), szp],
+            "kvq_chunk_attention": [ctypes.POINTER(KvqTierView), i32, vp, vp, i32, i32, ctypes.POINTER(KvqVisible), vp, sz,
+                                    vp, vp],
+            "kvq_decode_window_workspace_size": [ctypes.POINTER(KvqTierView), i32, i32, i32,
+                                                 ctypes.POINTER(KvqVisible), szp],
+            "kvq_decode_attention_window": [ctypes.POINTER(KvqTierView), i32, vp, i32, i32, ctypes.POINTER(KvqVisible),
+                                            vp, vp, sz, vp, vp],
             "kvq_decode_attention_noalloc": [ctypes.POINTER(KvqTierView), i32, vp, i32, i32, i32, vp, vp],
         }
         for name, args in sigs.items():
@@ -555,6 +569,88 @@ def kvq_decode_attention_shared(prefix_tiers, group_offsets, tiers, q, out, work
                                                           for x in (t.block_table, t.seq_lens)]))
     if result:
         raise KvqError(result, "kvq_decode_attention_shared")
+
+
+def _visible(window: int, sinks: int):
+    for name, x in (("window", window), ("sinks", sinks)):
+        if not -(2 ** 31) <= x < 2 ** 31:
+            raise ValueError(f"{name} holds a number beyond int32")
+    return ctypes.byref(KvqVisible(window, sinks))
+
+
+def kvq_chunk_workspace_size(tiers, batch: int, num_tokens: int, num_q_heads: int, window: int = 0,
+                             sinks: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().kvq_chunk_workspace_size(_views(tiers), len(tiers), batch, num_tokens, num_q_heads,
+                                          _visible(window, sinks), ctypes.byref(n)), "kvq_chunk_workspace_size")
+    return n.value
+
+
+def _workspace_bytes(workspace) -> int:
+    if workspace is None or not getattr(workspace, "is_cuda", False):
+        raise ValueError("workspace must be a CUDA tensor")
+    _dense(workspace)
+    return workspace.numel() * workspace.element_size()
+
+
+def kvq_chunk_attention(tiers, q_offsets, q, out, workspace, window: int = 0, sinks: int = 0, status=None,
+                        stream=None) -> None:
+    """Attention of the newest tokens of every sequence over all its cached tokens.  tiers: TierViews,
+    oldest tokens first; q_offsets: int32 [B + 1] (sequence b's queries are q_offsets[b] ..
+    q_offsets[b + 1] - 1), or None for one query a sequence; q, out: fp16 [T, Hq, D] CUDA tensors or
+    strided views (out may be q); window, sinks: a query sees the last `window` positions, its own
+    among them, and the first `sinks` (window 0: everything before it); workspace: uint8 CUDA tensor;
+    status: int32 CUDA tensor of one element."""
+    if not tiers:
+        raise ValueError("chunk attention needs at least one tier")
+    qs = _check_heads(q, "q", None, None, tiers[0].cache.struct.head_dim)
+    t, hq = q.shape[0], q.shape[1]
+    os = _check_heads(out, "out", t, hq, tiers[0].cache.struct.head_dim)
+    if q_offsets is None:
+        b = t
+    else:
+        _int_vector(q_offsets, "q_offsets", 1)
+        b = q_offsets.shape[0] - 1
+    _arg(status, "status", "int32", None, min_numel=1)
+    ws_bytes, visible = _workspace_bytes(workspace), _visible(window, sinks)
+    _check_views(tiers, b)
+    arr = _views(tiers, checked=True)
+    result = (_lib_handle or lib()).kvq_chunk_attention(
+        arr, len(tiers), _heads(q, qs, out, os), _ptr(q_offsets), b, t, visible, workspace.data_ptr(),
+        ws_bytes, _ptr(status), _call_stream(stream, q, out, q_offsets, workspace, status,
+                                   *[x for v in tiers for x in (v.block_table, v.seq_lens)]))
+    if result:
+        raise KvqError(result, "kvq_chunk_attention")
+
+
+def kvq_decode_window_workspace_size(tiers, batch: int, num_q_heads: int, window: int, sinks: int = 0) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().kvq_decode_window_workspace_size(_views(tiers), len(tiers), batch, num_q_heads,
+                                                  _visible(window, sinks), ctypes.byref(n)),
+           "kvq_decode_window_workspace_size")
+    return n.value
+
+
+def kvq_decode_attention_window(tiers, q, out, workspace, window: int, sinks: int = 0, status=None,
+                                stream=None) -> None:
+    """One query per sequence, at its newest cached token, over the last `window` positions and the
+    first `sinks`.  tiers: TierViews, oldest tokens first; q, out: fp16 [B, Hq, D]; workspace: uint8
+    CUDA tensor; status: int32 CUDA tensor of one element."""
+    if not tiers:
+        raise ValueError("decode attention needs at least one tier")
+    _dense(q, out, status)
+    _arg(q, "q", "float16", (None, None, tiers[0].cache.struct.head_dim))
+    _arg(out, "out", "float16", tuple(q.shape))
+    _arg(status, "status", "int32", None, min_numel=1)
+    ws_bytes, visible = _workspace_bytes(workspace), _visible(window, sinks)
+    b, hq = int(q.shape[0]), int(q.shape[1])
+    _check_views(tiers, b)
+    arr = _views(tiers, checked=True)
+    result = (_lib_handle or lib()).kvq_decode_attention_window(
+        arr, len(tiers), q.data_ptr(), b, hq, visible, out.data_ptr(), workspace.data_ptr(), ws_bytes, _ptr(status),
+        _call_stream(stream, q, out, workspace, status, *[x for v in tiers for x in (v.block_table, v.seq_lens)]))
+    if result:
+        raise KvqError(result, "kvq_decode_attention_window")
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20

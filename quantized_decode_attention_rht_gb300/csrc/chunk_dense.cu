@@ -1,0 +1,825 @@
+// Attention of long chunks (kvq_chunk_attention): what a chunk sees is unpacked once into tiles of
+// fp16 numbers, and each unit of up to 256 query rows runs over them on the tensor cores.
+//
+//   S = q~ K^T,  P = 2^(S - m),  O += P V,  l += rowsum P,
+// with rotated queries q~ (times log2 e / sqrt(D)) and the rotated keys and values as the cache holds them; the
+// value rotation is undone where partial results are joined.
+//
+// prepare_kernel writes every operand as the products read it (rows of 128 bytes, 16-byte pieces swizzled), so that
+// attention loads whole tiles by one bulk copy each:
+//   queries   two fp16 numbers, the nearest one and the rest: rounded once they would be off by 2^-12 of their size,
+//             which keys with outlier channels turn into 6e-4 of the output
+//   keys      fp16 and fp8 keys as they are; of codebooks the centroid under its table's scale, and the key's norm as
+//             a factor of its scores; keys with a sketch or outliers as one fp16 number
+//   values    fp16 as they are, INT4 levels times their scale (one rounding); of codebooks the centroid, and the norm
+//             as a factor of the weights.
+// Why unpack: a unit's products over 128 tokens take about 2 us on an SM, decoding the tokens 1.4 us; a chunk of 2048
+// tokens with four query heads a kv head would decode each token 32 times.
+//
+// attend_kernel: one item (tiles of a unit) a block of 10 warps: 2 x 4 softmax warps, a thread a row of two blocks of
+// 128 rows; one warp that loads, one that issues products.  While one row block's scores become weights, the other's
+// products run.  TMEM: two blocks of scores, over which the weights are written, and two accumulators, all 512
+// columns at head_dim 128.  (head_dim 256: one row block, tiles of 64 tokens, two score blocks in turn.)
+#include <algorithm>
+#include <atomic>
+
+#include "chunk.cuh"
+#include "rotate.cuh"
+#include "tc.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kPrepareThreads = 256;
+
+// ------------------------------------------------------------------------ unpacking
+// 16 coordinates from 16 c on as fp16 pairs: values of the plain formats, table entries of codebooks.
+__device__ __forceinline__ void unpack16(int fmt, int bits, const uint8_t* row, const __half* scales, int c,
+                                         const uint16_t* table, uint32_t (&h)[8], int* over) {
+  switch (fmt) {
+    case KVQ_FMT_FP16: {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(row) + 2 * c), b = __ldg(reinterpret_cast<const uint4*>(row) + 2 * c + 1);
+      h[0] = a.x, h[1] = a.y, h[2] = a.z, h[3] = a.w, h[4] = b.x, h[5] = b.y, h[6] = b.z, h[7] = b.w;
+      return;
+    }
+    case KVQ_FMT_FP8_E4M3: {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(row) + c);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[k]) : "h"((uint16_t)(w[k / 2] >> (16 * (k & 1)))));
+      return;
+    }
+    case KVQ_FMT_INT4_G32: {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(row) + c);
+      const __half s = scales[c / 2];
+      const uint16_t sb = __half_as_ushort(s) & 0x7FFFu;
+      if (sb >= 0x7092u && sb < 0x7C00u) *over = 1;  // a finite scale above 9352: seven times it is no fp16 number
+      const __half2 s2 = __half2half2(s);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        // levels n - 8, exact in fp16: 1024 + n less 1032
+        const uint32_t v = (k < 4 ? a.x : a.y) >> (8 * (k & 3));
+        const uint32_t up = (v & 15u) | (v & 0xF0u) << 12 | 0x64006400u;
+        const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&up), __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
+        const __half2 x = __hmul2(n, s2);
+        h[k] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+      return;
+    }
+    default: break;
+  }
+  uint64_t w;  // 16 codes
+  if (bits == 4) {
+    const uint2 a = __ldg(reinterpret_cast<const uint2*>(row) + c);
+    w = a.x | (uint64_t)a.y << 32;
+  } else if (bits == 3) {  // (rows of head_dim 64 are of 24 bytes)
+    const uint16_t* a = reinterpret_cast<const uint16_t*>(row) + 3 * c;
+    w = (uint64_t)__ldg(a) | (uint64_t)__ldg(a + 1) << 16 | (uint64_t)__ldg(a + 2) << 32;
+  } else {
+    w = __ldg(reinterpret_cast<const uint32_t*>(row) + c);
+  }
+  const uint32_t mask = (1u << bits) - 1u;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t lo = (uint32_t)(w >> (2 * k * bits)) & mask, hi = (uint32_t)(w >> ((2 * k + 1) * bits)) & mask;
+    h[k] = table[lo] | (uint32_t)table[hi] << 16;
+  }
+}
+
+__device__ __forceinline__ bool half2_finite(uint32_t h) {
+  return (h & 0x7C00u) != 0x7C00u && (h & 0x7C000000u) != 0x7C000000u;
+}
+// A power of two above a finite x >= 0.
+__device__ __forceinline__ float two_above(float x) {
+  return __uint_as_float((min(max(__float_as_uint(x) >> 23, 64u), 190u) + 1u) << 23);
+}
+__device__ __forceinline__ float finite_or_zero(float x) { return x < INFINITY ? x : 0.f; }  // (NaN: zero)
+
+// Offset of coordinate c (a multiple of 8) of row r in an operand tile of `rows` rows.
+__device__ __forceinline__ uint32_t tile_at(int rows, int r, int c) {
+  return (uint32_t)(c / 64) * rows * 128 + r * 128 + ((((c / 8) & 7) ^ (r & 7)) << 4);
+}
+
+// The norm of a codebook token's key (side 0) or value.
+__device__ __forceinline__ float norm_of(const ChunkTier& t, int side, uint32_t row) {
+  if (side) return __half2float(t.v_aux[row]);
+  if (t.k_fmt == KVQ_FMT_CODEBOOK_QJL) return __half2float(t.k_aux[2 * (size_t)row]);
+  if (t.k_fmt == KVQ_FMT_CODEBOOK_OUTLIER)
+    return __half2float(*reinterpret_cast<const __half*>(reinterpret_cast<const uint8_t*>(t.k_aux) + (size_t)row * (4 + KVQ_OUTLIER_CHANNELS)));
+  return __half2float(t.k_aux[row]);
+}
+
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+
+// Tier and row in its pool of a sequence's position (row kNone: no token there, or its page outside the pool).
+__device__ __forceinline__ uint32_t find_row(const ChunkParams& p, const ChunkSeq& s, int seq, int h, int pos, int& tier, int* bits) {
+  tier = 0;
+  if (pos < 0 || pos >= s.len) return kNone;
+#pragma unroll
+  for (int k = 1; k < KVQ_MAX_TIERS; ++k)
+    if (k < p.num_tiers && pos >= s.base[k]) tier = k;
+  const ChunkTier& t = p.tier[tier];
+  pos -= s.base[tier];
+  const int page = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
+  const int phys = __ldg(t.block_table + (size_t)seq * t.table_pages + page);
+  if (!page_in_pool(phys, t.num_pages, bits)) return kNone;
+  return ((uint32_t)phys * p.hkv + h) * p.page_size + (pos - page * p.page_size);  // below 2^32: the host checks
+}
+
+template <int D>
+__device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int h, const uint16_t (*tables)[2][16],
+                                            uint32_t* s_row, int* s_tier, int* s_bad, float* s_max) {
+  constexpr int TT = dense_tile(D), C = D / 16;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // the sequence: the last whose tiles begin at or before this one (unpacked ones alone have any)
+  int lo = 0, hi = p.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.seq[mid].tile0 <= tile) lo = mid;
+    else hi = mid;
+  }
+  const ChunkSeq s = p.seq[lo];
+  const int i = tile - s.tile0, j = i < s.sink_tiles ? i : s.window_tile + i - s.sink_tiles;
+  int bits = 0;
+  __syncthreads();  // (the item before is done with the shared arrays)
+  if (tid < TT) {
+    int tier;
+    s_row[tid] = find_row(p, s, lo, h, j * TT + tid, tier, &bits);
+    s_tier[tid] = tier;
+    s_bad[tid] = 0;
+  }
+  float unit = 1.0f;
+  if (p.codes) {
+    // what the values' norms are divided by: a power of two above those of the sequence's first tokens
+    float most = 0.f;
+    if (tid < 128) {
+      int tier, ignored = 0;
+      const uint32_t row = find_row(p, s, lo, h, tid, tier, &ignored);
+      if (row != kNone && p.tier[tier].v_fmt == KVQ_FMT_CODEBOOK)
+        most = finite_or_zero(norm_of(p.tier[tier], 1, row) * p.head->unscale[tier][1]);
+      most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
+      if (lane == 0) s_max[tid >> 5] = most;
+    }
+    __syncthreads();
+    most = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    unit = most > 0.f ? two_above(most) : 1.0f;
+    if (i == 0 && tid == 0) p.unit_of[(size_t)lo * p.hkv + h] = unit;
+  }
+  __syncthreads();
+  const float per_unit = 1.0f / unit;
+  const size_t at = ((size_t)tile * p.hkv + h) * (TT * D * 2);
+  int over = 0;
+  // values
+  for (int u = tid; u < TT * C; u += kPrepareThreads) {
+    const int r = u / C, c = u % C;
+    uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const uint32_t row = s_row[r];
+    if (row != kNone) {
+      const ChunkTier& t = p.tier[s_tier[r]];
+      unpack16(t.v_fmt, t.v_bits, t.v_rows + (size_t)row * t.v_row_bytes, t.v_aux + (size_t)row * (D / kGroup), c,
+               tables[s_tier[r]][1], x, &over);
+      bool fine = true;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) fine = fine && half2_finite(x[k]);
+      if (!fine) {  // a weight of zero must meet no infinity: the token's scores say it instead (its key is NaN)
+        s_bad[r] = 1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = 0;
+      }
+      if (p.codes && t.v_fmt != KVQ_FMT_CODEBOOK) {
+        const __half2 f = __float2half2_rn(per_unit);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], *reinterpret_cast<const uint32_t*>(&f));
+      }
+    }
+    uint8_t* to = p.vt + at;
+    *reinterpret_cast<uint4*>(to + tile_at(TT, r, 16 * c)) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(to + tile_at(TT, r, 16 * c + 8)) = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+  __syncthreads();
+  // keys
+  for (int u = tid; u < TT * C; u += kPrepareThreads) {
+    const int r = u / C, c = u % C;
+    uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const uint32_t row = s_row[r];
+    if (row != kNone) {
+      const int tier = s_tier[r];
+      const ChunkTier& t = p.tier[tier];
+      unpack16(t.k_fmt, t.k_bits, t.k_rows + (size_t)row * t.k_row_bytes, nullptr, c, tables[tier][0], x, &over);
+      if (t.k_fmt == KVQ_FMT_CODEBOOK_QJL || t.k_fmt == KVQ_FMT_CODEBOOK_OUTLIER) {
+        const float kn = norm_of(t, 0, row) * p.head->unscale[tier][0];
+        float y[16];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 f = unpack_half2(x[k]);
+          y[2 * k] = f.x * kn;
+          y[2 * k + 1] = f.y * kn;
+        }
+        if (t.k_fmt == KVQ_FMT_CODEBOOK_QJL) {
+          // + ||r|| sqrt(pi / 2) / m * sum_j z_j S_j
+          const float f = __half2float(t.k_aux[2 * (size_t)row + 1]) * (1.2533141373155003f / KVQ_QJL_DIM);
+          const uint32_t* z = reinterpret_cast<const uint32_t*>(t.k_rows + (size_t)row * t.k_row_bytes + D * t.k_bits / 8);
+          float sum[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) sum[k] = 0.f;
+#pragma unroll 1
+          for (int m = 0; m < KVQ_QJL_DIM; ++m) {
+            const uint32_t flip = ((__ldg(z + m / 32) >> (m % 32)) & 1u) ? 0u : 0x80000000u;
+            const float4* sj = reinterpret_cast<const float4*>(t.k_qjl + (size_t)m * D + 16 * c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float4 v = __ldg(sj + k);
+              sum[4 * k] += __uint_as_float(__float_as_uint(v.x) ^ flip);
+              sum[4 * k + 1] += __uint_as_float(__float_as_uint(v.y) ^ flip);
+              sum[4 * k + 2] += __uint_as_float(__float_as_uint(v.z) ^ flip);
+              sum[4 * k + 3] += __uint_as_float(__float_as_uint(v.w) ^ flip);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) y[k] = fmaf(f, sum[k], y[k]);
+        } else {
+          // + the rotated outliers: q_j s times column c_j of H diag(s) / sqrt(D)
+          const uint8_t* rec = reinterpret_cast<const uint8_t*>(t.k_aux) + (size_t)row * (4 + KVQ_OUTLIER_CHANNELS);
+          const float f = __half2float(*reinterpret_cast<const __half*>(rec + 2)) * inv_sqrt_dim(D);
+#pragma unroll 1
+          for (int m = 0; m < KVQ_OUTLIER_CHANNELS; ++m) {
+            const int ch = __ldg(t.k_outl + h * KVQ_OUTLIER_CHANNELS + m);
+            float v = f * (float)reinterpret_cast<const int8_t*>(rec)[4 + m];
+            if (__ldg(p.k_signs + (size_t)h * D + ch) < 0) v = -v;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) y[k] += __popc((16 * c + k) & ch) & 1 ? -v : v;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = half2_bits(y[2 * k], y[2 * k + 1]);
+      }
+      if (s_bad[r]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = 0x7E007E00u;
+      }
+    }
+    uint8_t* to = p.kt + at;
+    *reinterpret_cast<uint4*>(to + tile_at(TT, r, 16 * c)) = make_uint4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(to + tile_at(TT, r, 16 * c + 8)) = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+  if (p.codes) {
+    float vn = 0.f;
+    if (tid < TT) {
+      float kn = 1.0f;
+      vn = 1.0f;
+      const uint32_t row = s_row[tid];
+      if (row != kNone) {
+        const int tier = s_tier[tid];
+        const ChunkTier& t = p.tier[tier];
+        if (t.k_fmt == KVQ_FMT_CODEBOOK) kn = norm_of(t, 0, row) * p.head->unscale[tier][0];
+        if (t.v_fmt == KVQ_FMT_CODEBOOK) vn = norm_of(t, 1, row) * p.head->unscale[tier][1] * per_unit;
+      }
+      const size_t n = ((size_t)tile * p.hkv + h) * TT + tid;
+      p.kn[n] = kn;
+      p.vn[n] = vn;
+      const float most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(finite_or_zero(vn))));
+      if (lane == 0) s_max[4 + (tid >> 5)] = most;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      float most = s_max[4];
+      for (int k = 1; k < TT / 32; ++k) most = fmaxf(most, s_max[4 + k]);
+      p.top[(size_t)tile * p.hkv + h] = two_above(most);
+    }
+  }
+  if (over) bits |= KVQ_DEVERR_VALUE_RANGE;
+  if (bits) atomicOr(&p.head->err, bits);
+}
+
+// The rows of a unit's queries of one kv head: rotated, times log2(e) / D (1 / sqrt(D) of the rotation and of the
+// scores, which are then in base-2 units), as two fp16 numbers.
+template <int D>
+__device__ __forceinline__ void rotate_queries(const ChunkParams& p, int unit, int h) {
+  constexpr int E = D / 32, kRows = kChunkRows * dense_blocks(D);
+  constexpr float scale = 1.4426950408889634f / D;
+  const int lane = threadIdx.x & 31;
+  const ChunkUnit& x = p.unit[0][unit];
+  const ChunkSeq& s = p.seq[x.seq];
+  const int rows = s.tokens << p.group_shift;
+  for (int r = threadIdx.x >> 5; r < kRows; r += kPrepareThreads / 32) {
+    const int row = x.row0 + r;
+    if (r >= kChunkRows && x.row0 + kChunkRows >= rows) break;  // no second block
+    float y[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = 0.f;
+    if (row < rows) {
+      const int token = s.q0 + (row >> p.group_shift), head = (h << p.group_shift) + (row & (p.group - 1));
+      load_rotate<E>(p.q + token * p.q_token + head * p.q_head, p.k_signs + (size_t)h * D, lane, y);
+    }
+    uint8_t* to = p.qt + (((size_t)unit * p.hkv + h) * dense_blocks(D) + r / kChunkRows) * (2 * kChunkRows * D * 2);
+    const uint32_t at = tile_at(kChunkRows, r % kChunkRows, lane * E / 8 * 8) + lane * E % 8 * 2;
+    uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+    for (int k = 0; k < E / 2; ++k) {
+      const float a = y[2 * k] * scale, b = y[2 * k + 1] * scale;
+      hi[k] = half2_bits(a, b);
+      const float2 near = unpack_half2(hi[k]);
+      lo[k] = half2_bits(a - near.x, b - near.y);
+    }
+    uint8_t* rest = to + kChunkRows * D * 2;
+    if constexpr (E == 2) {
+      *reinterpret_cast<uint32_t*>(to + at) = hi[0];
+      *reinterpret_cast<uint32_t*>(rest + at) = lo[0];
+    } else if constexpr (E == 4) {
+      *reinterpret_cast<uint2*>(to + at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(rest + at) = make_uint2(lo[0], lo[1]);
+    } else {
+      *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(rest + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ ChunkParams p) {
+  constexpr int TT = dense_tile(D);
+  __shared__ uint32_t s_row[TT];
+  __shared__ int s_tier[TT], s_bad[TT];
+  __shared__ float s_max[8];
+  __shared__ uint16_t tables[KVQ_MAX_TIERS][2][16];
+  grid_wait();
+  grid_release();
+  if (threadIdx.x < KVQ_MAX_TIERS * 2 * 16) {
+    const int tier = threadIdx.x / 32, side = threadIdx.x / 16 % 2, code = threadIdx.x % 16;
+    float c = 0.f;
+    if (tier < p.num_tiers && p.tier[tier].v_fmt == KVQ_FMT_CODEBOOK) {
+      const ChunkTier& t = p.tier[tier];
+      if (code < 1 << (side ? t.v_bits : t.k_bits)) c = __ldg((side ? t.v_cent : t.k_cent) + code) * p.head->beta[tier][side];
+    }
+    tables[tier][side][code] = __half_as_ushort(__float2half_rn(c));
+  }
+  __syncthreads();
+  const int tiles = p.head->num_tiles * p.hkv, items = tiles + p.head->units[0] * p.hkv;
+  for (int x = blockIdx.x; x < items; x += gridDim.x) {
+    if (x < tiles) unpack_tile<D>(p, x / p.hkv, x % p.hkv, tables, s_row, s_tier, s_bad, s_max);
+    else rotate_queries<D>(p, (x - tiles) / p.hkv, (x - tiles) % p.hkv);
+  }
+}
+
+// ------------------------------------------------------------------------ attention
+// Half a tile's weights may sum to this before m is raised (the largest fp16 is 2^16), and m is then this far
+// below the largest score.
+constexpr float kMostWeight = 32768.0f, kHeadroom = 2.0f;
+constexpr float kNothing = -1e30f;  // m before any token is seen: finite, so that hidden scores (-inf) weigh 0
+
+template <int D>
+struct Shape {
+  static constexpr int TT = dense_tile(D), RT = dense_blocks(D);
+  static constexpr int kQBytes = 2 * kChunkRows * D * 2;  // a row block's queries, both parts
+  static constexpr int kTileBytes = TT * D * 2;
+  static constexpr int kBuffers = D == 64 ? 6 : 3;
+  static constexpr int kNormStages = (kBuffers + 2) / 2;  // a stage is free before the keys that need it are loaded
+  static constexpr int kOffRing = RT * kQBytes, kOffNorm = kOffRing + kBuffers * kTileBytes;
+  static constexpr int kNormBytes = 2 * TT * 4;
+  static constexpr int kOffCtl = kOffNorm + kNormStages * kNormBytes;
+  static constexpr int kSmem = kOffCtl + 512;
+  static constexpr int kThreads = RT * 128 + 64;
+  // TMEM: two blocks of scores, then the accumulators
+  static constexpr int kAccAt = 2 * TT, kColumns = D == 64 ? 512 : 512;
+  static_assert(kAccAt + RT * D <= kColumns, "tensor memory");
+  static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+};
+
+enum { A_FULL = 0, A_EMPTY = 6, A_Q = 12, A_S = 13, A_P = 15, A_O = 17, A_DONE = 18, A_N = 19, A_COUNT = 23 };
+struct AttendCtl {
+  unsigned long long bars[A_COUNT];
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// An accumulator row times f.
+template <int D>
+__device__ __forceinline__ void scale_row(uint32_t at, float f) {
+  uint32_t v[16];
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    tc_ld16(at + c, v);
+    tc_wait_ld(v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+    tc_st16(at + c, v);
+  }
+}
+
+// Bits c .. c + 31 of the columns below n.
+__device__ __forceinline__ uint32_t below(int n, int c) {
+  n -= c;
+  return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// 32 scores -> 16 weight pairs and their sum.  HIDE: columns that are not in `see` weigh nothing, whatever they hold.
+template <bool CODES, bool HIDE>
+__device__ __forceinline__ void weigh(const uint32_t (&v)[32], uint32_t see, float m, const float* kn, const float* vn,
+                                      uint32_t* h, unsigned long long& s0, unsigned long long& s1) {
+  const unsigned long long neg = pack2(-m, -m);
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    unsigned long long t0 = pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+    unsigned long long t1 = pack2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+    if constexpr (CODES) {  // scores are multiplied by the keys' norms
+      const float4 n = *reinterpret_cast<const float4*>(kn + e);
+      t0 = fma2(t0, pack2(n.x, n.y), neg);
+      t1 = fma2(t1, pack2(n.z, n.w), neg);
+    } else {
+      t0 = add2(t0, neg);
+      t1 = add2(t1, neg);
+    }
+    const float2 x = unpack2(t0), y = unpack2(t1);
+    float a0 = ex2(x.x), a1 = ex2(x.y), a2 = ex2(y.x), a3 = ex2(y.y);
+    if constexpr (HIDE) {
+      a0 = see >> e & 1u ? a0 : 0.f;
+      a1 = see >> (e + 1) & 1u ? a1 : 0.f;
+      a2 = see >> (e + 2) & 1u ? a2 : 0.f;
+      a3 = see >> (e + 3) & 1u ? a3 : 0.f;
+    }
+    if constexpr (CODES) {
+      s0 = add2(s0, pack2(a0, a1));
+      s1 = add2(s1, pack2(a2, a3));
+      const float4 n = *reinterpret_cast<const float4*>(vn + e);
+      a0 *= n.x;
+      a1 *= n.y;
+      a2 *= n.z;
+      a3 *= n.w;
+      if constexpr (HIDE) {  // (a norm may be infinite)
+        a0 = see >> e & 1u ? a0 : 0.f;
+        a1 = see >> (e + 1) & 1u ? a1 : 0.f;
+        a2 = see >> (e + 2) & 1u ? a2 : 0.f;
+        a3 = see >> (e + 3) & 1u ? a3 : 0.f;
+      }
+    }
+    h[e / 2] = half2_bits(a0, a1);
+    h[e / 2 + 1] = half2_bits(a2, a3);
+    if constexpr (!CODES) {  // the sum of what is multiplied: a token that outweighs all others keeps its value
+      const float2 u = unpack_half2(h[e / 2]), w = unpack_half2(h[e / 2 + 1]);
+      s0 = add2(s0, pack2(u.x, u.y));
+      s1 = add2(s1, pack2(w.x, w.y));
+    }
+  }
+}
+
+template <int D, bool CODES>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __grid_constant__ ChunkParams p) {
+  using X = Shape<D>;
+  constexpr int TT = X::TT, RT = X::RT;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t smem = smem_u32(smem_raw);
+  AttendCtl* ctl = reinterpret_cast<AttendCtl*>(smem_raw + X::kOffCtl);
+  volatile int* abort = &ctl->abort;
+  const uint32_t bars = smem + X::kOffCtl;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);
+  grid_wait();
+  grid_release();
+  const int num = p.head->items[0];
+  // longer items first; all heads of one unit, or (keys and values beyond L2) all units of one head side by side
+  const bool by_head = (size_t)p.head->num_tiles * p.hkv * (2 * X::kTileBytes) > ((size_t)64 << 20);
+  const int at = by_head ? (int)blockIdx.x % max(1, num) : (int)blockIdx.x / p.hkv;
+  const int h = by_head ? (int)blockIdx.x / max(1, num) : (int)blockIdx.x % p.hkv;
+  if (at >= num || h >= p.hkv) return;
+  const ChunkItem item = p.item[0][num - 1 - at];
+  const ChunkSeq& s = p.seq[item.seq];
+  const int n = item.count;
+  int* err = &p.head->err;
+  const int rows = s.tokens << p.group_shift;
+  const int blocks = RT == 2 && item.row0 + kChunkRows < rows ? 2 : 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < X::kBuffers; ++i) {
+      bar_init(bars + 8 * (A_FULL + i), 1);
+      bar_init(bars + 8 * (A_EMPTY + i), 1);
+    }
+    bar_init(bars + 8 * A_Q, 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(bars + 8 * (A_S + i), 1);
+      bar_init(bars + 8 * (A_P + i), 128);
+    }
+    for (int i = 0; i < X::kNormStages; ++i) bar_init(bars + 8 * (A_N + i), 1);
+    bar_init(bars + 8 * A_O, 1);
+    bar_init(bars + 8 * A_DONE, 1);
+    ctl->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == RT * 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem)), "n"(X::kColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+
+  if (warp < RT * 4) {
+    // ---- softmax: a thread a row
+    const int w = warp >> 2, r = threadIdx.x & 127;
+    if (w < blocks) {
+      const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t o_at = lane_base + X::kAccAt + w * D;
+      const int row = min(item.row0 + w * kChunkRows + r, rows - 1);
+      const int pos = s.len - s.tokens + (row >> p.group_shift);
+      const int from = p.window ? pos - p.window + 1 : 0;
+      float m = kNothing;
+      unsigned long long l2 = 0;
+      bool ok = true;
+      const float* tops = CODES ? p.top + h : nullptr;
+      auto tile_of = [&](int i) {  // of the sequence's unpacked tiles
+        const int x = item.first + i;
+        return x < item.sinks ? x : item.begin + x - item.sinks;
+      };
+      float top = 1.f, next_top = 1.f;
+      if (CODES) next_top = __ldg(tops + (size_t)(s.tile0 + tile_of(0)) * p.hkv);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int x = tile_of(i), start = (x < s.sink_tiles ? x : s.window_tile + x - s.sink_tiles) * TT;
+        const int b = RT == 2 ? w : i & 1;
+        const uint32_t s_at = lane_base + b * TT;
+        const float* kn = reinterpret_cast<const float*>(smem_raw + X::kOffNorm + i % X::kNormStages * X::kNormBytes);
+        const float* vn = kn + TT;
+        top = next_top;
+        if (CODES && i + 1 < n) next_top = __ldg(tops + (size_t)(s.tile0 + tile_of(i + 1)) * p.hkv);
+        // columns below `end`, and from `begin` on or below `first`
+        const int end = pos + 1 - start, begin = from - start, first = p.sinks - start;
+        const bool all = __all_sync(0xFFFFFFFFu, end >= TT && (begin <= 0 || first >= TT));
+        ok = bar_wait(bars + 8 * (A_S + b), (RT == 2 ? i : i >> 1) & 1, abort, err);
+        if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+        tc_fence_after();
+        if (CODES) {
+          ok = bar_wait(bars + 8 * (A_N + i % X::kNormStages), (i / X::kNormStages) & 1, abort, err);
+          if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+        }
+        auto see = [&](int c) { return below(end, c) & (~below(begin, c) | below(first, c)); };
+        uint32_t g[TT / 2];
+        unsigned long long sum;
+#pragma unroll 1
+        for (int again = 0;; ++again) {
+          unsigned long long s0 = 0, s1 = 0;
+          uint32_t va[32], vb[32];
+          tc_ld32(s_at, va);
+#pragma unroll
+          for (int c = 0; c < TT; c += 64) {
+            tc_wait_ld(va);
+            tc_ld32(s_at + c + 32, vb);
+            if (all) weigh<CODES, false>(va, 0, m, kn + c, vn + c, g + c / 2, s0, s1);
+            else weigh<CODES, true>(va, see(c), m, kn + c, vn + c, g + c / 2, s0, s1);
+            tc_wait_ld(vb);
+            if (c + 64 < TT) tc_ld32(s_at + c + 64, va);
+            if (all) weigh<CODES, false>(vb, 0, m, kn + c + 32, vn + c + 32, g + c / 2 + 16, s0, s1);
+            else weigh<CODES, true>(vb, see(c + 32), m, kn + c + 32, vn + c + 32, g + c / 2 + 16, s0, s1);
+          }
+          sum = add2(s0, s1);
+          const float2 t = unpack2(sum);
+          // All weights are positive: a sum of at most kMostWeight says that none is too large for fp16 either.  Only
+          // where it is exceeded (always at first) m is raised and the tile, still in TMEM, weighed again.
+          if (again || __all_sync(0xFFFFFFFFu, (t.x + t.y) * top <= kMostWeight)) break;
+          const float head = kHeadroom - (float)((int)(__float_as_uint(top) >> 23) - 127);
+          float mx = m;
+#pragma unroll 1
+          for (int c = 0; c < TT; c += 16) {
+            uint32_t y[16];
+            tc_ld16(s_at + c, y);
+            tc_wait_ld(y);
+            const uint32_t sees = see(c);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (sees >> e & 1u) mx = fmaxf(mx, __uint_as_float(y[e]) * (CODES ? kn[c + e] : 1.f) - head);
+          }
+          const float f = ex2(m - mx);
+          m = mx;
+          const float2 ll = unpack2(l2);
+          l2 = pack2(ll.x * f, ll.y * f);
+          if (i > 0) {
+            // (with two row blocks the products of earlier tiles precede these scores; with one they may still run)
+            if (RT == 1 && !__all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * A_O, (i - 1) & 1, abort, err))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            scale_row<D>(o_at, f);
+          }
+        }
+        if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+        l2 = add2(l2, sum);
+#pragma unroll
+        for (int c = 0; c < TT / 2; c += 16) {  // over the scores
+          uint32_t part[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) part[e] = g[c + e];
+          tc_st16(s_at + c, part);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        bar_arrive(bars + 8 * (A_P + b));
+      }
+      // all products are complete
+      if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * A_DONE, 0, abort, err));
+      tc_fence_after();
+      const bool there = item.row0 + w * kChunkRows + r < rows;
+      const size_t part = ((size_t)(item.part + w) * p.hkv + h) * kChunkRows + r;
+      if (ok) {
+        const float unit = CODES ? p.unit_of[(size_t)item.seq * p.hkv + h] : 1.f;
+        float* to = p.acc + part * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t v[32];
+          tc_ld32(o_at + c, v);
+          tc_wait_ld(v);
+          if (there) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              float y[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(v[e + k]) * unit;
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + c + e),
+                           "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+                           : "memory");
+            }
+          }
+        }
+      }
+      if (there) {
+        // (a row of NaN has no maximum: its partial must not pass for one without tokens)
+        const float l = unpack2(l2).x + unpack2(l2).y;
+        p.ml[part] = ok && l != 0.f ? make_float2(l == l ? m : l, l) : make_float2(-INFINITY, 0.f);
+      }
+    }
+  } else if (warp == RT * 4) {
+    // ---- products: the whole warp walks, one lane issues
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    constexpr uint32_t kIdescS = (1u << 4) | ((TT >> 3) << 17) | ((kChunkRows >> 4) << 24);
+    constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((D >> 3) << 17) | ((kChunkRows >> 4) << 24);
+    const uint64_t qd = desc_at(desc_base(16, 1024), smem), kd = desc_at(desc_base(16, 1024), smem + X::kOffRing);
+    const uint64_t vd = desc_at(desc_base(TT * 128, 1024), smem + X::kOffRing);
+    auto well = [&](uint32_t bar, uint32_t parity) -> bool {
+      return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, abort, err));
+    };
+    auto full = [&](int load) { return well(bars + 8 * (A_FULL + load % X::kBuffers), (load / X::kBuffers) & 1); };
+    auto scores = [&](int block, int i, int buffer) {  // of row block `block` and tile i
+      const uint64_t b = kd + ((2 * i) % X::kBuffers) * (X::kTileBytes >> 4);
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        const uint64_t a = qd + ((block * X::kQBytes + part * (X::kQBytes / 2)) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(tm + buffer * TT, a + (((kk >> 2) * (kChunkRows * 128) + (kk & 3) * 32) >> 4),
+                 b + (((kk >> 2) * (TT * 128) + (kk & 3) * 32) >> 4), kIdescS, part + kk > 0);
+      }
+      tc_commit(bars + 8 * (A_S + buffer));
+    };
+    auto values = [&](int block, int i, int buffer) {
+      const uint64_t b = vd + ((2 * i + 1) % X::kBuffers) * (X::kTileBytes >> 4);
+#pragma unroll
+      for (int kk = 0; kk < TT / 16; ++kk)
+        mma_ts(tm + X::kAccAt + block * D, tm + buffer * TT + kk * 8, b + ((kk * 2048) >> 4), kIdescO, i > 0 || kk > 0);
+    };
+    auto free_buffer = [&](int load) { tc_commit(bars + 8 * (A_EMPTY + load % X::kBuffers)); };
+    bool ok = well(bars + 8 * A_Q, 0) && full(0);
+    if (ok) {
+      tc_fence_after();
+      if (elect_one()) {
+        for (int b = 0; b < blocks; ++b) scores(b, 0, b);
+        free_buffer(0);
+      }
+      __syncwarp();
+    }
+    for (int i = 0; i < n && ok; ++i) {
+      const bool more = i + 1 < n;
+      if constexpr (RT == 2) {
+        for (int b = 0; b < blocks && ok; ++b) {
+          if (b == 0) ok = full(2 * i + 1);
+          ok = ok && well(bars + 8 * (A_P + b), i & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            values(b, i, b);
+            if (b + 1 == blocks) free_buffer(2 * i + 1);
+          }
+          __syncwarp();
+          if (!more) continue;
+          if (b == 0 && !(ok = full(2 * i + 2))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            scores(b, i + 1, b);
+            if (b + 1 == blocks) free_buffer(2 * i + 2);
+          }
+          __syncwarp();
+        }
+      } else {
+        if (more) {
+          if (!(ok = full(2 * i + 2))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            scores(0, i + 1, (i + 1) & 1);
+            free_buffer(2 * i + 2);
+          }
+          __syncwarp();
+        }
+        ok = full(2 * i + 1) && well(bars + 8 * (A_P + (i & 1)), (i >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          values(0, i, i & 1);
+          free_buffer(2 * i + 1);
+          tc_commit(bars + 8 * A_O);
+        }
+        __syncwarp();
+      }
+    }
+    // everything issued is over before tensor memory and the operands go
+    if (elect_one()) tc_commit(bars + 8 * A_DONE);
+    __syncwarp();
+    for (int i = 0; i < 1 << 22 && !bar_try(bars + 8 * A_DONE, 0); ++i) {
+    }
+  } else {
+    // ---- loads, one lane
+    int issued = 0;
+    if ((threadIdx.x & 31) == 0) {
+      const uint32_t q_bytes = blocks * X::kQBytes;
+      const uint8_t* q = p.qt + ((size_t)(s.unit0 + item.row0 / (kChunkRows * RT)) * p.hkv + h) * (RT * X::kQBytes);
+      bar_expect(bars + 8 * A_Q, q_bytes);
+      bulk_load(smem, q, q_bytes, bars + 8 * A_Q);
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i) {
+        const int x = item.first + i;
+        const size_t tile = (size_t)(s.tile0 + (x < item.sinks ? x : item.begin + x - item.sinks)) * p.hkv + h;
+        for (int side = 0; side < 2 && ok; ++side) {
+          const int load = 2 * i + side, slot = load % X::kBuffers, turn = load / X::kBuffers;
+          if (turn > 0 && !(ok = bar_wait(bars + 8 * (A_EMPTY + slot), (turn - 1) & 1, abort, err))) break;
+          const uint32_t bar = bars + 8 * (A_FULL + slot);
+          bar_expect(bar, X::kTileBytes);
+          bulk_load(smem + X::kOffRing + slot * X::kTileBytes, (side ? p.vt : p.kt) + tile * X::kTileBytes, X::kTileBytes, bar);
+          if (CODES && side == 0) {  // (a stage's norms have been read: the keys' buffer waits for later products)
+            const uint32_t to = smem + X::kOffNorm + i % X::kNormStages * X::kNormBytes, nbar = bars + 8 * (A_N + i % X::kNormStages);
+            bar_expect(nbar, X::kNormBytes);
+            bulk_load(to, p.kn + tile * TT, TT * 4, nbar);
+            bulk_load(to + TT * 4, p.vn + tile * TT, TT * 4, nbar);
+          }
+          issued = load + 1;
+        }
+      }
+      // no copy is under way when the block ends
+      for (int i = 0; i < 1 << 22 && !bar_try(bars + 8 * A_Q, 0); ++i) {
+      }
+      for (int i = max(0, (issued + 1) / 2 - X::kNormStages); CODES && i < (issued + 1) / 2; ++i)
+        for (int k = 0; k < 1 << 22 && !bar_try(bars + 8 * (A_N + i % X::kNormStages), (i / X::kNormStages) & 1); ++k) {
+        }
+      for (int load = max(0, issued - X::kBuffers); load < issued; ++load)
+        for (int i = 0; i < 1 << 22 && !bar_try(bars + 8 * (A_FULL + load % X::kBuffers), (load / X::kBuffers) & 1); ++i) {
+        }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == RT * 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(X::kColumns));
+}
+
+template <int D, bool CODES>
+cudaError_t launch_attend(const ChunkParams& p, cudaStream_t stream) {
+  auto kern = attend_kernel<D, CODES>;
+  static std::atomic<bool> configured[64];  // shared-memory limit raised on this device (a racing second raise is
+                                            // harmless)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    configured[dev].store(true, std::memory_order_relaxed);
+  }
+  const long long grid = (long long)p.max_items[0] * p.hkv;
+  return launch_dependent(reinterpret_cast<const void*>(kern), (unsigned)grid, Shape<D>::kThreads, Shape<D>::kSmem, p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_prepare(const ChunkParams& p, cudaStream_t stream) {
+  const long long items = ((long long)p.max_tiles + p.max_units[0]) * p.hkv;
+  const unsigned grid = (unsigned)std::max(1LL, std::min(items, p.sms * 8LL));
+  const void* k = p.head_dim == 64    ? reinterpret_cast<const void*>(prepare_kernel<64>)
+                  : p.head_dim == 128 ? reinterpret_cast<const void*>(prepare_kernel<128>)
+                                      : reinterpret_cast<const void*>(prepare_kernel<256>);
+  return launch_dependent(k, grid, kPrepareThreads, 0, p, stream);
+}
+
+cudaError_t launch_chunk_dense(const ChunkParams& p, cudaStream_t stream) {
+  if (p.head_dim == 64) return p.codes ? launch_attend<64, true>(p, stream) : launch_attend<64, false>(p, stream);
+  if (p.head_dim == 128) return p.codes ? launch_attend<128, true>(p, stream) : launch_attend<128, false>(p, stream);
+  return p.codes ? launch_attend<256, true>(p, stream) : launch_attend<256, false>(p, stream);
+}
+
+}  // namespace kvq
