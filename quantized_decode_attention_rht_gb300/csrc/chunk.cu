@@ -5,6 +5,7 @@
 #include "api_checks.cuh"
 #include "chunk.cuh"
 #include "rope.cuh"
+#include "window.cuh"
 
 namespace kvq {
 namespace {
@@ -186,9 +187,16 @@ KVQ_API kvq_status kvq_chunk_attention(const kvq_tier_view* tiers, int32_t num_t
                    workspace, workspace_bytes, status, static_cast<cudaStream_t>(stream));
 }
 
+// One token a sequence runs on the decode kernels where their plan allows it, else as a chunk call.
 KVQ_API kvq_status kvq_decode_window_workspace_size(const kvq_tier_view* tiers, int32_t num_tiers, int32_t batch,
                                                     int32_t num_q_heads, const kvq_visible* visible, size_t* bytes) {
-  return chunk_size({tiers, num_tiers, batch, batch, num_q_heads, false, visible}, bytes);
+  const ChunkCall c = {tiers, num_tiers, batch, batch, num_q_heads, false, visible};
+  if (!bytes) return KVQ_ERR_INVALID_ARGUMENT;
+  ChunkParams p;
+  const kvq_status st = chunk_plan(c, &p);
+  if (st != KVQ_OK) return st;
+  if (!window_plan(tiers, num_tiers, batch, num_q_heads, p.window, p.sinks, bytes)) *bytes = chunk_layout(&p, nullptr);
+  return KVQ_OK;
 }
 
 KVQ_API kvq_status kvq_decode_attention_window(const kvq_tier_view* tiers, int32_t num_tiers, const uint16_t* q,
@@ -198,7 +206,20 @@ KVQ_API kvq_status kvq_decode_attention_window(const kvq_tier_view* tiers, int32
   const ChunkCall c = {tiers, num_tiers, batch, batch, num_q_heads, false, visible};
   const int64_t d = tiers && num_tiers > 0 && tiers[0].cache ? tiers[0].cache->head_dim : 0;
   const kvq_heads h = {q, out, num_q_heads, num_q_heads * d, d, num_q_heads * d, d};
-  return chunk_run(c, h, nullptr, workspace, workspace_bytes, status, static_cast<cudaStream_t>(stream));
+  ChunkParams p;
+  const kvq_status st = chunk_plan(c, &p);
+  if (st != KVQ_OK) return st;
+  size_t need;
+  if (!window_plan(tiers, num_tiers, batch, num_q_heads, p.window, p.sinks, &need))
+    return chunk_run(c, h, nullptr, workspace, workspace_bytes, status, static_cast<cudaStream_t>(stream));
+  if (status && !aligned(status, 4)) return KVQ_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return KVQ_OK;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return KVQ_ERR_INVALID_ARGUMENT;
+  if (!workspace || !aligned(workspace, 256)) return KVQ_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < need) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  const cudaError_t e = window_run(tiers, num_tiers, q, batch, num_q_heads, p.window, p.sinks, out, workspace, status,
+                                   static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(kWarps * 32) decode_tier_kernel(const DecParam
     const size_t row_base = ((size_t)phys * p.hkv + hk) * p.page_size;
     for (int s0 = 0; s0 < p.page_size; s0 += TPS) {
       const int off = s0 + gi;
-      const bool valid = slot_holds_token(lp, off, p.page_size, t_end);
+      bool valid = slot_holds_token(lp, off, p.page_size, t_end);
+      if (lp * p.page_size < T.hide_end) valid = valid && !token_hidden(__ldg(T.hidden + b), lp * p.page_size + off);
       const size_t rowid = row_base + off;
       float x[DPL], ks = 0.f;
       if (valid) Row<KF, D, DPL>::load(T.k_rows, T.k_aux, rowid, T.k_row_bytes, e0, lut_k, x, ks);
@@ -355,6 +356,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const DecPa
     for (int i = threadIdx.x; i < p.batch * p.num_tiers; i += blockDim.x) {
       const DecTier& T = p.tier[i % p.num_tiers];
       checked_len(T.seq_lens[i / p.num_tiers], T.max_pages, p.page_size, &bits);
+      if (p.more_bits) bits |= p.more_bits[i];
     }
     bits = __reduce_or_sync(0xFFFFFFFFu, bits);
     if (lane == 0) s_part[warp] = bits;  // s_part is free until the split list below
@@ -493,6 +495,16 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const DecPa
   }
   constexpr float inv_sqrt_d = inv_sqrt_dim(D);
   const int8_t* sg = p.v_signs + hk * D + lane * PER;
+  if (p.out16) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out16 + ((size_t)b * p.hq + hq) * D + lane * PER);
+#pragma unroll
+    for (int k = 0; k < PER / 2; ++k) {
+      const __half2 v = __floats2half2_rn((sg[2 * k] < 0 ? -acc[2 * k] : acc[2 * k]) * inv_sqrt_d,
+                                          (sg[2 * k + 1] < 0 ? -acc[2 * k + 1] : acc[2 * k + 1]) * inv_sqrt_d);
+      dst[k] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    return;
+  }
   float* dst = p.out + ((size_t)b * p.hq + hq) * D + lane * PER;
   if constexpr (PER % 4 == 0) {
 #pragma unroll

@@ -7,6 +7,7 @@ namespace kvq {
 
 constexpr size_t PS_TOKENS = 16;  // tokens per page on the codebook path
 
+#ifndef KVQ_CB_HIDES
 bool cb_fast_supported(int head_dim, int group, int k_fmt, int v_fmt) {
   if (group == 8)  // plain codes: the 4-head instances, two items per chunk
     return (head_dim == 128 || head_dim == 256) && v_fmt == KVQ_FMT_CODEBOOK && k_fmt == KVQ_FMT_CODEBOOK;
@@ -15,6 +16,9 @@ bool cb_fast_supported(int head_dim, int group, int k_fmt, int v_fmt) {
          (k_fmt == KVQ_FMT_CODEBOOK || k_fmt == KVQ_FMT_CODEBOOK_OUTLIER ||
           (k_fmt == KVQ_FMT_CODEBOOK_QJL && head_dim == 128));
 }
+#else
+#define launch_decode_cb launch_decode_cb_hiding
+#endif
 
 cudaError_t launch_decode_cb(const DecParams& dp, int head_dim, int* counters, cudaStream_t stream,
                              bool after_split_k) {
@@ -44,6 +48,8 @@ cudaError_t launch_decode_cb(const DecParams& dp, int head_dim, int* counters, c
     p.t.v_norm = t.v_aux;
     p.t.block_table = t.block_table;
     p.t.seq_lens = t.seq_lens;
+    p.t.hidden = t.hidden;
+    p.t.hide_end = t.hide_end;
     p.t.num_pages = t.num_pages;
     p.t.max_pages = t.max_pages;
     p.t.chunk = t.chunk;

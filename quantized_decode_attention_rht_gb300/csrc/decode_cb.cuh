@@ -58,8 +58,21 @@
 
 #include "kvq_internal.cuh"
 
+// The kernel is compiled twice: as it is, and (KVQ_CB_HIDES) with the mask of a window's decode, in a namespace of
+// its own, which would cost the plain one registers (up to 44 bytes of spills in instances at their limit).
+#ifdef KVQ_CB_HIDES
+#define cbk cbk_hiding
+#endif
+
 namespace kvq {
 namespace cbk {
+
+#ifdef KVQ_CB_HIDES
+constexpr bool kHides = true;
+#else
+constexpr bool kHides = false;
+#endif
+
 
 constexpr int PS = 16;
 constexpr unsigned kFull = 0xFFFFFFFFu;
@@ -222,6 +235,8 @@ struct CbTier {
   const int32_t* seq_lens;
   int* err;  // the call's error word (KVQ_DEVERR_* bits)
   int num_pages, max_pages, chunk, nchunks, split_begin;
+  const int2* hidden;  // see DecTier
+  int hide_end;
 };
 
 struct CbParams {
@@ -428,6 +443,13 @@ __device__ __forceinline__ Item fetch_item(const CbParams& p, int item, int lane
 __device__ __forceinline__ int item_pages(const CbTier& T, const Item& it) {
   const int t1 = min(it.len, it.t0 + T.chunk);
   return t1 > it.t0 ? (t1 + PS - 1) / PS - it.t0 / PS : 0;
+}
+
+// Tokens t and t + 8 of sequence b that a window hides.
+__device__ __forceinline__ void hide(const CbTier& T, int b, int t, bool& v0, bool& v1) {
+  const int2 h = __ldg(T.hidden + b);
+  v0 = v0 && !token_hidden(h, t);
+  v1 = v1 && !token_hidden(h, t + 8);
 }
 
 // A warp's page stream: ring slots, their barriers, and how far it has issued and consumed.
@@ -719,7 +741,8 @@ struct Path1 {
       ++rg.consumed;
       fd.top_up(rg);
       const int tok0 = (pg0 + i) * PS;
-      const bool v0 = tok0 + t < t1, v1 = tok0 + t + 8 < t1;
+      bool v0 = tok0 + t < t1, v1 = tok0 + t + 8 < t1;
+      if (kHides && tok0 < p.t.hide_end) hide(p.t, it.b, tok0 + t, v0, v1);
       // ---- scores of tokens t and t+8
       u64 s[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -938,6 +961,7 @@ struct Path1W {
 #pragma unroll
       for (int r = 0; r < TPL; ++r) {
         val[r] = tok0 + t + TS * r < t1;
+        if (kHides && tok0 < p.t.hide_end) val[r] = val[r] && !token_hidden(__ldg(p.t.hidden + it.b), tok0 + t + TS * r);
         x[r] = val[r] ? x[r] : -INFINITY;
         mt = fmaxf(mt, x[r]);
       }
@@ -1206,7 +1230,8 @@ struct PathM {
         mma16816(sa[1], al, qf[ks][0], qf[ks][1]);
       }
       const int tok0 = (pg0 + i) * PS;
-      const bool v0 = tok0 + g < t1, v1 = tok0 + g + 8 < t1;
+      bool v0 = tok0 + g < t1, v1 = tok0 + g + 8 < t1;
+      if (kHides && tok0 < p.t.hide_end) hide(p.t, it.b, tok0 + g, v0, v1);
       float x0 = ((sa[0][0] + sa[0][1]) + (sa[1][0] + sa[1][1])) *
                  (__half2float(__ushort_as_half((uint16_t)nk0)) * sscale);
       float x1 = ((sa[0][2] + sa[0][3]) + (sa[1][2] + sa[1][3])) *

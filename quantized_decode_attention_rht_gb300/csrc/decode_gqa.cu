@@ -151,6 +151,8 @@ struct GqaTier {
   int far;    // 1: fp8 K + INT4-g32 V; 0: fp16 K + fp16 V
   int first;  // tier 0 of the call (the near tier of spike detection)
   int max_pages, chunk, nchunks, split_begin, item_begin;
+  const int2* hidden;  // see DecTier
+  int hide_end;
 };
 
 struct GqaParams {
@@ -317,7 +319,7 @@ struct Far {
 
   // WIDE: the weights go without the 2^8 and the levels with it, which fp16 holds exactly.
   template <bool WIDE>
-  __device__ static void page(const uint8_t* st, int nvalid, const uint32_t (&qf)[8][2], State& s, int lane,
+  __device__ static void page(const uint8_t* st, int nvalid, uint32_t hide, const uint32_t (&qf)[8][2], State& s, int lane,
                               bool track, bool gate, bool live) {
     const int g = lane >> 2, c = lane & 3;
     const uint32_t s0 = smem_addr(st);
@@ -338,7 +340,7 @@ struct Far {
     float x0 = ((sa[0][0] + sa[0][1]) + (sa[1][0] + sa[1][1])) * unq;  // token g, head c
     float x1 = ((sa[0][2] + sa[0][3]) + (sa[1][2] + sa[1][3])) * unq;  // token g + 8
     // ---- online softmax for head c over the 16 tokens
-    const bool v0 = g < nvalid, v1 = g + 8 < nvalid;
+    const bool v0 = g < nvalid && !(hide >> g & 1u), v1 = g + 8 < nvalid && !(hide >> (g + 8) & 1u);
     x0 = v0 ? x0 : -INFINITY;
     x1 = v1 ? x1 : -INFINITY;
     float mt = fmaxf(x0, x1);  // the page maximum: needed only above the running one (or for the gate)
@@ -359,8 +361,8 @@ struct Far {
     if (gate && __all_sync(kFull, !live || mt - s.m < -kGateLog2)) return;
     // ---- weights w = p * scale (x 2^8) per group for this lane's tokens (g, g+8), head c
     // (scales past the end, whatever their slots hold, are zero: a weight of 0 times NaN would be NaN)
-    if (nvalid < PS) {
-      if (lane >= nvalid && lane < PS) sts64_zero(s0 + F_S + 8 * lane);
+    if (nvalid < PS || hide) {
+      if ((lane >= nvalid || hide >> lane & 1u) && lane < PS) sts64_zero(s0 + F_S + 8 * lane);
       __syncwarp();
     }
     const uint2 sc0 = lds64(s0 + F_S + 8 * g), sc1 = lds64(s0 + F_S + 8 * (g + 8));
@@ -515,7 +517,7 @@ struct Near {
   }
 
   template <bool>
-  __device__ static void page(const uint8_t* st, int nvalid, const uint32_t (&qf)[8][2], State& s, int lane,
+  __device__ static void page(const uint8_t* st, int nvalid, uint32_t hide, const uint32_t (&qf)[8][2], State& s, int lane,
                               bool track, bool gate, bool live) {
     const int g = lane >> 2, c = lane & 3;
     const uint32_t s0 = smem_addr(st);
@@ -532,7 +534,7 @@ struct Near {
     constexpr float unq = 1.0f / kQScale;
     float x0 = ((sa[0][0] + sa[0][1]) + (sa[1][0] + sa[1][1])) * unq;
     float x1 = ((sa[0][2] + sa[0][3]) + (sa[1][2] + sa[1][3])) * unq;
-    const bool v0 = g < nvalid, v1 = g + 8 < nvalid;
+    const bool v0 = g < nvalid && !(hide >> g & 1u), v1 = g + 8 < nvalid && !(hide >> (g + 8) & 1u);
     x0 = v0 ? x0 : -INFINITY;
     x1 = v1 ? x1 : -INFINITY;
     float mt = fmaxf(x0, x1);  // the page maximum: needed only above the running one (or for the gate)
@@ -568,6 +570,11 @@ struct Near {
     // rows past the end, whatever their slots hold, are zero: a weight of 0 times NaN would be NaN
     if (nvalid < PS) {
       for (int i = 16 * nvalid + lane; i < 16 * PS; i += 32) sts128_zero(s0 + N_V + (i >> 4) * N_VSTR + (i & 15) * 16);
+      __syncwarp();
+    }
+    if (hide) {
+      for (int i = lane; i < 16 * PS; i += 32)
+        if (hide >> (i >> 4) & 1u) sts128_zero(s0 + N_V + (i >> 4) * N_VSTR + (i & 15) * 16);
       __syncwarp();
     }
     // ---- values: ldmatrix.trans gives V^T[16 coordinates x 16 tokens] fragments
@@ -614,8 +621,8 @@ __device__ __noinline__ void empty_partial(const GqaParams& p, const GqaTier& T,
   }
 }
 
-// One work item: pages [t0, t1) of sequence b, kv head hk in tier T.
-template <class TT>
+// One work item: pages [t0, t1) of sequence b, kv head hk in tier T.  HIDES: the tier has hidden tokens.
+template <class TT, bool HIDES>
 __device__ __forceinline__ void run_item(const GqaParams& p, const GqaTier& T, int b, int hk, int h0, int chunk,
                                          int t0, int t1, uint8_t* wsm, int lane, bool track) {
   const int g = lane >> 2, c = lane & 3;
@@ -656,7 +663,12 @@ __device__ __forceinline__ void run_item(const GqaParams& p, const GqaTier& T, i
       __syncwarp();
       const int slot = i % TT::S;
       const int nvalid = min(PS, t1 - (pg0 + i) * PS);
-      TT::template page<decltype(wide)::value>(wsm + slot * TT::STAGE, nvalid, qf, st, lane, track, p.gate != 0,
+      uint32_t hide = 0;  // tokens of the page that a window hides
+      if (HIDES && (pg0 + i) * PS < T.hide_end) {
+        const int2 h = __ldg(T.hidden + b);
+        hide = __ballot_sync(kFull, lane < PS && token_hidden(h, (pg0 + i) * PS + lane));
+      }
+      TT::template page<decltype(wide)::value>(wsm + slot * TT::STAGE, nvalid, hide, qf, st, lane, track, p.gate != 0,
                                                c < p.igroup);
       __syncwarp();
       if (i + TT::S < npg) TT::issue(T, pl, btab[i + TT::S], hk, p.hkv, ring + slot * TT::STAGE, lane);
@@ -677,6 +689,7 @@ __device__ __forceinline__ void run_item(const GqaParams& p, const GqaTier& T, i
   __syncwarp();
 }
 
+template <bool HIDES>
 __global__ void __launch_bounds__(kWarps * 32, 1) decode_gqa_kernel(const __grid_constant__ GqaParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -706,8 +719,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_gqa_kernel(const __grid
     if (t0 < len) {
       const int t1 = min(len, t0 + T.chunk);
       const bool track = p.spike && T.first;
-      if (T.far) run_item<Far>(p, T, b, hk, 4 * half, chunk, t0, t1, wsm, lane, track);
-      else run_item<Near>(p, T, b, hk, 4 * half, chunk, t0, t1, wsm, lane, track);
+      if (T.far) run_item<Far, HIDES>(p, T, b, hk, 4 * half, chunk, t0, t1, wsm, lane, track);
+      else run_item<Near, HIDES>(p, T, b, hk, 4 * half, chunk, t0, t1, wsm, lane, track);
     }
     item = __shfl_sync(kFull, next, 0);
   }
@@ -735,13 +748,14 @@ cudaError_t launch_decode_gqa(const DecParams& dp, int* counter, cudaStream_t st
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(decode_gqa_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    for (const auto kern : {decode_gqa_kernel<false>, decode_gqa_kernel<true>})
+      if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     configured[dev].store(true, std::memory_order_relaxed);
   }
   GqaParams p;
   memset(&p, 0, sizeof(p));
   int items = 0, n = 0;
+  bool hides = false;
   for (int i = 0; i < dp.num_tiers; ++i) {
     const DecTier& t = dp.tier[i];
     if (t.kind != TIER_GQA) continue;
@@ -753,6 +767,9 @@ cudaError_t launch_decode_gqa(const DecParams& dp, int* counter, cudaStream_t st
     g.block_table = t.block_table;
     g.seq_lens = t.seq_lens;
     g.num_pages = t.num_pages;
+    g.hidden = t.hidden;
+    hides = hides || t.hidden;
+    g.hide_end = t.hide_end;
     g.far = t.k_fmt == KVQ_FMT_FP8_E4M3;
     g.max_pages = t.max_pages;
     g.chunk = t.chunk;
@@ -794,7 +811,7 @@ cudaError_t launch_decode_gqa(const DecParams& dp, int* counter, cudaStream_t st
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = after ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, decode_gqa_kernel, p);
+  e = cudaLaunchKernelEx(&cfg, hides ? decode_gqa_kernel<true> : decode_gqa_kernel<false>, p);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e == cudaSuccess) note_launch();
   return e;

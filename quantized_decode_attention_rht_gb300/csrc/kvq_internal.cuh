@@ -112,7 +112,13 @@ struct DecTier {
   int kind;  // TierKind
   int num_pages;  // pages in the pool (block-table entries must lie below)
   int max_pages, split_begin, num_splits, chunk;
+  // A window's decode: tokens [x, x + y) of sequence b, (x, y) = hidden[b], are not attended; none at or beyond
+  // hide_end (0: none at all).
+  const int2* hidden;
+  int hide_end;
 };
+// Whether token t, below hide_end, is hidden.
+__device__ __forceinline__ bool token_hidden(int2 h, int t) { return (unsigned)(t - h.x) < (unsigned)h.y; }
 
 struct DecParams {
   DecTier tier[KVQ_MAX_TIERS];
@@ -121,6 +127,7 @@ struct DecParams {
   const int8_t* k_signs;
   const int8_t* v_signs;
   float* out;
+  uint16_t* out16;  // where set, the combine pass rounds to fp16 and stores here instead
   float* ws_acc;  // [B][Hq][S][D]
   float* ws_ml;   // [B][Hq][S][2]  (running max in log2 units, sum of exp2)
   float* ws_pq;   // [B][Hq][KVQ_QJL_DIM] projected queries when a tier's keys carry a sketch
@@ -128,6 +135,7 @@ struct DecParams {
   int* spike;     // [B][Hq] spike flags, or null
   int* err;       // the call's device error word (KVQ_DEVERR_* bits), zero at launch
   int* status;    // where the combine pass copies the error word, or null
+  const int* more_bits;  // [batch * num_tiers] error bits of a kernel before the split-K pass, or null
   int gate;       // score-gated value loading
   int batch, hq, hkv, page_size, total_splits;
 };
@@ -155,6 +163,9 @@ bool cb_fast_supported(int head_dim, int group, int k_fmt, int v_fmt);
 // programmatic dependents (overlapping its tail) and complete only after it.
 cudaError_t launch_decode_cb(const DecParams& p, int head_dim, int* counters, cudaStream_t stream,
                              bool after_split_k);
+// The same for tiers with hidden tokens.
+cudaError_t launch_decode_cb_hiding(const DecParams& p, int head_dim, int* counters, cudaStream_t stream,
+                                    bool after_split_k);
 cudaError_t launch_combine(const DecParams& p, int head_dim, cudaStream_t stream);
 
 // ------------------------------------------------------------------------ device helpers

@@ -175,12 +175,12 @@ def test_windows(name, d, window, sinks):
 @pytest.mark.parametrize("name,d", [("fp16", 128), ("fp8_int4", 128), ("cb4", 128), ("cb32", 128), ("cb4", 256), ("fp16", 64)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (64, 4), (1000, 1)])
 def test_decode_window(name, d, window, sinks):
-    """The decode form, and the chunk call without offsets, give the same."""
+    """The decode form, and the chunk call with one token a sequence."""
     torch, kvq = modules()
     c = Case(kvq, torch, [name], [[700, 0, 1, 65, 300]], [1] * 5, hq=8, hkv=2, d=d, window=window, sinks=sinks, seed=window)
     got = c.run(kvq, torch, decode=True)
     c.check(got)
-    assert np.array_equal(got, c.run(kvq, torch))
+    c.check(c.run(kvq, torch))
 
 
 @pytest.mark.parametrize("specs,lens", [(["fp8_int4", "fp16"], [[300, 0, 128, 7], [64, 33, 0, 1]]),
