@@ -22,6 +22,7 @@
 // columns at head_dim 128.  (head_dim 256: one row block, tiles of 64 tokens, two score blocks in turn.)
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "chunk.cuh"
 #include "rotate.cuh"
@@ -33,57 +34,98 @@ namespace {
 constexpr int kPrepareThreads = 256;
 
 // ------------------------------------------------------------------------ unpacking
-// 16 coordinates from 16 c on as fp16 pairs: values of the plain formats, table entries of codebooks.
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+
+// Formats as unpacking sees them.
+enum { U_F16, U_F8, U_I4, U_C4, U_C3, U_C2 };
+__device__ __forceinline__ int unpack_kind(int fmt, int bits) {
+  switch (fmt) {
+    case KVQ_FMT_FP16: return U_F16;
+    case KVQ_FMT_FP8_E4M3: return U_F8;
+    case KVQ_FMT_INT4_G32: return U_I4;
+    default: return bits == 4 ? U_C4 : (bits == 3 ? U_C3 : U_C2);
+  }
+}
+
+// 16 stored coordinates, from 16 c on, of a row.
+template <int F>
+struct Raw {
+  uint32_t w[F == U_F16 ? 8 : (F == U_F8 ? 4 : 2)];
+  uint16_t scale;
+};
+template <int F>
+__device__ __forceinline__ void load_raw(const uint8_t* row, const __half* scales, int c, Raw<F>& x) {
+  if constexpr (F == U_F16) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(row) + 2 * c), b = __ldg(reinterpret_cast<const uint4*>(row) + 2 * c + 1);
+    x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w, x.w[4] = b.x, x.w[5] = b.y, x.w[6] = b.z, x.w[7] = b.w;
+  } else if constexpr (F == U_F8) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(row) + c);
+    x.w[0] = a.x, x.w[1] = a.y, x.w[2] = a.z, x.w[3] = a.w;
+  } else if constexpr (F == U_I4 || F == U_C4) {
+    const uint2 a = __ldg(reinterpret_cast<const uint2*>(row) + c);
+    x.w[0] = a.x, x.w[1] = a.y;
+    if constexpr (F == U_I4) x.scale = __half_as_ushort(__ldg(scales + c / 2));
+  } else if constexpr (F == U_C3) {  // (rows of head_dim 64 are of 24 bytes)
+    const uint16_t* a = reinterpret_cast<const uint16_t*>(row) + 3 * c;
+    x.w[0] = (uint32_t)__ldg(a) | (uint32_t)__ldg(a + 1) << 16;
+    x.w[1] = __ldg(a + 2);
+  } else {
+    x.w[0] = __ldg(reinterpret_cast<const uint32_t*>(row) + c);
+    x.w[1] = 0;
+  }
+}
+// As fp16 pairs: values of the plain formats, table entries of codebooks.
+template <int F>
+__device__ __forceinline__ void decode_raw(const Raw<F>& x, const uint16_t* table, uint32_t (&h)[8], int* over) {
+  if constexpr (F == U_F16) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[k] = x.w[k];
+  } else if constexpr (F == U_F8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[k]) : "h"((uint16_t)(x.w[k / 2] >> (16 * (k & 1)))));
+  } else if constexpr (F == U_I4) {
+    const uint16_t size = x.scale & 0x7FFFu;
+    if (size >= 0x7092u && size < 0x7C00u) *over = 1;  // a finite scale above 9352: seven times it is no fp16 number
+    const uint32_t s2 = x.scale * 0x10001u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // levels n - 8, exact in fp16: 1024 + n less 1032
+      const uint32_t v = x.w[k / 4] >> (8 * (k & 3));
+      const uint32_t up = (v & 15u) | (v & 0xF0u) << 12 | 0x64006400u;
+      const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&up), __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
+      h[k] = hmul2(*reinterpret_cast<const uint32_t*>(&n), s2);
+    }
+  } else {
+    constexpr int B = F == U_C4 ? 4 : (F == U_C3 ? 3 : 2);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t e[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = (2 * k + i) * B;
+        const uint32_t f = at % 32 + B <= 32 ? x.w[at / 32] >> (at % 32) : __funnelshift_r(x.w[0], x.w[1], at % 32);
+        e[i] = table[f & ((1u << B) - 1u)];  // (16 entries lie in eight banks: no two lanes wait for one another)
+      }
+      h[k] = e[0] | e[1] << 16;
+    }
+  }
+}
+// Any format, one row.
 __device__ __forceinline__ void unpack16(int fmt, int bits, const uint8_t* row, const __half* scales, int c,
                                          const uint16_t* table, uint32_t (&h)[8], int* over) {
-  switch (fmt) {
-    case KVQ_FMT_FP16: {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(row) + 2 * c), b = __ldg(reinterpret_cast<const uint4*>(row) + 2 * c + 1);
-      h[0] = a.x, h[1] = a.y, h[2] = a.z, h[3] = a.w, h[4] = b.x, h[5] = b.y, h[6] = b.z, h[7] = b.w;
-      return;
-    }
-    case KVQ_FMT_FP8_E4M3: {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(row) + c);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[k]) : "h"((uint16_t)(w[k / 2] >> (16 * (k & 1)))));
-      return;
-    }
-    case KVQ_FMT_INT4_G32: {
-      const uint2 a = __ldg(reinterpret_cast<const uint2*>(row) + c);
-      const __half s = scales[c / 2];
-      const uint16_t sb = __half_as_ushort(s) & 0x7FFFu;
-      if (sb >= 0x7092u && sb < 0x7C00u) *over = 1;  // a finite scale above 9352: seven times it is no fp16 number
-      const __half2 s2 = __half2half2(s);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        // levels n - 8, exact in fp16: 1024 + n less 1032
-        const uint32_t v = (k < 4 ? a.x : a.y) >> (8 * (k & 3));
-        const uint32_t up = (v & 15u) | (v & 0xF0u) << 12 | 0x64006400u;
-        const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&up), __halves2half2(__ushort_as_half(0x6408), __ushort_as_half(0x6408)));
-        const __half2 x = __hmul2(n, s2);
-        h[k] = *reinterpret_cast<const uint32_t*>(&x);
-      }
-      return;
-    }
-    default: break;
-  }
-  uint64_t w;  // 16 codes
-  if (bits == 4) {
-    const uint2 a = __ldg(reinterpret_cast<const uint2*>(row) + c);
-    w = a.x | (uint64_t)a.y << 32;
-  } else if (bits == 3) {  // (rows of head_dim 64 are of 24 bytes)
-    const uint16_t* a = reinterpret_cast<const uint16_t*>(row) + 3 * c;
-    w = (uint64_t)__ldg(a) | (uint64_t)__ldg(a + 1) << 16 | (uint64_t)__ldg(a + 2) << 32;
-  } else {
-    w = __ldg(reinterpret_cast<const uint32_t*>(row) + c);
-  }
-  const uint32_t mask = (1u << bits) - 1u;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t lo = (uint32_t)(w >> (2 * k * bits)) & mask, hi = (uint32_t)(w >> ((2 * k + 1) * bits)) & mask;
-    h[k] = table[lo] | (uint32_t)table[hi] << 16;
+  auto one = [&](auto f) {
+    Raw<decltype(f)::value> x;
+    load_raw(row, scales, c, x);
+    decode_raw(x, table, h, over);
+  };
+  switch (unpack_kind(fmt, bits)) {
+    case U_F16: one(std::integral_constant<int, U_F16>{}); break;
+    case U_F8: one(std::integral_constant<int, U_F8>{}); break;
+    case U_I4: one(std::integral_constant<int, U_I4>{}); break;
+    case U_C4: one(std::integral_constant<int, U_C4>{}); break;
+    case U_C3: one(std::integral_constant<int, U_C3>{}); break;
+    default: one(std::integral_constant<int, U_C2>{});
   }
 }
 
@@ -101,6 +143,15 @@ __device__ __forceinline__ uint32_t tile_at(int rows, int r, int c) {
   return (uint32_t)(c / 64) * rows * 128 + r * 128 + ((((c / 8) & 7) ^ (r & 7)) << 4);
 }
 
+// 16 coordinates from 16 c on, which are neighbouring pieces whatever the row's swizzle: one store.
+__device__ __forceinline__ void store16(uint8_t* tile, int rows, int r, int c, const uint32_t (&x)[8]) {
+  const bool turn = r & 1;
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(tile + (tile_at(rows, r, 16 * c) & ~16u)),
+               "r"(turn ? x[4] : x[0]), "r"(turn ? x[5] : x[1]), "r"(turn ? x[6] : x[2]), "r"(turn ? x[7] : x[3]),
+               "r"(turn ? x[0] : x[4]), "r"(turn ? x[1] : x[5]), "r"(turn ? x[2] : x[6]), "r"(turn ? x[3] : x[7])
+               : "memory");
+}
+
 // The norm of a codebook token's key (side 0) or value.
 __device__ __forceinline__ float norm_of(const ChunkTier& t, int side, uint32_t row) {
   if (side) return __half2float(t.v_aux[row]);
@@ -109,8 +160,6 @@ __device__ __forceinline__ float norm_of(const ChunkTier& t, int side, uint32_t 
     return __half2float(*reinterpret_cast<const __half*>(reinterpret_cast<const uint8_t*>(t.k_aux) + (size_t)row * (4 + KVQ_OUTLIER_CHANNELS)));
   return __half2float(t.k_aux[row]);
 }
-
-constexpr uint32_t kNone = 0xFFFFFFFFu;
 
 // Tier and row in its pool of a sequence's position (row kNone: no token there, or its page outside the pool).
 __device__ __forceinline__ uint32_t find_row(const ChunkParams& p, const ChunkSeq& s, int seq, int h, int pos, int& tier, int* bits) {
@@ -125,6 +174,68 @@ __device__ __forceinline__ uint32_t find_row(const ChunkParams& p, const ChunkSe
   const int phys = __ldg(t.block_table + (size_t)seq * t.table_pages + page);
   if (!page_in_pool(phys, t.num_pages, bits)) return kNone;
   return ((uint32_t)phys * p.hkv + h) * p.page_size + (pos - page * p.page_size);  // below 2^32: the host checks
+}
+
+// A side of a tile whose tokens all lie in one tier, all of a thread's rows on their way at once.  VALUES: a row that
+// is not finite becomes zeros and is noted in s_bad; keys of such rows become NaN.
+template <int D, int F, bool VALUES>
+__device__ __forceinline__ void unpack_side(const ChunkTier& t, uint8_t* to, const uint16_t* table, const uint32_t* s_row,
+                                            int* s_bad, float factor, int* over) {
+  constexpr int TT = dense_tile(D), C = D / 16, kEach = TT * C / kPrepareThreads;
+  const uint8_t* rows = VALUES ? t.v_rows : t.k_rows;
+  const int row_bytes = VALUES ? t.v_row_bytes : t.k_row_bytes, c = threadIdx.x % C, r0 = threadIdx.x / C;
+  Raw<F> raw[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t row = s_row[r0 + i * (kPrepareThreads / C)];
+    load_raw(rows + (size_t)(row != kNone ? row : 0) * row_bytes, VALUES ? t.v_aux + (size_t)(row != kNone ? row : 0) * (D / kGroup) : nullptr,
+             c, raw[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int r = r0 + i * (kPrepareThreads / C);
+    uint32_t x[8];
+    decode_raw(raw[i], table, x, over);
+    bool zero = s_row[r] == kNone;
+    if constexpr (VALUES && (F == U_F16 || F == U_F8 || F == U_I4)) {
+      bool fine = true;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) fine = fine && half2_finite(x[k]);
+      if (!fine && !zero) s_bad[r] = 1;
+      zero = zero || !fine;
+      if (factor != 1.0f) {
+        const uint32_t f = half2_bits(factor, factor);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], f);
+      }
+    } else if constexpr (!VALUES) {
+      if (s_bad[r]) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = 0x7E007E00u;
+      }
+    }
+    if (zero) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = 0;
+    }
+    store16(to, TT, r, c, x);
+  }
+}
+template <int D, bool VALUES>
+__device__ __forceinline__ void unpack_any(const ChunkTier& t, uint8_t* to, const uint16_t* table, const uint32_t* s_row,
+                                           int* s_bad, float factor, int* over) {
+  switch (VALUES ? unpack_kind(t.v_fmt, t.v_bits) : unpack_kind(t.k_fmt, t.k_bits)) {
+    case U_F16: unpack_side<D, U_F16, VALUES>(t, to, table, s_row, s_bad, factor, over); break;
+    case U_F8:
+      if constexpr (!VALUES) unpack_side<D, U_F8, VALUES>(t, to, table, s_row, s_bad, factor, over);
+      break;
+    case U_I4:
+      if constexpr (VALUES) unpack_side<D, U_I4, VALUES>(t, to, table, s_row, s_bad, factor, over);
+      break;
+    case U_C4: unpack_side<D, U_C4, VALUES>(t, to, table, s_row, s_bad, factor, over); break;
+    case U_C3: unpack_side<D, U_C3, VALUES>(t, to, table, s_row, s_bad, factor, over); break;
+    default: unpack_side<D, U_C2, VALUES>(t, to, table, s_row, s_bad, factor, over);
+  }
 }
 
 template <int D>
@@ -170,8 +281,19 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
   const float per_unit = 1.0f / unit;
   const size_t at = ((size_t)tile * p.hkv + h) * (TT * D * 2);
   int over = 0;
+  // One tier's tokens alone, but for those that are not there, and keys without a sketch or an outlier stream?
+  const int first = s_tier[0], fmt = p.tier[first].k_fmt;
+  const bool simple = __syncthreads_and((tid >= TT || s_row[tid] == kNone || s_tier[tid] == first) && s_row[0] != kNone &&
+                                        fmt != KVQ_FMT_CODEBOOK_QJL && fmt != KVQ_FMT_CODEBOOK_OUTLIER);
+  if (simple) {
+    const ChunkTier& t = p.tier[first];
+    unpack_any<D, true>(t, p.vt + at, tables[first][1], s_row, s_bad,
+                        p.codes && t.v_fmt != KVQ_FMT_CODEBOOK ? per_unit : 1.0f, &over);
+    __syncthreads();
+    unpack_any<D, false>(t, p.kt + at, tables[first][0], s_row, s_bad, 1.0f, &over);
+  }
   // values
-  for (int u = tid; u < TT * C; u += kPrepareThreads) {
+  for (int u = tid; !simple && u < TT * C; u += kPrepareThreads) {
     const int r = u / C, c = u % C;
     uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const uint32_t row = s_row[r];
@@ -193,13 +315,11 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
         for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], *reinterpret_cast<const uint32_t*>(&f));
       }
     }
-    uint8_t* to = p.vt + at;
-    *reinterpret_cast<uint4*>(to + tile_at(TT, r, 16 * c)) = make_uint4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<uint4*>(to + tile_at(TT, r, 16 * c + 8)) = make_uint4(x[4], x[5], x[6], x[7]);
+    store16(p.vt + at, TT, r, c, x);
   }
-  __syncthreads();
+  if (!simple) __syncthreads();
   // keys
-  for (int u = tid; u < TT * C; u += kPrepareThreads) {
+  for (int u = tid; !simple && u < TT * C; u += kPrepareThreads) {
     const int r = u / C, c = u % C;
     uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const uint32_t row = s_row[r];
@@ -259,9 +379,7 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
         for (int k = 0; k < 8; ++k) x[k] = 0x7E007E00u;
       }
     }
-    uint8_t* to = p.kt + at;
-    *reinterpret_cast<uint4*>(to + tile_at(TT, r, 16 * c)) = make_uint4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<uint4*>(to + tile_at(TT, r, 16 * c + 8)) = make_uint4(x[4], x[5], x[6], x[7]);
+    store16(p.kt + at, TT, r, c, x);
   }
   if (p.codes) {
     float vn = 0.f;
@@ -337,7 +455,7 @@ __device__ __forceinline__ void rotate_queries(const ChunkParams& p, int unit, i
 }
 
 template <int D>
-__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kPrepareThreads, 4) prepare_kernel(const __grid_constant__ ChunkParams p) {
   constexpr int TT = dense_tile(D);
   __shared__ uint32_t s_row[TT];
   __shared__ int s_tier[TT], s_bad[TT];
@@ -368,13 +486,20 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
 constexpr float kMostWeight = 32768.0f, kHeadroom = 2.0f;
 constexpr float kNothing = -1e30f;  // m before any token is seen: finite, so that hidden scores (-inf) weigh 0
 
+// The order of loads.  With two row blocks keys and values take turns; with one, scores run a tile further ahead, and
+// the keys with them: K0 K1 V0 K2 V1 ...
+template <int RT>
+__device__ __forceinline__ constexpr int key_load(int i) { return RT == 2 ? 2 * i : (i ? 2 * i - 1 : 0); }
+template <int RT>
+__device__ __forceinline__ constexpr int value_load(int i, int n) { return RT == 2 ? 2 * i + 1 : (i + 1 < n ? 2 * i + 2 : 2 * i + 1); }
+
 template <int D>
 struct Shape {
   static constexpr int TT = dense_tile(D), RT = dense_blocks(D);
   static constexpr int kQBytes = 2 * kChunkRows * D * 2;  // a row block's queries, both parts
   static constexpr int kTileBytes = TT * D * 2;
   static constexpr int kBuffers = D == 64 ? 6 : 3;
-  static constexpr int kNormStages = (kBuffers + 2) / 2;  // a stage is free before the keys that need it are loaded
+  static constexpr int kNormStages = RT == 1 ? 3 : (kBuffers + 2) / 2;  // a stage is free before the keys that need it are loaded
   static constexpr int kOffRing = RT * kQBytes, kOffNorm = kOffRing + kBuffers * kTileBytes;
   static constexpr int kNormBytes = 2 * TT * 4;
   static constexpr int kOffCtl = kOffNorm + kNormStages * kNormBytes;
@@ -668,7 +793,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
     };
     auto full = [&](int load) { return well(bars + 8 * (A_FULL + load % X::kBuffers), (load / X::kBuffers) & 1); };
     auto scores = [&](int block, int i, int buffer) {  // of row block `block` and tile i
-      const uint64_t b = kd + ((2 * i) % X::kBuffers) * (X::kTileBytes >> 4);
+      const uint64_t b = kd + (key_load<RT>(i) % X::kBuffers) * (X::kTileBytes >> 4);
 #pragma unroll 1
       for (int part = 0; part < 2; ++part) {
         const uint64_t a = qd + ((block * X::kQBytes + part * (X::kQBytes / 2)) >> 4);
@@ -680,7 +805,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
       tc_commit(bars + 8 * (A_S + buffer));
     };
     auto values = [&](int block, int i, int buffer) {
-      const uint64_t b = vd + ((2 * i + 1) % X::kBuffers) * (X::kTileBytes >> 4);
+      const uint64_t b = vd + (value_load<RT>(i, n) % X::kBuffers) * (X::kTileBytes >> 4);
 #pragma unroll
       for (int kk = 0; kk < TT / 16; ++kk)
         mma_ts(tm + X::kAccAt + block * D, tm + buffer * TT + kk * 8, b + ((kk * 2048) >> 4), kIdescO, i > 0 || kk > 0);
@@ -692,6 +817,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
       if (elect_one()) {
         for (int b = 0; b < blocks; ++b) scores(b, 0, b);
         free_buffer(0);
+      }
+      __syncwarp();
+    }
+    if (RT == 1 && ok && n > 1 && (ok = full(key_load<RT>(1)))) {
+      tc_fence_after();
+      if (elect_one()) {
+        scores(0, 1, 1);
+        free_buffer(key_load<RT>(1));
       }
       __syncwarp();
     }
@@ -718,24 +851,24 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
           __syncwarp();
         }
       } else {
-        if (more) {
-          if (!(ok = full(2 * i + 2))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            scores(0, i + 1, (i + 1) & 1);
-            free_buffer(2 * i + 2);
-          }
-          __syncwarp();
-        }
-        ok = full(2 * i + 1) && well(bars + 8 * (A_P + (i & 1)), (i >> 1) & 1);
+        ok = full(value_load<RT>(i, n)) && well(bars + 8 * (A_P + (i & 1)), (i >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
           values(0, i, i & 1);
-          free_buffer(2 * i + 1);
+          free_buffer(value_load<RT>(i, n));
           tc_commit(bars + 8 * A_O);
         }
         __syncwarp();
+        if (i + 2 < n) {
+          if (!(ok = full(key_load<RT>(i + 2)))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            scores(0, i + 2, i & 1);
+            free_buffer(key_load<RT>(i + 2));
+          }
+          __syncwarp();
+        }
       }
     }
     // everything issued is over before tensor memory and the operands go
@@ -745,35 +878,36 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
     }
   } else {
     // ---- loads, one lane
-    int issued = 0;
+    int issued = 0, norms = 0;
     if ((threadIdx.x & 31) == 0) {
       const uint32_t q_bytes = blocks * X::kQBytes;
       const uint8_t* q = p.qt + ((size_t)(s.unit0 + item.row0 / (kChunkRows * RT)) * p.hkv + h) * (RT * X::kQBytes);
       bar_expect(bars + 8 * A_Q, q_bytes);
       bulk_load(smem, q, q_bytes, bars + 8 * A_Q);
       bool ok = true;
-      for (int i = 0; i < n && ok; ++i) {
-        const int x = item.first + i;
+      for (int load = 0; load < 2 * n && ok; ++load) {
+        // tile and side of this load
+        const bool value = RT == 2 ? load & 1 : (load > 0 && !(load & 1)) || load == 2 * n - 1;
+        const int i = RT == 2 ? load / 2 : (value ? (load == 2 * n - 1 ? n - 1 : load / 2 - 1) : (load + 1) / 2);
+        const int x = item.first + i, slot = load % X::kBuffers, turn = load / X::kBuffers;
         const size_t tile = (size_t)(s.tile0 + (x < item.sinks ? x : item.begin + x - item.sinks)) * p.hkv + h;
-        for (int side = 0; side < 2 && ok; ++side) {
-          const int load = 2 * i + side, slot = load % X::kBuffers, turn = load / X::kBuffers;
-          if (turn > 0 && !(ok = bar_wait(bars + 8 * (A_EMPTY + slot), (turn - 1) & 1, abort, err))) break;
-          const uint32_t bar = bars + 8 * (A_FULL + slot);
-          bar_expect(bar, X::kTileBytes);
-          bulk_load(smem + X::kOffRing + slot * X::kTileBytes, (side ? p.vt : p.kt) + tile * X::kTileBytes, X::kTileBytes, bar);
-          if (CODES && side == 0) {  // (a stage's norms have been read: the keys' buffer waits for later products)
-            const uint32_t to = smem + X::kOffNorm + i % X::kNormStages * X::kNormBytes, nbar = bars + 8 * (A_N + i % X::kNormStages);
-            bar_expect(nbar, X::kNormBytes);
-            bulk_load(to, p.kn + tile * TT, TT * 4, nbar);
-            bulk_load(to + TT * 4, p.vn + tile * TT, TT * 4, nbar);
-          }
-          issued = load + 1;
+        if (turn > 0 && !(ok = bar_wait(bars + 8 * (A_EMPTY + slot), (turn - 1) & 1, abort, err))) break;
+        const uint32_t bar = bars + 8 * (A_FULL + slot);
+        bar_expect(bar, X::kTileBytes);
+        bulk_load(smem + X::kOffRing + slot * X::kTileBytes, (value ? p.vt : p.kt) + tile * X::kTileBytes, X::kTileBytes, bar);
+        if (CODES && !value) {  // (a stage's norms have been read: the keys' buffer waits for later products)
+          const uint32_t to = smem + X::kOffNorm + i % X::kNormStages * X::kNormBytes, nbar = bars + 8 * (A_N + i % X::kNormStages);
+          bar_expect(nbar, X::kNormBytes);
+          bulk_load(to, p.kn + tile * TT, TT * 4, nbar);
+          bulk_load(to + TT * 4, p.vn + tile * TT, TT * 4, nbar);
+          norms = i + 1;
         }
+        issued = load + 1;
       }
       // no copy is under way when the block ends
       for (int i = 0; i < 1 << 22 && !bar_try(bars + 8 * A_Q, 0); ++i) {
       }
-      for (int i = max(0, (issued + 1) / 2 - X::kNormStages); CODES && i < (issued + 1) / 2; ++i)
+      for (int i = max(0, norms - X::kNormStages); i < norms; ++i)
         for (int k = 0; k < 1 << 22 && !bar_try(bars + 8 * (A_N + i % X::kNormStages), (i / X::kNormStages) & 1); ++k) {
         }
       for (int load = max(0, issued - X::kBuffers); load < issued; ++load)

@@ -58,6 +58,27 @@ __global__ void __launch_bounds__(128) narrow_kernel(const __grid_constant__ Nar
   }
 }
 
+// A window is a small cache, whose chunks the decode's plan makes too long for a full GPU: codebook tiers get 24 items
+// an SM (54 with one query head a kv head), others on the generic kernel four.  Measured (GB300), with the plan's
+// chunks and with these: 32 x 16/8 heads x 256 on 1037 tokens of 3/2-bit codes 85 and 56 us, 1 x 8 heads on 516 of
+// 4-bit 38 and 24, 8 x 32/8 heads on 1024 of 4-bit 42 and 32, 16 x 16/4 heads x 64 on 1024 42 and 30; 16 x 32 heads on
+// 2064 71 and 71.  (fp16 and fp8 tiers: no change, 64 x 32/8 heads on 4100 tokens 112 us.)
+void shorten_chunks(const kvq_tier_view* tiers, int n, int batch, int hq, Plan* plan) {
+  Plan x = *plan;
+  const int sms = device_sms(), hkv = tiers[0].cache->num_kv_heads, ps = tiers[0].cache->page_size;
+  x.total = 0;
+  for (int i = 0; i < n; ++i) {
+    const long long pages = (long long)batch * hkv * usable_pages(tiers[i]), room = (long long)usable_pages(tiers[i]) * ps;
+    long long chunk = x.chunk[i];
+    if (x.kind[i] == TIER_CB) chunk = std::min(chunk, std::max(1LL, pages / (sms * (hq == hkv ? 54LL : 24LL))) * ps);
+    if (x.kind[i] == TIER_GENERIC) chunk = std::min(chunk, std::max((64LL + ps - 1) / ps, pages / (sms * 4LL)) * ps);
+    x.chunk[i] = (int)chunk;
+    x.splits[i] = room ? (int)((room + chunk - 1) / chunk) : 0;
+    x.total += x.splits[i];
+  }
+  if (x.total <= KVQ_MAX_SPLITS) *plan = x;
+}
+
 // Tiers as the decode kernels see them, in the workspace from `base` on.
 struct Narrowed {
   kvq_tier_view view[KVQ_MAX_TIERS];
@@ -103,6 +124,7 @@ bool narrowed(const kvq_tier_view* tiers, int n, int batch, int hq, int window, 
     p.bits = reinterpret_cast<int*>(take((size_t)batch * n * 4));
   }
   if (make_plan(x->view, n, batch, hq, 0, true, &x->plan) != KVQ_OK) return false;
+  if (window) shorten_chunks(x->view, n, batch, hq, &x->plan);
   x->sketch = has_sketch(x->view, n);
   x->decode_bytes = workspace_bytes(batch, hq, c0->head_dim, x->plan.total, x->sketch);
   x->total = at + x->decode_bytes;
