@@ -1,14 +1,19 @@
 // kvq_chunk_attention and kvq_decode_attention_window: argument checks, workspace and launches.
 //
-// A call is the plan (chunk_plan.cu), the passes over the cache that some of its sequences may need
-// (chunk_dense.cu), and the joining of partial results.
+// A call is the plan (chunk_plan.cu), the passes over the cache that some of its sequences may need (chunk_dense.cu
+// for those with many rows, chunk_packed.cu for the others), and the joining of partial results.
 #include "api_checks.cuh"
 #include "chunk.cuh"
 #include "rope.cuh"
+#include "shared.cuh"
 #include "window.cuh"
 
 namespace kvq {
 namespace {
+
+// Query rows a kv head above which a sequence is unpacked.  A row block costs 1.45 us a tile of packed tokens, a pair of
+// them 2 us a tile of unpacked ones, and the unpacking as much once more.
+constexpr int kDenseRows = 512;
 
 struct ChunkCall {
   const kvq_tier_view* tiers;
@@ -75,16 +80,23 @@ kvq_status chunk_plan(const ChunkCall& c, ChunkParams* p) {
   p->sinks = c.visible ? c.visible->sinks : 0;
   p->head_dim = d;
   p->sms = device_sms();
-  p->dense_rows = -1;
-  // capacities
+  // Sequences of few rows stay packed where the prefix kernel takes all formats; a batch of long chunks is unpacked as
+  // a whole, which saves a launch whose blocks find nothing to do.
   const long long rows = (long long)c.num_tokens * p->group, seqs = std::min(c.batch, c.num_tokens);
+  p->dense_rows = seqs == 1 ? (rows > kDenseRows ? -1 : kDenseRows) : (rows > 4LL * kDenseRows * seqs ? -1 : kDenseRows);
+  for (int i = 0; i < c.num_tiers; ++i) {
+    const kvq_cache* k = c.tiers[i].cache;
+    if (!shared_tier_supported(d, k->k_format, k->v_format) || (k->v_format == KVQ_FMT_INT4_G32 && !aligned(k->v_aux, 8)))
+      p->dense_rows = -1;
+  }
+  // capacities
   const long long dense_seqs = p->dense_rows < 0 ? seqs : std::min(seqs, rows / (p->dense_rows + 1LL));
   const long long blocks = c.offsets ? rows / kChunkRows + seqs : seqs;
   const long long tile = dense_tile(d), unit_rows = kChunkRows * dense_blocks(d);
   const long long most = p->window ? std::min(room, (long long)p->window) + std::min(room, (long long)p->sinks) : room;
   const long long tiles = dense_seqs ? dense_seqs * (most / tile + 4) + c.num_tokens / tile : 0;
   const long long units = dense_seqs ? rows / unit_rows + dense_seqs : 0;
-  const long long extra = (2LL * p->sms + hkv - 1) / hkv, packed = p->dense_rows < 0 ? 0 : blocks;
+  const long long extra = (2LL * p->sms + hkv - 1) / hkv, packed = p->dense_rows < 0 ? 0 : std::min(blocks, seqs * (p->dense_rows / kChunkRows));
   const long long items[2] = {units ? units + extra : 0, packed ? packed * c.num_tiers + extra : 0};
   const long long parts = items[0] * dense_blocks(d) + items[1] * 2;
   if (tiles * hkv > 0x7FFFFFFFLL || parts * hkv * kChunkRows > 0x7FFFFFFFLL) return KVQ_ERR_UNSUPPORTED;
@@ -163,6 +175,7 @@ kvq_status chunk_run(const ChunkCall& c, const kvq_heads& q, const int32_t* offs
   cudaError_t e = launch_chunk_plan(p, stream);
   if (e == cudaSuccess && p.max_units[0]) e = launch_chunk_prepare(p, stream);
   if (e == cudaSuccess && p.max_units[0]) e = launch_chunk_dense(p, stream);
+  if (e == cudaSuccess && p.max_units[1]) e = launch_chunk_packed(p, p.max_units[0] > 0, stream);
   if (e == cudaSuccess) e = launch_chunk_join(p, stream);
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }

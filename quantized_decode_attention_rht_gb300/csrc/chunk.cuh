@@ -95,6 +95,7 @@ struct ChunkParams {
   int max_units[2], max_items[2];  // unpacked, packed
   int extra_items;  // that splitting may add to one a unit and tier
   int sms;
+  int wait_first;  // a pass on packed tiles directly behind the plan: it waits for it (else for the pass before, at its end)
   // in the workspace
   ChunkHead* head;
   ChunkSeq* seq;        // [batch]
@@ -119,6 +120,8 @@ cudaError_t launch_chunk_plan(const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_join(const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_prepare(const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_chunk_dense(const ChunkParams& p, cudaStream_t stream);
+// Items on the packed cache (shared_mma.cuh); behind: whether the unpacked path precedes.
+cudaError_t launch_chunk_packed(const ChunkParams& p, bool behind, cudaStream_t stream);
 
 // Programmatic dependents: a grid that may start while the one before it drains, and waits for it first of all.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -530,21 +530,20 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 // An accumulator row times f.
 template <int D>
 __device__ __forceinline__ void scale_row(uint32_t at, float f) {
-  uint32_t v[16];
+  uint32_t v[32];
 #pragma unroll 1
-  for (int c = 0; c < D; c += 16) {
-    tc_ld16(at + c, v);
-    tc_wait_ld(v);
+  for (int c = 0; c < D; c += 32) {
+    tc_ld32(at + c, v);
+    tc_wait_ld_only(v);
+    uint32_t x[16], y[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-    tc_st16(at + c, v);
+    for (int e = 0; e < 16; ++e) {
+      x[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+      y[e] = __float_as_uint(__uint_as_float(v[16 + e]) * f);
+    }
+    tc_st16(at + c, x);
+    tc_st16(at + c + 16, y);
   }
-}
-
-// Bits c .. c + 31 of the columns below n.
-__device__ __forceinline__ uint32_t below(int n, int c) {
-  n -= c;
-  return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
 // 32 scores -> 16 weight pairs and their sum.  HIDE: columns that are not in `see` weigh nothing, whatever they hold.
@@ -576,10 +575,8 @@ __device__ __forceinline__ void weigh(const uint32_t (&v)[32], uint32_t see, flo
       s0 = add2(s0, pack2(a0, a1));
       s1 = add2(s1, pack2(a2, a3));
       const float4 n = *reinterpret_cast<const float4*>(vn + e);
-      a0 *= n.x;
-      a1 *= n.y;
-      a2 *= n.z;
-      a3 *= n.w;
+      const float2 u = unpack2(mul2(pack2(a0, a1), pack2(n.x, n.y))), w = unpack2(mul2(pack2(a2, a3), pack2(n.z, n.w)));
+      a0 = u.x, a1 = u.y, a2 = w.x, a3 = w.y;
       if constexpr (HIDE) {  // (a norm may be infinite)
         a0 = see >> e & 1u ? a0 : 0.f;
         a1 = see >> (e + 1) & 1u ? a1 : 0.f;
@@ -676,6 +673,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
         const float* vn = kn + TT;
         top = next_top;
         if (CODES && i + 1 < n) next_top = __ldg(tops + (size_t)(s.tile0 + tile_of(i + 1)) * p.hkv);
+        const bool behind_sinks = i > 0 && item.first + i == item.sinks;
         // columns below `end`, and from `begin` on or below `first`
         const int end = pos + 1 - start, begin = from - start, first = p.sinks - start;
         const bool all = __all_sync(0xFFFFFFFFu, end >= TT && (begin <= 0 || first >= TT));
@@ -696,11 +694,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
           tc_ld32(s_at, va);
 #pragma unroll
           for (int c = 0; c < TT; c += 64) {
-            tc_wait_ld(va);
+            tc_wait_ld_only(va);
             tc_ld32(s_at + c + 32, vb);
             if (all) weigh<CODES, false>(va, 0, m, kn + c, vn + c, g + c / 2, s0, s1);
             else weigh<CODES, true>(va, see(c), m, kn + c, vn + c, g + c / 2, s0, s1);
-            tc_wait_ld(vb);
+            tc_wait_ld_only(vb);
             if (c + 64 < TT) tc_ld32(s_at + c + 64, va);
             if (all) weigh<CODES, false>(vb, 0, m, kn + c + 32, vn + c + 32, g + c / 2 + 16, s0, s1);
             else weigh<CODES, true>(vb, see(c + 32), m, kn + c + 32, vn + c + 32, g + c / 2 + 16, s0, s1);
@@ -708,19 +706,24 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
           sum = add2(s0, s1);
           const float2 t = unpack2(sum);
           // All weights are positive: a sum of at most kMostWeight says that none is too large for fp16 either.  Only
-          // where it is exceeded (always at first) m is raised and the tile, still in TMEM, weighed again.
-          if (again || __all_sync(0xFFFFFFFFu, (t.x + t.y) * top <= kMostWeight)) break;
+          // where it is exceeded (always at first) m is raised and the tile, still in TMEM, weighed again: of all rows of
+          // the warp, and of all behind the sinks, where the maximum of a few tokens would be exceeded row by row.  (A sum
+          // of NaN stays that.)
+          if (again || __all_sync(0xFFFFFFFFu, !behind_sinks && !((t.x + t.y) * top > kMostWeight))) break;
           const float head = kHeadroom - (float)((int)(__float_as_uint(top) >> 23) - 127);
           float mx = m;
 #pragma unroll 1
-          for (int c = 0; c < TT; c += 16) {
-            uint32_t y[16];
-            tc_ld16(s_at + c, y);
-            tc_wait_ld(y);
+          for (int c = 0; c < TT; c += 32) {
+            tc_ld32(s_at + c, va);
+            tc_wait_ld_only(va);
             const uint32_t sees = see(c);
+            float best = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (sees >> e & 1u) mx = fmaxf(mx, __uint_as_float(y[e]) * (CODES ? kn[c + e] : 1.f) - head);
+            for (int e = 0; e < 32; ++e) {
+              const float y = __uint_as_float(va[e]) * (CODES ? kn[c + e] : 1.f);
+              best = fmaxf(best, all || sees >> e & 1u ? y : -INFINITY);
+            }
+            mx = fmaxf(mx, best - head);
           }
           const float f = ex2(m - mx);
           m = mx;

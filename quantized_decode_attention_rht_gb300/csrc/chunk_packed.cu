@@ -1,0 +1,43 @@
+// Chunks with few rows, on the packed cache: the prefix kernel over a plan's items (shared_mma.cuh).
+#include <atomic>
+
+#include "shared_mma.cuh"
+
+namespace kvq {
+namespace {
+
+template <bool CODES>
+cudaError_t launch_kind(const ChunkParams& p, cudaStream_t stream) {
+  auto kern = shared_prefix_kernel<CODES, ChunkParams>;
+  static std::atomic<bool> configured[64];  // shared-memory limit raised on this device (a racing second raise is
+                                            // harmless)
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    configured[dev].store(true, std::memory_order_relaxed);
+  }
+  return launch_dependent(reinterpret_cast<const void*>(kern), (unsigned)((long long)p.max_items[1] * p.hkv), kThreads, kSmem, p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_packed(const ChunkParams& all, bool behind, cudaStream_t stream) {
+  ChunkParams p = all;
+  p.wait_first = !behind;
+  bool kinds[2] = {false, false};
+  for (int i = 0; i < p.num_tiers; ++i)
+    if (p.tier[i].max_pages) kinds[p.tier[i].v_fmt == KVQ_FMT_CODEBOOK] = true;
+  cudaError_t e = cudaSuccess;
+  if (kinds[0]) {
+    e = launch_kind<false>(p, stream);
+    p.wait_first = 0;
+  }
+  if (e == cudaSuccess && kinds[1]) e = launch_kind<true>(p, stream);
+  return e;
+}
+
+}  // namespace kvq

@@ -143,9 +143,18 @@ def test_lengths(context, count):
 @pytest.mark.parametrize("name", ["fp16", "fp8_int4", "fp8_fp16", "cb4", "cb32", "cb23"])
 @pytest.mark.parametrize("group", [1, 2, 4, 8])
 def test_formats_and_groups(name, group):
+    """With the second sequence unpacked, where it has the rows."""
     torch, kvq = modules()
-    c = Case(kvq, torch, [name], [[400, 60, 33]], [17, 3, 33], hq=2 * group, hkv=2, seed=group)
+    c = Case(kvq, torch, [name], [[400, 140, 33]], [17, 70, 33], hq=2 * group, hkv=2, seed=group)
     c.check(c.run(kvq, torch))
+
+
+@pytest.mark.parametrize("name", ["fp8_int4", "cb4"])
+@pytest.mark.parametrize("count", [511, 512, 513, 700])
+def test_where_unpacking_begins(name, count):
+    torch, kvq = modules()
+    c = Case(kvq, torch, [name], [[900, 800, 20]], [count, 8, 20], hq=2, hkv=2, seed=count)
+    c.check(c.run(kvq, torch), set(range(0, count, 37)) | set(range(count - 3, count + 28)))
 
 
 @pytest.mark.parametrize("name", ["fp16", "fp8_int4", "fp8_fp16", "cb4", "cb32", "cb23"])
@@ -163,12 +172,13 @@ def test_keys_with_extra(name, d, group):
     c.check(c.run(kvq, torch))
 
 
-@pytest.mark.parametrize("name,d", [("fp16", 128), ("cb4", 128), ("fp8_int4", 64), ("cb32", 256)])
+@pytest.mark.parametrize("name,d,hq", [("fp16", 128, 2), ("cb4", 128, 2), ("fp16", 128, 4), ("cb4", 128, 4), ("fp8_int4", 64, 2),
+                                       ("cb32", 256, 2)])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 4), (100, 0), (128, 128), (129, 3), (300, 200), (5000, 10)])
-def test_windows(name, d, window, sinks):
+def test_windows(name, d, hq, window, sinks):
     """Windows and sinks that begin and end inside pages and tiles, meet one another, or hold everything."""
     torch, kvq = modules()
-    c = Case(kvq, torch, [name], [[700, 90]], [150, 20], hq=2, hkv=1, d=d, window=window, sinks=sinks, seed=window)
+    c = Case(kvq, torch, [name], [[700, 90]], [150, 20], hq=hq, hkv=1, d=d, window=window, sinks=sinks, seed=window)
     c.check(c.run(kvq, torch))
 
 
@@ -187,11 +197,12 @@ def test_decode_window(name, d, window, sinks):
                                         (["cb4", "fp16"], [[300, 0, 128, 7], [64, 33, 0, 1]]),
                                         (["cb32", "cb4", "fp8_int4", "fp16"], [[130, 5, 0, 16], [100, 0, 2, 16], [40, 7, 0, 16], [50, 1, 1, 16]])])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (70, 9)])
-def test_tiers(specs, lens, window, sinks):
+@pytest.mark.parametrize("hq", [4, 16])
+def test_tiers(specs, lens, window, sinks, hq):
     """Tokens of several tiers, one tier after the other; chunks that reach across them, and tiers that a sequence has not."""
     torch, kvq = modules()
     counts = [80, 20, 2, 3]
-    c = Case(kvq, torch, specs, lens, counts, hq=4, hkv=2, window=window, sinks=sinks, seed=len(specs))
+    c = Case(kvq, torch, specs, lens, counts, hq=hq, hkv=2, window=window, sinks=sinks, seed=len(specs))
     c.check(c.run(kvq, torch))
 
 
@@ -295,13 +306,15 @@ def nan_at(positions, side):
     return edit
 
 
-@pytest.mark.parametrize("name,d", [("fp16", 128), ("cb4", 128), ("fp8_int4", 128), ("fp16", 64), ("cb32", 256)])
+@pytest.mark.parametrize("name,d,group", [("fp16", 128, 2), ("cb4", 128, 2), ("fp8_int4", 128, 2), ("fp8_fp16", 128, 1),
+                                          ("fp16", 128, 8), ("cb4", 128, 8), ("fp8_int4", 128, 8), ("fp16", 64, 2), ("cb32", 256, 2)])
 @pytest.mark.parametrize("side", ["k", "v"])
-def test_what_a_query_does_not_see_does_not_reach_it(name, d, side):
-    """Vectors that are not finite, behind a query, before its window, and (in pages) behind the sequence."""
+def test_what_a_query_does_not_see_does_not_reach_it(name, d, group, side):
+    """Vectors that are not finite, behind a query, before its window, and (in pages) behind the sequence; on
+    packed tiles and (eight heads a kv head; other head_dims) on unpacked ones."""
     torch, kvq = modules()
     bad = [(20, np.nan), (250, np.inf)]  # before the window of all queries; in the middle of the chunk
-    args = dict(specs=[name], lens=[[300]], counts=[120], hq=2, hkv=1, d=d, window=130, sinks=4, seed=1)
+    args = dict(specs=[name], lens=[[300]], counts=[120], hq=group, hkv=1, d=d, window=130, sinks=4, seed=1)
     with np.errstate(invalid="ignore"):
         c = Case(kvq, torch, edit=nan_at([(t, 1.0) for t, _ in bad], side), **args)
         e = Case(kvq, torch, edit=nan_at(bad, side), **args)
@@ -317,35 +330,38 @@ def test_what_a_query_does_not_see_does_not_reach_it(name, d, side):
                 aux[free] = float("nan")
     want, got = c.run(kvq, torch), e.run(kvq, torch)
     c.check(want)
-    # query i stands at 180 + i: it sees position 20 never (20 <= 180 - 130), position 250 from i = 70 on
-    assert np.array_equal(got[:70], want[:70])
-    if side == "v" or name == "fp16":
-        assert not np.isfinite(got[70:].astype(np.float64)).all(-1).any() or side == "k"
+    # query i stands at 180 + i: it sees position 20 never (20 <= 180 - 130), position 250 from i = 70 on.  (The
+    # others' results may differ in their last bit: running maxima are raised by the warp.)
+    c.check(got[:70], set(range(70)))
+    if side == "v":
+        assert not np.isfinite(got[70:].astype(np.float64)).all(-1).any()
 
 
-def test_a_query_that_is_not_finite_stays_alone():
+@pytest.mark.parametrize("hq", [4, 16])
+def test_a_query_that_is_not_finite_stays_alone(hq):
     torch, kvq = modules()
     for name in ("fp16", "cb4"):
-        c = Case(kvq, torch, [name], [[200]], [40], hq=4, hkv=2, seed=4)
+        c = Case(kvq, torch, [name], [[200]], [70], hq=hq, hkv=2, seed=4)
         want = c.run(kvq, torch)
         q = torch.from_numpy(c.q).cuda()
         q[7, 1, 5], q[20, 3, 0] = float("nan"), float("inf")
         got = c.run(kvq, torch, q=q)
-        same = np.ones((40, 4), dtype=bool)
-        same[7, 1] = same[20, 3] = False
-        assert np.array_equal(got[same], want[same]) and np.isnan(got[~same].astype(np.float64)).all()
+        assert np.isnan(got[7, 1].astype(np.float64)).all() and np.isnan(got[20, 3].astype(np.float64)).all()
+        got[7, 1], got[20, 3] = want[7, 1], want[20, 3]
+        c.check(got)
 
 
 @pytest.mark.parametrize("name", ["fp16", "cb4", "fp8_int4"])
-def test_large_scores_and_growing_maxima(name):
+@pytest.mark.parametrize("count", [200, 400])  # (two query heads a kv head: packed and unpacked)
+def test_large_scores_and_growing_maxima(name, count):
     """Scores that grow along the context, so that running maxima are raised again and again, and one token that outweighs all."""
     torch, kvq = modules()
 
     def edit(tier, b, k, v):
         k *= np.linspace(0.1, 4.0, len(k))[:, None, None].astype(np.float16)
         k[len(k) // 2] *= 6.0
-    c = Case(kvq, torch, [name], [[900]], [200], hq=2, hkv=1, seed=6, edit=edit)
-    c.check(c.run(kvq, torch), set(range(0, 200, 7)))
+    c = Case(kvq, torch, [name], [[900]], [count], hq=2, hkv=1, seed=6, edit=edit)
+    c.check(c.run(kvq, torch), set(range(0, count, 7)))
 
 
 def test_split_over_a_long_context():
