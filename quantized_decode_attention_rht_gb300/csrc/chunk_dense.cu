@@ -420,36 +420,43 @@ __device__ __forceinline__ void rotate_queries(const ChunkParams& p, int unit, i
   const ChunkUnit& x = p.unit[0][unit];
   const ChunkSeq& s = p.seq[x.seq];
   const int rows = s.tokens << p.group_shift;
-  for (int r = threadIdx.x >> 5; r < kRows; r += kPrepareThreads / 32) {
-    const int row = x.row0 + r;
-    if (r >= kChunkRows && x.row0 + kChunkRows >= rows) break;  // no second block
-    float y[E];
+  constexpr int kAtOnce = 4, kWarps = kPrepareThreads / 32;
+  for (int r0 = threadIdx.x >> 5; r0 < kRows; r0 += kWarps * kAtOnce) {
+    if (r0 >= kChunkRows && x.row0 + kChunkRows >= rows) break;  // no second block
+    float y[kAtOnce][E];
+    bool there[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = 0.f;
-    if (row < rows) {
-      const int token = s.q0 + (row >> p.group_shift), head = (h << p.group_shift) + (row & (p.group - 1));
-      load_rotate<E>(p.q + token * p.q_token + head * p.q_head, p.k_signs + (size_t)h * D, lane, y);
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int row = x.row0 + r0 + i * kWarps;
+      there[i] = row < rows;
+      const int safe = there[i] ? row : x.row0;
+      const int token = s.q0 + (safe >> p.group_shift), head = (h << p.group_shift) + (safe & (p.group - 1));
+      load_rotate<E>(p.q + token * p.q_token + head * p.q_head, p.k_signs + (size_t)h * D, lane, y[i]);
     }
-    uint8_t* to = p.qt + (((size_t)unit * p.hkv + h) * dense_blocks(D) + r / kChunkRows) * (2 * kChunkRows * D * 2);
-    const uint32_t at = tile_at(kChunkRows, r % kChunkRows, lane * E / 8 * 8) + lane * E % 8 * 2;
-    uint32_t hi[E / 2], lo[E / 2];
 #pragma unroll
-    for (int k = 0; k < E / 2; ++k) {
-      const float a = y[2 * k] * scale, b = y[2 * k + 1] * scale;
-      hi[k] = half2_bits(a, b);
-      const float2 near = unpack_half2(hi[k]);
-      lo[k] = half2_bits(a - near.x, b - near.y);
-    }
-    uint8_t* rest = to + kChunkRows * D * 2;
-    if constexpr (E == 2) {
-      *reinterpret_cast<uint32_t*>(to + at) = hi[0];
-      *reinterpret_cast<uint32_t*>(rest + at) = lo[0];
-    } else if constexpr (E == 4) {
-      *reinterpret_cast<uint2*>(to + at) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(rest + at) = make_uint2(lo[0], lo[1]);
-    } else {
-      *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(rest + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int r = r0 + i * kWarps;
+      uint8_t* to = p.qt + (((size_t)unit * p.hkv + h) * dense_blocks(D) + r / kChunkRows) * (2 * kChunkRows * D * 2);
+      const uint32_t at = tile_at(kChunkRows, r % kChunkRows, lane * E / 8 * 8) + lane * E % 8 * 2;
+      uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+      for (int k = 0; k < E / 2; ++k) {
+        const float a = there[i] ? y[i][2 * k] * scale : 0.f, b = there[i] ? y[i][2 * k + 1] * scale : 0.f;
+        hi[k] = half2_bits(a, b);
+        const float2 near = unpack_half2(hi[k]);
+        lo[k] = half2_bits(a - near.x, b - near.y);
+      }
+      uint8_t* rest = to + kChunkRows * D * 2;
+      if constexpr (E == 2) {
+        *reinterpret_cast<uint32_t*>(to + at) = hi[0];
+        *reinterpret_cast<uint32_t*>(rest + at) = lo[0];
+      } else if constexpr (E == 4) {
+        *reinterpret_cast<uint2*>(to + at) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(rest + at) = make_uint2(lo[0], lo[1]);
+      } else {
+        *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(rest + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
     }
   }
 }
@@ -673,7 +680,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
         const float* vn = kn + TT;
         top = next_top;
         if (CODES && i + 1 < n) next_top = __ldg(tops + (size_t)(s.tile0 + tile_of(i + 1)) * p.hkv);
-        const bool behind_sinks = i > 0 && item.first + i == item.sinks;
         // columns below `end`, and from `begin` on or below `first`
         const int end = pos + 1 - start, begin = from - start, first = p.sinks - start;
         const bool all = __all_sync(0xFFFFFFFFu, end >= TT && (begin <= 0 || first >= TT));
@@ -687,10 +693,45 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
         auto see = [&](int c) { return below(end, c) & (~below(begin, c) | below(first, c)); };
         uint32_t g[TT / 2];
         unsigned long long sum;
+        // All weights are positive: a sum of at most kMostWeight says that none is too large for fp16 either.  Only
+        // where it is exceeded m is raised and the tile, still in TMEM, weighed again: of all rows of the warp.  (A sum of
+        // NaN stays that.)  The first tile raises m anyway, and so does the first behind the sinks, where the maximum
+        // of a few tokens would be exceeded row by row.
+        bool raise = i == 0 || item.first + i == item.sinks;
 #pragma unroll 1
-        for (int again = 0;; ++again) {
-          unsigned long long s0 = 0, s1 = 0;
+        for (bool again = raise;; again = true) {
           uint32_t va[32], vb[32];
+          if (raise) {
+            const float head = kHeadroom - (float)((int)(__float_as_uint(top) >> 23) - 127);
+            float mx = m;
+#pragma unroll 1
+            for (int c = 0; c < TT; c += 32) {
+              tc_ld32(s_at + c, va);
+              tc_wait_ld_only(va);
+              const uint32_t sees = see(c);
+              float best = -INFINITY;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float y = __uint_as_float(va[e]) * (CODES ? kn[c + e] : 1.f);
+                best = fmaxf(best, all || sees >> e & 1u ? y : -INFINITY);
+              }
+              mx = fmaxf(mx, best - head);
+            }
+            const float f = ex2(m - mx);
+            m = mx;
+            const float2 ll = unpack2(l2);
+            l2 = pack2(ll.x * f, ll.y * f);
+            if (i > 0) {
+              // (with two row blocks the products of earlier tiles precede these scores; with one they may still run)
+              if (RT == 1 && !__all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * A_O, (i - 1) & 1, abort, err))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              scale_row<D>(o_at, f);
+            }
+          }
+          unsigned long long s0 = 0, s1 = 0;
           tc_ld32(s_at, va);
 #pragma unroll
           for (int c = 0; c < TT; c += 64) {
@@ -705,39 +746,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
           }
           sum = add2(s0, s1);
           const float2 t = unpack2(sum);
-          // All weights are positive: a sum of at most kMostWeight says that none is too large for fp16 either.  Only
-          // where it is exceeded (always at first) m is raised and the tile, still in TMEM, weighed again: of all rows of
-          // the warp, and of all behind the sinks, where the maximum of a few tokens would be exceeded row by row.  (A sum
-          // of NaN stays that.)
-          if (again || __all_sync(0xFFFFFFFFu, !behind_sinks && !((t.x + t.y) * top > kMostWeight))) break;
-          const float head = kHeadroom - (float)((int)(__float_as_uint(top) >> 23) - 127);
-          float mx = m;
-#pragma unroll 1
-          for (int c = 0; c < TT; c += 32) {
-            tc_ld32(s_at + c, va);
-            tc_wait_ld_only(va);
-            const uint32_t sees = see(c);
-            float best = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float y = __uint_as_float(va[e]) * (CODES ? kn[c + e] : 1.f);
-              best = fmaxf(best, all || sees >> e & 1u ? y : -INFINITY);
-            }
-            mx = fmaxf(mx, best - head);
-          }
-          const float f = ex2(m - mx);
-          m = mx;
-          const float2 ll = unpack2(l2);
-          l2 = pack2(ll.x * f, ll.y * f);
-          if (i > 0) {
-            // (with two row blocks the products of earlier tiles precede these scores; with one they may still run)
-            if (RT == 1 && !__all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * A_O, (i - 1) & 1, abort, err))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            scale_row<D>(o_at, f);
-          }
+          if (again || __all_sync(0xFFFFFFFFu, !((t.x + t.y) * top > kMostWeight))) break;
+          raise = true;
         }
         if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
         l2 = add2(l2, sum);

@@ -12,6 +12,8 @@ namespace kvq {
 namespace {
 
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+// A small plan is made in shared memory (a phase then costs a fifth of what it does through L2), and copied out.
+constexpr int kNearSeqs = 256, kNearUnits = 384;
 
 struct Sums {
   int a, b, c, d;
@@ -126,7 +128,7 @@ __device__ __forceinline__ Seen seen_by(const ChunkParams& p, const ChunkSeq& s,
 // Tokens per split, in tiles, of class c (0: unpacked, 1: packed): the cheapest of the longest unit's
 // tiles over 1, 2, ... 160.  Time in tiles: an item is its tiles and a fixed start and end; partial results cost
 // their pass through memory.
-__device__ __forceinline__ int choose_per(const ChunkParams& p, int c, int units, int longest,
+__device__ __forceinline__ int choose_per(const ChunkParams& p, int c, const ChunkUnit* unit, int units, int longest,
                                           unsigned long long* best) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float start = c ? 5.0f : 3.0f;
@@ -142,7 +144,7 @@ __device__ __forceinline__ int choose_per(const ChunkParams& p, int c, int units
 #pragma unroll
       for (int k = 0; k < KVQ_MAX_TIERS; ++k) {
         if (k >= p.num_tiers) continue;
-        const int n = p.unit[c][u].n[k];
+        const int n = unit[u].n[k];
         items += ceil_div(n, per);
         sum += n;
       }
@@ -166,6 +168,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   __shared__ int imax[kPlanWarps];
   __shared__ int err, longest[2];
   __shared__ unsigned long long best;
+  __shared__ ChunkSeq near_seq[kNearSeqs];
+  __shared__ ChunkUnit near_unit[kNearUnits];
+  ChunkSeq* const seq = p.batch <= kNearSeqs ? near_seq : p.seq;
+  const bool near_units = p.max_units[0] + p.max_units[1] <= kNearUnits;
+  ChunkUnit* const unit[2] = {near_units ? near_unit : p.unit[0], near_units ? near_unit + p.max_units[0] : p.unit[1]};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   grid_release();
   if (tid == 0) {
@@ -223,7 +230,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     s.first_block = at.a;
     s.tile0 = at.d;
     s.unit0 = s.dense ? at.b : at.c;
-    if (b < p.batch) p.seq[b] = s;
+    if (b < p.batch) {
+      seq[b] = s;
+      if (seq != p.seq) p.seq[b] = s;
+    }
   }
   if (bits) atomicOr(&err, bits);
   __syncthreads();
@@ -231,7 +241,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     for (int x = warp; x < 2 * p.num_tiers; x += kPlanWarps) plan_table(p, x / 2, x % 2);
   // ---- units of work, a warp a sequence
   for (int b = warp; b < p.batch; b += kPlanWarps) {
-    const ChunkSeq s = p.seq[b];
+    const ChunkSeq& s = seq[b];
     const int rows = s.tokens << p.group_shift, step = kChunkRows * (s.dense ? per_unit : 1);
     int n_most = 0;
     for (int r = lane * step; r < rows; r += 32 * step) {
@@ -260,7 +270,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
           n_most = max(n_most, u.n[k]);
         }
       }
-      p.unit[s.dense ? 0 : 1][s.unit0 + r / step] = u;
+      unit[s.dense ? 0 : 1][s.unit0 + r / step] = u;
+      if (near_units && s.dense) p.unit[0][s.unit0 + r / step] = u;  // (read again where queries are rotated)
     }
     n_most = __reduce_max_sync(0xFFFFFFFFu, n_most);
     if (lane == 0) atomicMax(&longest[s.dense ? 0 : 1], n_most);
@@ -271,7 +282,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   for (int c = 0; c < 2; ++c) {
     const int units = c ? total.c : total.b;
     if (units == 0) continue;
-    const int per = choose_per(p, c, units, longest[c], &best);
+    const int per = choose_per(p, c, unit[c], units, longest[c], &best);
     const int a_part = c ? 2 : per_unit;  // partials of kChunkRows rows an item leaves
     Sums all = {0, 0, 0, 0};
     for (int u0 = 0; u0 < units; u0 += kPlanThreads) {
@@ -281,15 +292,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 #pragma unroll
         for (int k = 0; k < KVQ_MAX_TIERS; ++k) {
           if (k >= p.num_tiers) continue;
-          const int n = ceil_div(p.unit[c][u].n[k], per);
+          const int n = ceil_div(unit[c][u].n[k], per);
           if (c && p.tier[k].v_fmt == KVQ_FMT_CODEBOOK) mine.b += n;
           else mine.a += n;
         }
       }
       const Sums at = scan(mine, all, warps);
       if (u < units) {
-        const ChunkUnit& x = p.unit[c][u];
-        const ChunkSeq& s = p.seq[x.seq];
+        const ChunkUnit& x = unit[c][u];
+        const ChunkSeq& s = seq[x.seq];
         const int rows = s.tokens << p.group_shift, n = mine.a + mine.b, part0 = parts + a_part * (at.a + at.b);
         if (c) {
           p.unit_items[1][u] = at.a;
@@ -313,7 +324,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     __syncthreads();
     for (int u = warp; u < units; u += kPlanWarps) {
-      const ChunkUnit x = p.unit[c][u];
+      const ChunkUnit& x = unit[c][u];
       int before = 0;
       const int part0 = parts + a_part * (c ? p.unit_items[1][u] + p.unit_items[2][u] : p.unit_items[0][u]);
       int at[2] = {p.unit_items[c ? 1 : 0][u], c ? p.unit_items[2][u] : 0};

@@ -1399,6 +1399,8 @@ __global__ void __launch_bounds__(P::L::WARPS * 32, 1) decode_cb_kernel(const __
   const uint32_t slane = pin((a_t + L::TABLE) | ((lane & 15) << 3));
   // items: the one in hand, the next (its metadata and queries fetched while this one
   // runs), and the one after (its counter ticket in flight)
+  // (tables, lengths and the counter come from the kernel before)
+  if (kHides) asm volatile("griddepcontrol.wait;" ::: "memory");
   int item = 0, next = 0;
   if (lane == 0) {
     item = atomicAdd(p.counter, 1);

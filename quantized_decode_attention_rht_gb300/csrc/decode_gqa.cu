@@ -696,6 +696,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_gqa_kernel(const __grid
   uint8_t* wsm = smem + warp * kWarpSmem;
   // a codebook split-K grid that follows may start on SMs this grid leaves idle
   if (p.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (tables, lengths and the counter come from the kernel before)
+  if (HIDES) asm volatile("griddepcontrol.wait;" ::: "memory");
   int item = 0;
   if (lane == 0) item = atomicAdd(p.counter, 1);
   item = __shfl_sync(kFull, item, 0);

@@ -33,6 +33,7 @@ struct NarrowParams {
 __global__ void __launch_bounds__(128) narrow_kernel(const __grid_constant__ NarrowParams p) {
   const int b = blockIdx.x, ti = blockIdx.y, ps = p.page_size;
   const NarrowTier& t = p.tier[ti];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the decode kernels wait where they need this)
   if (b == 0 && ti == 0 && threadIdx.x < 64) p.counters[threadIdx.x] = 0;
   int bits = 0, base = 0, all = 0, len = 0;
 #pragma unroll
@@ -168,9 +169,9 @@ cudaError_t window_run(const kvq_tier_view* tiers, int num_tiers, const uint16_t
   }
   bool fam[3] = {false, false, false};
   for (int i = 0; i < num_tiers; ++i) fam[x.plan.kind[i]] = true;
-  if (e == cudaSuccess && fam[TIER_GQA]) e = launch_decode_gqa(p, counters + kGqaCounter, stream, fam[TIER_CB]);
+  if (e == cudaSuccess && fam[TIER_GQA]) e = launch_decode_gqa(p, counters + kGqaCounter, stream, fam[TIER_CB], window != 0);
   if (e == cudaSuccess && fam[TIER_CB])
-    e = (window ? launch_decode_cb_hiding : launch_decode_cb)(p, c0->head_dim, counters, stream, fam[TIER_GQA]);
+    e = (window ? launch_decode_cb_hiding : launch_decode_cb)(p, c0->head_dim, counters, stream, fam[TIER_GQA] || window);
   if (e == cudaSuccess && fam[TIER_GENERIC]) e = launch_decode(p, c0->head_dim, hq / c0->num_kv_heads, stream);
   if (e == cudaSuccess) e = launch_combine(p, c0->head_dim, stream);
   return e;
