@@ -25,7 +25,6 @@
 #include <type_traits>
 
 #include "chunk.cuh"
-#include "rotate.cuh"
 #include "tc.cuh"
 
 namespace kvq {
@@ -411,52 +410,77 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
 }
 
 // The rows of a unit's queries of one kv head: rotated, times log2(e) / D (1 / sqrt(D) of the rotation and of the
-// scores, which are then in base-2 units), as two fp16 numbers.
+// scores, which are then in base-2 units), as two fp16 numbers.  D / 32 neighbouring lanes share a row, 32 coordinates
+// each: five stages of the transform run in a lane's registers, the others between them (a third of the instructions of
+// a warp a row).
 template <int D>
 __device__ __forceinline__ void rotate_queries(const ChunkParams& p, int unit, int h) {
-  constexpr int E = D / 32, kRows = kChunkRows * dense_blocks(D);
+  constexpr int L = D / 32, kRows = kChunkRows * dense_blocks(D), kAtOnce = kPrepareThreads / L;
   constexpr float scale = 1.4426950408889634f / D;
-  const int lane = threadIdx.x & 31;
+  const int sub = threadIdx.x % L;
   const ChunkUnit& x = p.unit[0][unit];
   const ChunkSeq& s = p.seq[x.seq];
   const int rows = s.tokens << p.group_shift;
-  constexpr int kAtOnce = 4, kWarps = kPrepareThreads / 32;
-  for (int r0 = threadIdx.x >> 5; r0 < kRows; r0 += kWarps * kAtOnce) {
-    if (r0 >= kChunkRows && x.row0 + kChunkRows >= rows) break;  // no second block
-    float y[kAtOnce][E];
-    bool there[kAtOnce];
+  uint32_t sg[8];
+  {
+    const uint4* from = reinterpret_cast<const uint4*>(p.k_signs + (size_t)h * D + 32 * sub);
+    const uint4 a = __ldg(from), b = __ldg(from + 1);
+    sg[0] = a.x, sg[1] = a.y, sg[2] = a.z, sg[3] = a.w, sg[4] = b.x, sg[5] = b.y, sg[6] = b.z, sg[7] = b.w;
+  }
+#pragma unroll 1
+  for (int r = threadIdx.x / L; r < kRows; r += kAtOnce) {
+    const int row = x.row0 + r;
+    if (r >= kChunkRows && x.row0 + kChunkRows >= rows) break;  // no second block (the warps agree: rows of a pass do)
+    unsigned long long y[16];
+    {
+      const int safe = min(row, rows - 1), token = s.q0 + (safe >> p.group_shift);
+      const int head = (h << p.group_shift) + (safe & (p.group - 1));
+      const uint4* from = reinterpret_cast<const uint4*>(p.q + token * p.q_token + head * p.q_head + 32 * sub);
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int row = x.row0 + r0 + i * kWarps;
-      there[i] = row < rows;
-      const int safe = there[i] ? row : x.row0;
-      const int token = s.q0 + (safe >> p.group_shift), head = (h << p.group_shift) + (safe & (p.group - 1));
-      load_rotate<E>(p.q + token * p.q_token + head * p.q_head, p.k_signs + (size_t)h * D, lane, y[i]);
+      for (int k = 0; k < 4; ++k) {
+        const uint4 v = __ldg(from + k);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = 4 * k + j;  // coordinates 2 e, 2 e + 1: sign bytes to the sign bits of the pair
+          const uint32_t flip = __byte_perm(sg[e / 2], 0, (e & 1) ? 0x3424 : 0x1404) & 0x80008000u;
+          const float2 f = unpack_half2(w[j] ^ flip);
+          y[e] = pack2(f.x + f.y, f.x - f.y);
+        }
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      const int r = r0 + i * kWarps;
-      uint8_t* to = p.qt + (((size_t)unit * p.hkv + h) * dense_blocks(D) + r / kChunkRows) * (2 * kChunkRows * D * 2);
-      const uint32_t at = tile_at(kChunkRows, r % kChunkRows, lane * E / 8 * 8) + lane * E % 8 * 2;
-      uint32_t hi[E / 2], lo[E / 2];
+    for (int step = 1; step < 16; step <<= 1) {
 #pragma unroll
-      for (int k = 0; k < E / 2; ++k) {
-        const float a = there[i] ? y[i][2 * k] * scale : 0.f, b = there[i] ? y[i][2 * k + 1] * scale : 0.f;
-        hi[k] = half2_bits(a, b);
-        const float2 near = unpack_half2(hi[k]);
-        lo[k] = half2_bits(a - near.x, b - near.y);
+      for (int e = 0; e < 16; ++e) {
+        if (e & step) continue;
+        const unsigned long long a = y[e], c = y[e + step];
+        y[e] = add2(a, c);
+        y[e + step] = fma2(c, pack2(-1.f, -1.f), a);
       }
-      uint8_t* rest = to + kChunkRows * D * 2;
-      if constexpr (E == 2) {
-        *reinterpret_cast<uint32_t*>(to + at) = hi[0];
-        *reinterpret_cast<uint32_t*>(rest + at) = lo[0];
-      } else if constexpr (E == 4) {
-        *reinterpret_cast<uint2*>(to + at) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(rest + at) = make_uint2(lo[0], lo[1]);
-      } else {
-        *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(rest + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+#pragma unroll
+    for (int step = 1; step < L; step <<= 1) {
+      const float sign = sub & step ? -1.0f : 1.0f;  // the upper lane keeps the other's less its own
+      const unsigned long long sign2 = pack2(sign, sign);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = fma2(y[e], sign2, __shfl_xor_sync(0xFFFFFFFFu, y[e], step));
+    }
+    uint8_t* to = p.qt + (((size_t)unit * p.hkv + h) * dense_blocks(D) + r / kChunkRows) * (2 * kChunkRows * D * 2);
+    const float by = row < rows ? scale : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2(mul2(y[4 * k + j], pack2(by, by)));
+        hi[j] = half2_bits(f.x, f.y);
+        const float2 near = unpack_half2(hi[j]);
+        lo[j] = half2_bits(f.x - near.x, f.y - near.y);
       }
+      const uint32_t at = tile_at(kChunkRows, r % kChunkRows, 32 * sub + 8 * k);
+      *reinterpret_cast<uint4*>(to + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(to + kChunkRows * D * 2 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   }
 }

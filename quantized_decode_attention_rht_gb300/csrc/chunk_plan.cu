@@ -58,57 +58,70 @@ __device__ __forceinline__ int scan_max(int x, int& carry, int (&warps)[kPlanWar
   }
   if (lane == 31) warps[warp] = x;
   __syncthreads();
-  int before = carry, all = carry;
-  for (int w = 0; w < kPlanWarps; ++w) {
-    if (w < warp) before = max(before, warps[w]);
-    all = max(all, warps[w]);
+  if (warp == 0) {
+    int w = warps[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+      if (lane >= o) w = max(w, y);
+    }
+    warps[lane] = w;
   }
   __syncthreads();
-  carry = all;
+  const int before = warp ? max(carry, warps[warp - 1]) : carry;
+  carry = max(carry, warps[kPlanWarps - 1]);
+  __syncthreads();
   return max(x, before);
 }
 
-// The scale of a tier's table, one warp.
-__device__ __forceinline__ void plan_table(const ChunkParams& p, int tier, int side) {
-  const int lane = threadIdx.x & 31;
+// The scales of a codebook tier's tables: keys by the first half of the block, values by the second, a candidate a thread.
+struct TablePick {
+  float least, slope;
+  int at;
+};
+__device__ __forceinline__ void plan_tables(const ChunkParams& p, int tier, TablePick (&picks)[kPlanWarps]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, side = warp / (kPlanWarps / 2);
   const ChunkTier& t = p.tier[tier];
-  const bool codes = t.v_fmt == KVQ_FMT_CODEBOOK;  // (then the keys are of a codebook format too)
-  float beta = 1.0f, unscale = 1.0f;
-  if (codes) {
-    const int bits = side ? t.v_bits : t.k_bits;
-    const float c = lane < (1 << bits) ? __ldg((side ? t.v_cent : t.k_cent) + lane) : 0.f;
-    float least = INFINITY, slope = 0.f;
-    int at = 0;
-    for (int j = 0; j < 4; ++j) {
-      float e, s;
-      int k;
-      table_candidates(c, bits, lane + 32 * j, e, s, k);
-      if (j == 0 || e < least || (e == least && k < at)) {
-        least = e;
-        slope = s;
-        at = k;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float other = __shfl_xor_sync(0xFFFFFFFFu, least, o), its = __shfl_xor_sync(0xFFFFFFFFu, slope, o);
-      const int k = __shfl_xor_sync(0xFFFFFFFFu, at, o);
-      if (other < least || (other == least && k < at)) {
-        least = other;
-        slope = its;
-        at = k;
-      }
-    }
-    beta = exp2f((float)at * (1.0f / kTableSteps)) * table_unit(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(c))));
-    unscale = inv_sqrt_dim(p.head_dim) * (1.0f - slope) / beta;
+  const int bits = side ? t.v_bits : t.k_bits;
+  const float c = lane < (1 << bits) ? __ldg((side ? t.v_cent : t.k_cent) + lane) : 0.f;
+  TablePick x;
+  table_candidates<1>(c, bits, (int)threadIdx.x % kTableSteps, x.least, x.slope, x.at);
+  auto better = [](const TablePick& a, const TablePick& b) { return a.least < b.least || (a.least == b.least && a.at < b.at); };
+  auto other = [&](const TablePick& a, int o) {
+    return TablePick{__shfl_xor_sync(0xFFFFFFFFu, a.least, o), __shfl_xor_sync(0xFFFFFFFFu, a.slope, o),
+                     __shfl_xor_sync(0xFFFFFFFFu, a.at, o)};
+  };
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
+    const TablePick y = other(x, o);
+    if (better(y, x)) x = y;
   }
-  if (lane == 0) {
-    p.head->beta[tier][side] = beta;
-    p.head->unscale[tier][side] = unscale;
+  if (lane == 0) picks[warp] = x;
+  __syncthreads();
+  if (warp % (kPlanWarps / 2) == 0) {
+    x = picks[warp + lane % (kPlanWarps / 2)];
+#pragma unroll 1
+    for (int o = kPlanWarps / 4; o > 0; o >>= 1) {
+      const TablePick y = other(x, o);
+      if (better(y, x)) x = y;
+    }
+    const float beta = exp2f((float)x.at * (1.0f / kTableSteps)) * table_unit(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(c))));
+    if (lane == 0) {
+      p.head->beta[tier][side] = beta;
+      p.head->unscale[tier][side] = inv_sqrt_dim(p.head_dim) * (1.0f - x.slope) / beta;
+    }
   }
+  __syncthreads();
 }
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// ceil(a / b) of 0 <= a < 2^24 (tiles), inverse = 1 / b rounded.
+__device__ __forceinline__ int ceil_times(int a, int b, float inverse) {
+  int q = (int)((float)a * inverse);
+  q -= q * b > a;
+  q += (q + 1) * b <= a;
+  return q + (q * b < a);
+}
 
 // Positions that rows [row0, row1) of a sequence see: [0, sinks) and [lo, hi); the first ends where the second begins
 // at the latest.
@@ -140,20 +153,21 @@ __device__ __forceinline__ int choose_per(const ChunkParams& p, int c, const Chu
     const int per = ceil_div(longest, s);
     if (s > 1 && ceil_div(longest, per) != s) continue;  // the same split as with fewer
     int items = 0, sum = 0;
+    const float inverse = 1.0f / per;
     for (int u = lane; u < units; u += 32) {
-#pragma unroll
-      for (int k = 0; k < KVQ_MAX_TIERS; ++k) {
-        if (k >= p.num_tiers) continue;
+#pragma unroll 1
+      for (int k = 0; k < p.num_tiers; ++k) {
         const int n = unit[u].n[k];
-        items += ceil_div(n, per);
+        items += ceil_times(n, per, inverse);
         sum += n;
       }
     }
     items = __reduce_add_sync(0xFFFFFFFFu, items);
     sum = __reduce_add_sync(0xFFFFFFFFu, sum);
-    const float all = (float)items * p.hkv, waves = ceilf(all / p.sms);
-    const float each = waves <= 1.0f ? per + start : waves * ((float)sum / items + start);
-    const float cost = fmaxf(each, per + start) + (s > 1 ? 0.02f * all / p.sms * 4.0f : 0.f);
+    const float all = (float)items * p.hkv, load = ((float)sum * p.hkv + all * start) / p.sms, each = per + start;
+    // items of one length run in waves; of different lengths, the longest first, until the last ends
+    const float waves = ceilf(all / p.sms), last = (float)sum > 0.9f * items * per ? waves * each : load + 0.12f * each;
+    const float cost = fmaxf(last, each) + (s > 1 ? 0.08f * all / p.sms : 0.f);
     if (lane == 0 && items <= units * (c ? p.num_tiers : 1) + p.extra_items && cost < 1e9f)
       atomicMin(best, (unsigned long long)__float_as_uint(cost) << 32 | (unsigned)s);
   }
@@ -166,6 +180,7 @@ __device__ __forceinline__ int choose_per(const ChunkParams& p, int c, const Chu
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ ChunkParams p) {
   __shared__ Sums warps[kPlanWarps];
   __shared__ int imax[kPlanWarps];
+  __shared__ TablePick picks[kPlanWarps];
   __shared__ int err, longest[2];
   __shared__ unsigned long long best;
   __shared__ ChunkSeq near_seq[kNearSeqs];
@@ -195,9 +210,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       next = b < p.batch ? __ldg(p.offsets + b + 1) : 0;
     }
     if (b < p.batch) {
-#pragma unroll
-      for (int k = 0; k < KVQ_MAX_TIERS; ++k) {
-        if (k >= p.num_tiers) continue;
+#pragma unroll 1
+      for (int k = 0; k < p.num_tiers; ++k) {
         s.base[k] = s.len;
         s.len += checked_len(__ldg(p.tier[k].lens + b), p.tier[k].max_pages, p.page_size, &bits);
       }
@@ -238,7 +252,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   if (bits) atomicOr(&err, bits);
   __syncthreads();
   if (p.codes)
-    for (int x = warp; x < 2 * p.num_tiers; x += kPlanWarps) plan_table(p, x / 2, x % 2);
+#pragma unroll 1
+    for (int k = 0; k < p.num_tiers; ++k)
+      if (p.tier[k].v_fmt == KVQ_FMT_CODEBOOK) plan_tables(p, k, picks);
   // ---- units of work, a warp a sequence
   for (int b = warp; b < p.batch; b += kPlanWarps) {
     const ChunkSeq& s = seq[b];
@@ -258,9 +274,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         u.n[0] = u.sinks[0] + max(0, ceil_div(x.hi, tile) - lo);
         n_most = max(n_most, u.n[0]);
       } else {
-#pragma unroll
-        for (int k = 0; k < KVQ_MAX_TIERS; ++k) {
-          if (k >= p.num_tiers) continue;
+#pragma unroll 1
+        for (int k = 0; k < p.num_tiers; ++k) {
           const int end = k + 1 < p.num_tiers ? s.base[k + 1] : s.len;
           const int lo = max(0, x.lo - s.base[k]), hi = min(x.hi, end) - s.base[k];
           u.begin[k] = lo / kMaskedTile;
@@ -289,10 +304,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       const int u = u0 + tid;
       Sums mine = {0, 0, 0, 0};
       if (u < units) {
-#pragma unroll
-        for (int k = 0; k < KVQ_MAX_TIERS; ++k) {
-          if (k >= p.num_tiers) continue;
-          const int n = ceil_div(unit[c][u].n[k], per);
+#pragma unroll 1
+        for (int k = 0; k < p.num_tiers; ++k) {
+          const int n = ceil_times(unit[c][u].n[k], per, 1.0f / per);
           if (c && p.tier[k].v_fmt == KVQ_FMT_CODEBOOK) mine.b += n;
           else mine.a += n;
         }
@@ -328,10 +342,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       int before = 0;
       const int part0 = parts + a_part * (c ? p.unit_items[1][u] + p.unit_items[2][u] : p.unit_items[0][u]);
       int at[2] = {p.unit_items[c ? 1 : 0][u], c ? p.unit_items[2][u] : 0};
-#pragma unroll
-      for (int k = 0; k < KVQ_MAX_TIERS; ++k) {
-        if (k >= p.num_tiers) continue;
-        const int n = ceil_div(x.n[k], per), kind = c && p.tier[k].v_fmt == KVQ_FMT_CODEBOOK ? 1 : 0;
+#pragma unroll 1
+      for (int k = 0; k < p.num_tiers; ++k) {
+        const int n = ceil_times(x.n[k], per, 1.0f / per), kind = c && p.tier[k].v_fmt == KVQ_FMT_CODEBOOK ? 1 : 0;
         // the tiles of a tier in equal shares
         const int share = n ? ceil_div(x.n[k], n) : 0;
         for (int i = lane; i < n; i += 32) {

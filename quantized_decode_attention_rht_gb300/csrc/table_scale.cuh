@@ -13,14 +13,15 @@ namespace {
 // near their root mean square.  So the centroids there weigh most: w = exp(-3.125 (|c| / c1 - 1)^2), c1 = the
 // largest over 1.51, 2.15 or 2.73, what 2, 3 or 4 bits of N(0, 1) reach to.  (4-bit keys with x30 outlier
 // channels: 1.3e-4 of the output instead of 2.9e-4 with equal weights and 128 steps.)  c: centroid `lane` in every
-// lane (0 beyond the codebook); the four candidates of thread `tid` of 128: the best one's error, slope and number.
+// lane (0 beyond the codebook); the candidates of thread `tid` of 512 / kEach: the best one's error, slope and number.
 constexpr int kTableSteps = 512;
 // 2^-3 over the largest magnitude's power of two (its bits given)
 __device__ __forceinline__ float table_unit(uint32_t most) {
   return __uint_as_float((251u - min(max(most >> 23, 2u), 249u)) << 23);
 }
+template <int kEach = 4>
 __device__ __forceinline__ void table_candidates(float c, int bits, int tid, float& least, float& slope, int& at) {
-  constexpr int kEach = 4, kSteps = kTableSteps;
+  constexpr int kSteps = kTableSteps, kThreads = kSteps / kEach;
   const int lane = tid & 31;
   const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(c)));
   const float over = (bits == 4 ? 2.73f : (bits == 3 ? 2.15f : 1.51f)) / __uint_as_float(max(most, 0x00800000u));
@@ -30,7 +31,7 @@ __device__ __forceinline__ void table_candidates(float c, int bits, int tid, flo
   float mine[kEach], dd[kEach], rd[kEach], rr[kEach];
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    mine[k] = exp2f((float)(k * 128 + tid) * (1.0f / kSteps));
+    mine[k] = exp2f((float)(k * kThreads + tid) * (1.0f / kSteps));
     dd[k] = rd[k] = rr[k] = 0.f;
   }
 #pragma unroll 2
@@ -54,7 +55,7 @@ __device__ __forceinline__ void table_candidates(float c, int bits, int tid, flo
     if (e < least) {
       least = e;
       slope = a;
-      at = k * 128 + tid;
+      at = k * kThreads + tid;
     }
   }
 }
