@@ -44,7 +44,7 @@ struct ChunkSeq {
 };
 
 // A row block: where its partial results lie (in partials of kChunkRows rows and one kv head, all heads of a
-// partial side by side).
+// partial side by side); parts -1: nowhere, its one item stores its rows.
 struct ChunkBlock {
   int seq, row0;  // of the sequence's rows
   int part0, parts, step;
@@ -59,7 +59,7 @@ struct ChunkUnit {
   int pad[2];
 };
 
-// A work item (of every kv head): tiles first .. first + count - 1 of a unit's.
+// A work item (of every kv head): tiles first .. first + count - 1 of a unit's.  part -1: it stores its rows.
 struct ChunkItem {
   int seq, row0, tier, part;
   int first, count, sinks, begin;

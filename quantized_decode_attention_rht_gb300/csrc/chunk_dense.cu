@@ -625,6 +625,56 @@ __device__ __forceinline__ void weigh(const uint32_t (&v)[32], uint32_t see, flo
   }
 }
 
+// An accumulator row times f with the value rotation undone, as fp16: y = s H (f o).  The thread's coordinates are its
+// registers: one stage of the transform after the other (head_dim 256: its last stage first, of which each half of the
+// row is one result).  Lanes without an address only take part.
+template <int D>
+__device__ __forceinline__ void store_row(uint32_t o_at, int part, float f, const uint4* signs, uint16_t* to) {
+  constexpr int N = D == 256 ? 128 : D;
+  unsigned long long y[N / 2];
+  const unsigned long long f2 = pack2(f, f), g2 = pack2(part ? -f : f, part ? -f : f);
+#pragma unroll
+  for (int c = 0; c < N; c += 32) {
+    uint32_t v[32];
+    tc_ld32(o_at + c, v);
+    tc_wait_ld(v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) y[c / 2 + e] = mul2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f2);
+    if constexpr (D == 256) {
+      tc_ld32(o_at + 128 + c, v);
+      tc_wait_ld(v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        y[c / 2 + e] = fma2(pack2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), g2, y[c / 2 + e]);
+    }
+  }
+#pragma unroll
+  for (int step = 1; step < N / 2; step <<= 1) {
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      if (e & step) continue;
+      const unsigned long long a = y[e], c = y[e + step];
+      y[e] = add2(a, c);
+      y[e + step] = fma2(c, pack2(-1.f, -1.f), a);
+    }
+  }
+  if (!to) return;
+#pragma unroll
+  for (int k = 0; k < N / 16; ++k) {  // 16 coordinates
+    const uint4 sg = __ldg(signs + part * (N / 16) + k);
+    const uint32_t sw[4] = {sg.x, sg.y, sg.z, sg.w};
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 x = unpack2(y[8 * k + j]);
+      w[j] = half2_bits(x.x + x.y, x.x - x.y) ^ (__byte_perm(sw[j / 2], 0, (j & 1) ? 0x3424 : 0x1404) & 0x80008000u);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(to + part * N) + 2 * k;
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 template <int D, bool CODES>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __grid_constant__ ChunkParams p) {
   using X = Shape<D>;
@@ -790,32 +840,42 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
       if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * A_DONE, 0, abort, err));
       tc_fence_after();
       const bool there = item.row0 + w * kChunkRows + r < rows;
-      const size_t part = ((size_t)(item.part + w) * p.hkv + h) * kChunkRows + r;
-      if (ok) {
-        const float unit = CODES ? p.unit_of[(size_t)item.seq * p.hkv + h] : 1.f;
-        float* to = p.acc + part * D;
+      const float unit = CODES && ok ? p.unit_of[(size_t)item.seq * p.hkv + h] : 1.f;
+      const float l = unpack2(l2).x + unpack2(l2).y;
+      if (item.part < 0) {
+        // all of the row's tiles were here: the value rotation is undone in the thread's registers
+        if (ok) {
+          const float inv = l == 0.f ? 0.f : unit * inv_sqrt_dim(D) / l;
+          const int token = s.q0 + (row >> p.group_shift), head = (h << p.group_shift) + (row & (p.group - 1));
+          uint16_t* to = p.out + token * p.out_token + head * p.out_head;
+          const uint4* signs = reinterpret_cast<const uint4*>(p.v_signs + (size_t)h * D);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t v[32];
-          tc_ld32(o_at + c, v);
-          tc_wait_ld(v);
-          if (there) {
+          for (int part = 0; part < (D == 256 ? 2 : 1); ++part) store_row<D>(o_at, part, inv, signs, there ? to : nullptr);
+        }
+      } else {
+        const size_t part = ((size_t)(item.part + w) * p.hkv + h) * kChunkRows + r;
+        if (ok) {
+          float* to = p.acc + part * D;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t v[32];
+            tc_ld32(o_at + c, v);
+            tc_wait_ld(v);
+            if (there) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              float y[8];
+              for (int e = 0; e < 32; e += 8) {
+                float y[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(v[e + k]) * unit;
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + c + e),
-                           "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
-                           : "memory");
+                for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(v[e + k]) * unit;
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + c + e),
+                             "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+                             : "memory");
+              }
             }
           }
         }
-      }
-      if (there) {
         // (a row of NaN has no maximum: its partial must not pass for one without tokens)
-        const float l = unpack2(l2).x + unpack2(l2).y;
-        p.ml[part] = ok && l != 0.f ? make_float2(l == l ? m : l, l) : make_float2(-INFINITY, 0.f);
+        if (there) p.ml[part] = ok && l != 0.f ? make_float2(l == l ? m : l, l) : make_float2(-INFINITY, 0.f);
       }
     }
   } else if (warp == RT * 4) {

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
           y.seq = x.seq;
           y.row0 = r;
           y.part0 = part0 + i;
-          y.parts = c ? 2 * n : n;
+          y.parts = c ? 2 * n : (n == 1 ? -1 : n);  // (one unpacked item writes its rows itself)
           y.step = c ? 1 : per_unit;
           p.block[s.first_block + r / kChunkRows] = y;
         }
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
           y.seq = x.seq;
           y.row0 = x.row0;
           y.tier = k;
-          y.part = part0 + a_part * (before + i);
+          y.part = !c && n == 1 ? -1 : part0 + a_part * (before + i);
           y.first = min(x.n[k], i * share);
           y.count = min(x.n[k], (i + 1) * share) - y.first;
           y.sinks = x.sinks[k];
@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
     // (blocks of rows of one kv head side by side)
     const int r = (int)(x % kChunkRows), hk = (int)(x / kChunkRows % p.hkv), b = (int)(x / kChunkRows / p.hkv);
     const ChunkBlock y = p.block[b];
+    if (y.parts < 0) continue;
     const ChunkSeq& s = p.seq[y.seq];
     const int row = y.row0 + r;
     if (row >= s.tokens << p.group_shift) continue;
