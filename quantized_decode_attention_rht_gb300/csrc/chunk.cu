@@ -62,7 +62,10 @@ kvq_status chunk_plan(const ChunkCall& c, ChunkParams* p) {
     t.num_pages = k->num_pages;
     t.max_pages = usable_pages(c.tiers[i]);
     t.table_pages = c.tiers[i].max_pages;
-    if (is_codebook(k->v_format)) p->codes = 1;
+    if (is_codebook(k->v_format)) {
+      p->codes = c.num_tiers > 1 ? 2 : 1;
+      p->summed |= k->v_bits == 4;
+    }
   }
   if (room > 0x7FFFFFFFLL - 256) return KVQ_ERR_UNSUPPORTED;
   p->num_tiers = c.num_tiers;
@@ -135,7 +138,8 @@ size_t chunk_layout(ChunkParams* p, uint8_t* base) {
   p->vt = take(tiles * hkv * tile * d * 2);
   if (p->codes) {
     p->kn = reinterpret_cast<float*>(take(tiles * hkv * tile * sizeof(float)));
-    p->vn = reinterpret_cast<float*>(take(tiles * hkv * tile * sizeof(float)));
+    p->fn = reinterpret_cast<float*>(take(tiles * hkv * tile * sizeof(float)));
+    p->hn = reinterpret_cast<__half*>(take(p->summed * tiles * hkv * tile * sizeof(__half)));
     p->top = reinterpret_cast<float*>(take(tiles * hkv * sizeof(float)));
     p->unit_of = reinterpret_cast<float*>(take(p->batch * hkv * sizeof(float)));
   }

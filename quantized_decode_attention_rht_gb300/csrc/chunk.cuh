@@ -88,7 +88,8 @@ struct ChunkParams {
   const int8_t* v_signs;
   int* status;
   int batch, num_tokens, hq, hkv, group, group_shift, page_size, page_shift, window, sinks, head_dim;
-  int codes;       // some tier is of codebook keys: norms beside the unpacked tiles
+  int codes;       // norms beside the unpacked tiles: 1: the one tier is of codebooks, 2: one of several is
+  int summed;      // codebook values of four bits: weights are summed as they are rounded
   int dense_rows;  // sequences of more rows a kv head are unpacked (-1: all)
   // capacities that the workspace was laid out for
   int max_blocks, max_tiles, max_parts;
@@ -108,10 +109,11 @@ struct ChunkParams {
   uint8_t* qt;          // rotated queries of units [max_units][hkv][dense_blocks][2 parts][128 * D * 2]
   uint8_t* kt;          // unpacked keys [max_tiles][hkv][tile * D * 2], values behind them
   uint8_t* vt;
-  float* kn;            // [max_tiles][hkv][tile] factors of the scores, and of the weights
-  float* vn;
+  float* kn;            // [max_tiles][hkv][tile] factors of the scores,
+  float* fn;            // of the weights (the mantissas of the values' norms) or, where `summed`, their inverses
+  __half* hn;           // where `summed`, those factors
   float* top;           // [max_tiles][hkv] a power of two above a tile's weights' factors
-  float* unit_of;       // [batch][hkv] what the weights' factors were divided by
+  float* unit_of;       // [batch][hkv] what the values' norms were divided by
 };
 
 cudaError_t launch_dependent(const void* kernel, unsigned grid, unsigned block, size_t smem, const ChunkParams& p,

@@ -179,7 +179,7 @@ __device__ __forceinline__ uint32_t find_row(const ChunkParams& p, const ChunkSe
 // is not finite becomes zeros and is noted in s_bad; keys of such rows become NaN.
 template <int D, int F, bool VALUES>
 __device__ __forceinline__ void unpack_side(const ChunkTier& t, uint8_t* to, const uint16_t* table, const uint32_t* s_row,
-                                            int* s_bad, float factor, int* over) {
+                                            const uint32_t* s_power, int* s_bad, float factor, int* over) {
   constexpr int TT = dense_tile(D), C = D / 16, kEach = TT * C / kPrepareThreads;
   const uint8_t* rows = VALUES ? t.v_rows : t.k_rows;
   const int row_bytes = VALUES ? t.v_row_bytes : t.k_row_bytes, c = threadIdx.x % C, r0 = threadIdx.x / C;
@@ -207,7 +207,10 @@ __device__ __forceinline__ void unpack_side(const ChunkTier& t, uint8_t* to, con
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], f);
       }
-    } else if constexpr (!VALUES) {
+    } else if constexpr (VALUES) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], s_power[r]);
+    } else {
       if (s_bad[r]) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = 0x7E007E00u;
@@ -222,24 +225,24 @@ __device__ __forceinline__ void unpack_side(const ChunkTier& t, uint8_t* to, con
 }
 template <int D, bool VALUES>
 __device__ __forceinline__ void unpack_any(const ChunkTier& t, uint8_t* to, const uint16_t* table, const uint32_t* s_row,
-                                           int* s_bad, float factor, int* over) {
+                                           const uint32_t* s_power, int* s_bad, float factor, int* over) {
   switch (VALUES ? unpack_kind(t.v_fmt, t.v_bits) : unpack_kind(t.k_fmt, t.k_bits)) {
-    case U_F16: unpack_side<D, U_F16, VALUES>(t, to, table, s_row, s_bad, factor, over); break;
+    case U_F16: unpack_side<D, U_F16, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over); break;
     case U_F8:
-      if constexpr (!VALUES) unpack_side<D, U_F8, VALUES>(t, to, table, s_row, s_bad, factor, over);
+      if constexpr (!VALUES) unpack_side<D, U_F8, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over);
       break;
     case U_I4:
-      if constexpr (VALUES) unpack_side<D, U_I4, VALUES>(t, to, table, s_row, s_bad, factor, over);
+      if constexpr (VALUES) unpack_side<D, U_I4, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over);
       break;
-    case U_C4: unpack_side<D, U_C4, VALUES>(t, to, table, s_row, s_bad, factor, over); break;
-    case U_C3: unpack_side<D, U_C3, VALUES>(t, to, table, s_row, s_bad, factor, over); break;
-    default: unpack_side<D, U_C2, VALUES>(t, to, table, s_row, s_bad, factor, over);
+    case U_C4: unpack_side<D, U_C4, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over); break;
+    case U_C3: unpack_side<D, U_C3, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over); break;
+    default: unpack_side<D, U_C2, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over);
   }
 }
 
 template <int D>
 __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int h, const uint16_t (*tables)[2][16],
-                                            uint32_t* s_row, int* s_tier, int* s_bad, float* s_max) {
+                                            uint32_t* s_row, uint32_t* s_power, int* s_tier, int* s_bad, float* s_max) {
   constexpr int TT = dense_tile(D), C = D / 16;
   const int tid = threadIdx.x, lane = tid & 31;
   // the sequence: the last whose tiles begin at or before this one (unpacked ones alone have any)
@@ -267,7 +270,7 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
       int tier, ignored = 0;
       const uint32_t row = find_row(p, s, lo, h, tid, tier, &ignored);
       if (row != kNone && p.tier[tier].v_fmt == KVQ_FMT_CODEBOOK)
-        most = finite_or_zero(norm_of(p.tier[tier], 1, row) * p.head->unscale[tier][1]);
+        most = finite_or_zero(norm_of(p.tier[tier], 1, row));
       most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
       if (lane == 0) s_max[tid >> 5] = most;
     }
@@ -276,8 +279,31 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
     unit = most > 0.f ? two_above(most) : 1.0f;
     if (i == 0 && tid == 0) p.unit_of[(size_t)lo * p.hkv + h] = unit;
   }
-  __syncthreads();
   const float per_unit = 1.0f / unit;
+  // A value's norm over that is a mantissa in [1, 2), which multiplies weights, and a power of two (2^15 at most), which
+  // goes into its row: weights then keep their precision however small the value, and the sum can be taken of what is
+  // multiplied (a token that outweighs all others keeps its value).
+  float mantissa = 1.0f;
+  if (p.codes && tid < TT) {
+    float power = 1.0f;
+    const uint32_t row = s_row[tid];
+    if (row != kNone && p.tier[s_tier[tid]].v_fmt == KVQ_FMT_CODEBOOK) {
+      const float norm = norm_of(p.tier[s_tier[tid]], 1, row);
+      if (norm == 0.f) {
+        power = 0.f;
+      } else if (finite_or_zero(norm) != 0.f) {
+        const uint32_t two = __float_as_uint(norm) & 0x7F800000u;  // (an fp16 number: normal in float32)
+        power = fminf(__uint_as_float(two) * per_unit, 32768.0f);
+        mantissa = norm * per_unit / power;
+      } else {
+        mantissa = norm;
+      }
+      // (one tier's table scale comes behind the products; of several tiers it goes in here, rounded once)
+      if (p.codes > 1) mantissa = __half2float(__float2half_rn(mantissa * p.head->unscale[s_tier[tid]][1]));
+    }
+    s_power[tid] = half2_bits(power, power);
+  }
+  __syncthreads();
   const size_t at = ((size_t)tile * p.hkv + h) * (TT * D * 2);
   int over = 0;
   // One tier's tokens alone, but for those that are not there, and keys without a sketch or an outlier stream?
@@ -286,10 +312,10 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
                                         fmt != KVQ_FMT_CODEBOOK_QJL && fmt != KVQ_FMT_CODEBOOK_OUTLIER);
   if (simple) {
     const ChunkTier& t = p.tier[first];
-    unpack_any<D, true>(t, p.vt + at, tables[first][1], s_row, s_bad,
+    unpack_any<D, true>(t, p.vt + at, tables[first][1], s_row, s_power, s_bad,
                         p.codes && t.v_fmt != KVQ_FMT_CODEBOOK ? per_unit : 1.0f, &over);
     __syncthreads();
-    unpack_any<D, false>(t, p.kt + at, tables[first][0], s_row, s_bad, 1.0f, &over);
+    unpack_any<D, false>(t, p.kt + at, tables[first][0], s_row, s_power, s_bad, 1.0f, &over);
   }
   // values
   for (int u = tid; !simple && u < TT * C; u += kPrepareThreads) {
@@ -308,10 +334,10 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = 0;
       }
-      if (p.codes && t.v_fmt != KVQ_FMT_CODEBOOK) {
-        const __half2 f = __float2half2_rn(per_unit);
+      if (p.codes) {
+        const uint32_t f = t.v_fmt != KVQ_FMT_CODEBOOK ? half2_bits(per_unit, per_unit) : s_power[r];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], *reinterpret_cast<const uint32_t*>(&f));
+        for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], f);
       }
     }
     store16(p.vt + at, TT, r, c, x);
@@ -381,21 +407,16 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
     store16(p.kt + at, TT, r, c, x);
   }
   if (p.codes) {
-    float vn = 0.f;
     if (tid < TT) {
       float kn = 1.0f;
-      vn = 1.0f;
       const uint32_t row = s_row[tid];
-      if (row != kNone) {
-        const int tier = s_tier[tid];
-        const ChunkTier& t = p.tier[tier];
-        if (t.k_fmt == KVQ_FMT_CODEBOOK) kn = norm_of(t, 0, row) * p.head->unscale[tier][0];
-        if (t.v_fmt == KVQ_FMT_CODEBOOK) vn = norm_of(t, 1, row) * p.head->unscale[tier][1] * per_unit;
-      }
+      if (row != kNone && p.tier[s_tier[tid]].k_fmt == KVQ_FMT_CODEBOOK)
+        kn = norm_of(p.tier[s_tier[tid]], 0, row) * p.head->unscale[s_tier[tid]][0];
       const size_t n = ((size_t)tile * p.hkv + h) * TT + tid;
       p.kn[n] = kn;
-      p.vn[n] = vn;
-      const float most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(finite_or_zero(vn))));
+      p.fn[n] = p.summed ? 1.0f / mantissa : mantissa;
+      if (p.summed) p.hn[n] = __float2half_rn(mantissa);  // (exact: eleven bits)
+      const float most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(finite_or_zero(mantissa))));
       if (lane == 0) s_max[4 + (tid >> 5)] = most;
     }
     __syncthreads();
@@ -488,7 +509,7 @@ __device__ __forceinline__ void rotate_queries(const ChunkParams& p, int unit, i
 template <int D>
 __global__ void __launch_bounds__(kPrepareThreads, 4) prepare_kernel(const __grid_constant__ ChunkParams p) {
   constexpr int TT = dense_tile(D);
-  __shared__ uint32_t s_row[TT];
+  __shared__ uint32_t s_row[TT], s_power[TT];
   __shared__ int s_tier[TT], s_bad[TT];
   __shared__ float s_max[8];
   __shared__ uint16_t tables[KVQ_MAX_TIERS][2][16];
@@ -506,7 +527,7 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) prepare_kernel(const __gri
   __syncthreads();
   const int tiles = p.head->num_tiles * p.hkv, items = tiles + p.head->units[0] * p.hkv;
   for (int x = blockIdx.x; x < items; x += gridDim.x) {
-    if (x < tiles) unpack_tile<D>(p, x / p.hkv, x % p.hkv, tables, s_row, s_tier, s_bad, s_max);
+    if (x < tiles) unpack_tile<D>(p, x / p.hkv, x % p.hkv, tables, s_row, s_power, s_tier, s_bad, s_max);
     else rotate_queries<D>(p, (x - tiles) / p.hkv, (x - tiles) % p.hkv);
   }
 }
@@ -532,7 +553,7 @@ struct Shape {
   static constexpr int kBuffers = D == 64 ? 6 : 3;
   static constexpr int kNormStages = RT == 1 ? 3 : (kBuffers + 2) / 2;  // a stage is free before the keys that need it are loaded
   static constexpr int kOffRing = RT * kQBytes, kOffNorm = kOffRing + kBuffers * kTileBytes;
-  static constexpr int kNormBytes = 2 * TT * 4;
+  static constexpr int kNormBytes = 10 * TT;  // factors of a tile's scores and of its weights (weigh)
   static constexpr int kOffCtl = kOffNorm + kNormStages * kNormBytes;
   static constexpr int kSmem = kOffCtl + 512;
   static constexpr int kThreads = RT * 128 + 64;
@@ -577,16 +598,28 @@ __device__ __forceinline__ void scale_row(uint32_t at, float f) {
   }
 }
 
-// 32 scores -> 16 weight pairs and their sum.  HIDE: columns that are not in `see` weigh nothing, whatever they hold.
-template <bool CODES, bool HIDE>
-__device__ __forceinline__ void weigh(const uint32_t (&v)[32], uint32_t see, float m, const float* kn, const float* vn,
-                                      uint32_t* h, unsigned long long& s0, unsigned long long& s1) {
+// What an item's tiles hold: values as they are; or codebooks, whose norms are factors of scores and weights, with the sum
+// of the weights as they are (kCodes) or of the weights that the rounded products stand for (kCodesSummed).  Values of four
+// bits take the last: a token that outweighs all others then keeps its value, 2.8e-4 of the output instead of 3.4e-4, for
+// 268 instead of 250 us of a 4096-token prompt x 32 heads; those of two and three bits, whose fewer centroids lose less,
+// stay below 2.9e-4 without (337 instead of 360 us for 16 ragged chunks on 8000 tokens).
+enum { kValues, kCodes, kCodesSummed };
+
+// 32 scores -> 16 weight pairs (codebooks: times the values' factors) and their sum.  HIDE: columns that are not in `see`
+// weigh nothing, whatever they hold.  fn: the factors (kCodes) or their inverses; hn: the factors as fp16, exact.
+template <int KIND, bool HIDE>
+__device__ __forceinline__ void weigh(const uint32_t (&v)[32], uint32_t see, float m, const float* kn, const float* fn,
+                                      const uint2* hn, uint32_t* h, unsigned long long& s0, unsigned long long& s1) {
   const unsigned long long neg = pack2(-m, -m);
+  auto hide = [&](unsigned long long x, int e) {
+    const float2 y = unpack2(x);
+    return pack2(see >> e & 1u ? y.x : 0.f, see >> (e + 1) & 1u ? y.y : 0.f);
+  };
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
     unsigned long long t0 = pack2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
     unsigned long long t1 = pack2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-    if constexpr (CODES) {  // scores are multiplied by the keys' norms
+    if constexpr (KIND != kValues) {  // scores are multiplied by the keys' norms
       const float4 n = *reinterpret_cast<const float4*>(kn + e);
       t0 = fma2(t0, pack2(n.x, n.y), neg);
       t1 = fma2(t1, pack2(n.z, n.w), neg);
@@ -595,32 +628,46 @@ __device__ __forceinline__ void weigh(const uint32_t (&v)[32], uint32_t see, flo
       t1 = add2(t1, neg);
     }
     const float2 x = unpack2(t0), y = unpack2(t1);
-    float a0 = ex2(x.x), a1 = ex2(x.y), a2 = ex2(y.x), a3 = ex2(y.y);
+    unsigned long long a = pack2(ex2(x.x), ex2(x.y)), b = pack2(ex2(y.x), ex2(y.y));
     if constexpr (HIDE) {
-      a0 = see >> e & 1u ? a0 : 0.f;
-      a1 = see >> (e + 1) & 1u ? a1 : 0.f;
-      a2 = see >> (e + 2) & 1u ? a2 : 0.f;
-      a3 = see >> (e + 3) & 1u ? a3 : 0.f;
+      a = hide(a, e);
+      b = hide(b, e + 2);
     }
-    if constexpr (CODES) {
-      s0 = add2(s0, pack2(a0, a1));
-      s1 = add2(s1, pack2(a2, a3));
-      const float4 n = *reinterpret_cast<const float4*>(vn + e);
-      const float2 u = unpack2(mul2(pack2(a0, a1), pack2(n.x, n.y))), w = unpack2(mul2(pack2(a2, a3), pack2(n.z, n.w)));
-      a0 = u.x, a1 = u.y, a2 = w.x, a3 = w.y;
-      if constexpr (HIDE) {  // (a norm may be infinite)
-        a0 = see >> e & 1u ? a0 : 0.f;
-        a1 = see >> (e + 1) & 1u ? a1 : 0.f;
-        a2 = see >> (e + 2) & 1u ? a2 : 0.f;
-        a3 = see >> (e + 3) & 1u ? a3 : 0.f;
-      }
+    if constexpr (KIND == kCodes) {
+      s0 = add2(s0, a);
+      s1 = add2(s1, b);
+      const float4 n = *reinterpret_cast<const float4*>(fn + e);
+      a = mul2(a, pack2(n.x, n.y));
+      b = mul2(b, pack2(n.z, n.w));
     }
-    h[e / 2] = half2_bits(a0, a1);
-    h[e / 2 + 1] = half2_bits(a2, a3);
-    if constexpr (!CODES) {  // the sum of what is multiplied: a token that outweighs all others keeps its value
+    if constexpr (KIND == kCodesSummed) {
+      const uint2 n = hn[e / 4];
+      const float2 n0 = unpack_half2(n.x), n1 = unpack_half2(n.y);
+      a = mul2(a, pack2(n0.x, n0.y));
+      b = mul2(b, pack2(n1.x, n1.y));
+    }
+    if constexpr (HIDE && KIND != kValues) {  // (a factor may be infinite)
+      a = hide(a, e);
+      b = hide(b, e + 2);
+    }
+    const float2 p = unpack2(a), q = unpack2(b);
+    h[e / 2] = half2_bits(p.x, p.y);
+    h[e / 2 + 1] = half2_bits(q.x, q.y);
+    if constexpr (KIND != kCodes) {
       const float2 u = unpack_half2(h[e / 2]), w = unpack_half2(h[e / 2 + 1]);
-      s0 = add2(s0, pack2(u.x, u.y));
-      s1 = add2(s1, pack2(w.x, w.y));
+      if constexpr (KIND == kCodesSummed) {
+        const float4 n = *reinterpret_cast<const float4*>(fn + e);
+        unsigned long long n0 = pack2(n.x, n.y), n1 = pack2(n.z, n.w);
+        if constexpr (HIDE) {
+          n0 = hide(n0, e);
+          n1 = hide(n1, e + 2);
+        }
+        s0 = fma2(pack2(u.x, u.y), n0, s0);
+        s1 = fma2(pack2(w.x, w.y), n1, s1);
+      } else {
+        s0 = add2(s0, pack2(u.x, u.y));
+        s1 = add2(s1, pack2(w.x, w.y));
+      }
     }
   }
 }
@@ -675,9 +722,10 @@ __device__ __forceinline__ void store_row(uint32_t o_at, int part, float f, cons
   }
 }
 
-template <int D, bool CODES>
+template <int D, int KIND>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __grid_constant__ ChunkParams p) {
   using X = Shape<D>;
+  constexpr bool CODES = KIND != kValues;
   constexpr int TT = X::TT, RT = X::RT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t smem = smem_u32(smem_raw);
@@ -751,7 +799,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
         const int b = RT == 2 ? w : i & 1;
         const uint32_t s_at = lane_base + b * TT;
         const float* kn = reinterpret_cast<const float*>(smem_raw + X::kOffNorm + i % X::kNormStages * X::kNormBytes);
-        const float* vn = kn + TT;
+        const float* fn = kn + TT;
+        const uint2* hn = reinterpret_cast<const uint2*>(fn + TT);
         top = next_top;
         if (CODES && i + 1 < n) next_top = __ldg(tops + (size_t)(s.tile0 + tile_of(i + 1)) * p.hkv);
         // columns below `end`, and from `begin` on or below `first`
@@ -811,12 +860,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
           for (int c = 0; c < TT; c += 64) {
             tc_wait_ld_only(va);
             tc_ld32(s_at + c + 32, vb);
-            if (all) weigh<CODES, false>(va, 0, m, kn + c, vn + c, g + c / 2, s0, s1);
-            else weigh<CODES, true>(va, see(c), m, kn + c, vn + c, g + c / 2, s0, s1);
+            if (all) weigh<KIND, false>(va, 0, m, kn + c, fn + c, hn + c / 4, g + c / 2, s0, s1);
+            else weigh<KIND, true>(va, see(c), m, kn + c, fn + c, hn + c / 4, g + c / 2, s0, s1);
             tc_wait_ld_only(vb);
             if (c + 64 < TT) tc_ld32(s_at + c + 64, va);
-            if (all) weigh<CODES, false>(vb, 0, m, kn + c + 32, vn + c + 32, g + c / 2 + 16, s0, s1);
-            else weigh<CODES, true>(vb, see(c + 32), m, kn + c + 32, vn + c + 32, g + c / 2 + 16, s0, s1);
+            if (all) weigh<KIND, false>(vb, 0, m, kn + c + 32, fn + c + 32, hn + c / 4 + 8, g + c / 2 + 16, s0, s1);
+            else weigh<KIND, true>(vb, see(c + 32), m, kn + c + 32, fn + c + 32, hn + c / 4 + 8, g + c / 2 + 16, s0, s1);
           }
           sum = add2(s0, s1);
           const float2 t = unpack2(sum);
@@ -840,8 +889,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
       if (ok) ok = __all_sync(0xFFFFFFFFu, bar_wait(bars + 8 * A_DONE, 0, abort, err));
       tc_fence_after();
       const bool there = item.row0 + w * kChunkRows + r < rows;
-      const float unit = CODES && ok ? p.unit_of[(size_t)item.seq * p.hkv + h] : 1.f;
       const float l = unpack2(l2).x + unpack2(l2).y;
+      const float unit = CODES && ok ? p.unit_of[(size_t)item.seq * p.hkv + h] * (p.codes == 1 ? p.head->unscale[0][1] : 1.f) : 1.f;
       if (item.part < 0) {
         // all of the row's tiles were here: the value rotation is undone in the thread's registers
         if (ok) {
@@ -994,9 +1043,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
         bulk_load(smem + X::kOffRing + slot * X::kTileBytes, (value ? p.vt : p.kt) + tile * X::kTileBytes, X::kTileBytes, bar);
         if (CODES && !value) {  // (a stage's norms have been read: the keys' buffer waits for later products)
           const uint32_t to = smem + X::kOffNorm + i % X::kNormStages * X::kNormBytes, nbar = bars + 8 * (A_N + i % X::kNormStages);
-          bar_expect(nbar, X::kNormBytes);
+          bar_expect(nbar, (KIND == kCodesSummed ? 10 : 8) * TT);
           bulk_load(to, p.kn + tile * TT, TT * 4, nbar);
-          bulk_load(to + TT * 4, p.vn + tile * TT, TT * 4, nbar);
+          bulk_load(to + TT * 4, p.fn + tile * TT, TT * 4, nbar);
+          if (KIND == kCodesSummed) bulk_load(to + TT * 8, p.hn + tile * TT, TT * 2, nbar);
           norms = i + 1;
         }
         issued = load + 1;
@@ -1018,9 +1068,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
   if (warp == RT * 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(X::kColumns));
 }
 
-template <int D, bool CODES>
+template <int D, int KIND>
 cudaError_t launch_attend(const ChunkParams& p, cudaStream_t stream) {
-  auto kern = attend_kernel<D, CODES>;
+  auto kern = attend_kernel<D, KIND>;
   static std::atomic<bool> configured[64];  // shared-memory limit raised on this device (a racing second raise is
                                             // harmless)
   int dev = 0;
@@ -1048,9 +1098,14 @@ cudaError_t launch_chunk_prepare(const ChunkParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_chunk_dense(const ChunkParams& p, cudaStream_t stream) {
-  if (p.head_dim == 64) return p.codes ? launch_attend<64, true>(p, stream) : launch_attend<64, false>(p, stream);
-  if (p.head_dim == 128) return p.codes ? launch_attend<128, true>(p, stream) : launch_attend<128, false>(p, stream);
-  return p.codes ? launch_attend<256, true>(p, stream) : launch_attend<256, false>(p, stream);
+  auto kind = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    if (!p.codes) return launch_attend<D, kValues>(p, stream);
+    return p.summed ? launch_attend<D, kCodesSummed>(p, stream) : launch_attend<D, kCodes>(p, stream);
+  };
+  if (p.head_dim == 64) return kind(std::integral_constant<int, 64>{});
+  if (p.head_dim == 128) return kind(std::integral_constant<int, 128>{});
+  return kind(std::integral_constant<int, 256>{});
 }
 
 }  // namespace kvq
