@@ -537,15 +537,20 @@ typedef struct kvq_visible {
  *   workspace : >= kvq_chunk_workspace_size() bytes for the same sizes and block tables, 256-byte
  *               aligned, scratch only.  Calls that may overlap on the GPU need one each
  *   status    : optional device int32: the call's KVQ_DEVERR_* bits (as in kvq_decode_options; not
- *               written by a call with batch 0 or num_tokens 0).  A token whose page lies outside
- *               the pool reads as zeros here
+ *               written by a call with batch 0 or num_tokens 0).  Tokens whose page lies outside
+ *               the pool read as zeros, or are left out with their share of the context
  * Offsets, lengths and block tables are read on the device when the call runs, also in a captured
  * graph.  Sign vectors 16-byte aligned; num_tokens x num_q_heads at most 2^26, batch at most 65536,
- * block tables of less than 2^31 - 256 tokens together and pools of less than 2^32 - 1 rows a side
- * (else KVQ_ERR_UNSUPPORTED).
+ * block tables of at most 2^30 tokens together and pools of less than 2^32 - 1 rows a side (else
+ * KVQ_ERR_UNSUPPORTED).
+ * Sequences of more than 512 rows (new tokens x query heads a kv head), and all where the formats or
+ * head_dim are not those that kvq_decode_attention_shared decodes on the tensor cores, are unpacked
+ * first: the workspace then holds 4 x head_dim bytes for every token and kv head that they may see
+ * (with a window: the windows, sinks and chunks).
  * The output is fp16, and so is what the tensor cores multiply (rotated queries as the sum of two
  * numbers, decoded rows that are not fp16 values already and softmax weights as one), with float32
- * scores, sums and accumulators.  The magnitudes of a query's elements may sum to at most 45000 x
+ * scores, sums and accumulators: the output's error is 2^-12 to 2^-11.7 of its size (2-norm over the
+ * outputs, on caches with outlier channels; 0.42 2^-11 is its own rounding).  The magnitudes of a query's elements may sum to at most 45000 x
  * head_dim.  INT4 scales above 9352 are reported (KVQ_DEVERR_VALUE_RANGE).  A cached vector that is
  * not finite gives NaN in the outputs of the queries that see it (its key alone may also give them no
  * weight), and does not reach the others. */
@@ -560,8 +565,10 @@ KVQ_API kvq_status kvq_chunk_attention(const kvq_tier_view* tiers, int32_t num_t
 /* Decode attention of layers with a sliding window: one query per sequence, its newest cached token
  * (p = L_b - 1), over the positions that it sees.  Reads the sinks' and the window's pages only.
  *   q, out : fp16 [batch][num_q_heads][head_dim], 16-byte aligned
- * The rest as in kvq_chunk_attention with one token a sequence; kvq_decode_window_workspace_size
- * gives the workspace.  visible NULL or with window 0 sees everything. */
+ * Runs on kvq_decode_attention's kernels, whose float32 result is rounded once, within their limits (and,
+ * beyond them, as a kvq_chunk_attention call).  The rest as in kvq_chunk_attention with one token a
+ * sequence; kvq_decode_window_workspace_size gives the workspace.  visible NULL or with window 0 sees
+ * everything. */
 KVQ_API kvq_status kvq_decode_window_workspace_size(const kvq_tier_view* tiers, int32_t num_tiers, int32_t batch,
                                                     int32_t num_q_heads, const kvq_visible* visible, size_t* bytes);
 KVQ_API kvq_status kvq_decode_attention_window(const kvq_tier_view* tiers, int32_t num_tiers, const uint16_t* q,

@@ -15,6 +15,9 @@ namespace {
 // them 2 us a tile of unpacked ones, and the unpacking as much once more.
 constexpr int kDenseRows = 512;
 
+// Tokens of a sequence at most: positions, and their distances over windows, then stay in 32 bits.
+constexpr long long kMostTokens = 1LL << 30;
+
 struct ChunkCall {
   const kvq_tier_view* tiers;
   int num_tiers, batch, num_tokens, hq;
@@ -67,7 +70,7 @@ kvq_status chunk_plan(const ChunkCall& c, ChunkParams* p) {
       p->summed |= k->v_bits == 4;
     }
   }
-  if (room > 0x7FFFFFFFLL - 256) return KVQ_ERR_UNSUPPORTED;
+  if (room > kMostTokens) return KVQ_ERR_UNSUPPORTED;
   p->num_tiers = c.num_tiers;
   p->k_signs = c0->k_signs;
   p->v_signs = c0->v_signs;
@@ -79,8 +82,8 @@ kvq_status chunk_plan(const ChunkCall& c, ChunkParams* p) {
   while ((1 << p->group_shift) < p->group) ++p->group_shift;
   p->page_size = c0->page_size;
   p->page_shift = page_shift_of(c0->page_size);
-  p->window = c.visible ? c.visible->window : 0;
-  p->sinks = c.visible ? c.visible->sinks : 0;
+  p->window = c.visible ? (int)std::min<long long>(c.visible->window, kMostTokens) : 0;  // (all there can be)
+  p->sinks = c.visible ? (int)std::min<long long>(c.visible->sinks, kMostTokens) : 0;
   p->head_dim = d;
   p->sms = device_sms();
   // Sequences of few rows stay packed where the prefix kernel takes all formats; a batch of long chunks is unpacked as

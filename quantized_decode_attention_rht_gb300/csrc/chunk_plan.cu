@@ -278,10 +278,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         for (int k = 0; k < p.num_tiers; ++k) {
           const int end = k + 1 < p.num_tiers ? s.base[k + 1] : s.len;
           const int lo = max(0, x.lo - s.base[k]), hi = min(x.hi, end) - s.base[k];
-          u.begin[k] = lo / kMaskedTile;
+          // (of a tier that ends before the window, the sinks alone)
+          u.begin[k] = hi > lo ? lo / kMaskedTile : ceil_div(max(0, hi), kMaskedTile);
           u.sinks[k] = min(max(0, ceil_div(min(x.sinks, end) - s.base[k], kMaskedTile)), u.begin[k]);
-          u.n[k] = u.sinks[k] + max(0, ceil_div(hi, kMaskedTile) - u.begin[k]);
-          if (hi <= lo) u.n[k] = u.sinks[k];
+          u.n[k] = u.sinks[k] + max(0, ceil_div(max(0, hi), kMaskedTile) - u.begin[k]);
           n_most = max(n_most, u.n[k]);
         }
       }

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(128) narrow_kernel(const __grid_constant__ Nar
     }
     all += n;
   }
-  const int from = min(len, max(0, all - p.window - base)), first = min(from, max(0, p.sinks - base));
+  const int from = min(len, max(0, max(0, all - p.window) - base)), first = min(from, max(0, p.sinks - base));
   const int page1 = from / ps, pages0 = min((first + ps - 1) / ps, page1);  // the second run's first page, the first run's pages
   const int pages = pages0 + (len + ps - 1) / ps - page1, moved = (page1 - pages0) * ps;
   const int32_t* row = t.table + (size_t)b * t.table_pages;
@@ -114,7 +114,7 @@ bool narrowed(const kvq_tier_view* tiers, int n, int batch, int hq, int window, 
       t.max_pages = usable_pages(tiers[i]);
       t.table_pages = tiers[i].max_pages;
       // (a run of m tokens touches at most (m - 1) / ps + 2 pages)
-      t.to_pages = (int)std::min<long long>(t.max_pages, (sinks + ps - 1LL) / ps + (window + ps - 1LL) / ps + 1);
+      t.to_pages = (int)std::min<long long>(t.max_pages, (sinks + (ps - 1LL)) / ps + (window + (ps - 1LL)) / ps + 1);
       t.to_table = reinterpret_cast<int32_t*>(take((size_t)batch * t.to_pages * 4));
       t.to_lens = reinterpret_cast<int32_t*>(take((size_t)batch * 4));
       t.hidden = reinterpret_cast<int2*>(take((size_t)batch * 8));
@@ -158,7 +158,7 @@ cudaError_t window_run(const kvq_tier_view* tiers, int num_tiers, const uint16_t
     const int ps = c0->page_size;
     for (int i = 0; i < num_tiers; ++i) {
       p.tier[i].hidden = x.narrow.tier[i].hidden;
-      p.tier[i].hide_end = (int)std::min<long long>(((sinks + ps - 1LL) / ps + 1) * ps, 0x7FFFFFFF);
+      p.tier[i].hide_end = (int)std::min<long long>(((sinks + (ps - 1LL)) / ps + 1) * ps, 0x7FFFFFFF);
     }
     p.more_bits = x.narrow.bits;
     x.narrow.counters = counters;

@@ -196,7 +196,7 @@ def test_decode_window(name, d, window, sinks):
 @pytest.mark.parametrize("specs,lens", [(["fp8_int4", "fp16"], [[300, 0, 128, 7], [64, 33, 0, 1]]),
                                         (["cb4", "fp16"], [[300, 0, 128, 7], [64, 33, 0, 1]]),
                                         (["cb32", "cb4", "fp8_int4", "fp16"], [[130, 5, 0, 16], [100, 0, 2, 16], [40, 7, 0, 16], [50, 1, 1, 16]])])
-@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 9)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 9), (5, 200), (30, 140)])
 @pytest.mark.parametrize("hq", [4, 16])
 def test_tiers(specs, lens, window, sinks, hq):
     """Tokens of several tiers, one tier after the other; chunks that reach across them, and tiers that a sequence has not."""
@@ -204,6 +204,9 @@ def test_tiers(specs, lens, window, sinks, hq):
     counts = [80, 20, 2, 3]
     c = Case(kvq, torch, specs, lens, counts, hq=hq, hkv=2, window=window, sinks=sinks, seed=len(specs))
     c.check(c.run(kvq, torch))
+    c = Case(kvq, torch, specs, lens, [1] * 4, hq=hq, hkv=2, window=window, sinks=sinks, seed=len(specs))
+    c.check(c.run(kvq, torch))
+    c.check(c.run(kvq, torch, decode=True))
 
 
 @pytest.mark.parametrize("ps", [1, 3, 8, 24, 128, 200])
@@ -435,3 +438,106 @@ def test_another_stream_and_calls_at_once():
     torch.cuda.synchronize()
     for x, (_, _, out, *_) in zip(want, jobs):
         assert np.array_equal(out.cpu().numpy(), x)
+
+
+def test_without_offsets_and_without_a_window():
+    """One token a sequence by NULL offsets, and the decode form that sees everything: kvq_decode_attention's, rounded."""
+    torch, kvq = modules()
+    for name, d in (("fp8_int4", 128), ("cb4", 128), ("fp16", 64)):
+        c = Case(kvq, torch, [name], [[700, 0, 1, 65, 300]], [1] * 5, hq=8, hkv=2, d=d, seed=11)
+        q = torch.from_numpy(c.q).cuda()
+        out = torch.empty_like(q)
+        ws = torch.empty(kvq.kvq_chunk_workspace_size(c.views, 5, 5, 8), dtype=torch.uint8, device="cuda")
+        kvq.kvq_chunk_attention(c.views, None, q, out, ws)
+        assert np.array_equal(out.cpu().numpy(), c.run(kvq, torch))
+        full = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+        ws = torch.empty(kvq.kvq_decode_workspace_size(c.views, 5, 8), dtype=torch.uint8, device="cuda")
+        kvq.kvq_decode_attention(c.views, q, full, ws)
+        assert np.array_equal(c.run(kvq, torch, decode=True), full.half().cpu().numpy())
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 0), (1, 2 ** 31 - 1), (2 ** 30, 5)])
+def test_largest_windows(window, sinks):
+    """Windows and sinks beyond any sequence, for chunks longer than theirs too."""
+    torch, kvq = modules()
+    for counts in ([30, 40], [1, 1]):
+        c = Case(kvq, torch, ["cb4", "fp16"], [[200, 5], [20, 3]], counts, hq=2, hkv=1, window=window, sinks=sinks, seed=1)
+        c.check(c.run(kvq, torch))
+    c.check(c.run(kvq, torch, decode=True))
+
+
+@pytest.mark.parametrize("d,hq", [(128, 2), (128, 16), (64, 2)])
+def test_pools_beyond_four_gigabytes(d, hq):
+    """Pages whose rows lie beyond 2^32 bytes of a pool: packed, unpacked, and under a window."""
+    torch, kvq = modules()
+    ps, hkv = 16, 2
+    c = Case(kvq, torch, ["fp16"], [[300, 90]], [70, 9], hq=hq, hkv=hkv, d=d, window=200, sinks=3, seed=2)
+    small = c.built.gpu[0]
+    pages = 2 ** 32 // (ps * hkv * d * 2) + 1000
+    far = kvq.PagedCache(d, hkv, pages, "fp16", "fp16", 0, 0, small.k_signs, small.v_signs, ps)
+    n = small.num_pages
+    far.k_rows[-n:], far.v_rows[-n:] = small.k_rows, small.v_rows
+    want, one = c.run(kvq, torch), None
+    c.views[0] = kvq.TierView(far, c.views[0].block_table + (pages - n), c.views[0].seq_lens)
+    assert np.array_equal(c.run(kvq, torch), want)
+    q = torch.from_numpy(c.q[[69, 78]]).cuda()
+    got, ws = torch.empty_like(q), torch.empty(kvq.kvq_decode_window_workspace_size(c.views, 2, hq, 200, 3), dtype=torch.uint8, device="cuda")
+    kvq.kvq_decode_attention_window(c.views, q, got, ws, 200, 3)
+    keep, c.q = c.q, c.q[[69, 78]]
+    c.check(got.cpu().numpy(), offsets=[0, 1, 2])
+    c.q = keep
+
+
+@pytest.mark.parametrize("name,count", [("cb4", 20), ("cb4", 300), ("cb32", 300), ("cb4+fp16", 300), ("cb4+fp16", 20)])
+def test_values_of_very_different_sizes(name, count):
+    """Values that grow and shrink by powers of two along the context, zero among them, under scores that favour the small ones:
+    weights have to keep their precision whatever the values' norms."""
+    torch, kvq = modules()
+
+    def edit(tier, b, k, v):
+        t = np.arange(len(v))
+        v *= (2.0 ** ((t * 7) % 17 - 10.0))[:, None, None].astype(np.float16)
+        v[::5] = 0
+        k *= np.where(t % 5 == 0, 1.5, 0.7)[:, None, None].astype(np.float16)
+    specs = name.split("+")
+    lens = [[700]] if len(specs) == 1 else [[500], [200]]
+    c = Case(kvq, torch, specs, lens, [count], hq=2, hkv=1, seed=12, edit=edit)
+    c.check(c.run(kvq, torch), set(range(0, count, 11)))
+
+
+def test_append_then_chunk_then_decode():
+    """As a serving loop uses them: a prompt in chunks, turned and appended, attended under a window, then steps of one
+    token; each against a call over the whole prompt."""
+    torch, kvq = modules()
+    rng = np.random.default_rng(0)
+    d, hkv, hq, ps, total, window, sinks = 128, 2, 8, 16, 420, 96, 4
+    ks, vs = kvq.kvq_make_signs(1, 0, hkv, d)
+    rope = kvq.Rope(d, base=10000.0)
+    x = torch.from_numpy(rng.standard_normal((total, hq + 2 * hkv, d)).astype(np.float16)).cuda()
+    positions = torch.arange(total, dtype=torch.int32, device="cuda")
+
+    def cache():
+        return kvq.PagedCache(d, hkv, total // ps + 2, "fp8_e4m3", "int4_g32", 0, 0, ks, vs, ps)
+    table = torch.from_numpy(rng.permutation(total // ps + 2)[None].astype(np.int32)).cuda()
+    slots = (table[0].long()[positions.long() // ps] * ps + positions.long() % ps).to(torch.int32)
+
+    def attend(c, first, last, one):
+        q = torch.empty((last - first, hq, d), dtype=torch.float16, device="cuda")
+        part = x[first:last]
+        kvq.kvq_rope_append(c.struct, rope, positions[first:last], part[:, hq:hq + hkv], part[:, hq + hkv:], slots[first:last],
+                            part[:, :hq], q)
+        views = [kvq.TierView(c, table, torch.tensor([last], dtype=torch.int32, device="cuda"))]
+        out = torch.empty_like(q)
+        if one:
+            ws = torch.empty(kvq.kvq_decode_window_workspace_size(views, 1, hq, window, sinks), dtype=torch.uint8, device="cuda")
+            kvq.kvq_decode_attention_window(views, q, out, ws, window, sinks)
+        else:
+            ws = torch.empty(kvq.kvq_chunk_workspace_size(views, 1, last - first, hq, window, sinks), dtype=torch.uint8, device="cuda")
+            kvq.kvq_chunk_attention(views, torch.tensor([0, last - first], dtype=torch.int32, device="cuda"), q, out, ws, window, sinks)
+        return out
+    whole = attend(cache(), 0, total, False).float()
+    c = cache()
+    parts = [attend(c, a, b, False) for a, b in ((0, 200), (200, 201), (201, 417))] + [attend(c, t, t + 1, True) for t in range(417, total)]
+    got = torch.cat(parts).float()
+    # each side is within 2^-9 of the exact result (2-norm), and so of the other within twice that
+    assert float((got - whole).norm() / whole.norm()) <= 2.0 ** -8
