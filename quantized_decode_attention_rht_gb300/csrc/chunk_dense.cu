@@ -598,6 +598,15 @@ __device__ __forceinline__ void scale_row(uint32_t at, float f) {
   }
 }
 
+// A pair of fp16 numbers added to two float32 sums, without conversions between.
+__device__ __forceinline__ unsigned long long add_halves(unsigned long long sum, uint32_t h) {
+  float2 s = unpack2(sum);
+  asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %2;\nadd.rn.f32.f16 %0, lo, %0;\nadd.rn.f32.f16 %1, hi, %1;\n}"
+      : "+f"(s.x), "+f"(s.y)
+      : "r"(h));
+  return pack2(s.x, s.y);
+}
+
 // What an item's tiles hold: values as they are; or codebooks, whose norms are factors of scores and weights, with the sum
 // of the weights as they are (kCodes) or of the weights that the rounded products stand for (kCodesSummed).  Values of four
 // bits take the last: a token that outweighs all others then keeps its value, 2.8e-4 of the output instead of 3.4e-4, for
@@ -665,8 +674,8 @@ __device__ __forceinline__ void weigh(const uint32_t (&v)[32], uint32_t see, flo
         s0 = fma2(pack2(u.x, u.y), n0, s0);
         s1 = fma2(pack2(w.x, w.y), n1, s1);
       } else {
-        s0 = add2(s0, pack2(u.x, u.y));
-        s1 = add2(s1, pack2(w.x, w.y));
+        s0 = add_halves(s0, h[e / 2]);
+        s1 = add_halves(s1, h[e / 2 + 1]);
       }
     }
   }
