@@ -3,7 +3,7 @@
 //
 //   S = q~ K^T,  P = 2^(S - m),  O += P V,  l += rowsum P,
 // with rotated queries q~ (times log2 e / sqrt(D)) and the rotated keys and values as the cache holds them; the
-// value rotation is undone where partial results are joined.
+// value rotation is undone where results are stored or joined.
 //
 // prepare_kernel writes every operand as the products read it (rows of 128 bytes, 16-byte pieces swizzled), so that
 // attention loads whole tiles by one bulk copy each:
@@ -11,15 +11,25 @@
 //             which keys with outlier channels turn into 6e-4 of the output
 //   keys      fp16 and fp8 keys as they are; of codebooks the centroid under its table's scale, and the key's norm as
 //             a factor of its scores; keys with a sketch or outliers as one fp16 number
-//   values    fp16 as they are, INT4 levels times their scale (one rounding); of codebooks the centroid, and the norm
-//             as a factor of the weights.
+//   values    fp16 as they are, INT4 levels times their scale (one rounding); of codebooks the centroid times the
+//             norm's power of two, and the norm's mantissa as a factor of the weights.
 // Why unpack: a unit's products over 128 tokens take about 2 us on an SM, decoding the tokens 1.4 us; a chunk of 2048
 // tokens with four query heads a kv head would decode each token 32 times.
+// Bounded by memory: a token's row is read once, 4 head_dim bytes a kv head are written, and written back where they
+// pass the L2.  75 us for 32768 tokens x 8 heads of fp8 keys and INT4 values (286 MB, 3.8 TB/s), 160 us for 2 x 16896
+// tokens x 16 heads x 256 of 4-bit codes.  (Rows of the next tile loaded ahead, or a key's and a value's together, took
+// the same time.)
 //
 // attend_kernel: one item (tiles of a unit) a block of 10 warps: 2 x 4 softmax warps, a thread a row of two blocks of
 // 128 rows; one warp that loads, one that issues products.  While one row block's scores become weights, the other's
 // products run.  TMEM: two blocks of scores, over which the weights are written, and two accumulators, all 512
 // columns at head_dim 128.  (head_dim 256: one row block, tiles of 64 tokens, two score blocks in turn.)
+// Bounded by the products: 4096 tokens x 32/8 heads on 28672 of fp8 keys and INT4 values take 1960 us, unpacking among
+// them: 1.05 PFLOP/s, 1.57 with the queries' second part.  A pair of row blocks over 128 tokens takes 3770 cycles,
+// 3070 of them products; what is left is the wait for the weights at a tile's turn.  Codebooks, and head_dim 64, whose
+// products are half as long, are bounded by the softmax warps' issue slots: 270 us for a prompt of 4096 tokens x 32
+// heads of 4-bit codes, 154 us for 3 x 777 tokens x 16/4 heads x 64 on 5001.  (Two threads a row took the same time; a
+// quarter to a third of the powers as polynomials, beside the special-function unit, up to a fifth longer.)
 #include <algorithm>
 #include <atomic>
 #include <type_traits>

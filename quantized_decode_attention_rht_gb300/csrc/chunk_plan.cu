@@ -4,6 +4,8 @@
 //   last token),
 //   which sequences are unpacked (many rows: chunk_dense.cu) and where their unpacked tiles lie,
 //   how the tiles are split where there are too few row blocks to fill the GPU.
+// Bounded by latency: 7 to 13 us of dependent loads, scans and barriers, with one sequence or 64; most for codebooks,
+// whose tables' scales are chosen here too.  Everything of the call waits for it.
 #include "chunk.cuh"
 #include "rotate.cuh"
 #include "table_scale.cuh"
@@ -139,8 +141,8 @@ __device__ __forceinline__ Seen seen_by(const ChunkParams& p, const ChunkSeq& s,
 }
 
 // Tokens per split, in tiles, of class c (0: unpacked, 1: packed): the cheapest of the longest unit's
-// tiles over 1, 2, ... 160.  Time in tiles: an item is its tiles and a fixed start and end; partial results cost
-// their pass through memory.
+// tiles over 1, 2, ... 160.  Time in tiles (of 2 and 1.45 us): an item is its tiles and a fixed start and end, about 6
+// and 7 us; partial results cost their pass through memory.
 __device__ __forceinline__ int choose_per(const ChunkParams& p, int c, const ChunkUnit* unit, int units, int longest,
                                           unsigned long long* best) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

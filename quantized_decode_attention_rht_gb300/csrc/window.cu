@@ -7,7 +7,9 @@
 // is seen, in whole pages, once.
 //
 // narrow_kernel writes tables, lengths and intervals, a block a sequence and tier; bounded by its launch and a
-// chain of two loads.
+// chain of two loads, 3.5 us.  The calls are bounded as their decode kernels are: 64 x 32/8 heads on 4100 tokens of fp8
+// keys and INT4 values 100 us (56% of the copy rate), 16 x 32 heads on 2064 of 4-bit codes 68 us, 32 x 16/8 heads x 256 on
+// up to 1037 of 3/2-bit codes 53 us; 1 x 8 heads on 516 of 4-bit codes 18.5 us, three launches and the loads' latency.
 #include "window.cuh"
 
 #include "api_checks.cuh"
