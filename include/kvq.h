@@ -507,7 +507,7 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
                                                size_t workspace_bytes, int32_t* status, void* stream);
 
 /* ---- chunks of new tokens, and windows ----------------------------------------------------
- * Which of a sequence's cached tokens a query sees.  The tokens of its tiles stand one after the
+ * Which of a sequence's cached tokens a query sees.  The tokens of its tiers stand one after the
  * other: token t of tier i at position t + the lengths of tiers 0 .. i - 1 (so tiers are listed
  * oldest tokens first).  A query at position p sees position t where
  *   t <= p  and  (window == 0  or  t > p - window  or  t < sinks):
@@ -550,10 +550,10 @@ typedef struct kvq_visible {
  * The output is fp16, and so is what the tensor cores multiply (rotated queries as the sum of two
  * numbers, decoded rows that are not fp16 values already and softmax weights as one), with float32
  * scores, sums and accumulators: the output's error is 2^-12 to 2^-11.7 of its size (2-norm over the
- * outputs, on caches with outlier channels; 0.42 2^-11 is its own rounding).  The magnitudes of a query's elements may sum to at most 45000 x
- * head_dim.  INT4 scales above 9352 are reported (KVQ_DEVERR_VALUE_RANGE).  A cached vector that is
- * not finite gives NaN in the outputs of the queries that see it (its key alone may also give them no
- * weight), and does not reach the others. */
+ * outputs, on caches with outlier channels; 0.42 2^-11 is its own rounding).  The magnitudes of a
+ * query's elements may sum to at most 45000 x head_dim.  INT4 scales above 9352 are reported
+ * (KVQ_DEVERR_VALUE_RANGE).  A cached vector that is not finite gives NaN in the outputs of the queries
+ * that see it (its key alone may also give them no weight), and does not reach the others. */
 KVQ_API kvq_status kvq_chunk_workspace_size(const kvq_tier_view* tiers, int32_t num_tiers, int32_t batch,
                                             int32_t num_tokens, int32_t num_q_heads, const kvq_visible* visible,
                                             size_t* bytes);

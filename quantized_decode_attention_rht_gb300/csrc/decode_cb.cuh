@@ -58,8 +58,8 @@
 
 #include "kvq_internal.cuh"
 
-// The kernel is compiled twice: as it is, and (KVQ_CB_HIDES) with the mask of a window's decode, in a namespace of
-// its own, which would cost the plain one registers (up to 44 bytes of spills in instances at their limit).
+// The kernel is compiled twice: as it is, and (KVQ_CB_HIDES), in a namespace of its own, with the mask of a window's
+// decode, for which instances at their register limit pay with up to 44 bytes of spills.
 #ifdef KVQ_CB_HIDES
 #define cbk cbk_hiding
 #endif
@@ -72,7 +72,6 @@ constexpr bool kHides = true;
 #else
 constexpr bool kHides = false;
 #endif
-
 
 constexpr int PS = 16;
 constexpr unsigned kFull = 0xFFFFFFFFu;
