@@ -193,6 +193,24 @@ def test_decode_window(name, d, window, sinks):
     c.check(c.run(kvq, torch))
 
 
+@pytest.mark.parametrize("name,d,group", [("qjl", 128, 1), ("qjl", 128, 4), ("outlier", 128, 4), ("outlier", 256, 1),
+                                          ("cb4", 128, 1), ("cb23", 128, 2), ("cb4", 128, 8), ("cb32", 256, 8), ("cb32", 256, 1),
+                                          ("fp16", 128, 1), ("fp16", 128, 8), ("fp8_int4", 128, 8), ("fp8_fp16", 128, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (33, 5)])
+def test_decode_window_of_every_kernel(name, d, group, window, sinks):
+    torch, kvq = modules()
+    c = Case(kvq, torch, [name], [[200, 31, 38, 0, 39]], [1] * 5, hq=2 * group, hkv=2, d=d, window=window, sinks=sinks, seed=group)
+    c.check(c.run(kvq, torch, decode=True))
+
+
+@pytest.mark.parametrize("ps", [1, 3, 24, 128, 200])
+@pytest.mark.parametrize("name", ["fp8_int4", "cb32"])
+def test_decode_window_page_sizes(name, ps):
+    torch, kvq = modules()
+    c = Case(kvq, torch, [name], [[301, 50, 155]], [1] * 3, hq=4, hkv=2, ps=ps, window=100, sinks=7, seed=ps)
+    c.check(c.run(kvq, torch, decode=True))
+
+
 @pytest.mark.parametrize("specs,lens", [(["fp8_int4", "fp16"], [[300, 0, 128, 7], [64, 33, 0, 1]]),
                                         (["cb4", "fp16"], [[300, 0, 128, 7], [64, 33, 0, 1]]),
                                         (["cb32", "cb4", "fp8_int4", "fp16"], [[130, 5, 0, 16], [100, 0, 2, 16], [40, 7, 0, 16], [50, 1, 1, 16]])])
@@ -338,6 +356,23 @@ def test_what_a_query_does_not_see_does_not_reach_it(name, d, group, side):
     c.check(got[:70], set(range(70)))
     if side == "v":
         assert not np.isfinite(got[70:].astype(np.float64)).all(-1).any()
+
+
+@pytest.mark.parametrize("name,d,group", [("fp16", 128, 4), ("fp16", 128, 8), ("fp8_int4", 128, 1), ("fp8_int4", 128, 4), ("fp8_fp16", 128, 2),
+                                          ("cb4", 128, 1), ("cb4", 128, 4), ("cb4", 128, 8), ("cb32", 256, 1), ("cb32", 256, 2),
+                                          ("qjl", 128, 1), ("qjl", 128, 2), ("outlier", 128, 2), ("outlier", 256, 1), ("fp16", 64, 2),
+                                          ("cb4", 64, 2)])
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_what_a_decode_window_hides_does_not_reach_it(name, d, group, side):
+    """Vectors that are not finite on the pages where the sinks end and the window begins."""
+    torch, kvq = modules()
+    bad = [(4, np.nan), (15, np.inf), (160, np.nan), (169, -np.inf)]  # of 300 tokens the first 4 and the last 130 are seen
+    args = dict(specs=[name], lens=[[300]], counts=[1], hq=group, hkv=1, d=d, window=130, sinks=4, seed=1)
+    with np.errstate(invalid="ignore"):
+        c = Case(kvq, torch, edit=nan_at([(t, 1.0) for t, _ in bad], side), **args)
+        e = Case(kvq, torch, edit=nan_at(bad, side), **args)
+    c.check(c.run(kvq, torch, decode=True))
+    c.check(e.run(kvq, torch, decode=True))
 
 
 @pytest.mark.parametrize("hq", [4, 16])
