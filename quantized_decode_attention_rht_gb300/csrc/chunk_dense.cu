@@ -27,11 +27,12 @@
 // Bounded by the products: 4096 tokens x 32/8 heads on 28672 of fp8 keys and INT4 values take 1960 us, unpacking among
 // them: 1.05 PFLOP/s, 1.57 with the queries' second part.  A pair of row blocks over 128 tokens takes 3770 cycles, 3070
 // of them products: a row block's scores (1024), weights (about 2000) and values (512) follow one another, as
-// the weights lie over the scores and TMEM has no room for more.  Where products are shorter or weights longer this
-// chain alone counts (tensor pipe 31%, issue slots 29%): 270 us for a prompt of 4096 tokens x 32 heads of 4-bit codes,
-// whose factors make weights 2200 to 3000 cycles, 150 us for 3 x 777 tokens x 16/4 heads x 64 on 5001.  (Two threads a
-// row took the same time; a quarter to a third of the powers as polynomials, beside the special-function unit, up to a
-// fifth longer.)
+// the weights lie over the scores and TMEM has no room for more.  Where products are shorter or weights longer the softmax
+// warps' latency alone counts, two warps a scheduler (tensor pipe 31%, issue slots 29%): 270 us for a prompt of 4096
+// tokens x 32 heads of 4-bit codes, whose factors make weights 2200 to 3000 cycles, 150 us for 3 x 777 tokens x 16/4
+// heads x 64 on 5001.  (Two threads a row took the same time; scores two tiles ahead, at head_dim 64, which TMEM holds
+// for tiles of 64 tokens, 171 instead of 148 us; a quarter to a third of the powers as polynomials, beside the
+// special-function unit, up to a fifth longer.)
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
