@@ -117,6 +117,7 @@ struct Pages {
   const int32_t* table;  // the group's block-table row
   int num_pages, page_size, page_shift, hkv, hk;
   int end;               // tokens of the prefix
+  int begin, sinks;      // a chunk's items (MASKED): the rows see tokens from begin on and below sinks, of those before end
 };
 struct Ring {
   uint32_t tiles, full, empty;  // shared addresses
@@ -124,18 +125,27 @@ struct Ring {
   uint32_t first_use;             // what the second stage waits for before its first tile, or 0
 };
 
-// A token that is not there reads as zero.  Past the end of the prefix its score is -inf; in a page
-// outside the pool it has a score like any other, and the whole item is left out (Ctl::bad_page).
+// A token that is not there reads as zero.  Past the end of the prefix its score is -inf, where no row of a chunk sees
+// it its weights are hidden; in a page outside the pool it has a score like any other, and the whole item is left out
+// (Ctl::bad_page).
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
-// Page of token t (-1 past the end).
+// Whether token t is looked up.  Of a chunk's tiles only what some row sees: the block table's other entries may be
+// of pages that the sequence has given back.
+template <bool MASKED>
+__device__ __forceinline__ bool there(const Pages& s, int t) {
+  return t < s.end && (!MASKED || t >= s.begin || t < s.sinks);
+}
+// Page of token t (-1 where it is not there).
+template <bool MASKED>
 __device__ __forceinline__ int page_of(const Pages& s, int t) {
-  if (t >= s.end) return -1;
+  if (!there<MASKED>(s, t)) return -1;
   return __ldg(s.table + (s.page_shift >= 0 ? t >> s.page_shift : t / s.page_size));
 }
-// Its row in the pool: kNoRow past the end, and for a page outside the pool (reported in bits).
+// Its row in the pool: kNoRow where it is not there, and for a page outside the pool (reported in bits).
+template <bool MASKED>
 __device__ __forceinline__ uint32_t row_of(const Pages& s, int t, int page, int* bits) {
-  if (t >= s.end || !page_in_pool(page, s.num_pages, bits)) return kNoRow;
+  if (!there<MASKED>(s, t) || !page_in_pool(page, s.num_pages, bits)) return kNoRow;
   const uint32_t off = s.page_shift >= 0 ? t & (s.page_size - 1) : t % s.page_size;
   return ((uint32_t)page * s.hkv + s.hk) * s.page_size + off;  // below 2^32: the plan checks
 }
@@ -181,11 +191,11 @@ __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
 // phase of the barrier for the one before the last.
 constexpr int kLookUps = 2;
 static_assert(kAhead % kLookUps == 0, "a stage's releases are waited for by one warp");
-template <class TileOf>
+template <bool MASKED, class TileOf>
 __device__ __forceinline__ void first_pages(const Pages& s, const TileOf& tile_of, int n, int first, int (&page)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    page[j] = first < n ? page_of(s, tile_of(first) * kTileTokens + (threadIdx.x & 31) + 32 * j) : -1;
+    page[j] = first < n ? page_of<MASKED>(s, tile_of(first) * kTileTokens + (threadIdx.x & 31) + 32 * j) : -1;
 }
 // The power of two above the finite norms of a tile's values, from the largest of each lane's four as
 // fp16 bits (2^-13 where all are zero).  Norms are divided by that of the item's first tile, so that a weight
@@ -216,7 +226,7 @@ __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __
     uint32_t row[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      row[j] = row_of(s, t0 + 32 * j, page[j], &bits);
+      row[j] = row_of<MASKED>(s, t0 + 32 * j, page[j], &bits);
       sts32(smem + kOffRow + at * kRowBytes + 4 * (lane + 32 * j), row[j]);
     }
     if (bits & KVQ_DEVERR_PAGE_INDEX) *reinterpret_cast<volatile int*>(&ctl->bad_page) = 1;
@@ -256,7 +266,7 @@ __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __
     }
     if (i + kLookUps < n) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) page[j] = page_of(s, tile_of(i + kLookUps) * kTileTokens + lane + 32 * j);
+      for (int j = 0; j < 4; ++j) page[j] = page_of<MASKED>(s, tile_of(i + kLookUps) * kTileTokens + lane + 32 * j);
     }
     if (k_norm) {
       uint32_t most = 0;
@@ -271,7 +281,7 @@ __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __
           for (int j = 0; j < 4; ++j) {
             int ignored = 0;
             const int t = tile_of(0) * kTileTokens + lane + 32 * j;
-            const uint32_t head = row_of(s, t, page_of(s, t), &ignored);
+            const uint32_t head = row_of<MASKED>(s, t, page_of<MASKED>(s, t), &ignored);
             if (head != kNoRow) most = max(most, finite_bits(__half_as_ushort(__ldg(v_norm + head))));
           }
           power = power_above(most);
@@ -808,6 +818,12 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   pages.hkv = p.hkv;
   pages.hk = hk;
   pages.end = len;
+  pages.begin = pages.sinks = 0;
+  if constexpr (MASKED) {
+    pages.end = min(len, stands + ((rows - 1) >> p.group_shift) + 1);
+    pages.begin = p.window ? stands - p.window + 1 : 0;
+    pages.sinks = p.sinks - p.seq[g].base[ti];
+  }
   // ---- before the block meets: everything that needs no barrier
   if (warp < 8) {
     // The block's queries are rotated as one more product, of the queries as they come (fp16,
@@ -874,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&ctl->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp < 17 + kLookUps) {
-    first_pages(pages, tile_of, n, warp - 17, page);
+    first_pages<MASKED>(pages, tile_of, n, warp - 17, page);
   }
   tc_fence_before();
   __syncthreads();

@@ -1,0 +1,81 @@
+"""GPU tests of kvq_chunk_attention and kvq_decode_attention_window at what no query sees: block-table
+entries, vectors and scales of tokens outside the windows and sinks of a call must not reach its
+results or its status.  Results are held to the bounds of test_gpu_chunk (its docstring derives
+them), where they are looked at for the sequence in question alone."""
+import numpy as np
+import pytest
+
+from oracle import chunk as ochunk
+from tests.test_gpu_chunk import Case, modules
+
+pytestmark = pytest.mark.gpu
+
+
+def unseen_entries(c, counts):
+    """Per tier [batch, pages]: entries of the block table that hold no token that a query sees."""
+    out = []
+    for i, tier in enumerate(c.tiers):
+        free = np.ones(tier.block_table.shape, dtype=bool)
+        for b, count in enumerate(counts):
+            length, base = (sum(int(t.lens[b]) for t in tiers) for tiers in (c.tiers, c.tiers[:i]))
+            seen = np.zeros(length, dtype=bool)
+            for p in range(length - count, length):
+                seen |= ochunk.sees(p, length, c.window, c.sinks)
+            for t in np.flatnonzero(seen[base:base + int(tier.lens[b])]):
+                free[b, t // tier.page_size] = False
+        out.append(free)
+    return out
+
+
+# one sequence of ordinary tokens and one of large ones, whose pages stand in for those that are not seen
+def two_sequences(name, d, hq, lens, counts, window, sinks, ps=16, hkv=1):
+    torch, kvq = modules()
+
+    def edit(tier, b, k, v):
+        v *= np.float16(2.0 ** 11 if b else 2.0 ** -3)
+    specs = name.split("+")
+    return torch, kvq, Case(kvq, torch, specs, [[n, n] for n in lens], [counts, counts], hq=hq, hkv=hkv, d=d, ps=ps, window=window,
+                            sinks=sinks, seed=window + 3 * sinks, edit=edit)
+
+
+def give_away(torch, c, free, other):
+    """Unseen entries of both sequences: outside the pool, or (of the first) the second's pages."""
+    for view, f, tier in zip(c.views, free, c.tiers):
+        table = view.block_table.cpu().numpy()
+        if other == "outside":
+            table[f] = np.resize([-1, 1 << 30, -(1 << 31)], int(f.sum()))
+        else:
+            pages = tier.block_table[1, :max(1, (int(tier.lens[1]) + tier.page_size - 1) // tier.page_size)]
+            table[0, f[0]] = np.resize(pages, int(f[0].sum()))
+        view.block_table.copy_(torch.from_numpy(table))
+
+
+def check_both(c, got, count):
+    """Each sequence by itself: the larger's outputs do not stand in for the smaller's."""
+    for b in range(2):
+        c.check(got, set(range(b * count, (b + 1) * count)))
+
+
+# (page size 24: pages and tiles end at different tokens)
+WINDOWS = [(1, 0), (33, 0), (40, 4), (100, 20), (130, 140), (257, 3)]
+PACKED = [("fp16", 128, 2, 20), ("fp8_int4", 128, 2, 20), ("fp8_fp16", 128, 1, 150), ("cb4", 128, 2, 20), ("cb32", 128, 1, 150)]
+
+
+@pytest.mark.parametrize("name,d,hq,count", PACKED)
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+@pytest.mark.parametrize("other", ["outside", "large"])
+def test_packed_pages_that_no_query_sees(name, d, hq, count, window, sinks, other):
+    for ps in (16, 24):
+        torch, kvq, c = two_sequences(name, d, hq, [700], count, window, sinks, ps)
+        give_away(torch, c, unseen_entries(c, [count, count]), other)
+        check_both(c, c.run(kvq, torch), count)
+
+
+@pytest.mark.parametrize("specs,lens,hq,count", [("fp8_int4+fp16", [500, 200], 2, 20), ("cb4+fp16", [333, 90], 2, 33),
+                                                 ("cb32+cb4+fp8_int4+fp16", [130, 101, 203, 60], 1, 9)])
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+@pytest.mark.parametrize("other", ["outside", "large"])
+def test_packed_pages_of_tiers_that_no_query_sees(specs, lens, hq, count, window, sinks, other):
+    torch, kvq, c = two_sequences(specs, 128, hq, lens, count, window, sinks)
+    give_away(torch, c, unseen_entries(c, [count, count]), other)
+    check_both(c, c.run(kvq, torch), count)
