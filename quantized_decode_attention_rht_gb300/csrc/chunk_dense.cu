@@ -173,10 +173,11 @@ __device__ __forceinline__ float norm_of(const ChunkTier& t, int side, uint32_t 
   return __half2float(t.k_aux[row]);
 }
 
-// Tier and row in its pool of a sequence's position (row kNone: no token there, or its page outside the pool).
+// Tier and row in its pool of a sequence's position (row kNone: no token there, none that a query sees, whose
+// block-table entry may be of a page that the sequence has given back, or its page outside the pool).
 __device__ __forceinline__ uint32_t find_row(const ChunkParams& p, const ChunkSeq& s, int seq, int h, int pos, int& tier, int* bits) {
   tier = 0;
-  if (pos < 0 || pos >= s.len) return kNone;
+  if (pos < 0 || pos >= s.len || (p.window && pos <= s.len - s.tokens - p.window && pos >= p.sinks)) return kNone;
 #pragma unroll
   for (int k = 1; k < KVQ_MAX_TIERS; ++k)
     if (k < p.num_tiers && pos >= s.base[k]) tier = k;
@@ -255,7 +256,8 @@ __device__ __forceinline__ void unpack_any(const ChunkTier& t, uint8_t* to, cons
 
 template <int D>
 __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int h, const uint16_t (*tables)[2][16],
-                                            uint32_t* s_row, uint32_t* s_power, int* s_tier, int* s_bad, float* s_max) {
+                                            uint32_t* s_row, uint32_t* s_power, int* s_tier, int* s_bad, float* s_max,
+                                            int* s_tiers) {
   constexpr int TT = dense_tile(D), C = D / 16;
   const int tid = threadIdx.x, lane = tid & 31;
   // the sequence: the last whose tiles begin at or before this one (unpacked ones alone have any)
@@ -274,6 +276,8 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
     s_row[tid] = find_row(p, s, lo, h, j * TT + tid, tier, &bits);
     s_tier[tid] = tier;
     s_bad[tid] = 0;
+    const int tiers = __reduce_or_sync(0xFFFFFFFFu, s_row[tid] != kNone ? 1 << tier : 0);
+    if (lane == 0) s_tiers[tid >> 5] = tiers;
   }
   float unit = 1.0f;
   if (p.codes) {
@@ -320,9 +324,11 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
   const size_t at = ((size_t)tile * p.hkv + h) * (TT * D * 2);
   int over = 0;
   // One tier's tokens alone, but for those that are not there, and keys without a sketch or an outlier stream?
-  const int first = s_tier[0], fmt = p.tier[first].k_fmt;
-  const bool simple = __syncthreads_and((tid >= TT || s_row[tid] == kNone || s_tier[tid] == first) && s_row[0] != kNone &&
-                                        fmt != KVQ_FMT_CODEBOOK_QJL && fmt != KVQ_FMT_CODEBOOK_OUTLIER);
+  int tiers = 0;
+#pragma unroll
+  for (int k = 0; k < TT / 32; ++k) tiers |= s_tiers[k];
+  const int first = max(0, __ffs(tiers) - 1), fmt = p.tier[first].k_fmt;
+  const bool simple = __popc(tiers) == 1 && fmt != KVQ_FMT_CODEBOOK_QJL && fmt != KVQ_FMT_CODEBOOK_OUTLIER;
   if (simple) {
     const ChunkTier& t = p.tier[first];
     unpack_any<D, true>(t, p.vt + at, tables[first][1], s_row, s_power, s_bad,
@@ -523,7 +529,7 @@ template <int D>
 __global__ void __launch_bounds__(kPrepareThreads, 4) prepare_kernel(const __grid_constant__ ChunkParams p) {
   constexpr int TT = dense_tile(D);
   __shared__ uint32_t s_row[TT], s_power[TT];
-  __shared__ int s_tier[TT], s_bad[TT];
+  __shared__ int s_tier[TT], s_bad[TT], s_tiers[TT / 32];
   __shared__ float s_max[8];
   __shared__ uint16_t tables[KVQ_MAX_TIERS][2][16];
   grid_wait();
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) prepare_kernel(const __gri
   __syncthreads();
   const int tiles = p.head->num_tiles * p.hkv, items = tiles + p.head->units[0] * p.hkv;
   for (int x = blockIdx.x; x < items; x += gridDim.x) {
-    if (x < tiles) unpack_tile<D>(p, x / p.hkv, x % p.hkv, tables, s_row, s_power, s_tier, s_bad, s_max);
+    if (x < tiles) unpack_tile<D>(p, x / p.hkv, x % p.hkv, tables, s_row, s_power, s_tier, s_bad, s_max, s_tiers);
     else rotate_queries<D>(p, (x - tiles) / p.hkv, (x - tiles) % p.hkv);
   }
 }

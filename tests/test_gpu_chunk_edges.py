@@ -59,6 +59,8 @@ def check_both(c, got, count):
 # (page size 24: pages and tiles end at different tokens)
 WINDOWS = [(1, 0), (33, 0), (40, 4), (100, 20), (130, 140), (257, 3)]
 PACKED = [("fp16", 128, 2, 20), ("fp8_int4", 128, 2, 20), ("fp8_fp16", 128, 1, 150), ("cb4", 128, 2, 20), ("cb32", 128, 1, 150)]
+UNPACKED = [("fp16", 128, 8, 120), ("fp8_int4", 128, 8, 120), ("cb4", 128, 8, 120), ("cb32", 256, 2, 20), ("cb4", 64, 1, 9),
+            ("fp16", 64, 2, 150), ("qjl", 128, 1, 7), ("outlier", 128, 2, 7), ("fp8_int4", 256, 1, 20)]
 
 
 @pytest.mark.parametrize("name,d,hq,count", PACKED)
@@ -78,4 +80,22 @@ def test_packed_pages_that_no_query_sees(name, d, hq, count, window, sinks, othe
 def test_packed_pages_of_tiers_that_no_query_sees(specs, lens, hq, count, window, sinks, other):
     torch, kvq, c = two_sequences(specs, 128, hq, lens, count, window, sinks)
     give_away(torch, c, unseen_entries(c, [count, count]), other)
+    check_both(c, c.run(kvq, torch), count)
+
+
+@pytest.mark.parametrize("name,d,hq,count", UNPACKED)
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+def test_unpacked_pages_that_no_query_sees(name, d, hq, count, window, sinks):
+    for ps in (16,) if name in ("qjl", "outlier") else (16, 24):  # (keys with a sketch or outliers: 16 only)
+        torch, kvq, c = two_sequences(name, d, hq, [700], count, window, sinks, ps)
+        give_away(torch, c, unseen_entries(c, [count, count]), "outside")
+        check_both(c, c.run(kvq, torch), count)
+
+
+@pytest.mark.parametrize("specs,lens,hq,count", [("fp8_int4+fp16", [500, 200], 8, 100), ("cb4+fp16", [333, 90], 8, 80),
+                                                 ("cb32+cb4+fp8_int4+fp16", [130, 101, 203, 60], 8, 70)])
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+def test_unpacked_pages_of_tiers_that_no_query_sees(specs, lens, hq, count, window, sinks):
+    torch, kvq, c = two_sequences(specs, 128, hq, lens, count, window, sinks)
+    give_away(torch, c, unseen_entries(c, [count, count]), "outside")
     check_both(c, c.run(kvq, torch), count)
