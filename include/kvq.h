@@ -512,7 +512,9 @@ KVQ_API kvq_status kvq_decode_attention_shared(const kvq_tier_view* prefix_tiers
  * oldest tokens first).  A query at position p sees position t where
  *   t <= p  and  (window == 0  or  t > p - window  or  t < sinks):
  * itself and what stands before it; of that, with a sliding window, the last `window` positions
- * (its own among them) and the first `sinks`.  NULL in place of the struct: no window. */
+ * (its own among them) and the first `sinks`.  NULL in place of the struct: no window.
+ * Block-table entries of pages without a token that some query of the call sees are not looked
+ * at: they may be of pages that the sequence has given back. */
 typedef struct kvq_visible {
   int32_t window; /* >= 0 */
   int32_t sinks;  /* >= 0; 0 unless window > 0 */

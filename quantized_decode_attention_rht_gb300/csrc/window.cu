@@ -49,14 +49,16 @@ __global__ void __launch_bounds__(128) narrow_kernel(const __grid_constant__ Nar
     all += n;
   }
   const int from = min(len, max(0, max(0, all - p.window) - base)), first = min(from, max(0, p.sinks - base));
-  const int page1 = from / ps, pages0 = min((first + ps - 1) / ps, page1);  // the second run's first page, the first run's pages
-  const int pages = pages0 + (len + ps - 1) / ps - page1, moved = (page1 - pages0) * ps;
+  // A tier that ends before the window has no second run: its last page, full or not, goes with the tokens on it.
+  const int end = from < len ? len : first, last = (end + ps - 1) / ps;
+  const int page1 = from < len ? from / ps : last, pages0 = min((first + ps - 1) / ps, page1);  // the second run's first page, the first run's pages
+  const int pages = pages0 + last - page1, moved = (page1 - pages0) * ps;
   const int32_t* row = t.table + (size_t)b * t.table_pages;
   for (int i = threadIdx.x; i < pages; i += 128)
     t.to_table[(size_t)b * t.to_pages + i] = __ldg(row + (i < pages0 ? i : page1 + i - pages0));
   if (threadIdx.x == 0) {
-    t.to_lens[b] = len - moved;
-    t.hidden[b] = make_int2(first, from - moved - first);
+    t.to_lens[b] = end - moved;
+    t.hidden[b] = make_int2(first, from < len ? from - moved - first : 0);
     p.bits[b * p.num_tiers + ti] = bits;
   }
 }

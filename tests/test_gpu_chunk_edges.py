@@ -99,3 +99,17 @@ def test_unpacked_pages_of_tiers_that_no_query_sees(specs, lens, hq, count, wind
     torch, kvq, c = two_sequences(specs, 128, hq, lens, count, window, sinks)
     give_away(torch, c, unseen_entries(c, [count, count]), "outside")
     check_both(c, c.run(kvq, torch), count)
+
+
+@pytest.mark.parametrize("name,d,hq,lens", [("fp16", 128, 2, [300, 200]), ("fp8_int4", 128, 8, [301, 200]), ("cb4", 128, 1, [303, 100]),
+                                            ("cb4", 128, 4, [303, 100]), ("cb32", 256, 2, [310, 77]), ("fp16", 64, 2, [297, 64]),
+                                            ("qjl", 128, 1, [301, 64]), ("outlier", 128, 2, [301, 64])])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (40, 0), (40, 4), (50, 300), (64, 17), (210, 5)])
+@pytest.mark.parametrize("other", ["outside", "large"])
+def test_decode_window_pages_that_the_query_does_not_see(name, d, hq, lens, window, sinks, other):
+    """Also of a tier whose last page is not full and ends before the window."""
+    for specs in (name, name + "+fp16"):
+        for ps in (16,) if name in ("qjl", "outlier") else (16, 24):  # (keys with a sketch or outliers: 16 only)
+            torch, kvq, c = two_sequences(specs, d, hq, lens[:specs.count("+") + 1], 1, window, sinks, ps)
+            give_away(torch, c, unseen_entries(c, [1, 1]), other)
+            check_both(c, c.run(kvq, torch, decode=True), 1)
