@@ -208,8 +208,10 @@ __device__ __forceinline__ void unpack_side(const ChunkTier& t, uint8_t* to, con
   for (int i = 0; i < kEach; ++i) {
     const int r = r0 + i * (kPrepareThreads / C);
     uint32_t x[8];
-    decode_raw(raw[i], table, x, over);
-    bool zero = s_row[r] == kNone;
+    int wide = 0;
+    decode_raw(raw[i], table, x, &wide);
+    bool zero = s_row[r] == kNone;  // (its raw coordinates are another token's)
+    if (!zero) *over |= wide;
     if constexpr (VALUES && (F == U_F16 || F == U_F8 || F == U_I4)) {
       bool fine = true;
 #pragma unroll

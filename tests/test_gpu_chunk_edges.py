@@ -113,3 +113,21 @@ def test_decode_window_pages_that_the_query_does_not_see(name, d, hq, lens, wind
             torch, kvq, c = two_sequences(specs, d, hq, lens[:specs.count("+") + 1], 1, window, sinks, ps)
             give_away(torch, c, unseen_entries(c, [1, 1]), other)
             check_both(c, c.run(kvq, torch, decode=True), 1)
+
+
+@pytest.mark.parametrize("d,hq,count", [(128, 8, 120), (64, 1, 5), (256, 1, 5), (128, 1, 5)])
+def test_scales_of_other_sequences_pages_are_not_reported(d, hq, count):
+    """INT4 scales that leave fp16, on the pool's first page, which holds no token of the call's sequences."""
+    torch, kvq = modules()
+    c = Case(kvq, torch, ["fp8_int4"], [[300, 77]], [count, 3], hq=hq, hkv=1, d=d, seed=3)
+    cache, view, tier = c.built.gpu[0], c.views[0], c.tiers[0]
+    held = np.zeros(cache.num_pages, dtype=bool)
+    for b, n in enumerate(tier.lens):
+        held[tier.block_table[b, :(int(n) + 15) // 16]] = True
+    if held[0]:
+        free = int(np.flatnonzero(~held)[0])
+        for x in (cache.k_rows, cache.v_rows, cache.v_aux):
+            x[free] = x[0]
+        view.block_table[view.block_table == 0] = free
+    cache.v_aux[0] = 60000.0
+    c.check(c.run(kvq, torch))
