@@ -148,7 +148,6 @@ size_t chunk_layout(ChunkParams* p, uint8_t* base) {
     p->fn = reinterpret_cast<float*>(take(tiles * hkv * tile * sizeof(float)));
     p->hn = reinterpret_cast<__half*>(take(p->summed * tiles * hkv * tile * sizeof(__half)));
     p->top = reinterpret_cast<float*>(take(tiles * hkv * sizeof(float)));
-    p->unit_of = reinterpret_cast<float*>(take(p->batch * hkv * sizeof(float)));
   }
   return at;
 }

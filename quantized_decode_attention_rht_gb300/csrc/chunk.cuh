@@ -113,7 +113,6 @@ struct ChunkParams {
   float* fn;            // of the weights (the mantissas of the values' norms) or, where `summed`, their inverses
   __half* hn;           // where `summed`, those factors
   float* top;           // [max_tiles][hkv] a power of two above a tile's weights' factors
-  float* unit_of;       // [batch][hkv] what the values' norms were divided by
 };
 
 cudaError_t launch_dependent(const void* kernel, unsigned grid, unsigned block, size_t smem, const ChunkParams& p,

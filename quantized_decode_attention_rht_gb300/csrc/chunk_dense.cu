@@ -193,7 +193,7 @@ __device__ __forceinline__ uint32_t find_row(const ChunkParams& p, const ChunkSe
 // is not finite becomes zeros and is noted in s_bad; keys of such rows become NaN.
 template <int D, int F, bool VALUES>
 __device__ __forceinline__ void unpack_side(const ChunkTier& t, uint8_t* to, const uint16_t* table, const uint32_t* s_row,
-                                            const uint32_t* s_power, int* s_bad, float factor, int* over) {
+                                            const uint32_t* s_power, int* s_bad, int* over) {
   constexpr int TT = dense_tile(D), C = D / 16, kEach = TT * C / kPrepareThreads;
   const uint8_t* rows = VALUES ? t.v_rows : t.k_rows;
   const int row_bytes = VALUES ? t.v_row_bytes : t.k_row_bytes, c = threadIdx.x % C, r0 = threadIdx.x / C;
@@ -218,11 +218,6 @@ __device__ __forceinline__ void unpack_side(const ChunkTier& t, uint8_t* to, con
       for (int k = 0; k < 8; ++k) fine = fine && half2_finite(x[k]);
       if (!fine && !zero) s_bad[r] = 1;
       zero = zero || !fine;
-      if (factor != 1.0f) {
-        const uint32_t f = half2_bits(factor, factor);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], f);
-      }
     } else if constexpr (VALUES) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], s_power[r]);
@@ -241,18 +236,18 @@ __device__ __forceinline__ void unpack_side(const ChunkTier& t, uint8_t* to, con
 }
 template <int D, bool VALUES>
 __device__ __forceinline__ void unpack_any(const ChunkTier& t, uint8_t* to, const uint16_t* table, const uint32_t* s_row,
-                                           const uint32_t* s_power, int* s_bad, float factor, int* over) {
+                                           const uint32_t* s_power, int* s_bad, int* over) {
   switch (VALUES ? unpack_kind(t.v_fmt, t.v_bits) : unpack_kind(t.k_fmt, t.k_bits)) {
-    case U_F16: unpack_side<D, U_F16, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over); break;
+    case U_F16: unpack_side<D, U_F16, VALUES>(t, to, table, s_row, s_power, s_bad, over); break;
     case U_F8:
-      if constexpr (!VALUES) unpack_side<D, U_F8, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over);
+      if constexpr (!VALUES) unpack_side<D, U_F8, VALUES>(t, to, table, s_row, s_power, s_bad, over);
       break;
     case U_I4:
-      if constexpr (VALUES) unpack_side<D, U_I4, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over);
+      if constexpr (VALUES) unpack_side<D, U_I4, VALUES>(t, to, table, s_row, s_power, s_bad, over);
       break;
-    case U_C4: unpack_side<D, U_C4, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over); break;
-    case U_C3: unpack_side<D, U_C3, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over); break;
-    default: unpack_side<D, U_C2, VALUES>(t, to, table, s_row, s_power, s_bad, factor, over);
+    case U_C4: unpack_side<D, U_C4, VALUES>(t, to, table, s_row, s_power, s_bad, over); break;
+    case U_C3: unpack_side<D, U_C3, VALUES>(t, to, table, s_row, s_power, s_bad, over); break;
+    default: unpack_side<D, U_C2, VALUES>(t, to, table, s_row, s_power, s_bad, over);
   }
 }
 
@@ -281,44 +276,30 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
     const int tiers = __reduce_or_sync(0xFFFFFFFFu, s_row[tid] != kNone ? 1 << tier : 0);
     if (lane == 0) s_tiers[tid >> 5] = tiers;
   }
-  float unit = 1.0f;
-  if (p.codes) {
-    // what the values' norms are divided by: a power of two above those of the sequence's first tokens
-    float most = 0.f;
-    if (tid < 128) {
-      int tier, ignored = 0;
-      const uint32_t row = find_row(p, s, lo, h, tid, tier, &ignored);
-      if (row != kNone && p.tier[tier].v_fmt == KVQ_FMT_CODEBOOK)
-        most = finite_or_zero(norm_of(p.tier[tier], 1, row));
-      most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
-      if (lane == 0) s_max[tid >> 5] = most;
-    }
-    __syncthreads();
-    most = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-    unit = most > 0.f ? two_above(most) : 1.0f;
-    if (i == 0 && tid == 0) p.unit_of[(size_t)lo * p.hkv + h] = unit;
-  }
-  const float per_unit = 1.0f / unit;
-  // A value's norm over that is a mantissa in [1, 2), which multiplies weights, and a power of two (2^15 at most), which
-  // goes into its row: weights then keep their precision however small the value, and the sum can be taken of what is
-  // multiplied (a token that outweighs all others keeps its value).
+  // A codebook value's norm is split in two: a mantissa in [1, 2), which multiplies weights, and a power of two, which
+  // goes into its row, where the table's entries take it without a rounding: weights then keep their precision however
+  // small the value, and the sum can be taken of what is multiplied (a token that outweighs all others keeps its
+  // value).  Rows hold 2^-6 to 2^15, so that no entry leaves fp16's normal numbers (the largest is 2^-3 to 2^-1); the mantissa of
+  // norms below 2^-6 is smaller instead, by up to 2^-8, and below 2^-14, where the output is an fp16 subnormal, rows too.
+  // Nothing is scaled by other tokens' norms, which the queries may not see, nor by other tiers' values.
   float mantissa = 1.0f;
   if (p.codes && tid < TT) {
     float power = 1.0f;
     const uint32_t row = s_row[tid];
     if (row != kNone && p.tier[s_tier[tid]].v_fmt == KVQ_FMT_CODEBOOK) {
-      const float norm = norm_of(p.tier[s_tier[tid]], 1, row);
+      float norm = norm_of(p.tier[s_tier[tid]], 1, row);
+      // (one tier's table scale comes behind the products; of several tiers it goes in here, rounded once)
+      if (p.codes > 1) norm *= p.head->unscale[s_tier[tid]][1];
       if (norm == 0.f) {
         power = 0.f;
       } else if (finite_or_zero(norm) != 0.f) {
-        const uint32_t two = __float_as_uint(norm) & 0x7F800000u;  // (an fp16 number: normal in float32)
-        power = fminf(__uint_as_float(two) * per_unit, 32768.0f);
-        mantissa = norm * per_unit / power;
+        const float two = __uint_as_float(__float_as_uint(norm) & 0x7F800000u);
+        power = two >= 0x1p-14f ? fminf(fmaxf(two, 0x1p-6f), 0x1p15f) : (two >= 0x1p-24f ? two * 0x1p8f : 0.f);
+        mantissa = power > 0.f ? norm / power : 1.0f;
+        if (p.codes > 1) mantissa = __half2float(__float2half_rn(mantissa));
       } else {
         mantissa = norm;
       }
-      // (one tier's table scale comes behind the products; of several tiers it goes in here, rounded once)
-      if (p.codes > 1) mantissa = __half2float(__float2half_rn(mantissa * p.head->unscale[s_tier[tid]][1]));
     }
     s_power[tid] = half2_bits(power, power);
   }
@@ -333,10 +314,9 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
   const bool simple = __popc(tiers) == 1 && fmt != KVQ_FMT_CODEBOOK_QJL && fmt != KVQ_FMT_CODEBOOK_OUTLIER;
   if (simple) {
     const ChunkTier& t = p.tier[first];
-    unpack_any<D, true>(t, p.vt + at, tables[first][1], s_row, s_power, s_bad,
-                        p.codes && t.v_fmt != KVQ_FMT_CODEBOOK ? per_unit : 1.0f, &over);
+    unpack_any<D, true>(t, p.vt + at, tables[first][1], s_row, s_power, s_bad, &over);
     __syncthreads();
-    unpack_any<D, false>(t, p.kt + at, tables[first][0], s_row, s_power, s_bad, 1.0f, &over);
+    unpack_any<D, false>(t, p.kt + at, tables[first][0], s_row, s_power, s_bad, &over);
   }
   // values
   for (int u = tid; !simple && u < TT * C; u += kPrepareThreads) {
@@ -355,10 +335,9 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = 0;
       }
-      if (p.codes) {
-        const uint32_t f = t.v_fmt != KVQ_FMT_CODEBOOK ? half2_bits(per_unit, per_unit) : s_power[r];
+      if (t.v_fmt == KVQ_FMT_CODEBOOK) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], f);
+        for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], s_power[r]);
       }
     }
     store16(p.vt + at, TT, r, c, x);
@@ -438,12 +417,12 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
       p.fn[n] = p.summed ? 1.0f / mantissa : mantissa;
       if (p.summed) p.hn[n] = __float2half_rn(mantissa);  // (exact: eleven bits)
       const float most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(finite_or_zero(mantissa))));
-      if (lane == 0) s_max[4 + (tid >> 5)] = most;
+      if (lane == 0) s_max[tid >> 5] = most;
     }
     __syncthreads();
     if (tid == 0) {
-      float most = s_max[4];
-      for (int k = 1; k < TT / 32; ++k) most = fmaxf(most, s_max[4 + k]);
+      float most = s_max[0];
+      for (int k = 1; k < TT / 32; ++k) most = fmaxf(most, s_max[k]);
       p.top[(size_t)tile * p.hkv + h] = two_above(most);
     }
   }
@@ -532,7 +511,7 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) prepare_kernel(const __gri
   constexpr int TT = dense_tile(D);
   __shared__ uint32_t s_row[TT], s_power[TT];
   __shared__ int s_tier[TT], s_bad[TT], s_tiers[TT / 32];
-  __shared__ float s_max[8];
+  __shared__ float s_max[TT / 32];
   __shared__ uint16_t tables[KVQ_MAX_TIERS][2][16];
   grid_wait();
   grid_release();
@@ -920,11 +899,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
       tc_fence_after();
       const bool there = item.row0 + w * kChunkRows + r < rows;
       const float l = unpack2(l2).x + unpack2(l2).y;
-      const float unit = CODES && ok ? p.unit_of[(size_t)item.seq * p.hkv + h] * (p.codes == 1 ? p.head->unscale[0][1] : 1.f) : 1.f;
+      const float unscale = CODES && ok && p.codes == 1 ? p.head->unscale[0][1] : 1.f;
       if (item.part < 0) {
         // all of the row's tiles were here: the value rotation is undone in the thread's registers
         if (ok) {
-          const float inv = l == 0.f ? 0.f : unit * inv_sqrt_dim(D) / l;
+          const float inv = l == 0.f ? 0.f : unscale * inv_sqrt_dim(D) / l;
           const int token = s.q0 + (row >> p.group_shift), head = (h << p.group_shift) + (row & (p.group - 1));
           uint16_t* to = p.out + token * p.out_token + head * p.out_head;
           const uint4* signs = reinterpret_cast<const uint4*>(p.v_signs + (size_t)h * D);
@@ -945,7 +924,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
               for (int e = 0; e < 32; e += 8) {
                 float y[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(v[e + k]) * unit;
+                for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(v[e + k]) * unscale;
                 asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + c + e),
                              "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
                              : "memory");

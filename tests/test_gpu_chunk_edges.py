@@ -115,6 +115,40 @@ def test_decode_window_pages_that_the_query_does_not_see(name, d, hq, lens, wind
             check_both(c, c.run(kvq, torch, decode=True), 1)
 
 
+@pytest.mark.parametrize("name,d,hq,count", [u for u in UNPACKED if u[0] not in ("fp16", "fp8_int4")])
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+def test_large_values_that_no_query_sees(name, d, hq, count, window, sinks):
+    """Finite ones, on pages of another sequence, set no scale of those that are seen."""
+    torch, kvq, c = two_sequences(name, d, hq, [700], count, window, sinks)
+    give_away(torch, c, unseen_entries(c, [count, count]), "large")
+    check_both(c, c.run(kvq, torch), count)
+
+
+def early_case(specs, lens, count, hq, d, early, late):
+    """Early tokens (400 of the first tier) with values of another size than all the others, seen, with next to no weight."""
+    torch, kvq = modules()
+
+    def edit(tier, b, k, v):
+        old = np.arange(len(v)) < (400 if tier == 0 else 0)
+        v *= np.where(old, early, late)[:, None, None].astype(np.float16)
+        k[old] = np.float16(-4.0)
+    c = Case(kvq, torch, specs.split("+"), [[n] for n in lens], [count], hq=hq, hkv=1, d=d, seed=1, edit=edit)
+    c.q = (1.0 + 0.25 * np.random.default_rng(2).standard_normal(c.q.shape)).astype(np.float16)
+    c.check(c.run(kvq, torch), set(range(0, count, 7)))
+
+
+SIZES = [("cb4+fp16", [400, 300]), ("cb32+fp16", [400, 300]), ("cb4+fp8_int4", [400, 300]), ("cb4", [700]), ("cb32", [700])]
+EARLY, LATE = [2.0 ** -17, 2.0 ** -12, 1.0, 2.0 ** 11], [2.0 ** -8, 8.0]
+
+
+@pytest.mark.parametrize("specs,lens", SIZES)
+@pytest.mark.parametrize("count,hq,d", [(120, 8, 128), (120, 8, 64), (20, 2, 256)])
+@pytest.mark.parametrize("early", EARLY)
+@pytest.mark.parametrize("late", LATE)
+def test_values_of_early_tokens_set_no_scale_of_unpacked_ones(specs, lens, count, hq, d, early, late):
+    early_case(specs, lens, count, hq, d, early, late)
+
+
 @pytest.mark.parametrize("d,hq,count", [(128, 8, 120), (64, 1, 5), (256, 1, 5), (128, 1, 5)])
 def test_scales_of_other_sequences_pages_are_not_reported(d, hq, count):
     """INT4 scales that leave fp16, on the pool's first page, which holds no token of the call's sequences."""
