@@ -117,7 +117,7 @@ struct Pages {
   const int32_t* table;  // the group's block-table row
   int num_pages, page_size, page_shift, hkv, hk;
   int end;               // tokens of the prefix
-  int begin, sinks;      // a chunk's items (MASKED): the rows see tokens from begin on and below sinks, of those before end
+  int hide, hidden;      // a chunk's items (MASKED): no row sees tokens hide .. hide + hidden - 1
 };
 struct Ring {
   uint32_t tiles, full, empty;  // shared addresses
@@ -134,7 +134,7 @@ constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 // of pages that the sequence has given back.
 template <bool MASKED>
 __device__ __forceinline__ bool there(const Pages& s, int t) {
-  return t < s.end && (!MASKED || t >= s.begin || t < s.sinks);
+  return t < s.end && (!MASKED || (unsigned)(t - s.hide) >= (unsigned)s.hidden);
 }
 // Page of token t (-1 where it is not there).
 template <bool MASKED>
@@ -818,11 +818,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
   pages.hkv = p.hkv;
   pages.hk = hk;
   pages.end = len;
-  pages.begin = pages.sinks = 0;
   if constexpr (MASKED) {
-    pages.end = min(len, stands + ((rows - 1) >> p.group_shift) + 1);
-    pages.begin = p.window ? stands - p.window + 1 : 0;
-    pages.sinks = p.sinks - p.seq[g].base[ti];
+    pages.hide = max(0, p.sinks - p.seq[g].base[ti]);
+    pages.hidden = p.window ? max(0, stands - p.window + 1 - pages.hide) : 0;
   }
   // ---- before the block meets: everything that needs no barrier
   if (warp < 8) {
