@@ -125,6 +125,10 @@ struct Ring {
   uint32_t first_use;             // what the second stage waits for before its first tile, or 0
 };
 
+// Half a tile's weights may sum to this before m is raised (the largest fp16 is 2^16), and m is then
+// this far below the largest score (64 weights of 2^2 are 2^8).
+constexpr float kMostWeight = 32768.0f, kHeadroom = 2.0f;
+
 // A token that is not there reads as zero.  Past the end of the prefix its score is -inf, where no row of a chunk sees
 // it its weights are hidden; in a page outside the pool it has a score like any other, and the whole item is left out
 // (Ctl::bad_page).
@@ -206,6 +210,12 @@ __device__ __forceinline__ float power_above(uint32_t most) {
 __device__ __forceinline__ uint32_t finite_bits(uint32_t norm) {
   norm &= 0x7FFFu;
   return norm < 0x7C00u ? norm : 0u;
+}
+
+// The exponent of the power of two above a value's norm: at least -40 (an fp16 number over another's power), so that
+// the weight of a token whose norm is zero stays finite, and at most 20, for a norm that is not.
+__device__ __forceinline__ float power_of(float norm) {
+  return (float)(min(max((int)(__float_as_uint(norm) >> 23 & 255u) - 126, -40), 20));
 }
 
 // MASKED (a chunk's items): where some row sees not all of a tile (`edge`), an INT4 scale that is not finite becomes
@@ -301,6 +311,7 @@ __device__ __forceinline__ void look_up(const Pages& s, int (&page)[4], const __
         const float vn = __half2float(__ushort_as_half((uint16_t)aux[j].y)) * value_unit;
         sts32(ka + 128 * j, __float_as_uint(row[j] != kNoRow ? kn : 1.0f));
         sts32(va + 4 * lane + 128 * j, __float_as_uint(row[j] != kNoRow ? vn : 1.0f));
+        if constexpr (MASKED) sts32(va + 4 * (kTileTokens + lane) + 128 * j, __float_as_uint(power_of(vn) - kHeadroom));
       } else if (v_scale) {
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(va + 8 * lane + 256 * j), "r"(aux[j].x), "r"(aux[j].y) : "memory");
       }
@@ -611,9 +622,6 @@ __device__ __forceinline__ int decode_kind(int fmt, int bits) {
 }
 
 // ------------------------------------------------------------------------ softmax
-// Half a tile's weights may sum to this before m is raised (the largest fp16 is 2^16), and m is then
-// this far below the largest score (64 weights of 2^2 are 2^8).
-constexpr float kMostWeight = 32768.0f, kHeadroom = 2.0f;
 // m of a chunk's row before it has seen a token: finite, so that hidden scores weigh nothing.
 constexpr float kNothing = -1e30f;
 // A weight where columns are hidden (not in `see`: none) or their values were not finite (`bad`: NaN).
@@ -969,7 +977,9 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
         // All weights are positive, so a sum of at most kMostWeight says that none is too large for
         // fp16 either; only where it is exceeded (always at first, where m is -inf) m is raised
         // and the half, still in TMEM, weighed again.  Of codebooks P holds weights times values'
-        // norms: both steps allow for the tile's largest.
+        // norms: both steps allow for the tile's largest.  (A chunk's items raise m above the largest product of a
+        // weight and its own norm instead: behind a large value with next to no weight, small ones that have it all
+        // would be fp16 subnormals, 8e-3 of the output for norms 2^19 apart.)
         const float top = CODES ? *reinterpret_cast<volatile float*>(&ctl->norm_top[at]) : 1.f;
 #pragma unroll 1
         for (int c0 = 0; c0 < kTileTokens; c0 += 64) {
@@ -1061,11 +1071,26 @@ __global__ void __launch_bounds__(kThreads, 1) shared_prefix_kernel(const __grid
               tc_ld16(s_at + c, x);
               tc_wait_ld(x);
               const uint32_t see = MASKED ? sees(c) : 0u;
+              if constexpr (MASKED && CODES) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (MASKED ? !hides || (see >> e & 1u) : c + e < valid)
-                  mx = fmaxf(mx, __uint_as_float(x[e]) * (CODES ? norm[c + e] : 1.f) - head);
+                for (int e = 0; e < 16; e += 4) {
+                  const float4 n = *reinterpret_cast<const float4*>(norm + c + e);
+                  const float4 w = *reinterpret_cast<const float4*>(v_norm + kTileTokens + c + e);
+                  const float y[4] = {fmaf(__uint_as_float(x[e]), n.x, w.x), fmaf(__uint_as_float(x[e + 1]), n.y, w.y),
+                                      fmaf(__uint_as_float(x[e + 2]), n.z, w.z), fmaf(__uint_as_float(x[e + 3]), n.w, w.w)};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    if (!hides || (see >> (e + k) & 1u)) mx = fmaxf(mx, y[k]);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (MASKED ? !hides || (see >> e & 1u) : c + e < valid)
+                    mx = fmaxf(mx, __uint_as_float(x[e]) * (CODES ? norm[c + e] : 1.f) - head);
+              }
             }
+            // (of codebooks the sum of the weights says only that a product may be too large)
+            if (MASKED && CODES && __all_sync(0xFFFFFFFFu, mx <= m)) break;
             const float f = ex2(m - mx);
             m = mx;
             const float2 ll = unpack2(l2);

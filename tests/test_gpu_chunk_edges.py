@@ -149,6 +149,14 @@ def test_values_of_early_tokens_set_no_scale_of_unpacked_ones(specs, lens, count
     early_case(specs, lens, count, hq, d, early, late)
 
 
+@pytest.mark.parametrize("specs,lens", SIZES)
+@pytest.mark.parametrize("count", [20, 300])
+@pytest.mark.parametrize("early", EARLY)
+@pytest.mark.parametrize("late", LATE)
+def test_values_of_early_tokens_set_no_scale_of_packed_ones(specs, lens, count, early, late):
+    early_case(specs, lens, count, 1, 128, early, late)
+
+
 @pytest.mark.parametrize("d,hq,count", [(128, 8, 120), (64, 1, 5), (256, 1, 5), (128, 1, 5)])
 def test_scales_of_other_sequences_pages_are_not_reported(d, hq, count):
     """INT4 scales that leave fp16, on the pool's first page, which holds no token of the call's sequences."""
