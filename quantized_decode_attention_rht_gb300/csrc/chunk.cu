@@ -88,12 +88,13 @@ kvq_status chunk_plan(const ChunkCall& c, ChunkParams* p) {
   p->sinks = c.visible ? (int)std::min<long long>(c.visible->sinks, kMostTokens) : 0;
   p->head_dim = d;
   p->sms = device_sms();
-  // Sequences of few rows stay packed where the prefix kernel takes all formats; a batch of long chunks (four times as
-  // many rows in the mean) is unpacked as a whole, which saves a launch whose blocks find nothing to do.  Measured (GB300,
-  // 32/8 heads, fp8 keys and INT4 values), as a whole and not: 4 x 2048 tokens 290 and 293 us, 4 x 1024 on 4000 404 and
-  // 408, 16 x 600 on 1000 406 and 412; 8 chunks of up to 2000 on up to 8000 409 and 409.
+  // Sequences of few rows stay packed where the prefix kernel takes all formats.  (A batch that is long in the mean could
+  // be unpacked as a whole, which saves a launch whose blocks find nothing to do, but not where single tokens stand
+  // beside a long chunk.  Measured (GB300, 32/8 heads, fp8 keys and INT4 values), by sequence and as a whole: 4 x 2048
+  // tokens 278 and 275 us, 16 x 600 on 1000 393 and 389; 8192 and 15 x 1 on 4000 1054 and 1102, 2048 and 3 x 1 on 8000 370
+  // and 380, 4096 and 7 x 1 on 30000 2173 and 2188.)
   const long long rows = (long long)c.num_tokens * p->group, seqs = std::min(c.batch, c.num_tokens);
-  p->dense_rows = seqs == 1 ? (rows > kDenseRows ? -1 : kDenseRows) : (rows > 4LL * kDenseRows * seqs ? -1 : kDenseRows);
+  p->dense_rows = seqs == 1 && rows > kDenseRows ? -1 : kDenseRows;
   for (int i = 0; i < c.num_tiers; ++i) {
     const kvq_cache* k = c.tiers[i].cache;
     if (!shared_tier_supported(d, k->k_format, k->v_format) || (k->v_format == KVQ_FMT_INT4_G32 && !aligned(k->v_aux, 8)))
