@@ -548,11 +548,12 @@ typedef struct kvq_visible {
  * Sequences of more than 512 rows (new tokens x query heads a kv head), and all where the formats or
  * head_dim are not those that kvq_decode_attention_shared decodes on the tensor cores, are unpacked
  * first: the workspace then holds 4 x head_dim bytes for every token and kv head that they may see
- * (with a window: the windows, sinks and chunks).
- * The output is fp16, and so is what the tensor cores multiply (rotated queries as the sum of two
- * numbers, decoded rows that are not fp16 values already and softmax weights as one), with float32
- * scores, sums and accumulators: the output's error is 2^-12 to 2^-11.7 of its size (2-norm over the
- * outputs, on caches with outlier channels; 0.42 2^-11 is its own rounding).  The magnitudes of a
+ * (with a window: the windows, sinks and chunks), 6 x where keys have a sketch or an outlier stream.
+ * The output is fp16, and so is what the tensor cores multiply (rotated queries, and keys with a sketch
+ * or an outlier stream, as the sum of two numbers, other decoded rows that are not fp16 values already
+ * and softmax weights as one), with float32 scores, sums and accumulators.  The output's error (2-norm
+ * over a call's outputs, over formats, head_dims and lengths, with and without outlier channels) was
+ * measured up to 0.93 2^-11 of its size, of which 0.42 2^-11 is its own rounding.  The magnitudes of a
  * query's elements may sum to at most 45000 x head_dim.  INT4 scales above 9352 are reported
  * (KVQ_DEVERR_VALUE_RANGE).  A cached vector that is not finite gives NaN in the outputs of the queries
  * that see it (its key alone may also give them no weight), and does not reach the others. */

@@ -43,6 +43,7 @@ kvq_status chunk_plan(const ChunkCall& c, ChunkParams* p) {
   if ((long long)c.num_tokens * c.hq > (1LL << 26) || c.batch > 65536) return KVQ_ERR_UNSUPPORTED;
   const int d = c0->head_dim, hkv = c0->num_kv_heads;
   long long room = 0;
+  p->key_parts = 1;
   for (int i = 0; i < c.num_tiers; ++i) {
     const kvq_cache* k = c.tiers[i].cache;
     room += (long long)usable_pages(c.tiers[i]) * k->page_size;
@@ -71,6 +72,7 @@ kvq_status chunk_plan(const ChunkCall& c, ChunkParams* p) {
       p->codes = c.num_tiers > 1 ? 2 : 1;
       p->summed |= k->v_bits == 4;
     }
+    if (k->k_format == KVQ_FMT_CODEBOOK_QJL || k->k_format == KVQ_FMT_CODEBOOK_OUTLIER) p->key_parts = 2;
   }
   if (room > kMostTokens) return KVQ_ERR_UNSUPPORTED;
   p->num_tiers = c.num_tiers;
@@ -142,7 +144,7 @@ size_t chunk_layout(ChunkParams* p, uint8_t* base) {
   p->ml = reinterpret_cast<float2*>(take(p->max_parts * hkv * kChunkRows * sizeof(float2)));
   p->acc = reinterpret_cast<float*>(take(p->max_parts * hkv * kChunkRows * d * sizeof(float)));
   p->qt = take(p->max_units[0] * hkv * dense_blocks(p->head_dim) * 2 * kChunkRows * d * 2);
-  p->kt = take(tiles * hkv * tile * d * 2);
+  p->kt = take(p->key_parts * tiles * hkv * tile * d * 2);
   p->vt = take(tiles * hkv * tile * d * 2);
   if (p->codes) {
     p->kn = reinterpret_cast<float*>(take(tiles * hkv * tile * sizeof(float)));

@@ -90,6 +90,7 @@ struct ChunkParams {
   int batch, num_tokens, hq, hkv, group, group_shift, page_size, page_shift, window, sinks, head_dim;
   int codes;       // norms beside the unpacked tiles: 1: the one tier is of codebooks, 2: one of several is
   int summed;      // codebook values of four bits: weights are summed as they are rounded
+  int key_parts;   // fp16 numbers of an unpacked key's coordinate: 2 where a tier's keys have a sketch or an outlier stream
   int dense_rows;  // sequences of more rows a kv head are unpacked (-1: all)
   // capacities that the workspace was laid out for
   int max_blocks, max_tiles, max_parts;
@@ -107,8 +108,8 @@ struct ChunkParams {
   float* acc;           // [max_parts][hkv][kChunkRows][D]
   float2* ml;           // [max_parts][hkv][kChunkRows]: (m, l)
   uint8_t* qt;          // rotated queries of units [max_units][hkv][dense_blocks][2 parts][128 * D * 2]
-  uint8_t* kt;          // unpacked keys [max_tiles][hkv][tile * D * 2], values behind them
-  uint8_t* vt;
+  uint8_t* kt;          // unpacked keys [max_tiles][hkv][key_parts][tile * D * 2] and
+  uint8_t* vt;          // values [max_tiles][hkv][tile * D * 2]
   float* kn;            // [max_tiles][hkv][tile] factors of the scores,
   float* fn;            // of the weights (the mantissas of the values' norms) or, where `summed`, their inverses
   __half* hn;           // where `summed`, those factors

@@ -10,7 +10,8 @@
 //   queries   two fp16 numbers, the nearest one and the rest: rounded once they would be off by 2^-12 of their size,
 //             which keys with outlier channels turn into 6e-4 of the output
 //   keys      fp16 and fp8 keys as they are; of codebooks the centroid under its table's scale, and the key's norm as
-//             a factor of its scores; keys with a sketch or outliers as one fp16 number
+//             a factor of its scores; keys with a sketch or outliers as two fp16 numbers, as queries (one
+//             alone: 1.7e-3 of the output where channels thirty times the others make keys large)
 //   values    fp16 as they are, INT4 levels times their scale (one rounding); of codebooks the centroid times the
 //             norm's power of two, and the norm's mantissa as a factor of the weights.
 // Why unpack: a unit's products over 128 tokens take about 2 us on an SM, decoding the tokens 1.4 us; a chunk of 2048
@@ -316,7 +317,11 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
     const ChunkTier& t = p.tier[first];
     unpack_any<D, true>(t, p.vt + at, tables[first][1], s_row, s_power, s_bad, &over);
     __syncthreads();
-    unpack_any<D, false>(t, p.kt + at, tables[first][0], s_row, s_power, s_bad, &over);
+    unpack_any<D, false>(t, p.kt + p.key_parts * at, tables[first][0], s_row, s_power, s_bad, &over);
+    if (p.key_parts == 2) {  // (another tier's keys have a second part)
+      const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      for (int u = tid; u < TT * C; u += kPrepareThreads) store16(p.kt + 2 * at + TT * D * 2, TT, u / C, u % C, none);
+    }
   }
   // values
   for (int u = tid; !simple && u < TT * C; u += kPrepareThreads) {
@@ -346,7 +351,7 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
   // keys
   for (int u = tid; !simple && u < TT * C; u += kPrepareThreads) {
     const int r = u / C, c = u % C;
-    uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0}, rest[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const uint32_t row = s_row[r];
     if (row != kNone) {
       const int tier = s_tier[r];
@@ -397,14 +402,19 @@ __device__ __forceinline__ void unpack_tile(const ChunkParams& p, int tile, int 
           }
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = half2_bits(y[2 * k], y[2 * k + 1]);
+        for (int k = 0; k < 8; ++k) {
+          x[k] = half2_bits(y[2 * k], y[2 * k + 1]);
+          const float2 near = unpack_half2(x[k]);
+          rest[k] = half2_bits(y[2 * k] - near.x, y[2 * k + 1] - near.y);
+        }
       }
       if (s_bad[r]) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = 0x7E007E00u;
       }
     }
-    store16(p.kt + at, TT, r, c, x);
+    store16(p.kt + p.key_parts * at, TT, r, c, x);
+    if (p.key_parts == 2) store16(p.kt + 2 * at + TT * D * 2, TT, r, c, rest);
   }
   if (p.codes) {
     if (tid < TT) {
@@ -538,12 +548,14 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) prepare_kernel(const __gri
 constexpr float kMostWeight = 32768.0f, kHeadroom = 2.0f;
 constexpr float kNothing = -1e30f;  // m before any token is seen: finite, so that hidden scores (-inf) weigh 0
 
-// The order of loads.  With two row blocks keys and values take turns; with one, scores run a tile further ahead, and
-// the keys with them: K0 K1 V0 K2 V1 ...
-template <int RT>
-__device__ __forceinline__ constexpr int key_load(int i) { return RT == 2 ? 2 * i : (i ? 2 * i - 1 : 0); }
-template <int RT>
-__device__ __forceinline__ constexpr int value_load(int i, int n) { return RT == 2 ? 2 * i + 1 : (i + 1 < n ? 2 * i + 2 : 2 * i + 1); }
+// The order of loads, the keys' KP parts one behind the other.  With two row blocks keys and values take turns; with one,
+// scores run a tile further ahead, and the keys with them: K0 K1 V0 K2 V1 ...
+template <int RT, int KP>
+__device__ __forceinline__ constexpr int key_load(int i) { return RT == 2 ? (KP + 1) * i : (i ? KP + (KP + 1) * (i - 1) : 0); }
+template <int RT, int KP>
+__device__ __forceinline__ constexpr int value_load(int i, int n) {
+  return RT == 2 ? (KP + 1) * i + KP : (i + 1 < n ? KP + (KP + 1) * i + KP : (KP + 1) * n - 1);
+}
 
 template <int D>
 struct Shape {
@@ -731,7 +743,7 @@ __device__ __forceinline__ void store_row(uint32_t o_at, int part, float f, cons
   }
 }
 
-template <int D, int KIND>
+template <int D, int KIND, int KP>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __grid_constant__ ChunkParams p) {
   using X = Shape<D>;
   constexpr bool CODES = KIND != kValues;
@@ -746,7 +758,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
   grid_release();
   const int num = p.head->items[0];
   // longer items first; all heads of one unit, or (keys and values beyond L2) all units of one head side by side
-  const bool by_head = (size_t)p.head->num_tiles * p.hkv * (2 * X::kTileBytes) > ((size_t)64 << 20);
+  const bool by_head = (size_t)p.head->num_tiles * p.hkv * ((KP + 1) * X::kTileBytes) > ((size_t)64 << 20);
   const int at = by_head ? (int)blockIdx.x % max(1, num) : (int)blockIdx.x / p.hkv;
   const int h = by_head ? (int)blockIdx.x / max(1, num) : (int)blockIdx.x % p.hkv;
   if (at >= num || h >= p.hkv) return;
@@ -947,11 +959,17 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
       return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, abort, err));
     };
     auto full = [&](int load) { return well(bars + 8 * (A_FULL + load % X::kBuffers), (load / X::kBuffers) & 1); };
+    auto keys_full = [&](int i) {
+      bool ok = full(key_load<RT, KP>(i));
+      if (KP == 2) ok = ok && full(key_load<RT, KP>(i) + 1);
+      return ok;
+    };
     auto scores = [&](int block, int i, int buffer) {  // of row block `block` and tile i
-      const uint64_t b = kd + (key_load<RT>(i) % X::kBuffers) * (X::kTileBytes >> 4);
+      // the queries' two parts with the keys, and of keys of two parts the first with the second
 #pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        const uint64_t a = qd + ((block * X::kQBytes + part * (X::kQBytes / 2)) >> 4);
+      for (int part = 0; part < KP + 1; ++part) {
+        const uint64_t a = qd + ((block * X::kQBytes + (part & 1) * (X::kQBytes / 2)) >> 4);
+        const uint64_t b = kd + ((key_load<RT, KP>(i) + (part >> 1)) % X::kBuffers) * (X::kTileBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           mma_ss(tm + buffer * TT, a + (((kk >> 2) * (kChunkRows * 128) + (kk & 3) * 32) >> 4),
@@ -960,26 +978,29 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
       tc_commit(bars + 8 * (A_S + buffer));
     };
     auto values = [&](int block, int i, int buffer) {
-      const uint64_t b = vd + (value_load<RT>(i, n) % X::kBuffers) * (X::kTileBytes >> 4);
+      const uint64_t b = vd + (value_load<RT, KP>(i, n) % X::kBuffers) * (X::kTileBytes >> 4);
 #pragma unroll
       for (int kk = 0; kk < TT / 16; ++kk)
         mma_ts(tm + X::kAccAt + block * D, tm + buffer * TT + kk * 8, b + ((kk * 2048) >> 4), kIdescO, i > 0 || kk > 0);
     };
     auto free_buffer = [&](int load) { tc_commit(bars + 8 * (A_EMPTY + load % X::kBuffers)); };
-    bool ok = well(bars + 8 * A_Q, 0) && full(0);
+    auto free_keys = [&](int i) {
+      for (int part = 0; part < KP; ++part) free_buffer(key_load<RT, KP>(i) + part);
+    };
+    bool ok = well(bars + 8 * A_Q, 0) && keys_full(0);
     if (ok) {
       tc_fence_after();
       if (elect_one()) {
         for (int b = 0; b < blocks; ++b) scores(b, 0, b);
-        free_buffer(0);
+        free_keys(0);
       }
       __syncwarp();
     }
-    if (RT == 1 && ok && n > 1 && (ok = full(key_load<RT>(1)))) {
+    if (RT == 1 && ok && n > 1 && (ok = keys_full(1))) {
       tc_fence_after();
       if (elect_one()) {
         scores(0, 1, 1);
-        free_buffer(key_load<RT>(1));
+        free_keys(1);
       }
       __syncwarp();
     }
@@ -987,40 +1008,40 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
       const bool more = i + 1 < n;
       if constexpr (RT == 2) {
         for (int b = 0; b < blocks && ok; ++b) {
-          if (b == 0) ok = full(2 * i + 1);
+          if (b == 0) ok = full(value_load<RT, KP>(i, n));
           ok = ok && well(bars + 8 * (A_P + b), i & 1);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             values(b, i, b);
-            if (b + 1 == blocks) free_buffer(2 * i + 1);
+            if (b + 1 == blocks) free_buffer(value_load<RT, KP>(i, n));
           }
           __syncwarp();
           if (!more) continue;
-          if (b == 0 && !(ok = full(2 * i + 2))) break;
+          if (b == 0 && !(ok = keys_full(i + 1))) break;
           tc_fence_after();
           if (elect_one()) {
             scores(b, i + 1, b);
-            if (b + 1 == blocks) free_buffer(2 * i + 2);
+            if (b + 1 == blocks) free_keys(i + 1);
           }
           __syncwarp();
         }
       } else {
-        ok = full(value_load<RT>(i, n)) && well(bars + 8 * (A_P + (i & 1)), (i >> 1) & 1);
+        ok = full(value_load<RT, KP>(i, n)) && well(bars + 8 * (A_P + (i & 1)), (i >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
           values(0, i, i & 1);
-          free_buffer(value_load<RT>(i, n));
+          free_buffer(value_load<RT, KP>(i, n));
           tc_commit(bars + 8 * A_O);
         }
         __syncwarp();
         if (i + 2 < n) {
-          if (!(ok = full(key_load<RT>(i + 2)))) break;
+          if (!(ok = keys_full(i + 2))) break;
           tc_fence_after();
           if (elect_one()) {
             scores(0, i + 2, i & 1);
-            free_buffer(key_load<RT>(i + 2));
+            free_keys(i + 2);
           }
           __syncwarp();
         }
@@ -1040,17 +1061,22 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
       bar_expect(bars + 8 * A_Q, q_bytes);
       bulk_load(smem, q, q_bytes, bars + 8 * A_Q);
       bool ok = true;
-      for (int load = 0; load < 2 * n && ok; ++load) {
-        // tile and side of this load
-        const bool value = RT == 2 ? load & 1 : (load > 0 && !(load & 1)) || load == 2 * n - 1;
-        const int i = RT == 2 ? load / 2 : (value ? (load == 2 * n - 1 ? n - 1 : load / 2 - 1) : (load + 1) / 2);
+      for (int load = 0; load < (KP + 1) * n && ok; ++load) {
+        // tile and part of this load: the keys' parts, then the values (key_load, value_load)
+        const int turns = RT == 2 ? load : load - KP, step = turns >= 0 ? turns / (KP + 1) : -1;
+        int part = turns - step * (KP + 1), i = RT == 2 ? step : step + 1;
+        if (RT == 1 && load < KP) part = load;
+        if (RT == 1 && load >= KP) i -= part == KP;  // values of the tile before
+        if (RT == 1 && load == (KP + 1) * n - 1) part = KP, i = n - 1;
+        const bool value = part == KP;
         const int x = item.first + i, slot = load % X::kBuffers, turn = load / X::kBuffers;
         const size_t tile = (size_t)(s.tile0 + (x < item.sinks ? x : item.begin + x - item.sinks)) * p.hkv + h;
         if (turn > 0 && !(ok = bar_wait(bars + 8 * (A_EMPTY + slot), (turn - 1) & 1, abort, err))) break;
         const uint32_t bar = bars + 8 * (A_FULL + slot);
         bar_expect(bar, X::kTileBytes);
-        bulk_load(smem + X::kOffRing + slot * X::kTileBytes, (value ? p.vt : p.kt) + tile * X::kTileBytes, X::kTileBytes, bar);
-        if (CODES && !value) {  // (a stage's norms have been read: the keys' buffer waits for later products)
+        bulk_load(smem + X::kOffRing + slot * X::kTileBytes, value ? p.vt + tile * X::kTileBytes : p.kt + (tile * KP + part) * X::kTileBytes,
+                  X::kTileBytes, bar);
+        if (CODES && part == 0) {  // (a stage's norms have been read: the keys' buffer waits for later products)
           const uint32_t to = smem + X::kOffNorm + i % X::kNormStages * X::kNormBytes, nbar = bars + 8 * (A_N + i % X::kNormStages);
           bar_expect(nbar, (KIND == kCodesSummed ? 10 : 8) * TT);
           bulk_load(to, p.kn + tile * TT, TT * 4, nbar);
@@ -1077,9 +1103,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
   if (warp == RT * 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(X::kColumns));
 }
 
-template <int D, int KIND>
+template <int D, int KIND, int KP = 1>
 cudaError_t launch_attend(const ChunkParams& p, cudaStream_t stream) {
-  auto kern = attend_kernel<D, KIND>;
+  auto kern = attend_kernel<D, KIND, KP>;
   static std::atomic<bool> configured[64];  // shared-memory limit raised on this device (a racing second raise is
                                             // harmless)
   int dev = 0;
@@ -1110,6 +1136,9 @@ cudaError_t launch_chunk_dense(const ChunkParams& p, cudaStream_t stream) {
   auto kind = [&](auto dim) {
     constexpr int D = decltype(dim)::value;
     if (!p.codes) return launch_attend<D, kValues>(p, stream);
+    if constexpr (D != 64) {  // (such keys are of 128 or 256 coordinates, with codebook values)
+      if (p.key_parts == 2) return p.summed ? launch_attend<D, kCodesSummed, 2>(p, stream) : launch_attend<D, kCodes, 2>(p, stream);
+    }
     return p.summed ? launch_attend<D, kCodesSummed>(p, stream) : launch_attend<D, kCodes>(p, stream);
   };
   if (p.head_dim == 64) return kind(std::integral_constant<int, 64>{});
