@@ -553,7 +553,8 @@ typedef struct kvq_visible {
  * or an outlier stream, as the sum of two numbers, other decoded rows that are not fp16 values already
  * and softmax weights as one), with float32 scores, sums and accumulators.  The output's error (2-norm
  * over a call's outputs, over formats, head_dims and lengths, with and without outlier channels) was
- * measured up to 0.93 2^-11 of its size, of which 0.42 2^-11 is its own rounding.  The magnitudes of a
+ * measured up to 0.93 2^-11 of its size, of which 0.42 2^-11 is its own rounding; of a few outputs
+ * alone up to 2.5 2^-11 (codebook keys with large scores).  The magnitudes of a
  * query's elements may sum to at most 45000 x head_dim.  INT4 scales above 9352 are reported
  * (KVQ_DEVERR_VALUE_RANGE).  A cached vector that is not finite gives NaN in the outputs of the queries
  * that see it (its key alone may also give them no weight), and does not reach the others. */

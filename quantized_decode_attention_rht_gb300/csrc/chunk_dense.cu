@@ -25,8 +25,9 @@
 // 128 rows; one warp that loads, one that issues products.  While one row block's scores become weights, the other's
 // products run.  TMEM: two blocks of scores, over which the weights are written, and two accumulators, all 512
 // columns at head_dim 128.  (head_dim 256: one row block, tiles of 64 tokens, two score blocks in turn.)
-// Bounded by the products: 4096 tokens x 32/8 heads on 28672 of fp8 keys and INT4 values take 1960 us, unpacking among
-// them: 1.05 PFLOP/s, 1.57 with the queries' second part.  A pair of row blocks over 128 tokens takes 3770 cycles, 3070
+// Bounded by the products and by waves: 4096 tokens x 32/8 heads on 28672 of fp8 keys and INT4 values take 1960 us,
+// unpacking among them: 1.05 PFLOP/s, 1.57 with the queries' second part.  Its 512 items of one length are 3.37 waves of
+// 152 SMs, 966 tiles one after the other where equal shares would be 820.  A pair of row blocks over 128 tokens takes 3770 cycles, 3070
 // of them products: a row block's scores (1024), weights (about 2000) and values (512) follow one another, as
 // the weights lie over the scores and TMEM has no room for more.  Where products are shorter or weights longer the softmax
 // warps' latency alone counts, two warps a scheduler (tensor pipe 31%, issue slots 29%): 270 us for a prompt of 4096
@@ -570,7 +571,7 @@ struct Shape {
   static constexpr int kSmem = kOffCtl + 512;
   static constexpr int kThreads = RT * 128 + 64;
   // TMEM: two blocks of scores, then the accumulators
-  static constexpr int kAccAt = 2 * TT, kColumns = D == 64 ? 512 : 512;
+  static constexpr int kAccAt = 2 * TT, kColumns = 512;
   static_assert(kAccAt + RT * D <= kColumns, "tensor memory");
   static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 };
@@ -623,7 +624,7 @@ __device__ __forceinline__ unsigned long long add_halves(unsigned long long sum,
 // of the weights as they are (kCodes) or of the weights that the rounded products stand for (kCodesSummed).  Values of four
 // bits take the last: a token that outweighs all others then keeps its value, 2.8e-4 of the output instead of 3.4e-4, for
 // 268 instead of 250 us of a 4096-token prompt x 32 heads; those of two and three bits, whose fewer centroids lose less,
-// stay below 2.9e-4 without (337 instead of 360 us for 16 ragged chunks on 8000 tokens).
+// stay below 2.9e-4 without, of one tier (337 instead of 360 us for 16 ragged chunks on 8000 tokens).
 enum { kValues, kCodes, kCodesSummed };
 
 // 32 scores -> 16 weight pairs (codebooks: times the values' factors) and their sum.  HIDE: columns that are not in `see`
@@ -697,7 +698,7 @@ __device__ __forceinline__ void weigh(const uint32_t (&v)[32], uint32_t see, flo
 // registers: one stage of the transform after the other (head_dim 256: its last stage first, of which each half of the
 // row is one result).  Lanes without an address only take part.
 template <int D>
-__device__ __forceinline__ void store_row(uint32_t o_at, int part, float f, const uint4* signs, uint16_t* to) {
+__device__ __forceinline__ void store_turned(uint32_t o_at, int part, float f, const uint4* signs, uint16_t* to) {
   constexpr int N = D == 256 ? 128 : D;
   unsigned long long y[N / 2];
   const unsigned long long f2 = pack2(f, f), g2 = pack2(part ? -f : f, part ? -f : f);
@@ -920,7 +921,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attend_kernel(const __g
           uint16_t* to = p.out + token * p.out_token + head * p.out_head;
           const uint4* signs = reinterpret_cast<const uint4*>(p.v_signs + (size_t)h * D);
 #pragma unroll 1
-          for (int part = 0; part < (D == 256 ? 2 : 1); ++part) store_row<D>(o_at, part, inv, signs, there ? to : nullptr);
+          for (int part = 0; part < (D == 256 ? 2 : 1); ++part) store_turned<D>(o_at, part, inv, signs, there ? to : nullptr);
         }
       } else {
         const size_t part = ((size_t)(item.part + w) * p.hkv + h) * kChunkRows + r;

@@ -1,7 +1,7 @@
 // Chunks with few rows, on the packed cache: the prefix kernel over a plan's items (shared_mma.cuh), with a mask where a
 // row block's tokens do not all see a tile.  Bounded as there, by 1.4 to 1.5 us a tile whatever the rows, and, where
 // there are few tiles, by the plan before it and the item's start: 4 x 5 tokens x 32/8 heads on 2000 of fp8 keys and INT4
-// values 33.5 us, 8 chunks of up to 64 tokens on up to 8192, the newest 256 in fp16, 79 to 97 us by the
+// values 33 us, 8 chunks of up to 64 tokens on up to 8192, the newest 256 in fp16, 81 to 97 us by the
 // lengths drawn (the newest are items of their own, two tiles long behind the same start).
 #include <atomic>
 

@@ -8,7 +8,7 @@
 //
 // narrow_kernel writes tables, lengths and intervals, a block a sequence and tier; bounded by its launch and a
 // chain of two loads, 3.5 us.  The calls are bounded as their decode kernels are: 64 x 32/8 heads on 4100 tokens of fp8
-// keys and INT4 values 100 us (56% of the copy rate), 16 x 32 heads on 2064 of 4-bit codes 68 us, 32 x 16/8 heads x 256 on
+// keys and INT4 values 99 to 104 us (54 to 57% of the copy rate), 16 x 32 heads on 2064 of 4-bit codes 68 us, 32 x 16/8 heads x 256 on
 // up to 1037 of 3/2-bit codes 53 us; 1 x 8 heads on 516 of 4-bit codes 18.5 us, three launches and the loads' latency.
 #include "window.cuh"
 
@@ -64,8 +64,8 @@ __global__ void __launch_bounds__(128) narrow_kernel(const __grid_constant__ Nar
 }
 
 // A window is a small cache, whose chunks the decode's plan makes too long for a full GPU: codebook tiers get 24 items
-// an SM (54 with one query head a kv head), others on the generic kernel four.  Measured (GB300), with the plan's
-// chunks and with these: 32 x 16/8 heads x 256 on 1037 tokens of 3/2-bit codes 85 and 56 us, 1 x 8 heads on 516 of
+// an SM (54 with one query head a kv head; of 32 x 8 heads on 66 pages that is four pages an item), others on the
+// generic kernel four.  Measured (GB300), with the plan's chunks and with these: 32 x 16/8 heads x 256 on 1037 tokens of 3/2-bit codes 85 and 56 us, 1 x 8 heads on 516 of
 // 4-bit 38 and 24, 8 x 32/8 heads on 1024 of 4-bit 42 and 32, 16 x 16/4 heads x 64 on 1024 42 and 30; 16 x 32 heads on
 // 2064 71 and 71.  (fp16 and fp8 tiers: no change, 64 x 32/8 heads on 4100 tokens 112 us.)
 void shorten_chunks(const kvq_tier_view* tiers, int n, int batch, int hq, Plan* plan) {
