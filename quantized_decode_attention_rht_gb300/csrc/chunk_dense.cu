@@ -17,7 +17,7 @@
 // Why unpack: a unit's products over 128 tokens take about 2 us on an SM, decoding the tokens 1.4 us; a chunk of 2048
 // tokens with four query heads a kv head would decode each token 32 times.
 // Bounded by memory: a token's row is read once, 4 head_dim bytes a kv head are written, and written back where they
-// pass the L2.  75 us for 32768 tokens x 8 heads of fp8 keys and INT4 values (286 MB, 3.8 TB/s), 160 us for 2 x 16896
+// pass the L2.  75 us for 32768 tokens x 8 heads of fp8 keys and INT4 values (286 MB, 3.8 TB/s), 155 us for 2 x 16896
 // tokens x 16 heads x 256 of 4-bit codes.  (Rows of the next tile loaded ahead, or a key's and a value's together, took
 // the same time.)
 //
